@@ -26,6 +26,12 @@ MOE_DEV_BAD_EXPERT_INDEX = 1
 MOE_DEV_WAIT_TIMEOUT = 2
 MOE_DEV_FP16_RANGE = 4
 MOE_DEV_NONFINITE = 8
+MOE_DEV_BAD_PAGE = 16
+MOE_DEV_BAD_POSITION = 32
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_KV_BF16 = 0
+MOE_KV_E4M3 = 1
 
 
 class MoeError(RuntimeError):
@@ -51,7 +57,44 @@ class Fp8Ffn(ctypes.Structure):
     _fields_ = [("gate", Fp8Mat), ("up", Fp8Mat), ("down", Fp8Mat)]
 
 
+class SelectRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("scale_token_stride", ctypes.c_int64)]
+
+
+class QkDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("n_pos", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("qkv_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64)]
+
+
+class AttnDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("table_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64)]
+
+
+class LinearDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
 _vp = ctypes.c_void_p
+_i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _st = ctypes.c_int32
 
@@ -77,6 +120,12 @@ _SIGNATURES = {
                                _vp, ctypes.c_int, _vp, _vp, _sz, _vp]),
     "moe_read_device_status": (_st, [_vp, ctypes.POINTER(ctypes.c_int32), _vp]),
     "moe_permute_static_scratch": (_st, [_vp, Dims, _vp, _vp, _vp, _vp]),
+    "moe_select_experts": (_st, [_vp, _i64, _vp, SelectRule, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "moe_qk_norm_rope": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, QkDims, KvCache, _vp, _vp, _vp]),
+    "moe_paged_attention_workspace_bytes": (_st, [AttnDims, _i32, ctypes.POINTER(_sz)]),
+    "moe_paged_attention": (_st, [_vp, KvCache, _vp, _vp, AttnDims, _vp, _vp, _sz, _vp, _vp]),
+    "moe_linear_fp8_workspace_bytes": (_st, [LinearDims, ctypes.POINTER(_sz)]),
+    "moe_linear_fp8": (_st, [_vp, Fp8Mat, _vp, LinearDims, _vp, _vp, _sz, _vp, _vp]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -244,6 +293,46 @@ def moe_read_device_status(ws, stream=None) -> int:
     if st == MOE_ERR_DEVICE_STATUS:
         raise MoeError(st, "moe_read_device_status", f"device status bits 0x{v.value:x}")
     return v.value
+
+
+def moe_select_experts(logits, row_stride: int, bias, rule: SelectRule, T: int, E: int, k: int,
+                       topk_idx, topk_w, stream=None) -> None:
+    _check(lib().moe_select_experts(_ptr(logits), row_stride, _ptr(bias), rule, T, E, k,
+                                    _ptr(topk_idx), _ptr(topk_w), _stream(stream)),
+           "moe_select_experts")
+
+
+def moe_qk_norm_rope(qkv, q_norm, k_norm, cos_sin, pos, slots, d: QkDims, cache: KvCache, q_out,
+                     status=None, stream=None) -> None:
+    _check(lib().moe_qk_norm_rope(_ptr(qkv), _ptr(q_norm), _ptr(k_norm), _ptr(cos_sin), _ptr(pos),
+                                  _ptr(slots), d, cache, _ptr(q_out), _ptr(status),
+                                  _stream(stream)), "moe_qk_norm_rope")
+
+
+def paged_attention_workspace_bytes(d: AttnDims, D: int) -> int:
+    n = _sz(0)
+    _check(lib().moe_paged_attention_workspace_bytes(d, D, ctypes.byref(n)),
+           "moe_paged_attention_workspace_bytes")
+    return n.value
+
+
+def moe_paged_attention(q, cache: KvCache, block_table, seq_lens, d: AttnDims, out, ws,
+                        status=None, stream=None) -> None:
+    _check(lib().moe_paged_attention(_ptr(q), cache, _ptr(block_table), _ptr(seq_lens), d,
+                                     _ptr(out), _ptr(ws), _nbytes(ws), _ptr(status),
+                                     _stream(stream)), "moe_paged_attention")
+
+
+def linear_fp8_workspace_bytes(d: LinearDims) -> int:
+    n = _sz(0)
+    _check(lib().moe_linear_fp8_workspace_bytes(d, ctypes.byref(n)),
+           "moe_linear_fp8_workspace_bytes")
+    return n.value
+
+
+def moe_linear_fp8(x, w: Fp8Mat, bias, d: LinearDims, out, ws, status=None, stream=None) -> None:
+    _check(lib().moe_linear_fp8(_ptr(x), w, _ptr(bias), d, _ptr(out), _ptr(ws), _nbytes(ws),
+                                _ptr(status), _stream(stream)), "moe_linear_fp8")
 
 
 EXPORTED = tuple(_SIGNATURES)

@@ -3,8 +3,6 @@
 // moe_read_device_status, whose job is to read a device word back.
 #include <algorithm>
 #include <atomic>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -12,49 +10,13 @@
 #include <string>
 #include <utility>
 
+#include "api_check.h"
 #include "moe_internal.h"
 
 namespace moe {
 namespace {
 
 thread_local std::string g_last_error;
-
-moe_status fail(moe_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-moe_status fail(moe_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return s;
-}
-
-moe_status cuda_fail(cudaError_t e, const char* where) {
-  return fail(MOE_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-size_t align_up(size_t v) { return (v + 255) & ~size_t(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-#define REQUIRE_PTR(p)                                                                    \
-  do {                                                                                    \
-    if ((p) == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", #p);               \
-    if (!aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p); \
-  } while (0)
-
-#define REQUIRE_OPT_PTR(p)                                                   \
-  do {                                                                       \
-    if ((p) != nullptr && !aligned16(p))                                     \
-      return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p);    \
-  } while (0)
-
-#define CUDA_CHECK(expr, where)                           \
-  do {                                                    \
-    cudaError_t e_ = (expr);                              \
-    if (e_ != cudaSuccess) return cuda_fail(e_, where);   \
-  } while (0)
 
 moe_status check_dims(const moe_dims& d) {
   if (d.T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", d.T);
@@ -95,11 +57,6 @@ moe_status check_ws(const moe_dims& d, const void* ws, size_t ws_bytes) {
   if (ws_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", ws_bytes, need);
   return MOE_OK;
-}
-
-template <class T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
 }  // namespace

@@ -68,6 +68,9 @@ typedef int32_t moe_status;
 #define MOE_DEV_FP16_RANGE 4       /* an fp16 intermediate left its range   */
 #define MOE_DEV_NONFINITE 8        /* an input (x, a block scale) or an
                                       intermediate was infinite or NaN      */
+#define MOE_DEV_BAD_PAGE 16        /* a cache slot, page number or sequence
+                                      length outside the cache or its table */
+#define MOE_DEV_BAD_POSITION 32    /* a position outside the cos/sin table  */
 
 /* Layer dimensions. T tokens, hidden size H, routed-expert intermediate I,
  * E routed experts, top-k, shared-expert intermediate I_shared (0 = none). */
@@ -348,6 +351,179 @@ moe_status moe_verify_layer(const uint16_t* x, moe_fp8_ffn routed,
  */
 moe_status moe_read_device_status(const void* ws, int32_t* status,
                                   void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The rest of a decoder layer around the MoE layer: expert selection with
+ * balance bias and groups, query/key norms with rotary positions into a paged
+ * key/value cache, attention of one new token per sequence over that cache,
+ * and the block-FP8 linear layers between them.  None of these has a
+ * counterpart in the pages, which state the MoE layer only.
+ *
+ * They follow the conventions above, with two additions:
+ *  - `status` (may be NULL) is a device array of 16 int32 that the caller
+ *    zeroes once.  A call ORs MOE_DEV_* bits into word 0 and never clears
+ *    them; moe_read_device_status(status, ...) reads it.
+ *  - Rows may be strided.  A row stride counts elements and is at least the
+ *    row's length; the elements inside a row are contiguous, and every row
+ *    starts on a 16-byte boundary where noted.
+ * ---------------------------------------------------------------------------
+ */
+
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
+/* How moe_select_experts scores and picks. */
+typedef struct {
+  int32_t score;      /* MOE_SCORE_*                                         */
+  int32_t groups;     /* equal groups of consecutive experts; 1: no groups   */
+  int32_t top_groups; /* groups that stay in the running                     */
+  int32_t group_top;  /* 1 or 2: a group's score is the sum of that many of
+                         its largest keys                                    */
+  int32_t renorm;     /* 1: divide the weights by their sum                  */
+  float scale;        /* factor on the weights                               */
+} moe_select_rule;
+
+/*
+ * Experts from router logits:
+ *   s[t,e] = softmax(logits[t,:])[e] or 1 / (1 + exp(-logits[t,e]))
+ *   key    = s + bias          (bias balances the load; it only steers the
+ *                               choice and never enters the weights)
+ *   the top_groups groups of the largest group score are kept (ties: the
+ *   lower group), then the k largest keys among their experts are chosen
+ *   (descending, ties: the lower expert)
+ *   topk_w = scale * s (renorm: divided by the sum of the k chosen s)
+ * logits float [T, row_stride >= E]; bias float [E] or NULL; topk_idx int32
+ * [T, k], topk_w float [T, k], as moe_permute and moe_combine take them.
+ * 1 <= E <= 1024, 1 <= k <= 32, groups <= 32 divides E, E / groups >=
+ * group_top, k <= top_groups * (E / groups).  Everything is fp32.  A logit of
+ * -inf (an expert that is switched off) scores 0; where the chosen scores sum
+ * to 0 the weights are 0, not NaN.  A NaN key counts as the largest key, and
+ * NaN logits give NaN weights; the indices are valid whatever the logits.
+ */
+moe_status moe_select_experts(const float* logits, int64_t row_stride,
+                              const float* bias, moe_select_rule rule,
+                              int32_t T, int32_t E, int32_t k,
+                              int32_t* topk_idx, float* topk_w, void* stream);
+
+#define MOE_KV_BF16 0
+#define MOE_KV_E4M3 1
+
+/* A paged key/value cache.  Token slot n (n = page * page_size + offset) of
+ * head h starts at element page * page_stride + h * head_stride + offset *
+ * token_stride of k and of v, D contiguous elements each; the strides are
+ * multiples of 16 bytes.  MOE_KV_BF16: bf16 elements, k_scale and v_scale
+ * NULL.  MOE_KV_E4M3: E4M3 codes, and one float per token and head at
+ * element page * scale_page_stride + h * scale_head_stride + offset *
+ * scale_token_stride of k_scale and of v_scale; the value is code * scale. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t pages, page_size, Hkv, D, format;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+} moe_kv_cache;
+
+/* One moe_qk_norm_rope call.  rot: leading dimensions of each head that are
+ * rotated (0: none), a multiple of 16 and at most D; interleaved: 1 rotates
+ * the pairs (2i, 2i + 1), 0 the pairs (i, i + rot / 2).  n_pos: rows of
+ * cos_sin.  Strides in elements, multiples of 8. */
+typedef struct {
+  int32_t T, Hq, rot, interleaved, n_pos;
+  float eps;
+  int64_t qkv_stride, q_stride;
+} moe_qk_dims;
+
+/*
+ * Per token t, on row t of qkv (bf16: Hq query heads, then Hkv key heads,
+ * then Hkv value heads, D elements each, D = 64, 128 or 256):
+ *   x' = x / sqrt(mean(x^2) + eps) * norm      query and key heads; norm NULL:
+ *                                              x' = x
+ *   (a, b) -> (a cos - b sin, b cos + a sin)   the rotated pairs i, with
+ *                                              cos = cos_sin[pos[t]][i],
+ *                                              sin = cos_sin[pos[t]][rot/2 + i]
+ * in fp32, rounded once.  Queries go to q_out bf16 [T, q_stride >= Hq * D].
+ * Keys and values go to slot slots[t] of the cache (slots[t] < 0: a padding
+ * token, nothing is stored); two tokens of one call must not share a slot.
+ * MOE_KV_E4M3: per token and head with a = the largest magnitude, code =
+ * E4M3(v * fp32(448 / a)) to nearest even, scale = fp32(a / 448); a = 0 gives
+ * zero codes and scale; groups with 0 < a < 2^-117 are treated as a = 0.
+ * q_norm, k_norm float [D] or NULL; cos_sin float [n_pos, rot], pos int32 [T]
+ * (both NULL iff rot == 0); slots int64 [T].
+ * A position outside [0, n_pos) raises MOE_DEV_BAD_POSITION: the token's
+ * queries are NaN and it stores nothing.  A slot past the cache raises
+ * MOE_DEV_BAD_PAGE and stores nothing.
+ */
+moe_status moe_qk_norm_rope(const uint16_t* qkv, const float* q_norm,
+                            const float* k_norm, const float* cos_sin,
+                            const int32_t* pos, const int64_t* slots,
+                            moe_qk_dims d, moe_kv_cache cache, uint16_t* q_out,
+                            int32_t* status, void* stream);
+
+/* One moe_paged_attention call: B sequences, Hq query heads (a multiple of
+ * the cache's Hkv; query head h reads key/value head h / (Hq / Hkv)).
+ * table_width: page numbers per sequence in block_table, table_stride apart.
+ * window > 0: only the last `window` tokens are attended to; 0: all.
+ * q_stride, out_stride: elements between sequences, multiples of 8. */
+typedef struct {
+  int32_t B, Hq, table_width, window;
+  float scale;
+  int64_t table_stride, q_stride, out_stride;
+} moe_attn_dims;
+
+/*
+ * Attention of one new token per sequence over the paged cache:
+ *   out[b,h] = sum_t softmax_t(scale * q[b,h] . k[b,t]) v[b,t],
+ *   t in [max(0, len - window), len), len = seq_lens[b]
+ * q bf16 [B, q_stride] (Hq heads of D), block_table int32 [B, table_stride]:
+ * token t of sequence b is offset t % page_size of page block_table[b][t /
+ * page_size]; seq_lens int32 [B]; out bf16 [B, out_stride].  The cache's
+ * length splits over the GPU and the parts are joined in a fixed order, so
+ * equal calls give equal bits.  A sequence of length 0 gives zeros.  Cache
+ * elements outside [max(0, len - window), len) are never read: they may
+ * hold anything, and the pages of a window's past may be reused.
+ * Scores, maxima, sums and outputs are fp32; the softmax weights are rounded
+ * to the cache's multiplication type (bf16 next to bf16 values, fp16 next to
+ * E4M3 values).  D = 64, 128 or 256; up to 2^31 - 1 tokens per sequence.
+ * A page number outside [0, pages) or a length outside [0, table_width *
+ * page_size] raises MOE_DEV_BAD_PAGE; the tokens of such a page are left
+ * out, and such a length is clamped.
+ */
+moe_status moe_paged_attention_workspace_bytes(moe_attn_dims d, int32_t D,
+                                               size_t* bytes);
+moe_status moe_paged_attention(const uint16_t* q, moe_kv_cache cache,
+                               const int32_t* block_table,
+                               const int32_t* seq_lens, moe_attn_dims d,
+                               uint16_t* out, void* ws, size_t ws_bytes,
+                               int32_t* status, void* stream);
+
+/* One moe_linear_fp8 call: x [M, K] -> out [M, N].  N a multiple of 8 and K
+ * of 16, both at most 65536; x_stride, out_stride: elements between rows,
+ * multiples of 8. */
+typedef struct {
+  int32_t M, N, K;
+  int64_t x_stride, out_stride;
+} moe_linear_dims;
+
+/*
+ * out = x_q W^T + bias on E4M3 tensor-core products, W = dec(codes) * block
+ * scale (w: one matrix [N, K] with scales [ceil(N/128), ceil(K/128)]).  The
+ * activations are quantised in the call per row and group of 128 columns,
+ * with a the group's largest magnitude:
+ *   code = E4M3(x * fp32(448 / a)) to nearest even, scale = fp32(a / 448);
+ *   a = 0, or below 2^-117, gives zero codes and scale.
+ * Each 128-wide block's products are summed and scaled by both scales in
+ * fp32, the blocks are summed in fp32, and the result is rounded once.
+ * x bf16 [M, x_stride], bias float [N] or NULL, out bf16 [M, out_stride].
+ * An infinite or NaN activation raises MOE_DEV_NONFINITE (its output row is
+ * then NaN or infinite).
+ */
+moe_status moe_linear_fp8_workspace_bytes(moe_linear_dims d, size_t* bytes);
+moe_status moe_linear_fp8(const uint16_t* x, moe_fp8_mat w, const float* bias,
+                          moe_linear_dims d, uint16_t* out, void* ws,
+                          size_t ws_bytes, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }
