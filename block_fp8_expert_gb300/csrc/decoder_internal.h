@@ -13,12 +13,14 @@ namespace moe {
 // Smallest largest-magnitude that is quantised: 448 / a stays finite.
 constexpr uint32_t kQuantMinBits = 0x05000000u;  // 2^-117
 
-// From the bits of a group's largest magnitude: the factor v -> code and the
-// scale code -> v, both rounded to nearest (0 for a group that holds nothing).
+// From the bits of a group's largest magnitude: the factor v -> code, which
+// is 448 times the rounded reciprocal (what tensor programs compute for
+// 448 / a, so that activations quantised by one agree code for code), and the
+// scale code -> v, each rounded to nearest (0 for a group that holds nothing).
 __device__ __forceinline__ void quant_factors(uint32_t maxbits, float& to_code, float& scale) {
   const float a = __uint_as_float(maxbits);
   const bool any = maxbits >= kQuantMinBits;
-  to_code = any ? __fdiv_rn(448.f, a) : 0.f;
+  to_code = any ? __fmul_rn(448.f, __frcp_rn(a)) : 0.f;
   scale = any ? __fdiv_rn(a, 448.f) : 0.f;
 }
 // Two floats -> two E4M3 codes (lo in bits 0..7), nearest even, saturated.

@@ -496,7 +496,7 @@ def _ref_linear(torch, x, codes, scales, bias=None):
         a = np.abs(xb).max(1, keepdims=True)
         real = a >= np.float32(2.0 ** -117)
         with np.errstate(divide="ignore", over="ignore"):
-            f = np.where(real, np.float32(448) / a, np.float32(0)).astype(np.float32)
+            f = np.where(real, np.float32(448) * (np.float32(1) / a), np.float32(0)).astype(np.float32)
             s = np.where(real, a / np.float32(448), np.float32(0)).astype(np.float32)
         c = torch.from_numpy((xb * f).clip(-448, 448)).to(torch.float8_e4m3fn).double().cuda()
         wb = w[:, 128 * b:128 * b + 128] * scales[:, b].double().repeat_interleave(128)[:N, None]
