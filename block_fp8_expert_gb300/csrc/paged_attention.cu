@@ -13,27 +13,36 @@ namespace moe {
 
 namespace {
 
-constexpr int kTile = 16;     // tokens per tile: one MMA K step of the second product
 constexpr int kWarps = 4;     // warps per CTA, each with its own tiles and pipeline
-constexpr int kRows = 16;     // query heads per CTA segment (MMA M)
+constexpr int kMaxRows = 16;  // query heads per CTA segment at most
+constexpr int kMinUnits = 8;  // least share of a CTA, in units (below)
+// What a segment costs a CTA beside its tiles (table and query loads, filling
+// and draining the pipeline, the join), in tiles.
+constexpr int kSegCost = 8;
 // E4M3: the largest weight times value scale is held as 2^15, so that fp16
 // keeps weights down to 2^-39 of it (a long cache's many small ones)
 constexpr float kWTop = 15.f;
-constexpr int kMinTiles = 8;  // least tiles per CTA: shorter shares cost more in joining
 
-template <int D, bool E4M3>
+// NH: groups of 8 query heads per CTA segment (the MMA's N).
+template <int D, bool E4M3, int NH>
 struct AttnShape {
+  static constexpr int kRows = 8 * NH;
   static constexpr int kRowBytes = E4M3 ? D : 2 * D;
+  // 16-token MMA tiles per step: about 8 KB of keys and values
+  static constexpr int MT = kRowBytes >= 256 ? 1 : 2;
+  static constexpr int kTile = 16 * MT;
   static constexpr int kStage = 2 * kTile * kRowBytes + (E4M3 ? 2 * kTile * 4 : 0);
-  static constexpr int kStages = kStage >= 8192 ? 3 : (24576 / kStage < 8 ? 24576 / kStage : 8);
+  static constexpr int kCtasPerSm = D == 256 ? (E4M3 ? 2 : 1) : (NH == 1 ? 3 : 2);
+  static constexpr int kStagesFit = (220 * 1024 / kCtasPerSm - (D == 256 ? 8192 * NH : 0)) / (kWarps * kStage);
+  static constexpr int kStages = kStagesFit < 2 ? 2 : (kStagesFit > 6 ? 6 : kStagesFit);
   static constexpr int kWarpBytes = kStages * kStage;
   // the query fragments of D = 256 live in shared memory: with them in
-  // registers next to 128 accumulators a thread would need more than 255
+  // registers next to its accumulators a thread would need more than 255
   static constexpr bool kQShared = D == 256;
-  static constexpr int kQBytes = kQShared ? (D / 16) * 32 * 16 : 0;
+  static constexpr int kQBytes = kQShared ? (D / 16) * NH * 32 * 8 : 0;
   static constexpr int kSmem = kWarps * kWarpBytes + kQBytes;
-  static constexpr int kCtasPerSm = kSmem > 113 * 1024 ? 1 : 2;
   static_assert(kWarpBytes >= kRows * D * 4, "the join of the warps reuses the stages");
+  static_assert(kSmem + 2048 <= 227 * 1024 / kCtasPerSm, "shared memory");
 };
 
 struct AttnArgs {
@@ -42,10 +51,12 @@ struct AttnArgs {
   const int32_t* block_table;
   const int32_t* seq_lens;
   moe_attn_dims d;
-  int G, gtiles, HG;  // query heads per kv head, 16-head tiles of them, Hkv * gtiles
+  int G, rows, gtiles, HG;  // query heads per kv head; a segment's heads; segments per kv head, in all
+  int tile;                 // tokens per tile
+  uint32_t ps_mul, ps_shift;  // t / page_size = umulhi(t, ps_mul) >> ps_shift (page_size > 1)
   uint16_t* out;
-  float* part_o;   // [2 * grid][16][D]
-  float* part_ml;  // [2 * grid][2][16]
+  float* part_o;   // [2 * grid][kMaxRows][D]
+  float* part_ml;  // [2 * grid][2][kMaxRows]
   int grid;
   int32_t* status;
 };
@@ -60,17 +71,27 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
   Span s;
   s.len = (int)min((long long)max(len0, 0), cap);
   s.lo = a.d.window > 0 ? max(0, s.len - a.d.window) : 0;
-  s.first = s.lo / kTile;
-  s.tiles = (int)(((long long)s.len + kTile - 1) / kTile) - s.first;
+  s.first = s.lo / a.tile;
+  s.tiles = (int)(((long long)s.len + a.tile - 1) / a.tile) - s.first;
   if (s.len <= 0) s.tiles = 0;
   return s;
 }
 
-// The tiles of all sequences and heads in one row, sequence-major, then head:
-// CTA c takes tiles [c share, (c + 1) share).  A sequence's tiles for one
-// head are a segment; one that crosses CTAs is joined by k_attn_join.  Every
-// thread of the CTA calls this; it returns the sequence that holds tile
-// `want` and the tiles (times heads) before it, and the total.
+// A sequence's tiles for one tile of heads are a segment of tiles + kSegCost
+// units; empty sequences have none.  All segments lie in one row, sequence-
+// major, then head: CTA c takes units [c share, (c + 1) share), and with them
+// the same part of the segment's tiles.  A segment that crosses CTAs is
+// joined by k_attn_join.  So ragged batches, many short and one long sequence
+// alike, give every CTA the same time.
+__device__ __forceinline__ int units_of(const Span& s) { return s.tiles ? s.tiles + kSegCost : 0; }
+// The tile at which unit u of a segment begins.
+__device__ __forceinline__ int tile_at(const Span& s, long long u) {
+  return (int)(u * s.tiles / units_of(s));
+}
+
+// Every thread of the CTA calls this; it finds the sequence that holds unit
+// `want * share` (by_share) or is number `want`, with the units of all the
+// sequences before it, and returns all segments' units.
 struct Place {
   int b;
   long long before;
@@ -81,7 +102,7 @@ __device__ __forceinline__ long long plan(const AttnArgs& a, long long* s_scan, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
   const int per = cdiv(a.d.B, n), b0 = min(tid * per, a.d.B), b1 = min(b0 + per, a.d.B);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += span_of(a, b).tiles;
+  for (int b = b0; b < b1; ++b) mine += units_of(span_of(a, b));
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -97,14 +118,14 @@ __device__ __forceinline__ long long plan(const AttnArgs& a, long long* s_scan, 
     total += s_scan[w];
   }
   total *= a.HG;
-  share = max((long long)kMinTiles, (total + a.grid - 1) / a.grid);
+  share = max((long long)kMinUnits, (total + a.grid - 1) / a.grid);
   if (by_share) {
     const long long t0 = want * share;
     if (before * a.HG <= t0 && t0 < (before + mine) * a.HG) {
       long long at0 = before;
       int b = b0;
       for (; b < b1; ++b) {
-        const int k = span_of(a, b).tiles;
+        const int k = units_of(span_of(a, b));
         if (t0 < (at0 + k) * a.HG) break;
         at0 += k;
       }
@@ -112,7 +133,7 @@ __device__ __forceinline__ long long plan(const AttnArgs& a, long long* s_scan, 
     }
   } else if (want >= b0 && want < b1) {
     long long at0 = before;
-    for (int b = b0; b < (int)want; ++b) at0 += span_of(a, b).tiles;
+    for (int b = b0; b < (int)want; ++b) at0 += units_of(span_of(a, b));
     *s_place = Place{(int)want, at0 * a.HG};
   }
   __syncthreads();
@@ -131,6 +152,12 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// An 8 x 8 matrix of 16-bit values held as one MMA fragment, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -173,11 +200,22 @@ __device__ __forceinline__ int v_chunk(int r, int j) {
 
 }  // namespace
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32, AttnShape<D, E4M3>::kCtasPerSm)
+// Both products take tokens or dimensions as the MMA's M and the query heads
+// as its N = 8, so up to eight heads of a key/value head waste nothing:
+//   scores   S^T[token, head] = K Q^T     A = 16 tokens x 16 dimensions
+//   outputs  O^T[dim, head]  += V^T P^T   A = 16 dimensions x 16 tokens
+// The weights P^T leave the first product as accumulators with a token per
+// row and enter the second as its B operand with a token per k: one 8 x 8
+// transposition (movmatrix) per 8 tokens.  bf16 operands come out of shared
+// memory by ldmatrix; E4M3 codes by 16-byte loads of a permuted order of the
+// dimensions (the same for q and k; free for the output) and an exact
+// conversion to fp16, the values' codes of two tokens paired by byte permutes.
+template <int D, bool E4M3, int NH>
+__global__ void __launch_bounds__(kWarps * 32, AttnShape<D, E4M3, NH>::kCtasPerSm)
 k_paged_attention(const AttnArgs a) {
-  using S = AttnShape<D, E4M3>;
+  using S = AttnShape<D, E4M3, NH>;
   constexpr unsigned kAll = 0xffffffffu;
+  constexpr int MT = S::MT, kTile = S::kTile, kRows = S::kRows;
   constexpr int LPR = S::kRowBytes / 16;       // lanes (16-byte chunks) per token row
   constexpr int NI = kTile * LPR / 32;         // copies per lane and matrix
   constexpr int DPL = D == 64 ? 8 : 16;        // E4M3: dimensions per lane of the second product
@@ -190,7 +228,7 @@ k_paged_attention(const AttnArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   const uint32_t stages = smem_u32(smem) + warp * S::kWarpBytes;
-  uint8_t* const qshared = smem + kWarps * S::kWarpBytes;
+  uint2* const qshared = reinterpret_cast<uint2*>(smem + kWarps * S::kWarpBytes);
 
   Place at;
   long long share;
@@ -200,298 +238,361 @@ k_paged_attention(const AttnArgs a) {
   if (cur >= end) return;
   int b = at.b;
   Span sp = span_of(a, b);
-  const long long first_tile = cur;
+  const long long first_unit = cur;
+  const float scale2 = a.d.scale * 1.44269504088896341f;
 
   while (cur < end) {
-    while (cur >= at.before + (long long)sp.tiles * a.HG) {  // next sequence with a token
-      at.before += (long long)sp.tiles * a.HG;
+    while (cur >= at.before + (long long)units_of(sp) * a.HG) {  // next sequence with a token
+      at.before += (long long)units_of(sp) * a.HG;
       sp = span_of(a, ++b);
     }
     if (tid == 0 && a.seq_lens[b] != sp.len) raise_status(a.status, MOE_DEV_BAD_PAGE);
-    const int hg = (int)((cur - at.before) / sp.tiles);
-    const long long s0 = at.before + (long long)hg * sp.tiles, s1 = s0 + sp.tiles;
+    const int units = units_of(sp);
+    const int hg = (int)((cur - at.before) / units);
+    const long long s0 = at.before + (long long)hg * units, s1 = s0 + units;
     const long long stop = min(s1, end);
-    const int i0 = (int)(cur - s0), i1 = (int)(stop - s0);  // tiles of the segment
+    const int i0 = tile_at(sp, cur - s0), i1 = tile_at(sp, stop - s0);  // tiles of the segment
     const int hkv = hg / a.gtiles, row0 = (hg % a.gtiles) * kRows;
     const int rows = min(kRows, a.G - row0);
 
     // ---- this warp's tiles: i0 + warp, + kWarps, ...
     const int n = i1 - i0 > warp ? (i1 - i0 - warp + kWarps - 1) / kWarps : 0;
     const int32_t* table = a.block_table + (size_t)b * a.d.table_stride;
-    const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k);
-    const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v);
-    // lane i (and i + 16) looks up token i of tile j: its page, or -1
-    auto token_of = [&](int j) { return (sp.first + i0 + warp + j * kWarps) * kTile + (lane & 15); };
-    auto page_of = [&](int j) {
-      if (j >= n) return -1;
-      const int tok = token_of(j);
-      if (tok < sp.lo || tok >= sp.len) return -1;
-      const int p = __ldg(table + (unsigned)tok / (unsigned)a.c.page_size);
-      if (p >= 0 && p < a.c.pages) return p;
-      raise_status(a.status, MOE_DEV_BAD_PAGE);
-      return -1;
+    const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) +
+                           (long long)hkv * a.c.head_stride * (E4M3 ? 1 : 2);
+    const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) +
+                           (long long)hkv * a.c.head_stride * (E4M3 ? 1 : 2);
+    // lane i (and i + 16 of a 16-token tile) looks up token i of tile j: its
+    // page (-1: no such token) and its place in the page
+    struct Spot {
+      int page, inpage;
     };
-    auto issue = [&](int j, int page) {
+    auto look_up = [&](int j) {
+      Spot r{-1, 0};
+      if (j >= n) return r;
+      const int tok = (sp.first + i0 + warp + j * kWarps) * kTile + (lane & (kTile - 1));
+      if (tok < sp.lo || tok >= sp.len) return r;
+      const uint32_t idx = a.c.page_size > 1 ? __umulhi((uint32_t)tok, a.ps_mul) >> a.ps_shift : tok;
+      r.inpage = tok - (int)(idx * (uint32_t)a.c.page_size);
+      const int p = __ldg(table + idx);
+      if (p >= 0 && p < a.c.pages)
+        r.page = p;
+      else
+        raise_status(a.status, MOE_DEV_BAD_PAGE);
+      return r;
+    };
+    auto issue = [&](int j, const Spot& sl) {
       if (j < n) {
-        const int inpage = (int)((unsigned)token_of(j) % (unsigned)a.c.page_size);
-        const long long off =
-            page < 0 ? -1
-                     : (long long)page * a.c.page_stride + (long long)hkv * a.c.head_stride +
-                           (long long)inpage * a.c.token_stride;
+        const bool real = sl.page >= 0;
+        const long long off = real ? ((long long)sl.page * a.c.page_stride +
+                                      (long long)sl.inpage * a.c.token_stride) *
+                                         (E4M3 ? 1 : 2)
+                                   : -1;
         const uint32_t kt = stages + (j % S::kStages) * S::kStage, vt = kt + kTile * S::kRowBytes;
-        const unsigned seen = __ballot_sync(kAll, page >= 0);
+        const unsigned seen = __ballot_sync(kAll, real);
         if (lane == 0) s_seen[warp][j % S::kStages] = seen;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           const int r = i * (32 / LPR) + lane / LPR, ch = lane % LPR;
           const long long o = __shfl_sync(kAll, off, r);
           const bool ok = o >= 0;
-          const long long byte = (ok ? o * (E4M3 ? 1 : 2) : 0) + ch * 16;
+          const long long byte = (ok ? o : 0) + ch * 16;
           cp_async16_z(kt + r * S::kRowBytes + k_chunk<D, E4M3>(r, ch) * 16, kbase + byte, ok);
           cp_async16_z(vt + r * S::kRowBytes + v_chunk<D, E4M3>(r, ch) * 16, vbase + byte, ok);
         }
-        if (E4M3) {  // lanes 0-15 the keys' scales, 16-31 the values'
-          const long long so = page < 0 ? 0
-                                        : (long long)page * a.c.scale_page_stride +
-                                              (long long)hkv * a.c.scale_head_stride +
-                                              (long long)inpage * a.c.scale_token_stride;
-          cp_async4_z(vt + kTile * S::kRowBytes + lane * 4,
-                      (lane < 16 ? a.c.k_scale : a.c.v_scale) + so, page >= 0);
+        if (E4M3) {  // the scales: kTile of the keys, then kTile of the values
+          const long long so = real ? (long long)sl.page * a.c.scale_page_stride +
+                                          (long long)hkv * a.c.scale_head_stride +
+                                          (long long)sl.inpage * a.c.scale_token_stride
+                                    : 0;
+          const uint32_t sc = vt + kTile * S::kRowBytes + lane * 4;
+          if (MT == 1) {  // lanes 0-15 the keys', 16-31 the values'
+            cp_async4_z(sc, (lane < 16 ? a.c.k_scale : a.c.v_scale) + so, real);
+          } else {
+            cp_async4_z(sc, a.c.k_scale + so, real);
+            cp_async4_z(sc + kTile * 4, a.c.v_scale + so, real);
+          }
         }
       }
       cp_async_commit();
     };
-    int page = page_of(0);
+    Spot spot = look_up(0);
+
+    // ---- queries: the B operand, head 8 nh + g, loaded beside the first page
+    // numbers.  E4M3: chunk of 64 columns ks / 4, step ks % 4: columns 16 c +
+    // 4 step + {0,1}, {2,3}; the four lanes of a quad hold a whole head.
+    const uint16_t* q0 = a.q + (size_t)b * a.d.q_stride + (size_t)(hkv * a.G + row0) * D;
+    uint2 qr[D / 16][NH];
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      const bool real = 8 * nh + g < rows;
+      const uint16_t* p = q0 + (real ? (size_t)(8 * nh + g) * D : 0);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        if (E4M3) {
+          qr[ks][nh] = __ldg(reinterpret_cast<const uint2*>(p + 64 * (ks >> 2) + 16 * c + 4 * (ks & 3)));
+        } else {
+          qr[ks][nh].x = __ldg(reinterpret_cast<const uint32_t*>(p + 16 * ks + 2 * c));
+          qr[ks][nh].y = __ldg(reinterpret_cast<const uint32_t*>(p + 16 * ks + 2 * c + 8));
+        }
+        if (!real) qr[ks][nh] = make_uint2(0u, 0u);
+      }
+    }
 #pragma unroll 1
     for (int j = 0; j < S::kStages - 1; ++j) {
-      const int next = page_of(j + 1);
-      issue(j, page);
-      page = next;
+      const Spot next = look_up(j + 1);
+      issue(j, spot);
+      spot = next;
     }
-
-    // ---- queries: the A operand, rows g and g + 8
-    const uint16_t* q0 = a.q + (size_t)b * a.d.q_stride + (size_t)(hkv * a.G + row0) * D;
-    float qf[2] = {a.d.scale * 1.44269504088896341f, a.d.scale * 1.44269504088896341f};
-    float qn[2] = {1.f, 1.f};
-    if (E4M3) {
-      // fp16 operands: each row times a power of two that puts its largest
-      // magnitude into [2^14, 2^15), undone on the scores (exact)
+    float qf[NH][2];  // factor on the scores of heads 8 nh + 2 c + {0, 1}
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int nh = 0; nh < NH; ++nh) {
+      qf[nh][0] = qf[nh][1] = scale2;
+      if (E4M3) {
+        // fp16 operands: each head times a power of two that puts its largest
+        // magnitude into [2^14, 2^15), undone on the scores (exact)
         uint32_t m = 0;
-        if (g + 8 * h < rows)
-          for (int i = c * 8; i < D; i += 32) {
-            const uint4 v = ldg16(q0 + (size_t)(g + 8 * h) * D + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) m = max(m, max(w[u] & 0x7FFFu, (w[u] >> 16) & 0x7FFFu));
-          }
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint2 v = qr[ks][nh];
+          m = max(m, max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)));
+        }
         m = max(m, __shfl_xor_sync(kAll, m, 1));
         m = max(m, __shfl_xor_sync(kAll, m, 2));
         const int E = min(exp_of_bits(m << 16), 126);
-        qn[h] = pow2f(kGroupTop - E);
-        qf[h] *= pow2f(E - kGroupTop);
+        const float f = pow2f(kGroupTop - E), back = pow2f(E - kGroupTop);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint2& v = qr[ks][nh];
+          v.x = pack_f16x2(bf16_lo(v.x) * f, bf16_hi(v.x) * f);
+          v.y = pack_f16x2(bf16_lo(v.y) * f, bf16_hi(v.y) * f);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) qf[nh][u] *= __shfl_sync(kAll, back, 4 * (2 * c + u));
       }
     }
-    auto q_frag = [&](int ks) {
-      uint32_t f[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = g + 8 * (u & 1);
-        int d0;
-        if (E4M3)  // chunk of 64 columns ks / 4, step ks % 4: columns 16 c + 4 step + {0,1}, {2,3}
-          d0 = 64 * (ks >> 2) + 16 * c + 4 * (ks & 3) + 2 * (u >> 1);
-        else
-          d0 = 16 * ks + 2 * c + 8 * (u >> 1);
-        uint32_t v = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + (size_t)r * D + d0)) : 0u;
-        if (E4M3) v = pack_f16x2(bf16_lo(v) * qn[u & 1], bf16_hi(v) * qn[u & 1]);
-        f[u] = v;
-      }
-      return make_uint4(f[0], f[1], f[2], f[3]);
-    };
-    uint4 qr[S::kQShared ? 1 : D / 16];
     if (S::kQShared) {
-      for (int ks = warp; ks < D / 16; ks += kWarps)
-        reinterpret_cast<uint4*>(qshared)[ks * 32 + lane] = q_frag(ks);
-      __syncthreads();
-    } else {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) qr[S::kQShared ? 0 : ks] = q_frag(ks);
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+          if ((ks * NH + nh) % kWarps == warp) qshared[(ks * NH + nh) * 32 + lane] = qr[ks][nh];
+      __syncthreads();
     }
+    auto q_at = [&](int ks, int nh) {
+      return S::kQShared ? qshared[(ks * NH + nh) * 32 + lane] : qr[ks][nh];
+    };
 
     // ---- one pass over the tiles
-    float o[D / 8][4];
+    float o[D / 16][NH][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) o[i][u] = 0.f;
-    // m: running maximum of the scores; w: of score + log2(value scale), the
-    // exponent the accumulators are kept at (bf16: the same as m)
-    float m[2] = {-INFINITY, -INFINITY}, w[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[i][nh][u] = 0.f;
+    // per head 8 nh + 2 c + u: m, the running maximum of the scores, w, that of
+    // score + log2(value scale), the exponent the accumulators are kept at
+    // (bf16: the same as m), and l, this lane's part of the weights' sum
+    float m[NH][2], w[NH][2], l[NH][2];
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        m[nh][u] = w[nh][u] = -INFINITY;
+        l[nh][u] = 0.f;
+      }
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const int next = page_of(j + S::kStages);
-      issue(j + S::kStages - 1, page);
-      page = next;
+      const Spot next = look_up(j + S::kStages);
+      issue(j + S::kStages - 1, spot);
+      spot = next;
       cp_async_wait<S::kStages - 1>();
       __syncwarp();
       const uint32_t kt = stages + (j % S::kStages) * S::kStage, vt = kt + kTile * S::kRowBytes;
-      float s[2][4];
+      float s[MT][NH][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) s[nt][u] = 0.f;
-      auto q_at = [&](int ks) {
-        return S::kQShared ? reinterpret_cast<const uint4*>(qshared)[ks * 32 + lane]
-                           : qr[S::kQShared ? 0 : ks];
-      };
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) s[mt][nh][u] = 0.f;
       if (E4M3) {
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          uint32_t kb[2][8];
+        for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const int r = 8 * nt + g;
-            decode16_f16(lds128(kt + r * S::kRowBytes + k_chunk<D, E4M3>(r, 4 * h + c) * 16), kb[nt]);
-          }
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t lo[8], hi[8];  // tokens 16 mt + g and + 8
+            const int r = 16 * mt + g;
+            decode16_f16(lds128(kt + r * S::kRowBytes + k_chunk<D, E4M3>(r, 4 * h + c) * 16), lo);
+            decode16_f16(lds128(kt + (r + 8) * S::kRowBytes + k_chunk<D, E4M3>(r + 8, 4 * h + c) * 16), hi);
 #pragma unroll
-          for (int st = 0; st < 4; ++st) {
-            const uint4 qv = q_at(4 * h + st);
-            const uint32_t av[4] = {qv.x, qv.y, qv.z, qv.w};
+            for (int st = 0; st < 4; ++st) {
+              const uint32_t av[4] = {lo[2 * st], hi[2 * st], lo[2 * st + 1], hi[2 * st + 1]};
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const uint32_t bv[2] = {kb[nt][2 * st], kb[nt][2 * st + 1]};
-              mma_f16_16x8x16(s[nt], av, bv);
+              for (int nh = 0; nh < NH; ++nh) {
+                const uint2 qv = q_at(4 * h + st, nh);
+                const uint32_t bv[2] = {qv.x, qv.y};
+                mma_f16_16x8x16(s[mt][nh], av, bv);
+              }
             }
           }
-        }
       } else {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint4 qv = q_at(ks);
-          const uint32_t av[4] = {qv.x, qv.y, qv.z, qv.w};
-          const int mi = lane >> 3, r = (mi >> 1) * 8 + (lane & 7);
-          uint32_t kb[4];
-          ldmatrix_x4(kt + r * S::kRowBytes + k_chunk<D, E4M3>(r, 2 * ks + (mi & 1)) * 16, kb);
-          const uint32_t b0[2] = {kb[0], kb[1]}, b1[2] = {kb[2], kb[3]};
-          mma_bf16_16x8x16(s[0], av, b0);
-          mma_bf16_16x8x16(s[1], av, b1);
-        }
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            // matrices: tokens 0-7 and 8-15 of dimensions 0-7, then of 8-15
+            const int mi = lane >> 3, r = 16 * mt + (mi & 1) * 8 + (lane & 7);
+            uint32_t av[4];
+            ldmatrix_x4(kt + r * S::kRowBytes + k_chunk<D, E4M3>(r, 2 * ks + (mi >> 1)) * 16, av);
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) {
+              const uint2 qv = q_at(ks, nh);
+              const uint32_t bv[2] = {qv.x, qv.y};
+              mma_bf16_16x8x16(s[mt][nh], av, bv);
+            }
+          }
       }
-      // scores of tokens 8 nt + 2 c + {0, 1}; -inf where there is none
-      float lv[2][2];  // E4M3: log2 of the values' scales
+      // scores of tokens 16 mt + g + 8 x; -inf where there is none
       const unsigned seen = s_seen[warp][j % S::kStages];
+      float lv[MT][2];  // E4M3: log2 of the values' scales
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int tt = 8 * nt + 2 * c + u;
+        for (int x = 0; x < 2; ++x) {
+          const int tt = 16 * mt + 8 * x + g;
           float ks = 1.f;
-          lv[nt][u] = 0.f;
+          lv[mt][x] = 0.f;
           if (E4M3) {
             const float* sc = reinterpret_cast<const float*>(
                 smem + (vt - smem_u32(smem)) + kTile * S::kRowBytes);
             ks = sc[tt];
-            lv[nt][u] = __log2f(sc[16 + tt]);
+            lv[mt][x] = __log2f(sc[kTile + tt]);
           }
           const bool ok = (seen >> tt) & 1u;
-          s[nt][u] = ok ? s[nt][u] * (qf[0] * ks) : -INFINITY;
-          s[nt][2 + u] = ok ? s[nt][2 + u] * (qf[1] * ks) : -INFINITY;
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float& v = s[mt][nh][2 * x + u];
+              v = ok ? v * (E4M3 ? qf[nh][u] * ks : qf[nh][u]) : -INFINITY;
+            }
         }
-      uint32_t pa[4];
+      uint32_t pb[MT][NH][2];  // the weights as the second product's B operand
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float mx = m[h], wx = w[h];
+      for (int nh = 0; nh < NH; ++nh) {
+        float mx[2], wx[2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int u = 0; u < 2; ++u) {
+          mx[u] = m[nh][u];
+          wx[u] = w[nh][u];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float v = s[mt][nh][2 * x + u];
+              mx[u] = fmaxf(mx[u], v);
+              if (E4M3) wx[u] = fmaxf(wx[u], v + lv[mt][x]);
+            }
+        }
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            mx = fmaxf(mx, s[nt][2 * h + u]);
-            if (E4M3) wx = fmaxf(wx, s[nt][2 * h + u] + lv[nt][u]);
+            mx[u] = fmaxf(mx[u], __shfl_xor_sync(kAll, mx[u], sh));
+            if (E4M3) wx[u] = fmaxf(wx[u], __shfl_xor_sync(kAll, wx[u], sh));
           }
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
-        if (E4M3) {
-          wx = fmaxf(wx, __shfl_xor_sync(kAll, wx, 1));
-          wx = fmaxf(wx, __shfl_xor_sync(kAll, wx, 2));
-        } else {
-          wx = mx;
+        float ms[2], ws[2];
+        bool moved = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (!E4M3) wx[u] = mx[u];
+          ms[u] = mx[u] == -INFINITY ? 0.f : mx[u];
+          ws[u] = wx[u] == -INFINITY ? 0.f : wx[u];
+          moved |= mx[u] != m[nh][u] || wx[u] != w[nh][u];
         }
-        // the maxima moved: the sums so far are scaled down to them
-        const float ms = mx == -INFINITY ? 0.f : mx, ws = wx == -INFINITY ? 0.f : wx;
-        if (mx != m[h]) l[h] *= exp2_fast(m[h] - ms);
-        if (__any_sync(kAll, wx != w[h])) {
-          const float f = exp2_fast(w[h] - ws);
+        if (__any_sync(kAll, moved)) {  // the sums so far are scaled to the new maxima
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][2 * h] *= f;
-            o[i][2 * h + 1] *= f;
-          }
-        }
-        m[h] = mx;
-        w[h] = wx;
+          for (int u = 0; u < 2; ++u) {
+            const float f = exp2_fast(w[nh][u] - ws[u]);
+            l[nh][u] *= E4M3 ? exp2_fast(m[nh][u] - ms[u]) : f;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const float s_a = s[nt][2 * h], s_b = s[nt][2 * h + 1];
-          uint32_t p;
-          if (E4M3) {
-            l[h] += exp2_fast(s_a - ms) + exp2_fast(s_b - ms);
-            p = pack_f16x2(exp2_fast(s_a + lv[nt][0] - ws + kWTop),
-                           exp2_fast(s_b + lv[nt][1] - ws + kWTop));
-          } else {
-            p = pack_bf16x2(exp2_fast(s_a - ms), exp2_fast(s_b - ms));
-            l[h] += bf16_lo(p) + bf16_hi(p);  // the weights as they are multiplied
-          }
-          pa[2 * nt + h] = p;
-        }
-      }
-      if (E4M3) {
-#pragma unroll
-        for (int blk = 0; blk < (D == 256 ? 2 : 1); ++blk) {
-          // codes of tokens 2c, 2c + 1, 2c + 8, 2c + 9, this lane's DPL dimensions
-          uint32_t v[4][DPL / 4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r = 2 * c + (u & 1) + 8 * (u >> 1);
-            if (D == 64) {
-              const uint32_t addr = vt + r * S::kRowBytes + v_chunk<D, E4M3>(r, g >> 1) * 16 + (g & 1) * 8;
-              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
-                           : "=r"(v[u][0]), "=r"(v[u][1])
-                           : "r"(addr)
-                           : "memory");
-            } else {
-              const uint4 x = lds128(vt + r * S::kRowBytes + v_chunk<D, E4M3>(r, 8 * blk + g) * 16);
-              v[u][0] = x.x;
-              v[u][1] = x.y;
-              v[u][DPL / 4 - 2] = x.z;
-              v[u][DPL / 4 - 1] = x.w;
+            for (int i = 0; i < D / 16; ++i) {
+              o[i][nh][u] *= f;
+              o[i][nh][2 + u] *= f;
             }
+            m[nh][u] = mx[u];
+            w[nh][u] = wx[u];
           }
+        }
 #pragma unroll
-          for (int i = 0; i < DPL / 4; ++i) {
-            // bytes (token a, token b) of dimensions 4 i .. 4 i + 3
-            const uint32_t lo01 = __byte_perm(v[0][i], v[1][i], 0x5140);
-            const uint32_t lo23 = __byte_perm(v[0][i], v[1][i], 0x7362);
-            const uint32_t hi01 = __byte_perm(v[2][i], v[3][i], 0x5140);
-            const uint32_t hi23 = __byte_perm(v[2][i], v[3][i], 0x7362);
-            const uint32_t lo[4] = {lo01 & 0xffffu, lo01 >> 16, lo23 & 0xffffu, lo23 >> 16};
-            const uint32_t hi[4] = {hi01 & 0xffffu, hi01 >> 16, hi23 & 0xffffu, hi23 >> 16};
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float sa = s[mt][nh][2 * x], sb = s[mt][nh][2 * x + 1];
+            uint32_t p;
+            if (E4M3) {
+              l[nh][0] += exp2_fast(sa - ms[0]);
+              l[nh][1] += exp2_fast(sb - ms[1]);
+              p = pack_f16x2(exp2_fast(sa + lv[mt][x] - ws[0] + kWTop),
+                             exp2_fast(sb + lv[mt][x] - ws[1] + kWTop));
+            } else {
+              p = pack_bf16x2(exp2_fast(sa - ms[0]), exp2_fast(sb - ms[1]));
+              l[nh][0] += bf16_lo(p);  // the weights as they are multiplied
+              l[nh][1] += bf16_hi(p);
+            }
+            pb[mt][nh][x] = transpose8x8(p);
+          }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (E4M3) {
+#pragma unroll
+          for (int blk = 0; blk < (D == 256 ? 2 : 1); ++blk) {
+            // codes of tokens 2c, 2c + 1, 2c + 8, 2c + 9, this lane's DPL dimensions
+            uint32_t v[4][DPL / 4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const uint32_t bv[2] = {e4m3x2_to_f16x2(lo[u]), e4m3x2_to_f16x2(hi[u])};
-              mma_f16_16x8x16(o[DPL * blk + 4 * i + u], pa, bv);
+              const int r = 16 * mt + 2 * c + (u & 1) + 8 * (u >> 1);
+              if (D == 64) {
+                const uint32_t addr =
+                    vt + r * S::kRowBytes + v_chunk<D, E4M3>(r, g >> 1) * 16 + (g & 1) * 8;
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
+                             : "=r"(v[u][0]), "=r"(v[u][1])
+                             : "r"(addr)
+                             : "memory");
+              } else {
+                const uint4 x = lds128(vt + r * S::kRowBytes + v_chunk<D, E4M3>(r, 8 * blk + g) * 16);
+                v[u][0] = x.x;
+                v[u][1] = x.y;
+                v[u][DPL / 4 - 2] = x.z;
+                v[u][DPL / 4 - 1] = x.w;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < DPL / 2; ++i) {
+              // dimensions 2 i and 2 i + 1: bytes (token a, token b) of each
+              const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+              const uint32_t ta = __byte_perm(v[0][i / 2], v[1][i / 2], sel);
+              const uint32_t tb = __byte_perm(v[2][i / 2], v[3][i / 2], sel);
+              const uint32_t av[4] = {e4m3x2_to_f16x2(ta & 0xffffu), e4m3x2_to_f16x2(ta >> 16),
+                                      e4m3x2_to_f16x2(tb & 0xffffu), e4m3x2_to_f16x2(tb >> 16)};
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh)
+                mma_f16_16x8x16(o[(DPL / 2) * blk + i][nh], av, pb[mt][nh]);
             }
           }
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int jj = 0; jj < D / 16; ++jj) {
-          const int mi = lane >> 3, r = (mi & 1) * 8 + (lane & 7);
-          uint32_t vb[4];
-          ldmatrix_x4_trans(vt + r * S::kRowBytes + v_chunk<D, E4M3>(r, 2 * jj + (mi >> 1)) * 16, vb);
-          const uint32_t b0[2] = {vb[0], vb[1]}, b1[2] = {vb[2], vb[3]};
-          mma_bf16_16x8x16(o[2 * jj], pa, b0);
-          mma_bf16_16x8x16(o[2 * jj + 1], pa, b1);
+          for (int i = 0; i < D / 16; ++i) {
+            // matrices: dimensions 0-7 and 8-15 of tokens 0-7, then of 8-15
+            const int mi = lane >> 3, r = 16 * mt + (mi >> 1) * 8 + (lane & 7);
+            uint32_t av[4];
+            ldmatrix_x4_trans(vt + r * S::kRowBytes + v_chunk<D, E4M3>(r, 2 * i + (mi & 1)) * 16, av);
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) mma_bf16_16x8x16(o[i][nh], av, pb[mt][nh]);
+          }
         }
       }
       __syncwarp();
@@ -499,34 +600,37 @@ k_paged_attention(const AttnArgs a) {
     cp_async_wait<0>();
 
     // ---- join the four warps (their stages are drained)
-    float* mine = reinterpret_cast<float*>(smem + warp * S::kWarpBytes);  // [16][D]
+    float* mine = reinterpret_cast<float*>(smem + warp * S::kWarpBytes);  // [kRows][D]
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(kAll, l[h], 1);
-      l[h] += __shfl_xor_sync(kAll, l[h], 2);
-      if (c == 0) {
-        s_m[warp][g + 8 * h] = m[h];
-        s_l[warp][g + 8 * h] = l[h];
-      }
-      // accumulators from exponent w to exponent m
-      const float f = (E4M3 && w[h] != -INFINITY) ? exp2f(w[h] - m[h] - kWTop) : 1.f;
+    for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        int d0, d1;
-        if (E4M3) {
-          d0 = 128 * (i / DPL) * (D == 64 ? 0 : 1) + DPL * 2 * c + i % DPL;
-          d1 = d0 + DPL;
-        } else {
-          d0 = 8 * i + 2 * c;
-          d1 = d0 + 1;
+      for (int u = 0; u < 2; ++u) {
+        const int r = 8 * nh + 2 * c + u;
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) l[nh][u] += __shfl_xor_sync(kAll, l[nh][u], sh);
+        if (g == 0) {
+          s_m[warp][r] = m[nh][u];
+          s_l[warp][r] = l[nh][u];
         }
-        mine[(g + 8 * h) * D + d0] = o[i][2 * h] * f;
-        mine[(g + 8 * h) * D + d1] = o[i][2 * h + 1] * f;
+        // accumulators from exponent w to exponent m
+        const float f = (E4M3 && w[nh][u] != -INFINITY) ? exp2f(w[nh][u] - m[nh][u] - kWTop) : 1.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          int d0, d1;
+          if (E4M3) {
+            d0 = 128 * (i / (DPL / 2)) * (D == 64 ? 0 : 1) + DPL * g + 2 * (i % (DPL / 2));
+            d1 = d0 + 1;
+          } else {
+            d0 = 16 * i + g;
+            d1 = d0 + 8;
+          }
+          mine[r * D + d0] = o[i][nh][u] * f;
+          mine[r * D + d1] = o[i][nh][2 + u] * f;
+        }
       }
-    }
     __syncthreads();
     const bool whole = cur == s0 && stop == s1;
-    const int slot = 2 * blockIdx.x + (s0 <= first_tile ? 0 : 1);
+    const int slot = 2 * blockIdx.x + (s0 <= first_unit ? 0 : 1);
     for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
       const int r = e / (D / 4), d4 = e % (D / 4);
       float M = s_m[0][r];
@@ -553,10 +657,10 @@ k_paged_attention(const AttnArgs a) {
         *reinterpret_cast<uint2*>(a.out + (size_t)b * a.d.out_stride +
                                   (size_t)(hkv * a.G + row0 + r) * D + 4 * d4) = r2;
       } else {
-        *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kRows + r) * D + 4 * d4) = acc;
+        *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kMaxRows + r) * D + 4 * d4) = acc;
         if (d4 == 0) {
-          a.part_ml[(size_t)slot * 2 * kRows + r] = M;
-          a.part_ml[(size_t)slot * 2 * kRows + kRows + r] = L;
+          a.part_ml[(size_t)slot * 2 * kMaxRows + r] = M;
+          a.part_ml[(size_t)slot * 2 * kMaxRows + kMaxRows + r] = L;
         }
       }
     }
@@ -567,20 +671,20 @@ k_paged_attention(const AttnArgs a) {
 
 // Joins the parts of every segment that crosses CTAs, in CTA order, and
 // writes the zeros of empty sequences.  One CTA per (sequence, head tile) and
-// query head: the parts' maxima and sums first, then their outputs, D / 4
-// threads per part and several parts at a time.
+// query head: D / 4 threads per part and several parts at a time.
+constexpr int kJoinThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinThreads)
 k_attn_join(const AttnArgs a) {
-  constexpr int TP = D / 4, PP = 128 / TP;  // threads per part, parts at a time
-  extern __shared__ float s_f[];            // [grid] factor of each part
-  __shared__ long long s_scan[4];
+  constexpr int TP = D / 4, PP = kJoinThreads / TP;  // threads per part, parts at a time
+  extern __shared__ float s_f[];  // [2][grid] maximum and sum of each part
+  __shared__ long long s_scan[kJoinThreads / 32];
   __shared__ Place s_place;
-  __shared__ float s_red[4], s_l[PP];
+  __shared__ float s_red[kJoinThreads / 32], s_l[PP];
   __shared__ float4 s_acc[PP][TP];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / a.HG, hg = blockIdx.x % a.HG, r = blockIdx.y;
-  const int hkv = hg / a.gtiles, row0 = (hg % a.gtiles) * kRows;
+  const int hkv = hg / a.gtiles, row0 = (hg % a.gtiles) * a.rows;
   Place at;
   long long share;
   plan(a, s_scan, &s_place, false, b, at, share);
@@ -592,36 +696,55 @@ k_attn_join(const AttnArgs a) {
     if (tid == 0 && a.seq_lens[b] != sp.len) raise_status(a.status, MOE_DEV_BAD_PAGE);
     return;
   }
-  const long long s0 = at.before + (long long)hg * sp.tiles, s1 = s0 + sp.tiles;
+  const long long s0 = at.before + (long long)hg * units_of(sp), s1 = s0 + units_of(sp);
   const int c0 = (int)(s0 / share), c1 = (int)((s1 - 1) / share);
   if (c0 == c1) return;  // written by its CTA
   griddep_wait();
   const int n = c1 - c0 + 1;
   auto slot_of = [&](int i) { return 2 * (c0 + i) + (s0 <= (c0 + i) * share ? 0 : 1); };
+  // the first kAhead parts of each thread's are on their way while the maxima
+  // are found
+  constexpr int kAhead = 4;
+  const int p = tid / TP, d4 = tid % TP;
+  float4 v[kAhead];
+  auto load = [&](int i) {
+    return i < n ? __ldcg(reinterpret_cast<const float4*>(
+                       a.part_o + ((size_t)slot_of(i) * kMaxRows + r) * D + 4 * d4))
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) v[u] = load(p + u * PP);
   float M = -INFINITY;
-  for (int i = tid; i < n; i += 128) M = fmaxf(M, __ldcg(a.part_ml + (size_t)slot_of(i) * 2 * kRows + r));
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const float* ml = a.part_ml + (size_t)slot_of(i) * 2 * kMaxRows + r;
+    const float m = __ldcg(ml);
+    s_f[i] = m;
+    s_f[a.grid + i] = __ldcg(ml + kMaxRows);
+    M = fmaxf(M, m);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) s_red[warp] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+#pragma unroll
+  for (int x = 0; x < kJoinThreads / 32; ++x) M = fmaxf(M, s_red[x]);
   const float Ms = M == -INFINITY ? 0.f : M;
-  for (int i = tid; i < n; i += 128)
-    s_f[i] = exp2f(__ldcg(a.part_ml + (size_t)slot_of(i) * 2 * kRows + r) - Ms);
-  __syncthreads();
-  const int p = tid / TP, d4 = tid % TP;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float L = 0.f;
-#pragma unroll 4
-  for (int i = p; i < n; i += PP) {
-    const float f = s_f[i];
-    const size_t sl = (size_t)slot_of(i);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (sl * kRows + r) * D + 4 * d4));
-    L = fmaf(__ldcg(a.part_ml + sl * 2 * kRows + kRows + r), f, L);
-    acc.x = fmaf(v.x, f, acc.x);
-    acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z);
-    acc.w = fmaf(v.w, f, acc.w);
+  for (int i0 = p; i0 < n; i0 += kAhead * PP) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * PP;
+      if (i < n) {
+        const float f = exp2f(s_f[i] - Ms);
+        L = fmaf(s_f[a.grid + i], f, L);
+        acc.x = fmaf(v[u].x, f, acc.x);
+        acc.y = fmaf(v[u].y, f, acc.y);
+        acc.z = fmaf(v[u].z, f, acc.z);
+        acc.w = fmaf(v[u].w, f, acc.w);
+      }
+      v[u] = load(i + kAhead * PP);
+    }
   }
   s_acc[p][d4] = acc;
   if (d4 == 0) s_l[p] = L;
@@ -648,33 +771,40 @@ k_attn_join(const AttnArgs a) {
 
 namespace {
 
-int attn_head_tiles(const moe_attn_dims& d, int Hkv) { return Hkv * cdiv(d.Hq / Hkv, kRows); }
+// The workspace is sized for the most CTAs per SM that any shape runs.
+int attn_max_grid() { return 3 * num_sms(); }
 
-// The least CTAs per SM over the shapes bounds nothing: the workspace is
-// sized for the most, two.
-int attn_max_grid() { return 2 * num_sms(); }
+template <int D, bool E4M3, int NH>
+cudaError_t launch_attn_nh(AttnArgs& a, cudaStream_t s) {
+  using S = AttnShape<D, E4M3, NH>;
+  static_assert(S::kCtasPerSm <= 3, "attn_max_grid");
+  cudaError_t err = ensure_smem((const void*)k_paged_attention<D, E4M3, NH>, S::kSmem);
+  if (err != cudaSuccess) return err;
+  a.rows = S::kRows;
+  a.tile = S::kTile;
+  a.gtiles = cdiv(a.G, S::kRows);
+  a.HG = a.c.Hkv * a.gtiles;
+  // no more CTAs than the table could give the least shares
+  const long long most = (long long)a.d.B * a.HG *
+                         (((long long)a.d.table_width * a.c.page_size + S::kTile - 1) / S::kTile + 1 + kSegCost);
+  a.grid = (int)std::max(1ll, std::min((long long)S::kCtasPerSm * num_sms(),
+                                       (most + kMinUnits - 1) / kMinUnits));
+  err = launch_k(k_paged_attention<D, E4M3, NH>, dim3(a.grid), dim3(kWarps * 32), S::kSmem, s, false, a);
+  if (err != cudaSuccess) return err;
+  return launch_k(k_attn_join<D>, dim3(a.d.B * a.HG, std::min(a.G, S::kRows)), dim3(kJoinThreads),
+                  2 * (size_t)a.grid * sizeof(float), s, true, a);
+}
 
 template <int D, bool E4M3>
 cudaError_t launch_attn(AttnArgs& a, cudaStream_t s) {
-  using S = AttnShape<D, E4M3>;
-  cudaError_t err = ensure_smem((const void*)k_paged_attention<D, E4M3>, S::kSmem);
-  if (err != cudaSuccess) return err;
-  // no more CTAs than the table could give least shares
-  const long long most = (long long)a.d.B * a.HG *
-                         (((long long)a.d.table_width * a.c.page_size + kTile - 1) / kTile + 1);
-  a.grid = (int)std::max(1ll, std::min((long long)S::kCtasPerSm * num_sms(),
-                                       (most + kMinTiles - 1) / kMinTiles));
-  err = launch_k(k_paged_attention<D, E4M3>, dim3(a.grid), dim3(kWarps * 32), S::kSmem, s, false, a);
-  if (err != cudaSuccess) return err;
-  return launch_k(k_attn_join<D>, dim3(a.d.B * a.HG, std::min(a.G, kRows)), dim3(128),
-                  (size_t)a.grid * sizeof(float), s, true, a);
+  return a.G <= 8 ? launch_attn_nh<D, E4M3, 1>(a, s) : launch_attn_nh<D, E4M3, 2>(a, s);
 }
 
 }  // namespace
 
 size_t paged_attention_workspace(const moe_attn_dims&, int D) {
   const size_t slots = 2 * (size_t)attn_max_grid();
-  return slots * kRows * ((size_t)D + 2) * sizeof(float);
+  return slots * kMaxRows * ((size_t)D + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attention(const uint16_t* q, const moe_kv_cache& cache,
@@ -688,12 +818,16 @@ cudaError_t launch_paged_attention(const uint16_t* q, const moe_kv_cache& cache,
   a.seq_lens = seq_lens;
   a.d = d;
   a.G = d.Hq / cache.Hkv;
-  a.gtiles = cdiv(a.G, kRows);
-  a.HG = attn_head_tiles(d, cache.Hkv);
   a.out = out;
   a.part_o = static_cast<float*>(ws);
-  a.part_ml = a.part_o + 2 * (size_t)attn_max_grid() * kRows * cache.D;
+  a.part_ml = a.part_o + 2 * (size_t)attn_max_grid() * kMaxRows * cache.D;
   a.status = status;
+  // t / page_size for 0 <= t < 2^31: with 2^(e-1) < page_size <= 2^e and mul =
+  // ceil(2^(31+e) / page_size) < 2^32, floor(t mul / 2^(31+e)) is exact
+  int e = 0;
+  while ((1ll << e) < cache.page_size) ++e;
+  a.ps_mul = (uint32_t)(((1ull << (31 + e)) + cache.page_size - 1) / cache.page_size);
+  a.ps_shift = e > 0 ? e - 1 : 0;
   const bool f8 = cache.format == MOE_KV_E4M3;
   if (cache.D == 64) return f8 ? launch_attn<64, true>(a, s) : launch_attn<64, false>(a, s);
   if (cache.D == 128) return f8 ? launch_attn<128, true>(a, s) : launch_attn<128, false>(a, s);

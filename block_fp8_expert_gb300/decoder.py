@@ -9,8 +9,8 @@
 Each object holds what a serving program sets up once; ``forward`` takes the
 step's tensors, and output buffers and a workspace where the program keeps
 them (they are allocated otherwise).  Everything runs in libmoe_fp8.so on the
-current stream or the one given; tensors are checked for device, type and
-layout here and for their sizes in the library.  What the kernels themselves
+current stream or the one given; tensors are checked for device, type, shape
+and layout here and for their sizes in the library.  What the kernels themselves
 find wrong in their data (a page number outside the cache, say) is recorded in
 ``status``, a device array that ``check()`` reads after synchronising.
 """
@@ -23,36 +23,45 @@ import torch
 
 from . import _lib
 
+_BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
+                                torch.uint8)
 
-def _need(t: torch.Tensor, name: str, dtype, ndim: int) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != ndim:
-        raise TypeError(f"{name}: need a {ndim}-d {dtype} tensor, got "
-                        f"{getattr(t, 'dtype', type(t))} {tuple(getattr(t, 'shape', ()))}")
+
+def _stream_on(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+# The checks of a call cost host time on every step, so forward() asks one
+# question per tensor and looks for the words only when the answer is no.
+
+def _refuse(t, name: str, dtype, shape, device: Optional[int] = None, layout: str = "") -> None:
+    """Raise for what is wrong with t, which is not a `dtype` tensor of
+    `shape` on CUDA device `device` with the layout that is described."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: need a tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: need {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} is not on a CUDA device")
-    if ndim and t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t
-
-
-def _shape(t: torch.Tensor, name: str, *shape) -> torch.Tensor:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {shape}")
-    return t
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on device {t.get_device()}, the first tensor on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {tuple(shape)}")
+    raise ValueError(f"{name}: strides {t.stride()}: {layout or 'must be contiguous'}")
 
 
 def _dense(t: Optional[torch.Tensor], name: str, dtype, *shape) -> Optional[torch.Tensor]:
-    if t is None:
-        return None
-    _shape(_need(t, name, dtype, len(shape)), name, *shape)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    """A contiguous CUDA tensor (or None), checked at set-up."""
+    if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype
+                              and tuple(t.shape) == shape and t.is_contiguous()):
+        _refuse(t, name, dtype, shape)
     return t
 
 
-def _row_stride(t: torch.Tensor, width: int) -> int:
-    """Elements between rows of a tensor whose rows are `width` wide."""
-    return t.stride(0) if t.shape[0] > 1 else width
+_ROWS = "the elements of a row must be contiguous"
+_HEADS = "the heads of a row must be contiguous"
 
 
 def _new(stream, *shape, dtype, device) -> torch.Tensor:
@@ -69,6 +78,7 @@ class _Status:
 
     def __init__(self, device):
         self.status = torch.zeros(16, dtype=torch.int32, device=device)
+        self._status = self.status.data_ptr()
 
     def check(self, stream=None) -> None:
         """Synchronise and raise MoeError if a kernel flagged its data."""
@@ -91,21 +101,31 @@ class ExpertSelector:
         self.rule = _lib.SelectRule(
             _lib.MOE_SCORE_SIGMOID if score == "sigmoid" else _lib.MOE_SCORE_SOFTMAX,
             groups, top_groups, group_top, int(bool(renorm)), scale)
+        self._bias = _lib._ptr(self.bias)
+        self._call = _lib.lib().moe_select_experts
 
     def forward(self, logits: torch.Tensor, topk_idx: Optional[torch.Tensor] = None,
                 topk_w: Optional[torch.Tensor] = None, stream=None):
-        """logits float32 [T, E] -> (topk_idx int32 [T, k], topk_w float32 [T, k])."""
-        _need(logits, "logits", torch.float32, 2)
-        T = logits.shape[0]
-        _shape(logits, "logits", T, self.E)
+        """logits float32 [T, E] (rows may be strided) -> (topk_idx int32
+        [T, k], topk_w float32 [T, k])."""
+        dev, T, E, k = logits.get_device(), logits.shape[0], self.E, self.k
+        if dev < 0 or logits.dtype != _F32 or logits.shape != (T, E) or (
+                logits.stride(1) != 1 and E > 1):
+            _refuse(logits, "logits", _F32, (T, E), layout=_ROWS)
         if topk_idx is None:
-            topk_idx = _new(stream, T, self.k, dtype=torch.int32, device=logits.device)
+            topk_idx = _new(stream, T, k, dtype=_I32, device=logits.device)
         if topk_w is None:
-            topk_w = _new(stream, T, self.k, dtype=torch.float32, device=logits.device)
-        _dense(topk_idx, "topk_idx", torch.int32, T, self.k)
-        _dense(topk_w, "topk_w", torch.float32, T, self.k)
-        _lib.moe_select_experts(logits, _row_stride(logits, self.E), self.bias, self.rule, T,
-                                self.E, self.k, topk_idx, topk_w, stream)
+            topk_w = _new(stream, T, k, dtype=_F32, device=logits.device)
+        if (topk_idx.dtype != _I32 or topk_idx.get_device() != dev or topk_idx.shape != (T, k)
+                or not topk_idx.is_contiguous()):
+            _refuse(topk_idx, "topk_idx", _I32, (T, k), dev)
+        if (topk_w.dtype != _F32 or topk_w.get_device() != dev or topk_w.shape != (T, k)
+                or not topk_w.is_contiguous()):
+            _refuse(topk_w, "topk_w", _F32, (T, k), dev)
+        st = self._call(logits.data_ptr(), logits.stride(0) if T > 1 else E, self._bias, self.rule,
+                        T, E, k, topk_idx.data_ptr(), topk_w.data_ptr(), _stream_on(stream, dev))
+        if st:
+            _lib._check(st, "moe_select_experts")
         return topk_idx, topk_w
 
 
@@ -122,9 +142,11 @@ class PagedCache:
         if self.e4m3:
             k = k.view(torch.uint8) if k.dtype == torch.float8_e4m3fn else k
             v = v.view(torch.uint8) if v.dtype == torch.float8_e4m3fn else v
-        dtype = torch.uint8 if self.e4m3 else torch.bfloat16
-        _need(k, "k", dtype, 4)
-        _shape(_need(v, "v", dtype, 4), "v", *k.shape)
+        dtype = _U8 if self.e4m3 else _BF16
+        for t, name in ((k, "k"), (v, "v")):
+            if not (t.is_cuda and t.dtype == dtype and t.dim() == 4 and t.shape == k.shape
+                    and t.stride(3) == 1):
+                _refuse(t, name, dtype, k.shape, layout=_ROWS)
         if k.stride() != v.stride():
             raise ValueError(f"k and v have different strides: {k.stride()}, {v.stride()}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
@@ -134,9 +156,8 @@ class PagedCache:
             raise ValueError("k_scale and v_scale come together")
         if self.e4m3:
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                if not (t.is_cuda and t.dtype == torch.float32):
-                    raise TypeError(f"{name}: need a float32 CUDA tensor")
-                _shape(t, name, *k.shape[:3])
+                if not (t.is_cuda and t.dtype == _F32 and t.shape == k.shape[:3]):
+                    _refuse(t, name, _F32, k.shape[:3])
             if k_scale.stride() != v_scale.stride():
                 raise ValueError("k_scale and v_scale have different strides")
             ss = k_scale.stride()
@@ -216,6 +237,10 @@ class QkNormRope(_Status):
         self.n_pos, self.rot = (0, 0) if cos_sin is None else cos_sin.shape
         if cos_sin is not None:
             _dense(cos_sin, "cos_sin", torch.float32, self.n_pos, self.rot)
+        self.width = (Hq + 2 * Hkv) * D
+        self._q_norm, self._k_norm, self._cos_sin = (_lib._ptr(t) for t in (q_norm, k_norm, cos_sin))
+        self._key, self._dims = None, None  # the last call's sizes, as the library takes them
+        self._call = _lib.lib().moe_qk_norm_rope
 
     def forward(self, qkv: torch.Tensor, positions: Optional[torch.Tensor], slots: torch.Tensor,
                 cache: PagedCache, q_out: Optional[torch.Tensor] = None,
@@ -223,32 +248,37 @@ class QkNormRope(_Status):
         """qkv bf16 [T, (Hq + 2 Hkv) D] (rows may be strided), positions int32
         [T], slots int64 [T] (page * page_size + offset, or < 0 for padding)
         -> q_out bf16 [T, Hq, D]."""
-        _need(qkv, "qkv", torch.bfloat16, 2)
-        T, width = qkv.shape
-        if width != (self.Hq + 2 * self.Hkv) * self.D:
-            raise ValueError(f"qkv: rows of {width}, need {(self.Hq + 2 * self.Hkv) * self.D}")
-        if cache.Hkv != self.Hkv or cache.D != self.D:
-            raise ValueError("the cache has other heads")
+        Hq, D, width = self.Hq, self.D, self.width
+        dev, T = qkv.get_device(), qkv.shape[0]
+        if dev < 0 or qkv.dtype != _BF16 or qkv.shape != (T, width) or qkv.stride(1) != 1:
+            _refuse(qkv, "qkv", _BF16, (T, width), layout=_ROWS)
+        if cache.Hkv != self.Hkv or cache.D != D:
+            raise ValueError(f"the cache has {cache.Hkv} heads of {cache.D}, need {self.Hkv} of {D}")
         if (positions is None) != (self.cos_sin is None):
             raise ValueError("positions and the rotation table come together")
-        _dense(positions, "positions", torch.int32, T)
-        _dense(slots, "slots", torch.int64, T)
+        if positions is not None and (positions.dtype != _I32 or positions.get_device() != dev
+                                      or positions.shape != (T,) or not positions.is_contiguous()):
+            _refuse(positions, "positions", _I32, (T,), dev)
+        if (slots.dtype != _I64 or slots.get_device() != dev or slots.shape != (T,)
+                or not slots.is_contiguous()):
+            _refuse(slots, "slots", _I64, (T,), dev)
         if q_out is None:
-            q_out = _new(stream, T, self.Hq, self.D, dtype=torch.bfloat16, device=qkv.device)
-        _heads(q_out, "q_out", T, self.Hq, self.D)
-        d = _lib.QkDims(T, self.Hq, self.rot, int(self.interleaved), self.n_pos, self.eps,
-                        _row_stride(qkv, width), _row_stride(q_out, self.Hq * self.D))
-        _lib.moe_qk_norm_rope(qkv, self.q_norm, self.k_norm, self.cos_sin, positions, slots, d,
-                              cache.abi(), q_out, self.status, stream)
+            q_out = _new(stream, T, Hq, D, dtype=_BF16, device=qkv.device)
+        if (q_out.dtype != _BF16 or q_out.get_device() != dev or q_out.shape != (T, Hq, D)
+                or q_out.stride(2) != 1 or (Hq > 1 and q_out.stride(1) != D)):
+            _refuse(q_out, "q_out", _BF16, (T, Hq, D), dev, _HEADS)
+        key = (T, qkv.stride(0), q_out.stride(0))
+        if key != self._key:
+            self._dims = _lib.QkDims(T, Hq, self.rot, int(self.interleaved), self.n_pos, self.eps,
+                                     key[1] if T > 1 else width, key[2] if T > 1 else Hq * D)
+            self._key = key
+        st = self._call(qkv.data_ptr(), self._q_norm, self._k_norm, self._cos_sin,
+                        None if positions is None else positions.data_ptr(), slots.data_ptr(),
+                        self._dims, cache._abi, q_out.data_ptr(), self._status,
+                        _stream_on(stream, dev))
+        if st:
+            _lib._check(st, "moe_qk_norm_rope")
         return q_out
-
-
-def _heads(t: torch.Tensor, name: str, n: int, H: int, D: int) -> torch.Tensor:
-    """A bf16 tensor [n, H, D] whose heads lie one after another."""
-    _shape(_need(t, name, torch.bfloat16, 3), name, n, H, D)
-    if n and H > 1 and t.stride(1) != D:
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t
 
 
 class PagedAttention(_Status):
@@ -260,6 +290,8 @@ class PagedAttention(_Status):
         super().__init__(device)
         self.Hq, self.Hkv, self.D, self.window = Hq, Hkv, D, window
         self.scale = 1.0 / math.sqrt(D) if scale is None else scale
+        self._key, self._dims = None, None  # the last call's sizes, as the library takes them
+        self._call = _lib.lib().moe_paged_attention
 
     def workspace(self, B: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to B sequences (of any length)."""
@@ -272,25 +304,38 @@ class PagedAttention(_Status):
                 ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """q bf16 [B, Hq, D], block_table int32 [B, pages per sequence],
         seq_lens int32 [B] (the new token included) -> out bf16 [B, Hq, D]."""
-        B = q.shape[0]
-        _heads(q, "q", B, self.Hq, self.D)
-        if cache.Hkv != self.Hkv or cache.D != self.D:
-            raise ValueError("the cache has other heads")
-        _need(block_table, "block_table", torch.int32, 2)
+        Hq, D = self.Hq, self.D
+        dev, B = q.get_device(), q.shape[0]
+        if (dev < 0 or q.dtype != _BF16 or q.shape != (B, Hq, D) or q.stride(2) != 1
+                or (Hq > 1 and q.stride(1) != D)):
+            _refuse(q, "q", _BF16, (B, Hq, D), layout=_HEADS)
+        if cache.Hkv != self.Hkv or cache.D != D:
+            raise ValueError(f"the cache has {cache.Hkv} heads of {cache.D}, need {self.Hkv} of {D}")
         width = block_table.shape[1]
-        _shape(block_table, "block_table", B, width)
-        _dense(seq_lens, "seq_lens", torch.int32, B)
+        if (block_table.dtype != _I32 or block_table.get_device() != dev
+                or block_table.shape != (B, width) or (width > 1 and block_table.stride(1) != 1)):
+            _refuse(block_table, "block_table", _I32, (B, width), dev, _ROWS)
+        if (seq_lens.dtype != _I32 or seq_lens.get_device() != dev or seq_lens.shape != (B,)
+                or not seq_lens.is_contiguous()):
+            _refuse(seq_lens, "seq_lens", _I32, (B,), dev)
         if out is None:
-            out = _new(stream, B, self.Hq, self.D, dtype=torch.bfloat16, device=q.device)
-        _heads(out, "out", B, self.Hq, self.D)
+            out = _new(stream, B, Hq, D, dtype=_BF16, device=q.device)
+        if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (B, Hq, D)
+                or out.stride(2) != 1 or (Hq > 1 and out.stride(1) != D)):
+            _refuse(out, "out", _BF16, (B, Hq, D), dev, _HEADS)
         if ws is None:
             ws = self.workspace(B, stream)
-        row = self.Hq * self.D
-        d = _lib.AttnDims(B, self.Hq, width, self.window, self.scale,
-                          _row_stride(block_table, width), _row_stride(q, row),
-                          _row_stride(out, row))
-        _lib.moe_paged_attention(q, cache.abi(), block_table, seq_lens, d, out, ws, self.status,
-                                 stream)
+        key = (B, width, block_table.stride(0), q.stride(0), out.stride(0))
+        if key != self._key:
+            row = Hq * D
+            strides = key[2:] if B > 1 else (width, row, row)
+            self._dims = _lib.AttnDims(B, Hq, width, self.window, self.scale, *strides)
+            self._key = key
+        st = self._call(q.data_ptr(), cache._abi, block_table.data_ptr(), seq_lens.data_ptr(),
+                        self._dims, out.data_ptr(), ws.data_ptr(), ws.nbytes, self._status,
+                        _stream_on(stream, dev))
+        if st:
+            _lib._check(st, "moe_paged_attention")
         return out
 
 
@@ -310,6 +355,9 @@ class Fp8Linear(_Status):
         self.bias = _dense(bias, "bias", torch.float32, self.N)
         super().__init__(codes.device)
         self._mat = _lib.Fp8Mat(codes.data_ptr(), scales.data_ptr())
+        self._bias = _lib._ptr(bias)
+        self._key, self._dims = None, None  # the last call's sizes, as the library takes them
+        self._call = _lib.lib().moe_linear_fp8
 
     def workspace(self, M: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to M rows."""
@@ -319,14 +367,23 @@ class Fp8Linear(_Status):
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
                 ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """x bf16 [M, K] -> out bf16 [M, N]; rows of either may be strided."""
-        _need(x, "x", torch.bfloat16, 2)
-        M = x.shape[0]
-        _shape(x, "x", M, self.K)
+        N, K = self.N, self.K
+        dev, M = x.get_device(), x.shape[0]
+        if dev < 0 or x.dtype != _BF16 or x.shape != (M, K) or x.stride(1) != 1:
+            _refuse(x, "x", _BF16, (M, K), layout=_ROWS)
         if out is None:
-            out = _new(stream, M, self.N, dtype=torch.bfloat16, device=x.device)
-        _shape(_need(out, "out", torch.bfloat16, 2), "out", M, self.N)
+            out = _new(stream, M, N, dtype=_BF16, device=x.device)
+        if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (M, N)
+                or out.stride(1) != 1):
+            _refuse(out, "out", _BF16, (M, N), dev, _ROWS)
         if ws is None:
             ws = self.workspace(M, stream)
-        d = _lib.LinearDims(M, self.N, self.K, _row_stride(x, self.K), _row_stride(out, self.N))
-        _lib.moe_linear_fp8(x, self._mat, self.bias, d, out, ws, self.status, stream)
+        key = (M, x.stride(0), out.stride(0))
+        if key != self._key:
+            self._dims = _lib.LinearDims(M, N, K, key[1] if M > 1 else K, key[2] if M > 1 else N)
+            self._key = key
+        st = self._call(x.data_ptr(), self._mat, self._bias, self._dims, out.data_ptr(),
+                        ws.data_ptr(), ws.nbytes, self._status, _stream_on(stream, dev))
+        if st:
+            _lib._check(st, "moe_linear_fp8")
         return out
