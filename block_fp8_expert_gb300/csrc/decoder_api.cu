@@ -157,6 +157,8 @@ moe_status moe_paged_attention(const uint16_t* q, moe_kv_cache cache, const int3
     return fail(MOE_ERR_INVALID_ARG, "table_stride = %lld < table_width", (long long)d.table_stride);
   if ((s = check_stride(d.q_stride, (long long)d.Hq * cache.D, 8, "q_stride")) != MOE_OK) return s;
   if ((s = check_stride(d.out_stride, (long long)d.Hq * cache.D, 8, "out_stride")) != MOE_OK) return s;
+  if (!paged_attention_fits(d, cache))
+    return fail(MOE_ERR_UNSUPPORTED, "B * Hkv * (table_width * page_size / 16 + 9) too large");
   REQUIRE_OPT_PTR(status);
   if (d.B == 0) return MOE_OK;
   REQUIRE_PTR(q);

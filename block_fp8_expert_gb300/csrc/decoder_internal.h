@@ -40,6 +40,8 @@ cudaError_t launch_qk_norm_rope(const uint16_t* qkv, const float* q_norm, const 
                                 const moe_qk_dims& d, const moe_kv_cache& cache, uint16_t* q_out,
                                 int32_t* status, cudaStream_t s);
 
+// Whether the work units that the block table has room for fit 31 bits.
+bool paged_attention_fits(const moe_attn_dims& d, const moe_kv_cache& cache);
 // Scratch bytes of one attention call: two partial results per CTA.
 size_t paged_attention_workspace(const moe_attn_dims& d, int D);
 cudaError_t launch_paged_attention(const uint16_t* q, const moe_kv_cache& cache,

@@ -57,6 +57,7 @@ struct AttnArgs {
   uint16_t* out;
   float* part_o;   // [2 * grid][kMaxRows][D]
   float* part_ml;  // [2 * grid][2][kMaxRows]
+  int4* jobs;      // [grid] what k_attn_join does for a CTA: {slot, parts, sequence, segment}
   int grid;
   int32_t* status;
 };
@@ -79,66 +80,86 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
 
 // A sequence's tiles for one tile of heads are a segment of tiles + kSegCost
 // units; empty sequences have none.  All segments lie in one row, sequence-
-// major, then head: CTA c takes units [c share, (c + 1) share), and with them
-// the same part of the segment's tiles.  A segment that crosses CTAs is
-// joined by k_attn_join.  So ragged batches, many short and one long sequence
-// alike, give every CTA the same time.
+// major, then head.  Where there are CTAs enough to give every segment its own
+// parts of about kMinUnits, a CTA takes one such part.  Otherwise CTA c takes
+// units [c share, (c + 1) share) of the row, and with them the same part of
+// each segment's tiles, so ragged batches, many short sequences and a few long
+// ones alike, give every CTA the same time.  A segment that several CTAs hold
+// is joined by k_attn_join.  (Units fit 31 bits: the host checks.)
 __device__ __forceinline__ int units_of(const Span& s) { return s.tiles ? s.tiles + kSegCost : 0; }
+__device__ __forceinline__ int parts_of(int units) { return (units + kMinUnits - 1) / kMinUnits; }
 // The tile at which unit u of a segment begins.
-__device__ __forceinline__ int tile_at(const Span& s, long long u) {
-  return (int)(u * s.tiles / units_of(s));
+__device__ __forceinline__ int tile_at(const Span& s, int u) {
+  const int units = units_of(s);
+  return u <= 0 ? 0 : u >= units ? s.tiles : (int)((long long)u * s.tiles / units);
 }
 
-// Every thread of the CTA calls this; it finds the sequence that holds unit
-// `want * share` (by_share) or is number `want`, with the units of all the
-// sequences before it, and returns all segments' units.
+// A CTA's range of units, the sequence that holds its first one, and where
+// that sequence begins.
 struct Place {
-  int b;
-  long long before;
+  int b, before, cur, end;
 };
-__device__ __forceinline__ long long plan(const AttnArgs& a, long long* s_scan, Place* s_place,
-                                          bool by_share, long long want, Place& at,
-                                          long long& share) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
-  const int per = cdiv(a.d.B, n), b0 = min(tid * per, a.d.B), b1 = min(b0 + per, a.d.B);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units_of(span_of(a, b));
-  long long incl = mine;
+// Every thread of the CTA calls this.  share: 0 where each CTA has one part.
+__device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s_place, int& share) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = cdiv(a.d.B, kWarps * 32), b0 = min(tid * per, a.d.B), b1 = min(b0 + per, a.d.B);
+  uint2 mine = make_uint2(0u, 0u);  // units, parts
+  for (int b = b0; b < b1; ++b) {
+    const int u = units_of(span_of(a, b));
+    mine.x += u;
+    mine.y += parts_of(u);
+  }
+  uint2 incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) {
+      incl.x += x;
+      incl.y += y;
+    }
   }
   if (lane == 31) s_scan[warp] = incl;
-  if (tid == 0) *s_place = Place{a.d.B, 0};
+  if (tid == 0) *s_place = Place{a.d.B, 0, 0, 0};
   __syncthreads();
-  long long before = incl - mine, total = 0;
-  for (int w = 0; w < n / 32; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-  }
-  total *= a.HG;
-  share = max((long long)kMinUnits, (total + a.grid - 1) / a.grid);
-  if (by_share) {
-    const long long t0 = want * share;
-    if (before * a.HG <= t0 && t0 < (before + mine) * a.HG) {
-      long long at0 = before;
-      int b = b0;
-      for (; b < b1; ++b) {
-        const int k = units_of(span_of(a, b));
-        if (t0 < (at0 + k) * a.HG) break;
-        at0 += k;
-      }
-      *s_place = Place{b, at0 * a.HG};
+  uint2 before = make_uint2(incl.x - mine.x, incl.y - mine.y), total = make_uint2(0u, 0u);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const uint2 v = s_scan[w];
+    if (w < warp) {
+      before.x += v.x;
+      before.y += v.y;
     }
-  } else if (want >= b0 && want < b1) {
-    long long at0 = before;
-    for (int b = b0; b < (int)want; ++b) at0 += units_of(span_of(a, b));
-    *s_place = Place{(int)want, at0 * a.HG};
+    total.x += v.x;
+    total.y += v.y;
+  }
+  total.x *= a.HG;
+  total.y *= a.HG;
+  const bool own = total.y <= (uint32_t)a.grid;
+  share = own ? 0 : max((uint32_t)kMinUnits, (total.x + a.grid - 1) / a.grid);
+  // the first unit, or the part, that this CTA looks for
+  const uint32_t want = own ? blockIdx.x : min((uint32_t)blockIdx.x * share, total.x);
+  const uint32_t from = own ? before.y : before.x, len = own ? mine.y : mine.x;
+  if (from * a.HG <= want && want < (from + len) * a.HG) {
+    uint32_t at = from;
+    int b = b0, u = 0, k = 0;
+    for (; b < b1; ++b) {
+      u = units_of(span_of(a, b));
+      k = own ? parts_of(u) : u;
+      if (want < (at + k) * a.HG) break;
+      at += k;
+      before.x += u;
+    }
+    Place p{b, (int)(before.x * a.HG), (int)want, (int)min(want + share, total.x)};
+    if (own) {
+      const int hg = (int)(want - at * a.HG) / k, part = (int)(want - at * a.HG) % k;
+      const int s0 = p.before + hg * u;
+      p.cur = s0 + part * u / k;
+      p.end = s0 + (part + 1) * u / k;
+    }
+    *s_place = p;
   }
   __syncthreads();
-  at = *s_place;
-  return total;
+  return *s_place;
 }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -220,7 +241,7 @@ k_paged_attention(const AttnArgs a) {
   constexpr int NI = kTile * LPR / 32;         // copies per lane and matrix
   constexpr int DPL = D == 64 ? 8 : 16;        // E4M3: dimensions per lane of the second product
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_scan[kWarps];
+  __shared__ uint2 s_scan[kWarps];
   __shared__ Place s_place;
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ unsigned s_seen[kWarps][S::kStages];  // tokens of each stage that exist
@@ -230,27 +251,36 @@ k_paged_attention(const AttnArgs a) {
   const uint32_t stages = smem_u32(smem) + warp * S::kWarpBytes;
   uint2* const qshared = reinterpret_cast<uint2*>(smem + kWarps * S::kWarpBytes);
 
-  Place at;
-  long long share;
-  const long long total = plan(a, s_scan, &s_place, true, blockIdx.x, at, share);
-  long long cur = (long long)blockIdx.x * share;
-  const long long end = min(total, cur + share);
-  if (cur >= end) return;
+  int share;
+  Place at = plan(a, s_scan, &s_place, share);
+  int cur = at.cur;
+  const int end = at.end;
+  // empty sequences answer zeros
+  for (int e = blockIdx.x; e < a.d.B; e += a.grid) {
+    if (span_of(a, e).tiles) continue;
+    uint4* row = reinterpret_cast<uint4*>(a.out + (size_t)e * a.d.out_stride);
+    for (int i = tid; i < a.d.Hq * D / 8; i += kWarps * 32) row[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0 && a.seq_lens[e] != 0) raise_status(a.status, MOE_DEV_BAD_PAGE);
+  }
+  int4 job = make_int4(0, 0, 0, 0);
+  if (cur >= end) {
+    if (tid == 0) a.jobs[blockIdx.x] = job;
+    return;
+  }
   int b = at.b;
   Span sp = span_of(a, b);
-  const long long first_unit = cur;
+  const int first_unit = cur;
   const float scale2 = a.d.scale * 1.44269504088896341f;
 
   while (cur < end) {
-    while (cur >= at.before + (long long)units_of(sp) * a.HG) {  // next sequence with a token
-      at.before += (long long)units_of(sp) * a.HG;
+    while (cur >= at.before + units_of(sp) * a.HG) {  // next sequence with a token
+      at.before += units_of(sp) * a.HG;
       sp = span_of(a, ++b);
     }
     if (tid == 0 && a.seq_lens[b] != sp.len) raise_status(a.status, MOE_DEV_BAD_PAGE);
     const int units = units_of(sp);
-    const int hg = (int)((cur - at.before) / units);
-    const long long s0 = at.before + (long long)hg * units, s1 = s0 + units;
-    const long long stop = min(s1, end);
+    const int hg = (cur - at.before) / units;
+    const int s0 = at.before + hg * units, s1 = s0 + units, stop = min(s1, end);
     const int i0 = tile_at(sp, cur - s0), i1 = tile_at(sp, stop - s0);  // tiles of the segment
     const int hkv = hg / a.gtiles, row0 = (hg % a.gtiles) * kRows;
     const int rows = min(kRows, a.G - row0);
@@ -664,115 +694,107 @@ k_paged_attention(const AttnArgs a) {
         }
       }
     }
+    // a segment that begins here and goes on is joined from here
+    if (cur == s0 && stop < s1)
+      job = make_int4(slot, share ? (s1 - 1) / share - (int)blockIdx.x + 1 : parts_of(units), b, hg);
     __syncthreads();
     cur = stop;
   }
+  if (tid == 0) a.jobs[blockIdx.x] = job;
 }
 
-// Joins the parts of every segment that crosses CTAs, in CTA order, and
-// writes the zeros of empty sequences.  One CTA per (sequence, head tile) and
-// query head: D / 4 threads per part and several parts at a time.
-constexpr int kJoinThreads = 256;
+// Joins the parts of the segment that begins in CTA blockIdx.x of the
+// attention kernel and goes on in the next ones, two heads per CTA.  A thread
+// owns four dimensions of a head; groups of threads take every GP-th part
+// each, and the groups' sums are added in order.
+constexpr int kJoinThreads = 256, kJoinHeads = 2;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
 k_attn_join(const AttnArgs a) {
-  constexpr int TP = D / 4, PP = kJoinThreads / TP;  // threads per part, parts at a time
-  extern __shared__ float s_f[];  // [2][grid] maximum and sum of each part
-  __shared__ long long s_scan[kJoinThreads / 32];
-  __shared__ Place s_place;
-  __shared__ float s_red[kJoinThreads / 32], s_l[PP];
-  __shared__ float4 s_acc[PP][TP];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / a.HG, hg = blockIdx.x % a.HG, r = blockIdx.y;
-  const int hkv = hg / a.gtiles, row0 = (hg % a.gtiles) * a.rows;
-  Place at;
-  long long share;
-  plan(a, s_scan, &s_place, false, b, at, share);
-  const Span sp = span_of(a, b);
-  if (row0 + r >= a.G) return;  // uniform
-  uint16_t* out = a.out + (size_t)b * a.d.out_stride + (size_t)(hkv * a.G + row0 + r) * D;
-  if (sp.tiles == 0) {
-    if (tid < TP) *reinterpret_cast<uint2*>(out + 4 * tid) = make_uint2(0, 0);
-    if (tid == 0 && a.seq_lens[b] != sp.len) raise_status(a.status, MOE_DEV_BAD_PAGE);
-    return;
-  }
-  const long long s0 = at.before + (long long)hg * units_of(sp), s1 = s0 + units_of(sp);
-  const int c0 = (int)(s0 / share), c1 = (int)((s1 - 1) / share);
-  if (c0 == c1) return;  // written by its CTA
+  constexpr int E = kJoinHeads * D / 4, GP = kJoinThreads / E, kAhead = 8;
+  __shared__ float4 s_acc[GP][E];
+  __shared__ float s_m[GP][kJoinHeads], s_l[GP][kJoinHeads];
   griddep_wait();
-  const int n = c1 - c0 + 1;
-  auto slot_of = [&](int i) { return 2 * (c0 + i) + (s0 <= (c0 + i) * share ? 0 : 1); };
-  // the first kAhead parts of each thread's are on their way while the maxima
-  // are found
-  constexpr int kAhead = 4;
-  const int p = tid / TP, d4 = tid % TP;
-  float4 v[kAhead];
-  auto load = [&](int i) {
-    return i < n ? __ldcg(reinterpret_cast<const float4*>(
-                       a.part_o + ((size_t)slot_of(i) * kMaxRows + r) * D + 4 * d4))
-                 : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) v[u] = load(p + u * PP);
-  float M = -INFINITY;
-  for (int i = tid; i < n; i += kJoinThreads) {
-    const float* ml = a.part_ml + (size_t)slot_of(i) * 2 * kMaxRows + r;
-    const float m = __ldcg(ml);
-    s_f[i] = m;
-    s_f[a.grid + i] = __ldcg(ml + kMaxRows);
-    M = fmaxf(M, m);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_red[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int x = 0; x < kJoinThreads / 32; ++x) M = fmaxf(M, s_red[x]);
-  const float Ms = M == -INFINITY ? 0.f : M;
+  const int4 job = __ldcg(a.jobs + blockIdx.x);
+  const int n = job.y;
+  const int hkv = job.w / a.gtiles, row0 = (job.w % a.gtiles) * a.rows, rows = min(a.rows, a.G - row0);
+  if (n == 0 || (int)blockIdx.y * kJoinHeads >= rows) return;  // uniform
+  const int grp = threadIdx.x / E, el = threadIdx.x % E;
+  const int hr = el / (D / 4), r = blockIdx.y * kJoinHeads + hr, d4 = el % (D / 4);
+  float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f;
-  for (int i0 = p; i0 < n; i0 += kAhead * PP) {
+  auto add = [&](float f, float l, const float4& v) {
+    L = fmaf(l, f, L);
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
+  };
+  for (int i0 = grp; i0 < n; i0 += kAhead * GP) {
+    float4 v[kAhead];
+    float m[kAhead], l[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u * PP;
-      if (i < n) {
-        const float f = exp2f(s_f[i] - Ms);
-        L = fmaf(s_f[a.grid + i], f, L);
-        acc.x = fmaf(v[u].x, f, acc.x);
-        acc.y = fmaf(v[u].y, f, acc.y);
-        acc.z = fmaf(v[u].z, f, acc.z);
-        acc.w = fmaf(v[u].w, f, acc.w);
+      const int i = i0 + u * GP;
+      const size_t sl = i == 0 ? (size_t)job.x : 2 * ((size_t)blockIdx.x + i);
+      m[u] = -INFINITY;
+      l[u] = 0.f;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n && r < rows) {
+        const float* ml = a.part_ml + sl * 2 * kMaxRows + r;
+        m[u] = __ldcg(ml);
+        l[u] = __ldcg(ml + kMaxRows);
+        v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (sl * kMaxRows + r) * D + 4 * d4));
       }
-      v[u] = load(i + kAhead * PP);
     }
-  }
-  s_acc[p][d4] = acc;
-  if (d4 == 0) s_l[p] = L;
-  __syncthreads();
-  if (p == 0) {
-    float Lt = 0.f;
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M2 = M;
 #pragma unroll
-    for (int x = 0; x < PP; ++x) {
-      Lt += s_l[x];
-      const float4 v = s_acc[x][d4];
-      t.x += v.x;
-      t.y += v.y;
-      t.z += v.z;
-      t.w += v.w;
-    }
-    const float inv = Lt == 0.f ? 0.f : 1.f / Lt;
-    uint2 r2;
-    r2.x = pack_bf16x2(t.x * inv, t.y * inv);
-    r2.y = pack_bf16x2(t.z * inv, t.w * inv);
-    *reinterpret_cast<uint2*>(out + 4 * d4) = r2;
+    for (int u = 0; u < kAhead; ++u) M2 = fmaxf(M2, m[u]);
+    const float Ms = M2 == -INFINITY ? 0.f : M2, f0 = exp2f(M - Ms);
+    L *= f0;
+    acc.x *= f0;
+    acc.y *= f0;
+    acc.z *= f0;
+    acc.w *= f0;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) add(exp2f(m[u] - Ms), l[u], v[u]);
+    M = M2;
   }
+  s_acc[grp][el] = acc;
+  if (d4 == 0) {
+    s_m[grp][hr] = M;
+    s_l[grp][hr] = L;
+  }
+  __syncthreads();
+  if (grp || r >= rows) return;
+  M = s_m[0][hr];
+#pragma unroll
+  for (int x = 1; x < GP; ++x) M = fmaxf(M, s_m[x][hr]);
+  const float Ms = M == -INFINITY ? 0.f : M;
+  L = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int x = 0; x < GP; ++x) add(exp2f(s_m[x][hr] - Ms), s_l[x][hr], s_acc[x][el]);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint2 r2;
+  r2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  r2.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(a.out + (size_t)job.z * a.d.out_stride +
+                            (size_t)(hkv * a.G + row0 + r) * D + 4 * d4) = r2;
 }
 
 namespace {
 
 // The workspace is sized for the most CTAs per SM that any shape runs.
 int attn_max_grid() { return 3 * num_sms(); }
+
+// The most units that the block table has room for, with `rows` heads per
+// segment and `tile` tokens per tile.
+long long attn_units(const moe_attn_dims& d, const moe_kv_cache& c, int rows, int tile) {
+  const long long tokens = std::min((long long)d.table_width * c.page_size, 0x7fffffffll);
+  const long long seg = (tokens + tile - 1) / tile + 1 + kSegCost;
+  return (long long)d.B * c.Hkv * cdiv(d.Hq / c.Hkv, rows) * seg;
+}
 
 template <int D, bool E4M3, int NH>
 cudaError_t launch_attn_nh(AttnArgs& a, cudaStream_t s) {
@@ -784,15 +806,13 @@ cudaError_t launch_attn_nh(AttnArgs& a, cudaStream_t s) {
   a.tile = S::kTile;
   a.gtiles = cdiv(a.G, S::kRows);
   a.HG = a.c.Hkv * a.gtiles;
-  // no more CTAs than the table could give the least shares
-  const long long most = (long long)a.d.B * a.HG *
-                         (((long long)a.d.table_width * a.c.page_size + S::kTile - 1) / S::kTile + 1 + kSegCost);
-  a.grid = (int)std::max(1ll, std::min((long long)S::kCtasPerSm * num_sms(),
-                                       (most + kMinUnits - 1) / kMinUnits));
+  // no more CTAs than the table could give parts
+  const long long most = attn_units(a.d, a.c, S::kRows, S::kTile) / kMinUnits + (long long)a.d.B * a.HG;
+  a.grid = (int)std::max(1ll, std::min((long long)S::kCtasPerSm * num_sms(), most));
   err = launch_k(k_paged_attention<D, E4M3, NH>, dim3(a.grid), dim3(kWarps * 32), S::kSmem, s, false, a);
   if (err != cudaSuccess) return err;
-  return launch_k(k_attn_join<D>, dim3(a.d.B * a.HG, std::min(a.G, S::kRows)), dim3(kJoinThreads),
-                  2 * (size_t)a.grid * sizeof(float), s, true, a);
+  return launch_k(k_attn_join<D>, dim3(a.grid, cdiv(std::min(a.G, S::kRows), kJoinHeads)),
+                  dim3(kJoinThreads), 0, s, true, a);
 }
 
 template <int D, bool E4M3>
@@ -802,9 +822,13 @@ cudaError_t launch_attn(AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+bool paged_attention_fits(const moe_attn_dims& d, const moe_kv_cache& cache) {
+  return attn_units(d, cache, 8, 16) + (1ll << 24) < (1ll << 31);
+}
+
 size_t paged_attention_workspace(const moe_attn_dims&, int D) {
   const size_t slots = 2 * (size_t)attn_max_grid();
-  return slots * kMaxRows * ((size_t)D + 2) * sizeof(float);
+  return slots * kMaxRows * ((size_t)D + 2) * sizeof(float) + attn_max_grid() * sizeof(int4);
 }
 
 cudaError_t launch_paged_attention(const uint16_t* q, const moe_kv_cache& cache,
@@ -821,6 +845,7 @@ cudaError_t launch_paged_attention(const uint16_t* q, const moe_kv_cache& cache,
   a.out = out;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = a.part_o + 2 * (size_t)attn_max_grid() * kMaxRows * cache.D;
+  a.jobs = reinterpret_cast<int4*>(a.part_ml + 2 * (size_t)attn_max_grid() * 2 * kMaxRows);
   a.status = status;
   // t / page_size for 0 <= t < 2^31: with 2^(e-1) < page_size <= 2^e and mul =
   // ceil(2^(31+e) / page_size) < 2^32, floor(t mul / 2^(31+e)) is exact

@@ -486,7 +486,8 @@ typedef struct {
  * hold anything, and the pages of a window's past may be reused.
  * Scores, maxima, sums and outputs are fp32; the softmax weights are rounded
  * to the cache's multiplication type (bf16 next to bf16 values, fp16 next to
- * E4M3 values).  D = 64, 128 or 256; up to 2^31 - 1 tokens per sequence.
+ * E4M3 values).  D = 64, 128 or 256; up to 2^31 - 1 tokens per sequence,
+ * and about 2^31 tiles of 16 tokens in all (B * Hkv * the table's room).
  * A page number outside [0, pages) or a length outside [0, table_width *
  * page_size] raises MOE_DEV_BAD_PAGE; the tokens of such a page are left
  * out, and such a length is clamped.

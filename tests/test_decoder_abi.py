@@ -88,7 +88,8 @@ def test_qk_norm_rope_refusals(L, kw, code):
     (dict(B=-1), INV), (dict(Hq=0), UNS), (dict(Hq=7), UNS), (dict(window=-1), INV),
     (dict(width=-1), INV), (dict(table_stride=3), INV), (dict(q_stride=1000), INV),
     (dict(out_stride=1028), INV), (dict(q=None), INV), (dict(table=None), INV), (dict(lens=None), INV),
-    (dict(out=P + 8), INV), (dict(ws=None), INV), (dict(nws=1000), WS), (dict(status=P + 4), INV)])
+    (dict(out=P + 8), INV), (dict(ws=None), INV), (dict(nws=1000), WS), (dict(status=P + 4), INV),
+    (dict(B=1 << 20, width=1 << 14, table_stride=1 << 14), UNS)])
 def test_paged_attention_refusals(L, kw, code):
     a = dict(B=2, Hq=8, window=0, width=4, table_stride=4, q_stride=1024, out_stride=1024, q=P, table=P,
              lens=P, out=P, ws=P, nws=1 << 30, status=None)
