@@ -2,6 +2,7 @@
 //   out[m, n] = sum_b Sx[m, b] Sw[n / 128, b] P_b[m, n] + bias[n],
 //   P_b[m, n] = sum over the 128 columns of block b of code_x code_w.
 #include "decoder_internal.h"
+#include "tcgen05.cuh"
 
 namespace moe {
 
@@ -142,18 +143,406 @@ k_linear_stream(const LinArgs a) {
   }
 }
 
-size_t linear_fp8_workspace(const moe_linear_dims&) { return 256; }
+// ---------------------------------------------------------------------------
+// Many rows: tcgen05
+// ---------------------------------------------------------------------------
+// Activations to E4M3: 16 lanes per group of 128 columns, 8 columns per lane.
+// codes [M][K]; scales transposed, sxt [ceil(K / 128)][ld], so that the GEMM's
+// lanes, which hold a row each, read them side by side.
+__global__ void __launch_bounds__(256)
+k_linear_quant(const uint16_t* __restrict__ x, long long x_stride, int M, int K,
+               uint8_t* __restrict__ codes, float* __restrict__ sxt, int ld,
+               int32_t* __restrict__ status) {
+  griddep_trigger();
+  const int nkb = cdiv(K, kScaleBlock);
+  const long long unit = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int part = threadIdx.x & 15;
+  const bool in = unit < (long long)M * nkb;
+  const int m = in ? (int)(unit / nkb) : 0, kb = in ? (int)(unit % nkb) : 0;
+  const int col = kb * kScaleBlock + 8 * part;
+  const bool real = in && col < K;
+  const uint4 v = real ? ldg_stream16(x + (size_t)m * x_stride + col) : make_uint4(0, 0, 0, 0);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t mx = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) mx = max(mx, max(w[u] & 0x7FFFu, (w[u] >> 16) & 0x7FFFu));
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (mx >= 0x7F80u && part == 0) raise_status(status, MOE_DEV_NONFINITE);
+  float f, scale;
+  quant_factors(mx << 16, f, scale);
+  uint32_t c[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    c[u] = f32x2_to_e4m3x2(bf16_lo(w[2 * u]) * f, bf16_hi(w[2 * u]) * f) |
+           (f32x2_to_e4m3x2(bf16_lo(w[2 * u + 1]) * f, bf16_hi(w[2 * u + 1]) * f) << 16);
+  if (real) *reinterpret_cast<uint2*>(codes + (size_t)m * K + col) = make_uint2(c[0], c[1]);
+  if (in && part == 0) sxt[(size_t)kb * ld + m] = scale;
+}
+
+namespace {
+constexpr int GM = 128, GN = 128;        // rows (TMEM lanes) x features (TMEM columns) per CTA
+constexpr int GSTAGES = 3;
+constexpr int G_TILE = 128 * 128;        // bytes of one operand's 128 rows x 128 K
+constexpr int G_STAGE = 2 * G_TILE;
+constexpr int G_PITCH = GN + 4;          // floats per row of the split's exchange
+constexpr int G_SMEM = GSTAGES * G_STAGE + 1024;
+constexpr int kProWarps = 8;
+constexpr int kGemmThreads = (2 + kProWarps) * 32;
+static_assert(GM * G_PITCH * 4 <= GSTAGES * G_STAGE, "the exchange reuses the stages");
+
+struct GemmArgs {
+  const float* sxt;
+  int ld;
+  const float* sw;
+  const float* bias;
+  uint16_t* out;
+  long long out_stride;
+  int M, N, nkb;
+  int32_t* status;
+};
+
+struct GemmShared {
+  uint64_t full[GSTAGES], empty[GSTAGES], p_full[2], p_empty[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Warp-uniform bounded wait: the warp gives up together once the budget is
+// spent or another role has given up.
+__device__ __forceinline__ bool gwait(GemmShared& sh, uint64_t* bar, uint32_t parity,
+                                      int32_t* status) {
+  constexpr unsigned kAll = 0xffffffffu;
+  bool done = mbar_try_wait(bar, parity);
+  if (__all_sync(kAll, done)) return true;
+  const WaitBudget b = wait_budget();
+  for (uint32_t n = 1;; ++n) {
+    if (__any_sync(kAll, done)) {
+      for (int r = 0; !done && r < (1 << 16); ++r) done = mbar_try_wait(bar, parity);
+      if (__all_sync(kAll, done)) return true;
+      break;
+    }
+    if ((n & 31) == 0) {
+      const bool give_up = *reinterpret_cast<volatile int*>(&sh.abort_flag) != 0 || budget_spent(b);
+      if (__any_sync(kAll, give_up)) break;
+    }
+    done = mbar_try_wait(bar, parity);
+  }
+  if ((threadIdx.x & 31) == 0 && !sh.abort_flag) {
+    sh.abort_flag = 1;
+    raise_status(status, MOE_DEV_WAIT_TIMEOUT);
+  }
+  __syncwarp();
+  return false;
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// (a.x, a.y) += (p.x, p.y) * (f, f)
+__device__ __forceinline__ void fma2(float2& a, uint32_t p0, uint32_t p1, float f) {
+  asm("{\n .reg .b64 A, P, F;\n mov.b64 A, {%0, %1};\n mov.b64 P, {%2, %3};\n mov.b64 F, {%4, %4};\n"
+      " fma.rn.f32x2 A, P, F, A;\n mov.b64 {%0, %1}, A;\n}\n"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(p0), "r"(p1), "f"(f));
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::
+                   : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t local, uint32_t rank) {
+  float4 v;
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(local), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(r)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float bias_at(const GemmArgs& a, int n) {
+  return a.bias ? __ldg(a.bias + n) : 0.f;
+}
+}  // namespace
+
+// One 128 x 128 tile of the output per cluster, the K blocks divided over its
+// CTAs.  Warp 0 fills a ring of stages by TMA (128 rows x 128 K of either
+// operand, 128-byte swizzled; what lies outside the matrices reads as zero),
+// one thread of warp 1 issues the four K = 32 MMAs of a block into one of two
+// TMEM buffers, and warps 2-9 add the block's sums, times Sx of their row and
+// Sw of the tile, to fp32 sums in registers (a thread: one row, 64 features).
+// The weights' first stages are on their way before the quantisation ends.
+// A cluster's sums meet in shared memory: each CTA adds its share of the rows
+// over the CTAs in order and writes it.
+template <int SPLIT>
+__global__ void __launch_bounds__(kGemmThreads, 2)
+k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+              const GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ GemmShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = SPLIT > 1 ? blockIdx.x : 0;
+  const int n0 = blockIdx.y * GN, m0 = blockIdx.z * GM;
+  const int kb0 = rank * a.nkb / SPLIT, kb1 = (rank + 1) * a.nkb / SPLIT, nk = kb1 - kb0;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  if (tid == 0) {
+    for (int s = 0; s < GSTAGES; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.p_full[b], 1);
+      mbar_init(&sh.p_empty[b], kProWarps);
+    }
+    sh.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&sh.tmem_base, 2 * GN);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;
+  float2 acc[32];
+
+  if (warp == 0) {
+    const int ahead = min(nk, GSTAGES);
+    if (tc::elect_one())
+      for (int i = 0; i < ahead; ++i) {
+        mbar_arrive_expect_tx(&sh.full[i], G_STAGE);
+        tc::tma_load_2d(smem + i * G_STAGE + G_TILE, &wmap, (kb0 + i) * kScaleBlock, n0, &sh.full[i]);
+      }
+    __syncwarp();
+    griddep_wait();  // the codes of x
+    if (tc::elect_one())
+      for (int i = 0; i < ahead; ++i)
+        tc::tma_load_2d(smem + i * G_STAGE, &xmap, (kb0 + i) * kScaleBlock, m0, &sh.full[i]);
+    __syncwarp();
+    int i = ahead;
+    for (; i < nk; ++i) {
+      const int s = i % GSTAGES;
+      if (!gwait(sh, &sh.empty[s], (uint32_t)((i / GSTAGES - 1) & 1), a.status)) break;
+      if (tc::elect_one()) {
+        mbar_arrive_expect_tx(&sh.full[s], G_STAGE);
+        tc::tma_load_2d(smem + s * G_STAGE + G_TILE, &wmap, (kb0 + i) * kScaleBlock, n0, &sh.full[s]);
+        tc::tma_load_2d(smem + s * G_STAGE, &xmap, (kb0 + i) * kScaleBlock, m0, &sh.full[s]);
+      }
+      __syncwarp();
+    }
+    // every copy has landed before the stages are reused or the CTA ends
+    if (lane == 0)
+      for (int j = max(0, i - GSTAGES); j < i; ++j)
+        mbar_wait(&sh.full[j % GSTAGES], (uint32_t)((j / GSTAGES) & 1));
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t idesc = tc::idesc_f16_f32(GM, GN);  // the same fields; format 0 is E4M3 here
+    int i = 0;
+    for (; i < nk; ++i) {
+      const int s = i % GSTAGES, b = i & 1;
+      if (!gwait(sh, &sh.full[s], (uint32_t)((i / GSTAGES) & 1), a.status)) break;
+      if (i >= 2 && !gwait(sh, &sh.p_empty[b], (uint32_t)((i / 2 - 1) & 1), a.status)) break;
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
+        const uint32_t xa = smem_u32(smem) + s * G_STAGE, wa = xa + G_TILE;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f8(tmem + b * GN, tc::sw128_desc(xa + 32 * k), tc::sw128_desc(wa + 32 * k), idesc, k > 0);
+        tc::commit(&sh.empty[s]);
+        tc::commit(&sh.p_full[b]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0 && i > 0) mbar_wait(&sh.p_full[(i - 1) & 1], (uint32_t)(((i - 1) / 2) & 1));
+    __syncwarp();
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int m = m0 + 32 * q + lane;
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16) + 64 * half;
+    const float* sw = a.sw + (size_t)(n0 / kScaleBlock) * a.nkb + kb0;
+    const float* sx = a.sxt + (size_t)kb0 * a.ld + (m < a.M ? m : 0);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[j] = make_float2(0.f, 0.f);
+    griddep_wait();  // the scales of x
+    // scales two blocks ahead: a block's MMAs are shorter than a load
+    float f0 = __ldcg(sx) * __ldg(sw), f1 = 0.f;
+    if (nk > 1) f1 = __ldcg(sx + a.ld) * __ldg(sw + 1);
+    for (int i = 0; i < nk; ++i) {
+      const int b = i & 1;
+      float x2 = 0.f, w2 = 0.f;
+      if (i + 2 < nk) {
+        x2 = __ldcg(sx + (size_t)(i + 2) * a.ld);
+        w2 = __ldg(sw + i + 2);
+      }
+      if (!gwait(sh, &sh.p_full[b], (uint32_t)((i / 2) & 1), a.status)) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[32];
+        tc::ld_32x32b_x32(t_lane + b * GN + 32 * h, p);
+        tc::wait_ld();
+        if (h == 1) {  // the next block but one may overwrite the buffer
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_empty[b]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) fma2(acc[16 * h + j], p[2 * j], p[2 * j + 1], f0);
+      }
+      f0 = f1;
+      f1 = x2 * w2;
+    }
+    if (SPLIT == 1) {
+      if (m < a.M) {
+        uint16_t* row = a.out + (size_t)m * a.out_stride;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int n = n0 + 64 * half + 8 * j;
+          if (n < a.N) {
+            uint32_t r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              r[u] = pack_bf16x2(acc[4 * j + u].x + bias_at(a, n + 2 * u),
+                                 acc[4 * j + u].y + bias_at(a, n + 2 * u + 1));
+            *reinterpret_cast<uint4*>(row + n) = make_uint4(r[0], r[1], r[2], r[3]);
+          }
+        }
+      }
+    }
+  }
+  if (SPLIT > 1) {
+    __syncthreads();  // every stage's copies have landed and every MMA has read them
+    float* ex = reinterpret_cast<float*>(smem);  // [GM][G_PITCH]
+    if (warp >= 2) {
+      float* row = ex + (32 * (warp & 3) + lane) * G_PITCH + 64 * ((warp - 2) >> 2);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        *reinterpret_cast<float4*>(row + 4 * j) =
+            make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+    }
+    __syncwarp();
+    cluster_sync();
+    constexpr int kRowsOf = GM / SPLIT;
+    for (int e = tid; e < kRowsOf * (GN / 8); e += kGemmThreads) {
+      const int r = rank * kRowsOf + e / (GN / 8), c8 = 8 * (e % (GN / 8));
+      if (m0 + r >= a.M || n0 + c8 >= a.N) continue;
+      const uint32_t at = smem_u32(ex + r * G_PITCH + c8);
+      float v[8] = {};
+#pragma unroll
+      for (int p = 0; p < SPLIT; ++p) {
+        const float4 lo = ld_cluster(at, p), hi = ld_cluster(at + 16, p);
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        o[u] = pack_bf16x2(v[2 * u] + bias_at(a, n0 + c8 + 2 * u), v[2 * u + 1] + bias_at(a, n0 + c8 + 2 * u + 1));
+      *reinterpret_cast<uint4*>(a.out + (size_t)(m0 + r) * a.out_stride + n0 + c8) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    __syncwarp();
+    cluster_sync();  // the neighbours have read this CTA's sums
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 2 * GN);
+  }
+}
+
+namespace {
+
+// Rows up to which the streamed kernel is the faster one.
+constexpr int kStreamRows = 16;
+
+bool linear_streams(const moe_linear_dims& d) { return d.M <= kStreamRows; }
+
+struct LinWs {
+  size_t codes, sxt, total;
+  int ld;
+};
+LinWs lin_ws(const moe_linear_dims& d) {
+  LinWs w{};
+  if (linear_streams(d)) {
+    w.total = 256;
+    return w;
+  }
+  const size_t nkb = cdiv(d.K, kScaleBlock);
+  w.ld = cdiv(d.M, 32) * 32;
+  w.codes = 0;
+  w.sxt = ((size_t)d.M * d.K + 255) & ~size_t(255);
+  w.total = w.sxt + nkb * w.ld * sizeof(float);
+  return w;
+}
+
+template <int SPLIT>
+cudaError_t launch_gemm(const CUtensorMap& xmap, const CUtensorMap& wmap, const GemmArgs& a,
+                        cudaStream_t s) {
+  cudaError_t err = ensure_smem((const void*)k_linear_gemm<SPLIT>, G_SMEM);
+  if (err != cudaSuccess) return err;
+  count_launch();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(SPLIT, cdiv(a.N, GN), cdiv(a.M, GM));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = G_SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = SPLIT;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_linear_gemm<SPLIT>, xmap, wmap, a);
+}
+
+}  // namespace
+
+size_t linear_fp8_workspace(const moe_linear_dims& d) { return lin_ws(d).total; }
 
 cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const float* bias,
                               const moe_linear_dims& d, uint16_t* out, void* ws, int32_t* status,
                               cudaStream_t s) {
-  const LinArgs a{x, d.x_stride, w.codes, w.scales, bias, out, d.out_stride, d.M, d.N, d.K, status};
-  const dim3 blk(kLinWarps * 32);
-  const int nt = d.M <= 8 ? 1 : d.M <= 16 ? 2 : 4;
-  const dim3 grid(cdiv(d.N, 16), cdiv(d.M, 8 * nt));
-  if (nt == 1) return launch_k(k_linear_stream<1>, grid, blk, 0, s, false, a);
-  if (nt == 2) return launch_k(k_linear_stream<2>, grid, blk, 0, s, false, a);
-  return launch_k(k_linear_stream<4>, grid, blk, 0, s, false, a);
+  if (linear_streams(d)) {
+    const LinArgs a{x, d.x_stride, w.codes, w.scales, bias, out, d.out_stride, d.M, d.N, d.K, status};
+    const dim3 blk(kLinWarps * 32), grid(cdiv(d.N, 16), 1);
+    if (d.M <= 8) return launch_k(k_linear_stream<1>, grid, blk, 0, s, false, a);
+    return launch_k(k_linear_stream<2>, grid, blk, 0, s, false, a);
+  }
+  const LinWs l = lin_ws(d);
+  uint8_t* codes = static_cast<uint8_t*>(ws) + l.codes;
+  float* sxt = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.sxt);
+  const int nkb = cdiv(d.K, kScaleBlock);
+  CUtensorMap xmap, wmap;
+  cudaError_t err;
+  if ((err = make_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, d.M, d.K,
+                                kScaleBlock, GM, 128)) != cudaSuccess ||
+      (err = make_tensor_map_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, d.N, d.K,
+                                kScaleBlock, GN, 128)) != cudaSuccess)
+    return err;
+  const long long groups = (long long)d.M * nkb;
+  err = launch_k(k_linear_quant, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, s, false, x,
+                 (long long)d.x_stride, d.M, d.K, codes, sxt, l.ld, status);
+  if (err != cudaSuccess) return err;
+  const GemmArgs a{sxt, l.ld, w.scales, bias, out, d.out_stride, d.M, d.N, nkb, status};
+  const int tiles = cdiv(d.M, GM) * cdiv(d.N, GN);
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 2 * num_sms() && nkb >= 4 * split) split *= 2;
+  if (split == 1) return launch_gemm<1>(xmap, wmap, a, s);
+  if (split == 2) return launch_gemm<2>(xmap, wmap, a, s);
+  if (split == 4) return launch_gemm<4>(xmap, wmap, a, s);
+  return launch_gemm<8>(xmap, wmap, a, s);
 }
 
 }  // namespace moe
