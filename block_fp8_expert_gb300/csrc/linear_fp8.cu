@@ -1,6 +1,8 @@
 // Block-FP8 linear layer on E4M3 activations (moe_linear_fp8):
 //   out[m, n] = sum_b Sx[m, b] Sw[n / 128, b] P_b[m, n] + bias[n],
 //   P_b[m, n] = sum over the 128 columns of block b of code_x code_w.
+#include <algorithm>
+
 #include "decoder_internal.h"
 #include "tcgen05.cuh"
 
@@ -205,12 +207,13 @@ struct GemmArgs {
 struct GemmShared {
   uint64_t full[GSTAGES], empty[GSTAGES], p_full[2], p_empty[2];
   uint32_t tmem_base;
-  int abort_flag;
+  volatile int abort_flag;
 };
 
 // Warp-uniform bounded wait: the warp gives up together once the budget is
 // spent or another role has given up.
-__device__ __forceinline__ bool gwait(GemmShared& sh, uint64_t* bar, uint32_t parity,
+template <class Shared>
+__device__ __forceinline__ bool gwait(Shared& sh, uint64_t* bar, uint32_t parity,
                                       int32_t* status) {
   constexpr unsigned kAll = 0xffffffffu;
   bool done = mbar_try_wait(bar, parity);
@@ -223,7 +226,7 @@ __device__ __forceinline__ bool gwait(GemmShared& sh, uint64_t* bar, uint32_t pa
       break;
     }
     if ((n & 31) == 0) {
-      const bool give_up = *reinterpret_cast<volatile int*>(&sh.abort_flag) != 0 || budget_spent(b);
+      const bool give_up = sh.abort_flag != 0 || budget_spent(b);
       if (__any_sync(kAll, give_up)) break;
     }
     done = mbar_try_wait(bar, parity);
@@ -265,6 +268,27 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t local, uint32_t rank) {
                : "memory");
   return v;
 }
+// A warp's 32 rows x 64 features (a row per lane) as bf16 into a 4 KB tile of
+// shared memory, 128-byte swizzled as the TMA store reads it: a thread's own
+// stores would touch 32 rows at a time, half a sector of each.
+__device__ __forceinline__ void stage_rows(uint8_t* tile, const float2 (&acc)[32], const float* bias,
+                                           int n0, int N, int lane) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint32_t r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float2 v = acc[4 * j + u];
+      const int n = n0 + 8 * j + 2 * u;
+      if (bias && n < N) {
+        v.x += __ldg(bias + n);
+        v.y += __ldg(bias + n + 1);
+      }
+      r[u] = pack_bf16x2(v.x, v.y);
+    }
+    *reinterpret_cast<uint4*>(tile + tc::sw128_off(lane, j)) = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+}
 __device__ __forceinline__ float bias_at(const GemmArgs& a, int n) {
   return a.bias ? __ldg(a.bias + n) : 0.f;
 }
@@ -282,7 +306,7 @@ __device__ __forceinline__ float bias_at(const GemmArgs& a, int n) {
 template <int SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 2)
 k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-              const GemmArgs a) {
+              const __grid_constant__ CUtensorMap omap, const GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ GemmShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -337,10 +361,13 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
       }
       __syncwarp();
     }
-    // every copy has landed before the stages are reused or the CTA ends
+    // every copy has landed and every commit has arrived before the stages are
+    // reused or the CTA ends
     if (lane == 0)
-      for (int j = max(0, i - GSTAGES); j < i; ++j)
+      for (int j = max(0, i - GSTAGES); j < i; ++j) {
         mbar_wait(&sh.full[j % GSTAGES], (uint32_t)((j / GSTAGES) & 1));
+        if (!sh.abort_flag) mbar_wait(&sh.empty[j % GSTAGES], (uint32_t)((j / GSTAGES) & 1));
+      }
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = tc::idesc_f16_f32(GM, GN);  // the same fields; format 0 is E4M3 here
@@ -372,53 +399,53 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
     for (int j = 0; j < 32; ++j) acc[j] = make_float2(0.f, 0.f);
     griddep_wait();  // the scales of x
     // scales two blocks ahead: a block's MMAs are shorter than a load
-    float f0 = __ldcg(sx) * __ldg(sw), f1 = 0.f;
-    if (nk > 1) f1 = __ldcg(sx + a.ld) * __ldg(sw + 1);
+    float x0 = __ldcg(sx), w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
+    if (nk > 1) {
+      x1 = __ldcg(sx + a.ld);
+      w1 = __ldg(sw + 1);
+    }
     for (int i = 0; i < nk; ++i) {
       const int b = i & 1;
-      float x2 = 0.f, w2 = 0.f;
+      const float f0 = x0 * w0;
+      x0 = x1;
+      w0 = w1;
       if (i + 2 < nk) {
-        x2 = __ldcg(sx + (size_t)(i + 2) * a.ld);
-        w2 = __ldg(sw + i + 2);
+        x1 = __ldcg(sx + (size_t)(i + 2) * a.ld);
+        w1 = __ldg(sw + i + 2);
       }
       if (!gwait(sh, &sh.p_full[b], (uint32_t)((i / 2) & 1), a.status)) break;
       tc::fence_after_sync();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
-        tc::ld_32x32b_x32(t_lane + b * GN + 32 * h, p);
+      for (int h = 0; h < 4; ++h) {
+        uint32_t p[16];
+        tc::ld_32x32b_x16(t_lane + b * GN + 16 * h, p);
         tc::wait_ld();
-        if (h == 1) {  // the next block but one may overwrite the buffer
+        if (h == 3) {  // the next block but one may overwrite the buffer
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.p_empty[b]);
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) fma2(acc[16 * h + j], p[2 * j], p[2 * j + 1], f0);
-      }
-      f0 = f1;
-      f1 = x2 * w2;
-    }
-    if (SPLIT == 1) {
-      if (m < a.M) {
-        uint16_t* row = a.out + (size_t)m * a.out_stride;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int n = n0 + 64 * half + 8 * j;
-          if (n < a.N) {
-            uint32_t r[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              r[u] = pack_bf16x2(acc[4 * j + u].x + bias_at(a, n + 2 * u),
-                                 acc[4 * j + u].y + bias_at(a, n + 2 * u + 1));
-            *reinterpret_cast<uint4*>(row + n) = make_uint4(r[0], r[1], r[2], r[3]);
-          }
-        }
+        for (int j = 0; j < 8; ++j) fma2(acc[8 * h + j], p[2 * j], p[2 * j + 1], f0);
       }
     }
   }
-  if (SPLIT > 1) {
-    __syncthreads();  // every stage's copies have landed and every MMA has read them
+  __syncthreads();  // every stage's copies have landed and every MMA has read them
+  if (SPLIT == 1) {
+    if (warp >= 2) {
+      const int n = n0 + 64 * ((warp - 2) >> 2), m = m0 + 32 * (warp & 3);
+      uint8_t* tile = smem + (warp - 2) * 4096;
+      stage_rows(tile, acc, a.bias, n, a.N, lane);
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (n < a.N && m < a.M && tc::elect_one()) {
+        tc::tma_store_2d(&omap, n, m, tile);
+        tc::bulk_commit();
+        tc::bulk_wait_all();
+      }
+      __syncwarp();
+    }
+  } else {
     float* ex = reinterpret_cast<float*>(smem);  // [GM][G_PITCH]
     if (warp >= 2) {
       float* row = ex + (32 * (warp & 3) + lane) * G_PITCH + 64 * ((warp - 2) >> 2);
@@ -459,6 +486,245 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many tiles: CTA pairs
+// ---------------------------------------------------------------------------
+// Two CTAs (cta_group::2) own a 256 x 256 tile: each holds 128 rows of x and
+// 128 rows of W in shared memory, the pair's MMA (M 256, N 256) reads both,
+// and each CTA's tensor memory receives its 128 rows x 256 features.  An SM
+// then loads 32 KB per K block where a lone CTA with the same tile per SM
+// (128 x 256) would load 48 KB, and its MMAs read a third less shared memory.
+// Roles as above, with these differences:
+//  - the first CTA's `full` barriers count the bytes of both CTAs' copies and
+//    its warp 1 issues all MMAs; the commits arrive in both CTAs;
+//  - the promoting warps of both CTAs arrive on the first CTA's p_empty;
+//  - sixteen promoting warps, a thread owns a row and 64 features: with eight
+//    (128 features each) the loads' latency, not their rate, set the pace;
+//  - the pairs walk over the tiles (persistent), the next tile's first blocks
+//    being computed while the last one is written.
+namespace {
+constexpr int PT = 256;                  // rows and features of a pair's tile
+constexpr int PSTAGES = 5;
+constexpr int kPairProWarps = 16;
+constexpr int kPairThreads = (2 + kPairProWarps) * 32;
+constexpr int P_SMEM = PSTAGES * G_STAGE + kPairProWarps * 4096 + 1024;
+static_assert(P_SMEM + 1024 <= 227 * 1024, "shared memory");
+
+struct PairShared {
+  uint64_t full[PSTAGES], empty[PSTAGES], p_full[2], p_empty[2];
+  uint32_t tmem_base;
+  volatile int abort_flag;
+};
+
+// The address of the same shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+// (relaxed: what it announces, tensor memory that has been read, is ordered by
+// the tcgen05 waits and fences; a release would wait for the loads in flight)
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+// TMA load into this CTA, its bytes counted on a barrier of the pair.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier of both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+}  // namespace
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
+                   const __grid_constant__ CUtensorMap wmap,
+                   const __grid_constant__ CUtensorMap omap, const GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PairShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int tn = cdiv(a.N, PT), tiles = tn * cdiv(a.M, PT), nk = a.nkb;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  if (tid == 0) {
+    for (int s = 0; s < PSTAGES; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.p_full[b], 1);
+      mbar_init(&sh.p_empty[b], 2 * kPairProWarps);
+    }
+    sh.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+                     smem_u32(&sh.tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers and tensor memory are ready
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;
+
+  if (warp == 0) {
+    int it = 0;
+    bool ok = true, waited = false;
+    for (int t = pair; t < tiles && ok; t += npairs) {
+      const int n0 = (t % tn) * PT + 128 * rank, m0 = (t / tn) * PT + 128 * rank;
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        const int s = it % PSTAGES;
+        if (it >= PSTAGES && !gwait(sh, &sh.empty[s], (uint32_t)((it / PSTAGES - 1) & 1), a.status)) {
+          ok = false;
+          break;
+        }
+        if (tc::elect_one()) {
+          const uint32_t bar = in_cta(&sh.full[s], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * G_STAGE);
+          tma_load_pair(smem + s * G_STAGE + G_TILE, &wmap, kb * kScaleBlock, n0, bar);
+        }
+        __syncwarp();
+        if (!waited) griddep_wait();  // the codes of x
+        waited = true;
+        if (tc::elect_one())
+          tma_load_pair(smem + s * G_STAGE, &xmap, kb * kScaleBlock, m0, in_cta(&sh.full[s], 0));
+        __syncwarp();
+      }
+    }
+    // every copy of the pair has landed (counted in the first CTA) and every
+    // commit has arrived
+    if (lane == 0)
+      for (int j = max(0, it - PSTAGES); j < it; ++j) {
+        if (rank == 0) mbar_wait(&sh.full[j % PSTAGES], (uint32_t)((j / PSTAGES) & 1));
+        if (!sh.abort_flag) mbar_wait(&sh.empty[j % PSTAGES], (uint32_t)((j / PSTAGES) & 1));
+      }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t idesc = tc::idesc_f16_f32(PT, PT);  // the same fields; format 0 is E4M3 here
+      int it = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += npairs)
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % PSTAGES, b = it & 1;
+          if (!gwait(sh, &sh.full[s], (uint32_t)((it / PSTAGES) & 1), a.status) ||
+              (it >= 2 && !gwait(sh, &sh.p_empty[b], (uint32_t)((it / 2 - 1) & 1), a.status))) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            const uint32_t xa = smem_u32(smem) + s * G_STAGE, wa = xa + G_TILE;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f8_pair(tmem + b * PT, tc::sw128_desc(xa + 32 * k), tc::sw128_desc(wa + 32 * k), idesc,
+                          k > 0);
+            commit_pair(&sh.empty[s]);
+            commit_pair(&sh.p_full[b]);
+          }
+          __syncwarp();
+        }
+      if (lane == 0 && it > 0) mbar_wait(&sh.p_full[(it - 1) & 1], (uint32_t)(((it - 1) / 2) & 1));
+      __syncwarp();
+    }
+  } else {
+    const int q = warp & 3, part = (warp - 2) >> 2;  // lanes 32 q .., features 64 part ..
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16) + 64 * part;
+    uint8_t* const tile = smem + PSTAGES * G_STAGE + (warp - 2) * 4096;
+    const uint32_t p_empty[2] = {in_cta(&sh.p_empty[0], 0), in_cta(&sh.p_empty[1], 0)};
+    griddep_wait();  // the scales of x
+    int it = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += npairs) {
+      const int n0 = (t % tn) * PT + 64 * part, m = (t / tn) * PT + 128 * rank + 32 * q + lane;
+      // (a tile's last features may lie past the matrix: any scale will do for
+      // their zeros)
+      const float* sw = a.sw + (size_t)(n0 < a.N ? n0 / kScaleBlock : 0) * nk;
+      const float* sx = a.sxt + (m < a.M ? m : 0);
+      float2 acc[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) acc[j] = make_float2(0.f, 0.f);
+      // scales two blocks ahead: a block's MMAs are shorter than a load
+      float x0 = __ldcg(sx), w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
+      if (nk > 1) {
+        x1 = __ldcg(sx + a.ld);
+        w1 = __ldg(sw + 1);
+      }
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        const int b = it & 1;
+        const float f0 = x0 * w0;
+        x0 = x1;
+        w0 = w1;
+        if (kb + 2 < nk) {
+          x1 = __ldcg(sx + (size_t)(kb + 2) * a.ld);
+          w1 = __ldg(sw + kb + 2);
+        }
+        if (!gwait(sh, &sh.p_full[b], (uint32_t)((it / 2) & 1), a.status)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t p[16];
+          tc::ld_32x32b_x16(t_lane + b * PT + 16 * h, p);
+          tc::wait_ld();
+          if (h == 3) {  // the next block but one may overwrite the buffer
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(p_empty[b]);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) fma2(acc[8 * h + j], p[2 * j], p[2 * j + 1], f0);
+        }
+      }
+      if (ok) {
+        if (lane == 0) tc::bulk_wait_read_all();  // the previous tile has left the buffer
+        __syncwarp();
+        stage_rows(tile, acc, a.bias, n0, a.N, lane);
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0 && n0 < a.N && m < a.M) {
+          tc::tma_store_2d(&omap, n0, m, tile);
+          tc::bulk_commit();
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) tc::bulk_wait_all();
+    __syncwarp();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // nothing of the pair is on its way to either CTA any more
+  if (warp == 1) {
+    tc::fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+  }
+}
+
 namespace {
 
 // Rows up to which the streamed kernel is the faster one.
@@ -485,8 +751,8 @@ LinWs lin_ws(const moe_linear_dims& d) {
 }
 
 template <int SPLIT>
-cudaError_t launch_gemm(const CUtensorMap& xmap, const CUtensorMap& wmap, const GemmArgs& a,
-                        cudaStream_t s) {
+cudaError_t launch_gemm(const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& omap,
+                        const GemmArgs& a, cudaStream_t s) {
   cudaError_t err = ensure_smem((const void*)k_linear_gemm<SPLIT>, G_SMEM);
   if (err != cudaSuccess) return err;
   count_launch();
@@ -504,7 +770,41 @@ cudaError_t launch_gemm(const CUtensorMap& xmap, const CUtensorMap& wmap, const 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_linear_gemm<SPLIT>, xmap, wmap, a);
+  return cudaLaunchKernelEx(&cfg, k_linear_gemm<SPLIT>, xmap, wmap, omap, a);
+}
+
+// CTA pairs that can run at once on the current device.
+int max_pairs() {
+  static int cached[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms() / 2;
+  if (!cached[dev]) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = P_SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_linear_gemm_pair, &cfg) != cudaSuccess || n < 1)
+      n = num_sms() / 2;
+    cached[dev] = std::min(n, num_sms() / 2);
+  }
+  return cached[dev];
+}
+
+cudaError_t launch_gemm_pair(const CUtensorMap& xmap, const CUtensorMap& wmap,
+                             const CUtensorMap& omap, const GemmArgs& a, cudaStream_t s) {
+  cudaError_t err = ensure_smem((const void*)k_linear_gemm_pair, P_SMEM);
+  if (err != cudaSuccess) return err;
+  const int pairs = std::min(max_pairs(), cdiv(a.M, PT) * cdiv(a.N, PT));
+  return launch_k(k_linear_gemm_pair, dim3(2 * pairs), dim3(kPairThreads), (size_t)P_SMEM, s, true,
+                  xmap, wmap, omap, a);
 }
 
 }  // namespace
@@ -524,12 +824,14 @@ cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const flo
   uint8_t* codes = static_cast<uint8_t*>(ws) + l.codes;
   float* sxt = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.sxt);
   const int nkb = cdiv(d.K, kScaleBlock);
-  CUtensorMap xmap, wmap;
+  CUtensorMap xmap, wmap, omap;
   cudaError_t err;
   if ((err = make_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, d.M, d.K,
                                 kScaleBlock, GM, 128)) != cudaSuccess ||
       (err = make_tensor_map_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, d.N, d.K,
-                                kScaleBlock, GN, 128)) != cudaSuccess)
+                                kScaleBlock, GN, 128)) != cudaSuccess ||
+      (err = make_tensor_map_2d(&omap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, d.M, d.N, 64, 32,
+                                128, d.out_stride)) != cudaSuccess)
     return err;
   const long long groups = (long long)d.M * nkb;
   err = launch_k(k_linear_quant, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, s, false, x,
@@ -537,12 +839,13 @@ cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const flo
   if (err != cudaSuccess) return err;
   const GemmArgs a{sxt, l.ld, w.scales, bias, out, d.out_stride, d.M, d.N, nkb, status};
   const int tiles = cdiv(d.M, GM) * cdiv(d.N, GN);
+  if (cdiv(d.M, PT) * cdiv(d.N, PT) >= num_sms() / 2) return launch_gemm_pair(xmap, wmap, omap, a, s);
   int split = 1;
   while (split < 8 && tiles * split * 2 <= 2 * num_sms() && nkb >= 4 * split) split *= 2;
-  if (split == 1) return launch_gemm<1>(xmap, wmap, a, s);
-  if (split == 2) return launch_gemm<2>(xmap, wmap, a, s);
-  if (split == 4) return launch_gemm<4>(xmap, wmap, a, s);
-  return launch_gemm<8>(xmap, wmap, a, s);
+  if (split == 1) return launch_gemm<1>(xmap, wmap, omap, a, s);
+  if (split == 2) return launch_gemm<2>(xmap, wmap, omap, a, s);
+  if (split == 4) return launch_gemm<4>(xmap, wmap, omap, a, s);
+  return launch_gemm<8>(xmap, wmap, omap, a, s);
 }
 
 }  // namespace moe

@@ -516,7 +516,7 @@ def _linear_tol(ref, S):
 LINEAR = [(1, 64, 128), (1, 8, 16), (3, 136, 80), (8, 512, 2048), (9, 128, 256), (16, 264, 400),
           (17, 128, 128), (31, 1000, 1040), (33, 256, 512), (64, 2048, 4096), (65, 384, 896), (127, 136, 272),
           (128, 640, 1024), (200, 1288, 528), (257, 512, 16), (300, 264, 2048), (513, 1024, 1152),
-          (1030, 2056, 336)]
+          (1030, 2056, 336), (2600, 2056, 272), (1300, 4104, 1040), (4097, 1288, 640)]
 
 
 @pytest.mark.parametrize("M,N,K", LINEAR)
