@@ -22,6 +22,7 @@ inline moe_status fail(moe_status s, const char* fmt, ...) {
 }
 
 inline moe_status cuda_fail(cudaError_t e, const char* where) {
+  cudaGetLastError();  // reported here: the caller's next CUDA check shall not meet it again
   return fail(MOE_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 

@@ -189,6 +189,11 @@ constexpr int G_TILE = 128 * 128;        // bytes of one operand's 128 rows x 12
 constexpr int G_STAGE = 2 * G_TILE;
 constexpr int G_PITCH = GN + 4;          // floats per row of the split's exchange
 constexpr int G_SMEM = GSTAGES * G_STAGE + 1024;
+// The activation scales of a block's 128 rows ride with its stage, into a ring
+// of their own that is two slots longer: a stage is refilled once its MMAs are
+// done, when the sums of all but the last two blocks have been read (p_empty).
+constexpr int G_SX = 128 * 4;
+constexpr int GSX_SLOTS = GSTAGES + 2;
 constexpr int kProWarps = 8;
 constexpr int kGemmThreads = (2 + kProWarps) * 32;
 static_assert(GM * G_PITCH * 4 <= GSTAGES * G_STAGE, "the exchange reuses the stages");
@@ -205,6 +210,7 @@ struct GemmArgs {
 };
 
 struct GemmShared {
+  alignas(16) float sx[GSX_SLOTS][128];
   uint64_t full[GSTAGES], empty[GSTAGES], p_full[2], p_empty[2];
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -289,6 +295,19 @@ __device__ __forceinline__ void stage_rows(uint8_t* tile, const float2 (&acc)[32
     *reinterpret_cast<uint4*>(tile + tc::sw128_off(lane, j)) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
+// A tile row of weight scales, block kb of kb0 .. kb1 in lane (kb - kb0) % 32:
+// one load per 32 blocks, handed round by shuffles.
+struct BlockScales {
+  const float* p;
+  int n, lane;
+  float v;
+  __device__ __forceinline__ BlockScales(const float* p_, int n_, int lane_)
+      : p(p_), n(n_), lane(lane_), v(lane_ < n_ ? __ldg(p_ + lane_) : 0.f) {}
+  __device__ __forceinline__ float at(int i) {
+    if (i > 0 && (i & 31) == 0) v = i + lane < n ? __ldg(p + i + lane) : 0.f;
+    return __shfl_sync(0xffffffffu, v, i & 31);
+  }
+};
 __device__ __forceinline__ float bias_at(const GemmArgs& a, int n) {
   return a.bias ? __ldg(a.bias + n) : 0.f;
 }
@@ -335,29 +354,34 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
-  float2 acc[32];
+  float2 acc[32];  // warps 2-9
 
   if (warp == 0) {
     const int ahead = min(nk, GSTAGES);
+    const uint32_t sx_bytes = 4u * min(128, a.ld - m0);  // ld: the rows, up to a multiple of 32
+    auto load_x = [&](int i) {
+      const int s = i % GSTAGES;
+      bulk_g2s(sh.sx[i % GSX_SLOTS], a.sxt + (size_t)(kb0 + i) * a.ld + m0, sx_bytes, &sh.full[s]);
+      tc::tma_load_2d(smem + s * G_STAGE, &xmap, (kb0 + i) * kScaleBlock, m0, &sh.full[s]);
+    };
     if (tc::elect_one())
       for (int i = 0; i < ahead; ++i) {
-        mbar_arrive_expect_tx(&sh.full[i], G_STAGE);
+        mbar_arrive_expect_tx(&sh.full[i], G_STAGE + sx_bytes);
         tc::tma_load_2d(smem + i * G_STAGE + G_TILE, &wmap, (kb0 + i) * kScaleBlock, n0, &sh.full[i]);
       }
     __syncwarp();
-    griddep_wait();  // the codes of x
+    griddep_wait();  // the codes and scales of x
     if (tc::elect_one())
-      for (int i = 0; i < ahead; ++i)
-        tc::tma_load_2d(smem + i * G_STAGE, &xmap, (kb0 + i) * kScaleBlock, m0, &sh.full[i]);
+      for (int i = 0; i < ahead; ++i) load_x(i);
     __syncwarp();
     int i = ahead;
     for (; i < nk; ++i) {
       const int s = i % GSTAGES;
       if (!gwait(sh, &sh.empty[s], (uint32_t)((i / GSTAGES - 1) & 1), a.status)) break;
       if (tc::elect_one()) {
-        mbar_arrive_expect_tx(&sh.full[s], G_STAGE);
+        mbar_arrive_expect_tx(&sh.full[s], G_STAGE + sx_bytes);
         tc::tma_load_2d(smem + s * G_STAGE + G_TILE, &wmap, (kb0 + i) * kScaleBlock, n0, &sh.full[s]);
-        tc::tma_load_2d(smem + s * G_STAGE, &xmap, (kb0 + i) * kScaleBlock, m0, &sh.full[s]);
+        load_x(i);
       }
       __syncwarp();
     }
@@ -391,30 +415,16 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
     __syncwarp();
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
-    const int m = m0 + 32 * q + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16) + 64 * half;
-    const float* sw = a.sw + (size_t)(n0 / kScaleBlock) * a.nkb + kb0;
-    const float* sx = a.sxt + (size_t)kb0 * a.ld + (m < a.M ? m : 0);
+    BlockScales sw(a.sw + (size_t)(n0 / kScaleBlock) * a.nkb + kb0, nk, lane);
 #pragma unroll
     for (int j = 0; j < 32; ++j) acc[j] = make_float2(0.f, 0.f);
-    griddep_wait();  // the scales of x
-    // scales two blocks ahead: a block's MMAs are shorter than a load
-    float x0 = __ldcg(sx), w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
-    if (nk > 1) {
-      x1 = __ldcg(sx + a.ld);
-      w1 = __ldg(sw + 1);
-    }
     for (int i = 0; i < nk; ++i) {
       const int b = i & 1;
-      const float f0 = x0 * w0;
-      x0 = x1;
-      w0 = w1;
-      if (i + 2 < nk) {
-        x1 = __ldcg(sx + (size_t)(i + 2) * a.ld);
-        w1 = __ldg(sw + i + 2);
-      }
+      const float w = sw.at(i);
       if (!gwait(sh, &sh.p_full[b], (uint32_t)((i / 2) & 1), a.status)) break;
       tc::fence_after_sync();
+      const float f0 = w * sh.sx[i % GSX_SLOTS][32 * q + lane];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         uint32_t p[16];
@@ -504,13 +514,16 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
 //    being computed while the last one is written.
 namespace {
 constexpr int PT = 256;                  // rows and features of a pair's tile
-constexpr int PSTAGES = 5;
+constexpr int PSTAGES = 4;
 constexpr int kPairProWarps = 16;
 constexpr int kPairThreads = (2 + kPairProWarps) * 32;
 constexpr int P_SMEM = PSTAGES * G_STAGE + kPairProWarps * 4096 + 1024;
-static_assert(P_SMEM + 1024 <= 227 * 1024, "shared memory");
+static_assert(P_SMEM + 5 * 1024 <= 227 * 1024, "shared memory");
+
+constexpr int PSX_SLOTS = PSTAGES + 2;
 
 struct PairShared {
+  alignas(128) float sx[PSX_SLOTS][128];
   uint64_t full[PSTAGES], empty[PSTAGES], p_full[2], p_empty[2];
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -557,7 +570,8 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
                    const __grid_constant__ CUtensorMap wmap,
-                   const __grid_constant__ CUtensorMap omap, const GemmArgs a) {
+                   const __grid_constant__ CUtensorMap omap,
+                   const __grid_constant__ CUtensorMap smap, const GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ PairShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -602,14 +616,17 @@ k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
         }
         if (tc::elect_one()) {
           const uint32_t bar = in_cta(&sh.full[s], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * G_STAGE);
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * (G_STAGE + G_SX));
           tma_load_pair(smem + s * G_STAGE + G_TILE, &wmap, kb * kScaleBlock, n0, bar);
         }
         __syncwarp();
-        if (!waited) griddep_wait();  // the codes of x
+        if (!waited) griddep_wait();  // the codes and scales of x
         waited = true;
-        if (tc::elect_one())
-          tma_load_pair(smem + s * G_STAGE, &xmap, kb * kScaleBlock, m0, in_cta(&sh.full[s], 0));
+        if (tc::elect_one()) {
+          const uint32_t bar = in_cta(&sh.full[s], 0);
+          tma_load_pair(smem + s * G_STAGE, &xmap, kb * kScaleBlock, m0, bar);
+          tma_load_pair(sh.sx[it % PSX_SLOTS], &smap, m0, kb, bar);
+        }
         __syncwarp();
       }
     }
@@ -654,38 +671,25 @@ k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
     const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16) + 64 * part;
     uint8_t* const tile = smem + PSTAGES * G_STAGE + (warp - 2) * 4096;
     const uint32_t p_empty[2] = {in_cta(&sh.p_empty[0], 0), in_cta(&sh.p_empty[1], 0)};
-    griddep_wait();  // the scales of x
     int it = 0;
     bool ok = true;
     for (int t = pair; t < tiles && ok; t += npairs) {
-      const int n0 = (t % tn) * PT + 64 * part, m = (t / tn) * PT + 128 * rank + 32 * q + lane;
+      const int n0 = (t % tn) * PT + 64 * part, m = (t / tn) * PT + 128 * rank + 32 * q;
       // (a tile's last features may lie past the matrix: any scale will do for
       // their zeros)
-      const float* sw = a.sw + (size_t)(n0 < a.N ? n0 / kScaleBlock : 0) * nk;
-      const float* sx = a.sxt + (m < a.M ? m : 0);
+      BlockScales sw(a.sw + (size_t)(n0 < a.N ? n0 / kScaleBlock : 0) * nk, nk, lane);
       float2 acc[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) acc[j] = make_float2(0.f, 0.f);
-      // scales two blocks ahead: a block's MMAs are shorter than a load
-      float x0 = __ldcg(sx), w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
-      if (nk > 1) {
-        x1 = __ldcg(sx + a.ld);
-        w1 = __ldg(sw + 1);
-      }
       for (int kb = 0; kb < nk; ++kb, ++it) {
         const int b = it & 1;
-        const float f0 = x0 * w0;
-        x0 = x1;
-        w0 = w1;
-        if (kb + 2 < nk) {
-          x1 = __ldcg(sx + (size_t)(kb + 2) * a.ld);
-          w1 = __ldg(sw + kb + 2);
-        }
+        const float w = sw.at(kb);
         if (!gwait(sh, &sh.p_full[b], (uint32_t)((it / 2) & 1), a.status)) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
+        const float f0 = w * sh.sx[it % PSX_SLOTS][32 * q + lane];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           uint32_t p[16];
@@ -800,11 +804,15 @@ int max_pairs() {
 
 cudaError_t launch_gemm_pair(const CUtensorMap& xmap, const CUtensorMap& wmap,
                              const CUtensorMap& omap, const GemmArgs& a, cudaStream_t s) {
-  cudaError_t err = ensure_smem((const void*)k_linear_gemm_pair, P_SMEM);
+  CUtensorMap smap;  // the activation scales [nkb][ld]: 128 of a block
+  cudaError_t err = make_tensor_map_2d(&smap, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.sxt, a.nkb, a.ld,
+                                       128, 1, 0);
+  if (err != cudaSuccess) return err;
+  err = ensure_smem((const void*)k_linear_gemm_pair, P_SMEM);
   if (err != cudaSuccess) return err;
   const int pairs = std::min(max_pairs(), cdiv(a.M, PT) * cdiv(a.N, PT));
   return launch_k(k_linear_gemm_pair, dim3(2 * pairs), dim3(kPairThreads), (size_t)P_SMEM, s, true,
-                  xmap, wmap, omap, a);
+                  xmap, wmap, omap, smap, a);
 }
 
 }  // namespace
