@@ -277,22 +277,23 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t local, uint32_t rank) {
 // A warp's 32 rows x 64 features (a row per lane) as bf16 into a 4 KB tile of
 // shared memory, 128-byte swizzled as the TMA store reads it: a thread's own
 // stores would touch 32 rows at a time, half a sector of each.
-__device__ __forceinline__ void stage_rows(uint8_t* tile, const float2 (&acc)[32], const float* bias,
+__device__ __forceinline__ void stage_rows(uint8_t* tile, float2 (&acc)[32], const float* bias,
                                            int n0, int N, int lane) {
+  if (bias) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int n = min(n0 + 2 * j, N - 2);  // (features past the matrix are not stored)
+      acc[j].x += __ldg(bias + n);
+      acc[j].y += __ldg(bias + n + 1);
+    }
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    uint32_t r[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float2 v = acc[4 * j + u];
-      const int n = n0 + 8 * j + 2 * u;
-      if (bias && n < N) {
-        v.x += __ldg(bias + n);
-        v.y += __ldg(bias + n + 1);
-      }
-      r[u] = pack_bf16x2(v.x, v.y);
-    }
-    *reinterpret_cast<uint4*>(tile + tc::sw128_off(lane, j)) = make_uint4(r[0], r[1], r[2], r[3]);
+    const uint4 v = make_uint4(pack_bf16x2(acc[4 * j].x, acc[4 * j].y),
+                               pack_bf16x2(acc[4 * j + 1].x, acc[4 * j + 1].y),
+                               pack_bf16x2(acc[4 * j + 2].x, acc[4 * j + 2].y),
+                               pack_bf16x2(acc[4 * j + 3].x, acc[4 * j + 3].y));
+    *reinterpret_cast<uint4*>(tile + tc::sw128_off(lane, j)) = v;
   }
 }
 // A tile row of weight scales, block kb of kb0 .. kb1 in lane (kb - kb0) % 32:
@@ -301,8 +302,12 @@ struct BlockScales {
   const float* p;
   int n, lane;
   float v;
-  __device__ __forceinline__ BlockScales(const float* p_, int n_, int lane_)
-      : p(p_), n(n_), lane(lane_), v(lane_ < n_ ? __ldg(p_ + lane_) : 0.f) {}
+  __device__ __forceinline__ void start(const float* p_, int n_, int lane_) {
+    p = p_;
+    n = n_;
+    lane = lane_;
+    v = lane < n ? __ldg(p + lane) : 0.f;
+  }
   __device__ __forceinline__ float at(int i) {
     if (i > 0 && (i & 31) == 0) v = i + lane < n ? __ldg(p + i + lane) : 0.f;
     return __shfl_sync(0xffffffffu, v, i & 31);
@@ -416,7 +421,8 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16) + 64 * half;
-    BlockScales sw(a.sw + (size_t)(n0 / kScaleBlock) * a.nkb + kb0, nk, lane);
+    BlockScales sw;
+    sw.start(a.sw + (size_t)(n0 / kScaleBlock) * a.nkb + kb0, nk, lane);
 #pragma unroll
     for (int j = 0; j < 32; ++j) acc[j] = make_float2(0.f, 0.f);
     for (int i = 0; i < nk; ++i) {
@@ -673,11 +679,14 @@ k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
     const uint32_t p_empty[2] = {in_cta(&sh.p_empty[0], 0), in_cta(&sh.p_empty[1], 0)};
     int it = 0;
     bool ok = true;
+    BlockScales sw;
+    auto scales_of = [&](int t) {  // (past the matrix any scale will do: its features are not stored)
+      const int n = min((t % tn) * PT + 64 * part, a.N - 1);
+      sw.start(a.sw + (size_t)(n / kScaleBlock) * nk, nk, lane);
+    };
+    scales_of(pair);
     for (int t = pair; t < tiles && ok; t += npairs) {
       const int n0 = (t % tn) * PT + 64 * part, m = (t / tn) * PT + 128 * rank + 32 * q;
-      // (a tile's last features may lie past the matrix: any scale will do for
-      // their zeros)
-      BlockScales sw(a.sw + (size_t)(n0 < a.N ? n0 / kScaleBlock : 0) * nk, nk, lane);
       float2 acc[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) acc[j] = make_float2(0.f, 0.f);
@@ -704,6 +713,7 @@ k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
           for (int j = 0; j < 8; ++j) fma2(acc[8 * h + j], p[2 * j], p[2 * j + 1], f0);
         }
       }
+      if (t + npairs < tiles) scales_of(t + npairs);
       if (ok) {
         if (lane == 0) tc::bulk_wait_read_all();  // the previous tile has left the buffer
         __syncwarp();
