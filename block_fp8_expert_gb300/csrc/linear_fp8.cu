@@ -9,8 +9,6 @@
 namespace moe {
 
 namespace {
-constexpr int kLinWarps = 8;
-
 struct LinArgs {
   const uint16_t* x;
   long long x_stride;
@@ -32,7 +30,7 @@ struct LinArgs {
 // group: its maximum is two shuffles.  Codes become fp16 (exactly) and feed
 // mma.sync with fp32 accumulation; the block's two scales are applied to its
 // sums, and the warps' sums are added in a fixed order.
-template <int NT>
+template <int NT, int kLinWarps>
 __global__ void __launch_bounds__(kLinWarps * 32)
 k_linear_stream(const LinArgs a) {
   constexpr unsigned kAll = 0xffffffffu;
@@ -741,10 +739,25 @@ k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
 
 namespace {
 
-// Rows up to which the streamed kernel is the faster one.
-constexpr int kStreamRows = 16;
+// The streamed kernel up to 16 rows (N 5120, K 2048: 5.0 - 8.1 us against
+// 8.0 - 8.7 on tcgen05), and with more where its CTAs of 16 features x 32 rows
+// all run at once over a short K (M 64, N 640, K 512: 3.2 against 5.4 us; but
+// M 24, N 2048, K 4096: 9.4 against 9.0, M 24, N 5120, K 2048: 14.6 against 8.5).
+bool linear_streams(const moe_linear_dims& d) {
+  return d.M <= 16 || (d.K <= 2048 && cdiv(d.N, 16) * (long long)cdiv(d.M, 32) <= num_sms());
+}
 
-bool linear_streams(const moe_linear_dims& d) { return d.M <= kStreamRows; }
+template <int NT>
+cudaError_t launch_stream(const LinArgs& a, cudaStream_t s) {
+  const dim3 grid(cdiv(a.N, 16), cdiv(a.M, 8 * NT));
+  // a warp per block of K up to 16, as long as every CTA runs at once
+  const int nkb = cdiv(a.K, kScaleBlock), ctas = grid.x * grid.y;
+  if (ctas * 16 <= num_sms() * 16 && nkb > 8)
+    return launch_k(k_linear_stream<NT, 16>, grid, dim3(512), 0, s, false, a);
+  if (ctas * 8 <= num_sms() * 16 && nkb > 4)
+    return launch_k(k_linear_stream<NT, 8>, grid, dim3(256), 0, s, false, a);
+  return launch_k(k_linear_stream<NT, 4>, grid, dim3(128), 0, s, false, a);
+}
 
 struct LinWs {
   size_t codes, sxt, total;
@@ -834,9 +847,9 @@ cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const flo
                               cudaStream_t s) {
   if (linear_streams(d)) {
     const LinArgs a{x, d.x_stride, w.codes, w.scales, bias, out, d.out_stride, d.M, d.N, d.K, status};
-    const dim3 blk(kLinWarps * 32), grid(cdiv(d.N, 16), 1);
-    if (d.M <= 8) return launch_k(k_linear_stream<1>, grid, blk, 0, s, false, a);
-    return launch_k(k_linear_stream<2>, grid, blk, 0, s, false, a);
+    if (d.M <= 8) return launch_stream<1>(a, s);
+    if (d.M <= 16) return launch_stream<2>(a, s);
+    return launch_stream<4>(a, s);
   }
   const LinWs l = lin_ws(d);
   uint8_t* codes = static_cast<uint8_t*>(ws) + l.codes;
@@ -858,12 +871,15 @@ cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const flo
   const GemmArgs a{sxt, l.ld, w.scales, bias, out, d.out_stride, d.M, d.N, nkb, status};
   const int tiles = cdiv(d.M, GM) * cdiv(d.N, GN);
   if (cdiv(d.M, PT) * cdiv(d.N, PT) >= num_sms() / 2) return launch_gemm_pair(xmap, wmap, omap, a, s);
+  // K divided while that leaves one CTA per SM and four blocks per CTA: clusters
+  // of four, two CTAs per SM take longer to place than they save (M 203, N 2048,
+  // K 4096: 15.8 / 12.7 / 11.7 / 19.3 us with 1 / 2 / 4 / 8 CTAs per tile; M 1000,
+  // N 2048, K 2048, 128 tiles: 11.4 / 13.8 us with 1 / 2)
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * num_sms() && nkb >= 4 * split) split *= 2;
+  while (split < 4 && tiles * split * 2 <= num_sms() && nkb >= 8 * split) split *= 2;
   if (split == 1) return launch_gemm<1>(xmap, wmap, omap, a, s);
   if (split == 2) return launch_gemm<2>(xmap, wmap, omap, a, s);
-  if (split == 4) return launch_gemm<4>(xmap, wmap, omap, a, s);
-  return launch_gemm<8>(xmap, wmap, omap, a, s);
+  return launch_gemm<4>(xmap, wmap, omap, a, s);
 }
 
 }  // namespace moe
