@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(kLinWarps * 32)
 k_linear_stream(const LinArgs a) {
   constexpr unsigned kAll = 0xffffffffu;
   __shared__ float red[kLinWarps][NT][4][32];
+  griddep_wait();
+  griddep_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int n0 = blockIdx.x * 16, m0 = blockIdx.y * (8 * NT);
@@ -153,7 +155,8 @@ __global__ void __launch_bounds__(256)
 k_linear_quant(const uint16_t* __restrict__ x, long long x_stride, int M, int K,
                uint8_t* __restrict__ codes, float* __restrict__ sxt, int ld,
                int32_t* __restrict__ status) {
-  griddep_trigger();
+  griddep_wait();
+  griddep_trigger();  // (after the wait: the GEMM reads weights before its own)
   const int nkb = cdiv(K, kScaleBlock);
   const long long unit = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
   const int part = threadIdx.x & 15;
@@ -753,10 +756,10 @@ cudaError_t launch_stream(const LinArgs& a, cudaStream_t s) {
   // a warp per block of K up to 16, as long as every CTA runs at once
   const int nkb = cdiv(a.K, kScaleBlock), ctas = grid.x * grid.y;
   if (ctas * 16 <= num_sms() * 16 && nkb > 8)
-    return launch_k(k_linear_stream<NT, 16>, grid, dim3(512), 0, s, false, a);
+    return launch_k(k_linear_stream<NT, 16>, grid, dim3(512), 0, s, true, a);
   if (ctas * 8 <= num_sms() * 16 && nkb > 4)
-    return launch_k(k_linear_stream<NT, 8>, grid, dim3(256), 0, s, false, a);
-  return launch_k(k_linear_stream<NT, 4>, grid, dim3(128), 0, s, false, a);
+    return launch_k(k_linear_stream<NT, 8>, grid, dim3(256), 0, s, true, a);
+  return launch_k(k_linear_stream<NT, 4>, grid, dim3(128), 0, s, true, a);
 }
 
 struct LinWs {
@@ -865,7 +868,7 @@ cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const flo
                                 128, d.out_stride)) != cudaSuccess)
     return err;
   const long long groups = (long long)d.M * nkb;
-  err = launch_k(k_linear_quant, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, s, false, x,
+  err = launch_k(k_linear_quant, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, s, true, x,
                  (long long)d.x_stride, d.M, d.K, codes, sxt, l.ld, status);
   if (err != cudaSuccess) return err;
   const GemmArgs a{sxt, l.ld, w.scales, bias, out, d.out_stride, d.M, d.N, nkb, status};

@@ -245,6 +245,7 @@ k_paged_attention(const AttnArgs a) {
   __shared__ Place s_place;
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ unsigned s_seen[kWarps][S::kStages];  // tokens of each stage that exist
+  griddep_wait();
   griddep_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -809,7 +810,7 @@ cudaError_t launch_attn_nh(AttnArgs& a, cudaStream_t s) {
   // no more CTAs than the table could give parts
   const long long most = attn_units(a.d, a.c, S::kRows, S::kTile) / kMinUnits + (long long)a.d.B * a.HG;
   a.grid = (int)std::max(1ll, std::min((long long)S::kCtasPerSm * num_sms(), most));
-  err = launch_k(k_paged_attention<D, E4M3, NH>, dim3(a.grid), dim3(kWarps * 32), S::kSmem, s, false, a);
+  err = launch_k(k_paged_attention<D, E4M3, NH>, dim3(a.grid), dim3(kWarps * 32), S::kSmem, s, true, a);
   if (err != cudaSuccess) return err;
   return launch_k(k_attn_join<D>, dim3(a.grid, cdiv(std::min(a.G, S::kRows), kJoinHeads)),
                   dim3(kJoinThreads), 0, s, true, a);

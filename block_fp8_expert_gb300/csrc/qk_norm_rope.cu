@@ -54,6 +54,8 @@ k_qk_norm_rope(const QkArgs a) {
   constexpr int HPW = 32 / LPH;      // heads per warp and step
   constexpr int kAhead = 4;
   constexpr unsigned kAll = 0xffffffffu;
+  griddep_wait();
+  griddep_trigger();
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int t = (int)(unit / a.chunks), ch = (int)(unit % a.chunks);
@@ -62,6 +64,18 @@ k_qk_norm_rope(const QkArgs a) {
   const int Hq = a.d.Hq, Hkv = a.c.Hkv, heads = Hq + 2 * Hkv;
   const int steps = cdiv(heads, HPW);
   const int rot = a.d.rot, half = rot / 2;
+
+  // the first heads are on their way while the token's place is found
+  const uint16_t* row = a.qkv + (size_t)t * a.d.qkv_stride;
+  uint4 raw[kAhead];
+  auto load_heads = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = (s0 + u * a.chunks) * HPW + sub;
+      raw[u] = h < heads ? ldg_stream16(row + (size_t)h * D + d0) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load_heads(ch);
 
   // the token's place: its position's rotation row and its cache slot
   const long long slot = a.slots[t];
@@ -106,14 +120,8 @@ k_qk_norm_rope(const QkArgs a) {
   if (a.q_norm) load_f32x8(a.q_norm + d0, qn);
   if (a.k_norm) load_f32x8(a.k_norm + d0, kn);
 
-  const uint16_t* row = a.qkv + (size_t)t * a.d.qkv_stride;
   for (int s0 = ch; s0 < steps; s0 += kAhead * a.chunks) {
-    uint4 raw[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = (s0 + u * a.chunks) * HPW + sub;
-      raw[u] = h < heads ? ldg_stream16(row + (size_t)h * D + d0) : make_uint4(0, 0, 0, 0);
-    }
+    if (s0 != ch) load_heads(s0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int st = s0 + u * a.chunks;
@@ -204,9 +212,9 @@ cudaError_t launch_qk_norm_rope(const uint16_t* qkv, const float* q_norm, const 
   a.chunks = (int)std::min<long long>(steps, std::max<long long>(cdiv(steps, 8), want / d.T));
   const long long warps = (long long)d.T * a.chunks;
   const dim3 grid((unsigned)((warps + 3) / 4)), blk(128);
-  if (cache.D == 64) return launch_k(k_qk_norm_rope<64>, grid, blk, 0, s, false, a);
-  if (cache.D == 128) return launch_k(k_qk_norm_rope<128>, grid, blk, 0, s, false, a);
-  return launch_k(k_qk_norm_rope<256>, grid, blk, 0, s, false, a);
+  if (cache.D == 64) return launch_k(k_qk_norm_rope<64>, grid, blk, 0, s, true, a);
+  if (cache.D == 128) return launch_k(k_qk_norm_rope<128>, grid, blk, 0, s, true, a);
+  return launch_k(k_qk_norm_rope<256>, grid, blk, 0, s, true, a);
 }
 
 }  // namespace moe
