@@ -22,7 +22,7 @@ struct QkArgs {
   int chunks;  // warps that share a token's heads
 };
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ void unpack_bf16x8(const uint4& v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -30,7 +30,15 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&f)[8]) {
     f[2 * i + 1] = bf16_hi(w[i]);
   }
 }
-__device__ __forceinline__ void load_f32x8(const float* p, float (&f)[8]) {
+__device__ __forceinline__ uint4 pack_bf16x8(const float* f) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ uint2 pack_e4m3x8(const float* f, float m) {
+  return make_uint2(f32x2_to_e4m3x2(f[0] * m, f[1] * m) | (f32x2_to_e4m3x2(f[2] * m, f[3] * m) << 16),
+                    f32x2_to_e4m3x2(f[4] * m, f[5] * m) | (f32x2_to_e4m3x2(f[6] * m, f[7] * m) << 16));
+}
+__device__ __forceinline__ void load_f32x8(const float* p, float* f) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
   const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -39,20 +47,21 @@ __device__ __forceinline__ void load_f32x8(const float* p, float (&f)[8]) {
 
 }  // namespace
 
-// A lane owns 8 consecutive dimensions of one head (one 16-byte load and, for
-// bf16, one 16-byte store), so LPH = D / 8 lanes make a head and a warp works
-// on 32 / LPH heads at once.  A token's heads are dealt to `chunks` warps; a
-// warp loads its lanes' cos, sin and norm values once and keeps kAhead head
-// loads in flight.  The mean of squares and the E4M3 maximum are butterflies
-// over the head's lanes.  Rotation: interleaved pairs sit inside a lane; in
-// the half layout the partner of dimension i is rot / 2 away, which is rot /
-// 16 lanes (rot a multiple of 16), one shuffle per value.
+// A lane owns 16 dimensions of one head in two runs of 8 (two 16-byte loads,
+// and two stores), so D / 16 lanes make a head and a warp takes 512 / D heads
+// per step.  In the half layout the runs of a rotated lane p are 8 p .. and
+// rot / 2 + 8 p .., which holds both partners of each pair; otherwise they are
+// neighbours, which holds the interleaved pairs: a rotation needs no shuffle.
+// The mean of squares and the E4M3 maximum are butterflies over the head's
+// lanes.  A token's steps, those of the query heads before the key heads'
+// before the value heads', are dealt to `chunks` warps; a warp keeps two
+// steps' loads in flight, the first ones on their way before the token's
+// position and slot are known.
 template <int D>
 __global__ void __launch_bounds__(128)
 k_qk_norm_rope(const QkArgs a) {
-  constexpr int LPH = D / 8;         // lanes per head
-  constexpr int HPW = 32 / LPH;      // heads per warp and step
-  constexpr int kAhead = 4;
+  constexpr int LPH = D / 16;    // lanes per head
+  constexpr int HPW = 32 / LPH;  // heads per warp and step
   constexpr unsigned kAll = 0xffffffffu;
   griddep_wait();
   griddep_trigger();
@@ -60,22 +69,30 @@ k_qk_norm_rope(const QkArgs a) {
   const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int t = (int)(unit / a.chunks), ch = (int)(unit % a.chunks);
   if (t >= a.d.T) return;  // warp-uniform
-  const int sub = lane / LPH, part = lane % LPH, d0 = 8 * part;
-  const int Hq = a.d.Hq, Hkv = a.c.Hkv, heads = Hq + 2 * Hkv;
-  const int steps = cdiv(heads, HPW);
-  const int rot = a.d.rot, half = rot / 2;
-
-  // the first heads are on their way while the token's place is found
+  const int sub = lane / LPH, p = lane % LPH;
+  const int Hq = a.d.Hq, Hkv = a.c.Hkv, rot = a.d.rot, half = rot / 2;
+  const bool rotated = 16 * p < rot;
+  const bool split = rotated && !a.d.interleaved;
+  const int oa = split ? 8 * p : 16 * p, ob = split ? half + 8 * p : 16 * p + 8;
+  const int sq = cdiv(Hq, HPW), sk = cdiv(Hkv, HPW), steps = sq + 2 * sk;
   const uint16_t* row = a.qkv + (size_t)t * a.d.qkv_stride;
-  uint4 raw[kAhead];
-  auto load_heads = [&](int s0) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = (s0 + u * a.chunks) * HPW + sub;
-      raw[u] = h < heads ? ldg_stream16(row + (size_t)h * D + d0) : make_uint4(0, 0, 0, 0);
-    }
+
+  // this lane's head of step s, counted within its kind, and its loads
+  auto head_of = [&](int s) { return (s < sq ? s : s < sq + sk ? s - sq : s - sq - sk) * HPW + sub; };
+  struct Raw {
+    uint4 a, b;
   };
-  load_heads(ch);
+  auto load = [&](int s) {
+    Raw r{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (s >= steps) return r;
+    const int h = head_of(s);
+    if (h >= (s < sq ? Hq : Hkv)) return r;
+    const uint16_t* x = row + (size_t)(h + (s < sq ? 0 : s < sq + sk ? Hq : Hq + Hkv)) * D;
+    r.a = ldg_stream16(x + oa);
+    r.b = ldg_stream16(x + ob);
+    return r;
+  };
+  Raw next0 = load(ch), next1 = load(ch + a.chunks);
 
   // the token's place: its position's rotation row and its cache slot
   const long long slot = a.slots[t];
@@ -86,23 +103,13 @@ k_qk_norm_rope(const QkArgs a) {
     cs[i] = 1.f;
     sn[i] = 0.f;
   }
-  const bool rotated = d0 < rot;
-  const int partner = rotated ? (d0 < half ? part + rot / 16 : part - rot / 16) : part;
   if (rot > 0) {
-    const int p = a.pos[t];
-    pos_ok = p >= 0 && p < a.d.n_pos;
+    const int pos = a.pos[t];
+    pos_ok = pos >= 0 && pos < a.d.n_pos;
     if (pos_ok && rotated) {
-      const float* row = a.cos_sin + (size_t)p * rot;
-      if (a.d.interleaved) {
-        const float4 c4 = __ldg(reinterpret_cast<const float4*>(row + d0 / 2));
-        const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + half + d0 / 2));
-        cs[0] = c4.x; cs[1] = c4.y; cs[2] = c4.z; cs[3] = c4.w;
-        sn[0] = s4.x; sn[1] = s4.y; sn[2] = s4.z; sn[3] = s4.w;
-      } else {
-        const int i0 = d0 < half ? d0 : d0 - half;
-        load_f32x8(row + i0, cs);
-        load_f32x8(row + half + i0, sn);
-      }
+      const float* tab = a.cos_sin + (size_t)pos * rot + 8 * p;
+      load_f32x8(tab, cs);
+      load_f32x8(tab + half, sn);
     }
   }
   const long long cap = (long long)a.c.pages * a.c.page_size;
@@ -112,88 +119,108 @@ k_qk_norm_rope(const QkArgs a) {
     if (!pos_ok) raise_status(a.status, MOE_DEV_BAD_POSITION);
     if (!slot_ok) raise_status(a.status, MOE_DEV_BAD_PAGE);
   }
-  const long long page = store ? slot / a.c.page_size : 0;
-  const long long off = store ? slot % a.c.page_size : 0;
-  float qn[8], kn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) qn[i] = kn[i] = 1.f;
-  if (a.q_norm) load_f32x8(a.q_norm + d0, qn);
-  if (a.k_norm) load_f32x8(a.k_norm + d0, kn);
+  long long at = 0, sat = 0;  // the slot's elements of head 0
+  if (store) {
+    long long page, off;
+    if (cap < (1ll << 31)) {
+      const unsigned pg = (unsigned)slot / (unsigned)a.c.page_size;
+      page = pg;
+      off = (unsigned)slot - pg * (unsigned)a.c.page_size;
+    } else {
+      page = slot / a.c.page_size;
+      off = slot % a.c.page_size;
+    }
+    at = page * a.c.page_stride + off * a.c.token_stride;
+    sat = page * a.c.scale_page_stride + off * a.c.scale_token_stride;
+  }
 
-  for (int s0 = ch; s0 < steps; s0 += kAhead * a.chunks) {
-    if (s0 != ch) load_heads(s0);
+  // x = norm and rotation of this lane's run of a head
+  auto norm_rope = [&](const Raw& r, const float* weight, float (&x)[16]) {
+    unpack_bf16x8(r.a, x);
+    unpack_bf16x8(r.b, x + 8);
+    if (weight) {
+      float ss = 0.f, w[16];
+      load_f32x8(weight + oa, w);
+      load_f32x8(weight + ob, w + 8);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int st = s0 + u * a.chunks;
-      if (st >= steps) break;  // warp-uniform
-      const int h = st * HPW + sub;
-      const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
-      float x[8];
-      unpack_bf16x8(raw[u], x);
-      if (st * HPW < Hq + Hkv) {  // warp-uniform: some head here is a query or a key
-        float ss = 0.f;
+      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+      for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(kAll, ss, o);
+      const float f = rsqrtf(ss * (1.f / D) + a.d.eps);  // (2 ulp)
 #pragma unroll
-        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(kAll, ss, o);
-        const bool normed = is_q ? a.q_norm != nullptr : (!is_v && a.k_norm != nullptr);
-        if (normed) {
-          const float r = 1.f / sqrtf(ss * (1.f / D) + a.d.eps);
+      for (int i = 0; i < 16; ++i) x[i] *= f * w[i];
+    }
+    if (rotated) {
+      if (a.d.interleaved) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (is_q ? qn[i] : kn[i]);
+        for (int i = 0; i < 8; ++i) {
+          const float u = x[2 * i], v = x[2 * i + 1];
+          x[2 * i] = u * cs[i] - v * sn[i];
+          x[2 * i + 1] = v * cs[i] + u * sn[i];
         }
-        if (a.d.interleaved) {
-          if (rotated && !is_v) {
+      } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float p = x[2 * i], q = x[2 * i + 1];
-              x[2 * i] = p * cs[i] - q * sn[i];
-              x[2 * i + 1] = q * cs[i] + p * sn[i];
-            }
-          }
-        } else if (rot > 0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(kAll, x[i], sub * LPH + partner);
-            if (rotated && !is_v) x[i] = d0 < half ? x[i] * cs[i] - o * sn[i] : x[i] * cs[i] + o * sn[i];
-          }
+        for (int i = 0; i < 8; ++i) {
+          const float u = x[i], v = x[8 + i];
+          x[i] = u * cs[i] - v * sn[i];
+          x[8 + i] = v * cs[i] + u * sn[i];
         }
       }
-      if (is_q) {
+    }
+  };
+  // codes and scale of a head's run into the cache
+  auto store_e4m3 = [&](const float (&x)[16], int h, void* codes, float* scales) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 1; o < LPH; o <<= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
+    float f, scale;
+    quant_factors(m, f, scale);
+    if (h < Hkv) {
+      uint8_t* c = static_cast<uint8_t*>(codes) + at + h * a.c.head_stride;
+      *reinterpret_cast<uint2*>(c + oa) = pack_e4m3x8(x, f);
+      *reinterpret_cast<uint2*>(c + ob) = pack_e4m3x8(x + 8, f);
+      if (p == 0) scales[sat + h * a.c.scale_head_stride] = scale;
+    }
+  };
+  const bool e4m3 = a.c.format == MOE_KV_E4M3;
+#pragma unroll 1
+  for (int s = ch; s < steps; s += a.chunks) {
+    const Raw r = next0;
+    next0 = next1;
+    next1 = load(s + 2 * a.chunks);
+    const int h = head_of(s);
+    float x[16];
+    if (s < sq) {
+      norm_rope(r, a.q_norm, x);
+      if (h < Hq) {
         if (!pos_ok) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = NAN;
+          for (int i = 0; i < 16; ++i) x[i] = NAN;
         }
-        *reinterpret_cast<uint4*>(a.q_out + (size_t)t * a.d.q_stride + (size_t)h * D + d0) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                       pack_bf16x2(x[6], x[7]));
+        uint16_t* q = a.q_out + (size_t)t * a.d.q_stride + (size_t)h * D;
+        *reinterpret_cast<uint4*>(q + oa) = pack_bf16x8(x);
+        *reinterpret_cast<uint4*>(q + ob) = pack_bf16x8(x + 8);
       }
-      if (st * HPW + HPW <= Hq || !store) continue;  // warp-uniform: no key or value to store
-      const int kvh = h - Hq - (is_v ? Hkv : 0);
-      const long long at = page * a.c.page_stride + kvh * a.c.head_stride + off * a.c.token_stride + d0;
-      if (a.c.format == MOE_KV_E4M3) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = 1; o < LPH; o <<= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
-        float f, scale;
-        quant_factors(m, f, scale);
-        if (!is_q && h < heads) {
-          uint2 codes;
-          codes.x = f32x2_to_e4m3x2(x[0] * f, x[1] * f) | (f32x2_to_e4m3x2(x[2] * f, x[3] * f) << 16);
-          codes.y = f32x2_to_e4m3x2(x[4] * f, x[5] * f) | (f32x2_to_e4m3x2(x[6] * f, x[7] * f) << 16);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + at) = codes;
-          if (part == 0) {
-            float* sc = is_v ? a.c.v_scale : a.c.k_scale;
-            sc[page * a.c.scale_page_stride + kvh * a.c.scale_head_stride +
-               off * a.c.scale_token_stride] = scale;
-          }
+    } else if (store) {
+      if (s < sq + sk) {
+        norm_rope(r, a.k_norm, x);
+        if (e4m3) {
+          store_e4m3(x, h, a.c.k, a.c.k_scale);
+        } else if (h < Hkv) {
+          uint16_t* c = static_cast<uint16_t*>(a.c.k) + at + h * a.c.head_stride;
+          *reinterpret_cast<uint4*>(c + oa) = pack_bf16x8(x);
+          *reinterpret_cast<uint4*>(c + ob) = pack_bf16x8(x + 8);
         }
-      } else if (!is_q && h < heads) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + at) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                       pack_bf16x2(x[6], x[7]));
+      } else if (e4m3) {
+        unpack_bf16x8(r.a, x);
+        unpack_bf16x8(r.b, x + 8);
+        store_e4m3(x, h, a.c.v, a.c.v_scale);
+      } else if (h < Hkv) {  // values are copied as they are
+        uint16_t* c = static_cast<uint16_t*>(a.c.v) + at + h * a.c.head_stride;
+        *reinterpret_cast<uint4*>(c + oa) = r.a;
+        *reinterpret_cast<uint4*>(c + ob) = r.b;
       }
     }
   }
@@ -204,12 +231,11 @@ cudaError_t launch_qk_norm_rope(const uint16_t* qkv, const float* q_norm, const 
                                 const moe_qk_dims& d, const moe_kv_cache& cache, uint16_t* q_out,
                                 int32_t* status, cudaStream_t s) {
   QkArgs a{qkv, q_norm, k_norm, cos_sin, pos, slots, d, cache, q_out, status, 1};
-  const int steps = cdiv(d.Hq + 2 * cache.Hkv, 32 / (cache.D / 8));
-  // one head step per warp while that leaves the SMs short of warps, then
-  // more steps per warp, which saves the repeated loads of the token's
-  // rotation row
+  const int hpw = 512 / cache.D, steps = cdiv(d.Hq, hpw) + 2 * cdiv(cache.Hkv, hpw);
+  // one step per warp while that leaves the SMs short of warps, then more
+  // steps per warp, which saves the repeated loads of the token's rotation row
   const long long want = (long long)num_sms() * 32;
-  a.chunks = (int)std::min<long long>(steps, std::max<long long>(cdiv(steps, 8), want / d.T));
+  a.chunks = (int)std::min<long long>(steps, std::max<long long>(cdiv(steps, 16), want / d.T));
   const long long warps = (long long)d.T * a.chunks;
   const dim3 grid((unsigned)((warps + 3) / 4)), blk(128);
   if (cache.D == 64) return launch_k(k_qk_norm_rope<64>, grid, blk, 0, s, true, a);
