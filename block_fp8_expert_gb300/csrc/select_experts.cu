@@ -36,9 +36,13 @@ __device__ __forceinline__ float warp_sum(float v) {
 //            its lanes (ALIGNED: groups of 2^i EPL experts); other group sizes:
 //            per group two warp-wide integer max reductions.  A group's
 //            score is ranked against the others'; the kept groups are a mask;
-//   top-k    per round a max reduction over the lanes' best remaining keys;
-//            the lowest lane that holds it wins (ties to the lower expert) and
-//            rescans its own experts.
+//   top-k    the k-th largest of the lanes' best keys bounds the k-th largest
+//            key from below.  The keys that reach it, seldom many more than k,
+//            are gathered one per lane and ranked against one another, ties to
+//            the lower expert; a lane's rank is its slot.  Where more than 32
+//            reach it (many equal keys), k rounds pick the largest remaining
+//            key each: a max reduction, the lowest lane that holds it wins and
+//            rescans its experts.
 template <int EPL, bool ALIGNED>
 __global__ void __launch_bounds__(128)
 k_select_experts(const float* __restrict__ logits, long long row_stride,
@@ -79,19 +83,16 @@ k_select_experts(const float* __restrict__ logits, long long row_stride,
     if (vmax == -INFINITY) vmax = 0.f;  // every expert off: all scores 0
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) s += expf(l[i] - vmax);
+    for (int i = 0; i < EPL; ++i) {
+      l[i] = expf(l[i] - vmax);
+      s += l[i];
+    }
     s = warp_sum(s);
     inv_sum = s == 0.f ? 0.f : 1.f / s;
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    float s;
-    if (sigmoid) {
-      s = __frcp_rn(1.f + expf(-l[i]));
-      l[i] = s;  // the weight's source: the score itself
-    } else {
-      s = expf(l[i] - vmax) * inv_sum;
-    }
+    float s = sigmoid ? __frcp_rn(1.f + expf(-l[i])) : l[i] * inv_sum;
     const bool real = e0 + i < E;
     if (bias && real) s += __ldg(bias + e0 + i);
     key[i] = real ? order_key(s) : INT_MIN;
@@ -152,38 +153,82 @@ k_select_experts(const float* __restrict__ logits, long long row_stride,
         if (e0 + i < E && !((kept >> ((e0 + i) / n)) & 1u)) key[i] = INT_MIN;
     }
   }
-  int hk, hs;  // the lane's best remaining key and its place
-  float hv;
-  auto rescan = [&]() {
-    hk = key[0];
-    hs = 0;
-    hv = l[0];
+  int hk, hs;  // the lane's best key and its place
+  auto rescan = [&]() {  // a tree, so that few of its steps wait for one another
+    int tk[EPL], ts[EPL];
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) {
-      const bool up = key[i] > hk;  // the first (lowest) expert of equal keys
-      hk = up ? key[i] : hk;
-      hs = up ? i : hs;
-      hv = up ? l[i] : hv;
+    for (int i = 0; i < EPL; ++i) {
+      tk[i] = key[i];
+      ts[i] = i;
     }
+#pragma unroll
+    for (int w = EPL / 2; w > 0; w /= 2)
+#pragma unroll
+      for (int i = 0; i < w; ++i) {
+        const bool up = tk[2 * i + 1] > tk[2 * i];  // equal keys: the lower expert
+        tk[i] = up ? tk[2 * i + 1] : tk[2 * i];
+        ts[i] = up ? ts[2 * i + 1] : ts[2 * i];
+      }
+    hk = tk[0];
+    hs = ts[0];
   };
   rescan();
+  __shared__ int2 s_pool[4][32];
+  int2* pool = s_pool[threadIdx.x >> 5];
   int my_idx = 0;
-  float my_v = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int wk = __reduce_max_sync(kAll, hk);
-    const int src = __ffs(__ballot_sync(kAll, hk == wk)) - 1;
-    const int we = __shfl_sync(kAll, e0 + hs, src);
-    const float wv = __shfl_sync(kAll, hv, src);
-    if (lane == j) {
-      my_idx = we;
-      my_v = wv;
-    }
-    if (lane == src) {
+  // the k-th largest best key (INT_MIN where fewer lanes have one)
+  pool[lane].x = hk;
+  __syncwarp();
+  int better = 0;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) {
+    const int o = pool[i].x;
+    better += o > hk || (o == hk && i < lane);
+  }
+  const int bound = __shfl_sync(kAll, hk, __ffs(__ballot_sync(kAll, better == k - 1)) - 1);
+  int mine = 0;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) key[i] = i == hs ? INT_MIN : key[i];
-      rescan();
+  for (int i = 0; i < EPL; ++i) mine += key[i] >= bound && key[i] != INT_MIN;
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, upto, o);
+    if (lane >= o) upto += v;
+  }
+  const int n_pool = __shfl_sync(kAll, upto, 31);
+  __syncwarp();  // the best keys have been read
+  if (n_pool <= 32) {
+    int w = upto - mine;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (key[i] >= bound && key[i] != INT_MIN) pool[w++] = make_int2(key[i], e0 + i);
+    __syncwarp();
+    const int2 me = pool[lane];
+    int rank = 0;  // (the pool is in ascending order of experts)
+    for (int i = 0; i < n_pool; ++i) {
+      const int o = pool[i].x;
+      rank += o > me.x || (o == me.x && i < lane);
+    }
+    __syncwarp();
+    if (lane < n_pool && rank < k) pool[rank].y = me.y;
+    __syncwarp();
+    if (lane < k) my_idx = pool[lane].y;
+  } else {
+    for (int j = 0; j < k; ++j) {
+      const int wk = __reduce_max_sync(kAll, hk);
+      const int src = __ffs(__ballot_sync(kAll, hk == wk)) - 1;
+      const int we = __shfl_sync(kAll, e0 + hs, src);
+      if (lane == j) my_idx = we;
+      if (lane == src) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = i == hs ? INT_MIN : key[i];
+        rescan();
+      }
     }
   }
+  // the chosen experts' logits again (cheaper than carrying them along)
+  float my_v = lane < k ? __ldg(row + my_idx) : -INFINITY;
+  if (sigmoid) my_v = __frcp_rn(1.f + expf(-my_v));
   // weights: the chosen scores, renormalised softmax as the softmax over the
   // chosen logits (the normaliser over all experts cancels)
   float w;
