@@ -16,12 +16,13 @@ constexpr uint32_t kQuantMinBits = 0x05000000u;  // 2^-117
 // From the bits of a group's largest magnitude: the factor v -> code, which
 // is 448 times the rounded reciprocal (what tensor programs compute for
 // 448 / a, so that activations quantised by one agree code for code), and the
-// scale code -> v, each rounded to nearest (0 for a group that holds nothing).
+// scale code -> v, a times the rounded 1 / 448 (0 for a group that holds
+// nothing).
 __device__ __forceinline__ void quant_factors(uint32_t maxbits, float& to_code, float& scale) {
   const float a = __uint_as_float(maxbits);
   const bool any = maxbits >= kQuantMinBits;
   to_code = any ? __fmul_rn(448.f, __frcp_rn(a)) : 0.f;
-  scale = any ? __fdiv_rn(a, 448.f) : 0.f;
+  scale = any ? __fmul_rn(a, 1.f / 448.f) : 0.f;
 }
 // Two floats -> two E4M3 codes (lo in bits 0..7), nearest even, saturated.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {

@@ -2,6 +2,7 @@
 //   out[m, n] = sum_b Sx[m, b] Sw[n / 128, b] P_b[m, n] + bias[n],
 //   P_b[m, n] = sum over the 128 columns of block b of code_x code_w.
 #include <algorithm>
+#include <type_traits>
 
 #include "decoder_internal.h"
 #include "tcgen05.cuh"
@@ -253,6 +254,13 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// (a.x, a.y) = (p.x, p.y) * (f, f)
+__device__ __forceinline__ void mul2(float2& a, uint32_t p0, uint32_t p1, float f) {
+  asm("{\n .reg .b64 A, P, F;\n mov.b64 P, {%2, %3};\n mov.b64 F, {%4, %4};\n"
+      " mul.rn.f32x2 A, P, F;\n mov.b64 {%0, %1}, A;\n}\n"
+      : "=f"(a.x), "=f"(a.y)
+      : "r"(p0), "r"(p1), "f"(f));
 }
 // (a.x, a.y) += (p.x, p.y) * (f, f)
 __device__ __forceinline__ void fma2(float2& a, uint32_t p0, uint32_t p1, float f) {
@@ -680,17 +688,17 @@ k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
     const uint32_t p_empty[2] = {in_cta(&sh.p_empty[0], 0), in_cta(&sh.p_empty[1], 0)};
     int it = 0;
     bool ok = true;
+    // tile t = (trow, tcol), the walk's step in rows and columns of tiles
+    int trow = pair / tn, tcol = pair % tn;
+    const int dr = npairs / tn, dc = npairs % tn;
     BlockScales sw;
-    auto scales_of = [&](int t) {  // (past the matrix any scale will do: its features are not stored)
-      const int n = min((t % tn) * PT + 64 * part, a.N - 1);
-      sw.start(a.sw + (size_t)(n / kScaleBlock) * nk, nk, lane);
+    auto scales_of = [&](int col) {  // (past the matrix any scale will do: its features are not stored)
+      sw.start(a.sw + (size_t)(min(col, a.N - 1) / kScaleBlock) * nk, nk, lane);
     };
-    scales_of(pair);
+    scales_of(tcol * PT + 64 * part);
     for (int t = pair; t < tiles && ok; t += npairs) {
-      const int n0 = (t % tn) * PT + 64 * part, m = (t / tn) * PT + 128 * rank + 32 * q;
+      const int n0 = tcol * PT + 64 * part, m = trow * PT + 128 * rank + 32 * q;
       float2 acc[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) acc[j] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < nk; ++kb, ++it) {
         const int b = it & 1;
         const float w = sw.at(kb);
@@ -700,21 +708,39 @@ k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
         }
         tc::fence_after_sync();
         const float f0 = w * sh.sx[it % PSX_SLOTS][32 * q + lane];
+        // the tile's first block sets the sums, the others add to them
+        auto promote = [&](auto first) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t p[16];
-          tc::ld_32x32b_x16(t_lane + b * PT + 16 * h, p);
-          tc::wait_ld();
-          if (h == 3) {  // the next block but one may overwrite the buffer
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(p_empty[b]);
+          for (int h = 0; h < 4; ++h) {
+            uint32_t p[16];
+            tc::ld_32x32b_x16(t_lane + b * PT + 16 * h, p);
+            tc::wait_ld();
+            if (h == 3) {  // the next block but one may overwrite the buffer
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) arrive_cluster(p_empty[b]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if constexpr (decltype(first)::value)
+                mul2(acc[8 * h + j], p[2 * j], p[2 * j + 1], f0);
+              else
+                fma2(acc[8 * h + j], p[2 * j], p[2 * j + 1], f0);
+            }
           }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) fma2(acc[8 * h + j], p[2 * j], p[2 * j + 1], f0);
-        }
+        };
+        if (kb == 0)
+          promote(std::true_type());
+        else
+          promote(std::false_type());
       }
-      if (t + npairs < tiles) scales_of(t + npairs);
+      trow += dr;
+      tcol += dc;
+      if (tcol >= tn) {
+        tcol -= tn;
+        ++trow;
+      }
+      if (t + npairs < tiles) scales_of(tcol * PT + 64 * part);
       if (ok) {
         if (lane == 0) tc::bulk_wait_read_all();  // the previous tile has left the buffer
         __syncwarp();

@@ -448,8 +448,9 @@ typedef struct {
  * Keys and values go to slot slots[t] of the cache (slots[t] < 0: a padding
  * token, nothing is stored); two tokens of one call must not share a slot.
  * MOE_KV_E4M3: per token and head with a = the largest magnitude, code =
- * E4M3(v * fp32(448 * fp32(1 / a))) to nearest even, scale = fp32(a / 448);
- * a = 0 gives zero codes and scale; 0 < a < 2^-117 is treated as a = 0.
+ * E4M3(v * fp32(448 * fp32(1 / a))) to nearest even, scale = fp32(a *
+ * fp32(1 / 448)); a = 0 gives zero codes and scale; 0 < a < 2^-117 is treated
+ * as a = 0.
  * q_norm, k_norm float [D] or NULL; cos_sin float [n_pos, rot], pos int32 [T]
  * (both NULL iff rot == 0); slots int64 [T].
  * A position outside [0, n_pos) raises MOE_DEV_BAD_POSITION: the token's
@@ -514,7 +515,8 @@ typedef struct {
  * activations are quantised in the call per row and group of 128 columns,
  * with a the group's largest magnitude:
  *   code = E4M3(x * fp32(448 * fp32(1 / a))) to nearest even,
- *   scale = fp32(a / 448); a = 0, or below 2^-117, gives zero codes and scale.
+ *   scale = fp32(a * fp32(1 / 448)); a = 0, or below 2^-117, gives zero codes
+ *   and scale.
  * Each 128-wide block's products are summed and scaled by both scales in
  * fp32, the blocks are summed in fp32, and the result is rounded once.
  * x bf16 [M, x_stride], bias float [N] or NULL, out bf16 [M, out_stride].
