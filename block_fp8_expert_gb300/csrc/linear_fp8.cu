@@ -2,7 +2,6 @@
 //   out[m, n] = sum_b Sx[m, b] Sw[n / 128, b] P_b[m, n] + bias[n],
 //   P_b[m, n] = sum over the 128 columns of block b of code_x code_w.
 #include <algorithm>
-#include <type_traits>
 
 #include "decoder_internal.h"
 #include "tcgen05.cuh"
@@ -220,8 +219,7 @@ struct GemmShared {
 
 // Warp-uniform bounded wait: the warp gives up together once the budget is
 // spent or another role has given up.
-template <class Shared>
-__device__ __forceinline__ bool gwait(Shared& sh, uint64_t* bar, uint32_t parity,
+__device__ __forceinline__ bool gwait(GemmShared& sh, uint64_t* bar, uint32_t parity,
                                       int32_t* status) {
   constexpr unsigned kAll = 0xffffffffu;
   bool done = mbar_try_wait(bar, parity);
@@ -254,13 +252,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-// (a.x, a.y) = (p.x, p.y) * (f, f)
-__device__ __forceinline__ void mul2(float2& a, uint32_t p0, uint32_t p1, float f) {
-  asm("{\n .reg .b64 A, P, F;\n mov.b64 P, {%2, %3};\n mov.b64 F, {%4, %4};\n"
-      " mul.rn.f32x2 A, P, F;\n mov.b64 {%0, %1}, A;\n}\n"
-      : "=f"(a.x), "=f"(a.y)
-      : "r"(p0), "r"(p1), "f"(f));
 }
 // (a.x, a.y) += (p.x, p.y) * (f, f)
 __device__ __forceinline__ void fma2(float2& a, uint32_t p0, uint32_t p1, float f) {
@@ -336,6 +327,17 @@ __device__ __forceinline__ float bias_at(const GemmArgs& a, int n) {
 // The weights' first stages are on their way before the quantisation ends.
 // A cluster's sums meet in shared memory: each CTA adds its share of the rows
 // over the CTAs in order and writes it.
+//
+// What bounds it, at M 4096, N 5120, K 2048 (53 us with the quantisation, 1.62
+// PFLOP/s): an SM takes in about 64 bytes per cycle, so the 32 KB of a block
+// take 500 cycles (the MMAs 256), 555 measured with two CTAs per SM, and 1280
+// equal tiles make five rounds of 304 where 4.2 would do.  Measured instead,
+// and left out: 128 x 256 tiles, one persistent CTA per SM (48 KB per block of
+// twice the features; 940 cycles a block, the copies' latency with three
+// stages: 51.7 us, and slower below 150 tiles), the same with W multicast to a
+// cluster of two (52.8 us), and 256 x 256 tiles of CTA pairs (32 KB per block,
+// but 880 cycles for the two buffers' way from MMA to registers and back
+// across the pair: 52.5 us).
 template <int SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 2)
 k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
@@ -511,261 +513,6 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
   }
 }
 
-// ---------------------------------------------------------------------------
-// Many tiles: CTA pairs
-// ---------------------------------------------------------------------------
-// Two CTAs (cta_group::2) own a 256 x 256 tile: each holds 128 rows of x and
-// 128 rows of W in shared memory, the pair's MMA (M 256, N 256) reads both,
-// and each CTA's tensor memory receives its 128 rows x 256 features.  An SM
-// then loads 32 KB per K block where a lone CTA with the same tile per SM
-// (128 x 256) would load 48 KB, and its MMAs read a third less shared memory.
-// Roles as above, with these differences:
-//  - the first CTA's `full` barriers count the bytes of both CTAs' copies and
-//    its warp 1 issues all MMAs; the commits arrive in both CTAs;
-//  - the promoting warps of both CTAs arrive on the first CTA's p_empty;
-//  - sixteen promoting warps, a thread owns a row and 64 features: with eight
-//    (128 features each) the loads' latency, not their rate, set the pace;
-//  - the pairs walk over the tiles (persistent), the next tile's first blocks
-//    being computed while the last one is written.
-namespace {
-constexpr int PT = 256;                  // rows and features of a pair's tile
-constexpr int PSTAGES = 4;
-constexpr int kPairProWarps = 16;
-constexpr int kPairThreads = (2 + kPairProWarps) * 32;
-constexpr int P_SMEM = PSTAGES * G_STAGE + kPairProWarps * 4096 + 1024;
-static_assert(P_SMEM + 5 * 1024 <= 227 * 1024, "shared memory");
-
-constexpr int PSX_SLOTS = PSTAGES + 2;
-
-struct PairShared {
-  alignas(128) float sx[PSX_SLOTS][128];
-  uint64_t full[PSTAGES], empty[PSTAGES], p_full[2], p_empty[2];
-  uint32_t tmem_base;
-  volatile int abort_flag;
-};
-
-// The address of the same shared variable in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-// (relaxed: what it announces, tensor memory that has been read, is ordered by
-// the tcgen05 waits and fences; a release would wait for the loads in flight)
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
-}
-// TMA load into this CTA, its bytes counted on a barrier of the pair.
-__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1,
-                                              uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrives on the barrier of both CTAs when the MMAs issued so far are done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-}  // namespace
-
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-k_linear_gemm_pair(const __grid_constant__ CUtensorMap xmap,
-                   const __grid_constant__ CUtensorMap wmap,
-                   const __grid_constant__ CUtensorMap omap,
-                   const __grid_constant__ CUtensorMap smap, const GemmArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ PairShared sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int tn = cdiv(a.N, PT), tiles = tn * cdiv(a.M, PT), nk = a.nkb;
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  if (tid == 0) {
-    for (int s = 0; s < PSTAGES; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&sh.p_full[b], 1);
-      mbar_init(&sh.p_empty[b], 2 * kPairProWarps);
-    }
-    sh.abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
-                     smem_u32(&sh.tmem_base))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
-  }
-  tc::fence_before_sync();
-  __syncthreads();
-  cluster_sync();  // both CTAs' barriers and tensor memory are ready
-  tc::fence_after_sync();
-  const uint32_t tmem = sh.tmem_base;
-
-  if (warp == 0) {
-    int it = 0;
-    bool ok = true, waited = false;
-    for (int t = pair; t < tiles && ok; t += npairs) {
-      const int n0 = (t % tn) * PT + 128 * rank, m0 = (t / tn) * PT + 128 * rank;
-      for (int kb = 0; kb < nk; ++kb, ++it) {
-        const int s = it % PSTAGES;
-        if (it >= PSTAGES && !gwait(sh, &sh.empty[s], (uint32_t)((it / PSTAGES - 1) & 1), a.status)) {
-          ok = false;
-          break;
-        }
-        if (tc::elect_one()) {
-          const uint32_t bar = in_cta(&sh.full[s], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * (G_STAGE + G_SX));
-          tma_load_pair(smem + s * G_STAGE + G_TILE, &wmap, kb * kScaleBlock, n0, bar);
-        }
-        __syncwarp();
-        if (!waited) griddep_wait();  // the codes and scales of x
-        waited = true;
-        if (tc::elect_one()) {
-          const uint32_t bar = in_cta(&sh.full[s], 0);
-          tma_load_pair(smem + s * G_STAGE, &xmap, kb * kScaleBlock, m0, bar);
-          tma_load_pair(sh.sx[it % PSX_SLOTS], &smap, m0, kb, bar);
-        }
-        __syncwarp();
-      }
-    }
-    // every copy of the pair has landed (counted in the first CTA) and every
-    // commit has arrived
-    if (lane == 0)
-      for (int j = max(0, it - PSTAGES); j < it; ++j) {
-        if (rank == 0) mbar_wait(&sh.full[j % PSTAGES], (uint32_t)((j / PSTAGES) & 1));
-        if (!sh.abort_flag) mbar_wait(&sh.empty[j % PSTAGES], (uint32_t)((j / PSTAGES) & 1));
-      }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (rank == 0) {
-      const uint32_t idesc = tc::idesc_f16_f32(PT, PT);  // the same fields; format 0 is E4M3 here
-      int it = 0;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += npairs)
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % PSTAGES, b = it & 1;
-          if (!gwait(sh, &sh.full[s], (uint32_t)((it / PSTAGES) & 1), a.status) ||
-              (it >= 2 && !gwait(sh, &sh.p_empty[b], (uint32_t)((it / 2 - 1) & 1), a.status))) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
-          if (tc::elect_one()) {
-            const uint32_t xa = smem_u32(smem) + s * G_STAGE, wa = xa + G_TILE;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f8_pair(tmem + b * PT, tc::sw128_desc(xa + 32 * k), tc::sw128_desc(wa + 32 * k), idesc,
-                          k > 0);
-            commit_pair(&sh.empty[s]);
-            commit_pair(&sh.p_full[b]);
-          }
-          __syncwarp();
-        }
-      if (lane == 0 && it > 0) mbar_wait(&sh.p_full[(it - 1) & 1], (uint32_t)(((it - 1) / 2) & 1));
-      __syncwarp();
-    }
-  } else {
-    const int q = warp & 3, part = (warp - 2) >> 2;  // lanes 32 q .., features 64 part ..
-    const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16) + 64 * part;
-    uint8_t* const tile = smem + PSTAGES * G_STAGE + (warp - 2) * 4096;
-    const uint32_t p_empty[2] = {in_cta(&sh.p_empty[0], 0), in_cta(&sh.p_empty[1], 0)};
-    int it = 0;
-    bool ok = true;
-    // tile t = (trow, tcol), the walk's step in rows and columns of tiles
-    int trow = pair / tn, tcol = pair % tn;
-    const int dr = npairs / tn, dc = npairs % tn;
-    BlockScales sw;
-    auto scales_of = [&](int col) {  // (past the matrix any scale will do: its features are not stored)
-      sw.start(a.sw + (size_t)(min(col, a.N - 1) / kScaleBlock) * nk, nk, lane);
-    };
-    scales_of(tcol * PT + 64 * part);
-    for (int t = pair; t < tiles && ok; t += npairs) {
-      const int n0 = tcol * PT + 64 * part, m = trow * PT + 128 * rank + 32 * q;
-      float2 acc[32];
-      for (int kb = 0; kb < nk; ++kb, ++it) {
-        const int b = it & 1;
-        const float w = sw.at(kb);
-        if (!gwait(sh, &sh.p_full[b], (uint32_t)((it / 2) & 1), a.status)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        const float f0 = w * sh.sx[it % PSX_SLOTS][32 * q + lane];
-        // the tile's first block sets the sums, the others add to them
-        auto promote = [&](auto first) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t p[16];
-            tc::ld_32x32b_x16(t_lane + b * PT + 16 * h, p);
-            tc::wait_ld();
-            if (h == 3) {  // the next block but one may overwrite the buffer
-              tc::fence_before_sync();
-              __syncwarp();
-              if (lane == 0) arrive_cluster(p_empty[b]);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if constexpr (decltype(first)::value)
-                mul2(acc[8 * h + j], p[2 * j], p[2 * j + 1], f0);
-              else
-                fma2(acc[8 * h + j], p[2 * j], p[2 * j + 1], f0);
-            }
-          }
-        };
-        if (kb == 0)
-          promote(std::true_type());
-        else
-          promote(std::false_type());
-      }
-      trow += dr;
-      tcol += dc;
-      if (tcol >= tn) {
-        tcol -= tn;
-        ++trow;
-      }
-      if (t + npairs < tiles) scales_of(tcol * PT + 64 * part);
-      if (ok) {
-        if (lane == 0) tc::bulk_wait_read_all();  // the previous tile has left the buffer
-        __syncwarp();
-        stage_rows(tile, acc, a.bias, n0, a.N, lane);
-        tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0 && n0 < a.N && m < a.M) {
-          tc::tma_store_2d(&omap, n0, m, tile);
-          tc::bulk_commit();
-        }
-        __syncwarp();
-      }
-    }
-    if (lane == 0) tc::bulk_wait_all();
-    __syncwarp();
-  }
-  tc::fence_before_sync();
-  __syncthreads();
-  cluster_sync();  // nothing of the pair is on its way to either CTA any more
-  if (warp == 1) {
-    tc::fence_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
-  }
-}
-
 namespace {
 
 // The streamed kernel up to 16 rows (N 5120, K 2048: 5.0 - 8.1 us against
@@ -829,44 +576,6 @@ cudaError_t launch_gemm(const CUtensorMap& xmap, const CUtensorMap& wmap, const 
   return cudaLaunchKernelEx(&cfg, k_linear_gemm<SPLIT>, xmap, wmap, omap, a);
 }
 
-// CTA pairs that can run at once on the current device.
-int max_pairs() {
-  static int cached[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms() / 2;
-  if (!cached[dev]) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = P_SMEM;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, k_linear_gemm_pair, &cfg) != cudaSuccess || n < 1)
-      n = num_sms() / 2;
-    cached[dev] = std::min(n, num_sms() / 2);
-  }
-  return cached[dev];
-}
-
-cudaError_t launch_gemm_pair(const CUtensorMap& xmap, const CUtensorMap& wmap,
-                             const CUtensorMap& omap, const GemmArgs& a, cudaStream_t s) {
-  CUtensorMap smap;  // the activation scales [nkb][ld]: 128 of a block
-  cudaError_t err = make_tensor_map_2d(&smap, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.sxt, a.nkb, a.ld,
-                                       128, 1, 0);
-  if (err != cudaSuccess) return err;
-  err = ensure_smem((const void*)k_linear_gemm_pair, P_SMEM);
-  if (err != cudaSuccess) return err;
-  const int pairs = std::min(max_pairs(), cdiv(a.M, PT) * cdiv(a.N, PT));
-  return launch_k(k_linear_gemm_pair, dim3(2 * pairs), dim3(kPairThreads), (size_t)P_SMEM, s, true,
-                  xmap, wmap, omap, smap, a);
-}
-
 }  // namespace
 
 size_t linear_fp8_workspace(const moe_linear_dims& d) { return lin_ws(d).total; }
@@ -899,7 +608,6 @@ cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const flo
   if (err != cudaSuccess) return err;
   const GemmArgs a{sxt, l.ld, w.scales, bias, out, d.out_stride, d.M, d.N, nkb, status};
   const int tiles = cdiv(d.M, GM) * cdiv(d.N, GN);
-  if (cdiv(d.M, PT) * cdiv(d.N, PT) >= num_sms() / 2) return launch_gemm_pair(xmap, wmap, omap, a, s);
   // K divided while that leaves one CTA per SM and four blocks per CTA: clusters
   // of four, two CTAs per SM take longer to place than they save (M 203, N 2048,
   // K 4096: 15.8 / 12.7 / 11.7 / 19.3 us with 1 / 2 / 4 / 8 CTAs per tile; M 1000,
