@@ -121,6 +121,7 @@ _SIGNATURES = {
     "moe_read_device_status": (_st, [_vp, ctypes.POINTER(ctypes.c_int32), _vp]),
     "moe_permute_static_scratch": (_st, [_vp, Dims, _vp, _vp, _vp, _vp]),
     "moe_select_experts": (_st, [_vp, _i64, _vp, SelectRule, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "moe_route_select": (_st, [_vp, _vp, _vp, _vp, SelectRule, Dims, _vp, _vp, _vp, _sz, _vp]),
     "moe_qk_norm_rope": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, QkDims, KvCache, _vp, _vp, _vp]),
     "moe_paged_attention_workspace_bytes": (_st, [AttnDims, _i32, ctypes.POINTER(_sz)]),
     "moe_paged_attention": (_st, [_vp, KvCache, _vp, _vp, AttnDims, _vp, _vp, _sz, _vp, _vp]),
@@ -300,6 +301,13 @@ def moe_select_experts(logits, row_stride: int, bias, rule: SelectRule, T: int, 
     _check(lib().moe_select_experts(_ptr(logits), row_stride, _ptr(bias), rule, T, E, k,
                                     _ptr(topk_idx), _ptr(topk_w), _stream(stream)),
            "moe_select_experts")
+
+
+def moe_route_select(x, Wr, logit_bias, bias, rule: SelectRule, d: Dims, topk_idx, topk_w, ws,
+                     stream=None) -> None:
+    _check(lib().moe_route_select(_ptr(x), _ptr(Wr), _ptr(logit_bias), _ptr(bias), rule, d,
+                                  _ptr(topk_idx), _ptr(topk_w), _ptr(ws), _nbytes(ws),
+                                  _stream(stream)), "moe_route_select")
 
 
 def moe_qk_norm_rope(qkv, q_norm, k_norm, cos_sin, pos, slots, d: QkDims, cache: KvCache, q_out,

@@ -53,6 +53,23 @@ moe_status check_attn(const moe_attn_dims& d, int D) {
   return MOE_OK;
 }
 
+moe_status check_rule(const moe_select_rule& rule, int E, int k) {
+  if (rule.score != MOE_SCORE_SOFTMAX && rule.score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_INVALID_ARG, "score %d", rule.score);
+  if (rule.groups < 1 || rule.groups > 32 || E % rule.groups)
+    return fail(MOE_ERR_UNSUPPORTED, "groups = %d: need 1 to 32 that divide E = %d", rule.groups, E);
+  if (rule.top_groups < 1 || rule.top_groups > rule.groups)
+    return fail(MOE_ERR_INVALID_ARG, "top_groups = %d outside [1, %d]", rule.top_groups, rule.groups);
+  const int n = E / rule.groups;
+  if (rule.group_top < 1 || rule.group_top > 2 || (rule.groups > 1 && rule.group_top > n))
+    return fail(MOE_ERR_INVALID_ARG, "group_top = %d: need 1 or 2, at most the group's %d experts",
+                rule.group_top, n);
+  if (k < 1 || k > 32 || k > rule.top_groups * n)
+    return fail(MOE_ERR_UNSUPPORTED, "k = %d outside [1, min(%d experts of the kept groups, 32)]", k,
+                rule.top_groups * n);
+  return MOE_OK;
+}
+
 moe_status check_linear(const moe_linear_dims& d) {
   if (d.M < 0) return fail(MOE_ERR_INVALID_ARG, "M = %d < 0", d.M);
   if (d.N < 8 || d.N > 65536 || d.N % 8)
@@ -77,19 +94,8 @@ moe_status moe_select_experts(const float* logits, int64_t row_stride, const flo
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", T);
   if (E < 1 || E > kMaxExperts)
     return fail(MOE_ERR_UNSUPPORTED, "E = %d outside [1, %d]", E, kMaxExperts);
-  if (rule.score != MOE_SCORE_SOFTMAX && rule.score != MOE_SCORE_SIGMOID)
-    return fail(MOE_ERR_INVALID_ARG, "score %d", rule.score);
-  if (rule.groups < 1 || rule.groups > 32 || E % rule.groups)
-    return fail(MOE_ERR_UNSUPPORTED, "groups = %d: need 1 to 32 that divide E = %d", rule.groups, E);
-  if (rule.top_groups < 1 || rule.top_groups > rule.groups)
-    return fail(MOE_ERR_INVALID_ARG, "top_groups = %d outside [1, %d]", rule.top_groups, rule.groups);
-  const int n = E / rule.groups;
-  if (rule.group_top < 1 || rule.group_top > 2 || (rule.groups > 1 && rule.group_top > n))
-    return fail(MOE_ERR_INVALID_ARG, "group_top = %d: need 1 or 2, at most the group's %d experts",
-                rule.group_top, n);
-  if (k < 1 || k > 32 || k > rule.top_groups * n)
-    return fail(MOE_ERR_UNSUPPORTED, "k = %d outside [1, min(%d experts of the kept groups, 32)]", k,
-                rule.top_groups * n);
+  const moe_status s = check_rule(rule, E, k);
+  if (s != MOE_OK) return s;
   if ((long long)T * k >= (1ll << 31)) return fail(MOE_ERR_UNSUPPORTED, "T*k too large");
   if (row_stride < E) return fail(MOE_ERR_INVALID_ARG, "row_stride = %lld < E", (long long)row_stride);
   if (T == 0) return MOE_OK;
@@ -97,9 +103,39 @@ moe_status moe_select_experts(const float* logits, int64_t row_stride, const flo
   REQUIRE_OPT_PTR(bias);
   REQUIRE_PTR(topk_idx);
   REQUIRE_PTR(topk_w);
-  CUDA_CHECK(launch_select_experts(logits, row_stride, bias, rule, T, E, k, topk_idx, topk_w,
-                                   (cudaStream_t)stream),
+  CUDA_CHECK(launch_select_experts(logits, row_stride, 1, 0, nullptr, bias, rule, T, E, k, topk_idx,
+                                   topk_w, (cudaStream_t)stream),
              "moe_select_experts");
+  return MOE_OK;
+}
+
+moe_status moe_route_select(const uint16_t* x, const float* Wr, const float* logit_bias,
+                            const float* bias, moe_select_rule rule, moe_dims d,
+                            int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
+                            void* stream) {
+  size_t need = 0;
+  moe_status s = moe_workspace_bytes(d, &need);  // checks the dims
+  if (s != MOE_OK) return s;
+  if ((s = check_rule(rule, d.E, d.k)) != MOE_OK) return s;
+  if (d.T == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(Wr);
+  REQUIRE_OPT_PTR(logit_bias);
+  REQUIRE_OPT_PTR(bias);
+  REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(topk_w);
+  REQUIRE_PTR(ws);
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", ws_bytes, need);
+  const WsLayout L = ws_layout(d);
+  float* part = at<float>(ws, L.logits);
+  const cudaStream_t st = (cudaStream_t)stream;
+  CUDA_CHECK(launch_router_logits(x, Wr, d.T, d.H, d.E, part, at<uint16_t>(ws, L.wr_planes), nullptr,
+                                  nullptr, at<int32_t>(ws, L.status), st, true),
+             "moe_route_select");
+  CUDA_CHECK(launch_select_experts(part, d.E, route_kslices(d.T, d.H, d.E), (long long)d.T * d.E,
+                                   logit_bias, bias, rule, d.T, d.E, d.k, topk_idx, topk_w, st),
+             "moe_route_select");
   return MOE_OK;
 }
 

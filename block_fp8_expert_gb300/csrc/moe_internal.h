@@ -83,6 +83,14 @@ cudaError_t launch_route(const uint16_t* x, const float* Wr, const float* bias, 
                          cudaStream_t s, bool pdl, const float* shared_gate = nullptr,
                          float* sgate = nullptr);
 
+// The router logits alone: route_kslices(T, H, E) slices of partial sums,
+// part[ks][t][e]; the reader adds the slices in order.  Clears the status
+// words.  Arguments as launch_route's.
+int route_kslices(int T, int H, int E);
+cudaError_t launch_router_logits(const uint16_t* x, const float* Wr, int T, int H, int E,
+                                 float* part, uint16_t* planes, uint16_t* xn, int8_t* xe,
+                                 int32_t* status, cudaStream_t s, bool pdl);
+
 // Router logits on the tensor cores (route_tc.cu): T >= 128, E % 128 == 0,
 // H % 64 == 0.  Writes KS slices of partial logits (KS from route_kslices).
 bool router_tc_ok(int T, int H, int E);

@@ -45,7 +45,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 //            rescans its experts.
 template <int EPL, bool ALIGNED>
 __global__ void __launch_bounds__(128)
-k_select_experts(const float* __restrict__ logits, long long row_stride,
+k_select_experts(const float* __restrict__ logits, long long row_stride, int slices,
+                 long long slice_stride, const float* __restrict__ logit_bias,
                  const float* __restrict__ bias, const moe_select_rule rule, int T, int E, int k,
                  int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
   constexpr unsigned kAll = 0xffffffffu;
@@ -72,6 +73,17 @@ k_select_experts(const float* __restrict__ logits, long long row_stride,
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) l[i] = e0 + i < E ? __ldg(row + e0 + i) : -INFINITY;
+  }
+  // the router's partial sums in order, then its bias
+#pragma unroll 1
+  for (int ks = 1; ks < slices; ++ks)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (e0 + i < E) l[i] += __ldg(row + ks * slice_stride + e0 + i);
+  if (logit_bias) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (e0 + i < E) l[i] += __ldg(logit_bias + e0 + i);
   }
   const bool sigmoid = rule.score == MOE_SCORE_SIGMOID;
   float vmax = 0.f, inv_sum = 0.f;  // softmax statistics
@@ -228,6 +240,10 @@ k_select_experts(const float* __restrict__ logits, long long row_stride,
   }
   // the chosen experts' logits again (cheaper than carrying them along)
   float my_v = lane < k ? __ldg(row + my_idx) : -INFINITY;
+  if (lane < k) {
+    for (int ks = 1; ks < slices; ++ks) my_v += __ldg(row + ks * slice_stride + my_idx);
+    if (logit_bias) my_v += __ldg(logit_bias + my_idx);
+  }
   if (sigmoid) my_v = __frcp_rn(1.f + expf(-my_v));
   // weights: the chosen scores, renormalised softmax as the softmax over the
   // chosen logits (the normaliser over all experts cancels)
@@ -252,9 +268,10 @@ k_select_experts(const float* __restrict__ logits, long long row_stride,
   }
 }
 
-cudaError_t launch_select_experts(const float* logits, long long row_stride, const float* bias,
-                                  const moe_select_rule& rule, int T, int E, int k,
-                                  int32_t* topk_idx, float* topk_w, cudaStream_t s) {
+cudaError_t launch_select_experts(const float* logits, long long row_stride, int slices,
+                                  long long slice_stride, const float* logit_bias,
+                                  const float* bias, const moe_select_rule& rule, int T, int E,
+                                  int k, int32_t* topk_idx, float* topk_w, cudaStream_t s) {
   const dim3 grid(cdiv(T, 4)), blk(128);
   int epl = 2;
   while (epl * 32 < E) epl *= 2;
@@ -262,9 +279,11 @@ cudaError_t launch_select_experts(const float* logits, long long row_stride, con
   const bool aligned = n % epl == 0 && (span & (span - 1)) == 0;
 #define MOE_SELECT(EPLV)                                                                        \
   return aligned ? launch_k(k_select_experts<EPLV, true>, grid, blk, 0, s, true, logits,        \
-                            row_stride, bias, rule, T, E, k, topk_idx, topk_w)                  \
+                            row_stride, slices, slice_stride, logit_bias, bias, rule, T, E, k,  \
+                            topk_idx, topk_w)                                                   \
                  : launch_k(k_select_experts<EPLV, false>, grid, blk, 0, s, true, logits,       \
-                            row_stride, bias, rule, T, E, k, topk_idx, topk_w)
+                            row_stride, slices, slice_stride, logit_bias, bias, rule, T, E, k,  \
+                            topk_idx, topk_w)
   if (epl <= 2) MOE_SELECT(2);
   if (epl <= 4) MOE_SELECT(4);
   if (epl <= 8) MOE_SELECT(8);

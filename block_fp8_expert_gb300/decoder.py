@@ -128,6 +128,27 @@ class ExpertSelector:
             _lib._check(st, "moe_select_experts")
         return topk_idx, topk_w
 
+    def route(self, x: torch.Tensor, layer, ws: torch.Tensor,
+              topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+              stream=None):
+        """The same choice from the tokens x bf16 [T, H] and a DeviceLayer's
+        router (moe_route_select); ws: the layer's workspace for T tokens."""
+        T = x.shape[0]
+        if layer.E != self.E or layer.k != self.k:
+            raise ValueError(f"the layer routes to {layer.k} of {layer.E} experts, "
+                             f"need {self.k} of {self.E}")
+        if not x.is_cuda or x.dtype != _BF16 or x.shape != (T, layer.H) or not x.is_contiguous():
+            _refuse(x, "x", _BF16, (T, layer.H))
+        if topk_idx is None:
+            topk_idx = _new(stream, T, self.k, dtype=_I32, device=x.device)
+        if topk_w is None:
+            topk_w = _new(stream, T, self.k, dtype=_F32, device=x.device)
+        _dense(topk_idx, "topk_idx", _I32, T, self.k)
+        _dense(topk_w, "topk_w", _F32, T, self.k)
+        _lib.moe_route_select(x, layer.Wr, layer.bias, self.bias, self.rule, layer.dims(T),
+                              topk_idx, topk_w, ws, stream)
+        return topk_idx, topk_w
+
 
 class PagedCache:
     """A paged key/value cache over tensors [pages, Hkv, page_size, D]: bf16,

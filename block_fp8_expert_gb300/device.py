@@ -100,6 +100,31 @@ class DeviceLayer:
                                    self.dims(T), out, topk_idx, topk_w, ws, stream)
         return out
 
+    def experts(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """out[T, H] (bf16) = the routed experts applied to x[T, H] (bf16) with
+        a routing made elsewhere (topk_idx int32 [T, k], topk_w float32
+        [T, k]): moe_permute, moe_expert_ffn_fp8 and moe_combine."""
+        if self.shared is not None:
+            raise ValueError("layers with a shared expert run through forward()")
+        T = x.shape[0]
+        d, P = self.dims(T), T * self.k
+        i32 = dict(dtype=torch.int32, device=x.device)
+        off, rows, slot_row = (torch.empty(n, **i32) for n in (self.E + 1, P, P))
+        y = torch.empty((P, self.H), dtype=torch.float32, device=x.device)
+        if out is None:
+            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device)
+        if ws is None:
+            ws = self.workspace(T)
+        if stream is not None:  # the call may still use them when this returns
+            s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+            for t in (off, rows, slot_row, y, out, ws):
+                t.record_stream(s)
+        _lib.moe_permute(topk_idx, d, off, rows, slot_row, ws, stream)
+        _lib.moe_expert_ffn_fp8(x, off, rows, self.routed.abi(), d, y, ws, stream)
+        _lib.moe_combine(y, slot_row, topk_w, None, d, out, stream)
+        return out
 
     def verify(self, x: torch.Tensor, out: torch.Tensor, topk_idx: torch.Tensor,
                topk_w: torch.Tensor, tokens, stream=None) -> dict:

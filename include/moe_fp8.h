@@ -406,6 +406,17 @@ moe_status moe_select_experts(const float* logits, int64_t row_stride,
                               int32_t T, int32_t E, int32_t k,
                               int32_t* topk_idx, float* topk_w, void* stream);
 
+/*
+ * moe_select_experts on the router's own logits: x Wr^T (+ logit_bias), as in
+ * moe_route (x bf16 [T, H], Wr float [E, H], logit_bias float [E] or NULL,
+ * workspace and status as there), then the selection by `rule`.
+ */
+moe_status moe_route_select(const uint16_t* x, const float* Wr,
+                            const float* logit_bias, const float* bias,
+                            moe_select_rule rule, moe_dims d,
+                            int32_t* topk_idx, float* topk_w, void* ws,
+                            size_t ws_bytes, void* stream);
+
 #define MOE_KV_BF16 0
 #define MOE_KV_E4M3 1
 

@@ -157,3 +157,16 @@ def test_rotation_tables():
             rope_cos_sin(8, rot, base, device="cpu", **bad)
     with pytest.raises(ValueError):
         rope_cos_sin(8, 7, device="cpu")
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(H=100), UNS), (dict(k=40), UNS), (dict(x=None), INV), (dict(Wr=P + 4), INV),
+    (dict(logit_bias=P + 4), INV), (dict(bias=P + 4), INV), (dict(idx=None), INV), (dict(w=None), INV),
+    (dict(ws=None), INV), (dict(nws=100), WS), (dict(groups=5), UNS), (dict(score=3), INV)])
+def test_route_select_refusals(L, kw, code):
+    a = dict(x=P, Wr=P, logit_bias=None, bias=None, idx=P, w=P, ws=P, nws=1 << 40, H=256, k=2, groups=1, score=0)
+    a.update(kw)
+    d = _lib.dims(8, a["H"], 128, 16, a["k"])
+    r = _rule(groups=a["groups"], top_groups=1, group_top=1, score=a["score"])
+    assert L.moe_route_select(a["x"], a["Wr"], a["logit_bias"], a["bias"], r, d, a["idx"], a["w"],
+                              a["ws"], a["nws"], None) == code
