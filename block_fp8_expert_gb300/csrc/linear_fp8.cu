@@ -189,7 +189,8 @@ constexpr int GSTAGES = 3;
 constexpr int G_TILE = 128 * 128;        // bytes of one operand's 128 rows x 128 K
 constexpr int G_STAGE = 2 * G_TILE;
 constexpr int G_PITCH = GN + 4;          // floats per row of the split's exchange
-constexpr int G_SMEM = GSTAGES * G_STAGE + 1024;
+constexpr int G_EXCHANGE = GM * G_PITCH * 4;
+constexpr int g_smem(int split) { return GSTAGES * G_STAGE + (split > 1 ? G_EXCHANGE : 0) + 1024; }
 // The activation scales of a block's 128 rows ride with its stage, into a ring
 // of their own that is two slots longer: a stage is refilled once its MMAs are
 // done, when the sums of all but the last two blocks have been read (p_empty).
@@ -197,7 +198,7 @@ constexpr int G_SX = 128 * 4;
 constexpr int GSX_SLOTS = GSTAGES + 2;
 constexpr int kProWarps = 8;
 constexpr int kGemmThreads = (2 + kProWarps) * 32;
-static_assert(GM * G_PITCH * 4 <= GSTAGES * G_STAGE, "the exchange reuses the stages");
+static_assert(kProWarps * 4096 <= GSTAGES * G_STAGE, "the output is staged in the ring");
 
 struct GemmArgs {
   const float* sxt;
@@ -260,19 +261,22 @@ __device__ __forceinline__ void fma2(float2& a, uint32_t p0, uint32_t p1, float 
       : "+f"(a.x), "+f"(a.y)
       : "r"(p0), "r"(p1), "f"(f));
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::
-                   : "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ float4 ld_cluster(uint32_t local, uint32_t rank) {
-  float4 v;
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// The address of the same shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
   uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(local), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(r)
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t at, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "f"(a), "f"(b), "f"(c),
+               "f"(d)
                : "memory");
-  return v;
 }
 // A warp's 32 rows x 64 features (a row per lane) as bf16 into a 4 KB tile of
 // shared memory, 128-byte swizzled as the TMA store reads it: a thread's own
@@ -325,8 +329,9 @@ __device__ __forceinline__ float bias_at(const GemmArgs& a, int n) {
 // TMEM buffers, and warps 2-9 add the block's sums, times Sx of their row and
 // Sw of the tile, to fp32 sums in registers (a thread: one row, 64 features).
 // The weights' first stages are on their way before the quantisation ends.
-// A cluster's sums meet in shared memory: each CTA adds its share of the rows
-// over the CTAs in order and writes it.
+// A cluster's sums meet in shared memory: each CTA owns a share of the rows, the
+// others store theirs for it straight from registers, and it adds them in the
+// CTAs' order and writes the result.
 //
 // What bounds it, at M 4096, N 5120, K 2048 (53 us with the quantisation, 1.62
 // PFLOP/s): an SM takes in about 64 bytes per cycle, so the 32 KB of a block
@@ -339,7 +344,7 @@ __device__ __forceinline__ float bias_at(const GemmArgs& a, int n) {
 // but 880 cycles for the two buffers' way from MMA to registers and back
 // across the pair: 52.5 us).
 template <int SPLIT>
-__global__ void __launch_bounds__(kGemmThreads, 2)
+__global__ void __launch_bounds__(kGemmThreads, SPLIT > 1 ? 1 : 2)
 k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
               const __grid_constant__ CUtensorMap omap, const GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -368,6 +373,7 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (SPLIT > 1) cluster_arrive();  // (waited for before the exchange: every CTA has begun)
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
   float2 acc[32];  // warps 2-9
@@ -473,25 +479,27 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
       __syncwarp();
     }
   } else {
-    float* ex = reinterpret_cast<float*>(smem);  // [GM][G_PITCH]
+    constexpr int kRowsOf = GM / SPLIT;  // rows a CTA owns
+    float* ex = reinterpret_cast<float*>(smem + GSTAGES * G_STAGE);  // [SPLIT][kRowsOf][G_PITCH]
+    cluster_wait();
     if (warp >= 2) {
-      float* row = ex + (32 * (warp & 3) + lane) * G_PITCH + 64 * ((warp - 2) >> 2);
+      const int row = 32 * (warp & 3) + lane, col = 64 * ((warp - 2) >> 2);
+      const uint32_t to = in_cta(ex + (rank * kRowsOf + row % kRowsOf) * G_PITCH + col, row / kRowsOf);
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        *reinterpret_cast<float4*>(row + 4 * j) =
-            make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+        st_cluster(to + 16 * j, acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
     }
     __syncwarp();
-    cluster_sync();
-    constexpr int kRowsOf = GM / SPLIT;
+    cluster_arrive();
+    cluster_wait();
     for (int e = tid; e < kRowsOf * (GN / 8); e += kGemmThreads) {
-      const int r = rank * kRowsOf + e / (GN / 8), c8 = 8 * (e % (GN / 8));
+      const int lr = e / (GN / 8), r = rank * kRowsOf + lr, c8 = 8 * (e % (GN / 8));
       if (m0 + r >= a.M || n0 + c8 >= a.N) continue;
-      const uint32_t at = smem_u32(ex + r * G_PITCH + c8);
       float v[8] = {};
 #pragma unroll
       for (int p = 0; p < SPLIT; ++p) {
-        const float4 lo = ld_cluster(at, p), hi = ld_cluster(at + 16, p);
+        const float4* src = reinterpret_cast<const float4*>(ex + (p * kRowsOf + lr) * G_PITCH + c8);
+        const float4 lo = src[0], hi = src[1];
         v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
         v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
       }
@@ -502,8 +510,6 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
       *reinterpret_cast<uint4*>(a.out + (size_t)(m0 + r) * a.out_stride + n0 + c8) =
           make_uint4(o[0], o[1], o[2], o[3]);
     }
-    __syncwarp();
-    cluster_sync();  // the neighbours have read this CTA's sums
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -556,13 +562,13 @@ LinWs lin_ws(const moe_linear_dims& d) {
 template <int SPLIT>
 cudaError_t launch_gemm(const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& omap,
                         const GemmArgs& a, cudaStream_t s) {
-  cudaError_t err = ensure_smem((const void*)k_linear_gemm<SPLIT>, G_SMEM);
+  cudaError_t err = ensure_smem((const void*)k_linear_gemm<SPLIT>, g_smem(SPLIT));
   if (err != cudaSuccess) return err;
   count_launch();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(SPLIT, cdiv(a.N, GN), cdiv(a.M, GM));
   cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = G_SMEM;
+  cfg.dynamicSmemBytes = g_smem(SPLIT);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
