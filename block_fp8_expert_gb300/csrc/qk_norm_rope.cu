@@ -3,10 +3,13 @@
 #include <algorithm>
 
 #include "decoder_internal.h"
+#include "tcgen05.cuh"
 
 namespace moe {
 
 namespace {
+
+constexpr int kRing = 4;
 
 struct QkArgs {
   const uint16_t* qkv;
@@ -54,15 +57,17 @@ __device__ __forceinline__ void load_f32x8(const float* p, float* f) {
 // neighbours, which holds the interleaved pairs: a rotation needs no shuffle.
 // The mean of squares and the E4M3 maximum are butterflies over the head's
 // lanes.  A token's steps, those of the query heads before the key heads'
-// before the value heads', are dealt to `chunks` warps; a warp keeps two
-// steps' loads in flight, the first ones on their way before the token's
-// position and slot are known.
+// before the value heads', are dealt to `chunks` warps.  A lane's loads go
+// through a ring of its own in shared memory (cp.async: registers would hold
+// two steps ahead, the ring holds kRing), the first ones on their way before
+// the token's position and slot are known.
 template <int D>
 __global__ void __launch_bounds__(128)
 k_qk_norm_rope(const QkArgs a) {
   constexpr int LPH = D / 16;    // lanes per head
   constexpr int HPW = 32 / LPH;  // heads per warp and step
   constexpr unsigned kAll = 0xffffffffu;
+  __shared__ uint4 ring[kRing][2][128];
   griddep_wait();
   griddep_trigger();
   const int lane = threadIdx.x & 31;
@@ -82,17 +87,19 @@ k_qk_norm_rope(const QkArgs a) {
   struct Raw {
     uint4 a, b;
   };
-  auto load = [&](int s) {
-    Raw r{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (s >= steps) return r;
-    const int h = head_of(s);
-    if (h >= (s < sq ? Hq : Hkv)) return r;
-    const uint16_t* x = row + (size_t)(h + (s < sq ? 0 : s < sq + sk ? Hq : Hq + Hkv)) * D;
-    r.a = ldg_stream16(x + oa);
-    r.b = ldg_stream16(x + ob);
-    return r;
+  auto fetch = [&](int i) {  // the i-th of this warp's steps
+    const int s = ch + i * a.chunks;
+    if (s < steps) {
+      const int h = head_of(s);
+      const bool real = h < (s < sq ? Hq : Hkv);
+      const uint16_t* x = row + (real ? (size_t)(h + (s < sq ? 0 : s < sq + sk ? Hq : Hq + Hkv)) * D : 0);
+      tc::cp_async16_zfill(&ring[i % kRing][0][threadIdx.x], x + oa, real);
+      tc::cp_async16_zfill(&ring[i % kRing][1][threadIdx.x], x + ob, real);
+    }
+    cp_async_commit();
   };
-  Raw next0 = load(ch), next1 = load(ch + a.chunks);
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch(i);
 
   // the token's place: its position's rotation row and its cache slot
   const long long slot = a.slots[t];
@@ -186,10 +193,10 @@ k_qk_norm_rope(const QkArgs a) {
   };
   const bool e4m3 = a.c.format == MOE_KV_E4M3;
 #pragma unroll 1
-  for (int s = ch; s < steps; s += a.chunks) {
-    const Raw r = next0;
-    next0 = next1;
-    next1 = load(s + 2 * a.chunks);
+  for (int s = ch, i = 0; s < steps; s += a.chunks, ++i) {
+    fetch(i + kRing - 1);
+    cp_async_wait<kRing - 1>();  // (a lane reads what it copied itself)
+    const Raw r{ring[i % kRing][0][threadIdx.x], ring[i % kRing][1][threadIdx.x]};
     const int h = head_of(s);
     float x[16];
     if (s < sq) {

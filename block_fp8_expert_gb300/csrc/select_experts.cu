@@ -20,6 +20,13 @@ __device__ __forceinline__ float order_value(int key) {
   return __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF));
 }
 
+// 1 / (1 + exp(-l)); the reciprocal to 1 ulp.
+__device__ __forceinline__ float sigmoid_of(float l) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-l)));
+  return r;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -104,7 +111,7 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    float s = sigmoid ? __frcp_rn(1.f + expf(-l[i])) : l[i] * inv_sum;
+    float s = sigmoid ? sigmoid_of(l[i]) : l[i] * inv_sum;
     const bool real = e0 + i < E;
     if (bias && real) s += __ldg(bias + e0 + i);
     key[i] = real ? order_key(s) : INT_MIN;
@@ -244,7 +251,7 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
     for (int ks = 1; ks < slices; ++ks) my_v += __ldg(row + ks * slice_stride + my_idx);
     if (logit_bias) my_v += __ldg(logit_bias + my_idx);
   }
-  if (sigmoid) my_v = __frcp_rn(1.f + expf(-my_v));
+  if (sigmoid) my_v = sigmoid_of(my_v);
   // weights: the chosen scores, renormalised softmax as the softmax over the
   // chosen logits (the normaliser over all experts cancels)
   float w;
