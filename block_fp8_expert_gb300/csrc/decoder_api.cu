@@ -72,6 +72,7 @@ moe_status check_rule(const moe_select_rule& rule, int E, int k) {
 
 moe_status check_linear(const moe_linear_dims& d) {
   if (d.M < 0) return fail(MOE_ERR_INVALID_ARG, "M = %d < 0", d.M);
+  if (d.M > (1 << 22)) return fail(MOE_ERR_UNSUPPORTED, "M = %d: at most 2^22 rows", d.M);
   if (d.N < 8 || d.N > 65536 || d.N % 8)
     return fail(MOE_ERR_UNSUPPORTED, "N = %d: need a multiple of 8 in [8, 65536]", d.N);
   if (d.K < 16 || d.K > 65536 || d.K % 16)

@@ -194,7 +194,6 @@ constexpr int g_smem(int split) { return GSTAGES * G_STAGE + (split > 1 ? G_EXCH
 // The activation scales of a block's 128 rows ride with its stage, into a ring
 // of their own that is two slots longer: a stage is refilled once its MMAs are
 // done, when the sums of all but the last two blocks have been read (p_empty).
-constexpr int G_SX = 128 * 4;
 constexpr int GSX_SLOTS = GSTAGES + 2;
 constexpr int kProWarps = 8;
 constexpr int kGemmThreads = (2 + kProWarps) * 32;
@@ -246,6 +245,16 @@ __device__ __forceinline__ bool gwait(GemmShared& sh, uint64_t* bar, uint32_t pa
   return false;
 }
 
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
@@ -451,7 +460,7 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         uint32_t p[16];
-        tc::ld_32x32b_x16(t_lane + b * GN + 16 * h, p);
+        ld_32x32b_x16(t_lane + b * GN + 16 * h, p);
         tc::wait_ld();
         if (h == 3) {  // the next block but one may overwrite the buffer
           tc::fence_before_sync();
@@ -541,6 +550,32 @@ cudaError_t launch_stream(const LinArgs& a, cudaStream_t s) {
   return launch_k(k_linear_stream<NT, 4>, grid, dim3(128), 0, s, true, a);
 }
 
+// TMA map of the output [M, N], rows `stride` elements apart: 64 features x 32
+// rows per box, 128-byte swizzled.
+cudaError_t output_map(CUtensorMap* map, uint16_t* out, int M, int N, long long stride) {
+  using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const EncodeTiled encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiled>(fn)
+               : nullptr;
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M}, strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64, 32}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 struct LinWs {
   size_t codes, sxt, total;
   int ld;
@@ -605,8 +640,7 @@ cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const flo
                                 kScaleBlock, GM, 128)) != cudaSuccess ||
       (err = make_tensor_map_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, d.N, d.K,
                                 kScaleBlock, GN, 128)) != cudaSuccess ||
-      (err = make_tensor_map_2d(&omap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, d.M, d.N, 64, 32,
-                                128, d.out_stride)) != cudaSuccess)
+      (err = output_map(&omap, out, d.M, d.N, d.out_stride)) != cudaSuccess)
     return err;
   const long long groups = (long long)d.M * nkb;
   err = launch_k(k_linear_quant, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, s, true, x,

@@ -47,11 +47,10 @@ cudaError_t ensure_smem(const void* func, int bytes);
 
 // 2-D TMA map over a row-major matrix [rows, cols] of esize-byte elements:
 // box = box_cols x box_rows, swizzle 0, 64 or 128 bytes, L2 256-byte
-// promotion, out-of-range elements read as zero.  row_stride: elements from
-// one row to the next (0: cols).
+// promotion, out-of-range elements read as zero.
 cudaError_t make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, int esize,
                                const void* base, long long rows, int cols, int box_cols,
-                               int box_rows, int swizzle_bytes, long long row_stride = 0);
+                               int box_rows, int swizzle_bytes);
 
 // Largest expert count the library accepts.
 constexpr int kMaxExperts = 1024;

@@ -12,7 +12,8 @@ them (they are allocated otherwise).  Everything runs in libmoe_fp8.so on the
 current stream or the one given; tensors are checked for device, type, shape
 and layout here and for their sizes in the library.  What the kernels themselves
 find wrong in their data (a page number outside the cache, say) is recorded in
-``status``, a device array that ``check()`` reads after synchronising.
+``status``, a device array that ``check()`` reads after synchronising; it keeps
+what was recorded until ``status.zero_()``.
 """
 from __future__ import annotations
 

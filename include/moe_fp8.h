@@ -512,8 +512,8 @@ moe_status moe_paged_attention(const uint16_t* q, moe_kv_cache cache,
                                uint16_t* out, void* ws, size_t ws_bytes,
                                int32_t* status, void* stream);
 
-/* One moe_linear_fp8 call: x [M, K] -> out [M, N].  N a multiple of 8 and K
- * of 16, both at most 65536; x_stride, out_stride: elements between rows,
+/* One moe_linear_fp8 call: x [M, K] -> out [M, N].  M at most 2^22; N a
+ * multiple of 8 and K of 16, both at most 65536; x_stride, out_stride: elements between rows,
  * multiples of 8. */
 typedef struct {
   int32_t M, N, K;

@@ -101,7 +101,7 @@ def test_paged_attention_refusals(L, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(M=-1), INV), (dict(N=12), UNS), (dict(N=65544), UNS), (dict(K=8), UNS), (dict(K=136), UNS),
+    (dict(M=-1), INV), (dict(M=1 << 23), UNS), (dict(N=12), UNS), (dict(N=65544), UNS), (dict(K=8), UNS), (dict(K=136), UNS),
     (dict(xs=120), INV), (dict(xs=132), INV), (dict(os=60), INV), (dict(x=None), INV), (dict(x=P + 2), INV),
     (dict(codes=None), INV), (dict(scales=P + 4), INV), (dict(bias=P + 4), INV), (dict(out=None), INV),
     (dict(ws=None), INV), (dict(nws=0), WS), (dict(status=P + 4), INV)])
