@@ -43,8 +43,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 //            its lanes (ALIGNED: groups of 2^i EPL experts); other group sizes:
 //            per group two warp-wide integer max reductions.  A group's
 //            score is ranked against the others'; the kept groups are a mask;
-//   top-k    the k-th largest of the lanes' best keys bounds the k-th largest
-//            key from below.  The keys that reach it, seldom many more than k,
+//   top-k    the k-th largest of the lanes' best keys (k max reductions) bounds
+//            the k-th largest key from below.  The keys that reach it, seldom many more than k,
 //            are gathered one per lane and ranked against one another, ties to
 //            the lower expert; a lane's rank is its slot.  Where more than 32
 //            reach it (many equal keys), k rounds pick the largest remaining
@@ -192,22 +192,22 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
     hs = ts[0];
   };
   rescan();
-  __shared__ int2 s_pool[4][32];
-  int2* pool = s_pool[threadIdx.x >> 5];
+  __shared__ int4 s_key[4][8];
+  __shared__ int s_expert[4][32];
+  int* pool = reinterpret_cast<int*>(s_key[threadIdx.x >> 5]);
+  int* expert = s_expert[threadIdx.x >> 5];
   int my_idx = 0;
-  // the k-th largest best key (INT_MIN where fewer lanes have one)
-  pool[lane].x = hk;
-  __syncwarp();
-  int better = 0;
-#pragma unroll 8
-  for (int i = 0; i < 32; ++i) {
-    const int o = pool[i].x;
-    better += o > hk || (o == hk && i < lane);
+  // a bound: the k-th largest best key (lower where lanes tie; INT_MIN where
+  // fewer lanes have one)
+  int head = hk, bound = INT_MIN;
+  for (int j = 0; j < k; ++j) {
+    bound = __reduce_max_sync(kAll, head);
+    if (head == bound) head = INT_MIN;
   }
-  const int bound = __shfl_sync(kAll, hk, __ffs(__ballot_sync(kAll, better == k - 1)) - 1);
+  bound = max(bound, INT_MIN + 1);
   int mine = 0;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) mine += key[i] >= bound && key[i] != INT_MIN;
+  for (int i = 0; i < EPL; ++i) mine += key[i] >= bound;
   int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -215,23 +215,28 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
     if (lane >= o) upto += v;
   }
   const int n_pool = __shfl_sync(kAll, upto, 31);
-  __syncwarp();  // the best keys have been read
   if (n_pool <= 32) {
+    pool[lane] = INT_MIN;
+    __syncwarp();
     int w = upto - mine;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (key[i] >= bound && key[i] != INT_MIN) pool[w++] = make_int2(key[i], e0 + i);
+      if (key[i] >= bound) {
+        pool[w] = key[i];
+        expert[w++] = e0 + i;
+      }
     __syncwarp();
-    const int2 me = pool[lane];
-    int rank = 0;  // (the pool is in ascending order of experts)
-    for (int i = 0; i < n_pool; ++i) {
-      const int o = pool[i].x;
-      rank += o > me.x || (o == me.x && i < lane);
+    const int me = pool[lane], my_expert = expert[lane];
+    int rank = 0;  // (the pool is in ascending order of experts: of equal keys the earlier one wins)
+    for (int q = 0; 4 * q < n_pool; ++q) {
+      const int4 o = s_key[threadIdx.x >> 5][q];
+      rank += (o.x > me || (o.x == me && 4 * q < lane)) + (o.y > me || (o.y == me && 4 * q + 1 < lane)) +
+              (o.z > me || (o.z == me && 4 * q + 2 < lane)) + (o.w > me || (o.w == me && 4 * q + 3 < lane));
     }
     __syncwarp();
-    if (lane < n_pool && rank < k) pool[rank].y = me.y;
+    if (lane < n_pool && rank < k) expert[rank] = my_expert;
     __syncwarp();
-    if (lane < k) my_idx = pool[lane].y;
+    if (lane < k) my_idx = expert[lane];
   } else {
     for (int j = 0; j < k; ++j) {
       const int wk = __reduce_max_sync(kAll, hk);
