@@ -95,17 +95,25 @@ __device__ __forceinline__ int tile_at(const Span& s, int u) {
 }
 
 // A CTA's range of units, the sequence that holds its first one, and where
-// that sequence begins.
+// that sequence begins; and whether sequence number blockIdx.x is empty (its
+// output is zeros, written by this CTA).
 struct Place {
   int b, before, cur, end;
+  Span span;
+  int empty;
 };
 // Every thread of the CTA calls this.  share: 0 where each CTA has one part.
 __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s_place, int& share) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = cdiv(a.d.B, kWarps * 32), b0 = min(tid * per, a.d.B), b1 = min(b0 + per, a.d.B);
+  if (tid == 0) *s_place = Place{a.d.B, 0, 0, 0, Span{0, 0, 0, 0}, 0};
   uint2 mine = make_uint2(0u, 0u);  // units, parts
+  Span span{0, 0, 0, 0};            // of the last of this thread's sequences
+  bool empty = false;
   for (int b = b0; b < b1; ++b) {
-    const int u = units_of(span_of(a, b));
+    span = span_of(a, b);
+    empty |= b == (int)blockIdx.x && span.tiles == 0;
+    const int u = units_of(span);
     mine.x += u;
     mine.y += parts_of(u);
   }
@@ -119,7 +127,6 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
     }
   }
   if (lane == 31) s_scan[warp] = incl;
-  if (tid == 0) *s_place = Place{a.d.B, 0, 0, 0};
   __syncthreads();
   uint2 before = make_uint2(incl.x - mine.x, incl.y - mine.y), total = make_uint2(0u, 0u);
 #pragma unroll
@@ -139,24 +146,31 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
   // the first unit, or the part, that this CTA looks for
   const uint32_t want = own ? blockIdx.x : min((uint32_t)blockIdx.x * share, total.x);
   const uint32_t from = own ? before.y : before.x, len = own ? mine.y : mine.x;
+  if (empty) s_place->empty = 1;
   if (from * a.HG <= want && want < (from + len) * a.HG) {
     uint32_t at = from;
     int b = b0, u = 0, k = 0;
     for (; b < b1; ++b) {
-      u = units_of(span_of(a, b));
+      if (per > 1) span = span_of(a, b);
+      u = units_of(span);
       k = own ? parts_of(u) : u;
       if (want < (at + k) * a.HG) break;
       at += k;
       before.x += u;
     }
-    Place p{b, (int)(before.x * a.HG), (int)want, (int)min(want + share, total.x)};
+    const int first = (int)(before.x * a.HG);
+    s_place->b = b;
+    s_place->before = first;
+    s_place->span = span;
     if (own) {
-      const int hg = (int)(want - at * a.HG) / k, part = (int)(want - at * a.HG) % k;
-      const int s0 = p.before + hg * u;
-      p.cur = s0 + part * u / k;
-      p.end = s0 + (part + 1) * u / k;
+      const int hg = (int)(want - at * a.HG) / k, part = (int)(want - at * a.HG) - hg * k;
+      const int s0 = first + hg * u;
+      s_place->cur = s0 + part * u / k;
+      s_place->end = s0 + (part + 1) * u / k;
+    } else {
+      s_place->cur = (int)want;
+      s_place->end = (int)min(want + share, total.x);
     }
-    *s_place = p;
   }
   __syncthreads();
   return *s_place;
@@ -256,9 +270,10 @@ k_paged_attention(const AttnArgs a) {
   Place at = plan(a, s_scan, &s_place, share);
   int cur = at.cur;
   const int end = at.end;
-  // empty sequences answer zeros
-  for (int e = blockIdx.x; e < a.d.B; e += a.grid) {
-    if (span_of(a, e).tiles) continue;
+  // empty sequences answer zeros: the one of this CTA's number, and those
+  // beyond the grid
+  for (int e = at.empty ? blockIdx.x : blockIdx.x + a.grid; e < a.d.B; e += a.grid) {
+    if (e != (int)blockIdx.x && span_of(a, e).tiles) continue;
     uint4* row = reinterpret_cast<uint4*>(a.out + (size_t)e * a.d.out_stride);
     for (int i = tid; i < a.d.Hq * D / 8; i += kWarps * 32) row[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0 && a.seq_lens[e] != 0) raise_status(a.status, MOE_DEV_BAD_PAGE);
@@ -269,7 +284,7 @@ k_paged_attention(const AttnArgs a) {
     return;
   }
   int b = at.b;
-  Span sp = span_of(a, b);
+  Span sp = at.span;
   const int first_unit = cur;
   const float scale2 = a.d.scale * 1.44269504088896341f;
 

@@ -364,7 +364,7 @@ ATTN = [  # lens, Hq, Hkv, D, page_size, e4m3, window
     ([900, 33, 100], 8, 2, 128, 16, False, 100), ([900, 33, 100], 8, 2, 128, 3, True, 33),
     ([64] * 70, 6, 2, 64, 1, False, 0), ([20000], 8, 2, 128, 16, False, 0), ([20000], 8, 2, 128, 64, True, 0),
     ([70000, 3], 4, 1, 64, 64, False, 0), ([9000, 8999], 2, 2, 256, 16, False, 0),
-    ([30, 7] * 300, 2, 1, 64, 16, False, 0)]
+    ([30, 7] * 300, 2, 1, 64, 16, False, 0), ([0, 5, 0] * 250, 2, 1, 64, 16, True, 0)]
 
 
 @pytest.mark.parametrize("case", ATTN)
