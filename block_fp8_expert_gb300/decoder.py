@@ -79,7 +79,7 @@ class _Status:
 
     def __init__(self, device):
         self.status = torch.zeros(16, dtype=torch.int32, device=device)
-        self._status = self.status.data_ptr()
+        self._status, self._dev = self.status.data_ptr(), self.status.get_device()
 
     def check(self, stream=None) -> None:
         """Synchronise and raise MoeError if a kernel flagged its data."""
@@ -146,6 +146,8 @@ class ExpertSelector:
             topk_w = _new(stream, T, self.k, dtype=_F32, device=x.device)
         _dense(topk_idx, "topk_idx", _I32, T, self.k)
         _dense(topk_w, "topk_w", _F32, T, self.k)
+        if ws.get_device() != x.get_device() or not ws.is_contiguous():
+            raise ValueError("ws must be contiguous and on x's device")
         _lib.moe_route_select(x, layer.Wr, layer.bias, self.bias, self.rule, layer.dims(T),
                               topk_idx, topk_w, ws, stream)
         return topk_idx, topk_w
@@ -167,19 +169,21 @@ class PagedCache:
         dtype = _U8 if self.e4m3 else _BF16
         for t, name in ((k, "k"), (v, "v")):
             if not (t.is_cuda and t.dtype == dtype and t.dim() == 4 and t.shape == k.shape
-                    and t.stride(3) == 1):
-                _refuse(t, name, dtype, k.shape, layout=_ROWS)
+                    and t.stride(3) == 1 and t.get_device() == k.get_device()):
+                _refuse(t, name, dtype, k.shape, k.get_device(), _ROWS)
         if k.stride() != v.stride():
             raise ValueError(f"k and v have different strides: {k.stride()}, {v.stride()}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.Hkv, self.page_size, self.D = k.shape
+        self.device = k.get_device()
         ss = (0, 0, 0)
         if (k_scale is None) != (v_scale is None):
             raise ValueError("k_scale and v_scale come together")
         if self.e4m3:
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                if not (t.is_cuda and t.dtype == _F32 and t.shape == k.shape[:3]):
-                    _refuse(t, name, _F32, k.shape[:3])
+                if not (t.is_cuda and t.dtype == _F32 and t.shape == k.shape[:3]
+                        and t.get_device() == k.get_device()):
+                    _refuse(t, name, _F32, k.shape[:3], k.get_device())
             if k_scale.stride() != v_scale.stride():
                 raise ValueError("k_scale and v_scale have different strides")
             ss = k_scale.stride()
@@ -202,6 +206,11 @@ class PagedCache:
 
     def abi(self) -> _lib.KvCache:
         return self._abi
+
+    def refuse(self, Hkv: int, D: int, device: int) -> None:
+        """Raise for a use that needs other heads or another device."""
+        raise ValueError(f"the cache has {self.Hkv} heads of {self.D} on device {self.device}, "
+                         f"need {Hkv} of {D} on {device}")
 
 
 def rope_cos_sin(n_pos: int, rot: int, base: float = 1e6, factor: float = 1.0,
@@ -271,11 +280,11 @@ class QkNormRope(_Status):
         [T], slots int64 [T] (page * page_size + offset, or < 0 for padding)
         -> q_out bf16 [T, Hq, D]."""
         Hq, D, width = self.Hq, self.D, self.width
-        dev, T = qkv.get_device(), qkv.shape[0]
-        if dev < 0 or qkv.dtype != _BF16 or qkv.shape != (T, width) or qkv.stride(1) != 1:
-            _refuse(qkv, "qkv", _BF16, (T, width), layout=_ROWS)
-        if cache.Hkv != self.Hkv or cache.D != D:
-            raise ValueError(f"the cache has {cache.Hkv} heads of {cache.D}, need {self.Hkv} of {D}")
+        dev, T, xs = qkv.get_device(), qkv.shape[0], qkv.stride()
+        if dev != self._dev or qkv.dtype != _BF16 or qkv.shape != (T, width) or xs[-1] != 1:
+            _refuse(qkv, "qkv", _BF16, (T, width), self._dev, _ROWS)
+        if cache.Hkv != self.Hkv or cache.D != D or cache.device != dev:
+            cache.refuse(self.Hkv, D, dev)
         if (positions is None) != (self.cos_sin is None):
             raise ValueError("positions and the rotation table come together")
         if positions is not None and (positions.dtype != _I32 or positions.get_device() != dev
@@ -286,10 +295,11 @@ class QkNormRope(_Status):
             _refuse(slots, "slots", _I64, (T,), dev)
         if q_out is None:
             q_out = _new(stream, T, Hq, D, dtype=_BF16, device=qkv.device)
+        qs = q_out.stride()
         if (q_out.dtype != _BF16 or q_out.get_device() != dev or q_out.shape != (T, Hq, D)
-                or q_out.stride(2) != 1 or (Hq > 1 and q_out.stride(1) != D)):
+                or qs[2] != 1 or (Hq > 1 and qs[1] != D)):
             _refuse(q_out, "q_out", _BF16, (T, Hq, D), dev, _HEADS)
-        key = (T, qkv.stride(0), q_out.stride(0))
+        key = (T, xs[0], qs[0])
         if key != self._key:
             self._dims = _lib.QkDims(T, Hq, self.rot, int(self.interleaved), self.n_pos, self.eps,
                                      key[1] if T > 1 else width, key[2] if T > 1 else Hq * D)
@@ -327,27 +337,31 @@ class PagedAttention(_Status):
         """q bf16 [B, Hq, D], block_table int32 [B, pages per sequence],
         seq_lens int32 [B] (the new token included) -> out bf16 [B, Hq, D]."""
         Hq, D = self.Hq, self.D
-        dev, B = q.get_device(), q.shape[0]
-        if (dev < 0 or q.dtype != _BF16 or q.shape != (B, Hq, D) or q.stride(2) != 1
-                or (Hq > 1 and q.stride(1) != D)):
-            _refuse(q, "q", _BF16, (B, Hq, D), layout=_HEADS)
-        if cache.Hkv != self.Hkv or cache.D != D:
-            raise ValueError(f"the cache has {cache.Hkv} heads of {cache.D}, need {self.Hkv} of {D}")
-        width = block_table.shape[1]
-        if (block_table.dtype != _I32 or block_table.get_device() != dev
-                or block_table.shape != (B, width) or (width > 1 and block_table.stride(1) != 1)):
+        dev, B, qs = q.get_device(), q.shape[0], q.stride()
+        if (dev != self._dev or q.dtype != _BF16 or q.shape != (B, Hq, D) or qs[2] != 1
+                or (Hq > 1 and qs[1] != D)):
+            _refuse(q, "q", _BF16, (B, Hq, D), self._dev, _HEADS)
+        if cache.Hkv != self.Hkv or cache.D != D or cache.device != dev:
+            cache.refuse(self.Hkv, D, dev)
+        rows, width = block_table.shape
+        ts = block_table.stride()
+        if (block_table.dtype != _I32 or block_table.get_device() != dev or rows != B
+                or (width > 1 and ts[1] != 1)):
             _refuse(block_table, "block_table", _I32, (B, width), dev, _ROWS)
         if (seq_lens.dtype != _I32 or seq_lens.get_device() != dev or seq_lens.shape != (B,)
                 or not seq_lens.is_contiguous()):
             _refuse(seq_lens, "seq_lens", _I32, (B,), dev)
         if out is None:
             out = _new(stream, B, Hq, D, dtype=_BF16, device=q.device)
+        os = out.stride()
         if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (B, Hq, D)
-                or out.stride(2) != 1 or (Hq > 1 and out.stride(1) != D)):
+                or os[2] != 1 or (Hq > 1 and os[1] != D)):
             _refuse(out, "out", _BF16, (B, Hq, D), dev, _HEADS)
         if ws is None:
             ws = self.workspace(B, stream)
-        key = (B, width, block_table.stride(0), q.stride(0), out.stride(0))
+        elif ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError("ws must be contiguous and on the tensors' device")
+        key = (B, width, ts[0], qs[0], os[0])
         if key != self._key:
             row = Hq * D
             strides = key[2:] if B > 1 else (width, row, row)
@@ -390,17 +404,19 @@ class Fp8Linear(_Status):
                 ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """x bf16 [M, K] -> out bf16 [M, N]; rows of either may be strided."""
         N, K = self.N, self.K
-        dev, M = x.get_device(), x.shape[0]
-        if dev < 0 or x.dtype != _BF16 or x.shape != (M, K) or x.stride(1) != 1:
-            _refuse(x, "x", _BF16, (M, K), layout=_ROWS)
+        dev, M, xs = x.get_device(), x.shape[0], x.stride()
+        if dev != self._dev or x.dtype != _BF16 or x.shape != (M, K) or xs[-1] != 1:
+            _refuse(x, "x", _BF16, (M, K), self._dev, _ROWS)
         if out is None:
             out = _new(stream, M, N, dtype=_BF16, device=x.device)
-        if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (M, N)
-                or out.stride(1) != 1):
+        os = out.stride()
+        if out.dtype != _BF16 or out.get_device() != dev or out.shape != (M, N) or os[1] != 1:
             _refuse(out, "out", _BF16, (M, N), dev, _ROWS)
         if ws is None:
             ws = self.workspace(M, stream)
-        key = (M, x.stride(0), out.stride(0))
+        elif ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError("ws must be contiguous and on the tensors' device")
+        key = (M, xs[0], os[0])
         if key != self._key:
             self._dims = _lib.LinearDims(M, N, K, key[1] if M > 1 else K, key[2] if M > 1 else N)
             self._key = key

@@ -622,6 +622,10 @@ def test_python_side_checks(torch):
         dec.ExpertSelector(8, 2, "relu")
     with pytest.raises(TypeError):
         dec.ExpertSelector(8, 2).forward(torch.zeros(4, 8, device="cuda", dtype=torch.float64))
+    with pytest.raises(ValueError):
+        lin.forward(x, ws=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(_lib().MoeError):
+        lin.forward(x, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     c = dec.PagedCache.empty(2, 2, 16, 64)
     with pytest.raises(ValueError):
         dec.PagedCache(c.k, c.v.transpose(0, 1).contiguous().transpose(0, 1))
