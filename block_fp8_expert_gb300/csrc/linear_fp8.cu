@@ -30,6 +30,10 @@ struct LinArgs {
 // group: its maximum is two shuffles.  Codes become fp16 (exactly) and feed
 // mma.sync with fp32 accumulation; the block's two scales are applied to its
 // sums, and the warps' sums are added in a fixed order.
+// One row, N 5120, K 2048: 4.5 us in a graph (10.5 MB of codes take 1.6 at the
+// copy rate): launch, one round of loads per warp, the exchange.  8 rows 5.3,
+// 16 rows 7.8 us: every CTA quantises all of x for itself, which is what
+// hands over to the tensor-core kernel beyond.
 template <int NT, int kLinWarps>
 __global__ void __launch_bounds__(kLinWarps * 32)
 k_linear_stream(const LinArgs a) {

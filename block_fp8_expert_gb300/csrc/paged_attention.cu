@@ -245,6 +245,16 @@ __device__ __forceinline__ int v_chunk(int r, int j) {
 // memory by ldmatrix; E4M3 codes by 16-byte loads of a permuted order of the
 // dimensions (the same for q and k; free for the output) and an exact
 // conversion to fp16, the values' codes of two tokens paired by byte permutes.
+//
+// Bound by HBM once its pipelines are full: 2 x 131072 tokens, 4 heads of 128,
+// bf16: 537 MB in 89.5 us, 6.0 TB/s, 0.89 of the copy rate; what is lost is
+// the first 5 us (lengths, page numbers, rows: loads that wait for one
+// another), the SMs' uneven rates (the last ends 12% after the mean) and the
+// join.  64 ragged sequences up to 12000: 62.8 us; 48 up to 4096, E4M3: 28.0
+// us, 0.44 of the copy rate (the bytes alone take 12).  With the heads as the
+// MMA's M (half of it empty for eight heads): 93, 66.7 and 56.9 us.  One user
+// with 777 tokens: 7.4 us, all latency.  A warp runs its tiles without any
+// barrier: its own copies, its own maximum, one join per segment.
 template <int D, bool E4M3, int NH>
 __global__ void __launch_bounds__(kWarps * 32, AttnShape<D, E4M3, NH>::kCtasPerSm)
 k_paged_attention(const AttnArgs a) {

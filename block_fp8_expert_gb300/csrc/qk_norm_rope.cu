@@ -61,6 +61,11 @@ __device__ __forceinline__ void load_f32x8(const float* p, float* f) {
 // through a ring of its own in shared memory (cp.async: registers would hold
 // two steps ahead, the ring holds kRing), the first ones on their way before
 // the token's position and slot are known.
+// Bound by HBM from some thousand tokens on: T 8192, 32 + 4 + 4 heads of 128,
+// bf16: 172 MB in 30.9 us, 5.6 TB/s, 0.82 of the copy rate (with eight
+// dimensions per lane and shuffles for the partners 64.9; the loads in
+// registers 37.6; warps that walk over several tokens 39.7; a ring of 3 or
+// 6, or fewer registers for more warps, 34 to 47).  T 8: 2.2 us.
 template <int D>
 __global__ void __launch_bounds__(128)
 k_qk_norm_rope(const QkArgs a) {

@@ -50,6 +50,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 //            reach it (many equal keys), k rounds pick the largest remaining
 //            key each: a max reduction, the lowest lane that holds it wins and
 //            rescans its experts.
+// Bound by instruction issue, not by the 4 E bytes a token reads: T 8192, E
+// 256, sigmoid, 8 groups, k 8: 9.0 us (8.9 MB would take 1.3 at the copy
+// rate), of which 1.7 for the groups and 0.8 for k 8 instead of 1; k rounds
+// for the top-k alone: 13.5.  T 5: 3.5 us, launch and one warp's latency, so
+// the code is kept short (unrolled rank loops and a second exp: 4.8).
 // (twelve CTAs per SM where the registers allow it: 9.0 against 10.0 us at T
 // 8192, E 256, where latency and issue slots share the time)
 template <int EPL, bool ALIGNED>
