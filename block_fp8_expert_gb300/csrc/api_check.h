@@ -49,6 +49,15 @@ T* at(void* ws, size_t off) {
       return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p);    \
   } while (0)
 
+// For arrays that are read or written one element at a time.
+#define REQUIRE_ELEMENTS(p)                                                                 \
+  do {                                                                                      \
+    if ((p) == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", #p);                 \
+    if (reinterpret_cast<uintptr_t>(p) % sizeof(*(p)))                                      \
+      return fail(MOE_ERR_INVALID_ARG, "%s is not aligned to its %zu-byte elements", #p,    \
+                  sizeof(*(p)));                                                            \
+  } while (0)
+
 #define CUDA_CHECK(expr, where)                           \
   do {                                                    \
     cudaError_t e_ = (expr);                              \

@@ -31,8 +31,8 @@ moe_status check_cache(const moe_kv_cache& c) {
   if ((s = check_stride(c.head_stride, 0, m, "head_stride")) != MOE_OK) return s;
   if ((s = check_stride(c.token_stride, 0, m, "token_stride")) != MOE_OK) return s;
   if (f8) {
-    REQUIRE_PTR(c.k_scale);
-    REQUIRE_PTR(c.v_scale);
+    REQUIRE_ELEMENTS(c.k_scale);
+    REQUIRE_ELEMENTS(c.v_scale);
     if ((s = check_stride(c.scale_page_stride, 0, 1, "scale_page_stride")) != MOE_OK) return s;
     if ((s = check_stride(c.scale_head_stride, 0, 1, "scale_head_stride")) != MOE_OK) return s;
     if ((s = check_stride(c.scale_token_stride, 0, 1, "scale_token_stride")) != MOE_OK) return s;
@@ -102,8 +102,8 @@ moe_status moe_select_experts(const float* logits, int64_t row_stride, const flo
   if (T == 0) return MOE_OK;
   REQUIRE_PTR(logits);
   REQUIRE_OPT_PTR(bias);
-  REQUIRE_PTR(topk_idx);
-  REQUIRE_PTR(topk_w);
+  REQUIRE_ELEMENTS(topk_idx);
+  REQUIRE_ELEMENTS(topk_w);
   CUDA_CHECK(launch_select_experts(logits, row_stride, 1, 0, nullptr, bias, rule, T, E, k, topk_idx,
                                    topk_w, (cudaStream_t)stream),
              "moe_select_experts");
@@ -123,8 +123,8 @@ moe_status moe_route_select(const uint16_t* x, const float* Wr, const float* log
   REQUIRE_PTR(Wr);
   REQUIRE_OPT_PTR(logit_bias);
   REQUIRE_OPT_PTR(bias);
-  REQUIRE_PTR(topk_idx);
-  REQUIRE_PTR(topk_w);
+  REQUIRE_ELEMENTS(topk_idx);
+  REQUIRE_ELEMENTS(topk_w);
   REQUIRE_PTR(ws);
   if (ws_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", ws_bytes, need);
@@ -162,11 +162,11 @@ moe_status moe_qk_norm_rope(const uint16_t* qkv, const float* q_norm, const floa
   REQUIRE_PTR(qkv);
   if (d.rot > 0) {
     REQUIRE_PTR(cos_sin);
-    REQUIRE_PTR(pos);
+    REQUIRE_ELEMENTS(pos);
   } else if (cos_sin || pos) {
     return fail(MOE_ERR_INVALID_ARG, "rot = 0 takes no cos_sin and no pos");
   }
-  REQUIRE_PTR(slots);
+  REQUIRE_ELEMENTS(slots);
   REQUIRE_PTR(q_out);
   CUDA_CHECK(launch_qk_norm_rope(qkv, q_norm, k_norm, cos_sin, pos, slots, d, cache, q_out, status,
                                  (cudaStream_t)stream),
@@ -199,8 +199,8 @@ moe_status moe_paged_attention(const uint16_t* q, moe_kv_cache cache, const int3
   REQUIRE_OPT_PTR(status);
   if (d.B == 0) return MOE_OK;
   REQUIRE_PTR(q);
-  if (d.table_width > 0) REQUIRE_PTR(block_table);
-  REQUIRE_PTR(seq_lens);
+  if (d.table_width > 0) REQUIRE_ELEMENTS(block_table);
+  REQUIRE_ELEMENTS(seq_lens);
   REQUIRE_PTR(out);
   REQUIRE_PTR(ws);
   const size_t need = align_up(paged_attention_workspace(d, cache.D));

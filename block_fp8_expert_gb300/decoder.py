@@ -23,6 +23,7 @@ from typing import Optional
 import torch
 
 from . import _lib
+from .device import new_on
 
 _BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
                                 torch.uint8)
@@ -65,15 +66,6 @@ _ROWS = "the elements of a row must be contiguous"
 _HEADS = "the heads of a row must be contiguous"
 
 
-def _new(stream, *shape, dtype, device) -> torch.Tensor:
-    """A tensor that a call on `stream` may still be using when the caller has
-    dropped it: the allocator is told of a stream other than the current one."""
-    t = torch.empty(*shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    return t
-
-
 class _Status:
     """The device status word of one operator object."""
 
@@ -114,9 +106,9 @@ class ExpertSelector:
                 logits.stride(1) != 1 and E > 1):
             _refuse(logits, "logits", _F32, (T, E), layout=_ROWS)
         if topk_idx is None:
-            topk_idx = _new(stream, T, k, dtype=_I32, device=logits.device)
+            topk_idx = new_on(stream, T, k, dtype=_I32, device=logits.device)
         if topk_w is None:
-            topk_w = _new(stream, T, k, dtype=_F32, device=logits.device)
+            topk_w = new_on(stream, T, k, dtype=_F32, device=logits.device)
         if (topk_idx.dtype != _I32 or topk_idx.get_device() != dev or topk_idx.shape != (T, k)
                 or not topk_idx.is_contiguous()):
             _refuse(topk_idx, "topk_idx", _I32, (T, k), dev)
@@ -141,9 +133,9 @@ class ExpertSelector:
         if not x.is_cuda or x.dtype != _BF16 or x.shape != (T, layer.H) or not x.is_contiguous():
             _refuse(x, "x", _BF16, (T, layer.H))
         if topk_idx is None:
-            topk_idx = _new(stream, T, self.k, dtype=_I32, device=x.device)
+            topk_idx = new_on(stream, T, self.k, dtype=_I32, device=x.device)
         if topk_w is None:
-            topk_w = _new(stream, T, self.k, dtype=_F32, device=x.device)
+            topk_w = new_on(stream, T, self.k, dtype=_F32, device=x.device)
         _dense(topk_idx, "topk_idx", _I32, T, self.k)
         _dense(topk_w, "topk_w", _F32, T, self.k)
         if ws.get_device() != x.get_device() or not ws.is_contiguous():
@@ -294,7 +286,7 @@ class QkNormRope(_Status):
                 or not slots.is_contiguous()):
             _refuse(slots, "slots", _I64, (T,), dev)
         if q_out is None:
-            q_out = _new(stream, T, Hq, D, dtype=_BF16, device=qkv.device)
+            q_out = new_on(stream, T, Hq, D, dtype=_BF16, device=qkv.device)
         qs = q_out.stride()
         if (q_out.dtype != _BF16 or q_out.get_device() != dev or q_out.shape != (T, Hq, D)
                 or qs[2] != 1 or (Hq > 1 and qs[1] != D)):
@@ -328,7 +320,7 @@ class PagedAttention(_Status):
     def workspace(self, B: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to B sequences (of any length)."""
         d = _lib.AttnDims(B, self.Hq, 0, self.window, self.scale, 0, 0, 0)
-        return _new(stream, _lib.paged_attention_workspace_bytes(d, self.D), dtype=torch.uint8,
+        return new_on(stream, _lib.paged_attention_workspace_bytes(d, self.D), dtype=torch.uint8,
                     device=self.status.device)
 
     def forward(self, q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor,
@@ -352,7 +344,7 @@ class PagedAttention(_Status):
                 or not seq_lens.is_contiguous()):
             _refuse(seq_lens, "seq_lens", _I32, (B,), dev)
         if out is None:
-            out = _new(stream, B, Hq, D, dtype=_BF16, device=q.device)
+            out = new_on(stream, B, Hq, D, dtype=_BF16, device=q.device)
         os = out.stride()
         if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (B, Hq, D)
                 or os[2] != 1 or (Hq > 1 and os[1] != D)):
@@ -398,7 +390,7 @@ class Fp8Linear(_Status):
     def workspace(self, M: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to M rows."""
         n = _lib.linear_fp8_workspace_bytes(_lib.LinearDims(M, self.N, self.K, self.K, self.N))
-        return _new(stream, n, dtype=torch.uint8, device=self.codes.device)
+        return new_on(stream, n, dtype=torch.uint8, device=self.codes.device)
 
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
                 ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -408,7 +400,7 @@ class Fp8Linear(_Status):
         if dev != self._dev or x.dtype != _BF16 or x.shape != (M, K) or xs[-1] != 1:
             _refuse(x, "x", _BF16, (M, K), self._dev, _ROWS)
         if out is None:
-            out = _new(stream, M, N, dtype=_BF16, device=x.device)
+            out = new_on(stream, M, N, dtype=_BF16, device=x.device)
         os = out.stride()
         if out.dtype != _BF16 or out.get_device() != dev or out.shape != (M, N) or os[1] != 1:
             _refuse(out, "out", _BF16, (M, N), dev, _ROWS)

@@ -18,6 +18,22 @@ def _dev(a: np.ndarray, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(a)).to(device)
 
 
+def new_on(stream, *shape, dtype, device) -> torch.Tensor:
+    """An uninitialised tensor for a call on `stream` (None: the current one;
+    a torch stream or a raw handle).  It comes from that stream's memory, which
+    no earlier work of the current stream can still be using, and is kept from
+    reuse until the current stream's later work is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device) if stream
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 @dataclasses.dataclass
 class DeviceFfn:
     gate_codes: torch.Tensor
@@ -110,17 +126,14 @@ class DeviceLayer:
             raise ValueError("layers with a shared expert run through forward()")
         T = x.shape[0]
         d, P = self.dims(T), T * self.k
-        i32 = dict(dtype=torch.int32, device=x.device)
-        off, rows, slot_row = (torch.empty(n, **i32) for n in (self.E + 1, P, P))
-        y = torch.empty((P, self.H), dtype=torch.float32, device=x.device)
+        dev = x.device
+        off, rows, slot_row = (new_on(stream, n, dtype=torch.int32, device=dev)
+                               for n in (self.E + 1, P, P))
+        y = new_on(stream, P, self.H, dtype=torch.float32, device=dev)
         if out is None:
-            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device)
+            out = new_on(stream, T, self.H, dtype=torch.bfloat16, device=dev)
         if ws is None:
-            ws = self.workspace(T)
-        if stream is not None:  # the call may still use them when this returns
-            s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-            for t in (off, rows, slot_row, y, out, ws):
-                t.record_stream(s)
+            ws = new_on(stream, _lib.workspace_bytes(d), dtype=torch.uint8, device=dev)
         _lib.moe_permute(topk_idx, d, off, rows, slot_row, ws, stream)
         _lib.moe_expert_ffn_fp8(x, off, rows, self.routed.abi(), d, y, ws, stream)
         _lib.moe_combine(y, slot_row, topk_w, None, d, out, stream)

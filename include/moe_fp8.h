@@ -367,6 +367,9 @@ moe_status moe_read_device_status(const void* ws, int32_t* status,
  *  - Rows may be strided.  A row stride counts elements and is at least the
  *    row's length; the elements inside a row are contiguous, and every row
  *    starts on a 16-byte boundary where noted.
+ *  - topk_idx, topk_w, pos, slots, block_table, seq_lens, k_scale and v_scale
+ *    need the alignment of their elements only (a step's part of a longer
+ *    array will do); every other pointer is 16-byte aligned.
  * ---------------------------------------------------------------------------
  */
 
@@ -513,8 +516,8 @@ moe_status moe_paged_attention(const uint16_t* q, moe_kv_cache cache,
                                int32_t* status, void* stream);
 
 /* One moe_linear_fp8 call: x [M, K] -> out [M, N].  M at most 2^22; N a
- * multiple of 8 and K of 16, both at most 65536; x_stride, out_stride: elements between rows,
- * multiples of 8. */
+ * multiple of 8 and K of 16, both at most 65536; x_stride, out_stride:
+ * elements between rows, multiples of 8. */
 typedef struct {
   int32_t M, N, K;
   int64_t x_stride, out_stride;

@@ -170,3 +170,18 @@ def test_route_select_refusals(L, kw, code):
     r = _rule(groups=a["groups"], top_groups=1, group_top=1, score=a["score"])
     assert L.moe_route_select(a["x"], a["Wr"], a["logit_bias"], a["bias"], r, d, a["idx"], a["w"],
                               a["ws"], a["nws"], None) == code
+
+
+def test_arrays_of_elements_need_their_alignment_only(L):
+    """Half an element off is refused for every array that is read or written
+    one element at a time (a whole element off is taken on the GPU)."""
+    assert _select(L, idx=P + 2) == INV and _select(L, w=P + 2) == INV
+    d = _lib.AttnDims(2, 8, 4, 0, 0.1, 4, 8 * 128, 8 * 128)
+    f8 = dict(format=1, k_scale=P, v_scale=P)
+    for cache, table, lens in ((_cache(), P + 2, P), (_cache(), P, P + 2),
+                               (_cache(**{**f8, "k_scale": P + 2}), P, P),
+                               (_cache(**{**f8, "v_scale": P + 1}), P, P)):
+        assert L.moe_paged_attention(P, cache, table, lens, d, P, P, 1 << 30, None, None) == INV
+    q = _lib.QkDims(2, 8, 16, 0, 4, 1e-6, 12 * 128, 8 * 128)
+    for pos, slots in ((P + 2, P), (P, P + 4)):
+        assert L.moe_qk_norm_rope(P, None, None, P, pos, slots, q, _cache(), P, None, None) == INV

@@ -633,3 +633,72 @@ def test_python_side_checks(torch):
         dec.PagedAttention(4, 1, 64).forward(torch.zeros(1, 4, 64, device="cuda", dtype=torch.bfloat16), c,
                                              torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
                                              torch.ones(1, dtype=torch.int32, device="cuda"))
+
+
+def test_index_arrays_out_of_longer_ones(torch):
+    """Routings, positions, slots, lengths, a table's columns and a cache's
+    scales that begin anywhere in a longer array give the bits of a plain call."""
+    dec, g = _dec(), _gen(torch, 23)
+
+    def inside(t, room=3):  # a copy that begins 1 element into its buffer
+        buf = torch.empty(t.numel() + room, dtype=t.dtype, device="cuda")
+        part = buf[1:1 + t.numel()].view(t.shape)
+        part.copy_(t)
+        assert part.data_ptr() % 16
+        return part
+
+    lens = [40, 1, 0, 97]
+    B, Hkv, D, page = len(lens), 2, 64, 16
+    _, table, _, _ = _paged(torch, g, lens, Hkv, D, page, True)
+    qkv = torch.randn(B, 8 * D, generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    slots = torch.arange(B, device="cuda") * page
+    logits = torch.randn(B, 64, generator=g, device="cuda")
+    rope = dec.QkNormRope(4, Hkv, D, cos_sin=dec.rope_cos_sin(100, D))
+    attn = dec.PagedAttention(4, Hkv, D)
+    pick = dec.ExpertSelector(64, 3)
+    codes = torch.randint(0, 120, (2, 64, Hkv, page, D), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.rand(2, 64, Hkv, page, generator=g, device="cuda")
+    res = []
+    for f in (lambda t: t, inside):
+        cache = dec.PagedCache(codes[0].clone(), codes[1].clone(), f(scales[0]), f(scales[1]))
+        q = rope.forward(qkv, f(pos), f(slots), cache)
+        wide = torch.cat([table[:, :1], table], 1)
+        o = attn.forward(q, cache, table if f is not inside else wide[:, 1:], f(pos))
+        idx, w = pick.forward(logits, f(torch.zeros(B, 3, dtype=torch.int32, device="cuda")),
+                              f(torch.zeros(B, 3, device="cuda")))
+        res.append([q, o, idx, w, cache.k, cache.v, cache.k_scale, cache.v_scale])
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+    rope.check()
+    attn.check()
+
+
+def test_memory_of_a_call_on_another_stream(torch):
+    """What a call on another stream allocates does not come from memory that
+    the current stream has just let go of, which its work may still be using."""
+    dec = _dec()
+    x, codes, scales = _linear_case(torch, 300, 512, 256)
+    lin = dec.Fp8Linear(codes, scales)
+    plain = lin.forward(x)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        held = [torch.empty_like(plain), lin.workspace(300)]
+        gone = {t.data_ptr() for t in held}
+        del held
+        ws = lin.workspace(300, stream)
+        out = lin.forward(x, ws=ws, stream=stream)
+        side.synchronize()
+        assert not gone & {out.data_ptr(), ws.data_ptr()}
+        assert torch.equal(out, plain)
+    with torch.cuda.stream(side):  # and the default stream from another one
+        side.wait_stream(torch.cuda.default_stream())
+        held = torch.empty_like(plain)
+        gone = held.data_ptr()
+        del held
+        out = lin.forward(x, stream=0)
+        assert out.data_ptr() != gone
+    torch.cuda.synchronize()
+    assert torch.equal(out, plain)
+    lin.check()
