@@ -545,11 +545,15 @@ bool linear_streams(const moe_linear_dims& d) {
 template <int NT>
 cudaError_t launch_stream(const LinArgs& a, cudaStream_t s) {
   const dim3 grid(cdiv(a.N, 16), cdiv(a.M, 8 * NT));
-  // a warp per block of K up to 16, as long as every CTA runs at once
+  // a warp per block of K, up to 16 where an SM has one CTA, up to 8 where it
+  // has two, otherwise 4; more than 8 rows take 8, whose quantisation hides
+  // (N x K, 1 row: 2048 x 4096 5.4 / 4.0 / 3.5 us with 4 / 8 / 16 warps, 4096 x
+  // 2048 3.9 / 3.5 / 4.1, 5120 x 2048 4.5 / 4.8 / 5.5; 16 rows, 5120 x 2048:
+  // 8.7 / 7.3 / 8.9)
   const int nkb = cdiv(a.K, kScaleBlock), ctas = grid.x * grid.y;
-  if (ctas * 16 <= num_sms() * 16 && nkb > 8)
+  if (ctas <= num_sms() && nkb > 8)
     return launch_k(k_linear_stream<NT, 16>, grid, dim3(512), 0, s, true, a);
-  if (ctas * 8 <= num_sms() * 16 && nkb > 4)
+  if ((ctas <= 2 * num_sms() || NT > 1) && nkb > 4)
     return launch_k(k_linear_stream<NT, 8>, grid, dim3(256), 0, s, true, a);
   return launch_k(k_linear_stream<NT, 4>, grid, dim3(128), 0, s, true, a);
 }

@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kWarps = 4;     // warps per CTA, each with its own tiles and pipeline
 constexpr int kMaxRows = 16;  // query heads per CTA segment at most
-constexpr int kMinUnits = 8;  // least share of a CTA, in units (below)
+constexpr int kMinTiles = 8;  // least share of a CTA
 // What a segment costs a CTA beside its tiles (table and query loads, filling
 // and draining the pipeline, the join), in tiles.
 constexpr int kSegCost = 8;
@@ -81,17 +81,19 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
 // A sequence's tiles for one tile of heads are a segment of tiles + kSegCost
 // units; empty sequences have none.  All segments lie in one row, sequence-
 // major, then head.  Where there are CTAs enough to give every segment its own
-// parts of about kMinUnits, a CTA takes one such part.  Otherwise CTA c takes
-// units [c share, (c + 1) share) of the row, and with them the same part of
-// each segment's tiles, so ragged batches, many short sequences and a few long
-// ones alike, give every CTA the same time.  A segment that several CTAs hold
-// is joined by k_attn_join.  (Units fit 31 bits: the host checks.)
+// parts of at most kMinTiles tiles, or else of an even share and kSegCost, a
+// CTA takes one such part.  Otherwise CTA c takes units [c share, (c + 1)
+// share) of the row, and with them the same part of each segment's tiles, so
+// ragged batches, many short sequences and a few long ones alike, give every
+// CTA the same time.  A segment that several CTAs hold is joined by
+// k_attn_join.  (Units fit 31 bits: the host checks.)
 __device__ __forceinline__ int units_of(const Span& s) { return s.tiles ? s.tiles + kSegCost : 0; }
-__device__ __forceinline__ int parts_of(int units) { return (units + kMinUnits - 1) / kMinUnits; }
-// The tile at which unit u of a segment begins.
+__device__ __forceinline__ int parts_of(int tiles, int most) { return cdiv(tiles, most); }
+// The tile at which unit u of a segment begins, in fp32: the CTAs on either
+// side get the same answer, and it never falls as u grows.
 __device__ __forceinline__ int tile_at(const Span& s, int u) {
   const int units = units_of(s);
-  return u <= 0 ? 0 : u >= units ? s.tiles : (int)((long long)u * s.tiles / units);
+  return u <= 0 ? 0 : u >= units ? s.tiles : min(s.tiles, (int)(u * ((float)s.tiles / (float)units)));
 }
 
 // A CTA's range of units, the sequence that holds its first one, and where
@@ -102,8 +104,10 @@ struct Place {
   Span span;
   int empty;
 };
-// Every thread of the CTA calls this.  share: 0 where each CTA has one part.
-__device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s_place, int& share) {
+// Every thread of the CTA calls this.  share: 0 where each CTA has one part,
+// of at most `most` tiles.
+__device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s_place, int& share,
+                                      int& most) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = cdiv(a.d.B, kWarps * 32), b0 = min(tid * per, a.d.B), b1 = min(b0 + per, a.d.B);
   if (tid == 0) *s_place = Place{a.d.B, 0, 0, 0, Span{0, 0, 0, 0}, 0};
@@ -115,34 +119,48 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
     empty |= b == (int)blockIdx.x && span.tiles == 0;
     const int u = units_of(span);
     mine.x += u;
-    mine.y += parts_of(u);
+    mine.y += parts_of(span.tiles, kMinTiles);
   }
-  uint2 incl = mine;
+  uint2 before, total;
+  auto scan = [&](uint2* s) {
+    uint2 incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
-    if (lane >= o) {
-      incl.x += x;
-      incl.y += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+      if (lane >= o) {
+        incl.x += x;
+        incl.y += y;
+      }
     }
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  uint2 before = make_uint2(incl.x - mine.x, incl.y - mine.y), total = make_uint2(0u, 0u);
+    if (lane == 31) s[warp] = incl;
+    __syncthreads();
+    before = make_uint2(incl.x - mine.x, incl.y - mine.y);
+    total = make_uint2(0u, 0u);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const uint2 v = s_scan[w];
-    if (w < warp) {
-      before.x += v.x;
-      before.y += v.y;
+    for (int w = 0; w < kWarps; ++w) {
+      const uint2 v = s[w];
+      if (w < warp) {
+        before.x += v.x;
+        before.y += v.y;
+      }
+      total.x += v.x;
+      total.y += v.y;
     }
-    total.x += v.x;
-    total.y += v.y;
+    total.x *= a.HG;
+    total.y *= a.HG;
+  };
+  scan(s_scan);
+  most = kMinTiles;
+  share = max((uint32_t)kMinTiles, (total.x + a.grid - 1) / a.grid);
+  bool own = total.y <= (uint32_t)a.grid;
+  if (!own && a.d.B * a.HG * 4 >= a.grid) {  // (the same for every thread)
+    most = share + kSegCost;
+    mine.y = 0;
+    for (int b = b0; b < b1; ++b) mine.y += parts_of(per > 1 ? span_of(a, b).tiles : span.tiles, most);
+    scan(s_scan + kWarps);
+    own = total.y <= (uint32_t)a.grid;
   }
-  total.x *= a.HG;
-  total.y *= a.HG;
-  const bool own = total.y <= (uint32_t)a.grid;
-  share = own ? 0 : max((uint32_t)kMinUnits, (total.x + a.grid - 1) / a.grid);
+  if (own) share = 0;
   // the first unit, or the part, that this CTA looks for
   const uint32_t want = own ? blockIdx.x : min((uint32_t)blockIdx.x * share, total.x);
   const uint32_t from = own ? before.y : before.x, len = own ? mine.y : mine.x;
@@ -153,7 +171,7 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
     for (; b < b1; ++b) {
       if (per > 1) span = span_of(a, b);
       u = units_of(span);
-      k = own ? parts_of(u) : u;
+      k = own ? parts_of(span.tiles, most) : u;
       if (want < (at + k) * a.HG) break;
       at += k;
       before.x += u;
@@ -165,8 +183,9 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
     if (own) {
       const int hg = (int)(want - at * a.HG) / k, part = (int)(want - at * a.HG) - hg * k;
       const int s0 = first + hg * u;
-      s_place->cur = s0 + part * u / k;
-      s_place->end = s0 + (part + 1) * u / k;
+      const int each = u / k, more = u - each * k;  // the first `more` parts have a unit more
+      s_place->cur = s0 + part * each + min(part, more);
+      s_place->end = s0 + (part + 1) * each + min(part + 1, more);
     } else {
       s_place->cur = (int)want;
       s_place->end = (int)min(want + share, total.x);
@@ -265,7 +284,7 @@ k_paged_attention(const AttnArgs a) {
   constexpr int NI = kTile * LPR / 32;         // copies per lane and matrix
   constexpr int DPL = D == 64 ? 8 : 16;        // E4M3: dimensions per lane of the second product
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint2 s_scan[kWarps];
+  __shared__ uint2 s_scan[2 * kWarps];
   __shared__ Place s_place;
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ unsigned s_seen[kWarps][S::kStages];  // tokens of each stage that exist
@@ -276,8 +295,8 @@ k_paged_attention(const AttnArgs a) {
   const uint32_t stages = smem_u32(smem) + warp * S::kWarpBytes;
   uint2* const qshared = reinterpret_cast<uint2*>(smem + kWarps * S::kWarpBytes);
 
-  int share;
-  Place at = plan(a, s_scan, &s_place, share);
+  int share, most;
+  Place at = plan(a, s_scan, &s_place, share, most);
   int cur = at.cur;
   const int end = at.end;
   // empty sequences answer zeros: the one of this CTA's number, and those
@@ -722,7 +741,7 @@ k_paged_attention(const AttnArgs a) {
     }
     // a segment that begins here and goes on is joined from here
     if (cur == s0 && stop < s1)
-      job = make_int4(slot, share ? (s1 - 1) / share - (int)blockIdx.x + 1 : parts_of(units), b, hg);
+      job = make_int4(slot, share ? (s1 - 1) / share - (int)blockIdx.x + 1 : parts_of(sp.tiles, most), b, hg);
     __syncthreads();
     cur = stop;
   }
@@ -833,7 +852,7 @@ cudaError_t launch_attn_nh(AttnArgs& a, cudaStream_t s) {
   a.gtiles = cdiv(a.G, S::kRows);
   a.HG = a.c.Hkv * a.gtiles;
   // no more CTAs than the table could give parts
-  const long long most = attn_units(a.d, a.c, S::kRows, S::kTile) / kMinUnits + (long long)a.d.B * a.HG;
+  const long long most = attn_units(a.d, a.c, S::kRows, S::kTile) / kMinTiles + (long long)a.d.B * a.HG;
   a.grid = (int)std::max(1ll, std::min((long long)S::kCtasPerSm * num_sms(), most));
   err = launch_k(k_paged_attention<D, E4M3, NH>, dim3(a.grid), dim3(kWarps * 32), S::kSmem, s, true, a);
   if (err != cudaSuccess) return err;

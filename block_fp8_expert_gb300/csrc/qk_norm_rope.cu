@@ -246,6 +246,8 @@ cudaError_t launch_qk_norm_rope(const uint16_t* qkv, const float* q_norm, const 
   const int hpw = 512 / cache.D, steps = cdiv(d.Hq, hpw) + 2 * cdiv(cache.Hkv, hpw);
   // one step per warp while that leaves the SMs short of warps, then more
   // steps per warp, which saves the repeated loads of the token's rotation row
+  // (32 + 4 + 4 heads of 128; T 8: 2.2 us against 5.6 with all of a token's
+  // steps in one warp; T 8192: 31.4 against 58.5 with one step per warp)
   const long long want = (long long)num_sms() * 32;
   a.chunks = (int)std::min<long long>(steps, std::max<long long>(cdiv(steps, 16), want / d.T));
   const long long warps = (long long)d.T * a.chunks;
