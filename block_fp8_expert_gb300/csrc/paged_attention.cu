@@ -5,7 +5,11 @@
 //
 // in one pass over the cache with a running maximum m and sum l; the query
 // heads of one key/value head (padded to 16) share every cache element read.
+#include <unistd.h>
+
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 
 #include "decoder_internal.h"
 
@@ -57,7 +61,8 @@ struct AttnArgs {
   uint16_t* out;
   float* part_o;   // [2 * grid][kMaxRows][D]
   float* part_ml;  // [2 * grid][2][kMaxRows]
-  int4* jobs;      // [grid] what k_attn_join does for a CTA: {slot, parts, sequence, segment}
+  unsigned long long* arrived;  // [3][grid], of any content
+  unsigned long long call;      // this launch's number << 8
   int grid;
   int32_t* status;
 };
@@ -85,8 +90,8 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
 // CTA takes one such part.  Otherwise CTA c takes units [c share, (c + 1)
 // share) of the row, and with them the same part of each segment's tiles, so
 // ragged batches, many short sequences and a few long ones alike, give every
-// CTA the same time.  A segment that several CTAs hold is joined by
-// k_attn_join.  (Units fit 31 bits: the host checks.)
+// CTA the same time.  A segment that several CTAs hold is joined by the last
+// of them to be done.  (Units fit 31 bits: the host checks.)
 __device__ __forceinline__ int units_of(const Span& s) { return s.tiles ? s.tiles + kSegCost : 0; }
 __device__ __forceinline__ int parts_of(int tiles, int most) { return cdiv(tiles, most); }
 // The tile at which unit u of a segment begins, in fp32: the CTAs on either
@@ -100,7 +105,7 @@ __device__ __forceinline__ int tile_at(const Span& s, int u) {
 // that sequence begins; and whether sequence number blockIdx.x is empty (its
 // output is zeros, written by this CTA).
 struct Place {
-  int b, before, cur, end;
+  int b, before, cur, end, part;  // part: which one of its segment, where a CTA has one part
   Span span;
   int empty;
 };
@@ -110,7 +115,7 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
                                       int& most) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = cdiv(a.d.B, kWarps * 32), b0 = min(tid * per, a.d.B), b1 = min(b0 + per, a.d.B);
-  if (tid == 0) *s_place = Place{a.d.B, 0, 0, 0, Span{0, 0, 0, 0}, 0};
+  if (tid == 0) *s_place = Place{a.d.B, 0, 0, 0, 0, Span{0, 0, 0, 0}, 0};
   uint2 mine = make_uint2(0u, 0u);  // units, parts
   Span span{0, 0, 0, 0};            // of the last of this thread's sequences
   bool empty = false;
@@ -183,6 +188,7 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
     if (own) {
       const int hg = (int)(want - at * a.HG) / k, part = (int)(want - at * a.HG) - hg * k;
       const int s0 = first + hg * u;
+      s_place->part = part;
       const int each = u / k, more = u - each * k;  // the first `more` parts have a unit more
       s_place->cur = s0 + part * each + min(part, more);
       s_place->end = s0 + (part + 1) * each + min(part + 1, more);
@@ -193,6 +199,23 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
   }
   __syncthreads();
   return *s_place;
+}
+
+// The counters of arrivals lie in the workspace, which may hold anything.  A
+// counter counts while its upper 56 bits are this launch's number, which no
+// other launch of the process has, and which what else is there meets with a
+// chance of 2^-56.  Every CTA that will arrive readies the counter early: one
+// exchange is enough, for if it fails, another CTA's has succeeded.  The last
+// one to arrive leaves 0, which is no launch's number, for the next replay of
+// the same launch.
+__device__ __forceinline__ void ready_counter(unsigned long long* counter, unsigned long long call) {
+  const unsigned long long seen = __ldcg(counter);
+  if ((seen & ~0xFFull) != call) atomicCAS(counter, seen, call);
+}
+__device__ __forceinline__ bool last_of(unsigned long long* counter, unsigned n) {
+  const bool last = (atomicAdd(counter, 1ull) & 0xFFu) == n - 1;
+  if (last) __stcg(counter, 0ull);
+  return last;
 }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -252,6 +275,129 @@ __device__ __forceinline__ int v_chunk(int r, int j) {
   return D == 64 ? j ^ ((r >> 1) & 3) : j ^ (((r >> 1) & 3) << 1);
 }
 
+// Joins `count` parts, base, base + step, ..., of the segment that begins in
+// CTA c0: to `out` (count is all there is), or into the first one's slot.  A
+// thread owns four dimensions of a row, the parts are added in order.
+template <int D>
+__device__ __forceinline__ void add_parts(const AttnArgs& a, int c0, int slot0, int base, int step,
+                                          int count, int rows, uint16_t* out) {
+  constexpr int kAhead = 8, kBoth = 2;  // parts, and elements of a thread, on their way at once
+  constexpr int kThreads = kWarps * 32;
+  const int n = rows * (D / 4);
+  auto slot_of = [&](int i) { return (size_t)(base + i == 0 ? slot0 : 2 * (c0 + base + i * step)); };
+  for (int e0 = threadIdx.x; e0 < cdiv(n, kThreads) * kThreads; e0 += kBoth * kThreads) {
+    float M[kBoth], L[kBoth];
+    float4 acc[kBoth];
+#pragma unroll
+    for (int x = 0; x < kBoth; ++x) {
+      M[x] = -INFINITY;
+      L[x] = 0.f;
+      acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int i0 = 0; i0 < count; i0 += kAhead) {
+      float4 v[kBoth][kAhead];
+      float m[kBoth][kAhead], l[kBoth][kAhead];
+#pragma unroll
+      for (int x = 0; x < kBoth; ++x)
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int e = e0 + x * kThreads, r = e / (D / 4), d4 = e % (D / 4);
+          m[x][u] = -INFINITY;
+          l[x][u] = 0.f;
+          v[x][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i0 + u < count && e < n) {
+            const size_t sl = slot_of(i0 + u);
+            const float* ml = a.part_ml + sl * 2 * kMaxRows + r;
+            m[x][u] = __ldcg(ml);
+            l[x][u] = __ldcg(ml + kMaxRows);
+            v[x][u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (sl * kMaxRows + r) * D + 4 * d4));
+          }
+        }
+#pragma unroll
+      for (int x = 0; x < kBoth; ++x) {
+        float M2 = M[x];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) M2 = fmaxf(M2, m[x][u]);
+        const float Ms = M2 == -INFINITY ? 0.f : M2, f0 = exp2f(M[x] - Ms);
+        L[x] *= f0;
+        acc[x].x *= f0;
+        acc[x].y *= f0;
+        acc[x].z *= f0;
+        acc[x].w *= f0;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const float f = exp2f(m[x][u] - Ms);
+          L[x] = fmaf(l[x][u], f, L[x]);
+          acc[x].x = fmaf(v[x][u].x, f, acc[x].x);
+          acc[x].y = fmaf(v[x][u].y, f, acc[x].y);
+          acc[x].z = fmaf(v[x][u].z, f, acc[x].z);
+          acc[x].w = fmaf(v[x][u].w, f, acc[x].w);
+        }
+        M[x] = M2;
+      }
+    }
+    if (!out) __syncthreads();  // the rows' other threads have read their m and l
+#pragma unroll
+    for (int x = 0; x < kBoth; ++x) {
+      const int e = e0 + x * kThreads, r = e / (D / 4), d4 = e % (D / 4);
+      if (e >= n) continue;
+      if (out) {
+        const float inv = L[x] == 0.f ? 0.f : 1.f / L[x];
+        *reinterpret_cast<uint2*>(out + (size_t)r * D + 4 * d4) =
+            make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
+      } else {
+        const size_t sl = slot_of(0);
+        *reinterpret_cast<float4*>(a.part_o + (sl * kMaxRows + r) * D + 4 * d4) = acc[x];
+        if (d4 == 0) {
+          a.part_ml[sl * 2 * kMaxRows + r] = M[x];
+          a.part_ml[sl * 2 * kMaxRows + kMaxRows + r] = L[x];
+        }
+      }
+    }
+  }
+}
+
+// The CTA's part i of `parts` of a segment is in its slot.  The last CTA of
+// each kFan neighbouring parts adds these up, and the last of those the
+// groups: few parts to read for any one, and the same sums whoever comes last.
+// A CTA begins one segment that goes on and continues one at most, so the
+// counters of first groups, of other groups and of segments never meet.
+constexpr int kFan = 8;
+struct Parts {
+  int c0, slot0;     // the segment's first CTA, the slot of its part
+  int parts, first;  // its parts, the first one of this CTA's group
+  __device__ __forceinline__ int groups() const { return cdiv(parts, kFan); }
+  __device__ __forceinline__ int size() const { return min(kFan, parts - first); }
+  __device__ __forceinline__ unsigned long long* group_counter(const AttnArgs& a) const {
+    return a.arrived + (first ? a.grid : 0) + c0 + first;
+  }
+  __device__ __forceinline__ unsigned long long* segment_counter(const AttnArgs& a) const {
+    return a.arrived + 2 * a.grid + c0;
+  }
+};
+template <int D>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, const Parts& p, int rows,
+                                           uint16_t* out, int* s_last) {
+  const int groups = p.groups(), size = p.size();
+  auto arrive = [&](unsigned long long* counter, int n) {
+    __syncthreads();  // (one thread's fences around the arrival hold for what the barriers order)
+    if (threadIdx.x == 0) {
+      __threadfence();
+      *s_last = last_of(counter, n);
+      __threadfence();
+    }
+    __syncthreads();
+    return *s_last != 0;
+  };
+  if (size > 1) {
+    if (!arrive(p.group_counter(a), size)) return;
+    add_parts<D>(a, p.c0, p.slot0, p.first, 1, size, rows, groups == 1 ? out : nullptr);
+    if (groups == 1) return;
+  }
+  if (!arrive(p.segment_counter(a), groups)) return;
+  add_parts<D>(a, p.c0, p.slot0, 0, kFan, groups, rows, out);
+}
+
 }  // namespace
 
 // Both products take tokens or dimensions as the MMA's M and the query heads
@@ -285,6 +431,7 @@ k_paged_attention(const AttnArgs a) {
   constexpr int DPL = D == 64 ? 8 : 16;        // E4M3: dimensions per lane of the second product
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint2 s_scan[2 * kWarps];
+  __shared__ int s_last;
   __shared__ Place s_place;
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ unsigned s_seen[kWarps][S::kStages];  // tokens of each stage that exist
@@ -307,11 +454,7 @@ k_paged_attention(const AttnArgs a) {
     for (int i = tid; i < a.d.Hq * D / 8; i += kWarps * 32) row[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0 && a.seq_lens[e] != 0) raise_status(a.status, MOE_DEV_BAD_PAGE);
   }
-  int4 job = make_int4(0, 0, 0, 0);
-  if (cur >= end) {
-    if (tid == 0) a.jobs[blockIdx.x] = job;
-    return;
-  }
+  if (cur >= end) return;
   int b = at.b;
   Span sp = at.span;
   const int first_unit = cur;
@@ -418,6 +561,20 @@ k_paged_attention(const AttnArgs a) {
       const Spot next = look_up(j + 1);
       issue(j, spot);
       spot = next;
+    }
+    const bool whole = cur == s0 && stop == s1;
+    auto part_of = [&]() {
+      Parts p;
+      p.c0 = share ? s0 / share : (int)blockIdx.x - at.part;
+      p.slot0 = 2 * p.c0 + (share && s0 > p.c0 * share ? 1 : 0);
+      p.parts = share ? (s1 - 1) / share - p.c0 + 1 : parts_of(sp.tiles, most);
+      p.first = ((int)blockIdx.x - p.c0) / kFan * kFan;
+      return p;
+    };
+    if (!whole && warp == kWarps - 1 && lane < 2) {  // (its loads are on their way)
+      const Parts p = part_of();
+      if (lane == 0 ? p.size() > 1 : p.groups() > 1)
+        ready_counter(lane == 0 ? p.group_counter(a) : p.segment_counter(a), a.call);
     }
     float qf[NH][2];  // factor on the scores of heads 8 nh + 2 c + {0, 1}
 #pragma unroll
@@ -704,7 +861,6 @@ k_paged_attention(const AttnArgs a) {
         }
       }
     __syncthreads();
-    const bool whole = cur == s0 && stop == s1;
     const int slot = 2 * blockIdx.x + (s0 <= first_unit ? 0 : 1);
     for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
       const int r = e / (D / 4), d4 = e % (D / 4);
@@ -739,99 +895,34 @@ k_paged_attention(const AttnArgs a) {
         }
       }
     }
-    // a segment that begins here and goes on is joined from here
-    if (cur == s0 && stop < s1)
-      job = make_int4(slot, share ? (s1 - 1) / share - (int)blockIdx.x + 1 : parts_of(sp.tiles, most), b, hg);
     __syncthreads();
+    if (!whole)
+      join_parts<D>(a, part_of(), rows,
+                    a.out + (size_t)b * a.d.out_stride + (size_t)(hkv * a.G + row0) * D, &s_last);
     cur = stop;
   }
-  if (tid == 0) a.jobs[blockIdx.x] = job;
-}
-
-// Joins the parts of the segment that begins in CTA blockIdx.x of the
-// attention kernel and goes on in the next ones, two heads per CTA.  A thread
-// owns four dimensions of a head; groups of threads take every GP-th part
-// each, and the groups' sums are added in order.
-constexpr int kJoinThreads = 256, kJoinHeads = 2;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads)
-k_attn_join(const AttnArgs a) {
-  constexpr int E = kJoinHeads * D / 4, GP = kJoinThreads / E, kAhead = 8;
-  __shared__ float4 s_acc[GP][E];
-  __shared__ float s_m[GP][kJoinHeads], s_l[GP][kJoinHeads];
-  griddep_wait();
-  const int4 job = __ldcg(a.jobs + blockIdx.x);
-  const int n = job.y;
-  const int hkv = job.w / a.gtiles, row0 = (job.w % a.gtiles) * a.rows, rows = min(a.rows, a.G - row0);
-  if (n == 0 || (int)blockIdx.y * kJoinHeads >= rows) return;  // uniform
-  const int grp = threadIdx.x / E, el = threadIdx.x % E;
-  const int hr = el / (D / 4), r = blockIdx.y * kJoinHeads + hr, d4 = el % (D / 4);
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float f, float l, const float4& v) {
-    L = fmaf(l, f, L);
-    acc.x = fmaf(v.x, f, acc.x);
-    acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z);
-    acc.w = fmaf(v.w, f, acc.w);
-  };
-  for (int i0 = grp; i0 < n; i0 += kAhead * GP) {
-    float4 v[kAhead];
-    float m[kAhead], l[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u * GP;
-      const size_t sl = i == 0 ? (size_t)job.x : 2 * ((size_t)blockIdx.x + i);
-      m[u] = -INFINITY;
-      l[u] = 0.f;
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < n && r < rows) {
-        const float* ml = a.part_ml + sl * 2 * kMaxRows + r;
-        m[u] = __ldcg(ml);
-        l[u] = __ldcg(ml + kMaxRows);
-        v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (sl * kMaxRows + r) * D + 4 * d4));
-      }
-    }
-    float M2 = M;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) M2 = fmaxf(M2, m[u]);
-    const float Ms = M2 == -INFINITY ? 0.f : M2, f0 = exp2f(M - Ms);
-    L *= f0;
-    acc.x *= f0;
-    acc.y *= f0;
-    acc.z *= f0;
-    acc.w *= f0;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) add(exp2f(m[u] - Ms), l[u], v[u]);
-    M = M2;
-  }
-  s_acc[grp][el] = acc;
-  if (d4 == 0) {
-    s_m[grp][hr] = M;
-    s_l[grp][hr] = L;
-  }
-  __syncthreads();
-  if (grp || r >= rows) return;
-  M = s_m[0][hr];
-#pragma unroll
-  for (int x = 1; x < GP; ++x) M = fmaxf(M, s_m[x][hr]);
-  const float Ms = M == -INFINITY ? 0.f : M;
-  L = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int x = 0; x < GP; ++x) add(exp2f(s_m[x][hr] - Ms), s_l[x][hr], s_acc[x][el]);
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint2 r2;
-  r2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-  r2.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(a.out + (size_t)job.z * a.d.out_stride +
-                            (size_t)(hkv * a.G + row0 + r) * D + 4 * d4) = r2;
 }
 
 namespace {
 
 // The workspace is sized for the most CTAs per SM that any shape runs.
 int attn_max_grid() { return 3 * num_sms(); }
+
+// A number of 56 bits for a launch, counted up from where the process began.
+unsigned long long call_number() {
+  static std::atomic<unsigned long long> next{[] {
+    // (a mix of the time and the process, so that processes begin far apart)
+    unsigned long long x = (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() +
+                           ((unsigned long long)getpid() << 40);
+    x = (x ^ (x >> 31)) * 0xD6E8FEB86659FD93ull;
+    return x ^ (x >> 29);
+  }()};
+  unsigned long long n;
+  do {
+    n = next.fetch_add(1) & ((1ull << 56) - 1);
+  } while (n == 0);
+  return n;
+}
 
 // The most units that the block table has room for, with `rows` heads per
 // segment and `tile` tokens per tile.
@@ -854,10 +945,7 @@ cudaError_t launch_attn_nh(AttnArgs& a, cudaStream_t s) {
   // no more CTAs than the table could give parts
   const long long most = attn_units(a.d, a.c, S::kRows, S::kTile) / kMinTiles + (long long)a.d.B * a.HG;
   a.grid = (int)std::max(1ll, std::min((long long)S::kCtasPerSm * num_sms(), most));
-  err = launch_k(k_paged_attention<D, E4M3, NH>, dim3(a.grid), dim3(kWarps * 32), S::kSmem, s, true, a);
-  if (err != cudaSuccess) return err;
-  return launch_k(k_attn_join<D>, dim3(a.grid, cdiv(std::min(a.G, S::kRows), kJoinHeads)),
-                  dim3(kJoinThreads), 0, s, true, a);
+  return launch_k(k_paged_attention<D, E4M3, NH>, dim3(a.grid), dim3(kWarps * 32), S::kSmem, s, true, a);
 }
 
 template <int D, bool E4M3>
@@ -873,7 +961,8 @@ bool paged_attention_fits(const moe_attn_dims& d, const moe_kv_cache& cache) {
 
 size_t paged_attention_workspace(const moe_attn_dims&, int D) {
   const size_t slots = 2 * (size_t)attn_max_grid();
-  return slots * kMaxRows * ((size_t)D + 2) * sizeof(float) + attn_max_grid() * sizeof(int4);
+  return slots * kMaxRows * ((size_t)D + 2) * sizeof(float) +
+         3 * attn_max_grid() * sizeof(unsigned long long);
 }
 
 cudaError_t launch_paged_attention(const uint16_t* q, const moe_kv_cache& cache,
@@ -890,7 +979,8 @@ cudaError_t launch_paged_attention(const uint16_t* q, const moe_kv_cache& cache,
   a.out = out;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = a.part_o + 2 * (size_t)attn_max_grid() * kMaxRows * cache.D;
-  a.jobs = reinterpret_cast<int4*>(a.part_ml + 2 * (size_t)attn_max_grid() * 2 * kMaxRows);
+  a.arrived = reinterpret_cast<unsigned long long*>(a.part_ml + 2 * (size_t)attn_max_grid() * 2 * kMaxRows);
+  a.call = call_number() << 8;
   a.status = status;
   // t / page_size for 0 <= t < 2^31: with 2^(e-1) < page_size <= 2^e and mul =
   // ceil(2^(31+e) / page_size) < 2^32, floor(t mul / 2^(31+e)) is exact

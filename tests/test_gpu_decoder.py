@@ -702,3 +702,35 @@ def test_memory_of_a_call_on_another_stream(torch):
     torch.cuda.synchronize()
     assert torch.equal(out, plain)
     lin.check()
+
+
+@pytest.mark.parametrize("lens", [[777], [700, 90, 0, 333], [9000, 40], [40000], [130] * 60])
+def test_paged_attention_workspaces_of_any_content(torch, lens):
+    """Whatever the workspace holds, and however often a captured call is
+    replayed over it, the bits are those of the first call, which is checked."""
+    dec, g = _dec(), _gen(torch, 31)
+    Hq, Hkv, D, page = 8, 2, 64, 16
+    cache, table, kd, vd = _paged(torch, g, lens, Hkv, D, page, False)
+    B = len(lens)
+    q = torch.randn(B, Hq, D, generator=g, device="cuda").to(torch.bfloat16)
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    attn = dec.PagedAttention(Hq, Hkv, D)
+    ws = attn.workspace(B)
+    first = attn.forward(q, cache, table, sl, ws=ws)
+    ref, A = _ref_attention(torch, q, kd, vd, table, lens, page, attn.scale, 0)
+    _check(_np(first), _np(ref), _attn_tol(_np(ref), _np(A), False), str(lens))
+    graph, held = torch.cuda.CUDAGraph(), torch.empty_like(first)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        attn.forward(q, cache, table, sl, out=held, ws=ws)
+    for fill in (0, 0xFF, 0x7F, None, None, "own"):
+        if fill is None:
+            ws.random_(256)
+        elif fill != "own":  # (own: as the last call left it)
+            ws.fill_(fill)
+        assert torch.equal(attn.forward(q, cache, table, sl, ws=ws), first)
+        for _ in range(20):
+            held.zero_()
+            graph.replay()
+            assert torch.equal(held, first)
+    attn.check()
