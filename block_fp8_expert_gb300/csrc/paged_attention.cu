@@ -19,23 +19,28 @@ namespace {
 
 constexpr int kWarps = 4;     // warps per CTA, each with its own tiles and pipeline
 constexpr int kMaxRows = 16;  // query heads per CTA segment at most
-constexpr int kMinTiles = 8;  // least share of a CTA
+constexpr int kMinTiles = 8;  // least share of a CTA (one user, 8000 tokens: 11.2 us; 16: 12.9)
 // What a segment costs a CTA beside its tiles (table and query loads, filling
-// and draining the pipeline, the join), in tiles.
+// and draining the pipeline, the join), in tiles (0 would make 24.5 us, of 48
+// ragged sequences up to 4096, 35.7; 16: 27.9).
 constexpr int kSegCost = 8;
 // E4M3: the largest weight times value scale is held as 2^15, so that fp16
 // keeps weights down to 2^-39 of it (a long cache's many small ones)
 constexpr float kWTop = 15.f;
 
-// NH: groups of 8 query heads per CTA segment (the MMA's N).
+// NH: groups of 8 query heads per CTA segment (the MMA's N).  The figures are
+// of 48 ragged E4M3 sequences up to 4096 tokens, 32 + 4 heads of 128 (24.5 us),
+// and of two of 131072 with heads of 64 (33.5 us).
 template <int D, bool E4M3, int NH>
 struct AttnShape {
   static constexpr int kRows = 8 * NH;
   static constexpr int kRowBytes = E4M3 ? D : 2 * D;
-  // 16-token MMA tiles per step: about 8 KB of keys and values
+  // 16-token MMA tiles per step: about 8 KB of keys and values (half of that,
+  // MT = 1: 31.0 and 48.4 us)
   static constexpr int MT = kRowBytes >= 256 ? 1 : 2;
   static constexpr int kTile = 16 * MT;
   static constexpr int kStage = 2 * kTile * kRowBytes + (E4M3 ? 2 * kTile * 4 : 0);
+  // as many as the registers allow (two instead of three: 27.7 and 37.5 us)
   static constexpr int kCtasPerSm = D == 256 ? (E4M3 ? 2 : 1) : (NH == 1 ? 3 : 2);
   static constexpr int kStagesFit = (220 * 1024 / kCtasPerSm - (D == 256 ? 8192 * NH : 0)) / (kWarps * kStage);
   static constexpr int kStages = kStagesFit < 2 ? 2 : (kStagesFit > 6 ? 6 : kStagesFit);
@@ -86,8 +91,11 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
 // A sequence's tiles for one tile of heads are a segment of tiles + kSegCost
 // units; empty sequences have none.  All segments lie in one row, sequence-
 // major, then head.  Where there are CTAs enough to give every segment its own
-// parts of at most kMinTiles tiles, or else of an even share and kSegCost, a
-// CTA takes one such part.  Otherwise CTA c takes units [c share, (c + 1)
+// parts of at most kMinTiles tiles, or else (asked only where the sequences
+// may be many enough) of an even share and a little more, a CTA takes one such
+// part: no CTA pays for two segments (64 sequences up to 500 tokens: 12.1 us
+// against 15.5, 32 up to 2000: 18.4 against 21.7; but two of 131072 with heads
+// of 64: 34.9 against 33.5).  Otherwise CTA c takes units [c share, (c + 1)
 // share) of the row, and with them the same part of each segment's tiles, so
 // ragged batches, many short sequences and a few long ones alike, give every
 // CTA the same time.  A segment that several CTAs hold is joined by the last
@@ -159,7 +167,7 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
   share = max((uint32_t)kMinTiles, (total.x + a.grid - 1) / a.grid);
   bool own = total.y <= (uint32_t)a.grid;
   if (!own && a.d.B * a.HG * 4 >= a.grid) {  // (the same for every thread)
-    most = share + kSegCost;
+    most = share + max(kSegCost, share / 6);
     mine.y = 0;
     for (int b = b0; b < b1; ++b) mine.y += parts_of(per > 1 ? span_of(a, b).tiles : span.tiles, most);
     scan(s_scan + kWarps);
@@ -357,11 +365,14 @@ __device__ __forceinline__ void add_parts(const AttnArgs& a, int c0, int slot0, 
   }
 }
 
-// The CTA's part i of `parts` of a segment is in its slot.  The last CTA of
-// each kFan neighbouring parts adds these up, and the last of those the
-// groups: few parts to read for any one, and the same sums whoever comes last.
-// A CTA begins one segment that goes on and continues one at most, so the
-// counters of first groups, of other groups and of segments never meet.
+// A segment's parts are in their slots.  The last CTA of each kFan neighbouring
+// parts adds these up, and the last of those the groups: few parts to read for
+// any one, and the same sums whoever comes last.  A CTA begins one segment that
+// goes on and continues one at most, so the counters of first groups, of other
+// groups and of segments never meet.  (A second kernel for the joins: 27.4
+// against 24.5 us for 48 ragged sequences, 7.5 against 5.9 for 30 up to 200,
+// and 2 us of the host's time; but 10.0 against 11.2 for one user with 8000
+// tokens, whose 32 parts take two rounds here.  Groups of 16: 12.7.)
 constexpr int kFan = 8;
 struct Parts {
   int c0, slot0;     // the segment's first CTA, the slot of its part
@@ -415,11 +426,12 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Parts& p, in
 // bf16: 537 MB in 89.5 us, 6.0 TB/s, 0.89 of the copy rate; what is lost is
 // the first 5 us (lengths, page numbers, rows: loads that wait for one
 // another), the SMs' uneven rates (the last ends 12% after the mean) and the
-// join.  64 ragged sequences up to 12000: 62.8 us; 48 up to 4096, E4M3: 28.0
-// us, 0.44 of the copy rate (the bytes alone take 12).  With the heads as the
-// MMA's M (half of it empty for eight heads): 93, 66.7 and 56.9 us.  One user
-// with 777 tokens: 7.4 us, all latency.  A warp runs its tiles without any
-// barrier: its own copies, its own maximum, one join per segment.
+// join.  64 ragged sequences up to 12000: 59.8 us; 48 up to 4096, E4M3: 24.5
+// us, 0.51 of the copy rate (the bytes alone take 12).  (With the heads as the
+// MMA's M, half of it empty for eight heads, an earlier version took 93, 66.7
+// and 56.9 us, and 90, 61 and 41 as it is here.)  One user with 777 tokens: 7.7
+// us, all latency (100 tokens, which need no join: 5.1).  A warp runs its tiles
+// without any barrier: its own copies, its own maximum, one join per segment.
 template <int D, bool E4M3, int NH>
 __global__ void __launch_bounds__(kWarps * 32, AttnShape<D, E4M3, NH>::kCtasPerSm)
 k_paged_attention(const AttnArgs a) {
