@@ -423,7 +423,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Parts& p, in
 // conversion to fp16, the values' codes of two tokens paired by byte permutes.
 //
 // Bound by HBM once its pipelines are full: 2 x 131072 tokens, 4 heads of 128,
-// bf16: 537 MB in 89.5 us, 6.0 TB/s, 0.89 of the copy rate; what is lost is
+// bf16: 537 MB in 90.6 us, 5.9 TB/s, 0.88 of the copy rate; what is lost is
 // the first 5 us (lengths, page numbers, rows: loads that wait for one
 // another), the SMs' uneven rates (the last ends 12% after the mean) and the
 // join.  64 ragged sequences up to 12000: 59.8 us; 48 up to 4096, E4M3: 24.5
