@@ -61,8 +61,8 @@ template <int EPL, bool ALIGNED>
 __global__ void __launch_bounds__(128, EPL <= 8 ? 12 : 1)
 k_select_experts(const float* __restrict__ logits, long long row_stride, int slices,
                  long long slice_stride, const float* __restrict__ logit_bias,
-                 const float* __restrict__ bias, const moe_select_rule rule, int T, int E, int k,
-                 int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+                 const float* __restrict__ bias, const moe_select_rule rule, int n, int span_log2,
+                 int T, int E, int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
   constexpr unsigned kAll = 0xffffffffu;
   griddep_wait();
   griddep_trigger();
@@ -117,14 +117,27 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
     inv_sum = s == 0.f ? 0.f : 1.f / s;
   }
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    float s = sigmoid ? sigmoid_of(l[i]) : l[i] * inv_sum;
-    const bool real = e0 + i < E;
-    if (bias && real) s += __ldg(bias + e0 + i);
-    key[i] = real ? order_key(s) : INT_MIN;
+  for (int i = 0; i < EPL; ++i) l[i] = sigmoid ? sigmoid_of(l[i]) : l[i] * inv_sum;
+  if (bias) {
+    if (EPL % 4 == 0 && (E & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += 4)
+        if (e0 + i < E) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(bias + e0 + i));
+          l[i] += v.x;
+          l[(i + 1) % EPL] += v.y;
+          l[(i + 2) % EPL] += v.z;
+          l[(i + 3) % EPL] += v.w;
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (e0 + i < E) l[i] += __ldg(bias + e0 + i);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) key[i] = e0 + i < E ? order_key(l[i]) : INT_MIN;
   if (rule.groups > 1) {
-    const int n = E / rule.groups;
     auto sum_of = [&](int first, int second) {  // a group's score
       float v = first == INT_MAX ? NAN : order_value(first);
       if (rule.group_top == 2) v += second == INT_MAX ? NAN : order_value(second);
@@ -137,16 +150,15 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
         b = max(b, min(a, key[i]));
         a = max(a, key[i]);
       }
-      const int span = n / EPL;  // lanes of a group
-      for (int o = 1; o < span; o <<= 1) {
+      for (int o = 1; o < 1 << span_log2; o <<= 1) {  // the group's lanes
         const int oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
         b = max(max(b, ob), min(a, oa));
         a = max(a, oa);
       }
-      const int g = e0 / n, sk = g < rule.groups ? sum_of(a, b) : INT_MIN;
+      const int g = lane >> span_log2, sk = g < rule.groups ? sum_of(a, b) : INT_MIN;
       int better = 0;
       for (int h = 0; h < rule.groups; ++h) {
-        const int o = __shfl_sync(kAll, sk, h * span);
+        const int o = __shfl_sync(kAll, sk, h << span_log2);
         better += o > sk || (o == sk && h < g);
       }
       if (better >= rule.top_groups) {
@@ -294,15 +306,18 @@ cudaError_t launch_select_experts(const float* logits, long long row_stride, int
   const dim3 grid(cdiv(T, 4)), blk(128);
   int epl = 2;
   while (epl * 32 < E) epl *= 2;
+  // experts of a group, and the lanes that hold them
   const int n = E / rule.groups, span = n / epl;
   const bool aligned = n % epl == 0 && (span & (span - 1)) == 0;
-#define MOE_SELECT(EPLV)                                                                        \
-  return aligned ? launch_k(k_select_experts<EPLV, true>, grid, blk, 0, s, true, logits,        \
-                            row_stride, slices, slice_stride, logit_bias, bias, rule, T, E, k,  \
-                            topk_idx, topk_w)                                                   \
-                 : launch_k(k_select_experts<EPLV, false>, grid, blk, 0, s, true, logits,       \
-                            row_stride, slices, slice_stride, logit_bias, bias, rule, T, E, k,  \
-                            topk_idx, topk_w)
+  int span_log2 = 0;
+  while ((2 << span_log2) <= span) ++span_log2;
+#define MOE_SELECT(EPLV)                                                                       \
+  return aligned ? launch_k(k_select_experts<EPLV, true>, grid, blk, 0, s, true, logits,       \
+                            row_stride, slices, slice_stride, logit_bias, bias, rule, n,       \
+                            span_log2, T, E, k, topk_idx, topk_w)                              \
+                 : launch_k(k_select_experts<EPLV, false>, grid, blk, 0, s, true, logits,      \
+                            row_stride, slices, slice_stride, logit_bias, bias, rule, n,       \
+                            span_log2, T, E, k, topk_idx, topk_w)
   if (epl <= 2) MOE_SELECT(2);
   if (epl <= 4) MOE_SELECT(4);
   if (epl <= 8) MOE_SELECT(8);
