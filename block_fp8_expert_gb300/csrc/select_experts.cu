@@ -35,14 +35,13 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 }  // namespace
 
-// A warp per token; lane l holds experts l EPL .. l EPL + EPL - 1, so the
-// logits arrive in whole rows, all loads in flight at once, a group of experts
-// is a run of lanes, and nothing touches memory again before the k results.
+// A warp per token; every group of experts (all of them, where there is one
+// group) has a run of 2^span_log2 lanes, which hold EPL consecutive experts
+// each while there are some: the logits arrive in whole rows, all loads in
+// flight at once, and nothing touches memory again before the k results.
 //   scores   softmax: the row maximum and sum over the warp;
 //   groups   a lane's two largest keys, then the group's by a butterfly over
-//            its lanes (ALIGNED: groups of 2^i EPL experts); other group sizes:
-//            per group two warp-wide integer max reductions.  A group's
-//            score is ranked against the others'; the kept groups are a mask;
+//            its lanes; its score is ranked against the others';
 //   top-k    the k-th largest of the lanes' best keys (k max reductions) bounds
 //            the k-th largest key from below.  The keys that reach it, seldom many more than k,
 //            are gathered one per lane and ranked against one another, ties to
@@ -57,28 +56,29 @@ __device__ __forceinline__ float warp_sum(float v) {
 // the code is kept short (unrolled rank loops and a second exp: 4.8).
 // (twelve CTAs per SM where the registers allow it: 9.0 against 10.0 us at T
 // 8192, E 256, where latency and issue slots share the time)
-template <int EPL, bool ALIGNED>
+template <int EPL>
 __global__ void __launch_bounds__(128, EPL <= 8 ? 12 : 1)
 k_select_experts(const float* __restrict__ logits, long long row_stride, int slices,
                  long long slice_stride, const float* __restrict__ logit_bias,
                  const float* __restrict__ bias, const moe_select_rule rule, int n, int span_log2,
-                 int T, int E, int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+                 int T, int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
   constexpr unsigned kAll = 0xffffffffu;
   griddep_wait();
   griddep_trigger();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (t >= T) return;  // warp-uniform
-  const int e0 = lane * EPL;
+  const int g = lane >> span_log2, place = (lane & ((1 << span_log2) - 1)) * EPL;
+  const int e0 = g * n + place, count = g < rule.groups ? n - place : 0;  // (may be over EPL, or below 0)
   const float* row = logits + (size_t)t * row_stride;
   float l[EPL];
   int key[EPL];
   // 16-byte loads where rows and lanes allow them
-  if (EPL % 4 == 0 && (row_stride & 3) == 0 && (E & 3) == 0) {
+  if (EPL % 4 == 0 && (row_stride & 3) == 0 && (n & 3) == 0) {
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
-      const float4 v = e0 + i < E ? __ldg(reinterpret_cast<const float4*>(row + e0 + i))
-                                  : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      const float4 v = i < count ? __ldg(reinterpret_cast<const float4*>(row + e0 + i))
+                                 : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       l[i] = v.x;
       l[(i + 1) % EPL] = v.y;  // (% EPL: no such lane where EPL = 2)
       l[(i + 2) % EPL] = v.z;
@@ -86,18 +86,18 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) l[i] = e0 + i < E ? __ldg(row + e0 + i) : -INFINITY;
+    for (int i = 0; i < EPL; ++i) l[i] = i < count ? __ldg(row + e0 + i) : -INFINITY;
   }
   // the router's partial sums in order, then its bias
 #pragma unroll 1
   for (int ks = 1; ks < slices; ++ks)
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (e0 + i < E) l[i] += __ldg(row + ks * slice_stride + e0 + i);
+      if (i < count) l[i] += __ldg(row + ks * slice_stride + e0 + i);
   if (logit_bias) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (e0 + i < E) l[i] += __ldg(logit_bias + e0 + i);
+      if (i < count) l[i] += __ldg(logit_bias + e0 + i);
   }
   const bool sigmoid = rule.score == MOE_SCORE_SIGMOID;
   float vmax = 0.f, inv_sum = 0.f;  // softmax statistics
@@ -119,10 +119,10 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
 #pragma unroll
   for (int i = 0; i < EPL; ++i) l[i] = sigmoid ? sigmoid_of(l[i]) : l[i] * inv_sum;
   if (bias) {
-    if (EPL % 4 == 0 && (E & 3) == 0) {
+    if (EPL % 4 == 0 && (n & 3) == 0) {
 #pragma unroll
       for (int i = 0; i < EPL; i += 4)
-        if (e0 + i < E) {
+        if (i < count) {
           const float4 v = __ldg(reinterpret_cast<const float4*>(bias + e0 + i));
           l[i] += v.x;
           l[(i + 1) % EPL] += v.y;
@@ -132,63 +132,37 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
     } else {
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (e0 + i < E) l[i] += __ldg(bias + e0 + i);
+        if (i < count) l[i] += __ldg(bias + e0 + i);
     }
   }
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) key[i] = e0 + i < E ? order_key(l[i]) : INT_MIN;
+  for (int i = 0; i < EPL; ++i) key[i] = i < count ? order_key(l[i]) : INT_MIN;
   if (rule.groups > 1) {
     auto sum_of = [&](int first, int second) {  // a group's score
       float v = first == INT_MAX ? NAN : order_value(first);
       if (rule.group_top == 2) v += second == INT_MAX ? NAN : order_value(second);
       return order_key(v);
     };
-    if (ALIGNED) {
-      int a = INT_MIN, b = INT_MIN;  // the two largest keys: the lane's, then the group's
+    int a = INT_MIN, b = INT_MIN;  // the two largest keys: the lane's, then the group's
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        b = max(b, min(a, key[i]));
-        a = max(a, key[i]);
-      }
-      for (int o = 1; o < 1 << span_log2; o <<= 1) {  // the group's lanes
-        const int oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
-        b = max(max(b, ob), min(a, oa));
-        a = max(a, oa);
-      }
-      const int g = lane >> span_log2, sk = g < rule.groups ? sum_of(a, b) : INT_MIN;
-      int better = 0;
-      for (int h = 0; h < rule.groups; ++h) {
-        const int o = __shfl_sync(kAll, sk, h << span_log2);
-        better += o > sk || (o == sk && h < g);
-      }
-      if (better >= rule.top_groups) {
+    for (int i = 0; i < EPL; ++i) {
+      b = max(b, min(a, key[i]));
+      a = max(a, key[i]);
+    }
+    for (int o = 1; o < 1 << span_log2; o <<= 1) {
+      const int oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
+      b = max(max(b, ob), min(a, oa));
+      a = max(a, oa);
+    }
+    const int sk = g < rule.groups ? sum_of(a, b) : INT_MIN;
+    int better = 0;
+    for (int h = 0; h < rule.groups; ++h) {
+      const int o = __shfl_sync(kAll, sk, h << span_log2);
+      better += o > sk || (o == sk && h < g);
+    }
+    if (better >= rule.top_groups) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = INT_MIN;
-      }
-    } else {
-      int sk = INT_MIN;  // lane g: group g's score
-      for (int g = 0; g < rule.groups; ++g) {
-        int a = INT_MIN, b = INT_MIN;  // this lane's two largest keys of the group
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const int x = (unsigned)(e0 + i - g * n) < (unsigned)n ? key[i] : INT_MIN;
-          b = max(b, min(a, x));
-          a = max(a, x);
-        }
-        const int first = __reduce_max_sync(kAll, a);
-        const unsigned holders = __ballot_sync(kAll, a == first);
-        const int second = __reduce_max_sync(kAll, lane == __ffs(holders) - 1 ? b : a);
-        if (lane == g) sk = sum_of(first, second);
-      }
-      int better = 0;
-      for (int g = 0; g < rule.groups; ++g) {
-        const int o = __shfl_sync(kAll, sk, g);
-        better += o > sk || (o == sk && g < lane);
-      }
-      const unsigned kept = __ballot_sync(kAll, lane < rule.groups && better < rule.top_groups);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (e0 + i < E && !((kept >> ((e0 + i) / n)) & 1u)) key[i] = INT_MIN;
+      for (int i = 0; i < EPL; ++i) key[i] = INT_MIN;
     }
   }
   int hk, hs;  // the lane's best key and its place
@@ -304,26 +278,21 @@ cudaError_t launch_select_experts(const float* logits, long long row_stride, int
                                   const float* bias, const moe_select_rule& rule, int T, int E,
                                   int k, int32_t* topk_idx, float* topk_w, cudaStream_t s) {
   const dim3 grid(cdiv(T, 4)), blk(128);
-  int epl = 2;
-  while (epl * 32 < E) epl *= 2;
-  // experts of a group, and the lanes that hold them
-  const int n = E / rule.groups, span = n / epl;
-  const bool aligned = n % epl == 0 && (span & (span - 1)) == 0;
+  const int n = E / rule.groups;  // experts of a group
   int span_log2 = 0;
-  while ((2 << span_log2) <= span) ++span_log2;
-#define MOE_SELECT(EPLV)                                                                       \
-  return aligned ? launch_k(k_select_experts<EPLV, true>, grid, blk, 0, s, true, logits,       \
-                            row_stride, slices, slice_stride, logit_bias, bias, rule, n,       \
-                            span_log2, T, E, k, topk_idx, topk_w)                              \
-                 : launch_k(k_select_experts<EPLV, false>, grid, blk, 0, s, true, logits,      \
-                            row_stride, slices, slice_stride, logit_bias, bias, rule, n,       \
-                            span_log2, T, E, k, topk_idx, topk_w)
-  if (epl <= 2) MOE_SELECT(2);
-  if (epl <= 4) MOE_SELECT(4);
-  if (epl <= 8) MOE_SELECT(8);
-  if (epl <= 16) MOE_SELECT(16);
+  while (rule.groups * (2 << span_log2) <= 32) ++span_log2;
+#define MOE_SELECT(EPL)                                                                          \
+  if ((EPL << span_log2) >= n)                                                                   \
+  return launch_k(k_select_experts<EPL>, grid, blk, 0, s, true, logits, row_stride, slices,      \
+                  slice_stride, logit_bias, bias, rule, n, span_log2, T, k, topk_idx, topk_w)
+  MOE_SELECT(2);
+  MOE_SELECT(4);
+  MOE_SELECT(8);
+  MOE_SELECT(16);
   MOE_SELECT(32);
+  MOE_SELECT(64);  // (1024 experts in 17 groups: 60 for a lane)
 #undef MOE_SELECT
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace moe

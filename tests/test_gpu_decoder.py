@@ -734,3 +734,26 @@ def test_paged_attention_workspaces_of_any_content(torch, lens):
             graph.replay()
             assert torch.equal(held, first)
     attn.check()
+
+
+@pytest.mark.parametrize("E,groups,top_groups,group_top,k", [
+    (1020, 17, 9, 2, 8), (1020, 15, 4, 1, 32), (1023, 3, 2, 2, 10), (1023, 31, 7, 2, 5), (45, 9, 4, 2, 3),
+    (105, 7, 3, 1, 6), (160, 5, 2, 2, 8), (20, 20, 6, 1, 4), (992, 31, 31, 2, 30), (64, 2, 1, 2, 16)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_select_groups_of_any_size(torch, E, groups, top_groups, group_top, k, sigmoid):
+    rng = np.random.default_rng(E + groups)
+    c = dict(k=k, sigmoid=sigmoid, groups=groups, top_groups=top_groups, group_top=group_top, renorm=True,
+             scale=2.0)
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    l = _clear_rows((1.5 * rng.standard_normal((24, E))).astype(np.float32), bias, c)
+    assert len(l) > 4
+    idx, w = _ref_select(l, bias, **c)
+    sel = _dec().ExpertSelector(E, k, "sigmoid" if sigmoid else "softmax", torch.from_numpy(bias).cuda(),
+                                groups, top_groups, group_top, True, 2.0)
+    for pad in (0, 4, 5):  # rows on 16-byte boundaries or not
+        wide = torch.full((len(l), E + pad), math.nan, device="cuda")
+        wide[:, :E] = torch.from_numpy(l).cuda()
+        gi, gw = sel.forward(wide[:, :E])
+        assert np.array_equal(gi.cpu().numpy(), idx)
+        # exponentials and sums of fp32: some tens of roundings of each weight
+        _check(_np(gw), w, 2.0 ** -18 * np.abs(w), f"E {E}, {groups} groups")
