@@ -43,21 +43,21 @@ __device__ __forceinline__ float warp_sum(float v) {
 //   groups   a lane's two largest keys, then the group's by a butterfly over
 //            its lanes; its score is ranked against the others';
 //   top-k    the k-th largest of the lanes' best keys (k max reductions) bounds
-//            the k-th largest key from below.  The keys that reach it, seldom many more than k,
-//            are gathered one per lane and ranked against one another, ties to
-//            the lower expert; a lane's rank is its slot.  Where more than 32
-//            reach it (many equal keys), k rounds pick the largest remaining
-//            key each: a max reduction, the lowest lane that holds it wins and
-//            rescans its experts.
+//            the k-th largest key from below.  The keys that reach it, seldom
+//            many more than k, are gathered one per lane and ranked against
+//            one another, ties to the lower expert; a lane's rank is its slot.
+//            Where more than 32 reach it (many equal keys), k rounds pick the
+//            largest remaining key each: a max reduction, the lowest lane that
+//            holds it wins and looks its experts through again.
 // Bound by instruction issue, not by the 4 E bytes a token reads: T 8192, E
-// 256, sigmoid, 8 groups, k 8: 9.0 us (8.9 MB would take 1.3 at the copy
-// rate), of which 1.7 for the groups and 0.8 for k 8 instead of 1; k rounds
-// for the top-k alone: 13.5.  T 5: 3.5 us, launch and one warp's latency, so
-// the code is kept short (unrolled rank loops and a second exp: 4.8).
-// (twelve CTAs per SM where the registers allow it: 9.0 against 10.0 us at T
-// 8192, E 256, where latency and issue slots share the time)
+// 256, sigmoid, 8 groups, k 8: 7.1 us (8.9 MB would take 1.3 at the copy
+// rate), of which 1.1 for the groups and 0.9 for k 8 instead of 1; an earlier
+// version took 13.5 with k rounds for the top-k alone and 11.0 as it is here.
+// T 5: 2.8 us, launch and one warp's latency, so the code is kept short: what
+// is rare (NaN keys, lanes with fewer experts) stands in branches of its own,
+// and a group's lanes share its comparisons with the other groups.
 template <int EPL>
-__global__ void __launch_bounds__(128, EPL <= 8 ? 12 : 1)
+__global__ void __launch_bounds__(128)
 k_select_experts(const float* __restrict__ logits, long long row_stride, int slices,
                  long long slice_stride, const float* __restrict__ logit_bias,
                  const float* __restrict__ bias, const moe_select_rule rule, int n, int span_log2,
@@ -135,8 +135,25 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
         if (i < count) l[i] += __ldg(bias + e0 + i);
     }
   }
+  // order_key() of the keys, which are never -0, with what is rare set apart
+  bool nan = false;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) key[i] = i < count ? order_key(l[i]) : INT_MIN;
+  for (int i = 0; i < EPL; ++i) {
+    const int b = __float_as_int(l[i]);
+    key[i] = b ^ ((b >> 31) & 0x7FFFFFFF);
+    nan |= l[i] != l[i];
+  }
+  if (nan) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (l[i] != l[i]) key[i] = INT_MAX;
+  }
+  if (count < EPL) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (i >= count) key[i] = INT_MIN;
+  }
+  int hk = INT_MIN;  // the lane's best key
   if (rule.groups > 1) {
     auto sum_of = [&](int first, int second) {  // a group's score
       float v = first == INT_MAX ? NAN : order_value(first);
@@ -149,42 +166,30 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
       b = max(b, min(a, key[i]));
       a = max(a, key[i]);
     }
+    hk = a;
     for (int o = 1; o < 1 << span_log2; o <<= 1) {
       const int oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
       b = max(max(b, ob), min(a, oa));
       a = max(a, oa);
     }
     const int sk = g < rule.groups ? sum_of(a, b) : INT_MIN;
+    // the group's lanes share the comparisons with the others
     int better = 0;
-    for (int h = 0; h < rule.groups; ++h) {
-      const int o = __shfl_sync(kAll, sk, h << span_log2);
-      better += o > sk || (o == sk && h < g);
+    const int j = lane & ((1 << span_log2) - 1);
+    for (int h0 = 0; h0 < rule.groups; h0 += 1 << span_log2) {
+      const int h = h0 + j, o = __shfl_sync(kAll, sk, h << span_log2);
+      better += h < rule.groups && (o > sk || (o == sk && h < g));
     }
+    for (int o = 1; o < 1 << span_log2; o <<= 1) better += __shfl_xor_sync(kAll, better, o);
     if (better >= rule.top_groups) {
+      hk = INT_MIN;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) key[i] = INT_MIN;
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) hk = max(hk, key[i]);
   }
-  int hk, hs;  // the lane's best key and its place
-  auto rescan = [&]() {  // a tree, so that few of its steps wait for one another
-    int tk[EPL], ts[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      tk[i] = key[i];
-      ts[i] = i;
-    }
-#pragma unroll
-    for (int w = EPL / 2; w > 0; w /= 2)
-#pragma unroll
-      for (int i = 0; i < w; ++i) {
-        const bool up = tk[2 * i + 1] > tk[2 * i];  // equal keys: the lower expert
-        tk[i] = up ? tk[2 * i + 1] : tk[2 * i];
-        ts[i] = up ? ts[2 * i + 1] : ts[2 * i];
-      }
-    hk = tk[0];
-    hs = ts[0];
-  };
-  rescan();
   __shared__ int4 s_key[4][8];
   __shared__ int s_expert[4][32];
   int* pool = reinterpret_cast<int*>(s_key[threadIdx.x >> 5]);
@@ -234,12 +239,18 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
     for (int j = 0; j < k; ++j) {
       const int wk = __reduce_max_sync(kAll, hk);
       const int src = __ffs(__ballot_sync(kAll, hk == wk)) - 1;
+      int hs = 0;  // (of equal keys the lower expert)
+#pragma unroll
+      for (int i = EPL - 1; i >= 0; --i) hs = key[i] == hk ? i : hs;
       const int we = __shfl_sync(kAll, e0 + hs, src);
       if (lane == j) my_idx = we;
       if (lane == src) {
+        hk = INT_MIN;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = i == hs ? INT_MIN : key[i];
-        rescan();
+        for (int i = 0; i < EPL; ++i) {
+          if (i == hs) key[i] = INT_MIN;
+          hk = max(hk, key[i]);
+        }
       }
     }
   }
