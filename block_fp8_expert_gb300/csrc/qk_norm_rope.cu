@@ -10,6 +10,7 @@ namespace moe {
 namespace {
 
 constexpr int kRing = 4;
+constexpr int kCtasPerSm = 6;  // of 4 warps, as many as the registers allow
 
 struct QkArgs {
   const uint16_t* qkv;
@@ -65,9 +66,10 @@ __device__ __forceinline__ void load_f32x8(const float* p, float* f) {
 // bf16: 172 MB in 30.9 us, 5.6 TB/s, 0.82 of the copy rate (with eight
 // dimensions per lane and shuffles for the partners 64.9; the loads in
 // registers 37.6; warps that walk over several tokens 39.7; a ring of 3 or
-// 6, or fewer registers for more warps, 34 to 47).  T 8: 2.2 us.
+// 6, or fewer registers for more warps, 34 to 47).  T 517, 16 + 2 + 2 heads of
+// 256, E4M3: 5.7 us, T 8: 2.2, both latency: the token's place, then its heads.
 template <int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, kCtasPerSm)
 k_qk_norm_rope(const QkArgs a) {
   constexpr int LPH = D / 16;    // lanes per head
   constexpr int HPW = 32 / LPH;  // heads per warp and step
@@ -244,12 +246,15 @@ cudaError_t launch_qk_norm_rope(const uint16_t* qkv, const float* q_norm, const 
                                 int32_t* status, cudaStream_t s) {
   QkArgs a{qkv, q_norm, k_norm, cos_sin, pos, slots, d, cache, q_out, status, 1};
   const int hpw = 512 / cache.D, steps = cdiv(d.Hq, hpw) + 2 * cdiv(cache.Hkv, hpw);
-  // one step per warp while that leaves the SMs short of warps, then more
-  // steps per warp, which saves the repeated loads of the token's rotation row
-  // (32 + 4 + 4 heads of 128; T 8: 2.2 us against 5.6 with all of a token's
-  // steps in one warp; T 8192: 31.4 against 58.5 with one step per warp)
-  const long long want = (long long)num_sms() * 32;
-  a.chunks = (int)std::min<long long>(steps, std::max<long long>(cdiv(steps, 16), want / d.T));
+  // one step per warp while all of the warps run at once, then as many as keep
+  // it so, the same number for each; at most 16 steps per warp.  (32 + 4 + 4
+  // heads of 128: T 8 2.2 us, against 5.6 with all of a token's steps in one
+  // warp; T 8192 31.1, against 58.5 with one step per warp; T 700 4.1, against
+  // 5.6 with uneven warps, T 1000 5.4 against 7.0 with warps for a third more
+  // than can run.)
+  const long long resident = (long long)num_sms() * kCtasPerSm * 4;
+  a.chunks = (int)std::min<long long>(steps, std::max<long long>(cdiv(steps, 16), resident / d.T));
+  a.chunks = cdiv(steps, cdiv(steps, a.chunks));
   const long long warps = (long long)d.T * a.chunks;
   const dim3 grid((unsigned)((warps + 3) / 4)), blk(128);
   if (cache.D == 64) return launch_k(k_qk_norm_rope<64>, grid, blk, 0, s, true, a);
