@@ -31,9 +31,11 @@ struct LinArgs {
 // mma.sync with fp32 accumulation; the block's two scales are applied to its
 // sums, and the warps' sums are added in a fixed order.
 // One row, N 5120, K 2048: 4.5 us in a graph (10.5 MB of codes take 1.6 at the
-// copy rate): launch, one round of loads per warp, the exchange.  8 rows 5.3,
-// 16 rows 7.8 us: every CTA quantises all of x for itself, which is what
-// hands over to the tensor-core kernel beyond.
+// copy rate): launch, one round of loads per warp, the exchange.  8 rows 4.8,
+// 16 rows 7.3 us: every CTA quantises all of x for itself, which is what
+// hands over to the tensor-core kernel beyond.  All four blocks' loads of a
+// warp at once take as long; a ring of cp.async copies twice as long, since
+// every CTA then brings its x in from L2 instead of the SM's first level.
 template <int NT, int kLinWarps>
 __global__ void __launch_bounds__(kLinWarps * 32)
 k_linear_stream(const LinArgs a) {
@@ -534,12 +536,15 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
 
 namespace {
 
-// The streamed kernel up to 16 rows (N 5120, K 2048: 5.0 - 8.1 us against
-// 8.0 - 8.7 on tcgen05), and with more where its CTAs of 16 features x 32 rows
-// all run at once over a short K (M 64, N 640, K 512: 3.2 against 5.4 us; but
-// M 24, N 2048, K 4096: 9.4 against 9.0, M 24, N 5120, K 2048: 14.6 against 8.5).
+// The streamed kernel up to 8 rows (N 5120, K 2048: 4.6 - 4.8 us against 8.5 on
+// tcgen05), up to 16 where the weights are few (N 5120, K 2048: 7.3 against 8.6,
+// but K 4096: 13.0 against 11.6 - 12.3, and N 10240, K 2048: 11.4 against 9.5),
+// and with more where its CTAs of 16 features x 32 rows all run at once over a
+// short K (M 64, N 640, K 512: 3.2 against 5.4 us; but M 24, N 2048, K 4096: 9.4
+// against 9.0, M 24, N 5120, K 2048: 14.6 against 8.5).
 bool linear_streams(const moe_linear_dims& d) {
-  return d.M <= 16 || (d.K <= 2048 && cdiv(d.N, 16) * (long long)cdiv(d.M, 32) <= num_sms());
+  return d.M <= 8 || (d.M <= 16 && (long long)d.N * d.K <= (1 << 24)) ||
+         (d.K <= 2048 && cdiv(d.N, 16) * (long long)cdiv(d.M, 32) <= num_sms());
 }
 
 template <int NT>

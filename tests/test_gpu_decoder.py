@@ -757,3 +757,14 @@ def test_select_groups_of_any_size(torch, E, groups, top_groups, group_top, k, s
         assert np.array_equal(gi.cpu().numpy(), idx)
         # exponentials and sums of fp32: some tens of roundings of each weight
         _check(_np(gw), w, 2.0 ** -18 * np.abs(w), f"E {E}, {groups} groups")
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 8200, 2048), (16, 8192, 2048), (16, 8192, 2064), (12, 4112, 4112)])
+def test_linear_where_sixteen_rows_change_kernels(torch, M, N, K):
+    """Either side of 2^24 weights with 9 to 16 rows."""
+    x, codes, scales = _linear_case(torch, M, N, K)
+    lin = _dec().Fp8Linear(codes, scales)
+    out = lin.forward(x)
+    lin.check()
+    ref, S = _ref_linear(torch, x, codes, scales)
+    _check(_np(out), ref, _linear_tol(ref, S), f"{M} x {N} x {K}")
