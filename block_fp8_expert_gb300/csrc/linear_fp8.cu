@@ -607,27 +607,50 @@ LinWs lin_ws(const moe_linear_dims& d) {
   return w;
 }
 
+// One launch of the GEMM, attributes and all.
+struct GemmLaunch {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  GemmLaunch(int split, int tiles_n, int tiles_m, cudaStream_t s) {
+    cfg.gridDim = dim3(split, tiles_n, tiles_m);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = g_smem(split);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+  }
+};
 template <int SPLIT>
 cudaError_t launch_gemm(const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& omap,
                         const GemmArgs& a, cudaStream_t s) {
   cudaError_t err = ensure_smem((const void*)k_linear_gemm<SPLIT>, g_smem(SPLIT));
   if (err != cudaSuccess) return err;
   count_launch();
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(SPLIT, cdiv(a.N, GN), cdiv(a.M, GM));
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = g_smem(SPLIT);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = SPLIT;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = SPLIT > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_linear_gemm<SPLIT>, xmap, wmap, omap, a);
+  const GemmLaunch l(SPLIT, cdiv(a.N, GN), cdiv(a.M, GM), s);
+  return cudaLaunchKernelEx(&l.cfg, k_linear_gemm<SPLIT>, xmap, wmap, omap, a);
+}
+// Clusters of SPLIT that the GPU holds at once (fewer than its SMs / SPLIT,
+// where its clusters of SMs are no multiples of it).
+template <int SPLIT>
+int clusters_at_once() {
+  static const int n = [] {
+    int most = 0;
+    GemmLaunch l(SPLIT, 1, 1, nullptr);
+    l.cfg.numAttrs = 1;
+    l.cfg.attrs = l.attr + 1;
+    if (ensure_smem((const void*)k_linear_gemm<SPLIT>, g_smem(SPLIT)) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&most, k_linear_gemm<SPLIT>, &l.cfg) == cudaSuccess)
+      return most;
+    cudaGetLastError();
+    return 0;
+  }();
+  return n;
 }
 
 }  // namespace
@@ -661,12 +684,15 @@ cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const flo
   if (err != cudaSuccess) return err;
   const GemmArgs a{sxt, l.ld, w.scales, bias, out, d.out_stride, d.M, d.N, nkb, status};
   const int tiles = cdiv(d.M, GM) * cdiv(d.N, GN);
-  // K divided while that leaves one CTA per SM and four blocks per CTA: clusters
-  // of four, two CTAs per SM take longer to place than they save (M 203, N 2048,
-  // K 4096: 15.8 / 12.7 / 11.7 / 19.3 us with 1 / 2 / 4 / 8 CTAs per tile; M 1000,
-  // N 2048, K 2048, 128 tiles: 11.4 / 13.8 us with 1 / 2)
+  // K divided while all clusters run at once, one CTA per SM, and a CTA has four
+  // blocks: clusters of four, two CTAs per SM take longer to place than they
+  // save (M 203, N 2048, K 4096: 15.8 / 12.7 / 11.7 / 19.3 us with 1 / 2 / 4 / 8
+  // CTAs per tile; M 1000, N 2048, K 2048, 128 tiles: 11.4 / 13.8 us with 1 / 2;
+  // M 64, N 4864, K 2048, 38 tiles: 9.1 / 14.5 with 2 / 4, as 38 clusters of 4
+  // do not fit)
   int split = 1;
-  while (split < 4 && tiles * split * 2 <= num_sms() && nkb >= 8 * split) split *= 2;
+  if (tiles <= clusters_at_once<2>() && nkb >= 8) split = 2;
+  if (tiles <= clusters_at_once<4>() && nkb >= 16) split = 4;
   if (split == 1) return launch_gemm<1>(xmap, wmap, omap, a, s);
   if (split == 2) return launch_gemm<2>(xmap, wmap, omap, a, s);
   return launch_gemm<4>(xmap, wmap, omap, a, s);

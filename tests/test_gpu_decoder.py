@@ -768,3 +768,14 @@ def test_linear_where_sixteen_rows_change_kernels(torch, M, N, K):
     lin.check()
     ref, S = _ref_linear(torch, x, codes, scales)
     _check(_np(out), ref, _linear_tol(ref, S), f"{M} x {N} x {K}")
+
+
+@pytest.mark.parametrize("M,N", [(40, 4864), (150, 2432), (64, 4352), (33, 9728)])
+def test_linear_around_a_wave_of_clusters(torch, M, N):
+    """Tile counts near those at which K is divided over fewer CTAs."""
+    x, codes, scales = _linear_case(torch, M, N, 2048, seed=3)
+    lin = _dec().Fp8Linear(codes, scales)
+    out = lin.forward(x)
+    lin.check()
+    ref, S = _ref_linear(torch, x, codes, scales)
+    _check(_np(out), ref, _linear_tol(ref, S), f"{M} x {N}")
