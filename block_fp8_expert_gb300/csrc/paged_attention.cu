@@ -268,6 +268,17 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// Two softmax weights as the sum of two bf16 pairs: hi their leading 8 bits, lo
+// the rest, rounded (2^-16 of the weight).  The lo of a weight that is not zero
+// is at least 2^-126, so that an infinite value meets no zero.
+__device__ __forceinline__ float low_part(float a) {
+  return fmaxf(a - bf16_hi(__float_as_uint(a)), fminf(a, 0x1p-126f));
+}
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  lo = pack_bf16x2(low_part(a), low_part(b));
+}
+
 // Where 16-byte chunk j of token row r lies in its tile.  bf16: the eight
 // rows of one ldmatrix fall on eight different chunks of a 128-byte line.
 // E4M3 keys: a quarter-warp reads four neighbouring chunks of two rows;
@@ -421,6 +432,12 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Parts& p, in
 // memory by ldmatrix; E4M3 codes by 16-byte loads of a permuted order of the
 // dimensions (the same for q and k; free for the output) and an exact
 // conversion to fp16, the values' codes of two tokens paired by byte permutes.
+// A weight rounded to bf16 once would be as far off as the output's own
+// rounding (2 x 131072 tokens: 1.95e-3 of the 64-bit result instead of 1.64e-3),
+// so bf16 values are multiplied by it in two parts (90.6 -> 91.2 us, 64 ragged
+// sequences 59.6 -> 59.9).  Next to E4M3 values one fp16 part stays: it rounds
+// eight times finer than the output, and a second one costs more there (48
+// ragged sequences 24.6 -> 25.7 us, 16 of 8000 with 16 heads of 256 51 -> 54).
 //
 // Bound by HBM once its pipelines are full: 2 x 131072 tokens, 4 heads of 128,
 // bf16: 537 MB in 90.6 us, 5.9 TB/s, 0.88 of the copy rate; what is lost is
@@ -441,6 +458,7 @@ k_paged_attention(const AttnArgs a) {
   constexpr int LPR = S::kRowBytes / 16;       // lanes (16-byte chunks) per token row
   constexpr int NI = kTile * LPR / 32;         // copies per lane and matrix
   constexpr int DPL = D == 64 ? 8 : 16;        // E4M3: dimensions per lane of the second product
+  constexpr int kParts = E4M3 ? 1 : 2;         // of a weight
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint2 s_scan[2 * kWarps];
   __shared__ int s_last;
@@ -723,7 +741,7 @@ k_paged_attention(const AttnArgs a) {
               v = ok ? v * (E4M3 ? qf[nh][u] * ks : qf[nh][u]) : -INFINITY;
             }
         }
-      uint32_t pb[MT][NH][2];  // the weights as the second product's B operand
+      uint32_t pb[kParts][MT][NH][2];  // the weights as the second product's B operand
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) {
         float mx[2], wx[2];
@@ -775,18 +793,17 @@ k_paged_attention(const AttnArgs a) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float sa = s[mt][nh][2 * x], sb = s[mt][nh][2 * x + 1];
-            uint32_t p;
-            if (E4M3) {
-              l[nh][0] += exp2_fast(sa - ms[0]);
-              l[nh][1] += exp2_fast(sb - ms[1]);
-              p = pack_f16x2(exp2_fast(sa + lv[mt][x] - ws[0] + kWTop),
-                             exp2_fast(sb + lv[mt][x] - ws[1] + kWTop));
-            } else {
-              p = pack_bf16x2(exp2_fast(sa - ms[0]), exp2_fast(sb - ms[1]));
-              l[nh][0] += bf16_lo(p);  // the weights as they are multiplied
-              l[nh][1] += bf16_hi(p);
-            }
-            pb[mt][nh][x] = transpose8x8(p);
+            const float pa = exp2_fast(sa - ms[0]), pc = exp2_fast(sb - ms[1]);
+            l[nh][0] += pa;
+            l[nh][1] += pc;
+            uint32_t p[kParts];
+            if (E4M3)
+              p[0] = pack_f16x2(exp2_fast(sa + lv[mt][x] - ws[0] + kWTop),
+                                exp2_fast(sb + lv[mt][x] - ws[1] + kWTop));
+            else
+              split_weights(pa, pc, p[0], p[kParts - 1]);
+#pragma unroll
+            for (int y = 0; y < kParts; ++y) pb[y][mt][nh][x] = transpose8x8(p[y]);
           }
       }
 #pragma unroll
@@ -824,7 +841,7 @@ k_paged_attention(const AttnArgs a) {
                                       e4m3x2_to_f16x2(tb & 0xffffu), e4m3x2_to_f16x2(tb >> 16)};
 #pragma unroll
               for (int nh = 0; nh < NH; ++nh)
-                mma_f16_16x8x16(o[(DPL / 2) * blk + i][nh], av, pb[mt][nh]);
+                mma_f16_16x8x16(o[(DPL / 2) * blk + i][nh], av, pb[0][mt][nh]);
             }
           }
         } else {
@@ -835,7 +852,9 @@ k_paged_attention(const AttnArgs a) {
             uint32_t av[4];
             ldmatrix_x4_trans(vt + r * S::kRowBytes + v_chunk<D, E4M3>(r, 2 * i + (mi & 1)) * 16, av);
 #pragma unroll
-            for (int nh = 0; nh < NH; ++nh) mma_bf16_16x8x16(o[i][nh], av, pb[mt][nh]);
+            for (int y = 0; y < kParts; ++y)
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh) mma_bf16_16x8x16(o[i][nh], av, pb[y][mt][nh]);
           }
         }
       }

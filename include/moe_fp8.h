@@ -499,9 +499,9 @@ typedef struct {
  * equal calls give equal bits.  A sequence of length 0 gives zeros.  Cache
  * elements outside [max(0, len - window), len) are never read: they may
  * hold anything, and the pages of a window's past may be reused.
- * Scores, maxima, sums and outputs are fp32; the softmax weights are rounded
- * to the cache's multiplication type (bf16 next to bf16 values, fp16 next to
- * E4M3 values).  D = 64, 128 or 256; up to 2^31 - 1 tokens per sequence,
+ * Scores, maxima, sums and outputs are fp32; the softmax weights enter the
+ * product with the values as two bf16 parts next to bf16 values (2^-16 of the
+ * weight), rounded to fp16 next to E4M3 values.  D = 64, 128 or 256; up to 2^31 - 1 tokens per sequence,
  * and about 2^31 tiles of 16 tokens in all (B * Hkv * the table's room).
  * A page number outside [0, pages) or a length outside [0, table_width *
  * page_size] raises MOE_DEV_BAD_PAGE; the tokens of such a page are left
