@@ -13,7 +13,8 @@ current stream or the one given; tensors are checked for device, type, shape
 and layout here and for their sizes in the library.  What the kernels themselves
 find wrong in their data (a page number outside the cache, say) is recorded in
 ``status``, a device array that ``check()`` reads after synchronising; it keeps
-what was recorded until ``status.zero_()``.
+what was recorded until ``status.zero_()``.  Host threads may share an object,
+each with its own output and workspace.
 """
 from __future__ import annotations
 
@@ -262,7 +263,7 @@ class QkNormRope(_Status):
             _dense(cos_sin, "cos_sin", torch.float32, self.n_pos, self.rot)
         self.width = (Hq + 2 * Hkv) * D
         self._q_norm, self._k_norm, self._cos_sin = (_lib._ptr(t) for t in (q_norm, k_norm, cos_sin))
-        self._key, self._dims = None, None  # the last call's sizes, as the library takes them
+        self._sizes = None, None  # (read and replaced as one: threads may share the object)
         self._call = _lib.lib().moe_qk_norm_rope
 
     def forward(self, qkv: torch.Tensor, positions: Optional[torch.Tensor], slots: torch.Tensor,
@@ -292,13 +293,14 @@ class QkNormRope(_Status):
                 or qs[2] != 1 or (Hq > 1 and qs[1] != D)):
             _refuse(q_out, "q_out", _BF16, (T, Hq, D), dev, _HEADS)
         key = (T, xs[0], qs[0])
-        if key != self._key:
-            self._dims = _lib.QkDims(T, Hq, self.rot, int(self.interleaved), self.n_pos, self.eps,
-                                     key[1] if T > 1 else width, key[2] if T > 1 else Hq * D)
-            self._key = key
+        known, dims = self._sizes
+        if key != known:
+            dims = _lib.QkDims(T, Hq, self.rot, int(self.interleaved), self.n_pos, self.eps,
+                               key[1] if T > 1 else width, key[2] if T > 1 else Hq * D)
+            self._sizes = key, dims
         st = self._call(qkv.data_ptr(), self._q_norm, self._k_norm, self._cos_sin,
                         None if positions is None else positions.data_ptr(), slots.data_ptr(),
-                        self._dims, cache._abi, q_out.data_ptr(), self._status,
+                        dims, cache._abi, q_out.data_ptr(), self._status,
                         _stream_on(stream, dev))
         if st:
             _lib._check(st, "moe_qk_norm_rope")
@@ -314,7 +316,7 @@ class PagedAttention(_Status):
         super().__init__(device)
         self.Hq, self.Hkv, self.D, self.window = Hq, Hkv, D, window
         self.scale = 1.0 / math.sqrt(D) if scale is None else scale
-        self._key, self._dims = None, None  # the last call's sizes, as the library takes them
+        self._sizes = None, None  # (read and replaced as one: threads may share the object)
         self._call = _lib.lib().moe_paged_attention
 
     def workspace(self, B: int, stream=None) -> torch.Tensor:
@@ -354,13 +356,14 @@ class PagedAttention(_Status):
         elif ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError("ws must be contiguous and on the tensors' device")
         key = (B, width, ts[0], qs[0], os[0])
-        if key != self._key:
+        known, dims = self._sizes
+        if key != known:
             row = Hq * D
             strides = key[2:] if B > 1 else (width, row, row)
-            self._dims = _lib.AttnDims(B, Hq, width, self.window, self.scale, *strides)
-            self._key = key
+            dims = _lib.AttnDims(B, Hq, width, self.window, self.scale, *strides)
+            self._sizes = key, dims
         st = self._call(q.data_ptr(), cache._abi, block_table.data_ptr(), seq_lens.data_ptr(),
-                        self._dims, out.data_ptr(), ws.data_ptr(), ws.nbytes, self._status,
+                        dims, out.data_ptr(), ws.data_ptr(), ws.nbytes, self._status,
                         _stream_on(stream, dev))
         if st:
             _lib._check(st, "moe_paged_attention")
@@ -384,7 +387,7 @@ class Fp8Linear(_Status):
         super().__init__(codes.device)
         self._mat = _lib.Fp8Mat(codes.data_ptr(), scales.data_ptr())
         self._bias = _lib._ptr(bias)
-        self._key, self._dims = None, None  # the last call's sizes, as the library takes them
+        self._sizes = None, None  # (read and replaced as one: threads may share the object)
         self._call = _lib.lib().moe_linear_fp8
 
     def workspace(self, M: int, stream=None) -> torch.Tensor:
@@ -409,10 +412,11 @@ class Fp8Linear(_Status):
         elif ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError("ws must be contiguous and on the tensors' device")
         key = (M, xs[0], os[0])
-        if key != self._key:
-            self._dims = _lib.LinearDims(M, N, K, key[1] if M > 1 else K, key[2] if M > 1 else N)
-            self._key = key
-        st = self._call(x.data_ptr(), self._mat, self._bias, self._dims, out.data_ptr(),
+        known, dims = self._sizes
+        if key != known:
+            dims = _lib.LinearDims(M, N, K, key[1] if M > 1 else K, key[2] if M > 1 else N)
+            self._sizes = key, dims
+        st = self._call(x.data_ptr(), self._mat, self._bias, dims, out.data_ptr(),
                         ws.data_ptr(), ws.nbytes, self._status, _stream_on(stream, dev))
         if st:
             _lib._check(st, "moe_linear_fp8")
