@@ -67,7 +67,21 @@ _ROWS = "the elements of a row must be contiguous"
 _HEADS = "the heads of a row must be contiguous"
 
 
-class _Status:
+class _Fixed:
+    """What is set up stays: its addresses and sizes are held as the library
+    takes them.  Only the attributes in _free may be set again; tensors may be
+    written in place."""
+
+    _free = frozenset()
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__ and name not in self._free:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed at set-up: "
+                                 "make a new object, or write into the tensor")
+        object.__setattr__(self, name, value)
+
+
+class _Status(_Fixed):
     """The device status word of one operator object."""
 
     def __init__(self, device):
@@ -79,7 +93,7 @@ class _Status:
         _lib.moe_read_device_status(self.status, stream)
 
 
-class ExpertSelector:
+class ExpertSelector(_Fixed):
     """Experts from router logits (moe_select_experts): softmax or sigmoid
     scores, a balance bias [E] that steers the choice only, `top_groups` of
     `groups` expert groups kept by the sum of their `group_top` largest keys,
@@ -146,7 +160,7 @@ class ExpertSelector:
         return topk_idx, topk_w
 
 
-class PagedCache:
+class PagedCache(_Fixed):
     """A paged key/value cache over tensors [pages, Hkv, page_size, D]: bf16,
     or E4M3 codes (uint8 or float8_e4m3fn) with float32 scales [pages, Hkv,
     page_size].  Any strides with D contiguous will do (a cache kept as
@@ -247,7 +261,10 @@ def rope_cos_sin(n_pos: int, rot: int, base: float = 1e6, factor: float = 1.0,
 class QkNormRope(_Status):
     """Query/key head norms and rotary positions, the keys and values stored
     into a paged cache (moe_qk_norm_rope).  q_norm, k_norm: float32 [D] or
-    None (no norm); cos_sin: a table of rope_cos_sin or None (no rotation)."""
+    None (no norm); cos_sin: a table of rope_cos_sin or None (no rotation).
+    eps and interleaved may be set again."""
+
+    _free = frozenset(("_sizes", "eps", "interleaved"))
 
     def __init__(self, Hq: int, Hkv: int, D: int, q_norm: Optional[torch.Tensor] = None,
                  k_norm: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
@@ -292,10 +309,10 @@ class QkNormRope(_Status):
         if (q_out.dtype != _BF16 or q_out.get_device() != dev or q_out.shape != (T, Hq, D)
                 or qs[2] != 1 or (Hq > 1 and qs[1] != D)):
             _refuse(q_out, "q_out", _BF16, (T, Hq, D), dev, _HEADS)
-        key = (T, xs[0], qs[0])
+        key = (T, xs[0], qs[0], self.eps, self.interleaved)
         known, dims = self._sizes
         if key != known:
-            dims = _lib.QkDims(T, Hq, self.rot, int(self.interleaved), self.n_pos, self.eps,
+            dims = _lib.QkDims(T, Hq, self.rot, int(bool(key[4])), self.n_pos, key[3],
                                key[1] if T > 1 else width, key[2] if T > 1 else Hq * D)
             self._sizes = key, dims
         st = self._call(qkv.data_ptr(), self._q_norm, self._k_norm, self._cos_sin,
@@ -309,7 +326,10 @@ class QkNormRope(_Status):
 
 class PagedAttention(_Status):
     """Attention of one new token per sequence over a paged cache
-    (moe_paged_attention); window > 0 keeps the last `window` tokens."""
+    (moe_paged_attention); window > 0 keeps the last `window` tokens.  scale
+    and window may be set again."""
+
+    _free = frozenset(("_sizes", "scale", "window"))
 
     def __init__(self, Hq: int, Hkv: int, D: int, scale: Optional[float] = None, window: int = 0,
                  device="cuda"):
@@ -355,12 +375,12 @@ class PagedAttention(_Status):
             ws = self.workspace(B, stream)
         elif ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError("ws must be contiguous and on the tensors' device")
-        key = (B, width, ts[0], qs[0], os[0])
+        key = (B, width, ts[0], qs[0], os[0], self.window, self.scale)
         known, dims = self._sizes
         if key != known:
             row = Hq * D
-            strides = key[2:] if B > 1 else (width, row, row)
-            dims = _lib.AttnDims(B, Hq, width, self.window, self.scale, *strides)
+            strides = key[2:5] if B > 1 else (width, row, row)
+            dims = _lib.AttnDims(B, Hq, width, key[5], key[6], *strides)
             self._sizes = key, dims
         st = self._call(q.data_ptr(), cache._abi, block_table.data_ptr(), seq_lens.data_ptr(),
                         dims, out.data_ptr(), ws.data_ptr(), ws.nbytes, self._status,
@@ -374,6 +394,8 @@ class Fp8Linear(_Status):
     """x W^T + bias with block-FP8 weights (codes [N, K] uint8 or
     float8_e4m3fn, scales float32 [ceil(N/128), ceil(K/128)]) and E4M3
     activations quantised in the call (moe_linear_fp8)."""
+
+    _free = frozenset(("_sizes",))
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor,
                  bias: Optional[torch.Tensor] = None):

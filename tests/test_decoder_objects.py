@@ -141,3 +141,39 @@ def test_threads_share_an_object(make, monkeypatch):
     finally:
         sys.setswitchinterval(before)
     assert not wrong
+
+
+def test_settings_take_effect_at_the_next_call(library):
+    """scale, window, eps and interleaved, set again between calls of one size."""
+    op, call, _ = attention()
+    call(2)
+    op.window, op.scale = 5, 0.25
+    call(2)
+    a, b = (args[4] for _, args in library.calls)
+    assert (a.window, a.scale) == (0, 0.125) and (b.window, b.scale) == (5, 0.25)
+    library.calls.clear()
+    op, call, _ = norm()
+    call(2)
+    op.eps, op.interleaved = 0.5, True
+    call(2)
+    a, b = (args[6] for _, args in library.calls)
+    assert a.interleaved == 0 and (b.eps, b.interleaved) == (0.5, 1)
+
+
+def test_what_is_held_as_addresses_and_sizes_is_fixed(library):
+    """Another tensor or size in place of one whose address or value the object
+    holds is refused, not ignored (the old tensor's memory may be gone)."""
+    f32 = torch.float32
+    lin, attn, rope = linear()[0], attention()[0], norm()[0]
+    sel = decoder.ExpertSelector(8, 2, bias=fake(8, dtype=f32))
+    cache = decoder.PagedCache(fake(3, 2, 16, 64, dtype=BF16), fake(3, 2, 16, 64, dtype=BF16))
+    for op, names in ((lin, ("codes", "scales", "bias", "N", "K", "status")), (attn, ("Hq", "Hkv", "D", "status")),
+                      (rope, ("q_norm", "k_norm", "cos_sin", "rot", "n_pos", "width")),
+                      (sel, ("bias", "E", "k", "rule")), (cache, ("k", "v", "k_scale", "pages", "page_size"))):
+        for name in names:
+            was = getattr(op, name)
+            with pytest.raises(AttributeError, match=name):
+                setattr(op, name, fake(8, dtype=f32))
+            assert getattr(op, name) is was
+    sel.bias.fill_(1.0)  # in place, as a balance bias is kept
+    sel.rule.scale = 2.0
