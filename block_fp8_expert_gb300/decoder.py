@@ -10,7 +10,8 @@ Each object holds what a serving program sets up once; ``forward`` takes the
 step's tensors, and output buffers and a workspace where the program keeps
 them (they are allocated otherwise).  Everything runs in libmoe_fp8.so on the
 current stream or the one given; tensors are checked for device, type, shape
-and layout here and for their sizes in the library.  What the kernels themselves
+and layout here and for their sizes in the library.  Their device has to be the
+current one.  What the kernels themselves
 find wrong in their data (a page number outside the cache, say) is recorded in
 ``status``, a device array that ``check()`` reads after synchronising; it keeps
 what was recorded until ``status.zero_()``.  Host threads may share an object,
@@ -28,6 +29,15 @@ from .device import new_on
 
 _BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
                                 torch.uint8)
+
+
+_current_device = torch._C._cuda_getDevice
+
+
+def _refuse_device(device: int) -> None:
+    raise ValueError(f"the tensors are on device {device}, the current device is "
+                     f"{_current_device()}: the library launches on the current one "
+                     "(torch.cuda.device changes it)")
 
 
 def _stream_on(stream, device: int) -> int:
@@ -55,11 +65,13 @@ def _refuse(t, name: str, dtype, shape, device: Optional[int] = None, layout: st
     raise ValueError(f"{name}: strides {t.stride()}: {layout or 'must be contiguous'}")
 
 
-def _dense(t: Optional[torch.Tensor], name: str, dtype, *shape) -> Optional[torch.Tensor]:
-    """A contiguous CUDA tensor (or None), checked at set-up."""
+def _dense(t: Optional[torch.Tensor], name: str, dtype, *shape,
+           device: Optional[int] = None) -> Optional[torch.Tensor]:
+    """A contiguous CUDA tensor (or None), on `device` where given."""
     if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype
-                              and tuple(t.shape) == shape and t.is_contiguous()):
-        _refuse(t, name, dtype, shape)
+                              and tuple(t.shape) == shape and t.is_contiguous()
+                              and (device is None or t.get_device() == device)):
+        _refuse(t, name, dtype, shape, device)
     return t
 
 
@@ -90,6 +102,8 @@ class _Status(_Fixed):
 
     def check(self, stream=None) -> None:
         """Synchronise and raise MoeError if a kernel flagged its data."""
+        if self._dev != _current_device():
+            _refuse_device(self._dev)
         _lib.moe_read_device_status(self.status, stream)
 
 
@@ -110,6 +124,7 @@ class ExpertSelector(_Fixed):
             _lib.MOE_SCORE_SIGMOID if score == "sigmoid" else _lib.MOE_SCORE_SOFTMAX,
             groups, top_groups, group_top, int(bool(renorm)), scale)
         self._bias = _lib._ptr(self.bias)
+        self._bias_dev = None if bias is None else bias.get_device()
         self._call = _lib.lib().moe_select_experts
 
     def forward(self, logits: torch.Tensor, topk_idx: Optional[torch.Tensor] = None,
@@ -120,6 +135,10 @@ class ExpertSelector(_Fixed):
         if dev < 0 or logits.dtype != _F32 or logits.shape != (T, E) or (
                 logits.stride(1) != 1 and E > 1):
             _refuse(logits, "logits", _F32, (T, E), layout=_ROWS)
+        if dev != _current_device():
+            _refuse_device(dev)
+        if self._bias_dev is not None and dev != self._bias_dev:
+            _refuse(self.bias, "bias", _F32, (E,), dev)
         if topk_idx is None:
             topk_idx = new_on(stream, T, k, dtype=_I32, device=logits.device)
         if topk_w is None:
@@ -147,13 +166,19 @@ class ExpertSelector(_Fixed):
                              f"need {self.k} of {self.E}")
         if not x.is_cuda or x.dtype != _BF16 or x.shape != (T, layer.H) or not x.is_contiguous():
             _refuse(x, "x", _BF16, (T, layer.H))
+        dev = x.get_device()
+        if dev != _current_device():
+            _refuse_device(dev)
+        _dense(self.bias, "bias", _F32, self.E, device=dev)
+        _dense(layer.Wr, "the layer's Wr", _F32, self.E, layer.H, device=dev)
+        _dense(layer.bias, "the layer's bias", _F32, self.E, device=dev)
         if topk_idx is None:
             topk_idx = new_on(stream, T, self.k, dtype=_I32, device=x.device)
         if topk_w is None:
             topk_w = new_on(stream, T, self.k, dtype=_F32, device=x.device)
-        _dense(topk_idx, "topk_idx", _I32, T, self.k)
-        _dense(topk_w, "topk_w", _F32, T, self.k)
-        if ws.get_device() != x.get_device() or not ws.is_contiguous():
+        _dense(topk_idx, "topk_idx", _I32, T, self.k, device=dev)
+        _dense(topk_w, "topk_w", _F32, T, self.k, device=dev)
+        if ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError("ws must be contiguous and on x's device")
         _lib.moe_route_select(x, layer.Wr, layer.bias, self.bias, self.rule, layer.dims(T),
                               topk_idx, topk_w, ws, stream)
@@ -272,12 +297,12 @@ class QkNormRope(_Status):
         super().__init__(device)
         self.Hq, self.Hkv, self.D, self.eps = Hq, Hkv, D, eps
         self.interleaved = bool(interleaved)
-        self.q_norm = _dense(q_norm, "q_norm", torch.float32, D)
-        self.k_norm = _dense(k_norm, "k_norm", torch.float32, D)
+        self.q_norm = _dense(q_norm, "q_norm", torch.float32, D, device=self._dev)
+        self.k_norm = _dense(k_norm, "k_norm", torch.float32, D, device=self._dev)
         self.cos_sin = cos_sin
         self.n_pos, self.rot = (0, 0) if cos_sin is None else cos_sin.shape
         if cos_sin is not None:
-            _dense(cos_sin, "cos_sin", torch.float32, self.n_pos, self.rot)
+            _dense(cos_sin, "cos_sin", torch.float32, self.n_pos, self.rot, device=self._dev)
         self.width = (Hq + 2 * Hkv) * D
         self._q_norm, self._k_norm, self._cos_sin = (_lib._ptr(t) for t in (q_norm, k_norm, cos_sin))
         self._sizes = None, None  # (read and replaced as one: threads may share the object)
@@ -293,6 +318,8 @@ class QkNormRope(_Status):
         dev, T, xs = qkv.get_device(), qkv.shape[0], qkv.stride()
         if dev != self._dev or qkv.dtype != _BF16 or qkv.shape != (T, width) or xs[-1] != 1:
             _refuse(qkv, "qkv", _BF16, (T, width), self._dev, _ROWS)
+        if dev != _current_device():
+            _refuse_device(dev)
         if cache.Hkv != self.Hkv or cache.D != D or cache.device != dev:
             cache.refuse(self.Hkv, D, dev)
         if (positions is None) != (self.cos_sin is None):
@@ -341,6 +368,8 @@ class PagedAttention(_Status):
 
     def workspace(self, B: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to B sequences (of any length)."""
+        if self._dev != _current_device():
+            _refuse_device(self._dev)
         d = _lib.AttnDims(B, self.Hq, 0, self.window, self.scale, 0, 0, 0)
         return new_on(stream, _lib.paged_attention_workspace_bytes(d, self.D), dtype=torch.uint8,
                     device=self.status.device)
@@ -355,6 +384,8 @@ class PagedAttention(_Status):
         if (dev != self._dev or q.dtype != _BF16 or q.shape != (B, Hq, D) or qs[2] != 1
                 or (Hq > 1 and qs[1] != D)):
             _refuse(q, "q", _BF16, (B, Hq, D), self._dev, _HEADS)
+        if dev != _current_device():
+            _refuse_device(dev)
         if cache.Hkv != self.Hkv or cache.D != D or cache.device != dev:
             cache.refuse(self.Hkv, D, dev)
         rows, width = block_table.shape
@@ -402,10 +433,11 @@ class Fp8Linear(_Status):
         if codes.dtype == torch.float8_e4m3fn:
             codes = codes.view(torch.uint8)
         self.N, self.K = codes.shape
+        dev = codes.get_device()
         self.codes = _dense(codes, "codes", torch.uint8, self.N, self.K)
         self.scales = _dense(scales, "scales", torch.float32, -(-self.N // 128),
-                             -(-self.K // 128))
-        self.bias = _dense(bias, "bias", torch.float32, self.N)
+                             -(-self.K // 128), device=dev)
+        self.bias = _dense(bias, "bias", torch.float32, self.N, device=dev)
         super().__init__(codes.device)
         self._mat = _lib.Fp8Mat(codes.data_ptr(), scales.data_ptr())
         self._bias = _lib._ptr(bias)
@@ -414,6 +446,8 @@ class Fp8Linear(_Status):
 
     def workspace(self, M: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to M rows."""
+        if self._dev != _current_device():
+            _refuse_device(self._dev)
         n = _lib.linear_fp8_workspace_bytes(_lib.LinearDims(M, self.N, self.K, self.K, self.N))
         return new_on(stream, n, dtype=torch.uint8, device=self.codes.device)
 
@@ -424,6 +458,8 @@ class Fp8Linear(_Status):
         dev, M, xs = x.get_device(), x.shape[0], x.stride()
         if dev != self._dev or x.dtype != _BF16 or x.shape != (M, K) or xs[-1] != 1:
             _refuse(x, "x", _BF16, (M, K), self._dev, _ROWS)
+        if dev != _current_device():
+            _refuse_device(dev)
         if out is None:
             out = new_on(stream, M, N, dtype=_BF16, device=x.device)
         os = out.stride()

@@ -23,6 +23,17 @@ def fake(*shape, dtype):
     return torch.zeros(*shape, dtype=dtype).as_subclass(Fake)
 
 
+class Elsewhere(Fake):
+    """The same on another device than the other tensors."""
+
+    def get_device(self):
+        return 3
+
+
+def elsewhere(*shape, dtype):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(Elsewhere)
+
+
 class Library:
     """In place of the library: notes each call's arguments."""
 
@@ -177,3 +188,82 @@ def test_what_is_held_as_addresses_and_sizes_is_fixed(library):
             assert getattr(op, name) is was
     sel.bias.fill_(1.0)  # in place, as a balance bias is kept
     sel.rule.scale = 2.0
+
+
+def selector():
+    op = decoder.ExpertSelector(8, 2)
+
+    def call(T):
+        op.forward(call.x(T), fake(T, 2, dtype=I32), fake(T, 2, dtype=torch.float32), stream=0)
+    call.x = lambda T: OnDevice0.zeros(T, 8)
+    return op, call
+
+
+class OnDevice0(Fake):
+    def get_device(self):
+        return 0
+
+    @staticmethod
+    def zeros(*shape):
+        return torch.zeros(*shape, dtype=torch.float32).as_subclass(OnDevice0)
+
+
+@pytest.mark.parametrize("make", [linear, attention, norm])
+def test_another_current_device_is_refused(library, monkeypatch, make):
+    """The library launches on the current device: tensors of another one never
+    reach it."""
+    op, call, _ = make()
+    call(2)
+    monkeypatch.setattr(decoder, "_current_device", lambda: 1)
+    library.calls.clear()
+    for refused in (lambda: call(2), op.check, *([lambda: op.workspace(2)] if hasattr(op, "workspace") else [])):
+        with pytest.raises(ValueError, match="current device"):
+            refused()
+    assert not library.calls
+
+
+def test_selector_on_another_current_device_is_refused(library, monkeypatch):
+    monkeypatch.setattr(decoder, "_current_device", lambda: 1)
+    op, call = selector()
+    with pytest.raises(ValueError, match="current device"):
+        call(2)
+    assert not library.calls
+
+
+def _layer(**kw):
+    at = dict(E=8, k=2, H=64, Wr=fake(8, 64, dtype=torch.float32), bias=None, dims=lambda T: _lib.dims(T, 64, 64, 8, 2))
+    at.update(kw)
+    return types.SimpleNamespace(**at)
+
+
+def test_tensors_of_several_devices_are_refused(library):
+    """At set-up and in a call; nothing reaches the library."""
+    f32, u8 = torch.float32, torch.uint8
+    codes, table = fake(64, 128, dtype=u8), fake(9, 32, dtype=f32)
+    for scales, bias in ((elsewhere(1, 1, dtype=f32), None), (fake(1, 1, dtype=f32), elsewhere(64, dtype=f32))):
+        with pytest.raises(ValueError, match="device 3"):
+            decoder.Fp8Linear(codes, scales, bias)
+    for bad in (dict(q_norm=elsewhere(64, dtype=f32)), dict(k_norm=elsewhere(64, dtype=f32)),
+                dict(cos_sin=table.as_subclass(Elsewhere))):
+        with pytest.raises(ValueError, match="device 3"):
+            decoder.QkNormRope(4, 2, 64, device="cpu", **bad)
+    x, ws = fake(3, 64, dtype=BF16), fake(1 << 16, dtype=u8)
+    idx, w, bias = fake(3, 2, dtype=I32), fake(3, 2, dtype=f32), fake(8, dtype=f32)
+    plain, biased = decoder.ExpertSelector(8, 2, bias=bias), decoder.ExpertSelector(8, 2, bias=elsewhere(8, dtype=f32))
+    plain.route(x, _layer(), ws, idx, w, stream=0)
+    for op, layer, ws_, idx_, w_ in (
+            (biased, _layer(), ws, idx, w), (plain, _layer(Wr=elsewhere(8, 64, dtype=f32)), ws, idx, w),
+            (plain, _layer(bias=elsewhere(8, dtype=f32)), ws, idx, w),
+            (plain, _layer(), elsewhere(1 << 16, dtype=u8), idx, w),
+            (plain, _layer(), ws, elsewhere(3, 2, dtype=I32), w), (plain, _layer(), ws, idx, elsewhere(3, 2, dtype=f32))):
+        with pytest.raises(ValueError, match="device"):
+            op.route(x, layer, ws_, idx_, w_, stream=0)
+    assert len(library.calls) == 1
+
+
+def test_selector_bias_of_another_device_is_refused(library, monkeypatch):
+    monkeypatch.setattr(decoder, "_current_device", lambda: 0)
+    op = decoder.ExpertSelector(8, 2, bias=elsewhere(8, dtype=torch.float32))
+    with pytest.raises(ValueError, match="bias is on device 3"):
+        op.forward(OnDevice0.zeros(2, 8), stream=0)
+    assert not library.calls
