@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "decoder_internal.h"
+#include "per_device.h"
 #include "tcgen05.cuh"
 
 namespace moe {
@@ -635,11 +636,14 @@ cudaError_t launch_gemm(const CUtensorMap& xmap, const CUtensorMap& wmap, const 
   const GemmLaunch l(SPLIT, cdiv(a.N, GN), cdiv(a.M, GM), s);
   return cudaLaunchKernelEx(&l.cfg, k_linear_gemm<SPLIT>, xmap, wmap, omap, a);
 }
-// Clusters of SPLIT that the GPU holds at once (fewer than its SMs / SPLIT,
-// where its clusters of SMs are no multiples of it).
+// Clusters of SPLIT that the current GPU holds at once (fewer than its SMs /
+// SPLIT, where its clusters of SMs are no multiples of it).
 template <int SPLIT>
 int clusters_at_once() {
-  static const int n = [] {
+  static PerDevice known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return known.get(dev, [] {
     int most = 0;
     GemmLaunch l(SPLIT, 1, 1, nullptr);
     l.cfg.numAttrs = 1;
@@ -648,9 +652,8 @@ int clusters_at_once() {
         cudaOccupancyMaxActiveClusters(&most, k_linear_gemm<SPLIT>, &l.cfg) == cudaSuccess)
       return most;
     cudaGetLastError();
-    return 0;
-  }();
-  return n;
+    return -1;
+  });
 }
 
 }  // namespace
