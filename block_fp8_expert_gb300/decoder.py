@@ -25,19 +25,12 @@ from typing import Optional
 import torch
 
 from . import _lib
+from ._checks import (current_device as _current_device, dense as _dense, refuse as _refuse,
+                      refuse_device as _refuse_device)
 from .device import new_on
 
 _BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
                                 torch.uint8)
-
-
-_current_device = torch._C._cuda_getDevice
-
-
-def _refuse_device(device: int) -> None:
-    raise ValueError(f"the tensors are on device {device}, the current device is "
-                     f"{_current_device()}: the library launches on the current one "
-                     "(torch.cuda.device changes it)")
 
 
 def _stream_on(stream, device: int) -> int:
@@ -48,32 +41,6 @@ def _stream_on(stream, device: int) -> int:
 
 # The checks of a call cost host time on every step, so forward() asks one
 # question per tensor and looks for the words only when the answer is no.
-
-def _refuse(t, name: str, dtype, shape, device: Optional[int] = None, layout: str = "") -> None:
-    """Raise for what is wrong with t, which is not a `dtype` tensor of
-    `shape` on CUDA device `device` with the layout that is described."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: need a tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: need {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} is not on a CUDA device")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"{name} is on device {t.get_device()}, the first tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {tuple(shape)}")
-    raise ValueError(f"{name}: strides {t.stride()}: {layout or 'must be contiguous'}")
-
-
-def _dense(t: Optional[torch.Tensor], name: str, dtype, *shape,
-           device: Optional[int] = None) -> Optional[torch.Tensor]:
-    """A contiguous CUDA tensor (or None), on `device` where given."""
-    if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype
-                              and tuple(t.shape) == shape and t.is_contiguous()
-                              and (device is None or t.get_device() == device)):
-        _refuse(t, name, dtype, shape, device)
-    return t
-
 
 _ROWS = "the elements of a row must be contiguous"
 _HEADS = "the heads of a row must be contiguous"
@@ -103,7 +70,7 @@ class _Status(_Fixed):
     def check(self, stream=None) -> None:
         """Synchronise and raise MoeError if a kernel flagged its data."""
         if self._dev != _current_device():
-            _refuse_device(self._dev)
+            _refuse_device(self._dev, _current_device())
         _lib.moe_read_device_status(self.status, stream)
 
 
@@ -136,7 +103,7 @@ class ExpertSelector(_Fixed):
                 logits.stride(1) != 1 and E > 1):
             _refuse(logits, "logits", _F32, (T, E), layout=_ROWS)
         if dev != _current_device():
-            _refuse_device(dev)
+            _refuse_device(dev, _current_device())
         if self._bias_dev is not None and dev != self._bias_dev:
             _refuse(self.bias, "bias", _F32, (E,), dev)
         if topk_idx is None:
@@ -168,7 +135,7 @@ class ExpertSelector(_Fixed):
             _refuse(x, "x", _BF16, (T, layer.H))
         dev = x.get_device()
         if dev != _current_device():
-            _refuse_device(dev)
+            _refuse_device(dev, _current_device())
         _dense(self.bias, "bias", _F32, self.E, device=dev)
         _dense(layer.Wr, "the layer's Wr", _F32, self.E, layer.H, device=dev)
         _dense(layer.bias, "the layer's bias", _F32, self.E, device=dev)
@@ -319,7 +286,7 @@ class QkNormRope(_Status):
         if dev != self._dev or qkv.dtype != _BF16 or qkv.shape != (T, width) or xs[-1] != 1:
             _refuse(qkv, "qkv", _BF16, (T, width), self._dev, _ROWS)
         if dev != _current_device():
-            _refuse_device(dev)
+            _refuse_device(dev, _current_device())
         if cache.Hkv != self.Hkv or cache.D != D or cache.device != dev:
             cache.refuse(self.Hkv, D, dev)
         if (positions is None) != (self.cos_sin is None):
@@ -369,7 +336,7 @@ class PagedAttention(_Status):
     def workspace(self, B: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to B sequences (of any length)."""
         if self._dev != _current_device():
-            _refuse_device(self._dev)
+            _refuse_device(self._dev, _current_device())
         d = _lib.AttnDims(B, self.Hq, 0, self.window, self.scale, 0, 0, 0)
         return new_on(stream, _lib.paged_attention_workspace_bytes(d, self.D), dtype=torch.uint8,
                     device=self.status.device)
@@ -385,7 +352,7 @@ class PagedAttention(_Status):
                 or (Hq > 1 and qs[1] != D)):
             _refuse(q, "q", _BF16, (B, Hq, D), self._dev, _HEADS)
         if dev != _current_device():
-            _refuse_device(dev)
+            _refuse_device(dev, _current_device())
         if cache.Hkv != self.Hkv or cache.D != D or cache.device != dev:
             cache.refuse(self.Hkv, D, dev)
         rows, width = block_table.shape
@@ -447,7 +414,7 @@ class Fp8Linear(_Status):
     def workspace(self, M: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to M rows."""
         if self._dev != _current_device():
-            _refuse_device(self._dev)
+            _refuse_device(self._dev, _current_device())
         n = _lib.linear_fp8_workspace_bytes(_lib.LinearDims(M, self.N, self.K, self.K, self.N))
         return new_on(stream, n, dtype=torch.uint8, device=self.codes.device)
 
@@ -459,7 +426,7 @@ class Fp8Linear(_Status):
         if dev != self._dev or x.dtype != _BF16 or x.shape != (M, K) or xs[-1] != 1:
             _refuse(x, "x", _BF16, (M, K), self._dev, _ROWS)
         if dev != _current_device():
-            _refuse_device(dev)
+            _refuse_device(dev, _current_device())
         if out is None:
             out = new_on(stream, M, N, dtype=_BF16, device=x.device)
         os = out.stride()

@@ -12,6 +12,8 @@ import numpy as np
 import torch
 
 from . import _lib
+from ._checks import (current_device as _current_device, dense as _dense, refuse as _refuse,
+                      refuse_device as _refuse_device)
 
 
 def _dev(a: np.ndarray, device) -> torch.Tensor:
@@ -124,9 +126,23 @@ class DeviceLayer:
         [T, k]): moe_permute, moe_expert_ffn_fp8 and moe_combine."""
         if self.shared is not None:
             raise ValueError("layers with a shared expert run through forward()")
-        T = x.shape[0]
+        T, dev = x.shape[0], x.device
+        at = x.get_device()
+        if x.dtype != torch.bfloat16 or x.shape != (T, self.H) or not x.is_contiguous() or not x.is_cuda:
+            _refuse(x, "x", torch.bfloat16, (T, self.H))
+        if at != _current_device():
+            _refuse_device(at, _current_device())
+        for t, name, dtype, width in ((topk_idx, "topk_idx", torch.int32, self.k),
+                                      (topk_w, "topk_w", torch.float32, self.k),
+                                      (out, "out", torch.bfloat16, self.H)):
+            if t is None and name != "out":
+                raise TypeError(f"{name}: need a tensor")
+            _dense(t, name, dtype, T, width, device=at)
+        if self.Wr.get_device() != at:
+            raise ValueError(f"the layer is on device {self.Wr.get_device()}, x on {at}")
+        if ws is not None and (ws.get_device() != at or not ws.is_contiguous()):
+            raise ValueError("ws must be contiguous and on x's device")
         d, P = self.dims(T), T * self.k
-        dev = x.device
         off, rows, slot_row = (new_on(stream, n, dtype=torch.int32, device=dev)
                                for n in (self.E + 1, P, P))
         y = new_on(stream, P, self.H, dtype=torch.float32, device=dev)

@@ -8,7 +8,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from block_fp8_expert_gb300 import _lib, decoder  # noqa: E402
+from block_fp8_expert_gb300 import _lib, decoder, device  # noqa: E402
 
 BF16, I32 = torch.bfloat16, torch.int32
 
@@ -52,6 +52,7 @@ def library(monkeypatch):
     L = Library()
     monkeypatch.setattr(_lib, "lib", lambda: L)
     monkeypatch.setattr(decoder, "_current_device", lambda: -1, raising=False)
+    monkeypatch.setattr(device, "_current_device", lambda: -1, raising=False)
     return L
 
 
@@ -266,4 +267,43 @@ def test_selector_bias_of_another_device_is_refused(library, monkeypatch):
     op = decoder.ExpertSelector(8, 2, bias=elsewhere(8, dtype=torch.float32))
     with pytest.raises(ValueError, match="bias is on device 3"):
         op.forward(OnDevice0.zeros(2, 8), stream=0)
+    assert not library.calls
+
+
+def _moe_layer():
+    f32, u8 = torch.float32, torch.uint8
+    I, E, H = 64, 8, 64
+    routed = device.DeviceFfn(*(fake(E, *s, dtype=t) for m in ((I, H), (I, H), (H, I))
+                                for s, t in ((m, u8), ((1, 1), f32))))
+    return device.DeviceLayer(H, I, E, 2, 0, fake(E, H, dtype=f32), None, routed, None)
+
+
+def test_experts_refuse_what_they_would_misread(library, monkeypatch):
+    """A routing made elsewhere in another type (torch.topk's indices are int64),
+    shape, layout or place, and tokens or results likewise: refused, and nothing
+    reaches the library."""
+    f32, u8 = torch.float32, torch.uint8
+    L = _moe_layer()
+    good = dict(x=fake(4, 64, dtype=BF16), topk_idx=fake(4, 2, dtype=I32), topk_w=fake(4, 2, dtype=f32),
+                out=fake(4, 64, dtype=BF16), ws=fake(1 << 16, dtype=u8), stream=0)
+    # (the scratch comes from the CUDA allocator)
+    monkeypatch.setattr(device, "new_on", lambda stream, *shape, dtype, device: fake(*shape, dtype=dtype))
+    L.experts(**good)
+    assert library.calls
+    library.calls.clear()
+    bad = dict(
+        x=[fake(4, 64, dtype=f32), fake(4, 32, dtype=BF16), fake(4, 128, dtype=BF16)[:, ::2], fake(64, 4, dtype=BF16).t(),
+           torch.zeros(4, 64, dtype=BF16)],
+        topk_idx=[fake(4, 2, dtype=torch.int64), fake(4, 3, dtype=I32), fake(3, 2, dtype=I32), fake(2, 4, dtype=I32).t(),
+                  torch.zeros(4, 2, dtype=I32), elsewhere(4, 2, dtype=I32), None],
+        topk_w=[fake(4, 2, dtype=BF16), fake(4, 1, dtype=f32), fake(4, 4, dtype=f32)[:, :2], elsewhere(4, 2, dtype=f32), None],
+        out=[fake(4, 64, dtype=f32), fake(3, 64, dtype=BF16), fake(4, 65, dtype=BF16)[:, :64], elsewhere(4, 64, dtype=BF16)],
+        ws=[fake(256, 256, dtype=u8).t()[:, ::2], elsewhere(1 << 16, dtype=u8)])
+    for name, values in bad.items():
+        for v in values:
+            with pytest.raises((TypeError, ValueError), match=name):
+                L.experts(**{**good, name: v})
+    monkeypatch.setattr(device, "_current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        L.experts(**good)
     assert not library.calls
