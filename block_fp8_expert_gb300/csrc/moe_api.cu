@@ -341,13 +341,21 @@ moe_status moe_combine(const float* y_perm, const int32_t* tok_slot_row, const f
 
 namespace moe {
 namespace {
+// A routing made before the call, and where its kernels record what they find
+// (16 words of the caller's, or NULL; never cleared).
+struct GivenRouting {
+  const int32_t* idx;
+  const float* w;
+  int32_t* status;
+};
 // The layer call, with an optional gate vector for the shared expert; act8:
-// the routed experts on E4M3 activations (routed experts only).
+// the routed experts on E4M3 activations (routed experts only); given: no
+// router (Wr, bias, topk_idx_out and topk_w_out are not used).
 moe_status layer_forward(const uint16_t* x, const float* Wr, const float* bias,
                          moe_fp8_ffn routed, const moe_fp8_ffn* shared,
                          const float* shared_gate, moe_dims d, uint16_t* out,
                          int32_t* topk_idx_out, float* topk_w_out, void* ws, size_t ws_bytes,
-                         void* stream, bool act8 = false) {
+                         void* stream, bool act8 = false, const GivenRouting* given = nullptr) {
   moe_status s;
   if ((s = check_dims(d)) != MOE_OK) return s;
   if (act8) {
@@ -359,7 +367,7 @@ moe_status layer_forward(const uint16_t* x, const float* Wr, const float* bias,
   }
   if (d.T == 0) return MOE_OK;  // no token: nothing is read or written
   REQUIRE_PTR(x);
-  REQUIRE_PTR(Wr);
+  if (!given) REQUIRE_PTR(Wr);
   REQUIRE_OPT_PTR(bias);
   REQUIRE_PTR(out);
   REQUIRE_OPT_PTR(topk_idx_out);
@@ -376,8 +384,10 @@ moe_status layer_forward(const uint16_t* x, const float* Wr, const float* bias,
   const WsLayout L = ws_layout(d);
   cudaStream_t st = (cudaStream_t)stream;
   const int P = d.T * d.k;
-  int32_t* idx = topk_idx_out ? topk_idx_out : at<int32_t>(ws, L.idx);
-  float* w = topk_w_out ? topk_w_out : at<float>(ws, L.w);
+  int32_t* idx_out = topk_idx_out ? topk_idx_out : at<int32_t>(ws, L.idx);
+  float* w_out = topk_w_out ? topk_w_out : at<float>(ws, L.w);
+  const int32_t* idx = given ? given->idx : idx_out;
+  const float* w = given ? given->w : w_out;
   int32_t* off = at<int32_t>(ws, L.off);
   int32_t* row_token = at<int32_t>(ws, L.row_token);
   int32_t* tok_slot_row = at<int32_t>(ws, L.tok_slot_row);
@@ -386,13 +396,15 @@ moe_status layer_forward(const uint16_t* x, const float* Wr, const float* bias,
   uint16_t* y_perm = at<uint16_t>(ws, L.y_perm);
   int16_t* yexp = at<int16_t>(ws, L.yexp);
 
-  int32_t* status = at<int32_t>(ws, L.status);
+  int32_t* status = given ? given->status : at<int32_t>(ws, L.status);
   int32_t* soff = at<int32_t>(ws, L.sh_off);
   int32_t* srows = at<int32_t>(ws, L.sh_rows);
   int32_t* sact = at<int32_t>(ws, L.sh_active);
   const bool has_shared = d.I_shared > 0;
   const bool gemm = act8 || use_expert_gemm(P, d.E, d.H, d.I);
-  const bool small = small_route_permute_ok(d.T, d.E, d.k);
+  // (a given routing may hold no valid expert at all: the fused combine, which
+  // ends in the routed experts' CTAs, is not for it)
+  const bool small = !given && small_route_permute_ok(d.T, d.E, d.k);
   // streamed GEMV, one-CTA permutation, no shared expert: the down kernel
   // also combines (its tickets cleared by the permutation)
   const bool shared_gemm = has_shared && use_expert_gemm(d.T, 1, d.H, d.I_shared);
@@ -414,7 +426,7 @@ moe_status layer_forward(const uint16_t* x, const float* Wr, const float* bias,
     // permutation) in one CTA
     CUDA_CHECK(launch_route_permute_small(
                    x, Wr, bias, d.T, d.H, d.E, d.k, at<float>(ws, L.logits),
-                   at<uint16_t>(ws, L.wr_planes), idx, w, off,
+                   at<uint16_t>(ws, L.wr_planes), idx_out, w_out, off,
                    row_token, tok_slot_row, at<int32_t>(ws, L.row_pair), active,
                    sep_shared ? soff : nullptr, sep_shared ? srows : nullptr,
                    sep_shared ? sact : nullptr, xn, xe,
@@ -425,10 +437,18 @@ moe_status layer_forward(const uint16_t* x, const float* Wr, const float* bias,
                    status, st, true, shared_gate, sgate),
                "moe_layer_forward: route+permute");
   } else {
-    CUDA_CHECK(launch_route(x, Wr, bias, d.T, d.H, d.E, d.k, at<float>(ws, L.logits),
-                            at<uint16_t>(ws, L.wr_planes), idx, w, xn, xe, status, st, true,
-                            shared_gate, sgate),
-               "moe_layer_forward: route");
+    if (!given) {
+      CUDA_CHECK(launch_route(x, Wr, bias, d.T, d.H, d.E, d.k, at<float>(ws, L.logits),
+                              at<uint16_t>(ws, L.wr_planes), idx_out, w_out, xn, xe, status, st,
+                              true, shared_gate, sgate),
+                 "moe_layer_forward: route");
+    } else {  // what else the routing kernels write
+      if (need_xn)
+        CUDA_CHECK(launch_x_norm(x, d.T, d.H, xn, xe, st, true), "moe_experts_forward");
+      if (sgate)
+        CUDA_CHECK(launch_shared_gate(x, shared_gate, d.T, d.H, sgate, st, true),
+                   "moe_experts_forward");
+    }
     // (with the tensor-core GEMM: also its token-tile prefix and zeroed
     // completion counters, so that no tile-offset launch follows)
     CUDA_CHECK(launch_permute(idx, d.T, d.E, d.k, at<int32_t>(ws, L.rank),
@@ -446,7 +466,9 @@ moe_status layer_forward(const uint16_t* x, const float* Wr, const float* bias,
   // and writes its k routed rows (and its shared-expert row when that expert
   // also runs on the GEMM); below, one warp per routed row keeps more CTAs
   // in flight (8 tokens per CTA would leave most SMs idle).
-  const bool token_gather = gemm && d.T >= kTokenGatherMin;
+  // A given routing keeps the row gather: with no valid row the GEMM's CTAs end
+  // without waiting for the gather, which then must have nothing left to write.
+  const bool token_gather = gemm && !given && d.T >= kTokenGatherMin;
   if (act8) {
     // E4M3 activations: x and hid codes with their group scales in the
     // activation-row and hid scratch (codes first, then the scales)
@@ -565,6 +587,23 @@ moe_status moe_layer_forward_act8(const uint16_t* x, const float* Wr, const floa
                                   size_t ws_bytes, void* stream) {
   return layer_forward(x, Wr, bias, routed, nullptr, nullptr, d, out, topk_idx_out, topk_w_out, ws,
                        ws_bytes, stream, true);
+}
+
+moe_status moe_experts_forward(const uint16_t* x, const int32_t* topk_idx, const float* topk_w,
+                               moe_fp8_ffn routed, const moe_fp8_ffn* shared,
+                               const float* shared_gate, moe_dims d, uint16_t* out, void* ws,
+                               size_t ws_bytes, int32_t* status, void* stream) {
+  const moe_status s = check_dims(d);
+  if (s != MOE_OK) return s;
+  if (shared_gate && d.I_shared == 0)
+    return fail(MOE_ERR_INVALID_ARG, "shared_gate given but I_shared == 0");
+  REQUIRE_OPT_PTR(status);
+  if (d.T == 0) return MOE_OK;
+  REQUIRE_ELEMENTS(topk_idx);
+  REQUIRE_ELEMENTS(topk_w);
+  const GivenRouting given{topk_idx, topk_w, status};
+  return layer_forward(x, nullptr, nullptr, routed, shared, shared_gate, d, out, nullptr, nullptr,
+                       ws, ws_bytes, stream, false, &given);
 }
 
 moe_status moe_verify_workspace_bytes(moe_dims d, int n_tokens, size_t* bytes) {

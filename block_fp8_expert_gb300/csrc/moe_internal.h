@@ -82,6 +82,11 @@ cudaError_t launch_route(const uint16_t* x, const float* Wr, const float* bias, 
                          cudaStream_t s, bool pdl, const float* shared_gate = nullptr,
                          float* sgate = nullptr);
 
+// sgate[t] = sigmoid(x[t] . shared_gate) alone, with the sums of the top-k
+// kernels.
+cudaError_t launch_shared_gate(const uint16_t* x, const float* shared_gate, int T, int H,
+                               float* sgate, cudaStream_t s, bool pdl);
+
 // The router logits alone: route_kslices(T, H, E) slices of partial sums,
 // part[ks][t][e]; the reader adds the slices in order.  Clears the status
 // words.  Arguments as launch_route's.
@@ -121,7 +126,7 @@ cudaError_t launch_route_permute_small(const uint16_t* x, const float* Wr, const
                                        const float* shared_gate = nullptr,
                                        float* sgate = nullptr);
 
-// The multi-kernel permutation (T*k > 4096).  tile_off (E + 1 ints, may be
+// The multi-kernel permutation (T*k > 4096, or a given routing).  tile_off (E + 1 ints, may be
 // NULL): also the tensor-core GEMM's token-tile prefix; counters[0,
 // n_counters) (may be NULL) are zeroed (the GEMM's completion counters).
 cudaError_t launch_permute(const int32_t* topk_idx, int T, int E, int k, int32_t* rank,

@@ -308,6 +308,24 @@ struct SharedGate {
   float* sgate = nullptr;  // [T] out
 };
 
+// The gate alone, a warp per token.
+__global__ void __launch_bounds__(256)
+k_shared_gate(const uint16_t* __restrict__ x, const float* __restrict__ g, int T, int H,
+              float* __restrict__ sgate) {
+  griddep_wait();
+  griddep_trigger();
+  const int lane = threadIdx.x & 31, t = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= T) return;  // warp-uniform
+  const float gt = warp_shared_gate(x, g, H, t, lane);
+  if (lane == 0) sgate[t] = gt;
+}
+
+cudaError_t launch_shared_gate(const uint16_t* x, const float* shared_gate, int T, int H,
+                               float* sgate, cudaStream_t s, bool pdl) {
+  return launch_k(k_shared_gate, dim3(cdiv(T, 8)), dim3(256), 0, s, pdl, x, shared_gate, T, H,
+                  sgate);
+}
+
 template <int EPL>
 __global__ void __launch_bounds__(256)
 k_router_topk(const float* __restrict__ part, int KS, const float* __restrict__ bias, int T,

@@ -69,6 +69,10 @@ class DeviceLayer:
     # gated shared expert: float32 [H] (None: ungated)
     shared_gate_w: Optional[torch.Tensor] = None
 
+    def __post_init__(self):
+        # what experts() finds wrong: bits are ORed in and stay (check())
+        self.status = torch.zeros(16, dtype=torch.int32, device=self.Wr.device)
+
     @classmethod
     def from_host(cls, layer, device="cuda") -> "DeviceLayer":
         """Upload a layer drawn by ``moe_inputs.make_layer`` (or any object
@@ -123,7 +127,8 @@ class DeviceLayer:
                 stream=None) -> torch.Tensor:
         """out[T, H] (bf16) = the routed experts applied to x[T, H] (bf16) with
         a routing made elsewhere (topk_idx int32 [T, k], topk_w float32
-        [T, k]): moe_permute, moe_expert_ffn_fp8 and moe_combine."""
+        [T, k]; moe_experts_forward).  What the kernels find wrong is recorded
+        in `status`, which check() reads."""
         if self.shared is not None:
             raise ValueError("layers with a shared expert run through forward()")
         T, dev = x.shape[0], x.device
@@ -142,18 +147,21 @@ class DeviceLayer:
             raise ValueError(f"the layer is on device {self.Wr.get_device()}, x on {at}")
         if ws is not None and (ws.get_device() != at or not ws.is_contiguous()):
             raise ValueError("ws must be contiguous and on x's device")
-        d, P = self.dims(T), T * self.k
-        off, rows, slot_row = (new_on(stream, n, dtype=torch.int32, device=dev)
-                               for n in (self.E + 1, P, P))
-        y = new_on(stream, P, self.H, dtype=torch.float32, device=dev)
+        d = self.dims(T)
         if out is None:
             out = new_on(stream, T, self.H, dtype=torch.bfloat16, device=dev)
         if ws is None:
             ws = new_on(stream, _lib.workspace_bytes(d), dtype=torch.uint8, device=dev)
-        _lib.moe_permute(topk_idx, d, off, rows, slot_row, ws, stream)
-        _lib.moe_expert_ffn_fp8(x, off, rows, self.routed.abi(), d, y, ws, stream)
-        _lib.moe_combine(y, slot_row, topk_w, None, d, out, stream)
+        _lib.moe_experts_forward(x, topk_idx, topk_w, self.routed.abi(), None, None, d, out, ws,
+                                 self.status, stream)
         return out
+
+    def check(self, stream=None) -> None:
+        """Synchronise and raise MoeError if a kernel of experts() flagged its
+        data; what was recorded stays until ``status.zero_()``."""
+        if self.status.get_device() != _current_device():
+            _refuse_device(self.status.get_device(), _current_device())
+        _lib.moe_read_device_status(self.status, stream)
 
     def verify(self, x: torch.Tensor, out: torch.Tensor, topk_idx: torch.Tensor,
                topk_w: torch.Tensor, tokens, stream=None) -> dict:

@@ -93,7 +93,7 @@ class DecoderLayer:
 
     def check(self):
         """Raise if a kernel flagged its data."""
-        for op in (self.qkv, self.rope, self.attention, self.o):
+        for op in (self.qkv, self.rope, self.attention, self.o, self.moe):
             op.check()
 
 

@@ -420,6 +420,24 @@ moe_status moe_route_select(const uint16_t* x, const float* Wr,
                             int32_t* topk_idx, float* topk_w, void* ws,
                             size_t ws_bytes, void* stream);
 
+/*
+ * The layer after its router: the experts on a routing made elsewhere, by
+ * moe_select_experts for example.  moe_layer_forward's permutation, routed
+ * experts, shared expert and combine with its arguments, workspace, precision
+ * and flags, except that topk_idx int32 [T, k] and topk_w float [T, k] are
+ * given (the alignment of their elements will do), shared_gate float [H] may be
+ * NULL (no gate), and the flags go to `status`; the workspace's own status word
+ * is neither read nor written.
+ * An index outside [0, E) raises MOE_DEV_BAD_EXPERT_INDEX and its pair adds
+ * nothing.  With moe_route's routing the result is moe_layer_forward's.
+ */
+moe_status moe_experts_forward(const uint16_t* x, const int32_t* topk_idx,
+                               const float* topk_w, moe_fp8_ffn routed,
+                               const moe_fp8_ffn* shared,
+                               const float* shared_gate, moe_dims d,
+                               uint16_t* out, void* ws, size_t ws_bytes,
+                               int32_t* status, void* stream);
+
 #define MOE_KV_BF16 0
 #define MOE_KV_E4M3 1
 

@@ -1,6 +1,7 @@
 """The decoder operators without a GPU: arguments are refused on the host
 before any CUDA call, workspaces are sized, and the rotation tables follow
 their formulas."""
+import ctypes
 import math
 
 import pytest
@@ -185,3 +186,25 @@ def test_arrays_of_elements_need_their_alignment_only(L):
     q = _lib.QkDims(2, 8, 16, 0, 4, 1e-6, 12 * 128, 8 * 128)
     for pos, slots in ((P + 2, P), (P, P + 4)):
         assert L.moe_qk_norm_rope(P, None, None, P, pos, slots, q, _cache(), P, None, None) == INV
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(H=100), UNS), (dict(k=40), UNS), (dict(x=None), INV), (dict(idx=None), INV), (dict(idx=P + 2), INV),
+    (dict(w=None), INV), (dict(w=P + 2), INV), (dict(codes=None), INV), (dict(out=P + 8), INV), (dict(ws=None), INV),
+    (dict(nws=100), WS), (dict(status=P + 4), INV), (dict(gate=P), INV), (dict(I_shared=64), INV),
+    (dict(shared=True), INV), (dict(I_shared=64, shared=True, gate=P + 4), INV)])
+def test_experts_forward_refusals(L, kw, code):
+    a = dict(x=P, idx=P, w=P, codes=P, out=P, ws=P, nws=1 << 40, status=None, gate=None, shared=False, H=256, k=2,
+             I_shared=0)
+    a.update(kw)
+    d = _lib.dims(8, a["H"], 128, 16, a["k"], a["I_shared"])
+    f = _lib.ffn(*(a["codes"], P) * 3)
+    assert L.moe_experts_forward(a["x"], a["idx"], a["w"], f, ctypes.byref(f) if a["shared"] else None, a["gate"],
+                                 d, a["out"], a["ws"], a["nws"], a["status"], None) == code
+    assert L.moe_last_error_message()
+
+
+def test_experts_forward_without_tokens(L):
+    f = _lib.ffn(*(P, P) * 3)
+    assert L.moe_experts_forward(None, None, None, f, None, None, _lib.dims(0, 256, 128, 16, 2), None, None, 0, None,
+                                 None) == _lib.MOE_OK
