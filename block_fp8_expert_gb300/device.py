@@ -125,12 +125,11 @@ class DeviceLayer:
     def experts(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                 out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
-        """out[T, H] (bf16) = the routed experts applied to x[T, H] (bf16) with
-        a routing made elsewhere (topk_idx int32 [T, k], topk_w float32
-        [T, k]; moe_experts_forward).  What the kernels find wrong is recorded
-        in `status`, which check() reads."""
-        if self.shared is not None:
-            raise ValueError("layers with a shared expert run through forward()")
+        """out[T, H] (bf16) = the layer applied to x[T, H] (bf16) with a routing
+        made elsewhere (topk_idx int32 [T, k], topk_w float32 [T, k]) in place
+        of its router's, its shared expert and that one's gate included
+        (moe_experts_forward).  What the kernels find wrong is recorded in
+        `status`, which check() reads."""
         T, dev = x.shape[0], x.device
         at = x.get_device()
         if x.dtype != torch.bfloat16 or x.shape != (T, self.H) or not x.is_contiguous() or not x.is_cuda:
@@ -152,8 +151,9 @@ class DeviceLayer:
             out = new_on(stream, T, self.H, dtype=torch.bfloat16, device=dev)
         if ws is None:
             ws = new_on(stream, _lib.workspace_bytes(d), dtype=torch.uint8, device=dev)
-        _lib.moe_experts_forward(x, topk_idx, topk_w, self.routed.abi(), None, None, d, out, ws,
-                                 self.status, stream)
+        shared = None if self.shared is None else self.shared.abi()
+        _lib.moe_experts_forward(x, topk_idx, topk_w, self.routed.abi(), shared, self.shared_gate_w,
+                                 d, out, ws, self.status, stream)
         return out
 
     def check(self, stream=None) -> None:

@@ -139,3 +139,36 @@ def test_example_layer_reports_its_experts(torch):
     L.step(x)
     with pytest.raises(_lib().MoeError, match="0x8"):
         L.check()
+
+
+# the shared expert streamed with the routed ones or by itself, or on the GEMM
+@pytest.mark.parametrize("name,T", [("large_sparse", 1), ("large_sparse", 16), ("large_sparse", 60), ("large_sparse", 256),
+                                    ("large_sparse", 1100)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_layers_with_a_shared_expert(torch, name, T, gated):
+    from block_fp8_expert_gb300.device import DeviceLayer, x_to_device
+    host = host_layer(name)
+    D = DeviceLayer.from_host(host)
+    if gated:
+        g = torch.Generator(device="cuda")
+        g.manual_seed(T)
+        D.shared_gate_w = 0.02 * torch.randn(D.H, generator=g, device="cuda")
+    x = x_to_device(mi.make_tokens(host, T, seed=1)[0])
+    idx = torch.empty(T, D.k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, D.k, device="cuda")
+    out = D.forward(x, topk_idx=idx, topk_w=w)
+    assert torch.equal(D.experts(x, idx, w), out)
+    D.check()
+    # the selector's choice on the same layer
+    from block_fp8_expert_gb300.decoder import ExpertSelector
+    i2, w2 = ExpertSelector(D.E, D.k).route(x, D, D.workspace(T))
+    assert torch.equal(i2, idx)
+    # (weights within 2^-17 of the router's, through one bf16 rounding)
+    got, ref = D.experts(x, i2, w2).double(), out.double()
+    assert ((got - ref).abs() <= 2.0 ** -7 * ref.abs() + 2.0 ** -10 * ref.square().mean().sqrt()).all()
+    # no valid routed expert: the shared one's output alone, flagged
+    alone = D.experts(x, torch.full_like(idx, -1), w)
+    same = D.experts(x, idx, torch.zeros_like(w))
+    assert torch.equal(alone, same) and (alone != 0).any()
+    with pytest.raises(_lib().MoeError, match="0x1"):
+        D.check()
