@@ -122,6 +122,8 @@ _SIGNATURES = {
     "moe_permute_static_scratch": (_st, [_vp, Dims, _vp, _vp, _vp, _vp]),
     "moe_select_experts": (_st, [_vp, _i64, _vp, SelectRule, _i32, _i32, _i32, _vp, _vp, _vp]),
     "moe_route_select": (_st, [_vp, _vp, _vp, _vp, SelectRule, Dims, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_select_status": (_st, [_vp, _vp, _vp, _vp, SelectRule, Dims, _vp, _vp, _vp, _sz, _vp,
+                                      _vp]),
     "moe_experts_forward": (_st, [_vp, _vp, _vp, Fp8Ffn, ctypes.POINTER(Fp8Ffn), _vp, Dims, _vp,
                                   _vp, _sz, _vp, _vp]),
     "moe_qk_norm_rope": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, QkDims, KvCache, _vp, _vp, _vp]),
@@ -306,10 +308,10 @@ def moe_select_experts(logits, row_stride: int, bias, rule: SelectRule, T: int, 
 
 
 def moe_route_select(x, Wr, logit_bias, bias, rule: SelectRule, d: Dims, topk_idx, topk_w, ws,
-                     stream=None) -> None:
-    _check(lib().moe_route_select(_ptr(x), _ptr(Wr), _ptr(logit_bias), _ptr(bias), rule, d,
-                                  _ptr(topk_idx), _ptr(topk_w), _ptr(ws), _nbytes(ws),
-                                  _stream(stream)), "moe_route_select")
+                     status=None, stream=None) -> None:
+    _check(lib().moe_route_select_status(_ptr(x), _ptr(Wr), _ptr(logit_bias), _ptr(bias), rule, d,
+                                         _ptr(topk_idx), _ptr(topk_w), _ptr(ws), _nbytes(ws),
+                                         _ptr(status), _stream(stream)), "moe_route_select")
 
 
 def moe_experts_forward(x, topk_idx, topk_w, routed: Fp8Ffn, shared: Optional[Fp8Ffn], shared_gate,

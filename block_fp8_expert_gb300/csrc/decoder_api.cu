@@ -105,7 +105,7 @@ moe_status moe_select_experts(const float* logits, int64_t row_stride, const flo
   REQUIRE_ELEMENTS(topk_idx);
   REQUIRE_ELEMENTS(topk_w);
   CUDA_CHECK(launch_select_experts(logits, row_stride, 1, 0, nullptr, bias, rule, T, E, k, topk_idx,
-                                   topk_w, (cudaStream_t)stream),
+                                   topk_w, nullptr, nullptr, (cudaStream_t)stream),
              "moe_select_experts");
   return MOE_OK;
 }
@@ -114,10 +114,19 @@ moe_status moe_route_select(const uint16_t* x, const float* Wr, const float* log
                             const float* bias, moe_select_rule rule, moe_dims d,
                             int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
                             void* stream) {
+  return moe_route_select_status(x, Wr, logit_bias, bias, rule, d, topk_idx, topk_w, ws, ws_bytes,
+                                 nullptr, stream);
+}
+
+moe_status moe_route_select_status(const uint16_t* x, const float* Wr, const float* logit_bias,
+                                   const float* bias, moe_select_rule rule, moe_dims d,
+                                   int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
+                                   int32_t* status, void* stream) {
   size_t need = 0;
   moe_status s = moe_workspace_bytes(d, &need);  // checks the dims
   if (s != MOE_OK) return s;
   if ((s = check_rule(rule, d.E, d.k)) != MOE_OK) return s;
+  REQUIRE_OPT_PTR(status);
   if (d.T == 0) return MOE_OK;
   REQUIRE_PTR(x);
   REQUIRE_PTR(Wr);
@@ -131,11 +140,13 @@ moe_status moe_route_select(const uint16_t* x, const float* Wr, const float* log
   const WsLayout L = ws_layout(d);
   float* part = at<float>(ws, L.logits);
   const cudaStream_t st = (cudaStream_t)stream;
+  int32_t* found = at<int32_t>(ws, L.status);
   CUDA_CHECK(launch_router_logits(x, Wr, d.T, d.H, d.E, part, at<uint16_t>(ws, L.wr_planes), nullptr,
-                                  nullptr, at<int32_t>(ws, L.status), st, true),
+                                  nullptr, found, st, true),
              "moe_route_select");
   CUDA_CHECK(launch_select_experts(part, d.E, route_kslices(d.T, d.H, d.E), (long long)d.T * d.E,
-                                   logit_bias, bias, rule, d.T, d.E, d.k, topk_idx, topk_w, st),
+                                   logit_bias, bias, rule, d.T, d.E, d.k, topk_idx, topk_w,
+                                   status ? found : nullptr, status, st),
              "moe_route_select");
   return MOE_OK;
 }

@@ -33,11 +33,13 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 
 // All launchers enqueue on `s`.
 // logits: `slices` arrays of [T, row_stride], slice_stride apart, which are
-// added in order, then logit_bias (may be NULL).
+// added in order, then logit_bias (may be NULL).  found (may be NULL): a status
+// word of the kernels before, whose bits are raised in status as well.
 cudaError_t launch_select_experts(const float* logits, long long row_stride, int slices,
                                   long long slice_stride, const float* logit_bias,
                                   const float* bias, const moe_select_rule& rule, int T, int E,
-                                  int k, int32_t* topk_idx, float* topk_w, cudaStream_t s);
+                                  int k, int32_t* topk_idx, float* topk_w, const int32_t* found,
+                                  int32_t* status, cudaStream_t s);
 
 cudaError_t launch_qk_norm_rope(const uint16_t* qkv, const float* q_norm, const float* k_norm,
                                 const float* cos_sin, const int32_t* pos, const int64_t* slots,

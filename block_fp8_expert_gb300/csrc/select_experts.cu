@@ -61,13 +61,19 @@ __global__ void __launch_bounds__(128)
 k_select_experts(const float* __restrict__ logits, long long row_stride, int slices,
                  long long slice_stride, const float* __restrict__ logit_bias,
                  const float* __restrict__ bias, const moe_select_rule rule, int n, int span_log2,
-                 int T, int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+                 int T, int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
+                 const int32_t* __restrict__ found, int32_t* __restrict__ status) {
   constexpr unsigned kAll = 0xffffffffu;
   griddep_wait();
   griddep_trigger();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (t >= T) return;  // warp-uniform
+  // what the kernels before found, where the caller keeps it
+  if (found && t == 0 && lane == 0) {
+    const int32_t bits = *found;
+    if (bits) raise_status(status, bits);
+  }
   const int g = lane >> span_log2, place = (lane & ((1 << span_log2) - 1)) * EPL;
   const int e0 = g * n + place, count = g < rule.groups ? n - place : 0;  // (may be over EPL, or below 0)
   const float* row = logits + (size_t)t * row_stride;
@@ -287,7 +293,8 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
 cudaError_t launch_select_experts(const float* logits, long long row_stride, int slices,
                                   long long slice_stride, const float* logit_bias,
                                   const float* bias, const moe_select_rule& rule, int T, int E,
-                                  int k, int32_t* topk_idx, float* topk_w, cudaStream_t s) {
+                                  int k, int32_t* topk_idx, float* topk_w, const int32_t* found,
+                                  int32_t* status, cudaStream_t s) {
   const dim3 grid(cdiv(T, 4)), blk(128);
   const int n = E / rule.groups;  // experts of a group
   int span_log2 = 0;
@@ -295,7 +302,8 @@ cudaError_t launch_select_experts(const float* logits, long long row_stride, int
 #define MOE_SELECT(EPL)                                                                          \
   if ((EPL << span_log2) >= n)                                                                   \
   return launch_k(k_select_experts<EPL>, grid, blk, 0, s, true, logits, row_stride, slices,      \
-                  slice_stride, logit_bias, bias, rule, n, span_log2, T, k, topk_idx, topk_w)
+                  slice_stride, logit_bias, bias, rule, n, span_log2, T, k, topk_idx, topk_w,    \
+                  found, status)
   MOE_SELECT(2);
   MOE_SELECT(4);
   MOE_SELECT(8);

@@ -126,7 +126,9 @@ class ExpertSelector(_Fixed):
               topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
               stream=None):
         """The same choice from the tokens x bf16 [T, H] and a DeviceLayer's
-        router (moe_route_select); ws: the layer's workspace for T tokens."""
+        router (moe_route_select_status); ws: the layer's workspace for T
+        tokens.  What the router finds wrong is recorded in the layer's
+        `status`, which its check() reads."""
         T = x.shape[0]
         if layer.E != self.E or layer.k != self.k:
             raise ValueError(f"the layer routes to {layer.k} of {layer.E} experts, "
@@ -148,7 +150,7 @@ class ExpertSelector(_Fixed):
         if ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError("ws must be contiguous and on x's device")
         _lib.moe_route_select(x, layer.Wr, layer.bias, self.bias, self.rule, layer.dims(T),
-                              topk_idx, topk_w, ws, stream)
+                              topk_idx, topk_w, ws, layer.status, stream)
         return topk_idx, topk_w
 
 

@@ -70,7 +70,8 @@ class DeviceLayer:
     shared_gate_w: Optional[torch.Tensor] = None
 
     def __post_init__(self):
-        # what experts() finds wrong: bits are ORed in and stay (check())
+        # what experts() and ExpertSelector.route() find wrong: bits are ORed in
+        # and stay (check())
         self.status = torch.zeros(16, dtype=torch.int32, device=self.Wr.device)
 
     @classmethod
@@ -157,8 +158,9 @@ class DeviceLayer:
         return out
 
     def check(self, stream=None) -> None:
-        """Synchronise and raise MoeError if a kernel of experts() flagged its
-        data; what was recorded stays until ``status.zero_()``."""
+        """Synchronise and raise MoeError if a kernel of experts(), or of
+        ExpertSelector.route() on this layer, flagged its data; what was
+        recorded stays until ``status.zero_()``."""
         if self.status.get_device() != _current_device():
             _refuse_device(self.status.get_device(), _current_device())
         _lib.moe_read_device_status(self.status, stream)

@@ -420,6 +420,15 @@ moe_status moe_route_select(const uint16_t* x, const float* Wr,
                             int32_t* topk_idx, float* topk_w, void* ws,
                             size_t ws_bytes, void* stream);
 
+/* moe_route_select that also ORs what it finds into `status` (may be NULL),
+ * where it stays: the workspace's word is cleared by the next call on it. */
+moe_status moe_route_select_status(const uint16_t* x, const float* Wr,
+                                   const float* logit_bias, const float* bias,
+                                   moe_select_rule rule, moe_dims d,
+                                   int32_t* topk_idx, float* topk_w, void* ws,
+                                   size_t ws_bytes, int32_t* status,
+                                   void* stream);
+
 /*
  * The layer after its router: the experts on a routing made elsewhere, by
  * moe_select_experts for example.  moe_layer_forward's permutation, routed

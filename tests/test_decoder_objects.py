@@ -232,7 +232,8 @@ def test_selector_on_another_current_device_is_refused(library, monkeypatch):
 
 
 def _layer(**kw):
-    at = dict(E=8, k=2, H=64, Wr=fake(8, 64, dtype=torch.float32), bias=None, dims=lambda T: _lib.dims(T, 64, 64, 8, 2))
+    at = dict(E=8, k=2, H=64, Wr=fake(8, 64, dtype=torch.float32), bias=None, dims=lambda T: _lib.dims(T, 64, 64, 8, 2),
+              status=fake(16, dtype=I32))
     at.update(kw)
     return types.SimpleNamespace(**at)
 
@@ -307,3 +308,13 @@ def test_experts_refuse_what_they_would_misread(library, monkeypatch):
     with pytest.raises(ValueError, match="current device"):
         L.experts(**good)
     assert not library.calls
+
+
+def test_route_records_in_the_layers_status(library):
+    """What a router call finds goes to the layer's own array, which no later
+    call on the workspace clears."""
+    L = _moe_layer()
+    decoder.ExpertSelector(8, 2).route(fake(3, 64, dtype=BF16), L, fake(1 << 16, dtype=torch.uint8),
+                                       fake(3, 2, dtype=I32), fake(3, 2, dtype=torch.float32), stream=0)
+    (name, args), = library.calls
+    assert L.status.data_ptr() in args

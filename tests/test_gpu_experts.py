@@ -172,3 +172,25 @@ def test_layers_with_a_shared_expert(torch, name, T, gated):
     assert torch.equal(alone, same) and (alone != 0).any()
     with pytest.raises(_lib().MoeError, match="0x1"):
         D.check()
+
+
+@pytest.mark.parametrize("name,T", [("tiny", 8), ("tiny", 300), ("qwen3moe_decode", 200)])
+def test_route_keeps_what_the_layer_recorded(torch, name, T):
+    """A clean router call neither clears nor adds to the layer's flags, and is
+    the call without them (both routers; many warps of tokens)."""
+    from block_fp8_expert_gb300 import decoder
+    lib = _lib()
+    D, x, idx, w, _ = _routed(torch, name, T)
+    ws = D.workspace(T)
+    ws.fill_(0xFF)
+    sel = decoder.ExpertSelector(D.E, D.k)
+    i2, w2 = sel.route(x, D, ws)
+    D.check()
+    D.status[0] = lib.MOE_DEV_NONFINITE
+    i3, w3 = sel.route(x, D, ws)
+    assert D.status.tolist() == [lib.MOE_DEV_NONFINITE] + [0] * 15
+    assert torch.equal(i2, idx) and torch.equal(i3, idx) and torch.equal(w2, w3)
+    i4, w4 = torch.empty_like(i2), torch.empty_like(w2)
+    lib.moe_route_select(x, D.Wr, D.bias, None, sel.rule, D.dims(T), i4, w4, ws)
+    assert torch.equal(i4, idx) and torch.equal(w4, w2)
+    assert lib.moe_read_device_status(ws) == 0
