@@ -33,14 +33,16 @@ _BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torc
                                 torch.uint8)
 
 
-def _stream_on(stream, device: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _handle(stream) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 # The checks of a call cost host time on every step, so forward() asks one
-# question per tensor and looks for the words only when the answer is no.
+# question per tensor, looks for the words only when the answer is no, and takes
+# what is fixed at set-up as one tuple (_held).
 
 _ROWS = "the elements of a row must be contiguous"
 _HEADS = "the heads of a row must be contiguous"
@@ -90,34 +92,36 @@ class ExpertSelector(_Fixed):
         self.rule = _lib.SelectRule(
             _lib.MOE_SCORE_SIGMOID if score == "sigmoid" else _lib.MOE_SCORE_SOFTMAX,
             groups, top_groups, group_top, int(bool(renorm)), scale)
-        self._bias = _lib._ptr(self.bias)
-        self._bias_dev = None if bias is None else bias.get_device()
-        self._call = _lib.lib().moe_select_experts
+        self._held = (E, k, self.rule, _lib._ptr(bias), None if bias is None else bias.get_device(),
+                      _lib.lib().moe_select_experts)
 
     def forward(self, logits: torch.Tensor, topk_idx: Optional[torch.Tensor] = None,
                 topk_w: Optional[torch.Tensor] = None, stream=None):
         """logits float32 [T, E] (rows may be strided) -> (topk_idx int32
         [T, k], topk_w float32 [T, k])."""
-        dev, T, E, k = logits.get_device(), logits.shape[0], self.E, self.k
-        if dev < 0 or logits.dtype != _F32 or logits.shape != (T, E) or (
-                logits.stride(1) != 1 and E > 1):
+        E, k, rule, bias, bias_dev, call = self._held
+        dev, shape, ls = logits.get_device(), logits.shape, logits.stride()
+        T = shape[0]
+        if dev < 0 or logits.dtype != _F32 or shape != (T, E) or (ls[1] != 1 and E > 1):
             _refuse(logits, "logits", _F32, (T, E), layout=_ROWS)
         if dev != _current_device():
             _refuse_device(dev, _current_device())
-        if self._bias_dev is not None and dev != self._bias_dev:
+        if bias is not None and dev != bias_dev:
             _refuse(self.bias, "bias", _F32, (E,), dev)
         if topk_idx is None:
             topk_idx = new_on(stream, T, k, dtype=_I32, device=logits.device)
         if topk_w is None:
             topk_w = new_on(stream, T, k, dtype=_F32, device=logits.device)
-        if (topk_idx.dtype != _I32 or topk_idx.get_device() != dev or topk_idx.shape != (T, k)
+        rows = (T, k)
+        if (topk_idx.dtype != _I32 or topk_idx.get_device() != dev or topk_idx.shape != rows
                 or not topk_idx.is_contiguous()):
             _refuse(topk_idx, "topk_idx", _I32, (T, k), dev)
-        if (topk_w.dtype != _F32 or topk_w.get_device() != dev or topk_w.shape != (T, k)
+        if (topk_w.dtype != _F32 or topk_w.get_device() != dev or topk_w.shape != rows
                 or not topk_w.is_contiguous()):
             _refuse(topk_w, "topk_w", _F32, (T, k), dev)
-        st = self._call(logits.data_ptr(), logits.stride(0) if T > 1 else E, self._bias, self.rule,
-                        T, E, k, topk_idx.data_ptr(), topk_w.data_ptr(), _stream_on(stream, dev))
+        st = call(logits.data_ptr(), ls[0] if T > 1 else E, bias, rule, T, E, k,
+                  topk_idx.data_ptr(), topk_w.data_ptr(),
+                  _raw_stream(dev) if stream is None else _handle(stream))
         if st:
             _lib._check(st, "moe_select_experts")
         return topk_idx, topk_w
@@ -177,6 +181,7 @@ class PagedCache(_Fixed):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.Hkv, self.page_size, self.D = k.shape
         self.device = k.get_device()
+        self._place = (self.Hkv, self.D, self.device)
         ss = (0, 0, 0)
         if (k_scale is None) != (v_scale is None):
             raise ValueError("k_scale and v_scale come together")
@@ -273,9 +278,10 @@ class QkNormRope(_Status):
         if cos_sin is not None:
             _dense(cos_sin, "cos_sin", torch.float32, self.n_pos, self.rot, device=self._dev)
         self.width = (Hq + 2 * Hkv) * D
-        self._q_norm, self._k_norm, self._cos_sin = (_lib._ptr(t) for t in (q_norm, k_norm, cos_sin))
         self._sizes = None, None  # (read and replaced as one: threads may share the object)
-        self._call = _lib.lib().moe_qk_norm_rope
+        self._held = (self._dev, Hq, D, self.width, (Hkv, D, self._dev), cos_sin is None,
+                      _lib._ptr(q_norm), _lib._ptr(k_norm), _lib._ptr(cos_sin), self._status,
+                      _lib.lib().moe_qk_norm_rope)
 
     def forward(self, qkv: torch.Tensor, positions: Optional[torch.Tensor], slots: torch.Tensor,
                 cache: PagedCache, q_out: Optional[torch.Tensor] = None,
@@ -283,15 +289,16 @@ class QkNormRope(_Status):
         """qkv bf16 [T, (Hq + 2 Hkv) D] (rows may be strided), positions int32
         [T], slots int64 [T] (page * page_size + offset, or < 0 for padding)
         -> q_out bf16 [T, Hq, D]."""
-        Hq, D, width = self.Hq, self.D, self.width
-        dev, T, xs = qkv.get_device(), qkv.shape[0], qkv.stride()
-        if dev != self._dev or qkv.dtype != _BF16 or qkv.shape != (T, width) or xs[-1] != 1:
-            _refuse(qkv, "qkv", _BF16, (T, width), self._dev, _ROWS)
+        here, Hq, D, width, place, bare, q_norm, k_norm, cos_sin, status, call = self._held
+        dev, shape, xs = qkv.get_device(), qkv.shape, qkv.stride()
+        T = shape[0]
+        if dev != here or qkv.dtype != _BF16 or shape != (T, width) or xs[-1] != 1:
+            _refuse(qkv, "qkv", _BF16, (T, width), here, _ROWS)
         if dev != _current_device():
             _refuse_device(dev, _current_device())
-        if cache.Hkv != self.Hkv or cache.D != D or cache.device != dev:
-            cache.refuse(self.Hkv, D, dev)
-        if (positions is None) != (self.cos_sin is None):
+        if cache._place != place:
+            cache.refuse(*place)
+        if (positions is None) != bare:
             raise ValueError("positions and the rotation table come together")
         if positions is not None and (positions.dtype != _I32 or positions.get_device() != dev
                                       or positions.shape != (T,) or not positions.is_contiguous()):
@@ -311,10 +318,9 @@ class QkNormRope(_Status):
             dims = _lib.QkDims(T, Hq, self.rot, int(bool(key[4])), self.n_pos, key[3],
                                key[1] if T > 1 else width, key[2] if T > 1 else Hq * D)
             self._sizes = key, dims
-        st = self._call(qkv.data_ptr(), self._q_norm, self._k_norm, self._cos_sin,
-                        None if positions is None else positions.data_ptr(), slots.data_ptr(),
-                        dims, cache._abi, q_out.data_ptr(), self._status,
-                        _stream_on(stream, dev))
+        st = call(qkv.data_ptr(), q_norm, k_norm, cos_sin,
+                  None if bare else positions.data_ptr(), slots.data_ptr(), dims, cache._abi,
+                  q_out.data_ptr(), status, _raw_stream(dev) if stream is None else _handle(stream))
         if st:
             _lib._check(st, "moe_qk_norm_rope")
         return q_out
@@ -333,7 +339,8 @@ class PagedAttention(_Status):
         self.Hq, self.Hkv, self.D, self.window = Hq, Hkv, D, window
         self.scale = 1.0 / math.sqrt(D) if scale is None else scale
         self._sizes = None, None  # (read and replaced as one: threads may share the object)
-        self._call = _lib.lib().moe_paged_attention
+        self._held = (self._dev, Hq, D, (Hkv, D, self._dev), self._status,
+                      _lib.lib().moe_paged_attention)
 
     def workspace(self, B: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to B sequences (of any length)."""
@@ -348,15 +355,16 @@ class PagedAttention(_Status):
                 ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """q bf16 [B, Hq, D], block_table int32 [B, pages per sequence],
         seq_lens int32 [B] (the new token included) -> out bf16 [B, Hq, D]."""
-        Hq, D = self.Hq, self.D
-        dev, B, qs = q.get_device(), q.shape[0], q.stride()
-        if (dev != self._dev or q.dtype != _BF16 or q.shape != (B, Hq, D) or qs[2] != 1
+        here, Hq, D, place, status, call = self._held
+        dev, shape, qs = q.get_device(), q.shape, q.stride()
+        B = shape[0]
+        if (dev != here or q.dtype != _BF16 or shape != (B, Hq, D) or qs[2] != 1
                 or (Hq > 1 and qs[1] != D)):
-            _refuse(q, "q", _BF16, (B, Hq, D), self._dev, _HEADS)
+            _refuse(q, "q", _BF16, (B, Hq, D), here, _HEADS)
         if dev != _current_device():
             _refuse_device(dev, _current_device())
-        if cache.Hkv != self.Hkv or cache.D != D or cache.device != dev:
-            cache.refuse(self.Hkv, D, dev)
+        if cache._place != place:
+            cache.refuse(*place)
         rows, width = block_table.shape
         ts = block_table.stride()
         if (block_table.dtype != _I32 or block_table.get_device() != dev or rows != B
@@ -368,7 +376,7 @@ class PagedAttention(_Status):
         if out is None:
             out = new_on(stream, B, Hq, D, dtype=_BF16, device=q.device)
         os = out.stride()
-        if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (B, Hq, D)
+        if (out.dtype != _BF16 or out.get_device() != dev or out.shape != shape
                 or os[2] != 1 or (Hq > 1 and os[1] != D)):
             _refuse(out, "out", _BF16, (B, Hq, D), dev, _HEADS)
         if ws is None:
@@ -382,9 +390,9 @@ class PagedAttention(_Status):
             strides = key[2:5] if B > 1 else (width, row, row)
             dims = _lib.AttnDims(B, Hq, width, key[5], key[6], *strides)
             self._sizes = key, dims
-        st = self._call(q.data_ptr(), cache._abi, block_table.data_ptr(), seq_lens.data_ptr(),
-                        dims, out.data_ptr(), ws.data_ptr(), ws.nbytes, self._status,
-                        _stream_on(stream, dev))
+        st = call(q.data_ptr(), cache._abi, block_table.data_ptr(), seq_lens.data_ptr(), dims,
+                  out.data_ptr(), ws.data_ptr(), ws.nbytes, status,
+                  _raw_stream(dev) if stream is None else _handle(stream))
         if st:
             _lib._check(st, "moe_paged_attention")
         return out
@@ -408,10 +416,9 @@ class Fp8Linear(_Status):
                              -(-self.K // 128), device=dev)
         self.bias = _dense(bias, "bias", torch.float32, self.N, device=dev)
         super().__init__(codes.device)
-        self._mat = _lib.Fp8Mat(codes.data_ptr(), scales.data_ptr())
-        self._bias = _lib._ptr(bias)
         self._sizes = None, None  # (read and replaced as one: threads may share the object)
-        self._call = _lib.lib().moe_linear_fp8
+        self._held = (self._dev, self.N, self.K, _lib.Fp8Mat(codes.data_ptr(), scales.data_ptr()),
+                      _lib._ptr(bias), self._status, _lib.lib().moe_linear_fp8)
 
     def workspace(self, M: int, stream=None) -> torch.Tensor:
         """A workspace for calls of up to M rows."""
@@ -423,10 +430,11 @@ class Fp8Linear(_Status):
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
                 ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """x bf16 [M, K] -> out bf16 [M, N]; rows of either may be strided."""
-        N, K = self.N, self.K
-        dev, M, xs = x.get_device(), x.shape[0], x.stride()
-        if dev != self._dev or x.dtype != _BF16 or x.shape != (M, K) or xs[-1] != 1:
-            _refuse(x, "x", _BF16, (M, K), self._dev, _ROWS)
+        here, N, K, mat, bias, status, call = self._held
+        dev, shape, xs = x.get_device(), x.shape, x.stride()
+        M = shape[0]
+        if dev != here or x.dtype != _BF16 or shape != (M, K) or xs[-1] != 1:
+            _refuse(x, "x", _BF16, (M, K), here, _ROWS)
         if dev != _current_device():
             _refuse_device(dev, _current_device())
         if out is None:
@@ -443,8 +451,8 @@ class Fp8Linear(_Status):
         if key != known:
             dims = _lib.LinearDims(M, N, K, key[1] if M > 1 else K, key[2] if M > 1 else N)
             self._sizes = key, dims
-        st = self._call(x.data_ptr(), self._mat, self._bias, dims, out.data_ptr(),
-                        ws.data_ptr(), ws.nbytes, self._status, _stream_on(stream, dev))
+        st = call(x.data_ptr(), mat, bias, dims, out.data_ptr(), ws.data_ptr(), ws.nbytes, status,
+                  _raw_stream(dev) if stream is None else _handle(stream))
         if st:
             _lib._check(st, "moe_linear_fp8")
         return out
