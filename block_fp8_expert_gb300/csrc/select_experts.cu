@@ -277,6 +277,7 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
     m = order_value(__reduce_max_sync(kAll, order_key(m)));
     if (m == -INFINITY) m = 0.f;
     w = lane < k ? expf(my_v - m) : 0.f;
+    if (inv_sum != inv_sum) w = inv_sum;  // a NaN anywhere in the row: every score is one
   } else {
     w = lane < k ? expf(my_v - vmax) * inv_sum : 0.f;
   }

@@ -79,3 +79,24 @@ def test_attention_value_without_weight(torch):
     A = cache.v.double()[table[0].long()[t // ps], 0, t % ps].abs().mean(0)
     tol = U16 * ref.abs() + 2.0 ** -15 * A          # equal weights: exact; a few sums in fp32
     assert ((out.double() - ref).abs() <= tol).all()
+
+
+# ------------------------------------------------------------------ selection
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (8, 2)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_softmax_of_a_row_with_a_nan(torch, value, groups, top_groups, renorm):
+    """One NaN (or infinite) logit makes every softmax score of the row NaN, so
+    the weights are, whichever experts are chosen; other rows are as ever."""
+    E, k = 64, 4
+    l = torch.randn(3, E, generator=_gen(torch, 3), device="cuda")
+    clean = l.clone()
+    l[1, 40] = value
+    op = _dec().ExpertSelector(E, k, "softmax", None, groups, top_groups, 1, renorm)
+    idx, w = op.forward(l)
+    assert torch.isnan(w[1]).all()
+    assert idx.min() >= 0 and idx.max() < E and len(set(idx[1].tolist())) == k
+    i2, w2 = op.forward(clean)
+    for t in (0, 2):
+        assert torch.equal(idx[t], i2[t]) and torch.equal(w[t], w2[t])
