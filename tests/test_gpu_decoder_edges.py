@@ -100,3 +100,29 @@ def test_softmax_of_a_row_with_a_nan(torch, value, groups, top_groups, renorm):
     i2, w2 = op.forward(clean)
     for t in (0, 2):
         assert torch.equal(idx[t], i2[t]) and torch.equal(w[t], w2[t])
+
+
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (4, 2)])
+def test_sigmoid_scores_near_the_end_of_fp32(torch, groups, top_groups):
+    """Logits about -88, whose scores are subnormal (4e-39 to 1e-38): they order
+    the experts and make the weights.  exp is within 2^-21 of its argument's
+    rounding (88 x 2^-24), the reciprocal within 2^-23, a subnormal score of
+    4e-39 is rounded by 2^-22, twice."""
+    E, k = 64, 6
+    rng = np.random.default_rng(2)
+    l = np.stack([rng.permutation(np.linspace(-88.4, -87.0, E)) for _ in range(5)]).astype(np.float32)
+    s = 1 / (1 + np.exp(-l.astype(np.float64)))
+    n = E // groups
+    for renorm in (False, True):
+        op = _dec().ExpertSelector(E, k, "sigmoid", None, groups, top_groups, 1, renorm)
+        idx, w = op.forward(torch.from_numpy(l).cuda())
+        for t in range(5):
+            best = sorted(range(groups), key=lambda g: -s[t, g * n:(g + 1) * n].max())[:top_groups]
+            cand = sorted((e for e in range(E) if e // n in best), key=lambda e: -s[t, e])[:k]
+            assert idx[t].tolist() == cand
+            ref = s[t, cand] / (s[t, cand].sum() if renorm else 1)
+            _check(_np(w[t]), ref, 2.0 ** -17 * ref, "weights")
+    idx, w = _dec().ExpertSelector(E, k, "sigmoid", renorm=False).forward(torch.full((1, E), -200.0, device="cuda"))
+    assert (w == 0).all() and idx[0].tolist() == list(range(k))
+    idx, w = _dec().ExpertSelector(E, k, "sigmoid", renorm=False).forward(torch.full((1, E), 200.0, device="cuda"))
+    assert (w == 1).all()
