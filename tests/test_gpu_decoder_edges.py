@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from gpu_common import require_gpu
-from test_gpu_decoder import F32, U16, _check, _dec, _gen, _np, _paged, _ref_attention
+from test_gpu_decoder import F32, U16, _attn_tol, _check, _dec, _gen, _np, _paged, _ref_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +126,87 @@ def test_sigmoid_scores_near_the_end_of_fp32(torch, groups, top_groups):
     assert (w == 0).all() and idx[0].tolist() == list(range(k))
     idx, w = _dec().ExpertSelector(E, k, "sigmoid", renorm=False).forward(torch.full((1, E), 200.0, device="cuda"))
     assert (w == 1).all()
+
+
+# ------------------------------------------------------------------ attention: how the work is divided
+
+def _division(torch, lens, Hq, Hkv, D, ps, e4m3, window, width):
+    """How the tiles of these sequences are divided, by the kernel's rules:
+    'short' (each segment its own parts of at most 8 tiles), 'even' (its own
+    parts of an even share and a little more) or 'row' (equal shares of all)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    G = Hq // Hkv
+    nh = 1 if G <= 8 else 2
+    tile = 16 * (1 if (D if e4m3 else 2 * D) >= 256 else 2)
+    per_sm = (2 if e4m3 else 1) if D == 256 else (3 if nh == 1 else 2)
+    HG = Hkv * -(-G // (8 * nh))
+    spans = []
+    for n in lens:
+        lo = max(0, n - window) if window else 0
+        spans.append(-(-n // tile) - lo // tile if n > 0 else 0)
+    most = len(lens) * HG * (-(-width * ps // tile) + 9) // 8 + len(lens) * HG
+    grid = max(1, min(per_sm * sms, most))
+
+    def parts(most):
+        return HG * sum(-(-t // most) for t in spans)
+
+    if parts(8) <= grid:
+        return "short"
+    share = max(8, -(-HG * sum(t + 8 for t in spans if t) // grid))
+    if len(lens) * HG * 4 >= grid and parts(share + max(8, share // 6)) <= grid:
+        return "even"
+    return "row"
+
+
+def _ragged(n, top, seed):
+    """n lengths up to top, one of them 0 and one 1."""
+    rng = np.random.default_rng(seed)
+    return [0, 1, top] + [int(v) for v in rng.integers(1, top + 1, n - 3)]
+
+
+DIVIDED = [  # lens, Hq, Hkv, D, page_size, e4m3, window, how
+    (_ragged(48, 4096, 1), 32, 4, 128, 16, True, 0, "even"), (_ragged(64, 3000, 2), 16, 2, 128, 32, False, 0, "even"),
+    (_ragged(40, 2500, 3), 24, 4, 64, 16, False, 0, "even"), (_ragged(33, 2000, 4), 8, 4, 256, 16, True, 0, "even"),
+    (_ragged(30, 1500, 5), 4, 2, 256, 16, False, 0, "even"), (_ragged(40, 3000, 6), 24, 2, 128, 7, True, 0, "even"),
+    (_ragged(64, 4000, 7), 32, 2, 128, 16, False, 900, "even"), ([2000] * 64, 8, 2, 128, 16, False, 0, "even"),
+    ([2000] * 32, 8, 2, 128, 16, False, 0, "row"),
+    (_ragged(300, 900, 8), 8, 2, 128, 16, True, 0, "row"), (_ragged(5, 40000, 9), 12, 2, 128, 16, True, 0, "row"),
+    ([30000, 1, 0, 9000, 29999], 8, 2, 64, 16, False, 25000, "row"), (_ragged(20, 250, 10), 8, 2, 128, 16, False, 0, "short")]
+
+
+@pytest.mark.parametrize("case", DIVIDED, ids=[f"{len(c[0])}x{max(c[0])}-{c[3]}-{c[-1]}" for c in DIVIDED])
+def test_attention_divided_each_way(torch, case):
+    """Ragged batches over every division of the work, each against float64 and
+    repeated on a workspace of any content."""
+    lens, Hq, Hkv, D, ps, e4m3, window, how = case
+    g = _gen(torch, len(lens) + D)
+    cache, table, kd, vd = _paged(torch, g, lens, Hkv, D, ps, e4m3)
+    assert _division(torch, lens, Hq, Hkv, D, ps, e4m3, window, table.shape[1]) == how
+    q = torch.randn(len(lens), Hq, D, generator=g, device="cuda").mul(1.5).to(torch.bfloat16)
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    op = _dec().PagedAttention(Hq, Hkv, D, None, window)
+    ws = op.workspace(len(lens))
+    ws.random_(256, generator=g)
+    out = op.forward(q, cache, table, sl, ws=ws)
+    op.check()
+    ref, A = (_np(t) for t in _ref_attention(torch, q, kd, vd, table, lens, ps, op.scale, window))
+    _check(_np(out), ref, _attn_tol(ref, A, e4m3), how)
+    for _ in range(3):
+        assert torch.equal(op.forward(q, cache, table, sl, ws=ws), out)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,ps,e4m3,window", [
+    ([700, 0, 45], 16, 1, 128, 16, True, 0), ([700, 0, 45], 12, 1, 256, 16, True, 0), ([700, 0, 45], 16, 1, 64, 16, False, 0),
+    ([5000, 333], 16, 1, 256, 64, True, 1000), ([12000], 24, 2, 128, 5, True, 0), ([9000, 40], 32, 2, 64, 16, False, 2500),
+    ([6000], 16, 1, 256, 16, False, 0), ([20000], 14, 1, 64, 16, True, 0)])
+def test_attention_of_more_than_eight_heads(torch, lens, Hq, Hkv, D, ps, e4m3, window):
+    """More than eight query heads on a key/value head, in every type and head
+    size: short, joined from many parts, windowed."""
+    g = _gen(torch, sum(lens) + Hq)
+    cache, table, kd, vd = _paged(torch, g, lens, Hkv, D, ps, e4m3)
+    q = torch.randn(len(lens), Hq, D, generator=g, device="cuda").mul(1.5).to(torch.bfloat16)
+    op = _dec().PagedAttention(Hq, Hkv, D, None, window)
+    out = op.forward(q, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    op.check()
+    ref, A = (_np(t) for t in _ref_attention(torch, q, kd, vd, table, lens, ps, op.scale, window))
+    _check(_np(out), ref, _attn_tol(ref, A, e4m3), "attention")
