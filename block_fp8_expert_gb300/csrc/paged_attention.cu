@@ -24,6 +24,7 @@ constexpr int kMinTiles = 8;  // least share of a CTA (one user, 8000 tokens: 11
 // and draining the pipeline, the join), in tiles (0 would make 24.5 us, of 48
 // ragged sequences up to 4096, 35.7; 16: 27.9).
 constexpr int kSegCost = 8;
+constexpr int kManySegments = 16;  // CTAs per segment at most for even parts (plan)
 // E4M3: the largest weight times value scale is held as 2^15, so that fp16
 // keeps weights down to 2^-39 of it (a long cache's many small ones)
 constexpr float kWTop = 15.f;
@@ -91,11 +92,14 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
 // A sequence's tiles for one tile of heads are a segment of tiles + kSegCost
 // units; empty sequences have none.  All segments lie in one row, sequence-
 // major, then head.  Where there are CTAs enough to give every segment its own
-// parts of at most kMinTiles tiles, or else (asked only where the sequences
-// may be many enough) of an even share and a little more, a CTA takes one such
-// part: no CTA pays for two segments (64 sequences up to 500 tokens: 12.1 us
-// against 15.5, 32 up to 2000: 18.4 against 21.7; but two of 131072 with heads
-// of 64: 34.9 against 33.5).  Otherwise CTA c takes units [c share, (c + 1)
+// parts of at most kMinTiles tiles, or else, where there may be a segment for
+// every 16 of them (kManySegments), of an even share and a little more, a CTA
+// takes one such part: no CTA pays for two segments (with 4 key/value heads of
+// 128, bf16: 8 sequences of 2000 tokens 13.9 us against 18.6, 24 up to 2000
+// 16.6 against 21.8, 8 of 8000 31.1 against 34.3, but 8 of 65536 168.5 against
+// 167.4; with fewer segments the parts are long and their number leaves CTAs
+// idle: 2 of 131072 91.8 against 90.7, E4M3 heads of 64 1 of 32000 13.8 against
+// 12.1, 2 of 131072 35.3 against 32.6).  Otherwise CTA c takes units [c share, (c + 1)
 // share) of the row, and with them the same part of each segment's tiles, so
 // ragged batches, many short sequences and a few long ones alike, give every
 // CTA the same time.  A segment that several CTAs hold is joined by the last
@@ -166,7 +170,7 @@ __device__ __forceinline__ Place plan(const AttnArgs& a, uint2* s_scan, Place* s
   most = kMinTiles;
   share = max((uint32_t)kMinTiles, (total.x + a.grid - 1) / a.grid);
   bool own = total.y <= (uint32_t)a.grid;
-  if (!own && a.d.B * a.HG * 4 >= a.grid) {  // (the same for every thread)
+  if (!own && a.d.B * a.HG >= cdiv(a.grid, kManySegments)) {  // (the same for every thread)
     most = share + max(kSegCost, share / 6);
     mine.y = 0;
     for (int b = b0; b < b1; ++b) mine.y += parts_of(per > 1 ? span_of(a, b).tiles : span.tiles, most);

@@ -153,7 +153,7 @@ def _division(torch, lens, Hq, Hkv, D, ps, e4m3, window, width):
     if parts(8) <= grid:
         return "short"
     share = max(8, -(-HG * sum(t + 8 for t in spans if t) // grid))
-    if len(lens) * HG * 4 >= grid and parts(share + max(8, share // 6)) <= grid:
+    if len(lens) * HG * 16 >= grid and parts(share + max(8, share // 6)) <= grid:
         return "even"
     return "row"
 
@@ -169,7 +169,7 @@ DIVIDED = [  # lens, Hq, Hkv, D, page_size, e4m3, window, how
     (_ragged(40, 2500, 3), 24, 4, 64, 16, False, 0, "even"), (_ragged(33, 2000, 4), 8, 4, 256, 16, True, 0, "even"),
     (_ragged(30, 1500, 5), 4, 2, 256, 16, False, 0, "even"), (_ragged(40, 3000, 6), 24, 2, 128, 7, True, 0, "even"),
     (_ragged(64, 4000, 7), 32, 2, 128, 16, False, 900, "even"), ([2000] * 64, 8, 2, 128, 16, False, 0, "even"),
-    ([2000] * 32, 8, 2, 128, 16, False, 0, "row"),
+    ([2000] * 32, 8, 2, 128, 16, False, 0, "even"), ([30000] * 9, 8, 1, 128, 64, False, 0, "row"),
     (_ragged(300, 900, 8), 8, 2, 128, 16, True, 0, "row"), (_ragged(5, 40000, 9), 12, 2, 128, 16, True, 0, "row"),
     ([30000, 1, 0, 9000, 29999], 8, 2, 64, 16, False, 25000, "row"), (_ragged(20, 250, 10), 8, 2, 128, 16, False, 0, "short")]
 
