@@ -210,3 +210,74 @@ def test_attention_of_more_than_eight_heads(torch, lens, Hq, Hkv, D, ps, e4m3, w
     op.check()
     ref, A = (_np(t) for t in _ref_attention(torch, q, kd, vd, table, lens, ps, op.scale, window))
     _check(_np(out), ref, _attn_tol(ref, A, e4m3), "attention")
+
+
+# ------------------------------------------------------------------ head norms: many steps per warp
+
+def _steps_per_warp(torch, T, Hq, Hkv, D):
+    """How many steps of 512 / D heads a warp takes, by the launch's rules."""
+    warps = torch.cuda.get_device_properties(0).multi_processor_count * 6 * 4
+    heads = 512 // D
+    steps = -(-Hq // heads) + 2 * -(-Hkv // heads)
+    chunks = min(steps, max(-(-steps // 16), warps // T))
+    return -(-steps // chunks)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,e4m3,ps", [
+    (3700, 32, 4, 128, 128, False, False, 64), (3700, 30, 5, 128, 64, True, True, 16), (3650, 17, 3, 64, 64, False, True, 64),
+    (2600, 16, 2, 256, 128, True, False, 7), (4001, 32, 8, 256, 256, False, True, 32), (3800, 64, 8, 128, 32, True, False, 1)])
+def test_head_norms_of_long_prompts(torch, T, Hq, Hkv, D, rot, inter, e4m3, ps):
+    """Prompts so long that a warp takes more steps than its ring of loads
+    holds (four), every element against float64."""
+    assert _steps_per_warp(torch, T, Hq, Hkv, D) >= 5
+    dec, g = _dec(), _gen(torch, T + D)
+    heads = Hq + 2 * Hkv
+    qkv = torch.randn(T, heads * D, generator=g, device="cuda").mul(2).to(torch.bfloat16)
+    qn, kn = ((1 + 0.2 * torch.randn(D, generator=g, device="cuda")) for _ in range(2))
+    cs = dec.rope_cos_sin(5000, rot, 1e4)
+    pos = torch.randint(0, 5000, (T,), generator=g, device="cuda").to(torch.int32)
+    pages = -(-T // ps) + 2
+    cache = dec.PagedCache.empty(pages, Hkv, ps, D, e4m3)
+    slots = torch.randperm(pages * ps, generator=g, device="cuda")[:T]
+    slots[::97] = -1
+    op = dec.QkNormRope(Hq, Hkv, D, qn, kn, cs, inter, 1e-6)
+    q = op.forward(qkv, pos, slots, cache)
+    op.check()
+
+    x = qkv.double().view(T, heads, D)
+    cos, sin = (c[:, None] for c in cs.double()[pos.long()].split(rot // 2, 1))
+
+    def norm_rope(x, w):
+        y = x / torch.sqrt(x.square().mean(-1, keepdim=True) + 1e-6) * w.double()
+        out = y.clone()
+        a, b = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, rot // 2), slice(rot // 2, rot))
+        out[..., a] = y[..., a] * cos - y[..., b] * sin
+        out[..., b] = y[..., b] * cos + y[..., a] * sin
+        return out
+
+    def close(got, ref, tol, what):
+        bad = ~((got - ref).abs() <= tol)
+        assert not bad.any(), (what, int(bad.sum()), float(((got - ref).abs() / tol).max()))
+
+    def top(t):
+        return t.abs().amax(-1, keepdim=True)
+
+    rq = norm_rope(x[:, :Hq], qn)
+    close(q.double(), rq, U16 * rq.abs() + F32 * top(rq), "queries")
+    kept = slots >= 0
+    at = slots[kept]
+    for codes, scales, ref, what in ((cache.k, cache.k_scale, norm_rope(x[:, Hq:Hq + Hkv], kn), "keys"),
+                                     (cache.v, cache.v_scale, x[:, Hq + Hkv:], "values")):
+        got, ref = codes[at // ps, :, at % ps], ref[kept]
+        if not e4m3:
+            close(got.double(), ref, U16 * ref.abs() + F32 * top(ref), what)
+            continue
+        s = scales[at // ps, :, at % ps].double()[..., None]
+        close(s, top(ref) / 448, F32 * top(ref) / 448, what)
+        close(got.view(torch.float8_e4m3fn).double() * s, ref,
+              torch.maximum(2.0 ** -4 * ref.abs(), 2.0 ** -10 * s) + F32 * top(ref), what)
+    # nothing else was touched
+    free = torch.ones(pages * ps, dtype=torch.bool, device="cuda")
+    free[at] = False
+    left = free.nonzero().flatten()
+    assert (cache.k[left // ps, :, left % ps] == 0).all() and (cache.v[left // ps, :, left % ps] == 0).all()
