@@ -2,6 +2,9 @@
 tighter than the plain parity tests', plans, rings and kernels that only some
 sizes reach, values at the ends of their ranges."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -281,3 +284,133 @@ def test_head_norms_of_long_prompts(torch, T, Hq, Hkv, D, rot, inter, e4m3, ps):
     free[at] = False
     left = free.nonzero().flatten()
     assert (cache.k[left // ps, :, left % ps] == 0).all() and (cache.v[left // ps, :, left % ps] == 0).all()
+
+
+# ------------------------------------------------------------------ captures, the functions on addresses, the example's routing
+
+@pytest.mark.parametrize("M,N,K", [(200, 1024, 2048), (300, 2048, 1024), (1100, 2048, 512), (24, 5120, 2048), (64, 640, 512)])
+def test_linear_in_a_graph(torch, M, N, K):
+    """Every kernel of the linear layer captured and replayed on new inputs:
+    quantisation and tcgen05 with K over a cluster or not, and the streamed one."""
+    dec, g = _dec(), _gen(torch, M)
+    codes = torch.randn(N, K, generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    scales = 0.005 + 0.015 * torch.rand(-(-N // 128), -(-K // 128), generator=g, device="cuda")
+    lin = dec.Fp8Linear(codes, scales)
+    xs = [torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    plain = [lin.forward(x) for x in xs]
+    x, held, ws = xs[0].clone(), torch.empty_like(plain[0]), lin.workspace(M)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        lin.forward(x, held, ws)
+    for i in (1, 2, 0, 1):
+        x.copy_(xs[i])
+        ws.fill_(0xA5)
+        graph.replay()
+        assert torch.equal(held, plain[i])
+    lin.check()
+
+
+FIRST_CALL = """
+import sys, torch
+from block_fp8_expert_gb300 import decoder
+g = torch.Generator(device="cuda"); g.manual_seed(0)
+M, N, K = {M}, 2048, 2048
+codes = torch.randn(N, K, generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+lin = decoder.Fp8Linear(codes, torch.rand(16, 16, generator=g, device="cuda"))
+x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+out, ws = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), lin.workspace(M)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    lin.forward(x, out, ws)
+graph.replay()
+torch.cuda.synchronize()
+held = out.clone()
+assert torch.equal(lin.forward(x), held) and torch.isfinite(held).all()
+lin.check()
+print("same")
+"""
+
+
+@pytest.mark.parametrize("M", [200, 1300])
+def test_first_call_of_a_process_in_a_capture(torch, M):
+    """What a first call sets up (shared-memory limits, the clusters that fit,
+    the tensor maps' encoder) can be set up while a stream is captured."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(M=M)], capture_output=True, text=True, timeout=280,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+def test_functions_on_addresses_are_the_objects_calls(torch):
+    """The functions of the binding that take plain addresses and structures
+    give the bits of the objects, which call the library themselves."""
+    from block_fp8_expert_gb300 import _lib as lib
+    import block_fp8_expert_gb300 as package
+    dec, g = _dec(), _gen(torch, 12)
+    T, E, k, Hq, Hkv, D, ps = 5, 64, 4, 8, 2, 64, 16
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    sel = dec.ExpertSelector(E, k, "sigmoid", bias, 8, 4, 2)
+    idx, w = sel.forward(logits)
+    i2, w2 = torch.empty_like(idx), torch.empty_like(w)
+    package.moe_select_experts(logits, E, bias, sel.rule, T, E, k, i2, w2)
+    assert torch.equal(idx, i2) and torch.equal(w, w2)
+
+    qkv = torch.randn(T, (Hq + 2 * Hkv) * D, generator=g, device="cuda").to(torch.bfloat16)
+    table = dec.rope_cos_sin(50, D)
+    pos = torch.tensor([3, 0, 49, 7, 8], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([17, 2, 40, 0, 33], device="cuda")
+    a, b = (dec.PagedCache.empty(4, Hkv, ps, D) for _ in range(2))
+    rope = dec.QkNormRope(Hq, Hkv, D, cos_sin=table)
+    q = rope.forward(qkv, pos, slots, a)
+    q2 = torch.empty_like(q)
+    d = lib.QkDims(T, Hq, D, 0, 50, 1e-6, qkv.stride(0), Hq * D)
+    package.moe_qk_norm_rope(qkv, None, None, table, pos, slots, d, b.abi(), q2, rope.status)
+    assert torch.equal(q, q2) and torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+
+    pages = torch.tensor([[1, 0], [0, 2], [2, 1], [3, 3], [2, 0]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([20, 1, 32, 0, 17], dtype=torch.int32, device="cuda")
+    attn = dec.PagedAttention(Hq, Hkv, D)
+    o = attn.forward(q, a, pages, lens)
+    o2 = torch.empty_like(o)
+    d = lib.AttnDims(T, Hq, 2, 0, D ** -0.5, 2, Hq * D, Hq * D)
+    ws = torch.empty(lib.paged_attention_workspace_bytes(d, D), dtype=torch.uint8, device="cuda")
+    package.moe_paged_attention(q, b.abi(), pages, lens, d, o2, ws, attn.status)
+    assert torch.equal(o, o2)
+
+    codes = torch.randn(128, Hq * D, generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    scales = torch.rand(1, Hq * D // 128, generator=g, device="cuda")
+    lin = dec.Fp8Linear(codes, scales)
+    x = o.view(T, Hq * D)
+    y = lin.forward(x)
+    y2 = torch.empty_like(y)
+    d = lib.LinearDims(T, 128, Hq * D, Hq * D, 128)
+    ws = torch.empty(lib.linear_fp8_workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    package.moe_linear_fp8(x, lib.Fp8Mat(codes.data_ptr(), scales.data_ptr()), None, d, y2, ws, lin.status)
+    assert torch.equal(y, y2)
+    for op in (rope, attn, lin):
+        op.check()
+
+
+def test_example_layers_routing(torch):
+    """The example's router and selection against float64 on tokens whose choice
+    hangs on no small difference, which most have to be."""
+    from examples.decoder_layer import DecoderLayer
+    E, k, groups, top = 16, 2, 4, 2
+    L = DecoderLayer(64, 16, H=256, Hq=4, Hkv=2, D=64, I=128, E=E, k=k, groups=groups, top_groups=top, page=4, seed=7)
+    h = torch.randn(64, 256, generator=_gen(torch, 2), device="cuda").to(torch.bfloat16)
+    idx, w = L.select.route(h, L.moe, L.moe_ws)
+    L.check()
+    score = torch.sigmoid(h.double() @ L.moe.Wr.double().t())
+    key = (score + L.select.bias.double()).view(64, groups, -1)
+    gs = key.topk(2, -1).values.sum(-1).sort(1, descending=True)
+    keep = torch.zeros(64, groups, device="cuda").scatter(1, gs.indices[:, :top], 1.0).unsqueeze(-1) > 0
+    flat = key.masked_fill(~keep, -math.inf).flatten(1).sort(1, descending=True)
+    clear = (gs.values[:, top - 1] - gs.values[:, top] > 1e-4) & (
+        flat.values[:, :k] - flat.values[:, 1:k + 1] > 1e-4).all(1)
+    assert clear.sum() > 48
+    assert torch.equal(idx[clear].long(), flat.indices[clear, :k])
+    s = score.gather(1, idx.long())
+    ref = s / s.sum(1, keepdim=True)
+    assert ((w.double() - ref).abs() <= 1e-4 * ref).all()
