@@ -180,16 +180,6 @@ __device__ __forceinline__ uint64_t sw64_desc(uint32_t smem_addr) {
   return d;
 }
 
-// D (+)= A B^T, A [128 x 32] and B [N x 32] E4M3 from shared memory, fp32 D.
-__device__ __forceinline__ void mma_f8_ss(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // One float -> E4M3 code, round to nearest even, saturated to +-448.
 __device__ __forceinline__ uint32_t f32_to_e4m3(float v) {
   uint16_t r;
@@ -417,8 +407,8 @@ k_expert_gemm_f8(const __grid_constant__ CUtensorMap cm0, const __grid_constant_
               const uint32_t a_addr = smem_base + OFF_C + (h ? sc1 : sc0) * C_BYTES + blk * (BW * BK);
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk)
-                mma_f8_ss(tmem + COL_P + blk * BT, sw64_desc(a_addr + kk * 32),
-                          sw64_desc(b_addr + kk * 32), idesc, (h | kk) ? 1u : 0u);
+                tc::mma_f8(tmem + COL_P + blk * BT, sw64_desc(a_addr + kk * 32),
+                           sw64_desc(b_addr + kk * 32), idesc, (h | kk) ? 1u : 0u);
             }
             tc::commit(&sh.p_full[blk]);
           }

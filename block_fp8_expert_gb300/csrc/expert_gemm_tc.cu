@@ -1019,12 +1019,13 @@ cudaError_t get_encoder(EncodeTiled* out) {
 
 // 2-D map over a row-major matrix [rows, cols] of esize-byte elements.
 cudaError_t make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, int esize, const void* base,
-                        long long rows, int cols, int box_cols, int box_rows, int swizzle_bytes) {
+                        long long rows, int cols, int box_cols, int box_rows, int swizzle_bytes,
+                        long long row_stride) {
   EncodeTiled enc;
   cudaError_t e = get_encoder(&enc);
   if (e != cudaSuccess) return e;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * esize};
+  const cuuint64_t strides[1] = {(cuuint64_t)(row_stride ? row_stride : cols) * esize};
   const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r =

@@ -262,14 +262,6 @@ __device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 // (a.x, a.y) += (p.x, p.y) * (f, f)
 __device__ __forceinline__ void fma2(float2& a, uint32_t p0, uint32_t p1, float f) {
   asm("{\n .reg .b64 A, P, F;\n mov.b64 A, {%0, %1};\n mov.b64 P, {%2, %3};\n mov.b64 F, {%4, %4};\n"
@@ -344,7 +336,10 @@ __device__ __forceinline__ float bias_at(const GemmArgs& a, int n) {
 // one thread of warp 1 issues the four K = 32 MMAs of a block into one of two
 // TMEM buffers, and warps 2-9 add the block's sums, times Sx of their row and
 // Sw of the tile, to fp32 sums in registers (a thread: one row, 64 features).
-// The weights' first stages are on their way before the quantisation ends.
+// The weights' first stages are on their way before the quantisation ends: only
+// warp 0 waits for the kernel before, and only for what it wrote.  The kernel
+// before that has ended by then, as this one may only follow a kernel that
+// triggers it after its own wait (k_linear_quant).
 // A cluster's sums meet in shared memory: each CTA owns a share of the rows, the
 // others store theirs for it straight from registers, and it adds them in the
 // CTAs' order and writes the result.
@@ -443,7 +438,7 @@ k_linear_gemm(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ 
         const uint32_t xa = smem_u32(smem) + s * G_STAGE, wa = xa + G_TILE;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_f8(tmem + b * GN, tc::sw128_desc(xa + 32 * k), tc::sw128_desc(wa + 32 * k), idesc, k > 0);
+          tc::mma_f8(tmem + b * GN, tc::sw128_desc(xa + 32 * k), tc::sw128_desc(wa + 32 * k), idesc, k > 0);
         tc::commit(&sh.empty[s]);
         tc::commit(&sh.p_full[b]);
       }
@@ -564,32 +559,6 @@ cudaError_t launch_stream(const LinArgs& a, cudaStream_t s) {
   return launch_k(k_linear_stream<NT, 4>, grid, dim3(128), 0, s, true, a);
 }
 
-// TMA map of the output [M, N], rows `stride` elements apart: 64 features x 32
-// rows per box, 128-byte swizzled.
-cudaError_t output_map(CUtensorMap* map, uint16_t* out, int M, int N, long long stride) {
-  using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static const EncodeTiled encode = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                           cudaEnableDefault, &found);
-    return e == cudaSuccess && found == cudaDriverEntryPointSuccess
-               ? reinterpret_cast<EncodeTiled>(fn)
-               : nullptr;
-  }();
-  if (!encode) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M}, strides[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t box[2] = {64, 32}, step[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
-}
-
 struct LinWs {
   size_t codes, sxt, total;
   int ld;
@@ -679,7 +648,9 @@ cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const flo
                                 kScaleBlock, GM, 128)) != cudaSuccess ||
       (err = make_tensor_map_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, d.N, d.K,
                                 kScaleBlock, GN, 128)) != cudaSuccess ||
-      (err = output_map(&omap, out, d.M, d.N, d.out_stride)) != cudaSuccess)
+      // stored 64 features x 32 rows at a time
+      (err = make_tensor_map_2d(&omap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, d.M, d.N, 64, 32, 128,
+                                d.out_stride)) != cudaSuccess)
     return err;
   const long long groups = (long long)d.M * nkb;
   err = launch_k(k_linear_quant, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, s, true, x,

@@ -45,12 +45,13 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
 // (host-side attribute; the first call on a device should precede capture).
 cudaError_t ensure_smem(const void* func, int bytes);
 
-// 2-D TMA map over a row-major matrix [rows, cols] of esize-byte elements:
-// box = box_cols x box_rows, swizzle 0, 64 or 128 bytes, L2 256-byte
-// promotion, out-of-range elements read as zero.
+// 2-D TMA map over a row-major matrix [rows, cols] of esize-byte elements, its
+// rows row_stride elements apart (0: cols): box = box_cols x box_rows, swizzle
+// 0, 64 or 128 bytes, L2 256-byte promotion, out-of-range elements read as zero
+// and are not stored.
 cudaError_t make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, int esize,
                                const void* base, long long rows, int cols, int box_cols,
-                               int box_rows, int swizzle_bytes);
+                               int box_rows, int swizzle_bytes, long long row_stride = 0);
 
 // Largest expert count the library accepts.
 constexpr int kMaxExperts = 1024;

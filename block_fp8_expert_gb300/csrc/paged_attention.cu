@@ -4,7 +4,8 @@
 //   out = sum_t p_t v_t / sum_t p_t,   p_t = 2^(s_t - m),  s_t = scale log2(e) q . k_t
 //
 // in one pass over the cache with a running maximum m and sum l; the query
-// heads of one key/value head (padded to 16) share every cache element read.
+// heads of one key/value head (up to eight, padded to 8, or 16 of them, padded
+// to 16, at a time) share every cache element read.
 #include <unistd.h>
 
 #include <algorithm>
@@ -61,7 +62,7 @@ struct AttnArgs {
   const int32_t* block_table;
   const int32_t* seq_lens;
   moe_attn_dims d;
-  int G, rows, gtiles, HG;  // query heads per kv head; a segment's heads; segments per kv head, in all
+  int G, gtiles, HG;  // query heads per kv head; segments per kv head, in all
   int tile;                 // tokens per tile
   uint32_t ps_mul, ps_shift;  // t / page_size = umulhi(t, ps_mul) >> ps_shift (page_size > 1)
   uint16_t* out;
@@ -973,7 +974,6 @@ cudaError_t launch_attn_nh(AttnArgs& a, cudaStream_t s) {
   static_assert(S::kCtasPerSm <= 3, "attn_max_grid");
   cudaError_t err = ensure_smem((const void*)k_paged_attention<D, E4M3, NH>, S::kSmem);
   if (err != cudaSuccess) return err;
-  a.rows = S::kRows;
   a.tile = S::kTile;
   a.gtiles = cdiv(a.G, S::kRows);
   a.HG = a.c.Hkv * a.gtiles;
