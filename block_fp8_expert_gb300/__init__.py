@@ -14,5 +14,6 @@ from ._lib import (  # noqa: F401
     moe_route, moe_permute, moe_expert_ffn_fp8, moe_combine, moe_layer_forward,
     moe_layer_forward_gated, moe_layer_forward_act8,
     moe_read_device_status, kernel_launches, expert_uses_gemm,
-    moe_select_experts, moe_route_select, moe_qk_norm_rope, moe_paged_attention, moe_linear_fp8,
+    moe_select_experts, moe_route_select, moe_experts_forward, moe_qk_norm_rope,
+    moe_paged_attention, moe_linear_fp8,
 )

@@ -439,14 +439,14 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Parts& p, in
 // conversion to fp16, the values' codes of two tokens paired by byte permutes.
 // A weight rounded to bf16 once would be as far off as the output's own
 // rounding (2 x 131072 tokens: 1.95e-3 of the 64-bit result instead of 1.64e-3),
-// so bf16 values are multiplied by it in two parts (90.6 -> 91.2 us, 64 ragged
-// sequences 59.6 -> 59.9).  Next to E4M3 values one fp16 part stays: it rounds
+// so bf16 values are multiplied by it in two parts (90.1 -> 90.6 us, 64 ragged
+// sequences 59.5 -> 59.7).  Next to E4M3 values one fp16 part stays: it rounds
 // eight times finer than the output, and a second one costs more there (48
-// ragged sequences 24.6 -> 25.7 us, 16 of 8000 with 16 heads of 256 51 -> 54).
+// ragged sequences 24.6 -> 25.7 us, 16 of 8000 with 16 heads of 256 41.7 -> 46.5).
 //
 // Bound by HBM once its pipelines are full: 2 x 131072 tokens, 4 heads of 128,
 // bf16: 537 MB in 90.6 us, 5.9 TB/s, 0.88 of the copy rate; what is lost is
-// the first 5 us (lengths, page numbers, rows: loads that wait for one
+// the first 5.6 us (lengths, page numbers, rows: loads that wait for one
 // another), the SMs' uneven rates (the last ends 12% after the mean) and the
 // join.  64 ragged sequences up to 12000: 59.8 us; 48 up to 4096, E4M3: 24.5
 // us, 0.51 of the copy rate (the bytes alone take 12).  (With the heads as the

@@ -66,8 +66,9 @@ __device__ __forceinline__ void load_f32x8(const float* p, float* f) {
 // bf16: 172 MB in 30.9 us, 5.6 TB/s, 0.82 of the copy rate (with eight
 // dimensions per lane and shuffles for the partners 64.9; the loads in
 // registers 37.6; warps that walk over several tokens 39.7; a ring of 3 or
-// 6, or fewer registers for more warps, 34 to 47).  T 517, 16 + 2 + 2 heads of
-// 256, E4M3: 5.7 us, T 8: 2.2, both latency: the token's place, then its heads.
+// 6, or fewer registers for more warps, 34 to 47).  T 8: 2.2 us,
+// latency: the token's place, then its heads.  T 517, 16 + 2 + 2 heads of 256,
+// E4M3: 5.7 us, the latency and 6.4 ns per token, which bf16 takes as well.
 template <int D>
 __global__ void __launch_bounds__(128, kCtasPerSm)
 k_qk_norm_rope(const QkArgs a) {

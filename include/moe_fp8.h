@@ -456,7 +456,8 @@ moe_status moe_experts_forward(const uint16_t* x, const int32_t* topk_idx,
  * multiples of 16 bytes.  MOE_KV_BF16: bf16 elements, k_scale and v_scale
  * NULL.  MOE_KV_E4M3: E4M3 codes, and one float per token and head at
  * element page * scale_page_stride + h * scale_head_stride + offset *
- * scale_token_stride of k_scale and of v_scale; the value is code * scale. */
+ * scale_token_stride of k_scale and of v_scale; the value is code * scale, a
+ * scale being 0 or positive. */
 typedef struct {
   void* k;
   void* v;
