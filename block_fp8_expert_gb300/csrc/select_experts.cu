@@ -63,7 +63,7 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
                  long long slice_stride, const float* __restrict__ logit_bias,
                  const float* __restrict__ bias, const moe_select_rule rule, int n, int span_log2,
                  int T, int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
-                 const int32_t* __restrict__ found, int32_t* __restrict__ status) {
+                 const int32_t* found, int32_t* status) {
   constexpr unsigned kAll = 0xffffffffu;
   griddep_wait();
   griddep_trigger();
@@ -72,7 +72,7 @@ k_select_experts(const float* __restrict__ logits, long long row_stride, int sli
   if (t >= T) return;  // warp-uniform
   // what the kernels before found, where the caller keeps it
   if (found && t == 0 && lane == 0) {
-    const int32_t bits = *found;
+    const int32_t bits = __ldcg(found);
     if (bits) raise_status(status, bits);
   }
   const int g = lane >> span_log2, place = (lane & ((1 << span_log2) - 1)) * EPL;
