@@ -92,6 +92,29 @@ class LinearDims(ctypes.Structure):
                 ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
 
 
+class DraftDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("n", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("table_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("q_row_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
+                ("mask_stride", ctypes.c_int64)]
+
+
+class LatentPages(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("R", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class LatentDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_pos", ctypes.c_int32), ("eps", ctypes.c_float), ("kv_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+                ("rows_stride", ctypes.c_int64)]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
@@ -129,6 +152,14 @@ _SIGNATURES = {
     "moe_qk_norm_rope": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, QkDims, KvCache, _vp, _vp, _vp]),
     "moe_paged_attention_workspace_bytes": (_st, [AttnDims, _i32, ctypes.POINTER(_sz)]),
     "moe_paged_attention": (_st, [_vp, KvCache, _vp, _vp, AttnDims, _vp, _vp, _sz, _vp, _vp]),
+    "moe_tree_attention_workspace_bytes": (_st, [DraftDims, _i32, _i32, ctypes.POINTER(_sz)]),
+    "moe_tree_attention": (_st, [_vp, KvCache, _vp, _vp, _vp, _vp, DraftDims, _vp, _vp, _sz, _vp,
+                                 _vp]),
+    "moe_latent_store": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, LatentDims, LatentPages, _vp, _vp, _vp,
+                               _vp]),
+    "moe_latent_attention_workspace_bytes": (_st, [DraftDims, _i32, ctypes.POINTER(_sz)]),
+    "moe_latent_attention": (_st, [_vp, LatentPages, _vp, _vp, _vp, _vp, DraftDims, _vp, _vp, _sz,
+                                   _vp, _vp]),
     "moe_linear_fp8_workspace_bytes": (_st, [LinearDims, ctypes.POINTER(_sz)]),
     "moe_linear_fp8": (_st, [_vp, Fp8Mat, _vp, LinearDims, _vp, _vp, _sz, _vp, _vp]),
 }
@@ -341,6 +372,41 @@ def moe_paged_attention(q, cache: KvCache, block_table, seq_lens, d: AttnDims, o
     _check(lib().moe_paged_attention(_ptr(q), cache, _ptr(block_table), _ptr(seq_lens), d,
                                      _ptr(out), _ptr(ws), _nbytes(ws), _ptr(status),
                                      _stream(stream)), "moe_paged_attention")
+
+
+def tree_attention_workspace_bytes(d: DraftDims, Hkv: int, D: int) -> int:
+    n = _sz(0)
+    _check(lib().moe_tree_attention_workspace_bytes(d, Hkv, D, ctypes.byref(n)),
+           "moe_tree_attention_workspace_bytes")
+    return n.value
+
+
+def moe_tree_attention(q, cache: KvCache, block_table, seq_lens, mask, draft_lens, d: DraftDims, out,
+                       ws, status=None, stream=None) -> None:
+    _check(lib().moe_tree_attention(_ptr(q), cache, _ptr(block_table), _ptr(seq_lens), _ptr(mask),
+                                    _ptr(draft_lens), d, _ptr(out), _ptr(ws), _nbytes(ws),
+                                    _ptr(status), _stream(stream)), "moe_tree_attention")
+
+
+def moe_latent_store(kv, norm, cos_sin, pos, slots, q, d: LatentDims, cache: LatentPages, q_out, rows,
+                     status=None, stream=None) -> None:
+    _check(lib().moe_latent_store(_ptr(kv), _ptr(norm), _ptr(cos_sin), _ptr(pos), _ptr(slots), _ptr(q),
+                                  d, cache, _ptr(q_out), _ptr(rows), _ptr(status), _stream(stream)),
+           "moe_latent_store")
+
+
+def latent_attention_workspace_bytes(d: DraftDims, R: int) -> int:
+    n = _sz(0)
+    _check(lib().moe_latent_attention_workspace_bytes(d, R, ctypes.byref(n)),
+           "moe_latent_attention_workspace_bytes")
+    return n.value
+
+
+def moe_latent_attention(q, cache: LatentPages, block_table, seq_lens, mask, draft_lens, d: DraftDims,
+                         out, ws, status=None, stream=None) -> None:
+    _check(lib().moe_latent_attention(_ptr(q), cache, _ptr(block_table), _ptr(seq_lens), _ptr(mask),
+                                      _ptr(draft_lens), d, _ptr(out), _ptr(ws), _nbytes(ws),
+                                      _ptr(status), _stream(stream)), "moe_latent_attention")
 
 
 def linear_fp8_workspace_bytes(d: LinearDims) -> int:

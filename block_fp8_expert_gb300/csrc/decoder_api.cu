@@ -70,6 +70,65 @@ moe_status check_rule(const moe_select_rule& rule, int E, int k) {
   return MOE_OK;
 }
 
+moe_status check_draft(const moe_draft_dims& d, int Hkv) {
+  if (d.B < 0 || d.window < 0 || d.table_width < 0)
+    return fail(MOE_ERR_INVALID_ARG, "B = %d, window = %d, table_width = %d", d.B, d.window,
+                d.table_width);
+  if (d.n < 1 || d.n > 64) return fail(MOE_ERR_UNSUPPORTED, "n = %d new tokens outside [1, 64]", d.n);
+  if (d.Hq < 1 || d.Hq > 1024) return fail(MOE_ERR_UNSUPPORTED, "Hq = %d outside [1, 1024]", d.Hq);
+  if (Hkv < 1 || Hkv > 1024) return fail(MOE_ERR_UNSUPPORTED, "Hkv = %d outside [1, 1024]", Hkv);
+  if (d.Hq % Hkv)
+    return fail(MOE_ERR_UNSUPPORTED, "Hq = %d is no multiple of Hkv = %d", d.Hq, Hkv);
+  if (d.n * (d.Hq / Hkv) > 8192)
+    return fail(MOE_ERR_UNSUPPORTED, "n * Hq / Hkv = %d: at most 8192", d.n * (d.Hq / Hkv));
+  if (d.window > 0 && d.window < d.n)
+    return fail(MOE_ERR_UNSUPPORTED, "window = %d: need 0, or at least the n = %d new tokens", d.window, d.n);
+  // the joining grid, and the outputs' rows
+  if ((long long)d.B * Hkv * ((d.n * (d.Hq / Hkv) + 63) / 64) >= (1ll << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "B * n * Hq too large");
+  return MOE_OK;
+}
+
+// What moe_tree_attention and moe_latent_attention check alike; Dq and DV: the
+// query and output elements of a head.
+moe_status check_draft_call(const moe_draft_dims& d, int Hkv, int Dq, int DV, const uint16_t* q,
+                            const int32_t* block_table, const int32_t* seq_lens,
+                            const int64_t* mask, const int32_t* draft_lens, const uint16_t* out,
+                            const void* ws, size_t ws_bytes) {
+  moe_status s;
+  if (d.table_stride < d.table_width)
+    return fail(MOE_ERR_INVALID_ARG, "table_stride = %lld < table_width", (long long)d.table_stride);
+  if ((s = check_stride(d.q_row_stride, (long long)d.Hq * Dq, 8, "q_row_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.out_row_stride, (long long)d.Hq * DV, 8, "out_row_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.q_stride, 0, 8, "q_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.out_stride, (long long)(d.B > 1 ? d.Hq : 0) * DV, 8, "out_stride")) != MOE_OK) return s;
+  if (mask && d.mask_stride != 0 && d.mask_stride < d.n)
+    return fail(MOE_ERR_INVALID_ARG, "mask_stride = %lld: need 0 or at least n = %d", (long long)d.mask_stride, d.n);
+  if (d.B == 0) return MOE_OK;
+  REQUIRE_PTR(q);
+  if (d.table_width > 0) REQUIRE_ELEMENTS(block_table);
+  REQUIRE_ELEMENTS(seq_lens);
+  if (mask) REQUIRE_ELEMENTS(mask);
+  if (draft_lens) REQUIRE_ELEMENTS(draft_lens);
+  REQUIRE_PTR(out);
+  REQUIRE_PTR(ws);
+  const size_t need = align_up(draft_attention_workspace(d, Hkv, DV));
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", ws_bytes, need);
+  return MOE_OK;
+}
+
+moe_status check_latent_cache(const moe_latent_cache& c) {
+  moe_status s;
+  if (c.R != 256 && c.R != 512) return fail(MOE_ERR_UNSUPPORTED, "latent size R = %d: need 256 or 512", c.R);
+  if (c.rot != 64) return fail(MOE_ERR_UNSUPPORTED, "rot = %d: need 64", c.rot);
+  if (c.pages < 1 || c.page_size < 1)
+    return fail(MOE_ERR_INVALID_ARG, "cache of %d pages of %d tokens", c.pages, c.page_size);
+  REQUIRE_PTR(c.data);
+  if ((s = check_stride(c.page_stride, 0, 8, "page_stride")) != MOE_OK) return s;
+  return check_stride(c.token_stride, 0, 8, "token_stride");
+}
+
 moe_status check_linear(const moe_linear_dims& d) {
   if (d.M < 0) return fail(MOE_ERR_INVALID_ARG, "M = %d < 0", d.M);
   if (d.M > (1 << 22)) return fail(MOE_ERR_UNSUPPORTED, "M = %d: at most 2^22 rows", d.M);
@@ -220,6 +279,110 @@ moe_status moe_paged_attention(const uint16_t* q, moe_kv_cache cache, const int3
   CUDA_CHECK(launch_paged_attention(q, cache, block_table, seq_lens, d, out, ws, status,
                                     (cudaStream_t)stream),
              "moe_paged_attention");
+  return MOE_OK;
+}
+
+moe_status moe_tree_attention_workspace_bytes(moe_draft_dims d, int32_t Hkv, int32_t D,
+                                              size_t* bytes) {
+  const moe_status s = check_draft(d, Hkv);
+  if (s != MOE_OK) return s;
+  if (D != 64 && D != 128 && D != 256)
+    return fail(MOE_ERR_UNSUPPORTED, "head size D = %d: need 64, 128 or 256", D);
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = align_up(draft_attention_workspace(d, Hkv, D));
+  return MOE_OK;
+}
+
+moe_status moe_tree_attention(const uint16_t* q, moe_kv_cache cache, const int32_t* block_table,
+                              const int32_t* seq_lens, const int64_t* mask,
+                              const int32_t* draft_lens, moe_draft_dims d, uint16_t* out, void* ws,
+                              size_t ws_bytes, int32_t* status, void* stream) {
+  moe_status s;
+  if ((s = check_cache(cache)) != MOE_OK) return s;
+  if ((s = check_draft(d, cache.Hkv)) != MOE_OK) return s;
+  if (!draft_attention_fits(d, cache))
+    return fail(MOE_ERR_UNSUPPORTED, "B * Hkv * (table_width * page_size / 64 + 5) too large");
+  REQUIRE_OPT_PTR(status);
+  if ((s = check_draft_call(d, cache.Hkv, cache.D, cache.D, q, block_table, seq_lens, mask,
+                            draft_lens, out, ws, ws_bytes)) != MOE_OK)
+    return s;
+  if (d.B == 0) return MOE_OK;
+  CUDA_CHECK(launch_draft_attention(q, cache, false, block_table, seq_lens, mask, draft_lens, d,
+                                    cache.D, out, ws, status, (cudaStream_t)stream),
+             "moe_tree_attention");
+  return MOE_OK;
+}
+
+moe_status moe_latent_store(const uint16_t* kv, const float* norm, const float* cos_sin,
+                            const int32_t* pos, const int64_t* slots, const uint16_t* q,
+                            moe_latent_dims d, moe_latent_cache cache, uint16_t* q_out,
+                            uint16_t* rows, int32_t* status, void* stream) {
+  moe_status s;
+  if (d.T < 0) return fail(MOE_ERR_INVALID_ARG, "T = %d < 0", d.T);
+  if (d.H < 0 || d.H > 1024) return fail(MOE_ERR_UNSUPPORTED, "H = %d outside [0, 1024]", d.H);
+  if ((s = check_latent_cache(cache)) != MOE_OK) return s;
+  if (d.n_pos < 1) return fail(MOE_ERR_INVALID_ARG, "n_pos = %d", d.n_pos);
+  const int width = cache.R + cache.rot;
+  if ((s = check_stride(d.kv_stride, width, 8, "kv_stride")) != MOE_OK) return s;
+  if (rows && (s = check_stride(d.rows_stride, width, 8, "rows_stride")) != MOE_OK) return s;
+  if (d.H > 0) {
+    if ((s = check_stride(d.q_head_stride, cache.rot, 8, "q_head_stride")) != MOE_OK) return s;
+    if ((s = check_stride(d.q_out_head_stride, cache.rot, 8, "q_out_head_stride")) != MOE_OK) return s;
+    if ((s = check_stride(d.q_stride, 0, 8, "q_stride")) != MOE_OK) return s;
+    if ((s = check_stride(d.q_out_stride, 0, 8, "q_out_stride")) != MOE_OK) return s;
+  } else if (q || q_out) {
+    return fail(MOE_ERR_INVALID_ARG, "H = 0 takes no q and no q_out");
+  }
+  REQUIRE_OPT_PTR(norm);
+  REQUIRE_OPT_PTR(rows);
+  REQUIRE_OPT_PTR(status);
+  if (d.T == 0) return MOE_OK;
+  REQUIRE_PTR(kv);
+  REQUIRE_PTR(cos_sin);
+  REQUIRE_ELEMENTS(pos);
+  REQUIRE_ELEMENTS(slots);
+  if (d.H > 0) {
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(q_out);
+  }
+  CUDA_CHECK(launch_latent_store(kv, norm, cos_sin, pos, slots, q, d, cache, q_out, rows, status,
+                                 (cudaStream_t)stream),
+             "moe_latent_store");
+  return MOE_OK;
+}
+
+moe_status moe_latent_attention_workspace_bytes(moe_draft_dims d, int32_t R, size_t* bytes) {
+  const moe_status s = check_draft(d, 1);
+  if (s != MOE_OK) return s;
+  if (R != 256 && R != 512) return fail(MOE_ERR_UNSUPPORTED, "latent size R = %d: need 256 or 512", R);
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = align_up(draft_attention_workspace(d, 1, R));
+  return MOE_OK;
+}
+
+moe_status moe_latent_attention(const uint16_t* q, moe_latent_cache cache,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                const int64_t* mask, const int32_t* draft_lens, moe_draft_dims d,
+                                uint16_t* out, void* ws, size_t ws_bytes, int32_t* status,
+                                void* stream) {
+  moe_status s;
+  if ((s = check_latent_cache(cache)) != MOE_OK) return s;
+  if ((s = check_draft(d, 1)) != MOE_OK) return s;
+  if (d.window) return fail(MOE_ERR_UNSUPPORTED, "window = %d: latent attention has none", d.window);
+  // the same cache as one head, whose values are its keys' leading dimensions
+  const moe_kv_cache kv{cache.data, cache.data, nullptr, nullptr, cache.pages, cache.page_size, 1,
+                        cache.R + cache.rot, MOE_KV_BF16, cache.page_stride, 0, cache.token_stride,
+                        0, 0, 0};
+  if (!draft_attention_fits(d, kv))
+    return fail(MOE_ERR_UNSUPPORTED, "B * (table_width * page_size / 64 + 5) too large");
+  REQUIRE_OPT_PTR(status);
+  if ((s = check_draft_call(d, 1, cache.R + cache.rot, cache.R, q, block_table, seq_lens, mask,
+                            draft_lens, out, ws, ws_bytes)) != MOE_OK)
+    return s;
+  if (d.B == 0) return MOE_OK;
+  CUDA_CHECK(launch_draft_attention(q, kv, true, block_table, seq_lens, mask, draft_lens, d, cache.R,
+                                    out, ws, status, (cudaStream_t)stream),
+             "moe_latent_attention");
   return MOE_OK;
 }
 

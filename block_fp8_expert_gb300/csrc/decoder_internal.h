@@ -55,6 +55,23 @@ cudaError_t launch_paged_attention(const uint16_t* q, const moe_kv_cache& cache,
                                    const moe_attn_dims& d, uint16_t* out, void* ws,
                                    int32_t* status, cudaStream_t s);
 
+// Whether the work units that the block table has room for fit 31 bits.
+bool draft_attention_fits(const moe_draft_dims& d, const moe_kv_cache& cache);
+// Scratch bytes of one call: two partial results per CTA, and where each
+// segment's begin.
+size_t draft_attention_workspace(const moe_draft_dims& d, int Hkv, int DV);
+// latent: cache has one head whose values are its keys' leading DV dimensions.
+cudaError_t launch_draft_attention(const uint16_t* q, const moe_kv_cache& cache, bool latent,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   const int64_t* mask, const int32_t* draft_lens,
+                                   const moe_draft_dims& d, int DV, uint16_t* out, void* ws,
+                                   int32_t* status, cudaStream_t s);
+
+cudaError_t launch_latent_store(const uint16_t* kv, const float* norm, const float* cos_sin,
+                                const int32_t* pos, const int64_t* slots, const uint16_t* q,
+                                const moe_latent_dims& d, const moe_latent_cache& cache,
+                                uint16_t* q_out, uint16_t* rows, int32_t* status, cudaStream_t s);
+
 size_t linear_fp8_workspace(const moe_linear_dims& d);
 cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const float* bias,
                               const moe_linear_dims& d, uint16_t* out, void* ws, int32_t* status,

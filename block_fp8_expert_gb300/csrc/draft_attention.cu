@@ -1,0 +1,908 @@
+// Attention of several new tokens per sequence, which see each other as a tree,
+// over a paged cache: of grouped key/value heads (moe_tree_attention), or of
+// one latent vector per token that is key and value of every head
+// (moe_latent_attention).
+//
+//   out = sum_t p_t v_t / sum_t p_t,   p_t = 2^(s_t - m),  s_t = scale log2(e) q . k_t
+//
+// in one pass over the cache with a running maximum m and sum l.  The rows of a
+// key/value head are its query heads times the new tokens.
+#include <algorithm>
+
+#include "attention_tc.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kTile = 64;      // tokens per tile
+constexpr int kRows = 64;      // rows (query head x new token) of a CTA at most
+constexpr int kChunk = 8192;   // 64 tokens or rows x 64 dimensions, 128-byte swizzled
+constexpr int kSoftWarps = 4;  // softmax, rescaling, output; the MMA warp; the loading warps
+constexpr int kSegCost = 3;    // what a segment costs a CTA beside its tiles, in tiles
+constexpr int kNoRow = 0x7fffffff;
+constexpr int kMinUnits = 2;   // least share of a CTA
+constexpr int kOCol = 2 * kTile;  // TMEM: two buffers of scores, then the outputs
+constexpr long long kMaxTokens = 0x7fffff80;  // of a sequence: its tiles' ends fit 31 bits
+constexpr int kJoinThreads = 512;
+
+// LATENT: the values are the leading DV dimensions of the keys.
+template <int DK, int DV, bool LATENT, bool E4M3>
+struct DraftShape {
+  static constexpr int kKChunks = DK / 64, kVChunks = LATENT ? 0 : DV / 64;
+  static constexpr int kStage = (kKChunks + kVChunks) * kChunk;
+  static constexpr int kVOff = LATENT ? 0 : kKChunks * kChunk;
+  static constexpr int kParts = LATENT ? 1 : 2;  // bf16 parts of a softmax weight
+  static constexpr int kQ = kKChunks * kChunk, kP = kParts * kChunk;
+  static constexpr int kCtas = kStage <= 32 * 1024 && !LATENT ? 2 : 1;  // per SM
+  // barriers and small arrays, the stages' E4M3 scales, and the tiles' alignment
+  static constexpr int kFixed = 1920 + (E4M3 ? 4 * 2 * kTile * 4 : 0) + 1024;
+  static constexpr int kFit = (227 * 1024 / kCtas - kFixed - kQ - kP) / kStage;
+  static constexpr int kStages = kFit >= 4 ? 4 : 2;
+  static_assert(kFit >= 2, "shared memory");
+  static constexpr int kGroupWarps = (kCtas == 1 ? 8 : 4) / kStages;  // loading warps per stage
+  static constexpr int kWarps = kSoftWarps + 1 + kStages * kGroupWarps;
+  static constexpr int kSmem = kQ + kP + kStages * kStage + 1024;
+  static constexpr int kBlocks = DV >= 128 ? DV / 128 : 1;  // of the outputs' dimensions
+  static constexpr int kCols = kOCol + kBlocks * kRows;
+  static constexpr int kTmem = kCols <= 256 ? 256 : 512;
+  static_assert(kTmem * kCtas <= 512, "TMEM");
+};
+
+struct DraftArgs {
+  const uint16_t* q;
+  moe_kv_cache c;  // the latent cache: one head, v = k
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int64_t* mask;        // NULL: every new token sees those before it
+  const int32_t* draft_lens;  // NULL: d.n
+  moe_draft_dims d;
+  int G, rows, gtiles;  // query heads per key/value head; n G; CTAs that share them
+  int cols;             // columns of the grid
+  uint32_t ps_mul, ps_shift;  // t / page_size = umulhi(t, ps_mul) >> ps_shift (page_size > 1)
+  uint16_t* out;
+  float* part_o;   // [2 cols][gtiles][kRows][DV]
+  float* part_ml;  // [2 cols][gtiles][2][kRows]
+  int2* info;      // [B][Hkv]: the segment's first slot, its parts
+  int32_t* status;
+};
+
+// A sequence's cached tokens [lo, len), of which those from ctx on are new.
+struct Span {
+  int lo, len, ctx, first, tiles;
+};
+__device__ __forceinline__ int drafted(const DraftArgs& a, int b) {
+  return a.draft_lens ? a.draft_lens[b] : a.d.n;
+}
+__device__ __forceinline__ Span span_of(const DraftArgs& a, int b, bool* bad = nullptr) {
+  const int len0 = a.seq_lens[b], n0 = drafted(a, b);
+  const long long cap = min((long long)a.d.table_width * a.c.page_size, kMaxTokens);
+  Span s;
+  s.len = (int)min((long long)max(len0, 0), cap);
+  const int n = min(min(max(n0, 0), a.d.n), s.len);
+  if (bad) *bad = s.len != len0 || (a.draft_lens || s.len > 0 ? n != n0 : false);
+  s.ctx = s.len - n;
+  s.lo = a.d.window > 0 ? max(0, s.ctx + 1 - a.d.window) : 0;
+  s.first = s.lo / kTile;
+  s.tiles = n > 0 ? (int)(((long long)s.len + kTile - 1) / kTile) - s.first : 0;
+  return s;
+}
+
+// A sequence's tiles for one key/value head are a segment of tiles + kSegCost
+// units; sequences without new tokens have none.  All segments lie in one row,
+// sequence-major, then head; column c of the grid takes units [c share, (c + 1)
+// share) of it, and with them the same part of each segment's tiles.  The CTAs
+// of a column do so for different rows of queries: they read the same tiles at
+// about the same time, so HBM gives them once.
+__device__ __forceinline__ int units_of(const Span& s) { return s.tiles ? s.tiles + kSegCost : 0; }
+// The tile at which unit u of a segment begins, in fp32: the columns on either
+// side get the same answer, and it never falls as u grows.
+__device__ __forceinline__ int tile_at(const Span& s, int u) {
+  const int units = units_of(s);
+  return u <= 0 ? 0 : u >= units ? s.tiles : min(s.tiles, (int)(u * ((float)s.tiles / (float)units)));
+}
+
+// What a column does, one segment's part after the other.
+struct Part {
+  int b, hkv, tile, n;  // tiles [tile, tile + n), in tiles of the sequence
+  int slot;             // of a part's results; -1: the whole segment
+  int parts;            // of the segment, if it begins here; else 0
+  Span sp;
+};
+struct Walk {
+  int b, before, cur, end, first, share;
+  Span sp;
+  __device__ __forceinline__ bool next(const DraftArgs& a, Part& p) {
+    if (cur >= end) return false;
+    while (cur >= before + units_of(sp) * a.c.Hkv) {
+      before += units_of(sp) * a.c.Hkv;
+      sp = span_of(a, ++b);
+    }
+    const int units = units_of(sp);
+    p.hkv = (cur - before) / units;
+    const int s0 = before + p.hkv * units, s1 = s0 + units, stop = min(s1, end);
+    const int i0 = tile_at(sp, cur - s0), i1 = tile_at(sp, stop - s0);
+    p.b = b;
+    p.tile = sp.first + i0;
+    p.n = i1 - i0;
+    p.slot = cur == s0 && stop == s1 ? -1 : 2 * (cur / share) + (cur == first ? 0 : 1);
+    p.parts = cur == s0 ? (s1 - 1) / share - cur / share + 1 : 0;
+    p.sp = sp;
+    cur = stop;
+    return true;
+  }
+  // The next part that has tiles.
+  __device__ __forceinline__ bool next_tiles(const DraftArgs& a, Part& p) {
+    while (next(a, p))
+      if (p.n > 0) return true;
+    return false;
+  }
+};
+
+// Every thread of the CTA calls this.
+template <int WARPS>
+__device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned* s_scan, Walk* s_walk) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = cdiv(a.d.B, WARPS * 32), b0 = min(tid * per, a.d.B), b1 = min(b0 + per, a.d.B);
+  if (tid == 0) *s_walk = Walk{0, 0, 0, 0, 0, 1, Span{0, 0, 0, 0, 0}};
+  unsigned mine = 0;
+  for (int b = b0; b < b1; ++b) mine += units_of(span_of(a, b));
+  unsigned incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned x = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  unsigned before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const unsigned v = s_scan[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  total *= a.c.Hkv;
+  const unsigned share = max((unsigned)kMinUnits, (total + a.cols - 1) / a.cols);
+  const unsigned want = min((unsigned)col * share, total);
+  if (before * a.c.Hkv <= want && want < (before + mine) * a.c.Hkv) {
+    Walk w;
+    w.sp = Span{0, 0, 0, 0, 0};
+    for (w.b = b0; w.b < b1; ++w.b) {
+      w.sp = span_of(a, w.b);
+      const unsigned u = units_of(w.sp);
+      if (want < (before + u) * a.c.Hkv) break;
+      before += u;
+    }
+    w.before = (int)(before * a.c.Hkv);
+    w.cur = w.first = (int)want;
+    w.end = (int)min(want + share, total);
+    w.share = (int)share;
+    *s_walk = w;
+  }
+  __syncthreads();
+  return *s_walk;
+}
+
+template <int STAGES, int WARPS, bool E4M3>
+struct DraftShared {
+  uint64_t full[STAGES], empty[STAGES], s_full[2], s_empty[2], p_full, pv_done, q_full;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  int add_to;  // the tile's products are added to what the outputs hold
+  uint32_t exists[STAGES][2];      // tokens of the stage that are there
+  alignas(8) float scale[E4M3 ? STAGES : 1][2][E4M3 ? kTile : 1];  // of its keys and values
+  float factor[kRows];             // on the outputs of a row, when its maximum moves
+  float inv[kRows];                // 1 / the row's sum
+  uint64_t seen[kRows];            // tokens of the tile that a row sees
+  long long at[kRows];             // the rows' outputs, in elements; -1: none
+  unsigned scan[WARPS];
+  Walk walk;
+};
+
+// E4M3 codes -> bf16, exact (every E4M3 value is a bf16 value); NaN stays NaN.
+__device__ __forceinline__ uint4 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
+  const uint32_t h[4] = {e4m3x2_to_f16x2(lo & 0xFFFFu), e4m3x2_to_f16x2(lo >> 16),
+                         e4m3x2_to_f16x2(hi & 0xFFFFu), e4m3x2_to_f16x2(hi >> 16)};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    r[i] = pack_bf16x2(f.x, f.y);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t v) {
+  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+}
+
+}  // namespace
+
+template <int DK, int DV, bool LATENT, bool E4M3>
+__global__ void __launch_bounds__(DraftShape<DK, DV, LATENT, E4M3>::kWarps * 32,
+                                  DraftShape<DK, DV, LATENT, E4M3>::kCtas)
+k_draft_attention(const DraftArgs a) {
+  using S = DraftShape<DK, DV, LATENT, E4M3>;
+  constexpr int ST = S::kStages, GW = S::kGroupWarps;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ DraftShared<ST, S::kWarps, E4M3> sh;
+  static_assert(sizeof(sh) + 1024 <= S::kFixed, "shared memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                   ~(uintptr_t)1023);
+  uint8_t* const sm_q = smem;
+  uint8_t* const sm_p = smem + S::kQ;
+  uint8_t* const sm_kv = smem + S::kQ + S::kP;
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&sh.full[i], GW);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_empty[i], kSoftWarps);
+    }
+    mbar_init(&sh.p_full, kSoftWarps);
+    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.q_full, kSoftWarps);
+    sh.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kSoftWarps) {
+    tc::tmem_alloc(&sh.tmem_base, S::kTmem);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;
+  griddep_wait();
+  griddep_trigger();
+
+  const int col = blockIdx.x / a.gtiles, rt = blockIdx.x % a.gtiles;
+  const int row0 = rt * kRows, rows = min(kRows, a.rows - row0);
+  const int npad = cdiv(rows, 16) * 16;
+  Walk walk = plan<S::kWarps>(a, col, sh.scan, &sh.walk);
+  volatile int* const dead = &sh.abort_flag;
+
+  if (warp > kSoftWarps) {
+    // ---- loading: a group of warps per stage, so that waiting for one
+    // stage's copies holds up no other
+    const int pw = warp - kSoftWarps - 1, stage = pw / GW, gw = pw % GW;
+    constexpr int TW = kTile / GW;           // tokens of a warp
+    constexpr int LL = TW < 32 ? 1 : TW / 32;  // of a lane
+    uint8_t* const dst = sm_kv + stage * S::kStage;
+    struct Tok {
+      long long at;   // elements from the head's first; -1: no such token
+      long long sat;  // E4M3: of its scales
+    };
+    Part p;
+    bool more = walk.next_tiles(a, p);
+    int i = stage;  // the tile of this part
+    auto settle = [&]() {
+      while (more && i >= p.n) {
+        i -= p.n;
+        more = walk.next_tiles(a, p);
+      }
+    };
+    auto look_up = [&](Tok (&tk)[LL]) {
+#pragma unroll
+      for (int u = 0; u < LL; ++u) {
+        tk[u].at = -1;
+        tk[u].sat = 0;
+        const int tok = (p.tile + i) * kTile + gw * TW + 32 * u + (TW < 32 ? lane % TW : lane);
+        if (!more || tok < p.sp.lo || tok >= p.sp.len) continue;
+        const uint32_t idx = a.c.page_size > 1 ? __umulhi((uint32_t)tok, a.ps_mul) >> a.ps_shift : tok;
+        const int in = tok - (int)(idx * (uint32_t)a.c.page_size);
+        const int page = __ldg(a.block_table + (size_t)p.b * a.d.table_stride + idx);
+        if (page < 0 || page >= a.c.pages) {
+          raise_status(a.status, MOE_DEV_BAD_PAGE);
+          continue;
+        }
+        tk[u].at = page * a.c.page_stride + p.hkv * a.c.head_stride + in * a.c.token_stride;
+        if (E4M3)
+          tk[u].sat = page * a.c.scale_page_stride + p.hkv * a.c.scale_head_stride +
+                      in * a.c.scale_token_stride;
+      }
+    };
+    settle();
+    Tok tk[LL];
+    look_up(tk);
+    for (int round = 0; more; ++round) {
+      // the tokens' addresses are handed out before the next tile's are looked up
+      if (E4M3) {
+        // codes to registers, and as bf16 into the stage once it is free
+        constexpr int LPR = DK / 16;            // lanes (16-byte chunks) per token row
+        constexpr int NI = TW * LPR / 32;       // loads per lane and matrix
+        uint4 kc[NI], vc[NI];
+        float ks[LL], vs[LL];
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+          const int r = n * (32 / LPR) + lane / LPR;
+          const long long o = __shfl_sync(kAll, tk[n * (32 / LPR) / 32].at, r & 31);
+          kc[n] = vc[n] = make_uint4(0, 0, 0, 0);
+          if (o >= 0) {
+            kc[n] = ldg_stream16(static_cast<const uint8_t*>(a.c.k) + o + (lane % LPR) * 16);
+            vc[n] = ldg_stream16(static_cast<const uint8_t*>(a.c.v) + o + (lane % LPR) * 16);
+          }
+        }
+        uint32_t there[LL];
+#pragma unroll
+        for (int u = 0; u < LL; ++u) {
+          const bool real = tk[u].at >= 0;
+          there[u] = __ballot_sync(kAll, real);
+          ks[u] = real ? __ldg(a.c.k_scale + tk[u].sat) : 0.f;
+          vs[u] = real ? __ldg(a.c.v_scale + tk[u].sat) : 0.f;
+        }
+        i += ST;
+        settle();
+        look_up(tk);
+        if (round > 0) role_wait(dead, &sh.empty[stage], (uint32_t)((round - 1) & 1), a.status);
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+          const int r = gw * TW + n * (32 / LPR) + lane / LPR, ch = lane % LPR;
+          uint8_t* k = dst + (ch >> 2) * kChunk;
+          uint8_t* v = k + S::kVOff;
+          const int j = 2 * (ch & 3);
+          *reinterpret_cast<uint4*>(k + tc::sw128_off(r, j)) = e4m3x8_to_bf16(kc[n].x, kc[n].y);
+          *reinterpret_cast<uint4*>(k + tc::sw128_off(r, j + 1)) = e4m3x8_to_bf16(kc[n].z, kc[n].w);
+          *reinterpret_cast<uint4*>(v + tc::sw128_off(r, j)) = e4m3x8_to_bf16(vc[n].x, vc[n].y);
+          *reinterpret_cast<uint4*>(v + tc::sw128_off(r, j + 1)) = e4m3x8_to_bf16(vc[n].z, vc[n].w);
+        }
+#pragma unroll
+        for (int u = 0; u < LL; ++u) {
+          if (TW >= 32 || lane < TW) {
+            sh.scale[stage][0][gw * TW + 32 * u + lane] = ks[u];
+            sh.scale[stage][1][gw * TW + 32 * u + lane] = vs[u];
+          }
+          if (lane == 0) {
+            if (TW < 32)
+              reinterpret_cast<uint16_t*>(sh.exists[stage])[gw] = (uint16_t)there[u];
+            else
+              sh.exists[stage][gw * LL + u] = there[u];
+          }
+        }
+      } else {
+        if (round > 0) role_wait(dead, &sh.empty[stage], (uint32_t)((round - 1) & 1), a.status);
+#pragma unroll
+        for (int u = 0; u < LL; ++u) {
+          const uint32_t there = __ballot_sync(kAll, tk[u].at >= 0);
+          if (lane == 0) {
+            if (TW < 32)
+              reinterpret_cast<uint16_t*>(sh.exists[stage])[gw] = (uint16_t)there;
+            else
+              sh.exists[stage][gw * LL + u] = there;
+          }
+        }
+        const int j = lane & 7;  // this lane's 16-byte chunk of a 128-byte row
+#pragma unroll
+        for (int r4 = 0; r4 < TW; r4 += 4) {
+          const int rl = r4 + (lane >> 3), r = gw * TW + rl;
+          const long long o = __shfl_sync(kAll, tk[r4 / 32].at, rl & 31);
+          const bool ok = o >= 0;
+          const uint16_t* k = static_cast<const uint16_t*>(a.c.k) + (ok ? o : 0) + 8 * j;
+          const uint16_t* v = static_cast<const uint16_t*>(a.c.v) + (ok ? o : 0) + 8 * j;
+          uint8_t* to = dst + tc::sw128_off(r, j);
+#pragma unroll
+          for (int c = 0; c < S::kKChunks; ++c) tc::cp_async16_zfill(to + c * kChunk, k + 64 * c, ok);
+#pragma unroll
+          for (int c = 0; c < S::kVChunks; ++c)
+            tc::cp_async16_zfill(to + S::kVOff + c * kChunk, v + 64 * c, ok);
+        }
+        cp_async_commit();
+        i += ST;
+        settle();
+        look_up(tk);
+        cp_async_wait<0>();
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.full[stage]);
+    }
+    cp_async_wait<0>();
+  } else if (warp == kSoftWarps) {
+    // ---- the products: S = Q K^T (rows x tokens) of one tile ahead of O^T +=
+    // V^T P^T (dimensions x rows)
+    const uint32_t q0 = smem_u32(sm_q), p0 = smem_u32(sm_p), kv0 = smem_u32(sm_kv);
+    constexpr uint32_t idesc_s = idesc_bf16(kRows, kTile, false, false);
+    const uint32_t idesc_o = idesc_bf16(DV >= 128 ? 128 : 64, npad, true, false);
+    int j = 0, parts = 0;
+    auto values = [&](int t) {  // the products with tile t's values
+      role_wait(dead, &sh.p_full, (uint32_t)(t & 1), a.status);
+      tc::fence_after_sync();
+      if (tc::elect_one() && !*dead) {
+        const uint32_t v = kv0 + (t % ST) * S::kStage + S::kVOff;
+        const uint32_t add = sh.add_to;
+#pragma unroll
+        for (int mb = 0; mb < S::kBlocks; ++mb)
+#pragma unroll
+          for (int y = 0; y < S::kParts; ++y)
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              tc::mma_f16(tmem + kOCol + mb * kRows,
+                          sw128_desc_mn(v + 2 * mb * kChunk + kk * 2048, kChunk),
+                          tc::sw128_desc(p0 + y * kChunk + kk * 32), idesc_o, add | (y | kk ? 1u : 0u));
+        tc::commit(&sh.empty[t % ST]);
+        tc::commit(&sh.pv_done);
+      }
+      __syncwarp();
+    };
+    Part p;
+    while (walk.next_tiles(a, p)) {
+      role_wait(dead, &sh.q_full, (uint32_t)(parts & 1), a.status);
+      for (int i = 0; i < p.n; ++i, ++j) {
+        role_wait(dead, &sh.full[j % ST], (uint32_t)((j / ST) & 1), a.status);
+        if (j >= 2) role_wait(dead, &sh.s_empty[j & 1], (uint32_t)((j / 2 - 1) & 1), a.status);
+        tc::fence_after_sync();
+        if (tc::elect_one() && !*dead) {
+          const uint32_t k = kv0 + (j % ST) * S::kStage;
+#pragma unroll
+          for (int c = 0; c < S::kKChunks; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_f16(tmem + (j & 1) * kTile, tc::sw128_desc(q0 + c * kChunk + kk * 32),
+                          tc::sw128_desc(k + c * kChunk + kk * 32), idesc_s, c | kk ? 1u : 0u);
+          tc::commit(&sh.s_full[j & 1]);
+        }
+        __syncwarp();
+        if (i > 0) values(j - 1);
+      }
+      values(j - 1);
+      ++parts;
+    }
+    // every product has been made before the CTA's memory goes
+    if (j > 0 && lane == 0) mbar_wait(&sh.pv_done, (uint32_t)((j - 1) & 1));
+    __syncwarp();
+  } else {
+    // ---- softmax.  A thread holds 16 tokens of rows ra and ra + 8, a quad of
+    // lanes a row.
+    const int g = lane >> 2, c = lane & 3, ra = 16 * warp + g;
+    const uint32_t quadrant = tmem + ((uint32_t)(32 * warp) << 16);
+    const float scale2 = a.d.scale * kLog2e;
+    Walk ahead = walk;
+    Part p;
+    auto load_q = [&](const Part& x) {
+      for (int e = tid; e < kRows * (DK / 8); e += kSoftWarps * 32) {
+        const int r = e / (DK / 8), ch = e % (DK / 8), R = row0 + r;
+        const int n = R / a.G, h = R - n * a.G;
+        const bool real = r < rows;
+        const uint16_t* src =
+            a.q + (real ? x.b * a.d.q_stride + n * a.d.q_row_stride + (long long)(x.hkv * a.G + h) * DK + 8 * ch
+                        : 0);
+        tc::cp_async16_zfill(sm_q + (ch >> 3) * kChunk + tc::sw128_off(r, ch & 7), src, real);
+      }
+      cp_async_commit();
+    };
+    bool more = ahead.next_tiles(a, p);
+    if (more) load_q(p);
+    int j = 0;
+    while (walk.next(a, p)) {
+      if (rt == 0 && tid == 0 && p.parts) a.info[p.b * a.c.Hkv + p.hkv] = make_int2(2 * (walk.first / walk.share) + (p.slot & 1), p.parts);
+      const size_t slot = (size_t)max(p.slot, 0) * a.gtiles + rt;
+      float* const part_ml = a.part_ml + slot * 2 * kRows;
+      if (p.n == 0) {  // (a part of fewer units than a tile)
+        if (tid < kRows) {
+          part_ml[tid] = -INFINITY;
+          part_ml[kRows + tid] = 0.f;
+        }
+        continue;
+      }
+      cp_async_wait<0>();
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
+      // what the thread's two rows see: the context from `low` on, and the new
+      // tokens of `tree`
+      uint64_t tree[2];
+      int low[2];
+      const int drafts = p.sp.len - p.sp.ctx;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int R = row0 + ra + 8 * x, n = R / a.G;
+        tree[x] = 0;
+        low[x] = kNoRow;
+        if (ra + 8 * x < rows && n < drafts) {
+          const uint64_t m = a.mask ? (uint64_t)a.mask[p.b * a.d.mask_stride + n] : low_bits(n + 1);
+          tree[x] = m & low_bits(drafts);
+          low[x] = a.d.window > 0 ? p.sp.ctx + max(1, __popcll(tree[x])) - a.d.window : 0;
+        }
+      }
+      if (tid < kRows) {
+        const int R = row0 + tid, n = R / a.G;
+        sh.at[tid] = tid < rows ? p.b * a.d.out_stride + n * a.d.out_row_stride +
+                                      (long long)(p.hkv * a.G + R - n * a.G) * DV
+                                : -1;
+      }
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int i = 0; i < p.n; ++i, ++j) {
+        const int st = j % ST, t0 = (p.tile + i) * kTile;
+        role_wait(dead, &sh.s_full[j & 1], (uint32_t)((j / 2) & 1), a.status);
+        tc::fence_after_sync();
+        uint32_t raw[32];
+        ld_16x256b_x8(quadrant + (j & 1) * kTile, raw);
+        tc::wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.s_empty[j & 1]);
+        if (i == p.n - 1) {  // the queries have been read for the last time
+          Part x;
+          more = ahead.next_tiles(a, x);
+          if (more) load_q(x);
+        }
+        const uint64_t exists = (uint64_t)sh.exists[st][1] << 32 | sh.exists[st][0];
+        // a tile that some rows see more of than others
+        const bool mixed = t0 + kTile > p.sp.ctx ||
+                           (a.d.window > 0 && t0 < p.sp.ctx + drafts - a.d.window);
+        float s[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) s[u] = __uint_as_float(raw[u]) * scale2;
+        if (E4M3) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float2 f = *reinterpret_cast<const float2*>(&sh.scale[st][0][8 * u + 2 * c]);
+            s[4 * u] *= f.x;
+            s[4 * u + 1] *= f.y;
+            s[4 * u + 2] *= f.x;
+            s[4 * u + 3] *= f.y;
+          }
+        }
+        if (mixed || ~exists) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint64_t seen = low_bits(p.sp.ctx - t0) & ~low_bits(min(low[x], t0 + kTile) - t0);
+            const int sft = p.sp.ctx - t0;
+            if (sft > -64 && sft < 64) seen |= sft >= 0 ? tree[x] << sft : tree[x] >> -sft;
+            seen &= exists;
+            if (c == 0) sh.seen[ra + 8 * x] = seen;
+            const uint64_t mine = seen >> (2 * c);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              if (!(mine >> (8 * u) & 1)) s[4 * u + 2 * x] = -INFINITY;
+              if (!(mine >> (8 * u + 1) & 1)) s[4 * u + 2 * x + 1] = -INFINITY;
+            }
+          }
+        }
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) mx[x] = fmaxf(mx[x], fmaxf(s[4 * u + 2 * x], s[4 * u + 2 * x + 1]));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(kAll, mx[x], 1));
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(kAll, mx[x], 2));
+        }
+        // (-inf + slack is -inf: a row's first score moves its maximum)
+        const bool moved = bar_any(1, kSoftWarps * 32, mx[0] > m[0] + kMaxSlack || mx[1] > m[1] + kMaxSlack);
+        if (j > 0) role_wait(dead, &sh.pv_done, (uint32_t)((j - 1) & 1), a.status);
+        tc::fence_after_sync();
+        if (moved) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float mn = fmaxf(m[x], mx[x]);
+            const float f = m[x] == mn ? 1.f : exp2_fast(m[x] - mn);
+            l[x] *= f;
+            m[x] = mn;
+            if (c == 0) sh.factor[ra + 8 * x] = f;
+          }
+          if (i > 0) {
+            named_bar(1, kSoftWarps * 32);
+            for (int mb = 0; mb < S::kBlocks; ++mb)
+              for (int r0 = 0; r0 < npad; r0 += 16) {
+                uint32_t o[16];
+                const uint32_t at = quadrant + kOCol + mb * kRows + r0;
+                ld_32x32b_x16(at, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                  o[u] = __float_as_uint(__uint_as_float(o[u]) * sh.factor[r0 + u]);
+                st_32x32b_x16(at, o);
+              }
+            tc::wait_st();
+          }
+        }
+        const float ms[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        // weights, as the second product's operand: row, then token
+        bool add_to = i > 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          float2 vs = make_float2(1.f, 1.f);
+          if (E4M3) vs = *reinterpret_cast<const float2*>(&sh.scale[st][1][8 * u + 2 * c]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float w0 = exp2_fast(s[4 * u + 2 * x] - ms[x]), w1 = exp2_fast(s[4 * u + 2 * x + 1] - ms[x]);
+            uint8_t* to = sm_p + tc::sw128_off(ra + 8 * x, u) + 4 * c;
+            if (S::kParts == 1) {
+              const uint32_t w = pack_bf16x2(w0, w1);
+              l[x] += bf16_lo(w) + bf16_hi(w);
+              *reinterpret_cast<uint32_t*>(to) = w;
+            } else {
+              l[x] += w0 + w1;
+              if (E4M3) {  // (a token that is not seen may have any scale)
+                w0 = w0 == 0.f ? 0.f : w0 * vs.x;
+                w1 = w1 == 0.f ? 0.f : w1 * vs.y;
+              }
+              const uint32_t hi = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
+              *reinterpret_cast<uint32_t*>(to) = hi;
+              *reinterpret_cast<uint32_t*>(to + kChunk) = pack_bf16x2(w0 - bf16_lo(hi), w1 - bf16_hi(hi));
+            }
+          }
+        }
+        if (mixed) {
+          // A value that is not finite reaches the rows that see its token and no
+          // other: it is added to their outputs, and the tile holds 0 in its place
+          // (times a weight of 0 it would be NaN).
+          uint8_t* const v = sm_kv + st * S::kStage + S::kVOff;
+          bool odd = false;
+          for (int e = tid; e < kTile * (DV / 8); e += kSoftWarps * 32) {
+            const uint4 w = *reinterpret_cast<const uint4*>(v + e * 16);
+            odd |= bf16x2_nonfinite(w.x) || bf16x2_nonfinite(w.y) || bf16x2_nonfinite(w.z) ||
+                   bf16x2_nonfinite(w.w);
+          }
+          if (bar_any(1, kSoftWarps * 32, odd)) {
+            for (int mb = 0; mb < S::kBlocks; ++mb) {
+              const int d = DV >= 128 ? mb * 128 + tid : 16 * warp + (lane & 15);
+              for (int r0 = 0; r0 < npad; r0 += 16) {
+                uint32_t o[16];
+                const uint32_t at = quadrant + kOCol + mb * kRows + r0;
+                ld_32x32b_x16(at, o);
+                tc::wait_ld();
+                for (int t = 0; t < kTile; ++t) {
+                  const uint32_t w = *reinterpret_cast<const uint16_t*>(
+                      v + (d >> 6) * kChunk + tc::sw128_off(t, (d >> 3) & 7) + 2 * (d & 7));
+                  const bool bad = (w & 0x7F80u) == 0x7F80u;
+#pragma unroll
+                  for (int u = 0; u < 16; ++u) {
+                    if (i == 0 && t == 0) o[u] = 0u;
+                    if (bad && (sh.seen[r0 + u] >> t & 1))
+                      o[u] = __float_as_uint(__uint_as_float(o[u]) + __uint_as_float(w << 16));
+                  }
+                }
+                st_32x32b_x16(at, o);
+              }
+            }
+            tc::wait_st();
+            named_bar(1, kSoftWarps * 32);  // every thread has read the values
+            for (int e = tid; e < kTile * DV; e += kSoftWarps * 32) {
+              uint16_t* w = reinterpret_cast<uint16_t*>(v) + e;
+              if ((*w & 0x7F80u) == 0x7F80u) *w = 0;
+            }
+            add_to = true;
+          }
+        }
+        if (tid == 0) sh.add_to = add_to;
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full);
+      }
+      // ---- the part's results
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[x] += __shfl_xor_sync(kAll, l[x], 1);
+        l[x] += __shfl_xor_sync(kAll, l[x], 2);
+        if (low[x] == kNoRow) {  // (tiles that all rows see alike have been taken in)
+          m[x] = -INFINITY;
+          l[x] = 0.f;
+        }
+        if (c == 0) {
+          const int r = ra + 8 * x;
+          sh.inv[r] = l[x] == 0.f ? 0.f : 1.f / l[x];
+          if (p.slot >= 0) {
+            part_ml[r] = m[x];
+            part_ml[kRows + r] = l[x];
+          }
+        }
+      }
+      role_wait(dead, &sh.pv_done, (uint32_t)((j - 1) & 1), a.status);
+      tc::fence_after_sync();
+      named_bar(1, kSoftWarps * 32);
+      float* const part_o = a.part_o + slot * kRows * DV;
+      const bool lives = DV >= 128 || lane < 16;
+      for (int mb = 0; mb < S::kBlocks; ++mb) {
+        const int d = DV >= 128 ? mb * 128 + tid : 16 * warp + (lane & 15);
+        for (int r0 = 0; r0 < npad; r0 += 16) {
+          uint32_t o[16];
+          ld_32x32b_x16(quadrant + kOCol + mb * kRows + r0, o);
+          tc::wait_ld();
+          if (p.slot >= 0) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+              if (lives && r0 + u < rows) part_o[(r0 + u) * DV + d] = __uint_as_float(o[u]);
+          } else {
+            // two neighbouring lanes trade, and each writes two dimensions of a row
+            const int odd = lane & 1;
+#pragma unroll
+            for (int u = 0; u < 16; u += 2) {
+              const float f0 = sh.inv[r0 + u], f1 = sh.inv[r0 + u + 1];
+              const float v0 = f0 == 0.f ? 0.f : __uint_as_float(o[u]) * f0;
+              const float v1 = f1 == 0.f ? 0.f : __uint_as_float(o[u + 1]) * f1;
+              const float got = __shfl_xor_sync(kAll, odd ? v0 : v1, 1);
+              const long long at = sh.at[r0 + u + odd];
+              if (lives && at >= 0)
+                *reinterpret_cast<uint32_t*>(a.out + at + (d - odd)) =
+                    odd ? pack_bf16x2(got, v1) : pack_bf16x2(v0, got);
+            }
+          }
+        }
+      }
+      tc::fence_before_sync();
+      named_bar(1, kSoftWarps * 32);  // the next part may write factors and places
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kSoftWarps) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, S::kTmem);
+  }
+}
+
+// Joins the parts of the segments that several columns hold, in order, and
+// answers zeros for sequences without new tokens.
+template <int DV>
+__global__ void __launch_bounds__(kJoinThreads) k_draft_join(const DraftArgs a) {
+  constexpr int kLanes = DV / 4, kGroups = kJoinThreads / kLanes;  // threads per row; shares of the parts
+  constexpr int kAhead = 8;
+  __shared__ float4 s_acc[kGroups][kLanes];
+  __shared__ float s_m[kGroups], s_l[kGroups];
+  griddep_wait();
+  griddep_trigger();
+  const int rt = blockIdx.x % a.gtiles, seg = blockIdx.x / a.gtiles, b = seg / a.c.Hkv, hkv = seg % a.c.Hkv;
+  const int row0 = rt * kRows, rows = min(kRows, a.rows - row0);
+  const int d4 = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+  bool bad;
+  const Span sp = span_of(a, b, &bad);
+  if (bad && threadIdx.x == 0 && blockIdx.y == 0 && hkv == 0 && rt == 0) raise_status(a.status, MOE_DEV_BAD_PAGE);
+  const int2 info = sp.tiles ? a.info[seg] : make_int2(0, 0);
+  if (info.y == 1) return;  // its column has written it
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int R = row0 + r, n = R / a.G;
+    uint16_t* out = a.out + b * a.d.out_stride + n * a.d.out_row_stride +
+                    (long long)(hkv * a.G + R - n * a.G) * DV + 4 * d4;
+    if (info.y == 0) {
+      if (grp == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
+      continue;
+    }
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int each = cdiv(info.y, kGroups), i1 = min(info.y, (grp + 1) * each);
+    for (int i0 = grp * each; i0 < i1; i0 += kAhead) {
+      float m[kAhead], l[kAhead];
+      float4 v[kAhead];
+      float M2 = M;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u;
+        m[u] = -INFINITY;
+        l[u] = 0.f;
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < i1) {
+          const size_t slot = (size_t)(i == 0 ? info.x : 2 * (info.x / 2 + i)) * a.gtiles + rt;
+          m[u] = __ldcg(a.part_ml + slot * 2 * kRows + r);
+          l[u] = __ldcg(a.part_ml + slot * 2 * kRows + kRows + r);
+          v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * kRows + r) * DV) + d4);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) M2 = fmaxf(M2, m[u]);
+      const float Ms = M2 == -INFINITY ? 0.f : M2, f0 = M == M2 ? 1.f : exp2f(M - Ms);
+      L *= f0;
+      acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (m[u] == -INFINITY) continue;  // (nothing of this row: the outputs may hold anything)
+        const float f = exp2f(m[u] - Ms);
+        L = fmaf(l[u], f, L);
+        acc.x = fmaf(v[u].x, f, acc.x);
+        acc.y = fmaf(v[u].y, f, acc.y);
+        acc.z = fmaf(v[u].z, f, acc.z);
+        acc.w = fmaf(v[u].w, f, acc.w);
+      }
+      M = M2;
+    }
+    s_acc[grp][d4] = acc;
+    if (d4 == 0) {
+      s_m[grp] = M;
+      s_l[grp] = L;
+    }
+    __syncthreads();
+    if (grp == 0) {
+      for (int x = 1; x < kGroups; ++x) M = fmaxf(M, s_m[x]);
+      const float Ms = M == -INFINITY ? 0.f : M;
+      L = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = 0; x < kGroups; ++x) {
+        if (s_m[x] == -INFINITY) continue;
+        const float f = exp2f(s_m[x] - Ms);
+        const float4 v = s_acc[x][d4];
+        L = fmaf(s_l[x], f, L);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      *reinterpret_cast<uint2*>(out) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();
+  }
+}
+
+namespace {
+
+int draft_gtiles(const moe_draft_dims& d, int Hkv) { return cdiv(d.n * (d.Hq / Hkv), kRows); }
+// Columns times row tiles at most, whatever the shape.
+int draft_slots(int gtiles) { return std::max(2 * num_sms(), gtiles); }
+
+template <int DK, int DV, bool LATENT, bool E4M3>
+cudaError_t launch_draft(DraftArgs& a, cudaStream_t s) {
+  using S = DraftShape<DK, DV, LATENT, E4M3>;
+  cudaError_t err = ensure_smem((const void*)k_draft_attention<DK, DV, LATENT, E4M3>, S::kSmem);
+  if (err != cudaSuccess) return err;
+  const long long tiles = (std::min((long long)a.d.table_width * a.c.page_size, kMaxTokens) + kTile - 1) / kTile + 1;
+  const long long units = (long long)a.d.B * a.c.Hkv * (tiles + kSegCost);
+  a.cols = (int)std::max(1ll, std::min<long long>(S::kCtas * num_sms() / a.gtiles, units / kMinUnits));
+  err = launch_k(k_draft_attention<DK, DV, LATENT, E4M3>, dim3(a.cols * a.gtiles), dim3(S::kWarps * 32), S::kSmem,
+                 s, true, a);
+  if (err != cudaSuccess) return err;
+  const int segs = a.d.B * a.c.Hkv * a.gtiles;
+  const int chunks = std::min(kRows, std::max(4, cdiv(2 * num_sms(), segs)));
+  return launch_k(k_draft_join<DV>, dim3(segs, chunks), dim3(kJoinThreads), 0, s, true, a);
+}
+
+}  // namespace
+
+bool draft_attention_fits(const moe_draft_dims& d, const moe_kv_cache& c) {
+  const long long tokens = std::min((long long)d.table_width * c.page_size, kMaxTokens);
+  return (long long)d.B * c.Hkv * (tokens / kTile + 2 + kSegCost) + (1ll << 24) < (1ll << 31);
+}
+
+size_t draft_attention_workspace(const moe_draft_dims& d, int Hkv, int DV) {
+  const int gtiles = draft_gtiles(d, Hkv);
+  const size_t slots = 2 * (size_t)draft_slots(gtiles);
+  return slots * kRows * ((size_t)DV + 2) * sizeof(float) + (size_t)d.B * Hkv * sizeof(int2);
+}
+
+cudaError_t launch_draft_attention(const uint16_t* q, const moe_kv_cache& cache, bool latent,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   const int64_t* mask, const int32_t* draft_lens,
+                                   const moe_draft_dims& d, int DV, uint16_t* out, void* ws,
+                                   int32_t* status, cudaStream_t s) {
+  DraftArgs a{};
+  a.q = q;
+  a.c = cache;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.mask = mask;
+  a.draft_lens = draft_lens;
+  a.d = d;
+  a.G = d.Hq / cache.Hkv;
+  a.rows = d.n * a.G;
+  a.gtiles = draft_gtiles(d, cache.Hkv);
+  a.out = out;
+  a.part_o = static_cast<float*>(ws);
+  const size_t slots = 2 * (size_t)draft_slots(a.gtiles);
+  a.part_ml = a.part_o + slots * kRows * DV;
+  a.info = reinterpret_cast<int2*>(a.part_ml + slots * 2 * kRows);
+  a.status = status;
+  // t / page_size for 0 <= t < 2^31: with 2^(e-1) < page_size <= 2^e and mul =
+  // ceil(2^(31+e) / page_size) < 2^32, floor(t mul / 2^(31+e)) is exact
+  int e = 0;
+  while ((1ll << e) < cache.page_size) ++e;
+  a.ps_mul = (uint32_t)(((1ull << (31 + e)) + cache.page_size - 1) / cache.page_size);
+  a.ps_shift = e > 0 ? e - 1 : 0;
+  if (latent) {
+    return DV == 512 ? launch_draft<576, 512, true, false>(a, s) : launch_draft<320, 256, true, false>(a, s);
+  }
+  const bool f8 = cache.format == MOE_KV_E4M3;
+  if (DV == 64) return f8 ? launch_draft<64, 64, false, true>(a, s) : launch_draft<64, 64, false, false>(a, s);
+  if (DV == 128) return f8 ? launch_draft<128, 128, false, true>(a, s) : launch_draft<128, 128, false, false>(a, s);
+  return f8 ? launch_draft<256, 256, false, true>(a, s) : launch_draft<256, 256, false, false>(a, s);
+}
+
+}  // namespace moe

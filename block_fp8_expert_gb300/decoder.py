@@ -398,6 +398,241 @@ class PagedAttention(_Status):
         return out
 
 
+class _DraftAttention(_Status):
+    """What attention of several new tokens per sequence has in common."""
+
+    _free = frozenset(("_sizes", "scale", "window"))
+
+    def _set_up(self, H, Dq, Dv, scale, window, place, call, name):
+        self.scale, self.window = scale, window
+        self._sizes = None, None  # (read and replaced as one: threads may share the object)
+        self._held = (self._dev, H, Dq, Dv, place, self._status, call, name)
+
+    def _bytes(self, d) -> int:
+        raise NotImplementedError
+
+    def workspace(self, B: int, n: int, stream=None) -> torch.Tensor:
+        """A workspace for calls of up to B sequences (of any length) with n
+        new tokens each, or fewer."""
+        if self._dev != _current_device():
+            _refuse_device(self._dev, _current_device())
+        d = _lib.DraftDims(B, n, self._held[1], 0, 0, self.scale, 0, 0, 0, 0, 0, 0)
+        return new_on(stream, self._bytes(d), dtype=torch.uint8, device=self.status.device)
+
+    def forward(self, q: torch.Tensor, cache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                mask: Optional[torch.Tensor] = None, draft_lens: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """q bf16 [B, n, heads, query size], block_table int32 [B, pages per
+        sequence], seq_lens int32 [B] (the new tokens included) -> out bf16
+        [B, n, heads, value size].  mask int64 [B, n]: bit j of mask[b, i]
+        tells whether new token i sees new token j (None: those up to itself;
+        mask.expand(B, n) where the sequences share one); draft_lens int32
+        [B]: the sequences' new tokens, the last ones of seq_lens (None: n).
+        Rows past them are zeros."""
+        here, H, Dq, Dv, place, status, call, name = self._held
+        dev, shape, qs = q.get_device(), q.shape, q.stride()
+        B, n = shape[0], shape[1]
+        if (dev != here or q.dtype != _BF16 or shape != (B, n, H, Dq) or qs[3] != 1
+                or (H > 1 and qs[2] != Dq)):
+            _refuse(q, "q", _BF16, (B, n, H, Dq), here, _HEADS)
+        if dev != _current_device():
+            _refuse_device(dev, _current_device())
+        if cache._place != place:
+            cache.refuse(*place)
+        rows, width = block_table.shape
+        ts = block_table.stride()
+        if (block_table.dtype != _I32 or block_table.get_device() != dev or rows != B
+                or (width > 1 and ts[1] != 1)):
+            _refuse(block_table, "block_table", _I32, (B, width), dev, _ROWS)
+        for t, what in ((seq_lens, "seq_lens"), (draft_lens, "draft_lens")):
+            if t is not None and (t.dtype != _I32 or t.get_device() != dev or t.shape != (B,)
+                                  or not t.is_contiguous()):
+                _refuse(t, what, _I32, (B,), dev)
+        ms = 0
+        if mask is not None:
+            ms = mask.stride()
+            if (mask.dtype != _I64 or mask.get_device() != dev or mask.shape != (B, n)
+                    or (n > 1 and ms[1] != 1)):
+                _refuse(mask, "mask", _I64, (B, n), dev, _ROWS)
+            ms = ms[0] if B > 1 else 0
+        if out is None:
+            out = new_on(stream, B, n, H, Dv, dtype=_BF16, device=q.device)
+        os = out.stride()
+        if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (B, n, H, Dv)
+                or os[3] != 1 or (H > 1 and os[2] != Dv)):
+            _refuse(out, "out", _BF16, (B, n, H, Dv), dev, _HEADS)
+        if ws is None:
+            ws = self.workspace(B, n, stream)
+        elif ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError("ws must be contiguous and on the tensors' device")
+        key = (B, n, width, ts[0], qs[0], qs[1], os[0], os[1], ms, self.window, self.scale)
+        known, dims = self._sizes
+        if key != known:
+            row = (qs[1], os[1]) if n > 1 else (H * Dq, H * Dv)
+            seq = (ts[0], qs[0], os[0]) if B > 1 else (width, n * row[0], n * row[1])
+            dims = _lib.DraftDims(B, n, H, width, key[9], key[10], seq[0], seq[1], row[0], seq[2],
+                                  row[1], ms)
+            self._sizes = key, dims
+        st = call(q.data_ptr(), cache._abi, block_table.data_ptr(), seq_lens.data_ptr(),
+                  None if mask is None else mask.data_ptr(),
+                  None if draft_lens is None else draft_lens.data_ptr(), dims, out.data_ptr(),
+                  ws.data_ptr(), ws.nbytes, status,
+                  _raw_stream(dev) if stream is None else _handle(stream))
+        if st:
+            _lib._check(st, name)
+        return out
+
+
+class TreeAttention(_DraftAttention):
+    """Attention of several new tokens per sequence, which see each other as a
+    tree (or a chain), over a PagedCache that holds them already
+    (moe_tree_attention); window > 0 leaves out what lies further back.  scale
+    and window may be set again."""
+
+    def __init__(self, Hq: int, Hkv: int, D: int, scale: Optional[float] = None, window: int = 0,
+                 device="cuda"):
+        super().__init__(device)
+        self.Hq, self.Hkv, self.D = Hq, Hkv, D
+        self._set_up(Hq, D, D, 1.0 / math.sqrt(D) if scale is None else scale, window,
+                     (Hkv, D, self._dev), _lib.lib().moe_tree_attention, "moe_tree_attention")
+
+    def _bytes(self, d):
+        return _lib.tree_attention_workspace_bytes(d, self.Hkv, self.D)
+
+
+class LatentCache(_Fixed):
+    """A paged cache of latent vectors over a bf16 tensor [pages, page_size,
+    R + rot]: R elements of the vector, then rot of the shared key part.  Any
+    strides with a token contiguous will do."""
+
+    def __init__(self, data: torch.Tensor, R: int):
+        if not (data.is_cuda and data.dtype == _BF16 and data.dim() == 3 and data.shape[2] > R
+                and data.stride(2) == 1):
+            _refuse(data, "data", _BF16, (*data.shape[:2], R + 64), layout=_ROWS)
+        self.data, self.R = data, R
+        self.pages, self.page_size = data.shape[:2]
+        self.rot = data.shape[2] - R
+        self.device = data.get_device()
+        self._place = (R, self.rot, self.device)
+        self._abi = _lib.LatentPages(data.data_ptr(), self.pages, self.page_size, R, self.rot,
+                                     data.stride(0), data.stride(1))
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, R: int, rot: int = 64,
+              device="cuda") -> "LatentCache":
+        return cls(torch.zeros(pages, page_size, R + rot, dtype=torch.bfloat16, device=device), R)
+
+    def abi(self) -> _lib.LatentPages:
+        return self._abi
+
+    def refuse(self, R: int, rot: int, device: int) -> None:
+        """Raise for a use that needs another layout or another device."""
+        raise ValueError(f"the cache holds vectors of {self.R} + {self.rot} on device "
+                         f"{self.device}, need {R} + {rot} on {device}")
+
+
+class LatentStore(_Status):
+    """Latent vectors normed, their shared key part rotated, stored into a
+    LatentCache, and the queries' rotated parts on the way (moe_latent_store).
+    norm: float32 [R] or None (no norm); cos_sin: a table of rope_cos_sin with
+    `rot` columns.  eps and interleaved may be set again."""
+
+    _free = frozenset(("_sizes", "eps", "interleaved"))
+
+    def __init__(self, H: int, R: int, cos_sin: torch.Tensor, norm: Optional[torch.Tensor] = None,
+                 rot: int = 64, interleaved: bool = False, eps: float = 1e-6, device="cuda"):
+        super().__init__(device)
+        self.H, self.R, self.rot, self.eps = H, R, rot, eps
+        self.interleaved = bool(interleaved)
+        self.norm = _dense(norm, "norm", torch.float32, R, device=self._dev)
+        self.n_pos = cos_sin.shape[0]
+        self.cos_sin = _dense(cos_sin, "cos_sin", torch.float32, self.n_pos, rot, device=self._dev)
+        self._sizes = None, None  # (read and replaced as one: threads may share the object)
+        self._held = (self._dev, H, rot, R + rot, (R, rot, self._dev), _lib._ptr(norm),
+                      _lib._ptr(cos_sin), self._status, _lib.lib().moe_latent_store)
+
+    def forward(self, kv: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                cache: LatentCache, q: Optional[torch.Tensor] = None,
+                q_out: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+                stream=None) -> Optional[torch.Tensor]:
+        """kv bf16 [T, R + rot] (rows may be strided), positions int32 [T],
+        slots int64 [T] (page * page_size + offset, or < 0 for padding), q bf16
+        [T, H, rot] (the rotated part of wider heads: any strides between
+        tokens and heads) -> q_out, of q's shape, which may be q itself.  rows
+        bf16 [T, R + rot]: what was stored, once more by token.  Without q, the
+        heads are left alone."""
+        here, H, rot, width, place, norm, cos_sin, status, call = self._held
+        dev, shape, xs = kv.get_device(), kv.shape, kv.stride()
+        T = shape[0]
+        if dev != here or kv.dtype != _BF16 or shape != (T, width) or xs[-1] != 1:
+            _refuse(kv, "kv", _BF16, (T, width), here, _ROWS)
+        if dev != _current_device():
+            _refuse_device(dev, _current_device())
+        if cache._place != place:
+            cache.refuse(*place)
+        if (positions.dtype != _I32 or positions.get_device() != dev or positions.shape != (T,)
+                or not positions.is_contiguous()):
+            _refuse(positions, "positions", _I32, (T,), dev)
+        if (slots.dtype != _I64 or slots.get_device() != dev or slots.shape != (T,)
+                or not slots.is_contiguous()):
+            _refuse(slots, "slots", _I64, (T,), dev)
+        qs = ps = (0, 0, 1)
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+            H = 0
+        else:
+            if q_out is None:
+                q_out = new_on(stream, T, H, rot, dtype=_BF16, device=kv.device)
+            qs, ps = q.stride(), q_out.stride()
+            for t, name, s in ((q, "q", qs), (q_out, "q_out", ps)):
+                if (t.dtype != _BF16 or t.get_device() != dev or t.shape != (T, H, rot)
+                        or s[2] != 1):
+                    _refuse(t, name, _BF16, (T, H, rot), dev, _ROWS)
+        rs = (0, 1)
+        if rows is not None:
+            rs = rows.stride()
+            if (rows.dtype != _BF16 or rows.get_device() != dev or rows.shape != (T, width)
+                    or rs[1] != 1):
+                _refuse(rows, "rows", _BF16, (T, width), dev, _ROWS)
+        key = (T, H, xs[0], qs, ps, rs[0], self.eps, self.interleaved)
+        known, dims = self._sizes
+        if key != known:
+            if T > 1:
+                kv_s, q_s, p_s, r_s = xs[0], qs[0], ps[0], rs[0]
+            else:
+                kv_s, q_s, p_s, r_s = width, 0, 0, width
+            qh, ph = (qs[1], ps[1]) if H > 1 else (rot, rot)
+            dims = _lib.LatentDims(T, H, int(bool(key[7])), self.n_pos, key[6], kv_s, q_s, qh, p_s, ph,
+                                   r_s)
+            self._sizes = key, dims
+        st = call(kv.data_ptr(), norm, cos_sin, positions.data_ptr(), slots.data_ptr(),
+                  None if q is None else q.data_ptr(), dims, cache._abi,
+                  None if q is None else q_out.data_ptr(),
+                  None if rows is None else rows.data_ptr(), status,
+                  _raw_stream(dev) if stream is None else _handle(stream))
+        if st:
+            _lib._check(st, "moe_latent_store")
+        return q_out
+
+
+class LatentAttention(_DraftAttention):
+    """Attention of one or several new tokens per sequence over a LatentCache
+    in the absorbed form: the latent vector is key and value of every head
+    (moe_latent_attention).  q is [B, n, H, R + rot], out [B, n, H, R]; scale
+    is that of the expanded heads, 1 / sqrt(their size), and may be set again."""
+
+    def __init__(self, H: int, R: int, scale: float, rot: int = 64, device="cuda"):
+        super().__init__(device)
+        self.H, self.R, self.rot = H, R, rot
+        self._set_up(H, R + rot, R, scale, 0, (R, rot, self._dev),
+                     _lib.lib().moe_latent_attention, "moe_latent_attention")
+
+    def _bytes(self, d):
+        return _lib.latent_attention_workspace_bytes(d, self.R)
+
+
 class Fp8Linear(_Status):
     """x W^T + bias with block-FP8 weights (codes [N, K] uint8 or
     float8_e4m3fn, scales float32 [ceil(N/128), ceil(K/128)]) and E4M3

@@ -570,6 +570,120 @@ moe_status moe_linear_fp8(const uint16_t* x, moe_fp8_mat w, const float* bias,
                           moe_linear_dims d, uint16_t* out, void* ws,
                           size_t ws_bytes, int32_t* status, void* stream);
 
+/* One moe_tree_attention or moe_latent_attention call: B sequences with n new
+ * tokens each at most, Hq query heads (moe_tree_attention: a multiple of the
+ * cache's Hkv).  n in [1, 64], n * Hq / Hkv at most 8192.  table_width: page
+ * numbers per sequence in block_table, table_stride apart.  window > 0 (at
+ * least n; moe_tree_attention only): tokens further back are not attended to.
+ * q_stride, out_stride: elements between sequences, q_row_stride,
+ * out_row_stride between a sequence's tokens, multiples of 8 (the heads of a
+ * token are contiguous); mask_stride: between the sequences' masks, 0 where
+ * they share one. */
+typedef struct {
+  int32_t B, n, Hq, table_width, window;
+  float scale;
+  int64_t table_stride, q_stride, q_row_stride, out_stride, out_row_stride,
+      mask_stride;
+} moe_draft_dims;
+
+/*
+ * Attention of several new tokens per sequence, a tree of drafted ones or the
+ * next few of a chain, over the paged cache that already holds them:
+ *   out[b,i,h] = sum_t softmax_t(scale * q[b,i,h] . k[b,t]) v[b,t]
+ * Sequence b has seq_lens[b] tokens in the cache, of which the last
+ * draft_lens[b] (NULL: n; none of an empty sequence) are its new tokens 0, 1,
+ * ...; those before are its context.  New token i sees the context, and new
+ * token j where bit j of mask[b][i] is set (its ancestors and itself; bits from
+ * draft_lens[b] on are ignored).  mask NULL: j <= i.  With a window, token i
+ * stands c = max(1, number of new tokens that it sees) places after the
+ * context's end and sees the last window - c tokens of the context.
+ * q bf16 [B, n, Hq, D] and out bf16 [B, n, Hq, D] by their strides; block_table
+ * as in moe_paged_attention; seq_lens, draft_lens int32 [B]; mask int64 [B, n].
+ * Rows from draft_lens[b] on, and rows that see nothing, are zeros.  Cache
+ * elements that no row may see are not read, and what a row does not see does
+ * not reach it, whatever it is (NaN and infinities included).
+ * The cache's length splits over the GPU and the parts are joined in a fixed
+ * order, so equal calls give equal bits.  Scores, maxima, sums and outputs are
+ * fp32; the softmax weights (E4M3: times the value's scale) enter the product
+ * with the values as two bf16 parts, 2^-16 of the weight.  A page number
+ * outside [0, pages), a length outside [0, table_width * page_size] or a
+ * draft_lens[b] outside [0, min(n, seq_lens[b])] raises MOE_DEV_BAD_PAGE; the
+ * tokens of such a page are left out, and such a length is clamped.
+ */
+moe_status moe_tree_attention_workspace_bytes(moe_draft_dims d, int32_t Hkv,
+                                              int32_t D, size_t* bytes);
+moe_status moe_tree_attention(const uint16_t* q, moe_kv_cache cache,
+                              const int32_t* block_table,
+                              const int32_t* seq_lens, const int64_t* mask,
+                              const int32_t* draft_lens, moe_draft_dims d,
+                              uint16_t* out, void* ws, size_t ws_bytes,
+                              int32_t* status, void* stream);
+
+/* A paged cache of latent vectors, bf16: token slot n (n = page * page_size +
+ * offset) is R elements of the vector and rot of the shared key part, R + rot
+ * contiguous elements at page * page_stride + offset * token_stride of data.
+ * R is 256 or 512, rot 64; the strides are multiples of 8. */
+typedef struct {
+  void* data;
+  int32_t pages, page_size, R, rot;
+  int64_t page_stride, token_stride;
+} moe_latent_cache;
+
+/* One moe_latent_store call: T tokens, H query heads (0: none).  interleaved:
+ * 1 rotates the pairs (2i, 2i + 1), 0 the pairs (i, i + rot / 2).  n_pos: rows
+ * of cos_sin.  Strides in elements, multiples of 8: between tokens, and
+ * between the heads of q and q_out. */
+typedef struct {
+  int32_t T, H, interleaved, n_pos;
+  float eps;
+  int64_t kv_stride, q_stride, q_head_stride, q_out_stride, q_out_head_stride,
+      rows_stride;
+} moe_latent_dims;
+
+/*
+ * Per token t, on row t of kv (bf16: R elements of the latent vector, then rot
+ * of the shared key part):
+ *   c' = c / sqrt(mean(c^2) + eps) * norm      norm NULL: c' = c
+ *   (a, b) -> (a cos - b sin, b cos + a sin)   the shared key part's pairs i, and
+ *                                              those of the rot elements of each
+ *                                              of the H heads of q, with
+ *                                              cos = cos_sin[pos[t]][i],
+ *                                              sin = cos_sin[pos[t]][rot/2 + i]
+ * in fp32, rounded once.  The vector and the key part go to slot slots[t] of
+ * the cache (slots[t] < 0: a padding token, nothing is stored; two tokens of
+ * one call must not share a slot) and, where rows is given, to row t of rows;
+ * the heads go to q_out, which may be q itself with its strides.
+ * norm float [R]; cos_sin float [n_pos, rot]; pos int32 [T]; slots int64 [T];
+ * q, q_out bf16 [T, H, rot] by their strides (NULL iff H == 0); rows bf16
+ * [T, R + rot] or NULL.  A position outside [0, n_pos) raises
+ * MOE_DEV_BAD_POSITION: the token's heads and its row are NaN and it stores
+ * nothing.  A slot past the cache raises MOE_DEV_BAD_PAGE and stores nothing.
+ */
+moe_status moe_latent_store(const uint16_t* kv, const float* norm,
+                            const float* cos_sin, const int32_t* pos,
+                            const int64_t* slots, const uint16_t* q,
+                            moe_latent_dims d, moe_latent_cache cache,
+                            uint16_t* q_out, uint16_t* rows, int32_t* status,
+                            void* stream);
+
+/*
+ * moe_tree_attention over latent vectors c[t] (latent attention in its absorbed
+ * form: the queries have been taken through the heads' key projections, and
+ * the outputs go through their value projections):
+ *   out[b,i,h] = sum_t softmax_t(scale * q[b,i,h] . c[b,t]) c[b,t][0 .. R)
+ * q bf16 [B, n, Hq, R + rot], out bf16 [B, n, Hq, R]; the rest as in
+ * moe_tree_attention, without a window.  The softmax weights are rounded to
+ * bf16 (2^-9 of the weight) before both the product and their sum.
+ */
+moe_status moe_latent_attention_workspace_bytes(moe_draft_dims d, int32_t R,
+                                                size_t* bytes);
+moe_status moe_latent_attention(const uint16_t* q, moe_latent_cache cache,
+                                const int32_t* block_table,
+                                const int32_t* seq_lens, const int64_t* mask,
+                                const int32_t* draft_lens, moe_draft_dims d,
+                                uint16_t* out, void* ws, size_t ws_bytes,
+                                int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
