@@ -115,6 +115,15 @@ class LatentDims(ctypes.Structure):
                 ("rows_stride", ctypes.c_int64)]
 
 
+class ExpandedDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Tq", ctypes.c_int32), ("Tk", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("rope_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
@@ -160,6 +169,7 @@ _SIGNATURES = {
     "moe_latent_attention_workspace_bytes": (_st, [DraftDims, _i32, ctypes.POINTER(_sz)]),
     "moe_latent_attention": (_st, [_vp, LatentPages, _vp, _vp, _vp, _vp, DraftDims, _vp, _vp, _sz,
                                    _vp, _vp]),
+    "moe_expanded_attention": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, ExpandedDims, _vp, _vp, _vp]),
     "moe_linear_fp8_workspace_bytes": (_st, [LinearDims, ctypes.POINTER(_sz)]),
     "moe_linear_fp8": (_st, [_vp, Fp8Mat, _vp, LinearDims, _vp, _vp, _sz, _vp, _vp]),
 }
@@ -407,6 +417,13 @@ def moe_latent_attention(q, cache: LatentPages, block_table, seq_lens, mask, dra
     _check(lib().moe_latent_attention(_ptr(q), cache, _ptr(block_table), _ptr(seq_lens), _ptr(mask),
                                       _ptr(draft_lens), d, _ptr(out), _ptr(ws), _nbytes(ws),
                                       _ptr(status), _stream(stream)), "moe_latent_attention")
+
+
+def moe_expanded_attention(q, k_nope, k_rope, v, cu_q, cu_k, d: ExpandedDims, out, status=None,
+                           stream=None) -> None:
+    _check(lib().moe_expanded_attention(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(cu_q),
+                                        _ptr(cu_k), d, _ptr(out), _ptr(status), _stream(stream)),
+           "moe_expanded_attention")
 
 
 def linear_fp8_workspace_bytes(d: LinearDims) -> int:

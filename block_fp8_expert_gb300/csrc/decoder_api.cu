@@ -386,6 +386,47 @@ moe_status moe_latent_attention(const uint16_t* q, moe_latent_cache cache,
   return MOE_OK;
 }
 
+moe_status moe_expanded_attention(const uint16_t* q, const uint16_t* k_nope,
+                                  const uint16_t* k_rope, const uint16_t* v, const int32_t* cu_q,
+                                  const int32_t* cu_k, moe_expanded_dims d, uint16_t* out,
+                                  int32_t* status, void* stream) {
+  moe_status s;
+  if (d.B < 0 || d.Tq < 0 || d.Tk < 0)
+    return fail(MOE_ERR_INVALID_ARG, "B = %d, Tq = %d, Tk = %d", d.B, d.Tq, d.Tk);
+  if (d.H < 1 || d.H > 1024) return fail(MOE_ERR_UNSUPPORTED, "H = %d outside [1, 1024]", d.H);
+  // (a query tile's rows and a key tile's tokens past the end count as 32 bits, too)
+  if (d.Tq > 0x7fffff00 || d.Tk > 0x7fffff00)
+    return fail(MOE_ERR_UNSUPPORTED, "Tq = %d, Tk = %d: at most 2^31 - 256", d.Tq, d.Tk);
+  if ((s = check_stride(d.q_stride, 192, 8, "q_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.q_head_stride, 192, 8, "q_head_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.k_stride, 128, 8, "k_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.k_head_stride, 128, 8, "k_head_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.rope_stride, 64, 8, "rope_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.v_stride, 128, 8, "v_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.v_head_stride, 128, 8, "v_head_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.out_stride, 128, 8, "out_stride")) != MOE_OK) return s;
+  if ((s = check_stride(d.out_head_stride, 128, 8, "out_head_stride")) != MOE_OK) return s;
+  // a copy's map holds byte strides below 2^40
+  for (const long long x : {d.q_stride, d.q_head_stride, d.k_stride, d.k_head_stride, d.rope_stride, d.v_stride,
+                            d.v_head_stride})
+    if (x >= (1ll << 39)) return fail(MOE_ERR_UNSUPPORTED, "a stride of %lld elements: need less than 2^39", x);
+  if (!expanded_attention_fits(d)) return fail(MOE_ERR_UNSUPPORTED, "(Tq / 256 + B) * H too large");
+  REQUIRE_OPT_PTR(status);
+  if (d.B == 0 || d.Tq == 0) return MOE_OK;
+  REQUIRE_PTR(q);
+  if (d.Tk > 0) {
+    REQUIRE_PTR(k_nope);
+    REQUIRE_PTR(k_rope);
+    REQUIRE_PTR(v);
+  }
+  REQUIRE_ELEMENTS(cu_q);
+  REQUIRE_ELEMENTS(cu_k);
+  REQUIRE_PTR(out);
+  CUDA_CHECK(launch_expanded_attention(q, k_nope, k_rope, v, cu_q, cu_k, d, out, status, (cudaStream_t)stream),
+             "moe_expanded_attention");
+  return MOE_OK;
+}
+
 moe_status moe_linear_fp8_workspace_bytes(moe_linear_dims d, size_t* bytes) {
   moe_status s = check_linear(d);
   if (s != MOE_OK) return s;

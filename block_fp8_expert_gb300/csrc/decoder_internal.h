@@ -72,6 +72,13 @@ cudaError_t launch_latent_store(const uint16_t* kv, const float* norm, const flo
                                 const moe_latent_dims& d, const moe_latent_cache& cache,
                                 uint16_t* q_out, uint16_t* rows, int32_t* status, cudaStream_t s);
 
+// Whether the grid fits 31 bits.
+bool expanded_attention_fits(const moe_expanded_dims& d);
+cudaError_t launch_expanded_attention(const uint16_t* q, const uint16_t* k_nope, const uint16_t* k_rope,
+                                      const uint16_t* v, const int32_t* cu_q, const int32_t* cu_k,
+                                      const moe_expanded_dims& d, uint16_t* out, int32_t* status,
+                                      cudaStream_t s);
+
 size_t linear_fp8_workspace(const moe_linear_dims& d);
 cudaError_t launch_linear_fp8(const uint16_t* x, const moe_fp8_mat& w, const float* bias,
                               const moe_linear_dims& d, uint16_t* out, void* ws, int32_t* status,

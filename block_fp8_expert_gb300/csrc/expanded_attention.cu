@@ -1,0 +1,481 @@
+// Causal attention over ragged sequences with heads of 128 + 64 query and key
+// dimensions, the 64 shared by the keys of all heads, and values of 128
+// (moe_expanded_attention: latent attention in its expanded form).
+//
+//   out = sum_t p_t v_t / sum_t p_t,   p_t = 2^(s_t - m),  s_t = scale log2(e) q . k_t
+//
+// in one pass over the keys with a running maximum m and sum l.
+#include <algorithm>
+
+#include "attention_tc.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kNope = 128, kRope = 64, kVd = 128;
+constexpr int kBlock = 128;         // rows of a query tile, tokens of a key tile
+constexpr int kSlot = kBlock * 128;  // 128 rows or tokens x 64 dimensions, 128-byte swizzled
+constexpr int kQChunks = (kNope + kRope) / 64, kVChunks = kVd / 64;
+constexpr int kSlots = 8;           // of the ring of keys and values: 5 per tile
+constexpr int kPerTile = kQChunks + kVChunks;
+constexpr int kSoftWarps = 8;       // four per query tile
+constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr int kSmem = (2 * kQChunks + kSlots) * kSlot + 1024;
+constexpr int kOCol = 2 * kBlock;   // TMEM: the two tiles' scores (then weights), then their outputs
+
+struct ExpandedArgs {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  moe_expanded_dims d;
+  int blocks;  // of 256 rows, at most, per head
+  float scale2;
+  uint16_t* out;
+  int32_t* status;
+};
+
+struct ExpandedShared {
+  uint64_t q_full[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2];
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  int add_to[2];  // the tile's products are added to what the outputs hold
+  int seq, blk;
+};
+
+// The rows and keys of a sequence, within the tensors.
+struct Seq {
+  int q0, lq, k0, lk;
+};
+__device__ __forceinline__ Seq seq_of(const ExpandedArgs& a, int b, bool* bad = nullptr) {
+  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+  Seq s;
+  s.q0 = min(max(q0, 0), a.d.Tq);
+  s.lq = min(max(q1, s.q0), a.d.Tq) - s.q0;
+  s.k0 = min(max(k0, 0), a.d.Tk);
+  s.lk = min(max(k1, s.k0), a.d.Tk) - s.k0;
+  if (bad) *bad = s.q0 != q0 || s.q0 + s.lq != q1 || s.k0 != k0 || s.k0 + s.lk != k1;
+  return s;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 A, B, R;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n mul.rn.f32x2 R, A, B;\n"
+      " mov.b64 {%0, %1}, R;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 A, B, R;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n add.rn.f32x2 R, A, B;\n"
+      " mov.b64 {%0, %1}, R;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t v) {
+  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1)
+k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap vmap,
+                     const ExpandedArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ExpandedShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                   ~(uintptr_t)1023);
+  uint8_t* const ring = smem + 2 * kQChunks * kSlot;
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sh.q_full[x], 1);
+      mbar_init(&sh.s_full[x], 1);
+      mbar_init(&sh.p_full[x], kSoftWarps / 2);
+      mbar_init(&sh.o_full[x], 1);
+    }
+    sh.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kSoftWarps) {
+    tc::tmem_alloc(&sh.tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  griddep_wait();
+  griddep_trigger();
+  // heads outermost, so that the CTAs at work share few heads' keys; a
+  // sequence's last rows, which see the most, first
+  const int h = blockIdx.x / a.blocks;
+  if (warp == 0) {
+    int want = blockIdx.x % a.blocks, seq = -1, blk = 0;
+    for (int b0 = 0; b0 < a.d.B && seq < 0; b0 += 32) {
+      const int b = b0 + lane;
+      int n = 0;
+      if (b < a.d.B) {
+        bool bad;
+        n = cdiv(seq_of(a, b, &bad).lq, 2 * kBlock);
+        if (bad && blockIdx.x == 0) raise_status(a.status, MOE_DEV_BAD_POSITION);
+      }
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const unsigned here = __ballot_sync(kAll, want < incl);
+      if (here) {
+        const int l = __ffs(here) - 1;
+        seq = b0 + l;
+        blk = __shfl_sync(kAll, incl, l) - 1 - want;  // (counted from the last)
+      } else {
+        want -= __shfl_sync(kAll, incl, 31);
+      }
+    }
+    if (lane == 0) {
+      sh.seq = seq;
+      sh.blk = blk;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;
+  volatile int* const dead = &sh.abort_flag;
+  const bool any = sh.seq >= 0;
+  const Seq s = any ? seq_of(a, sh.seq) : Seq{0, 0, 0, 0};
+  const int row0 = sh.blk * 2 * kBlock, off = s.lk - s.lq;
+  // key tiles of either query tile: up to what its last row sees
+  auto tiles_of = [&](int x) {
+    const int r0 = row0 + x * kBlock;
+    if (!any || r0 >= s.lq) return 0;
+    return cdiv(max(0, min(r0 + kBlock, s.lq) + off), kBlock);
+  };
+  const int nt[2] = {tiles_of(0), tiles_of(1)}, n = max(nt[0], nt[1]);
+
+  if (warp == kSoftWarps + 1) {
+    // ---- loads
+    if (tc::elect_one() && n > 0) {
+      for (int x = 0; x < 2; ++x)
+        if (nt[x] > 0) {
+          mbar_arrive_expect_tx(&sh.q_full[x], kQChunks * kSlot);
+          for (int c = 0; c < kQChunks; ++c)
+            tma_load_3d(smem + (x * kQChunks + c) * kSlot, &qmap, 64 * c, h, s.q0 + row0 + x * kBlock,
+                        &sh.q_full[x]);
+        }
+    }
+    __syncwarp();
+    int i = 0;
+    for (int j = 0; j < n; ++j)
+      for (int c = 0; c < kPerTile; ++c, ++i) {
+        const int slot = i % kSlots;
+        if (i >= kSlots) role_wait(dead, &sh.empty[slot], (uint32_t)((i / kSlots - 1) & 1), a.status);
+        if (tc::elect_one() && !*dead) {
+          mbar_arrive_expect_tx(&sh.full[slot], kSlot);
+          const int t = s.k0 + j * kBlock;
+          if (c < 2)
+            tma_load_3d(ring + slot * kSlot, &kmap, 64 * c, h, t, &sh.full[slot]);
+          else if (c == 2)
+            tc::tma_load_2d(ring + slot * kSlot, &rmap, 0, t, &sh.full[slot]);
+          else
+            tma_load_3d(ring + slot * kSlot, &vmap, 64 * (c - 3), h, t, &sh.full[slot]);
+        }
+        __syncwarp();
+      }
+    // every copy has landed and been read before the CTA's memory goes
+    if (lane == 0)
+      for (int k = max(0, i - kSlots); k < i; ++k) {
+        mbar_wait(&sh.full[k % kSlots], (uint32_t)((k / kSlots) & 1));
+        if (!*dead) mbar_wait(&sh.empty[k % kSlots], (uint32_t)((k / kSlots) & 1));
+      }
+    __syncwarp();
+  } else if (warp == kSoftWarps) {
+    // ---- the products of both query tiles, taking turns: S = Q K^T of the next
+    // key tile follows O += P V of this one
+    const uint32_t q0 = smem_u32(smem), r0 = smem_u32(ring);
+    constexpr uint32_t idesc_s = idesc_bf16(kBlock, kBlock, false, false);
+    constexpr uint32_t idesc_o = idesc_bf16(kBlock, 64, false, true);
+    auto wait_slot = [&](int i) {
+      role_wait(dead, &sh.full[i % kSlots], (uint32_t)((i / kSlots) & 1), a.status);
+    };
+    auto scores = [&](int x, int j) {  // of query tile x and key tile j
+      tc::fence_after_sync();
+      if (tc::elect_one() && !*dead) {
+#pragma unroll
+        for (int c = 0; c < kQChunks; ++c) {
+          const uint32_t k = r0 + ((j * kPerTile + c) % kSlots) * kSlot;
+          const uint32_t q = q0 + (x * kQChunks + c) * kSlot;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_f16(tmem + x * kBlock, tc::sw128_desc(q + kk * 32), tc::sw128_desc(k + kk * 32), idesc_s,
+                        c | kk ? 1u : 0u);
+        }
+        tc::commit(&sh.s_full[x]);
+      }
+      __syncwarp();
+    };
+    auto outputs = [&](int x, int j) {
+      role_wait(dead, &sh.p_full[x], (uint32_t)(j & 1), a.status);
+      tc::fence_after_sync();
+      if (tc::elect_one() && !*dead) {
+        const uint32_t add = sh.add_to[x];
+#pragma unroll
+        for (int c = 0; c < kVChunks; ++c) {
+          const uint32_t v = r0 + ((j * kPerTile + kQChunks + c) % kSlots) * kSlot;
+#pragma unroll
+          for (int kk = 0; kk < kBlock / 16; ++kk)
+            tc::mma_f16_ts(tmem + kOCol + x * kVd + 64 * c, tmem + x * kBlock + 8 * kk,
+                           sw128_desc_mn(v + kk * 2048, 0), idesc_o, add | (kk ? 1u : 0u));
+        }
+        if (j == nt[x] - 1) tc::commit(&sh.o_full[x]);
+      }
+      __syncwarp();
+    };
+    auto release = [&](int i0, int count) {
+      if (tc::elect_one() && !*dead)
+        for (int i = i0; i < i0 + count; ++i) tc::commit(&sh.empty[i % kSlots]);
+      __syncwarp();
+    };
+    for (int x = 0; x < 2; ++x)
+      if (nt[x] > 0) role_wait(dead, &sh.q_full[x], 0, a.status);
+    for (int j = -1; j < n; ++j) {
+      if (j >= 0)
+        for (int c = 0; c < kVChunks; ++c) wait_slot(j * kPerTile + kQChunks + c);
+      for (int x = 0; x < 2; ++x) {
+        if (j >= 0 && j < nt[x]) outputs(x, j);
+        if (j >= 0 && x == 1) release(j * kPerTile + kQChunks, kVChunks);
+        if (j + 1 < n && x == 0)
+          for (int c = 0; c < kQChunks; ++c) wait_slot((j + 1) * kPerTile + c);
+        if (j + 1 < nt[x]) scores(x, j + 1);
+      }
+      if (j + 1 < n) release((j + 1) * kPerTile, kQChunks);
+    }
+  } else {
+    // ---- softmax.  A thread owns a row.
+    const int x = warp >> 2, r = 32 * (warp & 3) + lane, i = row0 + x * kBlock + r;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t t_s = lanes + x * kBlock, t_o = lanes + kOCol + x * kVd;
+    const int limit = i < s.lq ? max(0, i + off + 1) : 0;  // keys that the row sees: the first ones
+    // tiles that every row of the warp, or of the CTA, sees whole
+    const int whole = (i - lane < s.lq ? max(0, i - lane + off + 1) : s.lk) / kBlock;
+    const int whole_cta = max(0, row0 + off + 1) / kBlock;
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < n; ++j) {
+      const bool mine = j < nt[x];
+      bool add_to = j > 0;
+      float2 v[kBlock / 2];
+      if (mine) {
+        role_wait(dead, &sh.s_full[x], (uint32_t)(j & 1), a.status);
+        tc::fence_after_sync();
+        uint32_t raw[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(t_s + 32 * c, raw[c]);
+        tc::wait_ld();
+#pragma unroll
+        for (int c = 0; c < kBlock / 2; ++c)
+          v[c] = mul2(make_float2(__uint_as_float(raw[c / 16][2 * c % 32]), __uint_as_float(raw[c / 16][2 * c % 32 + 1])),
+                      make_float2(a.scale2, a.scale2));
+        if (j >= whole) {
+          const int left = limit - j * kBlock;
+#pragma unroll
+          for (int c = 0; c < kBlock / 2; ++c) {
+            if (2 * c >= left) v[c].x = -INFINITY;
+            if (2 * c + 1 >= left) v[c].y = -INFINITY;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kBlock / 2; ++c) mx[c & 3] = fmaxf(mx[c & 3], fmaxf(v[c].x, v[c].y));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // (-inf + slack is -inf: a row's first score moves its maximum)
+        if (__any_sync(kAll, top > m + kMaxSlack)) {
+          const float mn = fmaxf(m, top);
+          const float f = m == mn ? 1.f : exp2_fast(m - mn);
+          l *= f;
+          m = mn;
+          if (j > 0) {  // (the products of the tile before came before these scores)
+#pragma unroll 1
+            for (int c = 0; c < kVd; c += 16) {
+              uint32_t o[16];
+              ld_32x32b_x16(t_o + c, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+              st_32x32b_x16(t_o + c, o);
+            }
+            tc::wait_st();
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            const float2 e = add2(v[32 * c + u], make_float2(-ms, -ms));
+            w[u] = pack_bf16x2(exp2_fast(e.x), exp2_fast(e.y));
+            sum = add2(sum, make_float2(bf16_lo(w[u]), bf16_hi(w[u])));
+          }
+          tc::st_32x32b_x32(t_s + 32 * c, w);
+        }
+        l += sum.x + sum.y;
+        tc::wait_st();
+      }
+      if (j >= whole_cta) {
+        // Tokens that some rows do not see, or that are another sequence's: a
+        // value that is not finite reaches the rows that see it and no other.  It
+        // is added to their outputs, and the tile holds 0 in its place (times a
+        // weight of 0 it would be NaN).
+        uint8_t* chunk[kVChunks];
+        bool odd = false;
+#pragma unroll
+        for (int c = 0; c < kVChunks; ++c) {
+          const int k = j * kPerTile + kQChunks + c;
+          chunk[c] = ring + (k % kSlots) * kSlot;
+          role_wait(dead, &sh.full[k % kSlots], (uint32_t)((k / kSlots) & 1), a.status);
+          for (int e = tid; e < kSlot / 16; e += kSoftWarps * 32) {
+            const uint4 w = *reinterpret_cast<const uint4*>(chunk[c] + e * 16);
+            odd |= bf16x2_nonfinite(w.x) || bf16x2_nonfinite(w.y) || bf16x2_nonfinite(w.z) ||
+                   bf16x2_nonfinite(w.w);
+          }
+        }
+        if (bar_any(1, kSoftWarps * 32, odd)) {
+          if (mine) {
+#pragma unroll 1
+            for (int d0 = 0; d0 < kVd; d0 += 16) {
+              uint32_t o[16];
+              ld_32x32b_x16(t_o + d0, o);
+              tc::wait_ld();
+              if (j == 0) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u) o[u] = 0u;
+              }
+#pragma unroll 1
+              for (int t = 0; t < kBlock; ++t) {
+                const uint8_t* row = chunk[0] + (d0 >> 6) * (chunk[1] - chunk[0]);
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                  const uint32_t w = *reinterpret_cast<const uint16_t*>(
+                      row + tc::sw128_off(t, ((d0 + u) >> 3) & 7) + 2 * (u & 7));
+                  if ((w & 0x7F80u) == 0x7F80u && j * kBlock + t < limit)
+                    o[u] = __float_as_uint(__uint_as_float(o[u]) + __uint_as_float(w << 16));
+                }
+              }
+              st_32x32b_x16(t_o + d0, o);
+            }
+            tc::wait_st();
+          }
+          named_bar(1, kSoftWarps * 32);  // every thread has read the values
+#pragma unroll
+          for (int c = 0; c < kVChunks; ++c)
+            for (int e = tid; e < kSlot / 2; e += kSoftWarps * 32) {
+              uint16_t* w = reinterpret_cast<uint16_t*>(chunk[c]) + e;
+              if ((*w & 0x7F80u) == 0x7F80u) *w = 0;
+            }
+          tc::fence_proxy_async();
+          named_bar(1, kSoftWarps * 32);  // none is left
+          add_to = true;
+        }
+      }
+      if (mine) {
+        if ((tid & 127) == 0) sh.add_to[x] = add_to;
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[x]);
+      }
+    }
+    // ---- the rows' outputs, through the query tile's shared memory (whose last
+    // product has been made), so that a row is written by neighbouring lanes
+    const int r_warp = row0 + x * kBlock + 32 * (warp & 3);
+    if (any && r_warp < s.lq) {
+      uint8_t* const stage = smem + x * kQChunks * kSlot + (warp & 3) * 32 * 2 * kVd;
+      if (nt[x] > 0) {
+        role_wait(dead, &sh.o_full[x], 0, a.status);
+        tc::fence_after_sync();
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (nt[x] > 0) {
+          tc::ld_32x32b_x32(t_o + 32 * c, o);
+          tc::wait_ld();
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv, __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+          if (l == 0.f) w[0] = w[1] = w[2] = w[3] = 0u;  // a row that sees nothing
+          const int k = 4 * c + u;  // the row's 16-byte chunk
+          *reinterpret_cast<uint4*>(stage + lane * 256 + ((k ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      __syncwarp();
+      for (int y = 0; y < 32; y += 2) {
+        const int row = y + (lane >> 4), k = lane & 15;
+        if (r_warp + row < s.lq)
+          *reinterpret_cast<uint4*>(a.out + (long long)(s.q0 + r_warp + row) * a.d.out_stride +
+                                    h * a.d.out_head_stride + 8 * k) =
+              *reinterpret_cast<const uint4*>(stage + row * 256 + ((k ^ (row & 7)) << 4));
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kSoftWarps) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+namespace {
+
+long long expanded_blocks(const moe_expanded_dims& d) { return (long long)d.Tq / (2 * kBlock) + d.B; }
+
+}  // namespace
+
+bool expanded_attention_fits(const moe_expanded_dims& d) { return expanded_blocks(d) * d.H < (1ll << 31); }
+
+cudaError_t launch_expanded_attention(const uint16_t* q, const uint16_t* k_nope, const uint16_t* k_rope,
+                                      const uint16_t* v, const int32_t* cu_q, const int32_t* cu_k,
+                                      const moe_expanded_dims& d, uint16_t* out, int32_t* status,
+                                      cudaStream_t s) {
+  CUtensorMap qmap, kmap, rmap, vmap;
+  cudaError_t err;
+  const int Tk = std::max(1, d.Tk);  // (without keys nothing is loaded)
+  if (d.Tk == 0) k_nope = k_rope = v = q;
+  if ((err = make_tensor_map_3d(&qmap, q, d.Tq, d.H, kNope + kRope, d.q_stride, d.q_head_stride, 64, kBlock)) !=
+          cudaSuccess ||
+      (err = make_tensor_map_3d(&kmap, k_nope, Tk, d.H, kNope, d.k_stride, d.k_head_stride, 64, kBlock)) !=
+          cudaSuccess ||
+      (err = make_tensor_map_2d(&rmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k_rope, Tk, kRope, 64, kBlock, 128,
+                                d.rope_stride)) != cudaSuccess ||
+      (err = make_tensor_map_3d(&vmap, v, Tk, d.H, kVd, d.v_stride, d.v_head_stride, 64, kBlock)) != cudaSuccess)
+    return err;
+  if ((err = ensure_smem((const void*)k_expanded_attention, kSmem)) != cudaSuccess) return err;
+  const ExpandedArgs a{cu_q, cu_k, d, (int)expanded_blocks(d), d.scale * kLog2e, out, status};
+  return launch_k(k_expanded_attention, dim3((unsigned)(expanded_blocks(d) * d.H)), dim3(kThreads), kSmem, s, true,
+                  qmap, kmap, rmap, vmap, a);
+}
+
+}  // namespace moe

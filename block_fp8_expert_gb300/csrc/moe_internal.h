@@ -53,6 +53,12 @@ cudaError_t make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, int 
                                const void* base, long long rows, int cols, int box_cols,
                                int box_rows, int swizzle_bytes, long long row_stride = 0);
 
+// 3-D TMA map over bf16 elements [rows, heads, cols] with row_stride and
+// head_stride (in elements): box = box_cols x 1 head x box_rows, 128-byte
+// swizzle, out-of-range elements read as zero.
+cudaError_t make_tensor_map_3d(CUtensorMap* map, const void* base, long long rows, int heads, int cols,
+                               long long row_stride, long long head_stride, int box_cols, int box_rows);
+
 // Largest expert count the library accepts.
 constexpr int kMaxExperts = 1024;
 

@@ -633,6 +633,70 @@ class LatentAttention(_DraftAttention):
         return _lib.latent_attention_workspace_bytes(d, self.R)
 
 
+class ExpandedAttention(_Status):
+    """Latent attention in its expanded form, for prompts: causal over ragged
+    sequences, keys of 128 dimensions per head and 64 that the heads share,
+    values of 128 (moe_expanded_attention).  scale may be set again."""
+
+    _free = frozenset(("_sizes", "scale"))
+
+    def __init__(self, H: int, scale: Optional[float] = None, device="cuda"):
+        super().__init__(device)
+        self.H = H
+        self.scale = 1.0 / math.sqrt(192) if scale is None else scale
+        self._sizes = None, None  # (read and replaced as one: threads may share the object)
+        self._held = (self._dev, H, self._status, _lib.lib().moe_expanded_attention)
+
+    def forward(self, q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
+                cu_q: torch.Tensor, cu_k: torch.Tensor, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """q bf16 [Tq, H, 192], k_nope and v bf16 [Tk, H, 128], k_rope bf16
+        [Tk, 64], any strides between tokens and heads; cu_q, cu_k int32 [B +
+        1]: where each sequence's tokens begin, its queries being its last
+        tokens -> out bf16 [Tq, H, 128] (rows of no sequence are left as they
+        were)."""
+        here, H, status, call = self._held
+        dev, qs = q.get_device(), q.stride()
+        Tq, Tk, B = q.shape[0], k_rope.shape[0], cu_q.shape[0] - 1
+        if dev != here or q.dtype != _BF16 or q.shape != (Tq, H, 192) or qs[-1] != 1:
+            _refuse(q, "q", _BF16, (Tq, H, 192), here, _ROWS)
+        if dev != _current_device():
+            _refuse_device(dev, _current_device())
+        ks, rs, vs = k_nope.stride(), k_rope.stride(), v.stride()
+        if (k_nope.dtype != _BF16 or k_nope.get_device() != dev or k_nope.shape != (Tk, H, 128)
+                or ks[2] != 1):
+            _refuse(k_nope, "k_nope", _BF16, (Tk, H, 128), dev, _ROWS)
+        if (k_rope.dtype != _BF16 or k_rope.get_device() != dev or k_rope.shape != (Tk, 64)
+                or rs[1] != 1):
+            _refuse(k_rope, "k_rope", _BF16, (Tk, 64), dev, _ROWS)
+        if v.dtype != _BF16 or v.get_device() != dev or v.shape != (Tk, H, 128) or vs[2] != 1:
+            _refuse(v, "v", _BF16, (Tk, H, 128), dev, _ROWS)
+        for t, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
+            if (t.dtype != _I32 or t.get_device() != dev or t.shape != (B + 1,) or B < 0
+                    or not t.is_contiguous()):
+                _refuse(t, name, _I32, (max(B, 0) + 1,), dev)
+        if out is None:
+            out = new_on(stream, Tq, H, 128, dtype=_BF16, device=q.device)
+        os = out.stride()
+        if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (Tq, H, 128)
+                or os[2] != 1):
+            _refuse(out, "out", _BF16, (Tq, H, 128), dev, _ROWS)
+        key = (B, Tq, Tk, qs, ks, rs[0], vs, os, self.scale)
+        known, dims = self._sizes
+        if key != known:
+            def pair(s, T, width):  # the strides that are used
+                return (s[0] if T > 1 else width, s[1] if H > 1 else width)
+            dims = _lib.ExpandedDims(B, Tq, Tk, H, key[8], *pair(qs, Tq, 192), *pair(ks, Tk, 128),
+                                     rs[0] if Tk > 1 else 64, *pair(vs, Tk, 128), *pair(os, Tq, 128))
+            self._sizes = key, dims
+        st = call(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
+                  cu_k.data_ptr(), dims, out.data_ptr(), status,
+                  _raw_stream(dev) if stream is None else _handle(stream))
+        if st:
+            _lib._check(st, "moe_expanded_attention")
+        return out
+
+
 class Fp8Linear(_Status):
     """x W^T + bias with block-FP8 weights (codes [N, K] uint8 or
     float8_e4m3fn, scales float32 [ceil(N/128), ceil(K/128)]) and E4M3

@@ -684,6 +684,39 @@ moe_status moe_latent_attention(const uint16_t* q, moe_latent_cache cache,
                                 uint16_t* out, void* ws, size_t ws_bytes,
                                 int32_t* status, void* stream);
 
+/* One moe_expanded_attention call: B sequences of Tq query tokens and Tk key
+ * tokens in all, H heads.  Strides in elements, multiples of 8: between tokens
+ * and between heads, at least what they step over. */
+typedef struct {
+  int32_t B, Tq, Tk, H;
+  float scale;
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride, rope_stride,
+      v_stride, v_head_stride, out_stride, out_head_stride;
+} moe_expanded_dims;
+
+/*
+ * Latent attention in its expanded form, for prompts: every head has keys of
+ * 128 dimensions of its own and 64 that all heads share, and values of 128:
+ *   out[i,h] = sum_t softmax_t(scale * (q[i,h,:128] . k_nope[t,h]
+ *                                       + q[i,h,128:] . k_rope[t])) v[t,h]
+ * Sequence b has query tokens cu_q[b] .. cu_q[b+1] - 1 and key tokens cu_k[b]
+ * .. cu_k[b+1] - 1, of which the last are its query tokens: query token i of lq
+ * sees the keys t <= i + lk - lq (a row that sees none answers zeros).
+ * q bf16 [Tq, H, 192], k_nope [Tk, H, 128], k_rope [Tk, 64], v [Tk, H, 128]
+ * and out [Tq, H, 128] by their strides; cu_q, cu_k int32 [B + 1], which do not
+ * fall.  Rows of no sequence are left as they were, and keys and values that a
+ * row does not see do not reach it, whatever they are.
+ * Scores, maxima, sums and outputs are fp32; the softmax weights are rounded
+ * to bf16 (2^-9 of the weight) before both the product and their sum.
+ * Offsets outside the tensors, or falling ones, raise MOE_DEV_BAD_POSITION and
+ * are clamped.
+ */
+moe_status moe_expanded_attention(const uint16_t* q, const uint16_t* k_nope,
+                                  const uint16_t* k_rope, const uint16_t* v,
+                                  const int32_t* cu_q, const int32_t* cu_k,
+                                  moe_expanded_dims d, uint16_t* out,
+                                  int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
