@@ -22,17 +22,38 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
   return tc::idesc_f16_f32(M, N) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16);
 }
-// Descriptor of an operand whose M (or N) axis is contiguous, 128-byte
-// swizzled: rows of one K each hold 64 elements of M, groups of 8 rows lie 1024
-// bytes apart, and the next 64 elements of M `next` bytes further on.
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t smem_addr, uint32_t next) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
-  d |= (uint64_t)(next >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Descriptors of 128-byte swizzled operands are built from their low words,
+// which alone hold addresses, so that stepping through a tile is one addition
+// (of bytes / 16).  K-major as tc::sw128_desc; with a contiguous M (or N) axis,
+// rows of one K each hold 64 elements of M, groups of 8 rows lie 1024 bytes
+// apart, and the next 64 elements of M `next` bytes further on.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k(uint32_t smem_addr) { return (smem_addr >> 4) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t smem_addr, uint32_t next) {
+  return (smem_addr >> 4) | (next >> 4) << 16;
+}
+// The same value in every lane, as the compiler then knows: MMA operands have
+// to be in uniform registers, and what it cannot prove uniform is moved there
+// word by word before each MMA (51 cycles for one of 64 x 64 x 16 that takes 32).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(kAll, v); }
+
+// D[tmem] (+)= A[smem] B[smem]^T, descriptors by their low words.
+__device__ __forceinline__ void mma_ss(uint32_t tmem_d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %5, 0;\n mov.b64 da, {%1, %3};\n"
+      " mov.b64 db, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n}\n" ::"r"(tmem_d),
+      "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]^T.
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %5, 0;\n mov.b64 db, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // Rows lane / 4 and lane / 4 + 8 of the first 16 lanes of this warp's TMEM
@@ -47,6 +68,16 @@ __device__ __forceinline__ void ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32])
         "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// The same of 32 columns.
+__device__ __forceinline__ void ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 // 16 consecutive columns of this thread's TMEM lane.
@@ -87,33 +118,58 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool yes) {
   return r != 0;
 }
 
+// mbar_try_wait that may sleep for kNap nanoseconds.
+constexpr uint32_t kNap = 20000;
+__device__ __forceinline__ bool mbar_nap(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kNap)
+      : "memory");
+  return ok != 0;
+}
 // Warp-uniform bounded wait.  Once one wait of a CTA has run out, `abort_flag`
-// is set and every other returns at once: the roles then run through the rest
+// is set and the others return after a nap: the roles then run through the rest
 // of their loops, whose results are reported as invalid, and keep their
-// barriers matched.
+// barriers matched.  (Clocks and flag are only read once a nap is over: reading
+// them takes as long as most waits, and a warp that polls takes issue slots and
+// shared-memory cycles from those that work.)
 __device__ __forceinline__ void role_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
                                           int32_t* status) {
-  bool done = mbar_try_wait(bar, parity);
-  if (__all_sync(kAll, done)) return;
+  if (__all_sync(kAll, mbar_nap(bar, parity))) return;
   const WaitBudget b = wait_budget();
-  for (uint32_t n = 1;; ++n) {
+  while (true) {
+    bool done = mbar_nap(bar, parity);
     if (__any_sync(kAll, done)) {
       // (the phase is complete: the others see it, too)
       for (int r = 0; !done && r < (1 << 16); ++r) done = mbar_try_wait(bar, parity);
       if (__all_sync(kAll, done)) return;
       break;
     }
-    if ((n & 31) == 1) {
-      const bool give_up = *abort_flag != 0 || budget_spent(b);
-      if (__any_sync(kAll, give_up)) break;
-    }
-    done = mbar_try_wait(bar, parity);
+    if (__any_sync(kAll, *abort_flag != 0 || budget_spent(b))) break;
   }
   if ((threadIdx.x & 31) == 0 && !*abort_flag) {
     *abort_flag = 1;
     raise_status(status, MOE_DEV_WAIT_TIMEOUT);
   }
   __syncwarp();
+}
+
+// The same by a thread on its own.
+__device__ __forceinline__ void lane_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
+                                          int32_t* status) {
+  if (mbar_nap(bar, parity)) return;
+  const WaitBudget b = wait_budget();
+  while (!mbar_nap(bar, parity)) {
+    if (*abort_flag) return;
+    if (budget_spent(b)) {
+      *abort_flag = 1;
+      raise_status(status, MOE_DEV_WAIT_TIMEOUT);
+      return;
+    }
+  }
 }
 
 // The low n bits, 0 <= n <= 64.

@@ -394,6 +394,7 @@ moe_status moe_expanded_attention(const uint16_t* q, const uint16_t* k_nope,
   if (d.B < 0 || d.Tq < 0 || d.Tk < 0)
     return fail(MOE_ERR_INVALID_ARG, "B = %d, Tq = %d, Tk = %d", d.B, d.Tq, d.Tk);
   if (d.H < 1 || d.H > 1024) return fail(MOE_ERR_UNSUPPORTED, "H = %d outside [1, 1024]", d.H);
+  if (!(d.scale > 0.f)) return fail(MOE_ERR_INVALID_ARG, "scale = %g: need a positive number", d.scale);
   // (a query tile's rows and a key tile's tokens past the end count as 32 bits, too)
   if (d.Tq > 0x7fffff00 || d.Tk > 0x7fffff00)
     return fail(MOE_ERR_UNSUPPORTED, "Tq = %d, Tk = %d: at most 2^31 - 256", d.Tq, d.Tk);

@@ -20,15 +20,20 @@ using namespace attn;
 constexpr int kTile = 64;      // tokens per tile
 constexpr int kRows = 64;      // rows (query head x new token) of a CTA at most
 constexpr int kChunk = 8192;   // 64 tokens or rows x 64 dimensions, 128-byte swizzled
-constexpr int kSoftWarps = 4;  // softmax, rescaling, output; the MMA warp; the loading warps
 constexpr int kSegCost = 3;    // what a segment costs a CTA beside its tiles, in tiles
 constexpr int kNoRow = 0x7fffffff;
 constexpr int kMinUnits = 2;   // least share of a CTA
 constexpr int kOCol = 2 * kTile;  // TMEM: two buffers of scores, then the outputs
 constexpr long long kMaxTokens = 0x7fffff80;  // of a sequence: its tiles' ends fit 31 bits
 constexpr int kJoinThreads = 512;
+// Tiles whose tokens' notes (which are there, their scales) are kept: keys may be
+// replaced two tiles before the softmax reads the notes.
+constexpr int kNotes = 4;
 
-// LATENT: the values are the leading DV dimensions of the keys.
+// LATENT: the values are the leading DV dimensions of the keys.  A stage (64
+// tokens) consists of pieces that are loaded, waited for and given back one by
+// one: the keys and the values, or, of latent vectors, the 128 dimensions that
+// one block of the outputs reads (the first piece with the shared key part).
 template <int DK, int DV, bool LATENT, bool E4M3>
 struct DraftShape {
   static constexpr int kKChunks = DK / 64, kVChunks = LATENT ? 0 : DV / 64;
@@ -37,15 +42,18 @@ struct DraftShape {
   static constexpr int kParts = LATENT ? 1 : 2;  // bf16 parts of a softmax weight
   static constexpr int kQ = kKChunks * kChunk, kP = kParts * kChunk;
   static constexpr int kCtas = kStage <= 32 * 1024 && !LATENT ? 2 : 1;  // per SM
-  // barriers and small arrays, the stages' E4M3 scales, and the tiles' alignment
-  static constexpr int kFixed = 1920 + (E4M3 ? 4 * 2 * kTile * 4 : 0) + 1024;
-  static constexpr int kFit = (227 * 1024 / kCtas - kFixed - kQ - kP) / kStage;
-  static constexpr int kStages = kFit >= 4 ? 4 : 2;
-  static_assert(kFit >= 2, "shared memory");
-  static constexpr int kGroupWarps = (kCtas == 1 ? 8 : 4) / kStages;  // loading warps per stage
-  static constexpr int kWarps = kSoftWarps + 1 + kStages * kGroupWarps;
-  static constexpr int kSmem = kQ + kP + kStages * kStage + 1024;
   static constexpr int kBlocks = DV >= 128 ? DV / 128 : 1;  // of the outputs' dimensions
+  static constexpr int kPieces = LATENT ? kBlocks : 2;
+  // barriers and small arrays, the stages' E4M3 scales, and the tiles' alignment
+  static constexpr int kFixed = 2048 + (E4M3 ? kNotes * 2 * kTile * 4 : 0) + 1024;
+  static constexpr int kFit = (227 * 1024 / kCtas - kFixed - kQ - kP) / kStage;
+  static constexpr int kStages = kFit >= 4 && LATENT ? 4 : 2;
+  static_assert(kFit >= 2, "shared memory");
+  // softmax warps per 16 rows: they share the tile's tokens
+  static constexpr int kSplit = LATENT ? 2 : 1;
+  static constexpr int kSoft = 4 * kSplit;  // softmax warps; then two for MMAs; then one per piece
+  static constexpr int kWarps = kSoft + 2 + kStages * kPieces;
+  static constexpr int kSmem = kQ + kP + kStages * kStage + 1024;
   static constexpr int kCols = kOCol + kBlocks * kRows;
   static constexpr int kTmem = kCols <= 256 ? 256 : 512;
   static_assert(kTmem * kCtas <= 512, "TMEM");
@@ -186,19 +194,23 @@ __device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned* s_sc
   return *s_walk;
 }
 
-template <int STAGES, int WARPS, bool E4M3>
+template <int STAGES, int PIECES, int WARPS, bool E4M3>
 struct DraftShared {
-  uint64_t full[STAGES], empty[STAGES], s_full[2], s_empty[2], p_full, pv_done, q_full;
+  uint64_t full[STAGES][PIECES], empty[STAGES][PIECES], s_full[2], s_empty[2], p_full, pv_done, q_full;
   uint32_t tmem_base;
   volatile int abort_flag;
-  int add_to;  // the tile's products are added to what the outputs hold
-  uint32_t exists[STAGES][2];      // tokens of the stage that are there
-  alignas(8) float scale[E4M3 ? STAGES : 1][2][E4M3 ? kTile : 1];  // of its keys and values
-  float factor[kRows];             // on the outputs of a row, when its maximum moves
-  float inv[kRows];                // 1 / the row's sum
-  uint64_t seen[kRows];            // tokens of the tile that a row sees
-  long long at[kRows];             // the rows' outputs, in elements; -1: none
-  unsigned scan[WARPS];
+  uint32_t exists[kNotes][2];  // tokens of the tile that are there
+  alignas(8) float scale[E4M3 ? kNotes : 1][2][E4M3 ? kTile : 1];  // of its keys and values
+  float factor[kRows];  // on the outputs of a row, when its maximum moves
+  union {
+    float top[2][kRows];  // the largest score of a row, by halves of the tile
+    float inv[kRows];     // after the last tile: 1 / the row's sum
+  };
+  union {
+    unsigned scan[WARPS];
+    uint64_t seen[kRows];  // tokens of the tile that a row sees
+    long long at[kRows];   // after the last tile: the rows' outputs, in elements; -1: none
+  };
   Walk walk;
 };
 
@@ -226,9 +238,9 @@ __global__ void __launch_bounds__(DraftShape<DK, DV, LATENT, E4M3>::kWarps * 32,
                                   DraftShape<DK, DV, LATENT, E4M3>::kCtas)
 k_draft_attention(const DraftArgs a) {
   using S = DraftShape<DK, DV, LATENT, E4M3>;
-  constexpr int ST = S::kStages, GW = S::kGroupWarps;
+  constexpr int ST = S::kStages, NP = S::kPieces, kSoft = S::kSoft, kSoftThreads = kSoft * 32;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ DraftShared<ST, S::kWarps, E4M3> sh;
+  __shared__ DraftShared<ST, NP, S::kWarps, E4M3> sh;
   static_assert(sizeof(sh) + 1024 <= S::kFixed, "shared memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -237,21 +249,22 @@ k_draft_attention(const DraftArgs a) {
   uint8_t* const sm_p = smem + S::kQ;
   uint8_t* const sm_kv = smem + S::kQ + S::kP;
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&sh.full[i], GW);
-      mbar_init(&sh.empty[i], 1);
-    }
+    for (int i = 0; i < ST; ++i)
+      for (int x = 0; x < NP; ++x) {
+        mbar_init(&sh.full[i][x], 1);
+        mbar_init(&sh.empty[i][x], 1);
+      }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_empty[i], kSoftWarps);
+      mbar_init(&sh.s_empty[i], kSoft);
     }
-    mbar_init(&sh.p_full, kSoftWarps);
+    mbar_init(&sh.p_full, kSoft);
     mbar_init(&sh.pv_done, 1);
-    mbar_init(&sh.q_full, kSoftWarps);
+    mbar_init(&sh.q_full, kSoft);
     sh.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kSoftWarps) {
+  if (warp == kSoft) {
     tc::tmem_alloc(&sh.tmem_base, S::kTmem);
     tc::tmem_relinquish();
   }
@@ -268,12 +281,12 @@ k_draft_attention(const DraftArgs a) {
   Walk walk = plan<S::kWarps>(a, col, sh.scan, &sh.walk);
   volatile int* const dead = &sh.abort_flag;
 
-  if (warp > kSoftWarps) {
-    // ---- loading: a group of warps per stage, so that waiting for one
-    // stage's copies holds up no other
-    const int pw = warp - kSoftWarps - 1, stage = pw / GW, gw = pw % GW;
-    constexpr int TW = kTile / GW;           // tokens of a warp
-    constexpr int LL = TW < 32 ? 1 : TW / 32;  // of a lane
+  if (warp > kSoft + 1) {
+    // ---- loading: a warp per piece and stage, so that waiting for one piece's
+    // copies holds up no other
+    const int stage = (warp - kSoft - 2) / NP, piece = (warp - kSoft - 2) % NP;
+    uint64_t* const full = &sh.full[stage][piece];
+    uint64_t* const empty = &sh.empty[stage][piece];
     uint8_t* const dst = sm_kv + stage * S::kStage;
     struct Tok {
       long long at;   // elements from the head's first; -1: no such token
@@ -288,12 +301,12 @@ k_draft_attention(const DraftArgs a) {
         more = walk.next_tiles(a, p);
       }
     };
-    auto look_up = [&](Tok (&tk)[LL]) {
+    auto look_up = [&](Tok (&tk)[2]) {  // of tokens lane and lane + 32
 #pragma unroll
-      for (int u = 0; u < LL; ++u) {
+      for (int u = 0; u < 2; ++u) {
         tk[u].at = -1;
         tk[u].sat = 0;
-        const int tok = (p.tile + i) * kTile + gw * TW + 32 * u + (TW < 32 ? lane % TW : lane);
+        const int tok = (p.tile + i) * kTile + 32 * u + lane;
         if (!more || tok < p.sp.lo || tok >= p.sp.len) continue;
         const uint32_t idx = a.c.page_size > 1 ? __umulhi((uint32_t)tok, a.ps_mul) >> a.ps_shift : tok;
         const int in = tok - (int)(idx * (uint32_t)a.c.page_size);
@@ -309,88 +322,67 @@ k_draft_attention(const DraftArgs a) {
       }
     };
     settle();
-    Tok tk[LL];
+    Tok tk[2];
     look_up(tk);
     for (int round = 0; more; ++round) {
-      // the tokens' addresses are handed out before the next tile's are looked up
+      const int note = (round * ST + stage) % kNotes;
+      const uint32_t there[2] = {__ballot_sync(kAll, tk[0].at >= 0), __ballot_sync(kAll, tk[1].at >= 0)};
       if (E4M3) {
         // codes to registers, and as bf16 into the stage once it is free
-        constexpr int LPR = DK / 16;            // lanes (16-byte chunks) per token row
-        constexpr int NI = TW * LPR / 32;       // loads per lane and matrix
-        uint4 kc[NI], vc[NI];
-        float ks[LL], vs[LL];
+        constexpr int LPR = DK / 16;          // lanes (16-byte chunks) per token row
+        constexpr int NI = kTile * LPR / 32;  // loads per lane
+        const uint8_t* const src = static_cast<const uint8_t*>(piece ? a.c.v : a.c.k);
+        const float* const scales = piece ? a.c.v_scale : a.c.k_scale;
+        uint4 codes[NI];
+        float sc[2];
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
           const int r = n * (32 / LPR) + lane / LPR;
           const long long o = __shfl_sync(kAll, tk[n * (32 / LPR) / 32].at, r & 31);
-          kc[n] = vc[n] = make_uint4(0, 0, 0, 0);
-          if (o >= 0) {
-            kc[n] = ldg_stream16(static_cast<const uint8_t*>(a.c.k) + o + (lane % LPR) * 16);
-            vc[n] = ldg_stream16(static_cast<const uint8_t*>(a.c.v) + o + (lane % LPR) * 16);
-          }
+          codes[n] = make_uint4(0, 0, 0, 0);
+          if (o >= 0) codes[n] = ldg_stream16(src + o + (lane % LPR) * 16);
         }
-        uint32_t there[LL];
 #pragma unroll
-        for (int u = 0; u < LL; ++u) {
-          const bool real = tk[u].at >= 0;
-          there[u] = __ballot_sync(kAll, real);
-          ks[u] = real ? __ldg(a.c.k_scale + tk[u].sat) : 0.f;
-          vs[u] = real ? __ldg(a.c.v_scale + tk[u].sat) : 0.f;
-        }
+        for (int u = 0; u < 2; ++u) sc[u] = tk[u].at >= 0 ? __ldg(scales + tk[u].sat) : 0.f;
         i += ST;
         settle();
         look_up(tk);
-        if (round > 0) role_wait(dead, &sh.empty[stage], (uint32_t)((round - 1) & 1), a.status);
+        if (round > 0) role_wait(dead, empty, (uint32_t)((round - 1) & 1), a.status);
+        uint8_t* const to = dst + (piece ? S::kVOff : 0) + ((lane % LPR) >> 2) * kChunk;
+        const int j = 2 * (lane & 3);
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
-          const int r = gw * TW + n * (32 / LPR) + lane / LPR, ch = lane % LPR;
-          uint8_t* k = dst + (ch >> 2) * kChunk;
-          uint8_t* v = k + S::kVOff;
-          const int j = 2 * (ch & 3);
-          *reinterpret_cast<uint4*>(k + tc::sw128_off(r, j)) = e4m3x8_to_bf16(kc[n].x, kc[n].y);
-          *reinterpret_cast<uint4*>(k + tc::sw128_off(r, j + 1)) = e4m3x8_to_bf16(kc[n].z, kc[n].w);
-          *reinterpret_cast<uint4*>(v + tc::sw128_off(r, j)) = e4m3x8_to_bf16(vc[n].x, vc[n].y);
-          *reinterpret_cast<uint4*>(v + tc::sw128_off(r, j + 1)) = e4m3x8_to_bf16(vc[n].z, vc[n].w);
+          const int r = n * (32 / LPR) + lane / LPR;
+          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, j)) = e4m3x8_to_bf16(codes[n].x, codes[n].y);
+          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, j + 1)) = e4m3x8_to_bf16(codes[n].z, codes[n].w);
         }
-#pragma unroll
-        for (int u = 0; u < LL; ++u) {
-          if (TW >= 32 || lane < TW) {
-            sh.scale[stage][0][gw * TW + 32 * u + lane] = ks[u];
-            sh.scale[stage][1][gw * TW + 32 * u + lane] = vs[u];
-          }
-          if (lane == 0) {
-            if (TW < 32)
-              reinterpret_cast<uint16_t*>(sh.exists[stage])[gw] = (uint16_t)there[u];
-            else
-              sh.exists[stage][gw * LL + u] = there[u];
-          }
-        }
+        sh.scale[note][piece][lane] = sc[0];
+        sh.scale[note][piece][32 + lane] = sc[1];
       } else {
-        if (round > 0) role_wait(dead, &sh.empty[stage], (uint32_t)((round - 1) & 1), a.status);
-#pragma unroll
-        for (int u = 0; u < LL; ++u) {
-          const uint32_t there = __ballot_sync(kAll, tk[u].at >= 0);
-          if (lane == 0) {
-            if (TW < 32)
-              reinterpret_cast<uint16_t*>(sh.exists[stage])[gw] = (uint16_t)there;
-            else
-              sh.exists[stage][gw * LL + u] = there;
-          }
+        if (round > 0) role_wait(dead, empty, (uint32_t)((round - 1) & 1), a.status);
+        // this lane's 16-byte chunk of the 128-byte rows of the piece's chunks
+        const int j = lane & 7;
+        const uint16_t* src = static_cast<const uint16_t*>(a.c.k) + 8 * j;
+        uint8_t* to = dst;
+        if (LATENT) {
+          src += 128 * piece;
+          to += 2 * piece * kChunk;
+        } else if (piece) {
+          src = static_cast<const uint16_t*>(a.c.v) + 8 * j;
+          to += S::kVOff;
         }
-        const int j = lane & 7;  // this lane's 16-byte chunk of a 128-byte row
-#pragma unroll
-        for (int r4 = 0; r4 < TW; r4 += 4) {
-          const int rl = r4 + (lane >> 3), r = gw * TW + rl;
-          const long long o = __shfl_sync(kAll, tk[r4 / 32].at, rl & 31);
+        constexpr int kOwn = LATENT ? 2 : S::kKChunks;
+#pragma unroll 4
+        for (int r4 = 0; r4 < kTile; r4 += 4) {
+          const int r = r4 + (lane >> 3);
+          const long long o = __shfl_sync(kAll, r4 < 32 ? tk[0].at : tk[1].at, r & 31);
           const bool ok = o >= 0;
-          const uint16_t* k = static_cast<const uint16_t*>(a.c.k) + (ok ? o : 0) + 8 * j;
-          const uint16_t* v = static_cast<const uint16_t*>(a.c.v) + (ok ? o : 0) + 8 * j;
-          uint8_t* to = dst + tc::sw128_off(r, j);
+          const uint16_t* x = src + (ok ? o : 0);
+          const uint32_t at = tc::sw128_off(r, j);
 #pragma unroll
-          for (int c = 0; c < S::kKChunks; ++c) tc::cp_async16_zfill(to + c * kChunk, k + 64 * c, ok);
-#pragma unroll
-          for (int c = 0; c < S::kVChunks; ++c)
-            tc::cp_async16_zfill(to + S::kVOff + c * kChunk, v + 64 * c, ok);
+          for (int c = 0; c < kOwn; ++c) tc::cp_async16_zfill(to + c * kChunk + at, x + 64 * c, ok);
+          if (LATENT && piece == 0)
+            tc::cp_async16_zfill(to + (S::kKChunks - 1) * kChunk + at, x + DV, ok);
         }
         cp_async_commit();
         i += ST;
@@ -398,81 +390,113 @@ k_draft_attention(const DraftArgs a) {
         look_up(tk);
         cp_async_wait<0>();
       }
+      if (piece == 0 && lane < 2) sh.exists[note][lane] = there[lane];
       tc::fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.full[stage]);
+      if (lane == 0) mbar_arrive(full);
     }
     cp_async_wait<0>();
-  } else if (warp == kSoftWarps) {
-    // ---- the products: S = Q K^T (rows x tokens) of one tile ahead of O^T +=
-    // V^T P^T (dimensions x rows)
-    const uint32_t q0 = smem_u32(sm_q), p0 = smem_u32(sm_p), kv0 = smem_u32(sm_kv);
-    constexpr uint32_t idesc_s = idesc_bf16(kRows, kTile, false, false);
-    const uint32_t idesc_o = idesc_bf16(DV >= 128 ? 128 : 64, npad, true, false);
-    int j = 0, parts = 0;
-    auto values = [&](int t) {  // the products with tile t's values
-      role_wait(dead, &sh.p_full, (uint32_t)(t & 1), a.status);
-      tc::fence_after_sync();
-      if (tc::elect_one() && !*dead) {
-        const uint32_t v = kv0 + (t % ST) * S::kStage + S::kVOff;
-        const uint32_t add = sh.add_to;
-#pragma unroll
-        for (int mb = 0; mb < S::kBlocks; ++mb)
-#pragma unroll
-          for (int y = 0; y < S::kParts; ++y)
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              tc::mma_f16(tmem + kOCol + mb * kRows,
-                          sw128_desc_mn(v + 2 * mb * kChunk + kk * 2048, kChunk),
-                          tc::sw128_desc(p0 + y * kChunk + kk * 32), idesc_o, add | (y | kk ? 1u : 0u));
-        tc::commit(&sh.empty[t % ST]);
-        tc::commit(&sh.pv_done);
-      }
-      __syncwarp();
-    };
+  } else if (warp == kSoft) {
+    // ---- scores: S = Q K^T (rows x tokens), up to two tiles ahead of the softmax
+    const uint32_t q0 = desc_k(smem_u32(sm_q)), kv0 = desc_k(smem_u32(sm_kv));
+    constexpr uint32_t idesc = idesc_bf16(kRows, kTile, false, false);
+    constexpr int kKeys = LATENT ? NP : 1;  // pieces with keys
     Part p;
+    int j = 0, parts = 0;
     while (walk.next_tiles(a, p)) {
       role_wait(dead, &sh.q_full, (uint32_t)(parts & 1), a.status);
-      for (int i = 0; i < p.n; ++i, ++j) {
-        role_wait(dead, &sh.full[j % ST], (uint32_t)((j / ST) & 1), a.status);
-        if (j >= 2) role_wait(dead, &sh.s_empty[j & 1], (uint32_t)((j / 2 - 1) & 1), a.status);
-        tc::fence_after_sync();
-        if (tc::elect_one() && !*dead) {
-          const uint32_t k = kv0 + (j % ST) * S::kStage;
-#pragma unroll
-          for (int c = 0; c < S::kKChunks; ++c)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_f16(tmem + (j & 1) * kTile, tc::sw128_desc(q0 + c * kChunk + kk * 32),
-                          tc::sw128_desc(k + c * kChunk + kk * 32), idesc_s, c | kk ? 1u : 0u);
-          tc::commit(&sh.s_full[j & 1]);
-        }
-        __syncwarp();
-        if (i > 0) values(j - 1);
-      }
-      values(j - 1);
       ++parts;
+      for (int i = 0; i < p.n; ++i, ++j) {
+        if (j >= 2) role_wait(dead, &sh.s_empty[j & 1], (uint32_t)((j / 2 - 1) & 1), a.status);
+        const uint32_t st = uniform(j % ST), buf = uniform(j & 1);
+#pragma unroll
+        for (int x = 0; x < kKeys; ++x) {
+          role_wait(dead, &sh.full[st][x], (uint32_t)((j / ST) & 1), a.status);
+          tc::fence_after_sync();
+          if (tc::elect_one() && !*dead) {
+            const uint32_t k = kv0 + st * (S::kStage / 16), d = tmem + buf * kTile;
+            auto chunk = [&](int c, uint32_t add) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss(d, q0 + c * (kChunk / 16) + 2 * kk, k + c * (kChunk / 16) + 2 * kk, idesc, kk ? 1u : add);
+            };
+            if (LATENT) {
+              chunk(2 * x, x);
+              chunk(2 * x + 1, 1);
+              if (x == 0) chunk(S::kKChunks - 1, 1);
+            } else {
+#pragma unroll
+              for (int c = 0; c < S::kKChunks; ++c) chunk(c, c);
+              tc::commit(&sh.empty[st][0]);
+            }
+            if (x == kKeys - 1) tc::commit(&sh.s_full[buf]);
+          }
+          __syncwarp();
+        }
+      }
     }
     // every product has been made before the CTA's memory goes
+    if (j > 0 && lane == 0) mbar_wait(&sh.s_full[(j - 1) & 1], (uint32_t)(((j - 1) / 2) & 1));
+    __syncwarp();
+  } else if (warp == kSoft + 1) {
+    // ---- outputs: O^T += V^T P^T (dimensions x rows).  A warp of their own: a
+    // warp's MMAs wait for its own checks, not for the other's.
+    const uint32_t p0 = desc_k(smem_u32(sm_p)), v0 = desc_mn(smem_u32(sm_kv) + S::kVOff, kChunk);
+    const uint32_t idesc = idesc_bf16(DV >= 128 ? 128 : 64, npad, true, false);
+    Part p;
+    int j = 0;
+    while (walk.next_tiles(a, p))
+      for (int i = 0; i < p.n; ++i, ++j) {
+        const uint32_t st = uniform(j % ST);
+        if (!LATENT) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / ST) & 1), a.status);
+        role_wait(dead, &sh.p_full, (uint32_t)(j & 1), a.status);
+        tc::fence_after_sync();
+        if (tc::elect_one() && !*dead) {
+          const uint32_t v = v0 + st * (S::kStage / 16);
+#pragma unroll
+          for (int mb = 0; mb < S::kBlocks; ++mb) {
+#pragma unroll
+            for (int y = 0; y < S::kParts; ++y)
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                mma_ss(tmem + kOCol + mb * kRows, v + (2 * mb * kChunk + kk * 2048) / 16,
+                       p0 + (y * kChunk + kk * 32) / 16, idesc, 1u);
+            if (LATENT) tc::commit(&sh.empty[st][mb]);
+          }
+          if (!LATENT) tc::commit(&sh.empty[st][NP - 1]);
+          tc::commit(&sh.pv_done);
+        }
+        __syncwarp();
+      }
     if (j > 0 && lane == 0) mbar_wait(&sh.pv_done, (uint32_t)((j - 1) & 1));
     __syncwarp();
   } else {
-    // ---- softmax.  A thread holds 16 tokens of rows ra and ra + 8, a quad of
-    // lanes a row.
-    const int g = lane >> 2, c = lane & 3, ra = 16 * warp + g;
-    const uint32_t quadrant = tmem + ((uint32_t)(32 * warp) << 16);
+    // ---- softmax.  A thread holds 8 kBlk tokens of rows ra and ra + 8, a quad
+    // of lanes (times kSplit warps) a row.
+    constexpr int kMine = kTile / S::kSplit, kBlk = kMine / 8;  // tokens of a warp, in blocks of 8
+    const int g = lane >> 2, c = lane & 3, quad = warp & 3, half = warp >> 2, ra = 16 * quad + g;
+    const int c0 = half * kMine;  // the warp's first token
+    const uint32_t quadrant = tmem + ((uint32_t)(32 * quad) << 16);
     const float scale2 = a.d.scale * kLog2e;
     Walk ahead = walk;
     Part p;
     auto load_q = [&](const Part& x) {
-      for (int e = tid; e < kRows * (DK / 8); e += kSoftWarps * 32) {
-        const int r = e / (DK / 8), ch = e % (DK / 8), R = row0 + r;
-        const int n = R / a.G, h = R - n * a.G;
-        const bool real = r < rows;
-        const uint16_t* src =
-            a.q + (real ? x.b * a.d.q_stride + n * a.d.q_row_stride + (long long)(x.hkv * a.G + h) * DK + 8 * ch
-                        : 0);
-        tc::cp_async16_zfill(sm_q + (ch >> 3) * kChunk + tc::sw128_off(r, ch & 7), src, real);
+      // a warp: kRows / kSoft rows, four at a time, eight lanes to a row
+      constexpr int kOwn = kRows / kSoft;
+      const int R = row0 + warp * kOwn + (lane & (kOwn - 1)), n = R / a.G;
+      const long long mine = warp * kOwn + (lane & (kOwn - 1)) < rows
+                                 ? x.b * a.d.q_stride + n * a.d.q_row_stride + (long long)(x.hkv * a.G + R - n * a.G) * DK
+                                 : -1;
+      const int j = lane & 7;
+#pragma unroll
+      for (int r4 = 0; r4 < kOwn; r4 += 4) {
+        const int r = r4 + (lane >> 3);
+        const long long o = __shfl_sync(kAll, mine, r);
+        const bool ok = o >= 0;
+        const uint16_t* src = a.q + (ok ? o : 0) + 8 * j;
+        uint8_t* to = sm_q + tc::sw128_off(warp * kOwn + r, j);
+#pragma unroll
+        for (int k = 0; k < S::kKChunks; ++k) tc::cp_async16_zfill(to + k * kChunk, src + 64 * k, ok);
       }
       cp_async_commit();
     };
@@ -480,7 +504,8 @@ k_draft_attention(const DraftArgs a) {
     if (more) load_q(p);
     int j = 0;
     while (walk.next(a, p)) {
-      if (rt == 0 && tid == 0 && p.parts) a.info[p.b * a.c.Hkv + p.hkv] = make_int2(2 * (walk.first / walk.share) + (p.slot & 1), p.parts);
+      if (rt == 0 && tid == 0 && p.parts)
+        a.info[p.b * a.c.Hkv + p.hkv] = make_int2(2 * (walk.first / walk.share) + (p.slot & 1), p.parts);
       const size_t slot = (size_t)max(p.slot, 0) * a.gtiles + rt;
       float* const part_ml = a.part_ml + slot * 2 * kRows;
       if (p.n == 0) {  // (a part of fewer units than a tile)
@@ -510,19 +535,16 @@ k_draft_attention(const DraftArgs a) {
           low[x] = a.d.window > 0 ? p.sp.ctx + max(1, __popcll(tree[x])) - a.d.window : 0;
         }
       }
-      if (tid < kRows) {
-        const int R = row0 + tid, n = R / a.G;
-        sh.at[tid] = tid < rows ? p.b * a.d.out_stride + n * a.d.out_row_stride +
-                                      (long long)(p.hkv * a.G + R - n * a.G) * DV
-                                : -1;
-      }
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       for (int i = 0; i < p.n; ++i, ++j) {
         const int st = j % ST, t0 = (p.tile + i) * kTile;
         role_wait(dead, &sh.s_full[j & 1], (uint32_t)((j / 2) & 1), a.status);
         tc::fence_after_sync();
-        uint32_t raw[32];
-        ld_16x256b_x8(quadrant + (j & 1) * kTile, raw);
+        uint32_t raw[4 * kBlk];
+        if constexpr (kBlk == 8)
+          ld_16x256b_x8(quadrant + (j & 1) * kTile + c0, raw);
+        else
+          ld_16x256b_x4(quadrant + (j & 1) * kTile + c0, raw);
         tc::wait_ld();
         tc::fence_before_sync();
         __syncwarp();
@@ -532,17 +554,18 @@ k_draft_attention(const DraftArgs a) {
           more = ahead.next_tiles(a, x);
           if (more) load_q(x);
         }
-        const uint64_t exists = (uint64_t)sh.exists[st][1] << 32 | sh.exists[st][0];
+        const int note = j % kNotes;
+        const uint64_t exists = (uint64_t)sh.exists[note][1] << 32 | sh.exists[note][0];
         // a tile that some rows see more of than others
         const bool mixed = t0 + kTile > p.sp.ctx ||
                            (a.d.window > 0 && t0 < p.sp.ctx + drafts - a.d.window);
-        float s[32];
+        float s[4 * kBlk];
 #pragma unroll
-        for (int u = 0; u < 32; ++u) s[u] = __uint_as_float(raw[u]) * scale2;
+        for (int u = 0; u < 4 * kBlk; ++u) s[u] = __uint_as_float(raw[u]) * scale2;
         if (E4M3) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float2 f = *reinterpret_cast<const float2*>(&sh.scale[st][0][8 * u + 2 * c]);
+          for (int u = 0; u < kBlk; ++u) {
+            const float2 f = *reinterpret_cast<const float2*>(&sh.scale[note][0][c0 + 8 * u + 2 * c]);
             s[4 * u] *= f.x;
             s[4 * u + 1] *= f.y;
             s[4 * u + 2] *= f.x;
@@ -556,10 +579,10 @@ k_draft_attention(const DraftArgs a) {
             const int sft = p.sp.ctx - t0;
             if (sft > -64 && sft < 64) seen |= sft >= 0 ? tree[x] << sft : tree[x] >> -sft;
             seen &= exists;
-            if (c == 0) sh.seen[ra + 8 * x] = seen;
-            const uint64_t mine = seen >> (2 * c);
+            if (c == 0 && half == 0) sh.seen[ra + 8 * x] = seen;
+            const uint64_t mine = seen >> (c0 + 2 * c);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < kBlk; ++u) {
               if (!(mine >> (8 * u) & 1)) s[4 * u + 2 * x] = -INFINITY;
               if (!(mine >> (8 * u + 1) & 1)) s[4 * u + 2 * x + 1] = -INFINITY;
             }
@@ -567,30 +590,42 @@ k_draft_attention(const DraftArgs a) {
         }
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < kBlk; ++u)
 #pragma unroll
           for (int x = 0; x < 2; ++x) mx[x] = fmaxf(mx[x], fmaxf(s[4 * u + 2 * x], s[4 * u + 2 * x + 1]));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           mx[x] = fmaxf(mx[x], __shfl_xor_sync(kAll, mx[x], 1));
           mx[x] = fmaxf(mx[x], __shfl_xor_sync(kAll, mx[x], 2));
+          if (S::kSplit > 1 && c == 0) sh.top[half][ra + 8 * x] = mx[x];
         }
         // (-inf + slack is -inf: a row's first score moves its maximum)
-        const bool moved = bar_any(1, kSoftWarps * 32, mx[0] > m[0] + kMaxSlack || mx[1] > m[1] + kMaxSlack);
+        const bool moved = bar_any(1, kSoftThreads, mx[0] > m[0] + kMaxSlack || mx[1] > m[1] + kMaxSlack);
         if (j > 0) role_wait(dead, &sh.pv_done, (uint32_t)((j - 1) & 1), a.status);
         tc::fence_after_sync();
+        if (i == 0) {  // the products are added to zeros
+          const uint32_t zero[16] = {};
+#pragma unroll 1
+          for (int mb = half; mb < S::kBlocks; mb += S::kSplit)
+#pragma unroll 1
+            for (int r0 = 0; r0 < npad; r0 += 16) st_32x32b_x16(quadrant + kOCol + mb * kRows + r0, zero);
+          tc::wait_st();
+        }
         if (moved) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
+            if (S::kSplit > 1) mx[x] = fmaxf(mx[x], sh.top[half ^ 1][ra + 8 * x]);
             const float mn = fmaxf(m[x], mx[x]);
             const float f = m[x] == mn ? 1.f : exp2_fast(m[x] - mn);
             l[x] *= f;
             m[x] = mn;
-            if (c == 0) sh.factor[ra + 8 * x] = f;
+            if (c == 0 && half == 0) sh.factor[ra + 8 * x] = f;
           }
+          named_bar(1, kSoftThreads);  // (before the halves' tops are written again, too)
           if (i > 0) {
-            named_bar(1, kSoftWarps * 32);
-            for (int mb = 0; mb < S::kBlocks; ++mb)
+#pragma unroll 1
+            for (int mb = half; mb < S::kBlocks; mb += S::kSplit)
+#pragma unroll 1
               for (int r0 = 0; r0 < npad; r0 += 16) {
                 uint32_t o[16];
                 const uint32_t at = quadrant + kOCol + mb * kRows + r0;
@@ -606,15 +641,17 @@ k_draft_attention(const DraftArgs a) {
         }
         const float ms[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
         // weights, as the second product's operand: row, then token
-        bool add_to = i > 0;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kBlk; ++u) {
           float2 vs = make_float2(1.f, 1.f);
-          if (E4M3) vs = *reinterpret_cast<const float2*>(&sh.scale[st][1][8 * u + 2 * c]);
+          if (E4M3) {
+            if (u == 0 && !*dead) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / ST) & 1), a.status);
+            vs = *reinterpret_cast<const float2*>(&sh.scale[note][1][c0 + 8 * u + 2 * c]);
+          }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             float w0 = exp2_fast(s[4 * u + 2 * x] - ms[x]), w1 = exp2_fast(s[4 * u + 2 * x + 1] - ms[x]);
-            uint8_t* to = sm_p + tc::sw128_off(ra + 8 * x, u) + 4 * c;
+            uint8_t* to = sm_p + tc::sw128_off(ra + 8 * x, c0 / 8 + u) + 4 * c;
             if (S::kParts == 1) {
               const uint32_t w = pack_bf16x2(w0, w1);
               l[x] += bf16_lo(w) + bf16_hi(w);
@@ -635,28 +672,31 @@ k_draft_attention(const DraftArgs a) {
           // A value that is not finite reaches the rows that see its token and no
           // other: it is added to their outputs, and the tile holds 0 in its place
           // (times a weight of 0 it would be NaN).
+          if (!LATENT) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / ST) & 1), a.status);
           uint8_t* const v = sm_kv + st * S::kStage + S::kVOff;
           bool odd = false;
-          for (int e = tid; e < kTile * (DV / 8); e += kSoftWarps * 32) {
+          for (int e = tid; e < kTile * (DV / 8); e += kSoftThreads) {
             const uint4 w = *reinterpret_cast<const uint4*>(v + e * 16);
             odd |= bf16x2_nonfinite(w.x) || bf16x2_nonfinite(w.y) || bf16x2_nonfinite(w.z) ||
                    bf16x2_nonfinite(w.w);
           }
-          if (bar_any(1, kSoftWarps * 32, odd)) {
-            for (int mb = 0; mb < S::kBlocks; ++mb) {
-              const int d = DV >= 128 ? mb * 128 + tid : 16 * warp + (lane & 15);
+          if (bar_any(1, kSoftThreads, odd)) {
+#pragma unroll 1
+            for (int mb = half; mb < S::kBlocks; mb += S::kSplit) {
+              const int d = DV >= 128 ? mb * 128 + 32 * quad + lane : 16 * quad + (lane & 15);
+#pragma unroll 1
               for (int r0 = 0; r0 < npad; r0 += 16) {
                 uint32_t o[16];
                 const uint32_t at = quadrant + kOCol + mb * kRows + r0;
                 ld_32x32b_x16(at, o);
                 tc::wait_ld();
+#pragma unroll 1
                 for (int t = 0; t < kTile; ++t) {
                   const uint32_t w = *reinterpret_cast<const uint16_t*>(
                       v + (d >> 6) * kChunk + tc::sw128_off(t, (d >> 3) & 7) + 2 * (d & 7));
                   const bool bad = (w & 0x7F80u) == 0x7F80u;
 #pragma unroll
                   for (int u = 0; u < 16; ++u) {
-                    if (i == 0 && t == 0) o[u] = 0u;
                     if (bad && (sh.seen[r0 + u] >> t & 1))
                       o[u] = __float_as_uint(__uint_as_float(o[u]) + __uint_as_float(w << 16));
                   }
@@ -665,45 +705,54 @@ k_draft_attention(const DraftArgs a) {
               }
             }
             tc::wait_st();
-            named_bar(1, kSoftWarps * 32);  // every thread has read the values
-            for (int e = tid; e < kTile * DV; e += kSoftWarps * 32) {
+            named_bar(1, kSoftThreads);  // every thread has read the values
+            for (int e = tid; e < kTile * DV; e += kSoftThreads) {
               uint16_t* w = reinterpret_cast<uint16_t*>(v) + e;
               if ((*w & 0x7F80u) == 0x7F80u) *w = 0;
             }
-            add_to = true;
           }
         }
-        if (tid == 0) sh.add_to = add_to;
         tc::fence_proxy_async();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full);
       }
       // ---- the part's results
+      if (tid < kRows) {
+        const int R = row0 + tid, n = R / a.G;
+        sh.at[tid] = tid < rows ? p.b * a.d.out_stride + n * a.d.out_row_stride +
+                                      (long long)(p.hkv * a.G + R - n * a.G) * DV
+                                : -1;
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         l[x] += __shfl_xor_sync(kAll, l[x], 1);
         l[x] += __shfl_xor_sync(kAll, l[x], 2);
-        if (low[x] == kNoRow) {  // (tiles that all rows see alike have been taken in)
-          m[x] = -INFINITY;
-          l[x] = 0.f;
-        }
-        if (c == 0) {
+        if (S::kSplit > 1 && c == 0 && half == 1) sh.factor[ra + 8 * x] = l[x];
+      }
+      if (S::kSplit > 1) named_bar(1, kSoftThreads);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (c == 0 && half == 0) {
           const int r = ra + 8 * x;
-          sh.inv[r] = l[x] == 0.f ? 0.f : 1.f / l[x];
+          if (S::kSplit > 1) l[x] += sh.factor[r];
+          // (a row that is none has taken in the tiles that all rows see alike)
+          const bool real = low[x] != kNoRow;
+          sh.inv[r] = l[x] == 0.f || !real ? 0.f : 1.f / l[x];
           if (p.slot >= 0) {
-            part_ml[r] = m[x];
-            part_ml[kRows + r] = l[x];
+            part_ml[r] = real ? m[x] : -INFINITY;
+            part_ml[kRows + r] = real ? l[x] : 0.f;
           }
         }
-      }
       role_wait(dead, &sh.pv_done, (uint32_t)((j - 1) & 1), a.status);
       tc::fence_after_sync();
-      named_bar(1, kSoftWarps * 32);
+      named_bar(1, kSoftThreads);
       float* const part_o = a.part_o + slot * kRows * DV;
       const bool lives = DV >= 128 || lane < 16;
-      for (int mb = 0; mb < S::kBlocks; ++mb) {
-        const int d = DV >= 128 ? mb * 128 + tid : 16 * warp + (lane & 15);
+#pragma unroll 1
+      for (int mb = half; mb < S::kBlocks; mb += S::kSplit) {
+        const int d = DV >= 128 ? mb * 128 + 32 * quad + lane : 16 * quad + (lane & 15);
+#pragma unroll 1
         for (int r0 = 0; r0 < npad; r0 += 16) {
           uint32_t o[16];
           ld_32x32b_x16(quadrant + kOCol + mb * kRows + r0, o);
@@ -730,12 +779,12 @@ k_draft_attention(const DraftArgs a) {
         }
       }
       tc::fence_before_sync();
-      named_bar(1, kSoftWarps * 32);  // the next part may write factors and places
+      named_bar(1, kSoftThreads);  // the next part may write factors and places
     }
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kSoftWarps) {
+  if (warp == kSoft) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, S::kTmem);
   }
@@ -745,7 +794,7 @@ k_draft_attention(const DraftArgs a) {
 // answers zeros for sequences without new tokens.
 template <int DV>
 __global__ void __launch_bounds__(kJoinThreads) k_draft_join(const DraftArgs a) {
-  constexpr int kLanes = DV / 4, kGroups = kJoinThreads / kLanes;  // threads per row; shares of the parts
+  constexpr int kLanes = DV / 4, kGroups = kJoinThreads / kLanes;  // threads per row; rows, or shares of the parts
   constexpr int kAhead = 8;
   __shared__ float4 s_acc[kGroups][kLanes];
   __shared__ float s_m[kGroups], s_l[kGroups];
@@ -754,23 +803,28 @@ __global__ void __launch_bounds__(kJoinThreads) k_draft_join(const DraftArgs a) 
   const int rt = blockIdx.x % a.gtiles, seg = blockIdx.x / a.gtiles, b = seg / a.c.Hkv, hkv = seg % a.c.Hkv;
   const int row0 = rt * kRows, rows = min(kRows, a.rows - row0);
   const int d4 = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+  int2 info = a.info[seg];  // (of no meaning for a sequence without new tokens)
   bool bad;
   const Span sp = span_of(a, b, &bad);
   if (bad && threadIdx.x == 0 && blockIdx.y == 0 && hkv == 0 && rt == 0) raise_status(a.status, MOE_DEV_BAD_PAGE);
-  const int2 info = sp.tiles ? a.info[seg] : make_int2(0, 0);
+  if (!sp.tiles) info = make_int2(0, 0);
   if (info.y == 1) return;  // its column has written it
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    const int R = row0 + r, n = R / a.G;
+  // as many threads for a row as it takes to have all of its parts on their way
+  int shares = 1;
+  while (shares < kGroups && shares * kAhead < info.y) shares *= 2;
+  const int at_once = kGroups / shares, mine = grp % shares;
+  for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
+    const int r = r0 + grp / shares, R = row0 + r, n = R / a.G;
     uint16_t* out = a.out + b * a.d.out_stride + n * a.d.out_row_stride +
                     (long long)(hkv * a.G + R - n * a.G) * DV + 4 * d4;
     if (info.y == 0) {
-      if (grp == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
+      if (r < rows) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
       continue;
     }
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int each = cdiv(info.y, kGroups), i1 = min(info.y, (grp + 1) * each);
-    for (int i0 = grp * each; i0 < i1; i0 += kAhead) {
+    const int each = cdiv(info.y, shares), i1 = r < rows ? min(info.y, (mine + 1) * each) : 0;
+    for (int i0 = mine * each; i0 < i1; i0 += kAhead) {
       float m[kAhead], l[kAhead];
       float4 v[kAhead];
       float M2 = M;
@@ -804,32 +858,36 @@ __global__ void __launch_bounds__(kJoinThreads) k_draft_join(const DraftArgs a) 
       }
       M = M2;
     }
-    s_acc[grp][d4] = acc;
-    if (d4 == 0) {
-      s_m[grp] = M;
-      s_l[grp] = L;
-    }
-    __syncthreads();
-    if (grp == 0) {
-      for (int x = 1; x < kGroups; ++x) M = fmaxf(M, s_m[x]);
-      const float Ms = M == -INFINITY ? 0.f : M;
-      L = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = 0; x < kGroups; ++x) {
-        if (s_m[x] == -INFINITY) continue;
-        const float f = exp2f(s_m[x] - Ms);
-        const float4 v = s_acc[x][d4];
-        L = fmaf(s_l[x], f, L);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
+    if (shares > 1) {
+      s_acc[grp][d4] = acc;
+      if (d4 == 0) {
+        s_m[grp] = M;
+        s_l[grp] = L;
       }
+      __syncthreads();
+      if (mine == 0) {
+        for (int x = 1; x < shares; ++x) M = fmaxf(M, s_m[grp + x]);
+        const float Ms = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < shares; ++x) {
+          if (s_m[grp + x] == -INFINITY) continue;
+          const float f = exp2f(s_m[grp + x] - Ms);
+          const float4 v = s_acc[grp + x][d4];
+          L = fmaf(s_l[grp + x], f, L);
+          acc.x = fmaf(v.x, f, acc.x);
+          acc.y = fmaf(v.y, f, acc.y);
+          acc.z = fmaf(v.z, f, acc.z);
+          acc.w = fmaf(v.w, f, acc.w);
+        }
+      }
+      __syncthreads();
+    }
+    if (mine == 0 && r < rows) {
       const float inv = L == 0.f ? 0.f : 1.f / L;
       *reinterpret_cast<uint2*>(out) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     }
-    __syncthreads();
   }
 }
 

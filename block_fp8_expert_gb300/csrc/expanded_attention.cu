@@ -22,7 +22,7 @@ constexpr int kQChunks = (kNope + kRope) / 64, kVChunks = kVd / 64;
 constexpr int kSlots = 8;           // of the ring of keys and values: 5 per tile
 constexpr int kPerTile = kQChunks + kVChunks;
 constexpr int kSoftWarps = 8;       // four per query tile
-constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr int kThreads = (kSoftWarps + 3) * 32;  // then a warp per query tile for its MMAs, one for the loads
 constexpr int kSmem = (2 * kQChunks + kSlots) * kSlot + 1024;
 constexpr int kOCol = 2 * kBlock;   // TMEM: the two tiles' scores (then weights), then their outputs
 
@@ -37,7 +37,7 @@ struct ExpandedArgs {
 };
 
 struct ExpandedShared {
-  uint64_t q_full[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], turn[2];
   uint32_t tmem_base;
   volatile int abort_flag;
   int add_to[2];  // the tile's products are added to what the outputs hold
@@ -68,12 +68,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
-  asm("{\n .reg .b64 A, B, R;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n mul.rn.f32x2 R, A, B;\n"
-      " mov.b64 {%0, %1}, R;\n}\n"
+  asm("{\n .reg .b64 A, B, C, R;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n mov.b64 C, {%6, %7};\n"
+      " fma.rn.f32x2 R, A, B, C;\n mov.b64 {%0, %1}, R;\n}\n"
       : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -104,13 +109,14 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], 2);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sh.q_full[x], 1);
       mbar_init(&sh.s_full[x], 1);
       mbar_init(&sh.p_full[x], kSoftWarps / 2);
       mbar_init(&sh.o_full[x], 1);
+      mbar_init(&sh.turn[x], 1);
     }
     sh.abort_flag = 0;
     fence_mbar_init();
@@ -170,9 +176,10 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   };
   const int nt[2] = {tiles_of(0), tiles_of(1)}, n = max(nt[0], nt[1]);
 
-  if (warp == kSoftWarps + 1) {
-    // ---- loads
-    if (tc::elect_one() && n > 0) {
+  if (warp == kSoftWarps + 2) {
+    // ---- loads, by one thread: queries, then a ring of keys and values
+    int i = 0;
+    if (tc::elect_one()) {
       for (int x = 0; x < 2; ++x)
         if (nt[x] > 0) {
           mbar_arrive_expect_tx(&sh.q_full[x], kQChunks * kSlot);
@@ -180,16 +187,14 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             tma_load_3d(smem + (x * kQChunks + c) * kSlot, &qmap, 64 * c, h, s.q0 + row0 + x * kBlock,
                         &sh.q_full[x]);
         }
-    }
-    __syncwarp();
-    int i = 0;
-    for (int j = 0; j < n; ++j)
-      for (int c = 0; c < kPerTile; ++c, ++i) {
-        const int slot = i % kSlots;
-        if (i >= kSlots) role_wait(dead, &sh.empty[slot], (uint32_t)((i / kSlots - 1) & 1), a.status);
-        if (tc::elect_one() && !*dead) {
+      for (int j = 0; j < n; ++j) {
+        const int t = s.k0 + j * kBlock;
+#pragma unroll
+        for (int c = 0; c < kPerTile; ++c) {
+          const int k = i + c, slot = k % kSlots;
+          if (k >= kSlots) lane_wait(dead, &sh.empty[slot], (uint32_t)((k / kSlots - 1) & 1), a.status);
+          if (*dead) break;
           mbar_arrive_expect_tx(&sh.full[slot], kSlot);
-          const int t = s.k0 + j * kBlock;
           if (c < 2)
             tma_load_3d(ring + slot * kSlot, &kmap, 64 * c, h, t, &sh.full[slot]);
           else if (c == 2)
@@ -197,8 +202,12 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           else
             tma_load_3d(ring + slot * kSlot, &vmap, 64 * (c - 3), h, t, &sh.full[slot]);
         }
-        __syncwarp();
+        if (*dead) break;
+        i += kPerTile;
       }
+    }
+    __syncwarp();
+    i = __reduce_max_sync(kAll, (unsigned)i);
     // every copy has landed and been read before the CTA's memory goes
     if (lane == 0)
       for (int k = max(0, i - kSlots); k < i; ++k) {
@@ -206,66 +215,66 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         if (!*dead) mbar_wait(&sh.empty[k % kSlots], (uint32_t)((k / kSlots) & 1));
       }
     __syncwarp();
-  } else if (warp == kSoftWarps) {
-    // ---- the products of both query tiles, taking turns: S = Q K^T of the next
-    // key tile follows O += P V of this one
-    const uint32_t q0 = smem_u32(smem), r0 = smem_u32(ring);
+  } else if (warp >= kSoftWarps) {
+    // ---- the products, a warp per query tile: O += P V of a key tile, then S = Q
+    // K^T of the next (which overwrites the weights P).  The warps take turns, so
+    // that one tile's products run while the other's softmax does, and each has
+    // made its checks before its turn comes: MMAs that wait for the checks of the
+    // warp that issues them leave the tensor cores idle for 500 cycles a time.
+    const int x = warp - kSoftWarps;
+    const uint32_t q0 = desc_k(smem_u32(smem) + x * kQChunks * kSlot), r0 = smem_u32(ring);
+    const uint32_t t_s = tmem + x * kBlock, t_o = tmem + kOCol + x * kVd;
     constexpr uint32_t idesc_s = idesc_bf16(kBlock, kBlock, false, false);
     constexpr uint32_t idesc_o = idesc_bf16(kBlock, 64, false, true);
-    auto wait_slot = [&](int i) {
-      role_wait(dead, &sh.full[i % kSlots], (uint32_t)((i / kSlots) & 1), a.status);
-    };
-    auto scores = [&](int x, int j) {  // of query tile x and key tile j
-      tc::fence_after_sync();
-      if (tc::elect_one() && !*dead) {
-#pragma unroll
-        for (int c = 0; c < kQChunks; ++c) {
-          const uint32_t k = r0 + ((j * kPerTile + c) % kSlots) * kSlot;
-          const uint32_t q = q0 + (x * kQChunks + c) * kSlot;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc::mma_f16(tmem + x * kBlock, tc::sw128_desc(q + kk * 32), tc::sw128_desc(k + kk * 32), idesc_s,
-                        c | kk ? 1u : 0u);
-        }
-        tc::commit(&sh.s_full[x]);
-      }
-      __syncwarp();
-    };
-    auto outputs = [&](int x, int j) {
-      role_wait(dead, &sh.p_full[x], (uint32_t)(j & 1), a.status);
-      tc::fence_after_sync();
-      if (tc::elect_one() && !*dead) {
-        const uint32_t add = sh.add_to[x];
-#pragma unroll
-        for (int c = 0; c < kVChunks; ++c) {
-          const uint32_t v = r0 + ((j * kPerTile + kQChunks + c) % kSlots) * kSlot;
-#pragma unroll
-          for (int kk = 0; kk < kBlock / 16; ++kk)
-            tc::mma_f16_ts(tmem + kOCol + x * kVd + 64 * c, tmem + x * kBlock + 8 * kk,
-                           sw128_desc_mn(v + kk * 2048, 0), idesc_o, add | (kk ? 1u : 0u));
-        }
-        if (j == nt[x] - 1) tc::commit(&sh.o_full[x]);
-      }
-      __syncwarp();
-    };
-    auto release = [&](int i0, int count) {
-      if (tc::elect_one() && !*dead)
-        for (int i = i0; i < i0 + count; ++i) tc::commit(&sh.empty[i % kSlots]);
-      __syncwarp();
-    };
-    for (int x = 0; x < 2; ++x)
-      if (nt[x] > 0) role_wait(dead, &sh.q_full[x], 0, a.status);
+    if (nt[x] > 0) role_wait(dead, &sh.q_full[x], 0, a.status);
     for (int j = -1; j < n; ++j) {
-      if (j >= 0)
-        for (int c = 0; c < kVChunks; ++c) wait_slot(j * kPerTile + kQChunks + c);
-      for (int x = 0; x < 2; ++x) {
-        if (j >= 0 && j < nt[x]) outputs(x, j);
-        if (j >= 0 && x == 1) release(j * kPerTile + kQChunks, kVChunks);
-        if (j + 1 < n && x == 0)
-          for (int c = 0; c < kQChunks; ++c) wait_slot((j + 1) * kPerTile + c);
-        if (j + 1 < nt[x]) scores(x, j + 1);
+      const uint32_t v0 = uniform((j * kPerTile + kQChunks) % kSlots);  // the values' first slot
+      const uint32_t k0 = uniform((j + 1) * kPerTile % kSlots);         // the next keys'
+      // (slots that it does not read are given back no sooner either)
+      if (j + 1 < n)
+        for (int i = (j + 1) * kPerTile; i < (j + 1) * kPerTile + kQChunks; ++i)
+          role_wait(dead, &sh.full[i % kSlots], (uint32_t)((i / kSlots) & 1), a.status);
+      if (j >= 0) {
+        for (int i = j * kPerTile + kQChunks; i < (j + 1) * kPerTile; ++i)
+          role_wait(dead, &sh.full[i % kSlots], (uint32_t)((i / kSlots) & 1), a.status);
+        if (j < nt[x]) role_wait(dead, &sh.p_full[x], (uint32_t)(j & 1), a.status);
       }
-      if (j + 1 < n) release((j + 1) * kPerTile, kQChunks);
+      const uint32_t add = uniform(sh.add_to[x]);
+      if (x == 1 || j >= 0) role_wait(dead, &sh.turn[x], (uint32_t)((j + x) & 1), a.status);
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
+        if (!*dead) {
+          if (j >= 0) {
+            if (j < nt[x]) {
+#pragma unroll
+              for (int c = 0; c < kVChunks; ++c) {
+                const uint32_t v = desc_mn(r0 + (v0 + c) % kSlots * kSlot, 0);
+#pragma unroll
+                for (int kk = 0; kk < kBlock / 16; ++kk)
+                  mma_ts(t_o + 64 * c, t_s + 8 * kk, v + kk * 128, idesc_o, add | (kk ? 1u : 0u));
+              }
+              if (j == nt[x] - 1) tc::commit(&sh.o_full[x]);
+            }
+#pragma unroll
+            for (int c = 0; c < kVChunks; ++c) tc::commit(&sh.empty[(v0 + c) % kSlots]);
+          }
+          if (j + 1 < n) {
+            if (j + 1 < nt[x]) {
+#pragma unroll
+              for (int c = 0; c < kQChunks; ++c) {
+                const uint32_t k = desc_k(r0 + (k0 + c) % kSlots * kSlot), q = q0 + c * (kSlot / 16);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) mma_ss(t_s, q + 2 * kk, k + 2 * kk, idesc_s, c | kk ? 1u : 0u);
+              }
+              tc::commit(&sh.s_full[x]);
+            }
+#pragma unroll
+            for (int c = 0; c < kQChunks; ++c) tc::commit(&sh.empty[(k0 + c) % kSlots]);
+          }
+        }
+        mbar_arrive(&sh.turn[x ^ 1]);
+      }
+      __syncwarp();
     }
   } else {
     // ---- softmax.  A thread owns a row.
@@ -290,8 +299,7 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         tc::wait_ld();
 #pragma unroll
         for (int c = 0; c < kBlock / 2; ++c)
-          v[c] = mul2(make_float2(__uint_as_float(raw[c / 16][2 * c % 32]), __uint_as_float(raw[c / 16][2 * c % 32 + 1])),
-                      make_float2(a.scale2, a.scale2));
+          v[c] = make_float2(__uint_as_float(raw[c / 16][2 * c % 32]), __uint_as_float(raw[c / 16][2 * c % 32 + 1]));
         if (j >= whole) {
           const int left = limit - j * kBlock;
 #pragma unroll
@@ -302,8 +310,8 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kBlock / 2; ++c) mx[c & 3] = fmaxf(mx[c & 3], fmaxf(v[c].x, v[c].y));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int c = 0; c < kBlock / 2; ++c) mx[c & 3] = max3(mx[c & 3], v[c].x, v[c].y);
+        const float top = a.scale2 * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));  // (scale > 0)
         // (-inf + slack is -inf: a row's first score moves its maximum)
         if (__any_sync(kAll, top > m + kMaxSlack)) {
           const float mn = fmaxf(m, top);
@@ -330,7 +338,7 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           uint32_t w[32];
 #pragma unroll
           for (int u = 0; u < 32; ++u) {
-            const float2 e = add2(v[32 * c + u], make_float2(-ms, -ms));
+            const float2 e = fma2(v[32 * c + u], make_float2(a.scale2, a.scale2), make_float2(-ms, -ms));
             w[u] = pack_bf16x2(exp2_fast(e.x), exp2_fast(e.y));
             sum = add2(sum, make_float2(bf16_lo(w[u]), bf16_hi(w[u])));
           }

@@ -686,7 +686,7 @@ moe_status moe_latent_attention(const uint16_t* q, moe_latent_cache cache,
 
 /* One moe_expanded_attention call: B sequences of Tq query tokens and Tk key
  * tokens in all, H heads.  Strides in elements, multiples of 8: between tokens
- * and between heads, at least what they step over. */
+ * and between heads, at least what they step over.  scale > 0. */
 typedef struct {
   int32_t B, Tq, Tk, H;
   float scale;
