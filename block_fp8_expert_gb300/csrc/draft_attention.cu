@@ -22,38 +22,52 @@ constexpr int kRows = 64;      // rows (query head x new token) of a CTA at most
 constexpr int kChunk = 8192;   // 64 tokens or rows x 64 dimensions, 128-byte swizzled
 constexpr int kSegCost = 3;    // what a segment costs a CTA beside its tiles, in tiles
 constexpr int kNoRow = 0x7fffffff;
-constexpr int kMinUnits = 2;   // least share of a CTA
+constexpr int kMinTiles = 2;   // per part, where there are columns for smaller ones
 constexpr int kOCol = 2 * kTile;  // TMEM: two buffers of scores, then the outputs
 constexpr long long kMaxTokens = 0x7fffff80;  // of a sequence: its tiles' ends fit 31 bits
-constexpr int kJoinThreads = 512;
-// Tiles whose tokens' notes (which are there, their scales) are kept: keys may be
-// replaced two tiles before the softmax reads the notes.
-constexpr int kNotes = 4;
+// Tiles whose tokens' notes (which are there, their scales) are kept: the codes
+// of a tile may be on their way while the softmax reads the notes of the sixth
+// before it (two tiles of codes ahead of the stages, two stages, two scores).
+constexpr int kNotes = 8;
 
 // LATENT: the values are the leading DV dimensions of the keys.  A stage (64
 // tokens) consists of pieces that are loaded, waited for and given back one by
 // one: the keys and the values, or, of latent vectors, the 128 dimensions that
 // one block of the outputs reads (the first piece with the shared key part).
-template <int DK, int DV, bool LATENT, bool E4M3>
+// TMA: pages of 8, 16, 32 or a multiple of 64 tokens are copied as boxes, E4M3
+// codes into a ring of their own, from where warps take them to the stages as
+// bf16; other page sizes are gathered token by token.
+template <int DK, int DV, bool LATENT, bool E4M3, bool TMA>
 struct DraftShape {
+  static constexpr bool kRaw = E4M3 && TMA;
   static constexpr int kKChunks = DK / 64, kVChunks = LATENT ? 0 : DV / 64;
-  static constexpr int kStage = (kKChunks + kVChunks) * kChunk;
-  static constexpr int kVOff = LATENT ? 0 : kKChunks * kChunk;
   static constexpr int kParts = LATENT ? 1 : 2;  // bf16 parts of a softmax weight
   static constexpr int kQ = kKChunks * kChunk, kP = kParts * kChunk;
-  static constexpr int kCtas = kStage <= 32 * 1024 && !LATENT ? 2 : 1;  // per SM
+  static constexpr int kCtas = DK <= (kRaw ? 64 : 128) ? 2 : 1;  // per SM
   static constexpr int kBlocks = DV >= 128 ? DV / 128 : 1;  // of the outputs' dimensions
   static constexpr int kPieces = LATENT ? kBlocks : 2;
-  // barriers and small arrays, the stages' E4M3 scales, and the tiles' alignment
-  static constexpr int kFixed = 2048 + (E4M3 ? kNotes * 2 * kTile * 4 : 0) + 1024;
-  static constexpr int kFit = (227 * 1024 / kCtas - kFixed - kQ - kP) / kStage;
-  static constexpr int kStages = kFit >= 4 && LATENT ? 4 : 2;
-  static_assert(kFit >= 2, "shared memory");
+  // barriers and small arrays, the tiles' E4M3 scales, and the tiles' alignment
+  static constexpr int kFixed = 2048 + (E4M3 ? kNotes * 2 * kTile * 4 + 256 : 0) + 1024;
+  static constexpr int kRoom = 227 * 1024 / kCtas - kFixed - kQ - kP;
+  // tiles of keys and of values in shared memory, keys first
+  static constexpr int kStages = LATENT && kRoom / (kKChunks * kChunk) >= 4 ? 4 : 2;
+  static constexpr int kVStages = LATENT ? kStages : kRaw && kCtas == 2 ? 1 : kRoom / kChunk >= 4 * kKChunks ? 2 : 1;
+  static constexpr int kStage = kKChunks * kChunk, kVStage = LATENT ? kStage : kVChunks * kChunk;
+  static constexpr int kV = LATENT ? 0 : kStages * kStage;  // where the values begin
+  static constexpr int kStaged = kStages * kStage + (LATENT ? 0 : kVStages * kVStage);
+  // the ring of codes, each slot 64 tokens' keys or values
+  static constexpr int kSlot = kTile * DK;
+  static constexpr int kSlotsFit = (kRoom - kStaged) / kSlot;
+  static constexpr int kSlots = !kRaw ? 0 : kSlotsFit >= 4 ? 4 : kSlotsFit;
+  static_assert(kRoom >= kStaged && (!kRaw || kSlots >= 2), "shared memory");
   // softmax warps per 16 rows: they share the tile's tokens
-  static constexpr int kSplit = LATENT ? 2 : 1;
-  static constexpr int kSoft = 4 * kSplit;  // softmax warps; then two for MMAs; then one per piece
-  static constexpr int kWarps = kSoft + 2 + kStages * kPieces;
-  static constexpr int kSmem = kQ + kP + kStages * kStage + 1024;
+  static constexpr int kSplit = kCtas == 1 && (LATENT || kRaw) ? 2 : 1;
+  // softmax warps; then two for MMAs; then the loading warps: one for the boxes
+  // and those that convert, or one per piece and stage
+  static constexpr int kSoft = 4 * kSplit;
+  static constexpr int kConvert = kRaw ? 4 * kSplit : 0;
+  static constexpr int kWarps = kSoft + 2 + (TMA ? 1 + kConvert : kStages * kPieces);
+  static constexpr int kSmem = kQ + kP + kStaged + kSlots * kSlot + 1024;
   static constexpr int kCols = kOCol + kBlocks * kRows;
   static constexpr int kTmem = kCols <= 256 ? 256 : 512;
   static_assert(kTmem * kCtas <= 512, "TMEM");
@@ -69,6 +83,7 @@ struct DraftArgs {
   moe_draft_dims d;
   int G, rows, gtiles;  // query heads per key/value head; n G; CTAs that share them
   int cols;             // columns of the grid
+  int box, box_shift;  // tokens of a page that one copy takes (TMA), a power of two
   uint32_t ps_mul, ps_shift;  // t / page_size = umulhi(t, ps_mul) >> ps_shift (page_size > 1)
   uint16_t* out;
   float* part_o;   // [2 cols][gtiles][kRows][DV]
@@ -98,12 +113,15 @@ __device__ __forceinline__ Span span_of(const DraftArgs& a, int b, bool* bad = n
   return s;
 }
 
-// A sequence's tiles for one key/value head are a segment of tiles + kSegCost
-// units; sequences without new tokens have none.  All segments lie in one row,
-// sequence-major, then head; column c of the grid takes units [c share, (c + 1)
-// share) of it, and with them the same part of each segment's tiles.  The CTAs
-// of a column do so for different rows of queries: they read the same tiles at
-// about the same time, so HBM gives them once.
+// A sequence's tiles for one key/value head are a segment; sequences without new
+// tokens have none.  All segments lie in one row, sequence-major, then head.
+// Where there are columns of the grid enough, each takes one part of one segment
+// (share 0): the segments are cut into parts of at most `most` tiles, the least
+// of a few sizes with which the parts are no more than the columns.  Otherwise a
+// segment counts as tiles + kSegCost units, and column c takes units [c share,
+// (c + 1) share) of the row, and with them the same part of each segment's tiles.
+// The CTAs of a column do so for different rows of queries: they read the same
+// tiles at about the same time, so HBM gives them once.
 __device__ __forceinline__ int units_of(const Span& s) { return s.tiles ? s.tiles + kSegCost : 0; }
 // The tile at which unit u of a segment begins, in fp32: the columns on either
 // side get the same answer, and it never falls as u grows.
@@ -112,32 +130,56 @@ __device__ __forceinline__ int tile_at(const Span& s, int u) {
   return u <= 0 ? 0 : u >= units ? s.tiles : min(s.tiles, (int)(u * ((float)s.tiles / (float)units)));
 }
 
+// x / y, 0 <= x, 0 < y: a guess in fp32, put right (an integer division takes
+// several times as long, and several of them stand before the first load).
+__device__ __forceinline__ int quotient(int x, int y) {
+  int q = (int)__fdividef((float)x, (float)y);
+  while ((long long)q * y > x) --q;
+  while ((long long)(q + 1) * y <= x) ++q;
+  return q;
+}
+
 // What a column does, one segment's part after the other.
 struct Part {
   int b, hkv, tile, n;  // tiles [tile, tile + n), in tiles of the sequence
   int slot;             // of a part's results; -1: the whole segment
-  int parts;            // of the segment, if it begins here; else 0
+  int first, parts;     // whether the segment begins here, and then of how many parts it is
   Span sp;
 };
 struct Walk {
-  int b, before, cur, end, first, share;
+  int b, before, cur, end, first, share, col;
+  int part, parts;  // share 0: which part of the segment, of how many
   Span sp;
   __device__ __forceinline__ bool next(const DraftArgs& a, Part& p) {
     if (cur >= end) return false;
+    p.sp = sp;
+    p.b = b;
+    if (!share) {  // cur: the key/value head
+      p.hkv = cur++;
+      const int each = quotient(sp.tiles, parts), more = sp.tiles - each * parts;
+      const int i0 = part * each + min(part, more);  // the first `more` parts have a tile more
+      p.tile = sp.first + i0;
+      p.n = each + (part < more);
+      p.slot = parts == 1 ? -1 : 2 * col;
+      p.first = part == 0;
+      p.parts = parts;
+      return true;
+    }
     while (cur >= before + units_of(sp) * a.c.Hkv) {
       before += units_of(sp) * a.c.Hkv;
       sp = span_of(a, ++b);
     }
     const int units = units_of(sp);
-    p.hkv = (cur - before) / units;
+    p.sp = sp;
+    p.b = b;
+    p.hkv = a.c.Hkv == 1 ? 0 : quotient(cur - before, units);
     const int s0 = before + p.hkv * units, s1 = s0 + units, stop = min(s1, end);
     const int i0 = tile_at(sp, cur - s0), i1 = tile_at(sp, stop - s0);
-    p.b = b;
     p.tile = sp.first + i0;
     p.n = i1 - i0;
-    p.slot = cur == s0 && stop == s1 ? -1 : 2 * (cur / share) + (cur == first ? 0 : 1);
-    p.parts = cur == s0 ? (s1 - 1) / share - cur / share + 1 : 0;
-    p.sp = sp;
+    p.slot = cur == s0 && stop == s1 ? -1 : 2 * col + (cur == first ? 0 : 1);
+    p.first = cur == s0;
+    p.parts = p.slot < 0 || !p.first ? 1 : quotient(s1 - 1, share) - col + 1;
     cur = stop;
     return true;
   }
@@ -149,53 +191,131 @@ struct Walk {
   }
 };
 
+// Tiles per part to try, in eighths of an even share.
+constexpr int kTries = 6;
+__device__ __forceinline__ int most_of(int even, int i) {
+  const int eighths[kTries] = {8, 9, 10, 11, 13, 16};
+  return max(kMinTiles, (even * eighths[i] + 7) / 8);
+}
 // Every thread of the CTA calls this.
 template <int WARPS>
-__device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned* s_scan, Walk* s_walk) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned (*s_scan)[WARPS], Walk* s_walk) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Hkv = a.c.Hkv;
   const int per = cdiv(a.d.B, WARPS * 32), b0 = min(tid * per, a.d.B), b1 = min(b0 + per, a.d.B);
-  if (tid == 0) *s_walk = Walk{0, 0, 0, 0, 0, 1, Span{0, 0, 0, 0, 0}};
-  unsigned mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units_of(span_of(a, b));
-  unsigned incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned x = __shfl_up_sync(kAll, incl, o);
-    if (lane >= o) incl += x;
+  if (a.d.B == 1 && Hkv <= a.cols) {  // every thread on its own
+    Walk w{0, 0, 0, 0, 0, 0, col, 0, 1, span_of(a, 0)};
+    const int most = most_of(quotient(w.sp.tiles * Hkv + a.cols - 1, a.cols), 0);
+    w.parts = max(1, quotient(w.sp.tiles + most - 1, most));
+    w.cur = quotient(col, w.parts);
+    w.part = col - w.cur * w.parts;
+    w.end = w.sp.tiles ? min(w.cur + 1, Hkv) : 0;
+    return w;
   }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  unsigned before = incl - mine, total = 0;
+  if (tid == 0) *s_walk = Walk{0, 0, 0, 0, 0, 1, col, 0, 1, Span{0, 0, 0, 0, 0}};
+  // inclusive sums over the warp's lanes, and the warp's own sum
+  auto scan = [&](unsigned v, unsigned* to) {
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    const unsigned v = s_scan[w];
-    if (w < warp) before += v;
-    total += v;
-  }
-  total *= a.c.Hkv;
-  const unsigned share = max((unsigned)kMinUnits, (total + a.cols - 1) / a.cols);
-  const unsigned want = min((unsigned)col * share, total);
-  if (before * a.c.Hkv <= want && want < (before + mine) * a.c.Hkv) {
-    Walk w;
-    w.sp = Span{0, 0, 0, 0, 0};
-    for (w.b = b0; w.b < b1; ++w.b) {
-      w.sp = span_of(a, w.b);
-      const unsigned u = units_of(w.sp);
-      if (want < (before + u) * a.c.Hkv) break;
-      before += u;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned x = __shfl_up_sync(kAll, v, o);
+      if (lane >= o) v += x;
     }
-    w.before = (int)(before * a.c.Hkv);
-    w.cur = w.first = (int)want;
-    w.end = (int)min(want + share, total);
-    w.share = (int)share;
-    *s_walk = w;
+    if (lane == 31) to[warp] = v;
+    return v;
+  };
+  // the sum over the warps before this one, and over all
+  auto sums = [&](const unsigned* s, unsigned& before, unsigned& total) {
+    before = total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const unsigned v = s[w];
+      if (w < warp) before += v;
+      total += v;
+    }
+  };
+  Span span{0, 0, 0, 0, 0};  // of the last of this thread's sequences
+  unsigned tiles = 0, units = 0, before, total;
+  for (int b = b0; b < b1; ++b) {
+    span = span_of(a, b);
+    tiles += span.tiles;
+    units += units_of(span);
+  }
+  scan(tiles, s_scan[0]);
+  const unsigned u_incl = scan(units, s_scan[1]);
+  __syncthreads();
+  sums(s_scan[0], before, total);
+  // (tiles fit 31 bits: the host checks)
+  const int even = quotient((int)(total * Hkv) + a.cols - 1, a.cols);
+  unsigned mine[kTries] = {}, incl[kTries];
+  for (int b = b0; b < b1; ++b) {
+    if (per > 1) span = span_of(a, b);
+#pragma unroll
+    for (int i = 0; i < kTries; ++i) {
+      const int m = most_of(even, i);
+      mine[i] += quotient(span.tiles + m - 1, m);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kTries; ++i) incl[i] = scan(mine[i], s_scan[2 + i]);
+  __syncthreads();
+  int most = 0;
+  unsigned parts = 0;
+#pragma unroll
+  for (int i = kTries - 1; i >= 0; --i) {
+    unsigned x, y;
+    sums(s_scan[2 + i], x, y);
+    // (a share has two segments at most)
+    if (y * Hkv <= (unsigned)a.cols && (i == 0 || most_of(even, i) <= even + 2 * kSegCost)) {
+      most = most_of(even, i);
+      before = x + incl[i] - mine[i];
+      parts = mine[i];
+    }
+  }
+  Walk w;
+  w.col = col;
+  if (most) {
+    if (before * Hkv <= (unsigned)col && (unsigned)col < (before + parts) * Hkv) {
+      for (w.b = b0; w.b < b1; ++w.b) {
+        w.sp = per > 1 ? span_of(a, w.b) : span;
+        w.parts = quotient(w.sp.tiles + most - 1, most);
+        if ((unsigned)col < (before + w.parts) * Hkv) break;
+        before += w.parts;
+      }
+      const int k = col - (int)(before * Hkv);
+      w.cur = quotient(k, w.parts);
+      w.part = k - w.cur * w.parts;
+      w.end = w.cur + 1;
+      w.before = w.first = w.share = 0;
+      *s_walk = w;
+    }
+  } else {
+    sums(s_scan[1], before, total);
+    before += u_incl - units;
+    total *= Hkv;
+    const unsigned share = quotient((int)(total + a.cols - 1), a.cols);
+    const unsigned want = min((unsigned)col * share, total);
+    if (before * Hkv <= want && want < (before + units) * Hkv) {
+      for (w.b = b0; w.b < b1; ++w.b) {
+        w.sp = per > 1 ? span_of(a, w.b) : span;
+        const unsigned u = units_of(w.sp);
+        if (want < (before + u) * Hkv) break;
+        before += u;
+      }
+      w.before = (int)(before * Hkv);
+      w.cur = w.first = (int)want;
+      w.end = (int)min(want + share, total);
+      w.share = (int)share;
+      w.part = 0;
+      w.parts = 1;
+      *s_walk = w;
+    }
   }
   __syncthreads();
   return *s_walk;
 }
 
-template <int STAGES, int PIECES, int WARPS, bool E4M3>
+template <int STAGES, int PIECES, int SLOTS, int WARPS, bool E4M3>
 struct DraftShared {
+  uint64_t raw_full[SLOTS ? SLOTS : 1], raw_empty[SLOTS ? SLOTS : 1];
   uint64_t full[STAGES][PIECES], empty[STAGES][PIECES], s_full[2], s_empty[2], p_full, pv_done, q_full;
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -207,7 +327,7 @@ struct DraftShared {
     float inv[kRows];     // after the last tile: 1 / the row's sum
   };
   union {
-    unsigned scan[WARPS];
+    unsigned scan[2 + kTries][WARPS];
     uint64_t seen[kRows];  // tokens of the tile that a row sees
     long long at[kRows];   // after the last tile: the rows' outputs, in elements; -1: none
   };
@@ -233,14 +353,15 @@ __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t v) {
 
 }  // namespace
 
-template <int DK, int DV, bool LATENT, bool E4M3>
-__global__ void __launch_bounds__(DraftShape<DK, DV, LATENT, E4M3>::kWarps * 32,
-                                  DraftShape<DK, DV, LATENT, E4M3>::kCtas)
-k_draft_attention(const DraftArgs a) {
-  using S = DraftShape<DK, DV, LATENT, E4M3>;
-  constexpr int ST = S::kStages, NP = S::kPieces, kSoft = S::kSoft, kSoftThreads = kSoft * 32;
+template <int DK, int DV, bool LATENT, bool E4M3, bool TMA>
+__global__ void __launch_bounds__(DraftShape<DK, DV, LATENT, E4M3, TMA>::kWarps * 32,
+                                  DraftShape<DK, DV, LATENT, E4M3, TMA>::kCtas)
+k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const DraftArgs a) {
+  using S = DraftShape<DK, DV, LATENT, E4M3, TMA>;
+  constexpr int ST = S::kStages, VST = S::kVStages, NP = S::kPieces, kSoft = S::kSoft, kSoftThreads = kSoft * 32;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ DraftShared<ST, NP, S::kWarps, E4M3> sh;
+  __shared__ DraftShared<ST, NP, S::kSlots, S::kWarps, E4M3> sh;
   static_assert(sizeof(sh) + 1024 <= S::kFixed, "shared memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -248,12 +369,17 @@ k_draft_attention(const DraftArgs a) {
   uint8_t* const sm_q = smem;
   uint8_t* const sm_p = smem + S::kQ;
   uint8_t* const sm_kv = smem + S::kQ + S::kP;
+  uint8_t* const sm_raw = sm_kv + S::kStaged;
   if (tid == 0) {
     for (int i = 0; i < ST; ++i)
       for (int x = 0; x < NP; ++x) {
-        mbar_init(&sh.full[i][x], 1);
+        mbar_init(&sh.full[i][x], S::kRaw ? S::kConvert / 2 : 1);
         mbar_init(&sh.empty[i][x], 1);
       }
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&sh.raw_full[i], 1 + 32);  // the codes, and every lane's scales
+      mbar_init(&sh.raw_empty[i], S::kConvert / 2);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], kSoft);
@@ -263,6 +389,10 @@ k_draft_attention(const DraftArgs a) {
     mbar_init(&sh.q_full, kSoft);
     sh.abort_flag = 0;
     fence_mbar_init();
+  }
+  if (TMA && tid == 32) {
+    prefetch_map(&kmap);
+    if (!LATENT) prefetch_map(&vmap);
   }
   if (warp == kSoft) {
     tc::tmem_alloc(&sh.tmem_base, S::kTmem);
@@ -281,13 +411,152 @@ k_draft_attention(const DraftArgs a) {
   Walk walk = plan<S::kWarps>(a, col, sh.scan, &sh.walk);
   volatile int* const dead = &sh.abort_flag;
 
-  if (warp > kSoft + 1) {
-    // ---- loading: a warp per piece and stage, so that waiting for one piece's
-    // copies holds up no other
+  if (TMA && warp == kSoft + 2) {
+    // ---- loading: every lane one box of tokens (a page, or 64 tokens of it)
+    Part p{};
+    struct Box {
+      int in, page;  // -1: no token of the box is attended to
+    };
+    const int shift = a.box_shift, boxes = kTile >> shift;
+    // the page number of this lane's box, which nothing waits for yet
+    auto look_up = [&](int tile) {
+      Box x{0, -1};
+      const int t0 = tile * kTile + (lane << shift);
+      if (lane < boxes && t0 < p.sp.len && t0 + a.box > p.sp.lo) {
+        const uint32_t idx = a.c.page_size > 1 ? __umulhi((uint32_t)t0, a.ps_mul) >> a.ps_shift : t0;
+        x.in = t0 - (int)(idx * (uint32_t)a.c.page_size);
+        x.page = __ldg(a.block_table + (size_t)p.b * a.d.table_stride + idx);
+        if (x.page < 0) x.page = 0x7fffffff;
+      }
+      return x;
+    };
+    int j = 0;
+    while (walk.next_tiles(a, p)) {
+      // the tile's boxes, and those of the next two
+      Box x, x1 = look_up(p.tile), x2 = look_up(p.tile + 1);
+      for (int i = 0; i < p.n; ++i, ++j) {
+        x = x1;
+        x1 = x2;
+        x2 = look_up(p.tile + i + 2);
+        const int st = j % ST, note = j % kNotes;
+        uint64_t there = 0;  // the box's tokens, as the tile's
+        if (x.page >= 0) {
+          const int t0 = (p.tile + i) * kTile + (lane << shift);
+          if (x.page < a.c.pages)
+            there = (low_bits(min(a.box, p.sp.len - t0)) & ~low_bits(p.sp.lo - t0)) << (lane << shift);
+          else
+            raise_status(a.status, MOE_DEV_BAD_PAGE);
+        }
+        if ((uint32_t)x.page >= (uint32_t)a.c.pages) x.page = a.c.pages;  // which reads as zeros
+        const uint32_t there_lo = __reduce_or_sync(kAll, (uint32_t)there);
+        const uint32_t there_hi = __reduce_or_sync(kAll, (uint32_t)(there >> 32));
+#pragma unroll
+        for (int y = 0; y < NP; ++y) {
+          uint64_t* full = &sh.full[st][y];
+          if (S::kRaw) {
+            const int k = 2 * j + y, slot = k % (S::kSlots ? S::kSlots : 1);
+            full = &sh.raw_full[slot];
+            if (k >= S::kSlots)
+              role_wait(dead, &sh.raw_empty[slot], (uint32_t)((k / (S::kSlots ? S::kSlots : 1) - 1) & 1), a.status);
+          } else if (j >= ST) {  // (as many stages for every piece)
+            role_wait(dead, &sh.empty[st][y], (uint32_t)((j / ST - 1) & 1), a.status);
+          }
+          if (y == 0 && lane == 0) {
+            sh.exists[note][0] = there_lo;
+            sh.exists[note][1] = there_hi;
+          }
+          if (*dead) continue;
+          constexpr int kFirst = (LATENT ? 3 : S::kKChunks) * kChunk;  // bytes of piece 0
+          __syncwarp();
+          if (lane == 0)
+            mbar_arrive_expect_tx(full, S::kRaw ? S::kSlot : y == 0 ? kFirst : LATENT ? 2 * kChunk : S::kVChunks * kChunk);
+          __syncwarp();
+          if (lane < boxes) {
+            const CUtensorMap* map = !LATENT && y ? &vmap : &kmap;
+            if (S::kRaw) {
+              uint8_t* to = sm_raw + (2 * j + y) % (S::kSlots ? S::kSlots : 1) * S::kSlot + (lane << shift) * DK;
+              tma_load_4d(to, map, 0, x.in, p.hkv, x.page, full);
+            } else {
+              uint8_t* to = sm_kv + (y && !LATENT ? S::kV + st * S::kVStage : st * S::kStage) + (lane << shift) * 128;
+              if (LATENT) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  tma_load_4d(to + (2 * y + c) * kChunk, map, 64 * (2 * y + c), x.in, 0, x.page, full);
+                if (y == 0) tma_load_4d(to + (S::kKChunks - 1) * kChunk, map, DV, x.in, 0, x.page, full);
+              } else {
+#pragma unroll
+                for (int c = 0; c < S::kKChunks; ++c)
+                  tma_load_4d(to + c * kChunk, map, 64 * c, x.in, p.hkv, x.page, full);
+              }
+            }
+          }
+          __syncwarp();
+          if (S::kRaw) {
+            // the tokens' scales, 0 where there is none
+            const float* src = y ? a.c.v_scale : a.c.k_scale;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int t = 32 * u + lane, l = t >> shift;
+              const int page = __shfl_sync(kAll, x.page, l), in = __shfl_sync(kAll, x.in, l) + (t & (a.box - 1));
+              const bool ok = (u ? there_hi : there_lo) >> lane & 1;
+              const long long at = ok ? page * a.c.scale_page_stride + p.hkv * a.c.scale_head_stride +
+                                            in * a.c.scale_token_stride
+                                      : 0;
+              cp_async4_zfill(&sh.scale[E4M3 ? note : 0][y][E4M3 ? t : 0], src + at, ok);
+            }
+            cp_async_arrive(full);
+          }
+        }
+      }
+    }
+    // every copy has landed before the CTA's memory goes
+    cp_async_wait<0>();
+    if (lane == 0 && j > 0 && !S::kRaw)
+      for (int y = 0; y < NP; ++y)
+        for (int k = max(0, j - ST); k < j; ++k) mbar_wait(&sh.full[k % ST][y], (uint32_t)((k / ST) & 1));
+    if (lane == 0 && S::kRaw)
+      for (int k = max(0, 2 * j - S::kSlots); k < 2 * j; ++k)
+        mbar_wait(&sh.raw_full[k % (S::kSlots ? S::kSlots : 1)], (uint32_t)((k / (S::kSlots ? S::kSlots : 1)) & 1));
+    __syncwarp();
+  } else if (TMA && warp > kSoft + 2) {
+    // ---- E4M3 codes to bf16: half of the warps the keys', half the values' (one
+    // does not wait for the other's stage), a warp its share of the tokens
+    constexpr int kSlots = S::kSlots ? S::kSlots : 1, kTok = kTile / (S::kConvert ? S::kConvert / 2 : 1);
+    constexpr int LPR = DK / 16;           // lanes (16-byte chunks) per token row
+    constexpr int NI = kTok * LPR / 32;    // chunks per lane
+    const int y = (warp - kSoft - 3) & 1, w = (warp - kSoft - 3) >> 1, ch = lane % LPR, jj = 2 * (lane & 3);
+    Part p;
+    int j = 0;
+    while (walk.next_tiles(a, p))
+      for (int i = 0; i < p.n; ++i, ++j) {
+        const int k = 2 * j + y, slot = k % kSlots, held = y ? VST : ST, st = j % held;
+        role_wait(dead, &sh.raw_full[slot], (uint32_t)((k / kSlots) & 1), a.status);
+        const uint8_t* src = sm_raw + slot * S::kSlot + w * kTok * DK + lane * 16;
+        uint4 codes[NI];
+#pragma unroll
+        for (int n = 0; n < NI; ++n) codes[n] = *reinterpret_cast<const uint4*>(src + n * 512);
+        if (j >= held) role_wait(dead, &sh.empty[st][y], (uint32_t)((j / held - 1) & 1), a.status);
+        uint8_t* const to = sm_kv + (y ? S::kV + st * S::kVStage : st * S::kStage) + (ch >> 2) * kChunk;
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+          const int r = w * kTok + n * (32 / LPR) + lane / LPR;
+          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, jj)) = e4m3x8_to_bf16(codes[n].x, codes[n].y);
+          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, jj + 1)) = e4m3x8_to_bf16(codes[n].z, codes[n].w);
+        }
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.raw_empty[slot]);
+          mbar_arrive(&sh.full[st][y]);
+        }
+      }
+  } else if (!TMA && warp > kSoft + 1) {
+    // ---- loading, token by token: a warp per piece and stage, so that waiting for
+    // one piece's copies holds up no other
     const int stage = (warp - kSoft - 2) / NP, piece = (warp - kSoft - 2) % NP;
     uint64_t* const full = &sh.full[stage][piece];
     uint64_t* const empty = &sh.empty[stage][piece];
-    uint8_t* const dst = sm_kv + stage * S::kStage;
+    uint8_t* const dst = sm_kv + (piece && !LATENT ? S::kV + stage * S::kVStage : stage * S::kStage);
     struct Tok {
       long long at;   // elements from the head's first; -1: no such token
       long long sat;  // E4M3: of its scales
@@ -348,7 +617,7 @@ k_draft_attention(const DraftArgs a) {
         settle();
         look_up(tk);
         if (round > 0) role_wait(dead, empty, (uint32_t)((round - 1) & 1), a.status);
-        uint8_t* const to = dst + (piece ? S::kVOff : 0) + ((lane % LPR) >> 2) * kChunk;
+        uint8_t* const to = dst + ((lane % LPR) >> 2) * kChunk;
         const int j = 2 * (lane & 3);
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
@@ -369,7 +638,6 @@ k_draft_attention(const DraftArgs a) {
           to += 2 * piece * kChunk;
         } else if (piece) {
           src = static_cast<const uint16_t*>(a.c.v) + 8 * j;
-          to += S::kVOff;
         }
         constexpr int kOwn = LATENT ? 2 : S::kKChunks;
 #pragma unroll 4
@@ -441,18 +709,18 @@ k_draft_attention(const DraftArgs a) {
   } else if (warp == kSoft + 1) {
     // ---- outputs: O^T += V^T P^T (dimensions x rows).  A warp of their own: a
     // warp's MMAs wait for its own checks, not for the other's.
-    const uint32_t p0 = desc_k(smem_u32(sm_p)), v0 = desc_mn(smem_u32(sm_kv) + S::kVOff, kChunk);
+    const uint32_t p0 = desc_k(smem_u32(sm_p)), v0 = desc_mn(smem_u32(sm_kv) + S::kV, kChunk);
     const uint32_t idesc = idesc_bf16(DV >= 128 ? 128 : 64, npad, true, false);
     Part p;
     int j = 0;
     while (walk.next_tiles(a, p))
       for (int i = 0; i < p.n; ++i, ++j) {
-        const uint32_t st = uniform(j % ST);
-        if (!LATENT) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / ST) & 1), a.status);
+        const uint32_t st = uniform(j % VST);
+        if (!LATENT) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / VST) & 1), a.status);
         role_wait(dead, &sh.p_full, (uint32_t)(j & 1), a.status);
         tc::fence_after_sync();
         if (tc::elect_one() && !*dead) {
-          const uint32_t v = v0 + st * (S::kStage / 16);
+          const uint32_t v = v0 + st * (S::kVStage / 16);
 #pragma unroll
           for (int mb = 0; mb < S::kBlocks; ++mb) {
 #pragma unroll
@@ -504,8 +772,7 @@ k_draft_attention(const DraftArgs a) {
     if (more) load_q(p);
     int j = 0;
     while (walk.next(a, p)) {
-      if (rt == 0 && tid == 0 && p.parts)
-        a.info[p.b * a.c.Hkv + p.hkv] = make_int2(2 * (walk.first / walk.share) + (p.slot & 1), p.parts);
+      if (rt == 0 && tid == 0 && p.first) a.info[p.b * a.c.Hkv + p.hkv] = make_int2(2 * col + (p.slot & 1), p.parts);
       const size_t slot = (size_t)max(p.slot, 0) * a.gtiles + rt;
       float* const part_ml = a.part_ml + slot * 2 * kRows;
       if (p.n == 0) {  // (a part of fewer units than a tile)
@@ -537,7 +804,7 @@ k_draft_attention(const DraftArgs a) {
       }
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       for (int i = 0; i < p.n; ++i, ++j) {
-        const int st = j % ST, t0 = (p.tile + i) * kTile;
+        const int st = j % VST, t0 = (p.tile + i) * kTile;
         role_wait(dead, &sh.s_full[j & 1], (uint32_t)((j / 2) & 1), a.status);
         tc::fence_after_sync();
         uint32_t raw[4 * kBlk];
@@ -561,16 +828,17 @@ k_draft_attention(const DraftArgs a) {
                            (a.d.window > 0 && t0 < p.sp.ctx + drafts - a.d.window);
         float s[4 * kBlk];
 #pragma unroll
-        for (int u = 0; u < 4 * kBlk; ++u) s[u] = __uint_as_float(raw[u]) * scale2;
-        if (E4M3) {
-#pragma unroll
-          for (int u = 0; u < kBlk; ++u) {
-            const float2 f = *reinterpret_cast<const float2*>(&sh.scale[note][0][c0 + 8 * u + 2 * c]);
-            s[4 * u] *= f.x;
-            s[4 * u + 1] *= f.y;
-            s[4 * u + 2] *= f.x;
-            s[4 * u + 3] *= f.y;
+        for (int u = 0; u < kBlk; ++u) {
+          float2 f = make_float2(scale2, scale2);
+          if (E4M3) {
+            f = *reinterpret_cast<const float2*>(&sh.scale[note][0][c0 + 8 * u + 2 * c]);
+            f.x *= scale2;
+            f.y *= scale2;
           }
+          s[4 * u] = __uint_as_float(raw[4 * u]) * f.x;
+          s[4 * u + 1] = __uint_as_float(raw[4 * u + 1]) * f.y;
+          s[4 * u + 2] = __uint_as_float(raw[4 * u + 2]) * f.x;
+          s[4 * u + 3] = __uint_as_float(raw[4 * u + 3]) * f.y;
         }
         if (mixed || ~exists) {
 #pragma unroll
@@ -645,7 +913,7 @@ k_draft_attention(const DraftArgs a) {
         for (int u = 0; u < kBlk; ++u) {
           float2 vs = make_float2(1.f, 1.f);
           if (E4M3) {
-            if (u == 0 && !*dead) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / ST) & 1), a.status);
+            if (u == 0 && !*dead) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / VST) & 1), a.status);
             vs = *reinterpret_cast<const float2*>(&sh.scale[note][1][c0 + 8 * u + 2 * c]);
           }
 #pragma unroll
@@ -672,8 +940,8 @@ k_draft_attention(const DraftArgs a) {
           // A value that is not finite reaches the rows that see its token and no
           // other: it is added to their outputs, and the tile holds 0 in its place
           // (times a weight of 0 it would be NaN).
-          if (!LATENT) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / ST) & 1), a.status);
-          uint8_t* const v = sm_kv + st * S::kStage + S::kVOff;
+          if (!LATENT) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / VST) & 1), a.status);
+          uint8_t* const v = sm_kv + S::kV + st * S::kVStage;
           bool odd = false;
           for (int e = tid; e < kTile * (DV / 8); e += kSoftThreads) {
             const uint4 w = *reinterpret_cast<const uint4*>(v + e * 16);
@@ -792,10 +1060,10 @@ k_draft_attention(const DraftArgs a) {
 
 // Joins the parts of the segments that several columns hold, in order, and
 // answers zeros for sequences without new tokens.
-template <int DV>
-__global__ void __launch_bounds__(kJoinThreads) k_draft_join(const DraftArgs a) {
-  constexpr int kLanes = DV / 4, kGroups = kJoinThreads / kLanes;  // threads per row; rows, or shares of the parts
-  constexpr int kAhead = 8;
+// kAhead: parts of a thread that are on their way at once.
+template <int DV, int THREADS, int kAhead>
+__global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
+  constexpr int kLanes = DV / 4, kGroups = THREADS / kLanes;  // threads per row; rows, or shares of the parts
   __shared__ float4 s_acc[kGroups][kLanes];
   __shared__ float s_m[kGroups], s_l[kGroups];
   griddep_wait();
@@ -897,20 +1165,45 @@ int draft_gtiles(const moe_draft_dims& d, int Hkv) { return cdiv(d.n * (d.Hq / H
 // Columns times row tiles at most, whatever the shape.
 int draft_slots(int gtiles) { return std::max(2 * num_sms(), gtiles); }
 
-template <int DK, int DV, bool LATENT, bool E4M3>
-cudaError_t launch_draft(DraftArgs& a, cudaStream_t s) {
-  using S = DraftShape<DK, DV, LATENT, E4M3>;
-  cudaError_t err = ensure_smem((const void*)k_draft_attention<DK, DV, LATENT, E4M3>, S::kSmem);
+template <int DK, int DV, bool LATENT, bool E4M3, bool TMA>
+cudaError_t launch_draft(DraftArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
+  using S = DraftShape<DK, DV, LATENT, E4M3, TMA>;
+  cudaError_t err = ensure_smem((const void*)k_draft_attention<DK, DV, LATENT, E4M3, TMA>, S::kSmem);
   if (err != cudaSuccess) return err;
   const long long tiles = (std::min((long long)a.d.table_width * a.c.page_size, kMaxTokens) + kTile - 1) / kTile + 1;
   const long long units = (long long)a.d.B * a.c.Hkv * (tiles + kSegCost);
-  a.cols = (int)std::max(1ll, std::min<long long>(S::kCtas * num_sms() / a.gtiles, units / kMinUnits));
-  err = launch_k(k_draft_attention<DK, DV, LATENT, E4M3>, dim3(a.cols * a.gtiles), dim3(S::kWarps * 32), S::kSmem,
-                 s, true, a);
+  a.cols = (int)std::max(1ll, std::min<long long>(S::kCtas * num_sms() / a.gtiles, units));
+  err = launch_k(k_draft_attention<DK, DV, LATENT, E4M3, TMA>, dim3(a.cols * a.gtiles), dim3(S::kWarps * 32),
+                 S::kSmem, s, true, kmap, vmap, a);
   if (err != cudaSuccess) return err;
+  // many parts per segment: as many of a row's as a CTA's registers hold at
+  // once; few: more CTAs (2 x 131072 latent vectors, 76 parts: 73.5 us in all
+  // against 79.9 with the other form; 32 trees of 16, E4M3: 104.5 against 113.8)
   const int segs = a.d.B * a.c.Hkv * a.gtiles;
-  const int chunks = std::min(kRows, std::max(4, cdiv(2 * num_sms(), segs)));
-  return launch_k(k_draft_join<DV>, dim3(segs, chunks), dim3(kJoinThreads), 0, s, true, a);
+  if (a.cols >= 8 * a.d.B * a.c.Hkv)
+    return launch_k(k_draft_join<DV, 512, 8>, dim3(segs, std::min(kRows, cdiv(4 * num_sms(), segs))), dim3(512), 0, s,
+                    true, a);
+  return launch_k(k_draft_join<DV, 256, 4>, dim3(segs, std::min(kRows, std::max(8, cdiv(4 * num_sms(), segs)))),
+                  dim3(256), 0, s, true, a);
+}
+
+// A cache of pages that tile boxes divide is copied by maps of [pages, heads,
+// tokens, dimensions]; any other is gathered.
+template <int DK, int DV, bool LATENT, bool E4M3>
+cudaError_t launch_draft(DraftArgs& a, cudaStream_t s) {
+  CUtensorMap kmap{}, vmap{};
+  const int ps = a.c.page_size;
+  bool boxes = ps >= 8 && (ps % kTile == 0 || kTile % ps == 0);
+  a.box = std::min(ps, kTile);
+  while (boxes && 1 << a.box_shift < a.box) ++a.box_shift;
+  if (boxes) {
+    const long long strides[3] = {a.c.token_stride, a.c.head_stride, a.c.page_stride};
+    const int extents[3] = {ps, a.c.Hkv, a.c.pages};
+    boxes = make_cache_map(&kmap, a.c.k, E4M3, DK, extents, strides, a.box) == cudaSuccess &&
+            (LATENT || make_cache_map(&vmap, a.c.v, E4M3, DV, extents, strides, a.box) == cudaSuccess);
+  }
+  return boxes ? launch_draft<DK, DV, LATENT, E4M3, true>(a, kmap, vmap, s)
+               : launch_draft<DK, DV, LATENT, E4M3, false>(a, kmap, vmap, s);
 }
 
 }  // namespace

@@ -1053,6 +1053,30 @@ cudaError_t make_tensor_map_3d(CUtensorMap* map, const void* base, long long row
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_cache_map(CUtensorMap* map, const void* base, bool e4m3, int cols, const int (&extents)[3],
+                           const long long (&strides)[3], int box) {
+  EncodeTiled enc;
+  cudaError_t e = get_encoder(&enc);
+  if (e != cudaSuccess) return e;
+  const int esize = e4m3 ? 1 : 2;
+  cuuint64_t dims[4] = {(cuuint64_t)cols}, bytes[3];
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = (cuuint64_t)extents[i];
+    // (the stride of a single token, head or page steps nowhere)
+    const long long s = extents[i] > 1 ? strides[i] : cols;
+    if (s < 1 || s >= (1ll << 39)) return cudaErrorInvalidValue;
+    bytes[i] = (cuuint64_t)s * esize;
+  }
+  const cuuint32_t boxes[4] = {(cuuint32_t)(e4m3 ? cols : 64), (cuuint32_t)box, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r =
+      enc(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+          bytes, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 namespace {
 // 2-D map over a stack of code matrices [rows_total, K] (uint8, row-major):
 // box = 64 bytes of K x 128 rows, 64-byte swizzle (conflict-free reads of a

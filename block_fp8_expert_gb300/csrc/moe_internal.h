@@ -59,6 +59,14 @@ cudaError_t make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, int 
 cudaError_t make_tensor_map_3d(CUtensorMap* map, const void* base, long long rows, int heads, int cols,
                                long long row_stride, long long head_stride, int box_cols, int box_rows);
 
+// 4-D TMA map over a paged cache [pages, heads, tokens, cols] with the given
+// extents and strides (in elements) of tokens, heads and pages: bf16, box 64
+// columns x `box` tokens, 128-byte swizzle, or E4M3 codes, box all columns x
+// `box` tokens.  Out-of-range elements read as zero.  cudaErrorInvalidValue for
+// a layout that no map holds.
+cudaError_t make_cache_map(CUtensorMap* map, const void* base, bool e4m3, int cols, const int (&extents)[3],
+                           const long long (&strides)[3], int box);
+
 // Largest expert count the library accepts.
 constexpr int kMaxExperts = 1024;
 

@@ -673,7 +673,7 @@ moe_status moe_latent_store(const uint16_t* kv, const float* norm,
  *   out[b,i,h] = sum_t softmax_t(scale * q[b,i,h] . c[b,t]) c[b,t][0 .. R)
  * q bf16 [B, n, Hq, R + rot], out bf16 [B, n, Hq, R]; the rest as in
  * moe_tree_attention, without a window.  The softmax weights are rounded to
- * bf16 (2^-9 of the weight) before both the product and their sum.
+ * bf16 (2^-8 of the weight) before both the product and their sum.
  */
 moe_status moe_latent_attention_workspace_bytes(moe_draft_dims d, int32_t R,
                                                 size_t* bytes);
@@ -707,7 +707,7 @@ typedef struct {
  * fall.  Rows of no sequence are left as they were, and keys and values that a
  * row does not see do not reach it, whatever they are.
  * Scores, maxima, sums and outputs are fp32; the softmax weights are rounded
- * to bf16 (2^-9 of the weight) before both the product and their sum.
+ * to bf16 (2^-8 of the weight) before both the product and their sum.
  * Offsets outside the tensors, or falling ones, raise MOE_DEV_BAD_POSITION and
  * are clamped.
  */
