@@ -16,10 +16,11 @@ constexpr float kLog2e = 1.44269504088896341f;
 // fp32 sums and bf16 weights hold as well as ones below 1.
 constexpr float kMaxSlack = 8.f;
 
-// Instruction descriptor: bf16 A and B, fp32 D; A K-major, or M-major (its
+// Instruction descriptor: bf16 A and B (HALF: fp16), fp32 D; A K-major, or M-major (its
 // rows run along the contiguous axis of shared memory), B K-major or N-major.
+template <bool HALF = false>
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
-  return tc::idesc_f16_f32(M, N) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
+  return tc::idesc_f16_f32(M, N) | (HALF ? 0u : (1u << 7) | (1u << 10)) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16);
 }
 // Descriptors of 128-byte swizzled operands are built from their low words,
@@ -144,6 +145,43 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 A, B, C, R;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n mov.b64 C, {%6, %7};\n"
+      " fma.rn.f32x2 R, A, B, C;\n mov.b64 {%0, %1}, R;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 A, B, R;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n add.rn.f32x2 R, A, B;\n"
+      " mov.b64 {%0, %1}, R;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 A, B, R;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n mul.rn.f32x2 R, A, B;\n"
+      " mov.b64 {%0, %1}, R;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// Whether a pair of bf16 (of fp16) values holds an infinity or a NaN.
+template <bool HALF>
+__device__ __forceinline__ bool nonfinite_16x2(uint32_t v) {
+  constexpr uint32_t lo = HALF ? 0x7C00u : 0x7F80u, hi = lo << 16;
+  return (v & lo) == lo || (v & hi) == hi;
+}
+
 // A barrier of `threads` threads that tells whether any of them says yes.
 __device__ __forceinline__ bool bar_any(int id, int threads, bool yes) {
   uint32_t r;
@@ -174,9 +212,9 @@ __device__ __forceinline__ bool mbar_nap(uint64_t* bar, uint32_t parity) {
 // barriers matched.  (Clocks and flag are only read once a nap is over: reading
 // them takes as long as most waits, and a warp that polls takes issue slots and
 // shared-memory cycles from those that work.)
-__device__ __forceinline__ void role_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
-                                          int32_t* status) {
-  if (__all_sync(kAll, mbar_nap(bar, parity))) return;
+// (out of line: every wait is in the way of the code that a first call fetches)
+static __device__ __noinline__ void role_wait_on(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
+                                                 int32_t* status) {
   const WaitBudget b = wait_budget();
   while (true) {
     bool done = mbar_nap(bar, parity);
@@ -193,6 +231,10 @@ __device__ __forceinline__ void role_wait(volatile int* abort_flag, uint64_t* ba
     raise_status(status, MOE_DEV_WAIT_TIMEOUT);
   }
   __syncwarp();
+}
+__device__ __forceinline__ void role_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
+                                          int32_t* status) {
+  if (!__all_sync(kAll, mbar_nap(bar, parity))) role_wait_on(abort_flag, bar, parity, status);
 }
 
 // The same by a thread on its own.

@@ -18,7 +18,6 @@ namespace {
 using namespace attn;
 
 constexpr int kTile = 64;      // tokens per tile
-constexpr int kRows = 64;      // rows (query head x new token) of a CTA at most
 constexpr int kChunk = 8192;   // 64 tokens or rows x 64 dimensions, 128-byte swizzled
 constexpr int kSegCost = 3;    // what a segment costs a CTA beside its tiles, in tiles
 constexpr int kNoRow = 0x7fffffff;
@@ -36,18 +35,20 @@ constexpr int kNotes = 8;
 // one block of the outputs reads (the first piece with the shared key part).
 // TMA: pages of 8, 16, 32 or a multiple of 64 tokens are copied as boxes, E4M3
 // codes into a ring of their own, from where warps take them to the stages as
-// bf16; other page sizes are gathered token by token.
-template <int DK, int DV, bool LATENT, bool E4M3, bool TMA>
+// fp16; other page sizes are gathered token by token.
+// ROWS: rows (query head x new token) of a CTA at most, 64 or 128.
+template <int DK, int DV, bool LATENT, bool E4M3, bool TMA, int ROWS>
 struct DraftShape {
   static constexpr bool kRaw = E4M3 && TMA;
   static constexpr int kKChunks = DK / 64, kVChunks = LATENT ? 0 : DV / 64;
-  static constexpr int kParts = LATENT ? 1 : 2;  // bf16 parts of a softmax weight
-  static constexpr int kQ = kKChunks * kChunk, kP = kParts * kChunk;
-  static constexpr int kCtas = DK <= (kRaw ? 64 : 128) ? 2 : 1;  // per SM
+  static constexpr int kParts = LATENT || E4M3 ? 1 : 2;  // parts of a softmax weight: bf16, E4M3: fp16
+  static constexpr int kQChunk = ROWS * 128;  // the rows x 64 dimensions, or tokens
+  static constexpr int kQ = kKChunks * kQChunk, kP = kParts * kQChunk;
+  static constexpr int kCtas = ROWS == 64 && DK <= (kRaw ? 64 : 128) ? 2 : 1;  // per SM
   static constexpr int kBlocks = DV >= 128 ? DV / 128 : 1;  // of the outputs' dimensions
   static constexpr int kPieces = LATENT ? kBlocks : 2;
   // barriers and small arrays, the tiles' E4M3 scales, and the tiles' alignment
-  static constexpr int kFixed = 2048 + (E4M3 ? kNotes * 2 * kTile * 4 + 256 : 0) + 1024;
+  static constexpr int kFixed = (ROWS == 64 ? 2048 : 4096) + (E4M3 ? kNotes * 2 * kTile * 4 + 256 : 0) + 1024;
   static constexpr int kRoom = 227 * 1024 / kCtas - kFixed - kQ - kP;
   // tiles of keys and of values in shared memory, keys first
   static constexpr int kStages = LATENT && kRoom / (kKChunks * kChunk) >= 4 ? 4 : 2;
@@ -58,17 +59,18 @@ struct DraftShape {
   // the ring of codes, each slot 64 tokens' keys or values
   static constexpr int kSlot = kTile * DK;
   static constexpr int kSlotsFit = (kRoom - kStaged) / kSlot;
-  static constexpr int kSlots = !kRaw ? 0 : kSlotsFit >= 4 ? 4 : kSlotsFit;
-  static_assert(kRoom >= kStaged && (!kRaw || kSlots >= 2), "shared memory");
+  // (an even number: a slot is always the keys' or always the values')
+  static constexpr int kSlots = !kRaw ? 0 : kSlotsFit >= 4 ? 4 : 2;
+  static_assert(kRoom >= kStaged && (!kRaw || kSlotsFit >= 2), "shared memory");
   // softmax warps per 16 rows: they share the tile's tokens
-  static constexpr int kSplit = kCtas == 1 && (LATENT || kRaw) ? 2 : 1;
+  static constexpr int kSplit = kCtas == 1 && (LATENT || kRaw || ROWS == 128) ? 2 : 1;
   // softmax warps; then two for MMAs; then the loading warps: one for the boxes
   // and those that convert, or one per piece and stage
   static constexpr int kSoft = 4 * kSplit;
   static constexpr int kConvert = kRaw ? 4 * kSplit : 0;
   static constexpr int kWarps = kSoft + 2 + (TMA ? 1 + kConvert : kStages * kPieces);
   static constexpr int kSmem = kQ + kP + kStaged + kSlots * kSlot + 1024;
-  static constexpr int kCols = kOCol + kBlocks * kRows;
+  static constexpr int kCols = kOCol + kBlocks * ROWS;
   static constexpr int kTmem = kCols <= 256 ? 256 : 512;
   static_assert(kTmem * kCtas <= 512, "TMEM");
 };
@@ -82,12 +84,13 @@ struct DraftArgs {
   const int32_t* draft_lens;  // NULL: d.n
   moe_draft_dims d;
   int G, rows, gtiles;  // query heads per key/value head; n G; CTAs that share them
+  int tile_rows;        // rows of a CTA at most
   int cols;             // columns of the grid
   int box, box_shift;  // tokens of a page that one copy takes (TMA), a power of two
   uint32_t ps_mul, ps_shift;  // t / page_size = umulhi(t, ps_mul) >> ps_shift (page_size > 1)
   uint16_t* out;
-  float* part_o;   // [2 cols][gtiles][kRows][DV]
-  float* part_ml;  // [2 cols][gtiles][2][kRows]
+  float* part_o;   // [2 cols][gtiles][tile_rows][DV]
+  float* part_ml;  // [2 cols][gtiles][2][tile_rows]
   int2* info;      // [B][Hkv]: the segment's first slot, its parts
   int32_t* status;
 };
@@ -192,10 +195,9 @@ struct Walk {
 };
 
 // Tiles per part to try, in eighths of an even share.
-constexpr int kTries = 6;
+constexpr int kTries = 5;
 __device__ __forceinline__ int most_of(int even, int i) {
-  const int eighths[kTries] = {8, 9, 10, 11, 13, 16};
-  return max(kMinTiles, (even * eighths[i] + 7) / 8);
+  return max(kMinTiles, (even * (8 + i + i / 4 * 4) + 7) / 8);  // 8, 9, 10, 11, 16
 }
 // Every thread of the CTA calls this.
 template <int WARPS>
@@ -212,68 +214,45 @@ __device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned (*s_s
     return w;
   }
   if (tid == 0) *s_walk = Walk{0, 0, 0, 0, 0, 1, col, 0, 1, Span{0, 0, 0, 0, 0}};
-  // inclusive sums over the warp's lanes, and the warp's own sum
-  auto scan = [&](unsigned v, unsigned* to) {
+  // Loops that stay loops: what runs once is paid for by the fetch of its code.
+  Span span{0, 0, 0, 0, 0};  // of the last of this thread's sequences
+  unsigned mine, before, total;
+  int most = 0, even = 0;
+#pragma unroll 1
+  for (int i = -1; i <= kTries; ++i) {
+    // i = -1: tiles; then parts with sizes to try; at last units
+    const int m = i >= 0 && i < kTries ? most_of(even, i) : 1;
+    if (i > 0 && i < kTries && m > even + 2 * kSegCost) continue;  // (a share has two segments at most)
+    mine = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      if (per > 1 || i < 0) span = span_of(a, b);
+      mine += i < 0 ? span.tiles : i == kTries ? units_of(span) : quotient(span.tiles + m - 1, m);
+    }
+    unsigned incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned x = __shfl_up_sync(kAll, v, o);
-      if (lane >= o) v += x;
+      const unsigned x = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += x;
     }
-    if (lane == 31) to[warp] = v;
-    return v;
-  };
-  // the sum over the warps before this one, and over all
-  auto sums = [&](const unsigned* s, unsigned& before, unsigned& total) {
-    before = total = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const unsigned v = s[w];
-      if (w < warp) before += v;
-      total += v;
-    }
-  };
-  Span span{0, 0, 0, 0, 0};  // of the last of this thread's sequences
-  unsigned tiles = 0, units = 0, before, total;
-  for (int b = b0; b < b1; ++b) {
-    span = span_of(a, b);
-    tiles += span.tiles;
-    units += units_of(span);
-  }
-  scan(tiles, s_scan[0]);
-  const unsigned u_incl = scan(units, s_scan[1]);
-  __syncthreads();
-  sums(s_scan[0], before, total);
-  // (tiles fit 31 bits: the host checks)
-  const int even = quotient((int)(total * Hkv) + a.cols - 1, a.cols);
-  unsigned mine[kTries] = {}, incl[kTries];
-  for (int b = b0; b < b1; ++b) {
-    if (per > 1) span = span_of(a, b);
-#pragma unroll
-    for (int i = 0; i < kTries; ++i) {
-      const int m = most_of(even, i);
-      mine[i] += quotient(span.tiles + m - 1, m);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kTries; ++i) incl[i] = scan(mine[i], s_scan[2 + i]);
-  __syncthreads();
-  int most = 0;
-  unsigned parts = 0;
-#pragma unroll
-  for (int i = kTries - 1; i >= 0; --i) {
-    unsigned x, y;
-    sums(s_scan[2 + i], x, y);
-    // (a share has two segments at most)
-    if (y * Hkv <= (unsigned)a.cols && (i == 0 || most_of(even, i) <= even + 2 * kSegCost)) {
-      most = most_of(even, i);
-      before = x + incl[i] - mine[i];
-      parts = mine[i];
+    unsigned* const s = s_scan[i & 1];
+    if (lane == 31) s[warp] = incl;
+    __syncthreads();
+    const unsigned v = lane < WARPS ? s[lane] : 0;
+    total = __reduce_add_sync(kAll, v) * Hkv;
+    before = __reduce_add_sync(kAll, lane < warp ? v : 0) + incl - mine;
+    // (tiles fit 31 bits: the host checks)
+    if (i < 0) {
+      even = quotient((int)total + a.cols - 1, a.cols);
+    } else if (i < kTries && total <= (unsigned)a.cols) {
+      most = m;
+      break;
     }
   }
   Walk w;
   w.col = col;
   if (most) {
-    if (before * Hkv <= (unsigned)col && (unsigned)col < (before + parts) * Hkv) {
+    if (before * Hkv <= (unsigned)col && (unsigned)col < (before + mine) * Hkv) {
       for (w.b = b0; w.b < b1; ++w.b) {
         w.sp = per > 1 ? span_of(a, w.b) : span;
         w.parts = quotient(w.sp.tiles + most - 1, most);
@@ -288,12 +267,9 @@ __device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned (*s_s
       *s_walk = w;
     }
   } else {
-    sums(s_scan[1], before, total);
-    before += u_incl - units;
-    total *= Hkv;
     const unsigned share = quotient((int)(total + a.cols - 1), a.cols);
     const unsigned want = min((unsigned)col * share, total);
-    if (before * Hkv <= want && want < (before + units) * Hkv) {
+    if (before * Hkv <= want && want < (before + mine) * Hkv) {
       for (w.b = b0; w.b < b1; ++w.b) {
         w.sp = per > 1 ? span_of(a, w.b) : span;
         const unsigned u = units_of(w.sp);
@@ -313,7 +289,7 @@ __device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned (*s_s
   return *s_walk;
 }
 
-template <int STAGES, int PIECES, int SLOTS, int WARPS, bool E4M3>
+template <int ROWS, int STAGES, int PIECES, int SLOTS, int WARPS, bool E4M3>
 struct DraftShared {
   uint64_t raw_full[SLOTS ? SLOTS : 1], raw_empty[SLOTS ? SLOTS : 1];
   uint64_t full[STAGES][PIECES], empty[STAGES][PIECES], s_full[2], s_empty[2], p_full, pv_done, q_full;
@@ -321,47 +297,51 @@ struct DraftShared {
   volatile int abort_flag;
   uint32_t exists[kNotes][2];  // tokens of the tile that are there
   alignas(8) float scale[E4M3 ? kNotes : 1][2][E4M3 ? kTile : 1];  // of its keys and values
-  float factor[kRows];  // on the outputs of a row, when its maximum moves
+  float factor[ROWS];  // on the outputs of a row, when its maximum moves
+  int vexp[kNotes];    // E4M3: exponents of the tiles' largest value scales
+  float q_scale[2][E4M3 ? ROWS : 1];  // E4M3: of the rows' queries, this part's and the next one's
   union {
-    float top[2][kRows];  // the largest score of a row, by halves of the tile
-    float inv[kRows];     // after the last tile: 1 / the row's sum
+    float top[2][ROWS];  // the largest score of a row, by halves of the tile; after the last tile [1]: half of its sum
+    float inv[ROWS];     // after the last tile: 1 / the row's sum
   };
   union {
-    unsigned scan[2 + kTries][WARPS];
-    uint64_t seen[kRows];  // tokens of the tile that a row sees
-    long long at[kRows];   // after the last tile: the rows' outputs, in elements; -1: none
+    unsigned scan[2][WARPS];
+    uint64_t seen[ROWS];  // tokens of the tile that a row sees
+    long long at[ROWS];   // after the last tile: the rows' outputs, in elements; -1: none
   };
   Walk walk;
 };
 
-// E4M3 codes -> bf16, exact (every E4M3 value is a bf16 value); NaN stays NaN.
-__device__ __forceinline__ uint4 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
-  const uint32_t h[4] = {e4m3x2_to_f16x2(lo & 0xFFFFu), e4m3x2_to_f16x2(lo >> 16),
-                         e4m3x2_to_f16x2(hi & 0xFFFFu), e4m3x2_to_f16x2(hi >> 16)};
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    r[i] = pack_bf16x2(f.x, f.y);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+// E4M3 codes -> fp16, exact (every E4M3 value is an fp16 value).
+__device__ __forceinline__ uint4 e4m3x8_to_f16(uint32_t lo, uint32_t hi) {
+  return make_uint4(e4m3x2_to_f16x2(lo & 0xFFFFu), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi & 0xFFFFu),
+                    e4m3x2_to_f16x2(hi >> 16));
 }
-
-__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t v) {
-  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+// Next to E4M3 codes the products are of fp16.  Weights times their value's scale
+// are held as w 2^(kWTop - e), e the exponent of the largest scale so far; as a
+// maximum moves here once it is exceeded four times (kHalfSlack), they stay below
+// 2^15, and fp16 keeps eleven bits down to 2^-26 of the largest, and steps of
+// 2^-36 of it below.
+constexpr float kWTop = 12.f, kHalfSlack = 2.f;
+constexpr int kExpMin = -120, kExpMax = 120;
+// The exponent of a scale, for the largest (what is not finite counts as none).
+__device__ __forceinline__ int scale_exp(float v) {
+  const uint32_t bits = __float_as_uint(v) & 0x7fffffffu;
+  return bits >= 0x7f800000u ? kExpMin : min(max((int)(bits >> 23) - 127, kExpMin), kExpMax);
 }
 
 }  // namespace
 
-template <int DK, int DV, bool LATENT, bool E4M3, bool TMA>
-__global__ void __launch_bounds__(DraftShape<DK, DV, LATENT, E4M3, TMA>::kWarps * 32,
-                                  DraftShape<DK, DV, LATENT, E4M3, TMA>::kCtas)
+template <int DK, int DV, bool LATENT, bool E4M3, bool TMA, int ROWS>
+__global__ void __launch_bounds__(DraftShape<DK, DV, LATENT, E4M3, TMA, ROWS>::kWarps * 32,
+                                  DraftShape<DK, DV, LATENT, E4M3, TMA, ROWS>::kCtas)
 k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const DraftArgs a) {
-  using S = DraftShape<DK, DV, LATENT, E4M3, TMA>;
+  using S = DraftShape<DK, DV, LATENT, E4M3, TMA, ROWS>;
+  constexpr int kRows = ROWS;
   constexpr int ST = S::kStages, VST = S::kVStages, NP = S::kPieces, kSoft = S::kSoft, kSoftThreads = kSoft * 32;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ DraftShared<ST, NP, S::kSlots, S::kWarps, E4M3> sh;
+  __shared__ DraftShared<ROWS, ST, NP, S::kSlots, S::kWarps, E4M3> sh;
   static_assert(sizeof(sh) + 1024 <= S::kFixed, "shared memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -519,7 +499,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         mbar_wait(&sh.raw_full[k % (S::kSlots ? S::kSlots : 1)], (uint32_t)((k / (S::kSlots ? S::kSlots : 1)) & 1));
     __syncwarp();
   } else if (TMA && warp > kSoft + 2) {
-    // ---- E4M3 codes to bf16: half of the warps the keys', half the values' (one
+    // ---- E4M3 codes to fp16: half of the warps the keys', half the values' (one
     // does not wait for the other's stage), a warp its share of the tokens
     constexpr int kSlots = S::kSlots ? S::kSlots : 1, kTok = kTile / (S::kConvert ? S::kConvert / 2 : 1);
     constexpr int LPR = DK / 16;           // lanes (16-byte chunks) per token row
@@ -540,8 +520,13 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
           const int r = w * kTok + n * (32 / LPR) + lane / LPR;
-          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, jj)) = e4m3x8_to_bf16(codes[n].x, codes[n].y);
-          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, jj + 1)) = e4m3x8_to_bf16(codes[n].z, codes[n].w);
+          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, jj)) = e4m3x8_to_f16(codes[n].x, codes[n].y);
+          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, jj + 1)) = e4m3x8_to_f16(codes[n].z, codes[n].w);
+        }
+        if (y && w == 0) {
+          const float* sc = sh.scale[E4M3 ? j % kNotes : 0][1];
+          const int e = max(scale_exp(sc[E4M3 ? lane : 0]), scale_exp(sc[E4M3 ? 32 + lane : 0]));
+          sh.vexp[j % kNotes] = __reduce_max_sync(kAll, e);
         }
         tc::fence_proxy_async();
         __syncwarp();
@@ -597,7 +582,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       const int note = (round * ST + stage) % kNotes;
       const uint32_t there[2] = {__ballot_sync(kAll, tk[0].at >= 0), __ballot_sync(kAll, tk[1].at >= 0)};
       if (E4M3) {
-        // codes to registers, and as bf16 into the stage once it is free
+        // codes to registers, and as fp16 into the stage once it is free
         constexpr int LPR = DK / 16;          // lanes (16-byte chunks) per token row
         constexpr int NI = kTile * LPR / 32;  // loads per lane
         const uint8_t* const src = static_cast<const uint8_t*>(piece ? a.c.v : a.c.k);
@@ -622,11 +607,12 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
           const int r = n * (32 / LPR) + lane / LPR;
-          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, j)) = e4m3x8_to_bf16(codes[n].x, codes[n].y);
-          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, j + 1)) = e4m3x8_to_bf16(codes[n].z, codes[n].w);
+          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, j)) = e4m3x8_to_f16(codes[n].x, codes[n].y);
+          *reinterpret_cast<uint4*>(to + tc::sw128_off(r, j + 1)) = e4m3x8_to_f16(codes[n].z, codes[n].w);
         }
         sh.scale[note][piece][lane] = sc[0];
         sh.scale[note][piece][32 + lane] = sc[1];
+        if (piece) sh.vexp[note] = __reduce_max_sync(kAll, max(scale_exp(sc[0]), scale_exp(sc[1])));
       } else {
         if (round > 0) role_wait(dead, empty, (uint32_t)((round - 1) & 1), a.status);
         // this lane's 16-byte chunk of the 128-byte rows of the piece's chunks
@@ -667,7 +653,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   } else if (warp == kSoft) {
     // ---- scores: S = Q K^T (rows x tokens), up to two tiles ahead of the softmax
     const uint32_t q0 = desc_k(smem_u32(sm_q)), kv0 = desc_k(smem_u32(sm_kv));
-    constexpr uint32_t idesc = idesc_bf16(kRows, kTile, false, false);
+    constexpr uint32_t idesc = idesc_bf16<E4M3>(kRows, kTile, false, false);
     constexpr int kKeys = LATENT ? NP : 1;  // pieces with keys
     Part p;
     int j = 0, parts = 0;
@@ -686,7 +672,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             auto chunk = [&](int c, uint32_t add) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_ss(d, q0 + c * (kChunk / 16) + 2 * kk, k + c * (kChunk / 16) + 2 * kk, idesc, kk ? 1u : add);
+                mma_ss(d, q0 + c * (S::kQChunk / 16) + 2 * kk, k + c * (kChunk / 16) + 2 * kk, idesc, kk ? 1u : add);
             };
             if (LATENT) {
               chunk(2 * x, x);
@@ -710,7 +696,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // ---- outputs: O^T += V^T P^T (dimensions x rows).  A warp of their own: a
     // warp's MMAs wait for its own checks, not for the other's.
     const uint32_t p0 = desc_k(smem_u32(sm_p)), v0 = desc_mn(smem_u32(sm_kv) + S::kV, kChunk);
-    const uint32_t idesc = idesc_bf16(DV >= 128 ? 128 : 64, npad, true, false);
+    const uint32_t idesc = idesc_bf16<E4M3>(DV >= 128 ? 128 : 64, npad, true, false);
     Part p;
     int j = 0;
     while (walk.next_tiles(a, p))
@@ -728,7 +714,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
                 mma_ss(tmem + kOCol + mb * kRows, v + (2 * mb * kChunk + kk * 2048) / 16,
-                       p0 + (y * kChunk + kk * 32) / 16, idesc, 1u);
+                       p0 + (y * S::kQChunk + kk * 32) / 16, idesc, 1u);
             if (LATENT) tc::commit(&sh.empty[st][mb]);
           }
           if (!LATENT) tc::commit(&sh.empty[st][NP - 1]);
@@ -739,16 +725,21 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     if (j > 0 && lane == 0) mbar_wait(&sh.pv_done, (uint32_t)((j - 1) & 1));
     __syncwarp();
   } else {
-    // ---- softmax.  A thread holds 8 kBlk tokens of rows ra and ra + 8, a quad
-    // of lanes (times kSplit warps) a row.
-    constexpr int kMine = kTile / S::kSplit, kBlk = kMine / 8;  // tokens of a warp, in blocks of 8
-    const int g = lane >> 2, c = lane & 3, quad = warp & 3, half = warp >> 2, ra = 16 * quad + g;
+    // ---- softmax.  Of 128 rows, a thread (times kSplit) has one, of 64 a quad of
+    // lanes has rows ra and ra + 8: a thread holds kE tokens of kX rows.
+    constexpr int kMine = kTile / S::kSplit;  // tokens of a warp
+    constexpr int kX = ROWS == 64 ? 2 : 1, kE = ROWS == 64 ? kMine / 4 : kMine;
+    const int c = lane & 3, quad = warp & 3, half = warp >> 2;
+    const int ra = ROWS == 64 ? 16 * quad + (lane >> 2) : 32 * quad + lane;
     const int c0 = half * kMine;  // the warp's first token
+    const bool writes = ROWS == 128 || c == 0;  // what a row has once
+    // the token of element e, from the warp's first on
+    auto token = [&](int e) { return ROWS == 64 ? 8 * (e / 2) + 2 * c + (e & 1) : e; };
     const uint32_t quadrant = tmem + ((uint32_t)(32 * quad) << 16);
     const float scale2 = a.d.scale * kLog2e;
     Walk ahead = walk;
     Part p;
-    auto load_q = [&](const Part& x) {
+    auto load_q = [&](const Part& x, int buf) {
       // a warp: kRows / kSoft rows, four at a time, eight lanes to a row
       constexpr int kOwn = kRows / kSoft;
       const int R = row0 + warp * kOwn + (lane & (kOwn - 1)), n = R / a.G;
@@ -756,21 +747,47 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                  ? x.b * a.d.q_stride + n * a.d.q_row_stride + (long long)(x.hkv * a.G + R - n * a.G) * DK
                                  : -1;
       const int j = lane & 7;
-#pragma unroll
+#pragma unroll 1
       for (int r4 = 0; r4 < kOwn; r4 += 4) {
         const int r = r4 + (lane >> 3);
         const long long o = __shfl_sync(kAll, mine, r);
         const bool ok = o >= 0;
         const uint16_t* src = a.q + (ok ? o : 0) + 8 * j;
         uint8_t* to = sm_q + tc::sw128_off(warp * kOwn + r, j);
+        if (!E4M3) {
 #pragma unroll
-        for (int k = 0; k < S::kKChunks; ++k) tc::cp_async16_zfill(to + k * kChunk, src + 64 * k, ok);
+          for (int k = 0; k < S::kKChunks; ++k) tc::cp_async16_zfill(to + k * S::kQChunk, src + 64 * k, ok);
+        } else {
+          // as fp16, the row times a power of two that puts its largest magnitude
+          // into [2^14, 2^15): exact but for what is below 2^-28 of it
+          uint4 v[S::kKChunks];
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < S::kKChunks; ++k) {
+            v[k] = ok ? ldg16(src + 64 * k) : make_uint4(0, 0, 0, 0);
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) top = max(top, max(u[y] & 0x7FFFu, (u[y] >> 16) & 0x7FFFu));
+          }
+#pragma unroll
+          for (int y = 1; y < 8; y <<= 1) top = max(top, __shfl_xor_sync(kAll, top, y));
+          const int E = min(exp_of_bits(top << 16), 126);
+          const float f = pow2f(kGroupTop - E);
+#pragma unroll
+          for (int k = 0; k < S::kKChunks; ++k) {
+            uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) u[y] = pack_f16x2(bf16_lo(u[y]) * f, bf16_hi(u[y]) * f);
+            *reinterpret_cast<uint4*>(to + k * S::kQChunk) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          if (j == 0) sh.q_scale[buf][E4M3 ? warp * kOwn + r : 0] = scale2 * pow2f(E - kGroupTop);
+        }
       }
       cp_async_commit();
     };
     bool more = ahead.next_tiles(a, p);
-    if (more) load_q(p);
-    int j = 0;
+    if (more) load_q(p, 0);
+    int j = 0, buf = 0;
     while (walk.next(a, p)) {
       if (rt == 0 && tid == 0 && p.first) a.info[p.b * a.c.Hkv + p.hkv] = make_int2(2 * col + (p.slot & 1), p.parts);
       const size_t slot = (size_t)max(p.slot, 0) * a.gtiles + rt;
@@ -788,11 +805,11 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       if (lane == 0) mbar_arrive(&sh.q_full);
       // what the thread's two rows see: the context from `low` on, and the new
       // tokens of `tree`
-      uint64_t tree[2];
-      int low[2];
+      uint64_t tree[kX];
+      int low[kX];
       const int drafts = p.sp.len - p.sp.ctx;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < kX; ++x) {
         const int R = row0 + ra + 8 * x, n = R / a.G;
         tree[x] = 0;
         low[x] = kNoRow;
@@ -802,73 +819,104 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           low[x] = a.d.window > 0 ? p.sp.ctx + max(1, __popcll(tree[x])) - a.d.window : 0;
         }
       }
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float m[kX], l[kX], qf[kX];  // the maximum, the sum, the factor on the scores
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        m[x] = -INFINITY;
+        l[x] = 0.f;
+        qf[x] = scale2;
+      }
+      int vexp = kExpMin;  // E4M3: the exponent that the weights are held at
       for (int i = 0; i < p.n; ++i, ++j) {
         const int st = j % VST, t0 = (p.tile + i) * kTile;
         role_wait(dead, &sh.s_full[j & 1], (uint32_t)((j / 2) & 1), a.status);
         tc::fence_after_sync();
-        uint32_t raw[4 * kBlk];
-        if constexpr (kBlk == 8)
-          ld_16x256b_x8(quadrant + (j & 1) * kTile + c0, raw);
-        else
-          ld_16x256b_x4(quadrant + (j & 1) * kTile + c0, raw);
-        tc::wait_ld();
+        float s[kX][kE];
+        {
+          uint32_t raw[kX * kE];
+          const uint32_t at = quadrant + (j & 1) * kTile + c0;
+          if constexpr (ROWS == 64 && kMine == 64)
+            ld_16x256b_x8(at, raw);
+          else if constexpr (ROWS == 64)
+            ld_16x256b_x4(at, raw);
+          else
+            tc::ld_32x32b_x32(at, raw);
+          tc::wait_ld();
+#pragma unroll
+          for (int x = 0; x < kX; ++x)
+#pragma unroll
+            for (int e = 0; e < kE; ++e)
+              s[x][e] = __uint_as_float(raw[ROWS == 64 ? 4 * (e / 2) + 2 * x + (e & 1) : e]);
+        }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.s_empty[j & 1]);
         if (i == p.n - 1) {  // the queries have been read for the last time
           Part x;
           more = ahead.next_tiles(a, x);
-          if (more) load_q(x);
+          if (more) load_q(x, buf ^ 1);
         }
         const int note = j % kNotes;
         const uint64_t exists = (uint64_t)sh.exists[note][1] << 32 | sh.exists[note][0];
         // a tile that some rows see more of than others
         const bool mixed = t0 + kTile > p.sp.ctx ||
                            (a.d.window > 0 && t0 < p.sp.ctx + drafts - a.d.window);
-        float s[4 * kBlk];
+        if (E4M3 && i == 0) {  // (with the first scores the queries' factors are there)
 #pragma unroll
-        for (int u = 0; u < kBlk; ++u) {
-          float2 f = make_float2(scale2, scale2);
-          if (E4M3) {
-            f = *reinterpret_cast<const float2*>(&sh.scale[note][0][c0 + 8 * u + 2 * c]);
-            f.x *= scale2;
-            f.y *= scale2;
+          for (int x = 0; x < kX; ++x) qf[x] = sh.q_scale[buf][E4M3 ? ra + 8 * x : 0];
+        }
+#pragma unroll
+        for (int e = 0; e < kE; e += 2) {
+          float2 f = make_float2(1.f, 1.f);
+          if (E4M3) f = *reinterpret_cast<const float2*>(&sh.scale[note][0][c0 + token(e)]);
+#pragma unroll
+          for (int x = 0; x < kX; ++x) {
+            const float2 g = E4M3 ? mul2(f, make_float2(qf[x], qf[x])) : make_float2(qf[x], qf[x]);
+            const float2 v = mul2(make_float2(s[x][e], s[x][e + 1]), g);
+            s[x][e] = v.x;
+            s[x][e + 1] = v.y;
           }
-          s[4 * u] = __uint_as_float(raw[4 * u]) * f.x;
-          s[4 * u + 1] = __uint_as_float(raw[4 * u + 1]) * f.y;
-          s[4 * u + 2] = __uint_as_float(raw[4 * u + 2]) * f.x;
-          s[4 * u + 3] = __uint_as_float(raw[4 * u + 3]) * f.y;
         }
         if (mixed || ~exists) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int x = 0; x < kX; ++x) {
             uint64_t seen = low_bits(p.sp.ctx - t0) & ~low_bits(min(low[x], t0 + kTile) - t0);
             const int sft = p.sp.ctx - t0;
             if (sft > -64 && sft < 64) seen |= sft >= 0 ? tree[x] << sft : tree[x] >> -sft;
             seen &= exists;
-            if (c == 0 && half == 0) sh.seen[ra + 8 * x] = seen;
-            const uint64_t mine = seen >> (c0 + 2 * c);
+            if (writes && half == 0) sh.seen[ra + 8 * x] = seen;
+            const uint64_t mine = seen >> (ROWS == 64 ? c0 + 2 * c : c0);
 #pragma unroll
-            for (int u = 0; u < kBlk; ++u) {
-              if (!(mine >> (8 * u) & 1)) s[4 * u + 2 * x] = -INFINITY;
-              if (!(mine >> (8 * u + 1) & 1)) s[4 * u + 2 * x + 1] = -INFINITY;
-            }
+            for (int e = 0; e < kE; ++e)
+              if (!(mine >> (ROWS == 64 ? 8 * (e / 2) + (e & 1) : e) & 1)) s[x][e] = -INFINITY;
           }
         }
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[kX];
+        bool above = false;
 #pragma unroll
-        for (int u = 0; u < kBlk; ++u)
+        for (int x = 0; x < kX; ++x) {
+          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int x = 0; x < 2; ++x) mx[x] = fmaxf(mx[x], fmaxf(s[4 * u + 2 * x], s[4 * u + 2 * x + 1]));
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          mx[x] = fmaxf(mx[x], __shfl_xor_sync(kAll, mx[x], 1));
-          mx[x] = fmaxf(mx[x], __shfl_xor_sync(kAll, mx[x], 2));
-          if (S::kSplit > 1 && c == 0) sh.top[half][ra + 8 * x] = mx[x];
+          for (int e = 0; e < kE; e += 2) top[e / 2 & 1] = max3(top[e / 2 & 1], s[x][e], s[x][e + 1]);
+          mx[x] = fmaxf(top[0], top[1]);
+          if (ROWS == 64) {
+            mx[x] = fmaxf(mx[x], __shfl_xor_sync(kAll, mx[x], 1));
+            mx[x] = fmaxf(mx[x], __shfl_xor_sync(kAll, mx[x], 2));
+          }
+          if (S::kSplit > 1 && writes) sh.top[half][ra + 8 * x] = mx[x];
+          above |= mx[x] > m[x] + (E4M3 ? kHalfSlack : kMaxSlack);  // (a row's first score moves its maximum from -inf)
         }
-        // (-inf + slack is -inf: a row's first score moves its maximum)
-        const bool moved = bar_any(1, kSoftThreads, mx[0] > m[0] + kMaxSlack || mx[1] > m[1] + kMaxSlack);
+        bool moved = bar_any(1, kSoftThreads, above);
+        float vmove = 1.f;
+        if (E4M3) {
+          role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / VST) & 1), a.status);  // the values' scales
+          const int top = sh.vexp[note];
+          if (top > vexp) {  // (in every thread)
+            vmove = ldexp2f(1.f, vexp - top);
+            vexp = top;
+            moved = true;
+          }
+        }
         if (j > 0) role_wait(dead, &sh.pv_done, (uint32_t)((j - 1) & 1), a.status);
         tc::fence_after_sync();
         if (i == 0) {  // the products are added to zeros
@@ -881,13 +929,13 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         if (moved) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int x = 0; x < kX; ++x) {
             if (S::kSplit > 1) mx[x] = fmaxf(mx[x], sh.top[half ^ 1][ra + 8 * x]);
             const float mn = fmaxf(m[x], mx[x]);
             const float f = m[x] == mn ? 1.f : exp2_fast(m[x] - mn);
             l[x] *= f;
             m[x] = mn;
-            if (c == 0 && half == 0) sh.factor[ra + 8 * x] = f;
+            if (writes && half == 0) sh.factor[ra + 8 * x] = f * vmove;
           }
           named_bar(1, kSoftThreads);  // (before the halves' tops are written again, too)
           if (i > 0) {
@@ -907,35 +955,53 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             tc::wait_st();
           }
         }
-        const float ms[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
         // weights, as the second product's operand: row, then token
+        const float vdown = pow2f(-vexp);
+        uint32_t w[S::kParts][ROWS == 64 ? 1 : 4];
+        float2 sum[kX];
 #pragma unroll
-        for (int u = 0; u < kBlk; ++u) {
-          float2 vs = make_float2(1.f, 1.f);
-          if (E4M3) {
-            if (u == 0 && !*dead) role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / VST) & 1), a.status);
-            vs = *reinterpret_cast<const float2*>(&sh.scale[note][1][c0 + 8 * u + 2 * c]);
-          }
+        for (int x = 0; x < kX; ++x) sum[x] = make_float2(0.f, 0.f);
+        {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float w0 = exp2_fast(s[4 * u + 2 * x] - ms[x]), w1 = exp2_fast(s[4 * u + 2 * x + 1] - ms[x]);
-            uint8_t* to = sm_p + tc::sw128_off(ra + 8 * x, c0 / 8 + u) + 4 * c;
-            if (S::kParts == 1) {
-              const uint32_t w = pack_bf16x2(w0, w1);
-              l[x] += bf16_lo(w) + bf16_hi(w);
-              *reinterpret_cast<uint32_t*>(to) = w;
-            } else {
-              l[x] += w0 + w1;
-              if (E4M3) {  // (a token that is not seen may have any scale)
-                w0 = w0 == 0.f ? 0.f : w0 * vs.x;
-                w1 = w1 == 0.f ? 0.f : w1 * vs.y;
+          for (int e = 0; e < kE; e += 2) {
+            float2 vs = make_float2(1.f, 1.f);
+            if (E4M3)
+              vs = mul2(*reinterpret_cast<const float2*>(&sh.scale[note][1][c0 + token(e)]), make_float2(vdown, vdown));
+#pragma unroll
+            for (int x = 0; x < kX; ++x) {
+              const float ms = (m[x] == -INFINITY ? 0.f : m[x]) - (E4M3 ? kWTop : 0.f);
+              const float2 d = add2(make_float2(s[x][e], s[x][e + 1]), make_float2(-ms, -ms));
+              float2 v = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+              const int k = ROWS == 64 ? 0 : e / 2 % 4;
+              if (E4M3) {
+                sum[x] = add2(sum[x], v);
+                float2 t = mul2(v, vs);
+                t.x = v.x == 0.f ? 0.f : t.x;  // (a token that is not seen may have any scale)
+                t.y = v.y == 0.f ? 0.f : t.y;
+                w[0][k] = pack_f16x2(t.x, t.y);
+              } else if (S::kParts == 1) {
+                w[0][k] = pack_bf16x2(v.x, v.y);
+                sum[x] = add2(sum[x], make_float2(bf16_lo(w[0][k]), bf16_hi(w[0][k])));
+              } else {
+                sum[x] = add2(sum[x], v);
+                w[0][k] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+                const float2 r = add2(v, make_float2(-bf16_lo(w[0][k]), -bf16_hi(w[0][k])));
+                w[S::kParts - 1][k] = pack_bf16x2(r.x, r.y);
               }
-              const uint32_t hi = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
-              *reinterpret_cast<uint32_t*>(to) = hi;
-              *reinterpret_cast<uint32_t*>(to + kChunk) = pack_bf16x2(w0 - bf16_lo(hi), w1 - bf16_hi(hi));
+#pragma unroll
+              for (int y = 0; y < S::kParts; ++y) {
+                if (ROWS == 64)
+                  *reinterpret_cast<uint32_t*>(sm_p + y * S::kQChunk + tc::sw128_off(ra + 8 * x, c0 / 8 + e / 2) +
+                                               4 * c) = w[y][0];
+                else if (k == 3)
+                  *reinterpret_cast<uint4*>(sm_p + y * S::kQChunk + tc::sw128_off(ra, (c0 + e) / 8)) =
+                      make_uint4(w[y][0], w[y][ROWS == 64 ? 0 : 1], w[y][ROWS == 64 ? 0 : 2], w[y][k]);
+              }
             }
           }
         }
+#pragma unroll
+        for (int x = 0; x < kX; ++x) l[x] += sum[x].x + sum[x].y;
         if (mixed) {
           // A value that is not finite reaches the rows that see its token and no
           // other: it is added to their outputs, and the tile holds 0 in its place
@@ -945,8 +1011,8 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           bool odd = false;
           for (int e = tid; e < kTile * (DV / 8); e += kSoftThreads) {
             const uint4 w = *reinterpret_cast<const uint4*>(v + e * 16);
-            odd |= bf16x2_nonfinite(w.x) || bf16x2_nonfinite(w.y) || bf16x2_nonfinite(w.z) ||
-                   bf16x2_nonfinite(w.w);
+            odd |= nonfinite_16x2<E4M3>(w.x) || nonfinite_16x2<E4M3>(w.y) || nonfinite_16x2<E4M3>(w.z) ||
+                   nonfinite_16x2<E4M3>(w.w);
           }
           if (bar_any(1, kSoftThreads, odd)) {
 #pragma unroll 1
@@ -962,11 +1028,12 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 for (int t = 0; t < kTile; ++t) {
                   const uint32_t w = *reinterpret_cast<const uint16_t*>(
                       v + (d >> 6) * kChunk + tc::sw128_off(t, (d >> 3) & 7) + 2 * (d & 7));
-                  const bool bad = (w & 0x7F80u) == 0x7F80u;
+                  const bool bad = nonfinite_16x2<E4M3>(w);
+                  const float add = E4M3 ? NAN : __uint_as_float(w << 16);  // (E4M3 has no infinity)
 #pragma unroll
                   for (int u = 0; u < 16; ++u) {
                     if (bad && (sh.seen[r0 + u] >> t & 1))
-                      o[u] = __float_as_uint(__uint_as_float(o[u]) + __uint_as_float(w << 16));
+                      o[u] = __float_as_uint(__uint_as_float(o[u]) + add);
                   }
                 }
                 st_32x32b_x16(at, o);
@@ -976,7 +1043,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             named_bar(1, kSoftThreads);  // every thread has read the values
             for (int e = tid; e < kTile * DV; e += kSoftThreads) {
               uint16_t* w = reinterpret_cast<uint16_t*>(v) + e;
-              if ((*w & 0x7F80u) == 0x7F80u) *w = 0;
+              if (nonfinite_16x2<E4M3>(*w)) *w = 0;
             }
           }
         }
@@ -993,20 +1060,22 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                 : -1;
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        l[x] += __shfl_xor_sync(kAll, l[x], 1);
-        l[x] += __shfl_xor_sync(kAll, l[x], 2);
-        if (S::kSplit > 1 && c == 0 && half == 1) sh.factor[ra + 8 * x] = l[x];
+      for (int x = 0; x < kX; ++x) {
+        if (ROWS == 64) {
+          l[x] += __shfl_xor_sync(kAll, l[x], 1);
+          l[x] += __shfl_xor_sync(kAll, l[x], 2);
+        }
+        if (S::kSplit > 1 && writes && half == 1) sh.top[1][ra + 8 * x] = l[x];  // (factors may be in use still)
       }
       if (S::kSplit > 1) named_bar(1, kSoftThreads);
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (c == 0 && half == 0) {
+      for (int x = 0; x < kX; ++x)
+        if (writes && half == 0) {
           const int r = ra + 8 * x;
-          if (S::kSplit > 1) l[x] += sh.factor[r];
+          if (S::kSplit > 1) l[x] += sh.top[1][r];
           // (a row that is none has taken in the tiles that all rows see alike)
           const bool real = low[x] != kNoRow;
-          sh.inv[r] = l[x] == 0.f || !real ? 0.f : 1.f / l[x];
+          sh.inv[r] = l[x] == 0.f || !real ? 0.f : E4M3 ? ldexp2f(1.f / l[x], vexp) : 1.f / l[x];
           if (p.slot >= 0) {
             part_ml[r] = real ? m[x] : -INFINITY;
             part_ml[kRows + r] = real ? l[x] : 0.f;
@@ -1028,7 +1097,8 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           if (p.slot >= 0) {
 #pragma unroll
             for (int u = 0; u < 16; ++u)
-              if (lives && r0 + u < rows) part_o[(r0 + u) * DV + d] = __uint_as_float(o[u]);
+              if (lives && r0 + u < rows)
+                part_o[(r0 + u) * DV + d] = E4M3 ? ldexp2f(__uint_as_float(o[u]), vexp) : __uint_as_float(o[u]);
           } else {
             // two neighbouring lanes trade, and each writes two dimensions of a row
             const int odd = lane & 1;
@@ -1047,6 +1117,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
       }
       tc::fence_before_sync();
+      buf ^= 1;
       named_bar(1, kSoftThreads);  // the next part may write factors and places
     }
   }
@@ -1068,6 +1139,7 @@ __global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
   __shared__ float s_m[kGroups], s_l[kGroups];
   griddep_wait();
   griddep_trigger();
+  const int kRows = a.tile_rows;
   const int rt = blockIdx.x % a.gtiles, seg = blockIdx.x / a.gtiles, b = seg / a.c.Hkv, hkv = seg % a.c.Hkv;
   const int row0 = rt * kRows, rows = min(kRows, a.rows - row0);
   const int d4 = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
@@ -1161,19 +1233,23 @@ __global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
 
 namespace {
 
-int draft_gtiles(const moe_draft_dims& d, int Hkv) { return cdiv(d.n * (d.Hq / Hkv), kRows); }
-// Columns times row tiles at most, whatever the shape.
-int draft_slots(int gtiles) { return std::max(2 * num_sms(), gtiles); }
+// Partial results of a call: two per CTA of one wave, counted in 64 rows (a CTA
+// of 128 rows has an SM for itself).
+size_t draft_slots(const moe_draft_dims& d, int Hkv) {
+  return 2 * (size_t)std::max(2 * num_sms(), 2 * cdiv(d.n * (d.Hq / Hkv), 128));
+}
 
-template <int DK, int DV, bool LATENT, bool E4M3, bool TMA>
+template <int DK, int DV, bool LATENT, bool E4M3, bool TMA, int ROWS>
 cudaError_t launch_draft(DraftArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  using S = DraftShape<DK, DV, LATENT, E4M3, TMA>;
-  cudaError_t err = ensure_smem((const void*)k_draft_attention<DK, DV, LATENT, E4M3, TMA>, S::kSmem);
+  using S = DraftShape<DK, DV, LATENT, E4M3, TMA, ROWS>;
+  cudaError_t err = ensure_smem((const void*)k_draft_attention<DK, DV, LATENT, E4M3, TMA, ROWS>, S::kSmem);
   if (err != cudaSuccess) return err;
+  a.tile_rows = ROWS;
+  a.gtiles = cdiv(a.rows, ROWS);
   const long long tiles = (std::min((long long)a.d.table_width * a.c.page_size, kMaxTokens) + kTile - 1) / kTile + 1;
   const long long units = (long long)a.d.B * a.c.Hkv * (tiles + kSegCost);
   a.cols = (int)std::max(1ll, std::min<long long>(S::kCtas * num_sms() / a.gtiles, units));
-  err = launch_k(k_draft_attention<DK, DV, LATENT, E4M3, TMA>, dim3(a.cols * a.gtiles), dim3(S::kWarps * 32),
+  err = launch_k(k_draft_attention<DK, DV, LATENT, E4M3, TMA, ROWS>, dim3(a.cols * a.gtiles), dim3(S::kWarps * 32),
                  S::kSmem, s, true, kmap, vmap, a);
   if (err != cudaSuccess) return err;
   // many parts per segment: as many of a row's as a CTA's registers hold at
@@ -1181,9 +1257,9 @@ cudaError_t launch_draft(DraftArgs& a, const CUtensorMap& kmap, const CUtensorMa
   // against 79.9 with the other form; 32 trees of 16, E4M3: 104.5 against 113.8)
   const int segs = a.d.B * a.c.Hkv * a.gtiles;
   if (a.cols >= 8 * a.d.B * a.c.Hkv)
-    return launch_k(k_draft_join<DV, 512, 8>, dim3(segs, std::min(kRows, cdiv(4 * num_sms(), segs))), dim3(512), 0, s,
+    return launch_k(k_draft_join<DV, 512, 8>, dim3(segs, std::min(ROWS, cdiv(4 * num_sms(), segs))), dim3(512), 0, s,
                     true, a);
-  return launch_k(k_draft_join<DV, 256, 4>, dim3(segs, std::min(kRows, std::max(8, cdiv(4 * num_sms(), segs)))),
+  return launch_k(k_draft_join<DV, 256, 4>, dim3(segs, std::min(ROWS, std::max(ROWS / 8, cdiv(4 * num_sms(), segs)))),
                   dim3(256), 0, s, true, a);
 }
 
@@ -1202,8 +1278,11 @@ cudaError_t launch_draft(DraftArgs& a, cudaStream_t s) {
     boxes = make_cache_map(&kmap, a.c.k, E4M3, DK, extents, strides, a.box) == cudaSuccess &&
             (LATENT || make_cache_map(&vmap, a.c.v, E4M3, DV, extents, strides, a.box) == cudaSuccess);
   }
-  return boxes ? launch_draft<DK, DV, LATENT, E4M3, true>(a, kmap, vmap, s)
-               : launch_draft<DK, DV, LATENT, E4M3, false>(a, kmap, vmap, s);
+  // more than 64 rows go through the cache once, not twice
+  if constexpr (!LATENT && DK <= 128)
+    if (boxes && a.rows > 64) return launch_draft<DK, DV, LATENT, E4M3, true, 128>(a, kmap, vmap, s);
+  return boxes ? launch_draft<DK, DV, LATENT, E4M3, true, 64>(a, kmap, vmap, s)
+               : launch_draft<DK, DV, LATENT, E4M3, false, 64>(a, kmap, vmap, s);
 }
 
 }  // namespace
@@ -1214,9 +1293,7 @@ bool draft_attention_fits(const moe_draft_dims& d, const moe_kv_cache& c) {
 }
 
 size_t draft_attention_workspace(const moe_draft_dims& d, int Hkv, int DV) {
-  const int gtiles = draft_gtiles(d, Hkv);
-  const size_t slots = 2 * (size_t)draft_slots(gtiles);
-  return slots * kRows * ((size_t)DV + 2) * sizeof(float) + (size_t)d.B * Hkv * sizeof(int2);
+  return draft_slots(d, Hkv) * 64 * ((size_t)DV + 2) * sizeof(float) + (size_t)d.B * Hkv * sizeof(int2);
 }
 
 cudaError_t launch_draft_attention(const uint16_t* q, const moe_kv_cache& cache, bool latent,
@@ -1234,12 +1311,11 @@ cudaError_t launch_draft_attention(const uint16_t* q, const moe_kv_cache& cache,
   a.d = d;
   a.G = d.Hq / cache.Hkv;
   a.rows = d.n * a.G;
-  a.gtiles = draft_gtiles(d, cache.Hkv);
   a.out = out;
   a.part_o = static_cast<float*>(ws);
-  const size_t slots = 2 * (size_t)draft_slots(a.gtiles);
-  a.part_ml = a.part_o + slots * kRows * DV;
-  a.info = reinterpret_cast<int2*>(a.part_ml + slots * 2 * kRows);
+  const size_t slots = draft_slots(d, cache.Hkv);
+  a.part_ml = a.part_o + slots * 64 * DV;
+  a.info = reinterpret_cast<int2*>(a.part_ml + slots * 2 * 64);
   a.status = status;
   // t / page_size for 0 <= t < 2^31: with 2^(e-1) < page_size <= 2^e and mul =
   // ceil(2^(31+e) / page_size) < 2^32, floor(t mul / 2^(31+e)) is exact

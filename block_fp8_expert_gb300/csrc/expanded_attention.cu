@@ -59,32 +59,6 @@ __device__ __forceinline__ Seq seq_of(const ExpandedArgs& a, int b, bool* bad = 
   return s;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n .reg .b64 A, B, C, R;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n mov.b64 C, {%6, %7};\n"
-      " fma.rn.f32x2 R, A, B, C;\n mov.b64 {%0, %1}, R;\n}\n"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n .reg .b64 A, B, R;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n add.rn.f32x2 R, A, B;\n"
-      " mov.b64 {%0, %1}, R;\n}\n"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-
-__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t v) {
-  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
-}
-
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -352,8 +326,8 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           role_wait(dead, &sh.full[k % kSlots], (uint32_t)((k / kSlots) & 1), a.status);
           for (int e = tid; e < kSlot / 16; e += kSoftWarps * 32) {
             const uint4 w = *reinterpret_cast<const uint4*>(chunk[c] + e * 16);
-            odd |= bf16x2_nonfinite(w.x) || bf16x2_nonfinite(w.y) || bf16x2_nonfinite(w.z) ||
-                   bf16x2_nonfinite(w.w);
+            odd |= nonfinite_16x2<false>(w.x) || nonfinite_16x2<false>(w.y) || nonfinite_16x2<false>(w.z) ||
+                   nonfinite_16x2<false>(w.w);
           }
         }
         if (bar_any(1, kSoftWarps * 32, odd)) {

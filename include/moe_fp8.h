@@ -604,8 +604,10 @@ typedef struct {
  * not reach it, whatever it is (NaN and infinities included).
  * The cache's length splits over the GPU and the parts are joined in a fixed
  * order, so equal calls give equal bits.  Scores, maxima, sums and outputs are
- * fp32; the softmax weights (E4M3: times the value's scale) enter the product
- * with the values as two bf16 parts, 2^-16 of the weight.  A page number
+ * fp32; the softmax weights enter the product with the values as two bf16 parts
+ * next to bf16 values (2^-15 of the weight), times the value's scale and rounded
+ * to fp16 next to E4M3 values (2^-11; the scales' largest and smallest may lie
+ * 2^24 apart without loss).  A page number
  * outside [0, pages), a length outside [0, table_width * page_size] or a
  * draft_lens[b] outside [0, min(n, seq_lens[b])] raises MOE_DEV_BAD_PAGE; the
  * tokens of such a page are left out, and such a length is clamped.

@@ -3,10 +3,15 @@ LatentAttention over latent vectors) against their formula in float64.
 
 Tolerances count the roundings: U16 = 2^-8 is the largest relative error of one
 rounding to bf16.  The softmax weights p, rounded by at most u (two bf16 parts:
-2^-15; one, summed as rounded: U16), move a normalised output by at most u (A +
+2^-15; one fp16 part, next to E4M3 values: 2^-11; one bf16 part, summed as
+rounded, next to latent vectors: U16), move a normalised output by at most u (A +
 |out|), A = sum p |v| / sum p.  A score's fp32 error e (a sum of `size` products
 that may truncate each addition, 2^-23 of the sum of magnitudes each, and 2^-20
 for the exponent's own) moves it by 2 e A, the sum over t tokens by t 2^-23 A.
+An fp16 weight below 2^-14 is rounded by 2^-25: they are held times 2^12 of the
+row's largest weight (which is at least 1 there, and their sum with it), over the
+largest scale's exponent, so t of them move an output by t 2^-37 of the largest
+scale times the largest code.
 """
 import math
 
@@ -123,7 +128,7 @@ class Batch:
         B, G = len(self.lens), self.Hq // self.Hkv
         out = torch.zeros(B, self.n, self.Hq, self.Dv, dtype=torch.float64, device="cuda")
         tol = torch.zeros_like(out)
-        u = U16 if self.kind == "latent" else 2.0 ** -15
+        u = {"latent": U16, "e4m3": 2.0 ** -11, "bf16": 2.0 ** -15}[self.kind]
         for b in range(B):
             if not self.lens[b]:
                 continue
@@ -142,6 +147,10 @@ class Batch:
                     out[b, i, h * G:(h + 1) * G] = o
                     tol[b, i, h * G:(h + 1) * G] = (U16 * o.abs() + u * (A + o.abs())
                                                    + (2 * e + len(t) * 2.0 ** -23) * A) * 1.01 + 1e-30
+                    if self.kind == "e4m3":
+                        page, off = self.table[b].long()[t // self.ps], t % self.ps
+                        top = self.vs[page, h, off].double().max() * self.v[page, h, off].double().abs().max()
+                        tol[b, i, h * G:(h + 1) * G] += len(t) * 2.0 ** -37 * top
         return out, tol
 
     def run(self, mask="own", window=0, **kw):
@@ -241,6 +250,33 @@ def test_division(torch, lens, kind):
     b.lens, b.drafts = [lens[i] for i in pick], [min(n, lens[i]) for i in pick]
     b.table, b.q, b.mask = b.table[pick], b.q[pick], b.mask[pick]
     _close(torch, got[pick], *b.reference())
+
+
+@pytest.mark.parametrize("kind,n,Hq,Hkv,D", [("bf16", 16, 8, 1, 128), ("e4m3", 16, 8, 1, 128), ("e4m3", 4, 8, 1, 128),
+                                             ("bf16", 3, 8, 2, 64), ("e4m3", 16, 16, 2, 64), ("e4m3", 5, 4, 1, 256),
+                                             ("latent", 2, 20, 1, 512), ("latent", 1, 64, 1, 256)])
+def test_maxima_that_move_in_every_tile(torch, kind, n, Hq, Hkv, D):
+    """Keys that grow along long ragged sequences: every tile moves the maxima and
+    rescales what is there, the last tile of each part of a sequence among them."""
+    lens = [700 + 331 * (i * 7 % 11) for i in range(40)]
+    Dk, Dv = (D + 64, D) if kind == "latent" else (D, D)
+    b = Batch(torch, lens, [n] * 40, n, Hq, Hkv, Dk, Dv, 16, kind, spread=2.0)
+    for s, length in enumerate(lens):
+        t = torch.arange(length, device="cuda")
+        page, off = b.table[s].long()[t // 16], t % 16
+        grow = 0.05 + t / 1500.0
+        if kind == "latent":
+            b.data[page, off] = (b.data[page, off].float() * grow.unsqueeze(1)).to(torch.bfloat16)
+        elif kind == "bf16":
+            b.k[page, :, off] = (b.k[page, :, off].float() * grow.view(-1, 1, 1)).to(torch.bfloat16)
+        else:
+            b.ks[page, :, off] *= grow.unsqueeze(1)
+            b.vs[page, :, off] *= grow.unsqueeze(1)
+    if kind != "latent":
+        b.scale = b.op.scale = 3.0 / math.sqrt(D)
+    got = [b.run() for _ in range(3)]
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    _close(torch, got[0], *b.reference())
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "latent"])
