@@ -319,10 +319,11 @@ __device__ __forceinline__ uint4 e4m3x8_to_f16(uint32_t lo, uint32_t hi) {
 }
 // Next to E4M3 codes the products are of fp16.  Weights times their value's scale
 // are held as w 2^(kWTop - e), e the exponent of the largest scale so far; as a
-// maximum moves here once it is exceeded four times (kHalfSlack), they stay below
-// 2^15, and fp16 keeps eleven bits down to 2^-26 of the largest, and steps of
-// 2^-36 of it below.
-constexpr float kWTop = 12.f, kHalfSlack = 2.f;
+// maximum moves here once it is exceeded by 2^5 (kHalfSlack), they stay below 2^15,
+// and fp16 keeps eleven bits down to 2^-23 of the largest, and steps of 2^-33 of
+// it below.  (Less slack keeps more of them, but maxima of 128 rows then move in
+// half of the tiles: 32 trees of 16: 83.1 us with 2^2.)
+constexpr float kWTop = 9.f, kHalfSlack = 5.f;
 constexpr int kExpMin = -120, kExpMax = 120;
 // The exponent of a scale, for the largest (what is not finite counts as none).
 __device__ __forceinline__ int scale_exp(float v) {
@@ -922,9 +923,10 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         if (i == 0) {  // the products are added to zeros
           const uint32_t zero[16] = {};
 #pragma unroll 1
-          for (int mb = half; mb < S::kBlocks; mb += S::kSplit)
+          for (int mb = 0; mb < S::kBlocks; ++mb)
 #pragma unroll 1
-            for (int r0 = 0; r0 < npad; r0 += 16) st_32x32b_x16(quadrant + kOCol + mb * kRows + r0, zero);
+            for (int r0 = 16 * half; r0 < npad; r0 += 16 * S::kSplit)
+              st_32x32b_x16(quadrant + kOCol + mb * kRows + r0, zero);
           tc::wait_st();
         }
         if (moved) {
@@ -940,9 +942,9 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           named_bar(1, kSoftThreads);  // (before the halves' tops are written again, too)
           if (i > 0) {
 #pragma unroll 1
-            for (int mb = half; mb < S::kBlocks; mb += S::kSplit)
+            for (int mb = 0; mb < S::kBlocks; ++mb)
 #pragma unroll 1
-              for (int r0 = 0; r0 < npad; r0 += 16) {
+              for (int r0 = 16 * half; r0 < npad; r0 += 16 * S::kSplit) {
                 uint32_t o[16];
                 const uint32_t at = quadrant + kOCol + mb * kRows + r0;
                 ld_32x32b_x16(at, o);
@@ -1016,10 +1018,10 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           }
           if (bar_any(1, kSoftThreads, odd)) {
 #pragma unroll 1
-            for (int mb = half; mb < S::kBlocks; mb += S::kSplit) {
+            for (int mb = 0; mb < S::kBlocks; ++mb) {
               const int d = DV >= 128 ? mb * 128 + 32 * quad + lane : 16 * quad + (lane & 15);
 #pragma unroll 1
-              for (int r0 = 0; r0 < npad; r0 += 16) {
+              for (int r0 = 16 * half; r0 < npad; r0 += 16 * S::kSplit) {
                 uint32_t o[16];
                 const uint32_t at = quadrant + kOCol + mb * kRows + r0;
                 ld_32x32b_x16(at, o);
@@ -1087,10 +1089,10 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       float* const part_o = a.part_o + slot * kRows * DV;
       const bool lives = DV >= 128 || lane < 16;
 #pragma unroll 1
-      for (int mb = half; mb < S::kBlocks; mb += S::kSplit) {
+      for (int mb = 0; mb < S::kBlocks; ++mb) {
         const int d = DV >= 128 ? mb * 128 + 32 * quad + lane : 16 * quad + (lane & 15);
 #pragma unroll 1
-        for (int r0 = 0; r0 < npad; r0 += 16) {
+        for (int r0 = 16 * half; r0 < npad; r0 += 16 * S::kSplit) {
           uint32_t o[16];
           ld_32x32b_x16(quadrant + kOCol + mb * kRows + r0, o);
           tc::wait_ld();
@@ -1149,9 +1151,9 @@ __global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
   if (bad && threadIdx.x == 0 && blockIdx.y == 0 && hkv == 0 && rt == 0) raise_status(a.status, MOE_DEV_BAD_PAGE);
   if (!sp.tiles) info = make_int2(0, 0);
   if (info.y == 1) return;  // its column has written it
-  // as many threads for a row as it takes to have all of its parts on their way
+  // enough threads for a row to fetch its parts in four rounds
   int shares = 1;
-  while (shares < kGroups && shares * kAhead < info.y) shares *= 2;
+  while (shares < kGroups && shares * 4 * kAhead < info.y) shares *= 2;
   const int at_once = kGroups / shares, mine = grp % shares;
   for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
     const int r = r0 + grp / shares, R = row0 + r, n = R / a.G;
@@ -1259,8 +1261,7 @@ cudaError_t launch_draft(DraftArgs& a, const CUtensorMap& kmap, const CUtensorMa
   if (a.cols >= 8 * a.d.B * a.c.Hkv)
     return launch_k(k_draft_join<DV, 512, 8>, dim3(segs, std::min(ROWS, cdiv(4 * num_sms(), segs))), dim3(512), 0, s,
                     true, a);
-  return launch_k(k_draft_join<DV, 256, 4>, dim3(segs, std::min(ROWS, std::max(ROWS / 8, cdiv(4 * num_sms(), segs)))),
-                  dim3(256), 0, s, true, a);
+  return launch_k(k_draft_join<DV, 256, 4>, dim3(segs, ROWS / (1024 / DV)), dim3(256), 0, s, true, a);
 }
 
 // A cache of pages that tile boxes divide is copied by maps of [pages, heads,

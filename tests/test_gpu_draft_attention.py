@@ -8,9 +8,9 @@ rounded, next to latent vectors: U16), move a normalised output by at most u (A 
 |out|), A = sum p |v| / sum p.  A score's fp32 error e (a sum of `size` products
 that may truncate each addition, 2^-23 of the sum of magnitudes each, and 2^-20
 for the exponent's own) moves it by 2 e A, the sum over t tokens by t 2^-23 A.
-An fp16 weight below 2^-14 is rounded by 2^-25: they are held times 2^12 of the
+An fp16 weight below 2^-14 is rounded by 2^-25: they are held times 2^9 of the
 row's largest weight (which is at least 1 there, and their sum with it), over the
-largest scale's exponent, so t of them move an output by t 2^-37 of the largest
+largest scale's exponent, so t of them move an output by t 2^-34 of the largest
 scale times the largest code.
 """
 import math
@@ -150,7 +150,7 @@ class Batch:
                     if self.kind == "e4m3":
                         page, off = self.table[b].long()[t // self.ps], t % self.ps
                         top = self.vs[page, h, off].double().max() * self.v[page, h, off].double().abs().max()
-                        tol[b, i, h * G:(h + 1) * G] += len(t) * 2.0 ** -37 * top
+                        tol[b, i, h * G:(h + 1) * G] += len(t) * 2.0 ** -34 * top
         return out, tol
 
     def run(self, mask="own", window=0, **kw):
