@@ -16,15 +16,17 @@ namespace {
 using namespace attn;
 
 constexpr int kNope = 128, kRope = 64, kVd = 128;
-constexpr int kBlock = 128;         // rows of a query tile, tokens of a key tile
-constexpr int kSlot = kBlock * 128;  // 128 rows or tokens x 64 dimensions, 128-byte swizzled
+constexpr int kBlock = 128;         // rows of a query tile
+constexpr int kKeys = 64;           // tokens of a key tile
+constexpr int kQChunk = kBlock * 128, kSlot = kKeys * 128;  // rows or tokens x 64 dimensions, 128-byte swizzled
 constexpr int kQChunks = (kNope + kRope) / 64, kVChunks = kVd / 64;
-constexpr int kSlots = 8;           // of the ring of keys and values: 5 per tile
-constexpr int kPerTile = kQChunks + kVChunks;
+constexpr int kStages = 3;          // tiles of keys, and of values, in shared memory
+constexpr int kKBytes = kQChunks * kSlot, kVBytes = kVChunks * kSlot;
 constexpr int kSoftWarps = 8;       // four per query tile
-constexpr int kThreads = (kSoftWarps + 3) * 32;  // then a warp per query tile for its MMAs, one for the loads
-constexpr int kSmem = (2 * kQChunks + kSlots) * kSlot + 1024;
-constexpr int kOCol = 2 * kBlock;   // TMEM: the two tiles' scores (then weights), then their outputs
+constexpr int kThreads = (kSoftWarps + 3) * 32;  // then one per query tile for its MMAs, one for the loads
+constexpr int kSmem = 2 * kQChunks * kQChunk + kStages * (kKBytes + kVBytes) + 1024;
+// TMEM: two buffers of scores (then weights) per query tile, then their outputs
+constexpr int kOCol = 4 * kKeys;
 
 struct ExpandedArgs {
   const int32_t* cu_q;
@@ -37,10 +39,10 @@ struct ExpandedArgs {
 };
 
 struct ExpandedShared {
-  uint64_t q_full[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], turn[2];
+  uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2];
   uint32_t tmem_base;
   volatile int abort_flag;
-  int add_to[2];  // the tile's products are added to what the outputs hold
   int seq, blk;
 };
 
@@ -70,18 +72,22 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                    ~(uintptr_t)1023);
-  uint8_t* const ring = smem + 2 * kQChunks * kSlot;
+  uint8_t* const sm_k = smem + 2 * kQChunks * kQChunk;
+  uint8_t* const sm_v = sm_k + kStages * kKBytes;
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 2);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 2);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 2);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sh.q_full[x], 1);
-      mbar_init(&sh.s_full[x], 1);
-      mbar_init(&sh.p_full[x], kSoftWarps / 2);
-      mbar_init(&sh.o_full[x], 1);
-      mbar_init(&sh.turn[x], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sh.s_full[x][b], 1);
+        mbar_init(&sh.p_full[x][b], kSoftWarps / 2);
+      }
+      mbar_init(&sh.pv_done[x], 1);
     }
     sh.abort_flag = 0;
     fence_mbar_init();
@@ -137,107 +143,106 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   auto tiles_of = [&](int x) {
     const int r0 = row0 + x * kBlock;
     if (!any || r0 >= s.lq) return 0;
-    return cdiv(max(0, min(r0 + kBlock, s.lq) + off), kBlock);
+    return cdiv(max(0, min(r0 + kBlock, s.lq) + off), kKeys);
   };
   const int nt[2] = {tiles_of(0), tiles_of(1)}, n = max(nt[0], nt[1]);
 
   if (warp == kSoftWarps + 2) {
-    // ---- loads, by one thread: queries, then a ring of keys and values
-    int i = 0;
+    // ---- loads, by one thread: queries, then the next tile's keys and this one's
+    // values in turn, as scores are made ahead
     if (tc::elect_one()) {
       for (int x = 0; x < 2; ++x)
         if (nt[x] > 0) {
-          mbar_arrive_expect_tx(&sh.q_full[x], kQChunks * kSlot);
+          mbar_arrive_expect_tx(&sh.q_full[x], kQChunks * kQChunk);
           for (int c = 0; c < kQChunks; ++c)
-            tma_load_3d(smem + (x * kQChunks + c) * kSlot, &qmap, 64 * c, h, s.q0 + row0 + x * kBlock,
+            tma_load_3d(smem + (x * kQChunks + c) * kQChunk, &qmap, 64 * c, h, s.q0 + row0 + x * kBlock,
                         &sh.q_full[x]);
         }
-      for (int j = 0; j < n; ++j) {
-        const int t = s.k0 + j * kBlock;
-#pragma unroll
-        for (int c = 0; c < kPerTile; ++c) {
-          const int k = i + c, slot = k % kSlots;
-          if (k >= kSlots) lane_wait(dead, &sh.empty[slot], (uint32_t)((k / kSlots - 1) & 1), a.status);
+      for (int j = -1; j < n && !*dead; ++j) {
+        if (const int k = j + 1, st = k % kStages; k < n) {
+          if (k >= kStages) lane_wait(dead, &sh.k_empty[st], (uint32_t)((k / kStages - 1) & 1), a.status);
           if (*dead) break;
-          mbar_arrive_expect_tx(&sh.full[slot], kSlot);
-          if (c < 2)
-            tma_load_3d(ring + slot * kSlot, &kmap, 64 * c, h, t, &sh.full[slot]);
-          else if (c == 2)
-            tc::tma_load_2d(ring + slot * kSlot, &rmap, 0, t, &sh.full[slot]);
-          else
-            tma_load_3d(ring + slot * kSlot, &vmap, 64 * (c - 3), h, t, &sh.full[slot]);
+          mbar_arrive_expect_tx(&sh.k_full[st], kKBytes);
+          uint8_t* to = sm_k + st * kKBytes;
+          for (int c = 0; c < 2; ++c)
+            tma_load_3d(to + c * kSlot, &kmap, 64 * c, h, s.k0 + k * kKeys, &sh.k_full[st]);
+          tc::tma_load_2d(to + 2 * kSlot, &rmap, 0, s.k0 + k * kKeys, &sh.k_full[st]);
         }
-        if (*dead) break;
-        i += kPerTile;
+        if (j >= 0) {
+          const int st = j % kStages;
+          if (j >= kStages) lane_wait(dead, &sh.v_empty[st], (uint32_t)((j / kStages - 1) & 1), a.status);
+          if (*dead) break;
+          mbar_arrive_expect_tx(&sh.v_full[st], kVBytes);
+          for (int c = 0; c < kVChunks; ++c)
+            tma_load_3d(sm_v + st * kVBytes + c * kSlot, &vmap, 64 * c, h, s.k0 + j * kKeys, &sh.v_full[st]);
+        }
+      }
+      // every copy has landed and been read before the CTA's memory goes
+      for (int j = max(0, n - kStages); j < n; ++j) {
+        const int st = j % kStages;
+        const uint32_t parity = (uint32_t)((j / kStages) & 1);
+        mbar_wait(&sh.k_full[st], parity);
+        mbar_wait(&sh.v_full[st], parity);
+        if (!*dead) {
+          mbar_wait(&sh.k_empty[st], parity);
+          mbar_wait(&sh.v_empty[st], parity);
+        }
       }
     }
     __syncwarp();
-    i = __reduce_max_sync(kAll, (unsigned)i);
-    // every copy has landed and been read before the CTA's memory goes
-    if (lane == 0)
-      for (int k = max(0, i - kSlots); k < i; ++k) {
-        mbar_wait(&sh.full[k % kSlots], (uint32_t)((k / kSlots) & 1));
-        if (!*dead) mbar_wait(&sh.empty[k % kSlots], (uint32_t)((k / kSlots) & 1));
-      }
-    __syncwarp();
   } else if (warp >= kSoftWarps) {
     // ---- the products, a warp per query tile: O += P V of a key tile, then S = Q
-    // K^T of the next (which overwrites the weights P).  The warps take turns, so
-    // that one tile's products run while the other's softmax does, and each has
-    // made its checks before its turn comes: MMAs that wait for the checks of the
-    // warp that issues them leave the tensor cores idle for 500 cycles a time.
+    // K^T of the next but one, into the buffer of the weights P
     const int x = warp - kSoftWarps;
-    const uint32_t q0 = desc_k(smem_u32(smem) + x * kQChunks * kSlot), r0 = smem_u32(ring);
-    const uint32_t t_s = tmem + x * kBlock, t_o = tmem + kOCol + x * kVd;
-    constexpr uint32_t idesc_s = idesc_bf16(kBlock, kBlock, false, false);
+    const uint32_t q0 = desc_k(smem_u32(smem) + x * kQChunks * kQChunk);
+    const uint32_t kd = desc_k(smem_u32(sm_k)), vd = desc_mn(smem_u32(sm_v), 0);
+    const uint32_t t_s = tmem + 2 * x * kKeys, t_o = tmem + kOCol + x * kVd;
+    constexpr uint32_t idesc_s = idesc_bf16(kBlock, kKeys, false, false);
     constexpr uint32_t idesc_o = idesc_bf16(kBlock, 64, false, true);
     if (nt[x] > 0) role_wait(dead, &sh.q_full[x], 0, a.status);
-    for (int j = -1; j < n; ++j) {
-      const uint32_t v0 = uniform((j * kPerTile + kQChunks) % kSlots);  // the values' first slot
-      const uint32_t k0 = uniform((j + 1) * kPerTile % kSlots);         // the next keys'
-      // (slots that it does not read are given back no sooner either)
-      if (j + 1 < n)
-        for (int i = (j + 1) * kPerTile; i < (j + 1) * kPerTile + kQChunks; ++i)
-          role_wait(dead, &sh.full[i % kSlots], (uint32_t)((i / kSlots) & 1), a.status);
+    for (int j = -2; j < n; ++j) {
+      const int kj = j + 2, jv = max(j, 0);  // the tile whose scores are made, and whose values are added
+      const int vs = jv % kStages, ks = kj % kStages;
+      const uint32_t u = uniform(vs | ks << 4 | (j & 1) << 8);
+      // (a stage that it does not read is given back no sooner either; what there
+      // is none of is a wait for what has been waited for)
+      const bool pv = j >= 0 && j < nt[x];
+      uint64_t* const kb = &sh.k_full[kj < n ? ks : (n - 1) % kStages];
+      const uint32_t kp = (uint32_t)(((kj < n ? kj : n - 1) / kStages) & 1);
       if (j >= 0) {
-        for (int i = j * kPerTile + kQChunks; i < (j + 1) * kPerTile; ++i)
-          role_wait(dead, &sh.full[i % kSlots], (uint32_t)((i / kSlots) & 1), a.status);
-        if (j < nt[x]) role_wait(dead, &sh.p_full[x], (uint32_t)(j & 1), a.status);
+        uint64_t* const vb = &sh.v_full[vs];
+        const uint32_t vp = (uint32_t)((jv / kStages) & 1);
+        role_wait3(dead, kb, kp, vb, vp, pv ? &sh.p_full[x][j & 1] : vb, pv ? (uint32_t)((j / 2) & 1) : vp, a.status);
+      } else if (kj < n) {
+        role_wait(dead, kb, kp, a.status);
       }
-      const uint32_t add = uniform(sh.add_to[x]);
-      if (x == 1 || j >= 0) role_wait(dead, &sh.turn[x], (uint32_t)((j + x) & 1), a.status);
       tc::fence_after_sync();
-      if (tc::elect_one()) {
-        if (!*dead) {
-          if (j >= 0) {
-            if (j < nt[x]) {
+      const uint32_t uv = u & 15, uk = u >> 4 & 15, buf = u >> 8;
+      if (tc::elect_one() && !*dead) {
+        if (j >= 0) {
+          if (pv) {
 #pragma unroll
-              for (int c = 0; c < kVChunks; ++c) {
-                const uint32_t v = desc_mn(r0 + (v0 + c) % kSlots * kSlot, 0);
+            for (int c = 0; c < kVChunks; ++c)
 #pragma unroll
-                for (int kk = 0; kk < kBlock / 16; ++kk)
-                  mma_ts(t_o + 64 * c, t_s + 8 * kk, v + kk * 128, idesc_o, add | (kk ? 1u : 0u));
-              }
-              if (j == nt[x] - 1) tc::commit(&sh.o_full[x]);
-            }
-#pragma unroll
-            for (int c = 0; c < kVChunks; ++c) tc::commit(&sh.empty[(v0 + c) % kSlots]);
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_ts(t_o + 64 * c, t_s + buf * kKeys + 8 * kk, vd + (uv * kVBytes + c * kSlot + kk * 2048) / 16,
+                       idesc_o, 1u);
+            tc::commit(&sh.pv_done[x]);
           }
-          if (j + 1 < n) {
-            if (j + 1 < nt[x]) {
-#pragma unroll
-              for (int c = 0; c < kQChunks; ++c) {
-                const uint32_t k = desc_k(r0 + (k0 + c) % kSlots * kSlot), q = q0 + c * (kSlot / 16);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_ss(t_s, q + 2 * kk, k + 2 * kk, idesc_s, c | kk ? 1u : 0u);
-              }
-              tc::commit(&sh.s_full[x]);
-            }
-#pragma unroll
-            for (int c = 0; c < kQChunks; ++c) tc::commit(&sh.empty[(k0 + c) % kSlots]);
-          }
+          tc::commit(&sh.v_empty[uv]);
         }
-        mbar_arrive(&sh.turn[x ^ 1]);
+        if (kj < n) {
+          if (kj < nt[x]) {
+#pragma unroll
+            for (int c = 0; c < kQChunks; ++c)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss(t_s + buf * kKeys, q0 + c * (kQChunk / 16) + 2 * kk, kd + (uk * kKBytes + c * kSlot) / 16 + 2 * kk,
+                       idesc_s, c | kk ? 1u : 0u);
+            tc::commit(&sh.s_full[x][buf]);
+          }
+          tc::commit(&sh.k_empty[uk]);
+        }
       }
       __syncwarp();
     }
@@ -245,37 +250,37 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     // ---- softmax.  A thread owns a row.
     const int x = warp >> 2, r = 32 * (warp & 3) + lane, i = row0 + x * kBlock + r;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t t_s = lanes + x * kBlock, t_o = lanes + kOCol + x * kVd;
+    const uint32_t t_s = lanes + 2 * x * kKeys, t_o = lanes + kOCol + x * kVd;
     const int limit = i < s.lq ? max(0, i + off + 1) : 0;  // keys that the row sees: the first ones
     // tiles that every row of the warp, or of the CTA, sees whole
-    const int whole = (i - lane < s.lq ? max(0, i - lane + off + 1) : s.lk) / kBlock;
-    const int whole_cta = max(0, row0 + off + 1) / kBlock;
+    const int whole = (i - lane < s.lq ? max(0, i - lane + off + 1) : s.lk) / kKeys;
+    const int whole_cta = max(0, row0 + off + 1) / kKeys;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
       const bool mine = j < nt[x];
-      bool add_to = j > 0;
-      float2 v[kBlock / 2];
+      const uint32_t t_p = t_s + (j & 1) * kKeys;
+      float2 v[kKeys / 2];
       if (mine) {
-        role_wait(dead, &sh.s_full[x], (uint32_t)(j & 1), a.status);
+        role_wait(dead, &sh.s_full[x][j & 1], (uint32_t)((j / 2) & 1), a.status);
         tc::fence_after_sync();
-        uint32_t raw[4][32];
+        uint32_t raw[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(t_s + 32 * c, raw[c]);
+        for (int c = 0; c < 2; ++c) tc::ld_32x32b_x32(t_p + 32 * c, raw[c]);
         tc::wait_ld();
 #pragma unroll
-        for (int c = 0; c < kBlock / 2; ++c)
+        for (int c = 0; c < kKeys / 2; ++c)
           v[c] = make_float2(__uint_as_float(raw[c / 16][2 * c % 32]), __uint_as_float(raw[c / 16][2 * c % 32 + 1]));
         if (j >= whole) {
-          const int left = limit - j * kBlock;
+          const int left = limit - j * kKeys;
 #pragma unroll
-          for (int c = 0; c < kBlock / 2; ++c) {
+          for (int c = 0; c < kKeys / 2; ++c) {
             if (2 * c >= left) v[c].x = -INFINITY;
             if (2 * c + 1 >= left) v[c].y = -INFINITY;
           }
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kBlock / 2; ++c) mx[c & 3] = max3(mx[c & 3], v[c].x, v[c].y);
+        for (int c = 0; c < kKeys / 2; ++c) mx[c & 3] = max3(mx[c & 3], v[c].x, v[c].y);
         const float top = a.scale2 * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));  // (scale > 0)
         // (-inf + slack is -inf: a row's first score moves its maximum)
         if (__any_sync(kAll, top > m + kMaxSlack)) {
@@ -283,7 +288,9 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           const float f = m == mn ? 1.f : exp2_fast(m - mn);
           l *= f;
           m = mn;
-          if (j > 0) {  // (the products of the tile before came before these scores)
+          if (j > 0) {
+            role_wait(dead, &sh.pv_done[x], (uint32_t)((j - 1) & 1), a.status);
+            tc::fence_after_sync();
 #pragma unroll 1
             for (int c = 0; c < kVd; c += 16) {
               uint32_t o[16];
@@ -296,19 +303,21 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             tc::wait_st();
           }
         }
+        if (j == 0) {  // the products are added to zeros
+          const uint32_t zero[16] = {};
+#pragma unroll 1
+          for (int c = 0; c < kVd; c += 16) st_32x32b_x16(t_o + c, zero);
+        }
         const float ms = m == -INFINITY ? 0.f : m;
         float2 sum = make_float2(0.f, 0.f);
+        uint32_t w[32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
-#pragma unroll
-          for (int u = 0; u < 32; ++u) {
-            const float2 e = fma2(v[32 * c + u], make_float2(a.scale2, a.scale2), make_float2(-ms, -ms));
-            w[u] = pack_bf16x2(exp2_fast(e.x), exp2_fast(e.y));
-            sum = add2(sum, make_float2(bf16_lo(w[u]), bf16_hi(w[u])));
-          }
-          tc::st_32x32b_x32(t_s + 32 * c, w);
+        for (int u = 0; u < 32; ++u) {
+          const float2 e = fma2(v[u], make_float2(a.scale2, a.scale2), make_float2(-ms, -ms));
+          w[u] = pack_bf16x2(exp2_fast(e.x), exp2_fast(e.y));
+          sum = add2(sum, make_float2(bf16_lo(w[u]), bf16_hi(w[u])));
         }
+        tc::st_32x32b_x32(t_p, w);
         l += sum.x + sum.y;
         tc::wait_st();
       }
@@ -321,9 +330,8 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         bool odd = false;
 #pragma unroll
         for (int c = 0; c < kVChunks; ++c) {
-          const int k = j * kPerTile + kQChunks + c;
-          chunk[c] = ring + (k % kSlots) * kSlot;
-          role_wait(dead, &sh.full[k % kSlots], (uint32_t)((k / kSlots) & 1), a.status);
+          chunk[c] = sm_v + j % kStages * kVBytes + c * kSlot;
+          if (c == 0) role_wait(dead, &sh.v_full[j % kStages], (uint32_t)((j / kStages) & 1), a.status);
           for (int e = tid; e < kSlot / 16; e += kSoftWarps * 32) {
             const uint4 w = *reinterpret_cast<const uint4*>(chunk[c] + e * 16);
             odd |= nonfinite_16x2<false>(w.x) || nonfinite_16x2<false>(w.y) || nonfinite_16x2<false>(w.z) ||
@@ -332,23 +340,21 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
         if (bar_any(1, kSoftWarps * 32, odd)) {
           if (mine) {
+            if (j > 0) role_wait(dead, &sh.pv_done[x], (uint32_t)((j - 1) & 1), a.status);
+            tc::fence_after_sync();
 #pragma unroll 1
             for (int d0 = 0; d0 < kVd; d0 += 16) {
               uint32_t o[16];
               ld_32x32b_x16(t_o + d0, o);
               tc::wait_ld();
-              if (j == 0) {
-#pragma unroll
-                for (int u = 0; u < 16; ++u) o[u] = 0u;
-              }
 #pragma unroll 1
-              for (int t = 0; t < kBlock; ++t) {
+              for (int t = 0; t < kKeys; ++t) {
                 const uint8_t* row = chunk[0] + (d0 >> 6) * (chunk[1] - chunk[0]);
 #pragma unroll
                 for (int u = 0; u < 16; ++u) {
                   const uint32_t w = *reinterpret_cast<const uint16_t*>(
                       row + tc::sw128_off(t, ((d0 + u) >> 3) & 7) + 2 * (u & 7));
-                  if ((w & 0x7F80u) == 0x7F80u && j * kBlock + t < limit)
+                  if ((w & 0x7F80u) == 0x7F80u && j * kKeys + t < limit)
                     o[u] = __float_as_uint(__uint_as_float(o[u]) + __uint_as_float(w << 16));
                 }
               }
@@ -365,23 +371,21 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             }
           tc::fence_proxy_async();
           named_bar(1, kSoftWarps * 32);  // none is left
-          add_to = true;
         }
       }
       if (mine) {
-        if ((tid & 127) == 0) sh.add_to[x] = add_to;
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[x]);
+        if (lane == 0) mbar_arrive(&sh.p_full[x][j & 1]);
       }
     }
     // ---- the rows' outputs, through the query tile's shared memory (whose last
     // product has been made), so that a row is written by neighbouring lanes
     const int r_warp = row0 + x * kBlock + 32 * (warp & 3);
     if (any && r_warp < s.lq) {
-      uint8_t* const stage = smem + x * kQChunks * kSlot + (warp & 3) * 32 * 2 * kVd;
+      uint8_t* const stage = smem + x * kQChunks * kQChunk + (warp & 3) * 32 * 2 * kVd;
       if (nt[x] > 0) {
-        role_wait(dead, &sh.o_full[x], 0, a.status);
+        role_wait(dead, &sh.pv_done[x], (uint32_t)((nt[x] - 1) & 1), a.status);
         tc::fence_after_sync();
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -439,11 +443,11 @@ cudaError_t launch_expanded_attention(const uint16_t* q, const uint16_t* k_nope,
   if (d.Tk == 0) k_nope = k_rope = v = q;
   if ((err = make_tensor_map_3d(&qmap, q, d.Tq, d.H, kNope + kRope, d.q_stride, d.q_head_stride, 64, kBlock)) !=
           cudaSuccess ||
-      (err = make_tensor_map_3d(&kmap, k_nope, Tk, d.H, kNope, d.k_stride, d.k_head_stride, 64, kBlock)) !=
+      (err = make_tensor_map_3d(&kmap, k_nope, Tk, d.H, kNope, d.k_stride, d.k_head_stride, 64, kKeys)) !=
           cudaSuccess ||
-      (err = make_tensor_map_2d(&rmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k_rope, Tk, kRope, 64, kBlock, 128,
+      (err = make_tensor_map_2d(&rmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k_rope, Tk, kRope, 64, kKeys, 128,
                                 d.rope_stride)) != cudaSuccess ||
-      (err = make_tensor_map_3d(&vmap, v, Tk, d.H, kVd, d.v_stride, d.v_head_stride, 64, kBlock)) != cudaSuccess)
+      (err = make_tensor_map_3d(&vmap, v, Tk, d.H, kVd, d.v_stride, d.v_head_stride, 64, kKeys)) != cudaSuccess)
     return err;
   if ((err = ensure_smem((const void*)k_expanded_attention, kSmem)) != cudaSuccess) return err;
   const ExpandedArgs a{cu_q, cu_k, d, (int)expanded_blocks(d), d.scale * kLog2e, out, status};
