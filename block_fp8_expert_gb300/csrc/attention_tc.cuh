@@ -234,7 +234,7 @@ static __device__ __noinline__ void role_wait_on(volatile int* abort_flag, uint6
 }
 __device__ __forceinline__ void role_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
                                           int32_t* status) {
-  if (!__all_sync(kAll, mbar_nap(bar, parity))) role_wait_on(abort_flag, bar, parity, status);
+  if (!__all_sync(kAll, mbar_try_wait(bar, parity))) role_wait_on(abort_flag, bar, parity, status);
 }
 
 // Three waits at once: a wait for what has long come still takes 180 cycles, which
