@@ -206,7 +206,8 @@ __device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned (*s_s
   const int per = cdiv(a.d.B, WARPS * 32), b0 = min(tid * per, a.d.B), b1 = min(b0 + per, a.d.B);
   if (a.d.B == 1 && Hkv <= a.cols) {  // every thread on its own
     Walk w{0, 0, 0, 0, 0, 0, col, 0, 1, span_of(a, 0)};
-    const int most = most_of(quotient(w.sp.tiles * Hkv + a.cols - 1, a.cols), 0);
+    const int each = quotient(a.cols, Hkv);  // columns of a head: no more parts than these
+    const int most = max(kMinTiles, quotient(w.sp.tiles + each - 1, each));
     w.parts = max(1, quotient(w.sp.tiles + most - 1, most));
     w.cur = quotient(col, w.parts);
     w.part = col - w.cur * w.parts;
@@ -217,7 +218,7 @@ __device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned (*s_s
   // Loops that stay loops: what runs once is paid for by the fetch of its code.
   Span span{0, 0, 0, 0, 0};  // of the last of this thread's sequences
   unsigned mine, before, total;
-  int most = 0, even = 0;
+  int most = 0, even = 0, turn = 0;
 #pragma unroll 1
   for (int i = -1; i <= kTries; ++i) {
     // i = -1: tiles; then parts with sizes to try; at last units
@@ -235,7 +236,7 @@ __device__ __forceinline__ Walk plan(const DraftArgs& a, int col, unsigned (*s_s
       const unsigned x = __shfl_up_sync(kAll, incl, o);
       if (lane >= o) incl += x;
     }
-    unsigned* const s = s_scan[i & 1];
+    unsigned* const s = s_scan[turn ^= 1];  // (some of the sizes are skipped: not by i)
     if (lane == 31) s[warp] = incl;
     __syncthreads();
     const unsigned v = lane < WARPS ? s[lane] : 0;

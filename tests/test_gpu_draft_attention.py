@@ -252,6 +252,19 @@ def test_division(torch, lens, kind):
     _close(torch, got[pick], *b.reference())
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,D,tiles", [(1, 3, 3, 256, 101), (1, 5, 5, 256, 301), (2, 5, 5, 64, 121),
+                                              (1, 7, 7, 128, 131), (32, 64, 8, 128, 19), (2, 11, 11, 256, 29)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_one_sequence_whose_heads_do_not_divide_the_columns(torch, n, Hq, Hkv, D, tiles, kind):
+    """All of its parts have a column: the last head's last tokens are there, and
+    a call of other lengths before it leaves nothing behind."""
+    for t in (tiles, tiles + 1, tiles - 2):
+        b = Batch(torch, [64 * t - 3], [n], n, Hq, Hkv, D, D, 64, kind, seed=t)
+        ws = b.op.workspace(1, n)
+        ws.fill_(0x7f)
+        _close(torch, b.run(ws=ws), *b.reference())
+
+
 @pytest.mark.parametrize("kind,n,Hq,Hkv,D", [("bf16", 16, 8, 1, 128), ("e4m3", 16, 8, 1, 128), ("e4m3", 4, 8, 1, 128),
                                              ("bf16", 3, 8, 2, 64), ("e4m3", 16, 16, 2, 64), ("e4m3", 5, 4, 1, 256),
                                              ("latent", 2, 20, 1, 512), ("latent", 1, 64, 1, 256)])
