@@ -303,7 +303,7 @@ struct DraftShared {
   float q_scale[2][E4M3 ? ROWS : 1];  // E4M3: of the rows' queries, this part's and the next one's
   union {
     float top[2][ROWS];  // the largest score of a row, by halves of the tile; after the last tile [1]: half of its sum
-    float inv[ROWS];     // after the last tile: 1 / the row's sum
+    float inv[ROWS];     // after the last tile: 1 / the row's sum, of a part's row what its weights were held at
   };
   union {
     unsigned scan[2][WARPS];
@@ -330,6 +330,13 @@ constexpr int kExpMin = -120, kExpMax = 120;
 __device__ __forceinline__ int scale_exp(float v) {
   const uint32_t bits = __float_as_uint(v) & 0x7fffffffu;
   return bits >= 0x7f800000u ? kExpMin : min(max((int)(bits >> 23) - 127, kExpMin), kExpMax);
+}
+// The same of the largest scale of the tokens that a row sees: what it does not
+// see takes no bits from its weights.
+__device__ __noinline__ int seen_exp(const float* scales, uint64_t seen) {
+  int top = kExpMin;
+  for (; seen; seen &= seen - 1) top = max(top, scale_exp(scales[__ffsll((long long)seen) - 1]));
+  return top;
 }
 
 }  // namespace
@@ -828,7 +835,11 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         l[x] = 0.f;
         qf[x] = scale2;
       }
-      int vexp = kExpMin;  // E4M3: the exponent that the weights are held at
+      // E4M3: the exponents that the rows' weights are held at, and what every
+      // row's is at least (the same in every thread)
+      int vexp[kX], vlow = kExpMin;
+#pragma unroll
+      for (int x = 0; x < kX; ++x) vexp[x] = kExpMin;
       for (int i = 0; i < p.n; ++i, ++j) {
         const int st = j % VST, t0 = (p.tile + i) * kTile;
         role_wait(dead, &sh.s_full[j & 1], (uint32_t)((j / 2) & 1), a.status);
@@ -909,15 +920,11 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           above |= mx[x] > m[x] + (E4M3 ? kHalfSlack : kMaxSlack);  // (a row's first score moves its maximum from -inf)
         }
         bool moved = bar_any(1, kSoftThreads, above);
-        float vmove = 1.f;
+        int tile_top = kExpMin;
         if (E4M3) {
           role_wait(dead, &sh.full[st][NP - 1], (uint32_t)((j / VST) & 1), a.status);  // the values' scales
-          const int top = sh.vexp[note];
-          if (top > vexp) {  // (in every thread)
-            vmove = ldexp2f(1.f, vexp - top);
-            vexp = top;
-            moved = true;
-          }
+          tile_top = sh.vexp[note];
+          moved |= tile_top > vlow;  // (the same in every thread)
         }
         if (j > 0) role_wait(dead, &sh.pv_done, (uint32_t)((j - 1) & 1), a.status);
         tc::fence_after_sync();
@@ -938,8 +945,17 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             const float f = m[x] == mn ? 1.f : exp2_fast(m[x] - mn);
             l[x] *= f;
             m[x] = mn;
+            float vmove = 1.f;
+            if (E4M3 && tile_top > vlow) {
+              const int top = mixed ? seen_exp(sh.scale[note][1], sh.seen[ra + 8 * x]) : tile_top;
+              if (top > vexp[x]) {
+                vmove = ldexp2f(1.f, vexp[x] - top);
+                vexp[x] = top;
+              }
+            }
             if (writes && half == 0) sh.factor[ra + 8 * x] = f * vmove;
           }
+          if (!mixed) vlow = max(vlow, tile_top);
           named_bar(1, kSoftThreads);  // (before the halves' tops are written again, too)
           if (i > 0) {
 #pragma unroll 1
@@ -959,7 +975,9 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           }
         }
         // weights, as the second product's operand: row, then token
-        const float vdown = pow2f(-vexp);
+        float vdown[kX];
+#pragma unroll
+        for (int x = 0; x < kX; ++x) vdown[x] = pow2f(-vexp[x]);
         uint32_t w[S::kParts][ROWS == 64 ? 1 : 4];
         float2 sum[kX];
 #pragma unroll
@@ -969,7 +987,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           for (int e = 0; e < kE; e += 2) {
             float2 vs = make_float2(1.f, 1.f);
             if (E4M3)
-              vs = mul2(*reinterpret_cast<const float2*>(&sh.scale[note][1][c0 + token(e)]), make_float2(vdown, vdown));
+              vs = *reinterpret_cast<const float2*>(&sh.scale[note][1][c0 + token(e)]);
 #pragma unroll
             for (int x = 0; x < kX; ++x) {
               const float ms = (m[x] == -INFINITY ? 0.f : m[x]) - (E4M3 ? kWTop : 0.f);
@@ -978,7 +996,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
               const int k = ROWS == 64 ? 0 : e / 2 % 4;
               if (E4M3) {
                 sum[x] = add2(sum[x], v);
-                float2 t = mul2(v, vs);
+                float2 t = mul2(v, mul2(vs, make_float2(vdown[x], vdown[x])));
                 t.x = v.x == 0.f ? 0.f : t.x;  // (a token that is not seen may have any scale)
                 t.y = v.y == 0.f ? 0.f : t.y;
                 w[0][k] = pack_f16x2(t.x, t.y);
@@ -1078,8 +1096,9 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           if (S::kSplit > 1) l[x] += sh.top[1][r];
           // (a row that is none has taken in the tiles that all rows see alike)
           const bool real = low[x] != kNoRow;
-          sh.inv[r] = l[x] == 0.f || !real ? 0.f : E4M3 ? ldexp2f(1.f / l[x], vexp) : 1.f / l[x];
+          sh.inv[r] = l[x] == 0.f || !real ? 0.f : E4M3 ? ldexp2f(1.f / l[x], vexp[x]) : 1.f / l[x];
           if (p.slot >= 0) {
+            if (E4M3) sh.inv[r] = pow2f(vexp[x]);
             part_ml[r] = real ? m[x] : -INFINITY;
             part_ml[kRows + r] = real ? l[x] : 0.f;
           }
@@ -1101,7 +1120,7 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
             for (int u = 0; u < 16; ++u)
               if (lives && r0 + u < rows)
-                part_o[(r0 + u) * DV + d] = E4M3 ? ldexp2f(__uint_as_float(o[u]), vexp) : __uint_as_float(o[u]);
+                part_o[(r0 + u) * DV + d] = __uint_as_float(o[u]) * (E4M3 ? sh.inv[r0 + u] : 1.f);
           } else {
             // two neighbouring lanes trade, and each writes two dimensions of a row
             const int odd = lane & 1;

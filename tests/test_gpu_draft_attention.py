@@ -265,6 +265,23 @@ def test_one_sequence_whose_heads_do_not_divide_the_columns(torch, n, Hq, Hkv, D
         _close(torch, b.run(ws=ws), *b.reference())
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,D,window", [(6, 4, 2, 128, 0), (6, 32, 2, 128, 0), (6, 4, 1, 64, 70), (5, 4, 4, 256, 0)])
+@pytest.mark.parametrize("ps", [16, 24])
+def test_a_huge_scale_stays_with_those_who_see_it(torch, n, Hq, Hkv, D, window, ps):
+    """A new token whose E4M3 scales are finite and huge: rows that do not see it
+    answer as if it were an ordinary one (alone, behind a context, across parts)."""
+    b = Batch(torch, [7, 150, 1500, 64 + n], [n] * 4, n, Hq, Hkv, D, D, ps, "e4m3")
+    b.mask[:] = torch.tensor([(1 << i) | 1 for i in range(n)], device="cuda")
+    ref, tol = b.reference(window=window)
+    for s, x in enumerate(b.lens):
+        t = x - n + 2  # new token 2, which none but itself sees
+        page, off = int(b.table[s, t // ps]), t % ps
+        b.ks[page, :, off], b.vs[page, :, off] = 1e20, 1e30
+    after = b.run(window=window)
+    others = [i for i in range(n) if i != 2]
+    _close(torch, after[:, others], ref[:, others], tol[:, others])
+
+
 @pytest.mark.parametrize("kind,n,Hq,Hkv,D", [("bf16", 16, 8, 1, 128), ("e4m3", 16, 8, 1, 128), ("e4m3", 4, 8, 1, 128),
                                              ("bf16", 3, 8, 2, 64), ("e4m3", 16, 16, 2, 64), ("e4m3", 5, 4, 1, 256),
                                              ("latent", 2, 20, 1, 512), ("latent", 1, 64, 1, 256)])
