@@ -5,6 +5,22 @@
 //   out = sum_t p_t v_t / sum_t p_t,   p_t = 2^(s_t - m),  s_t = scale log2(e) q . k_t
 //
 // in one pass over the keys with a running maximum m and sum l.
+//
+// A CTA has 256 rows of a head, two query tiles that take turns: while one's
+// softmax runs, the tensor cores work for the other.  S = Q K^T of 128 rows by 64
+// keys from shared memory, O += P V with the weights P as bf16 in tensor memory,
+// in the place of their scores; the scores are made two key tiles ahead.  A thread
+// owns a row, so maxima and sums need no exchange; the maximum moves once it is
+// exceeded by 2^8 and only then are the outputs rescaled.
+//
+// Bound by the tensor pipe where prompts are long: one of 8192 tokens and 32 heads
+// 497 us, 1.38 PFLOP/s of the half that is not masked, 0.71 of the measured bf16
+// rate.  64 keys of both query tiles take 1650 cycles, which is what the MMAs need
+// (an S of 128 x 64 x 16 takes 48 cycles for 32 of math: its keys and queries come
+// from shared memory; with 128 keys it would take 64 for 64, but then two buffers
+// of scores per query tile do not fit next to the outputs: 633 us against 520).
+// Short ones are bound by the start and the chain of key tiles: 3 chunks of 9
+// tokens on contexts of 700, 32 heads: 15 us.
 #include <algorithm>
 
 #include "attention_tc.cuh"
@@ -27,12 +43,15 @@ constexpr int kThreads = (kSoftWarps + 3) * 32;  // then one per query tile for 
 constexpr int kSmem = 2 * kQChunks * kQChunk + kStages * (kKBytes + kVBytes) + 1024;
 // TMEM: two buffers of scores (then weights) per query tile, then their outputs
 constexpr int kOCol = 4 * kKeys;
+constexpr int kHeads = 32;          // heads whose blocks are in one order
+constexpr int kHeld = 4;            // sequences per lane up to which blocks are ordered by size
 
 struct ExpandedArgs {
   const int32_t* cu_q;
   const int32_t* cu_k;
   moe_expanded_dims d;
   int blocks;  // of 256 rows, at most, per head
+  int by_size;
   float scale2;
   uint16_t* out;
   int32_t* status;
@@ -98,32 +117,86 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   }
   griddep_wait();
   griddep_trigger();
-  // heads outermost, so that the CTAs at work share few heads' keys; a
-  // sequence's last rows, which see the most, first
-  const int h = blockIdx.x / a.blocks;
+  // In groups of kHeads heads, the blocks of the last places in their sequences
+  // first, which see the most, and of one place all heads: small blocks are left
+  // for the end, and the CTAs at work share few heads' keys.  (One prompt of 8192,
+  // 32 heads: 497 us; 7 ragged ones, 20 heads: 63.7; head after head 521 and 76.3.
+  // All heads at once: 8192, 128 heads 1915 against 1800.)  Where CTAs are so many
+  // that their end does not count, or sequences more than a warp's registers hold:
+  // head after head, in the order of the sequences (40 ragged ones up to 900, 128
+  // heads: 850 us against 912 by size).
+  const int group = a.by_size ? min(kHeads, a.d.H) : 1, span = a.blocks * group;
+  const int h0 = (int)(blockIdx.x / span) * group, at = blockIdx.x % span;
+  const int heads = min(group, a.d.H - h0), h = h0 + at % heads;
   if (warp == 0) {
-    int want = blockIdx.x % a.blocks, seq = -1, blk = 0;
-    for (int b0 = 0; b0 < a.d.B && seq < 0; b0 += 32) {
-      const int b = b0 + lane;
-      int n = 0;
-      if (b < a.d.B) {
-        bool bad;
-        n = cdiv(seq_of(a, b, &bad).lq, 2 * kBlock);
-        if (bad && blockIdx.x == 0) raise_status(a.status, MOE_DEV_BAD_POSITION);
-      }
-      int incl = n;
+    int want = at / heads, seq = -1, blk = 0;
+    if (a.by_size) {
+      int n[kHeld];  // blocks of the sequences lane, lane + 32, ...
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += x;
+      for (int k = 0; k < kHeld; ++k) {
+        n[k] = 0;
+        if (32 * k + lane < a.d.B) {
+          bool bad;
+          n[k] = cdiv(seq_of(a, 32 * k + lane, &bad).lq, 2 * kBlock);
+          if (bad && blockIdx.x == 0) raise_status(a.status, MOE_DEV_BAD_POSITION);
+        }
       }
-      const unsigned here = __ballot_sync(kAll, want < incl);
-      if (here) {
-        const int l = __ffs(here) - 1;
-        seq = b0 + l;
-        blk = __shfl_sync(kAll, incl, l) - 1 - want;  // (counted from the last)
-      } else {
-        want -= __shfl_sync(kAll, incl, 31);
+      auto from = [&](int place) {  // blocks of this place or later
+        int f = 0;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) f += max(n[k] - place, 0);
+        return __reduce_add_sync(kAll, f);
+      };
+      int most = 0;
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) most = max(most, n[k]);
+      int lo = 0, hi = __reduce_max_sync(kAll, most), later = 0;
+      if (want < from(0)) {
+        while (hi - lo > 1) {  // from(lo) > want >= from(hi) = later
+          const int mid = (lo + hi) / 2, f = from(mid);
+          if (f > want) {
+            lo = mid;
+          } else {
+            hi = mid;
+            later = f;
+          }
+        }
+        blk = lo;
+        want -= later;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+          const unsigned have = __ballot_sync(kAll, n[k] > lo);
+          const bool me = n[k] > lo && __popc(have & ((1u << lane) - 1)) == want;
+          const unsigned it = __ballot_sync(kAll, me);
+          if (it) seq = 32 * k + __ffs(it) - 1;
+          want -= __popc(have);
+        }
+      }
+    } else {
+      // (the first CTA checks every sequence)
+      for (int b0 = 0; b0 < a.d.B && (seq < 0 || blockIdx.x == 0); b0 += 32) {
+        const int b = b0 + lane;
+        int n = 0;
+        if (b < a.d.B) {
+          bool bad;
+          n = cdiv(seq_of(a, b, &bad).lq, 2 * kBlock);
+          if (bad && blockIdx.x == 0) raise_status(a.status, MOE_DEV_BAD_POSITION);
+        }
+        if (seq >= 0) continue;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(kAll, incl, o);
+          if (lane >= o) incl += x;
+        }
+        const unsigned here = __ballot_sync(kAll, want < incl);
+        if (here) {
+          const int l = __ffs(here) - 1;
+          seq = b0 + l;
+          blk = __shfl_sync(kAll, incl, l) - 1 - want;  // (counted from the last)
+        } else {
+          want -= __shfl_sync(kAll, incl, 31);
+        }
       }
     }
     if (lane == 0) {
@@ -450,8 +523,10 @@ cudaError_t launch_expanded_attention(const uint16_t* q, const uint16_t* k_nope,
       (err = make_tensor_map_3d(&vmap, v, Tk, d.H, kVd, d.v_stride, d.v_head_stride, 64, kKeys)) != cudaSuccess)
     return err;
   if ((err = ensure_smem((const void*)k_expanded_attention, kSmem)) != cudaSuccess) return err;
-  const ExpandedArgs a{cu_q, cu_k, d, (int)expanded_blocks(d), d.scale * kLog2e, out, status};
-  return launch_k(k_expanded_attention, dim3((unsigned)(expanded_blocks(d) * d.H)), dim3(kThreads), kSmem, s, true,
+  const long long ctas = expanded_blocks(d) * d.H;
+  const ExpandedArgs a{cu_q, cu_k, d, (int)expanded_blocks(d), d.B <= 32 * kHeld && ctas <= 32ll * num_sms(),
+                       d.scale * kLog2e, out, status};
+  return launch_k(k_expanded_attention, dim3((unsigned)ctas), dim3(kThreads), kSmem, s, true,
                   qmap, kmap, rmap, vmap, a);
 }
 

@@ -246,6 +246,24 @@ def test_expanded_bad_offsets(torch):
     op.check()
 
 
+@pytest.mark.parametrize("B,H", [(1, 33), (3, 70), (31, 3), (32, 3), (33, 3), (70, 3), (128, 2), (129, 2), (300, 1)])
+def test_expanded_many_sequences(torch, B, H):
+    """Every block of every sequence and head is found, and the last sequence's offsets are
+    checked as the first one's."""
+    from block_fp8_expert_gb300 import MoeError
+    lens = [(b * 7 % 5) * (b * 37 % 211) for b in range(B)]
+    lens[B // 2] = 700
+    q, kv, rope, cu_q, cu_k = _expanded(torch, lens, [b % 3 for b in range(B)], H)
+    op = _dec().ExpandedAttention(H)
+    ref, tol = _expanded_ref(torch, q, kv, rope, cu_q, cu_k, op.scale)
+    _close(op.forward(q, kv[..., :128], rope, kv[..., 128:], cu_q, cu_k), ref, tol)
+    op.check()
+    cu_k[B] += 1
+    op.forward(q, kv[..., :128], rope, kv[..., 128:], cu_q, cu_k)
+    with pytest.raises(MoeError, match="0x20"):
+        op.check()
+
+
 def test_expanded_large_scores(torch):
     """Scores whose maximum moves along the keys, and a graph's replay."""
     q, kv, rope, cu_q, cu_k = _expanded(torch, [500], [100], 2, spread=4.0)
