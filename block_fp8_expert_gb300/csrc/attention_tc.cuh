@@ -33,9 +33,10 @@ __device__ __forceinline__ uint32_t desc_k(uint32_t smem_addr) { return (smem_ad
 __device__ __forceinline__ uint32_t desc_mn(uint32_t smem_addr, uint32_t next) {
   return (smem_addr >> 4) | (next >> 4) << 16;
 }
-// The same value in every lane, as the compiler then knows: MMA operands have
-// to be in uniform registers, and what it cannot prove uniform is moved there
-// word by word before each MMA (51 cycles for one of 64 x 64 x 16 that takes 32).
+// The same value in every lane, in a form that tells the compiler so: the words
+// of descriptors and TMEM addresses that change from tile to tile go through it
+// (36 MMAs of 64 x 64 x 16, 32 cycles each, then follow one another without gaps;
+// without it one took 51).
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(kAll, v); }
 
 // D[tmem] (+)= A[smem] B[smem]^T, descriptors by their low words.
@@ -111,13 +112,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-// The same box to L2 alone.
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];\n" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
                                             uint64_t* bar) {

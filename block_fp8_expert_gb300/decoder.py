@@ -1,10 +1,15 @@
 """The operators of a decoder layer around the MoE layer, on PyTorch tensors.
 
-    ExpertSelector   router logits -> chosen experts and weights
-    QkNormRope       head norms, rotary positions, store into a paged cache
-    PagedCache       the paged key/value cache (bf16 or E4M3)
-    PagedAttention   attention of one new token per sequence over it
-    Fp8Linear        x W^T with block-FP8 weights and E4M3 activations
+    ExpertSelector     router logits -> chosen experts and weights
+    QkNormRope         head norms, rotary positions, store into a paged cache
+    PagedCache         the paged key/value cache (bf16 or E4M3)
+    PagedAttention     attention of one new token per sequence over it
+    TreeAttention      attention of several, a tree of drafted tokens, over it
+    LatentCache        a paged cache of one latent vector per token
+    LatentStore        norm, rotary positions, store into it
+    LatentAttention    attention over it in the absorbed form (new or drafted tokens)
+    ExpandedAttention  the same attention in its expanded form, for prompts
+    Fp8Linear          x W^T with block-FP8 weights and E4M3 activations
 
 Each object holds what a serving program sets up once; ``forward`` takes the
 step's tensors, and output buffers and a workspace where the program keeps

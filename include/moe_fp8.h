@@ -356,8 +356,9 @@ moe_status moe_read_device_status(const void* ws, int32_t* status,
  * ---------------------------------------------------------------------------
  * The rest of a decoder layer around the MoE layer: expert selection with
  * balance bias and groups, query/key norms with rotary positions into a paged
- * key/value cache, attention of one new token per sequence over that cache,
- * and the block-FP8 linear layers between them.  None of these has a
+ * key/value cache, attention of one new token per sequence or of several
+ * drafted ones over that cache, a paged cache of latent vectors with the
+ * attention over it, and the block-FP8 linear layers between them.  None of these has a
  * counterpart in the pages, which state the MoE layer only.
  *
  * They follow the conventions above, with two additions:
@@ -367,9 +368,10 @@ moe_status moe_read_device_status(const void* ws, int32_t* status,
  *  - Rows may be strided.  A row stride counts elements and is at least the
  *    row's length; the elements inside a row are contiguous, and every row
  *    starts on a 16-byte boundary where noted.
- *  - topk_idx, topk_w, pos, slots, block_table, seq_lens, k_scale and v_scale
- *    need the alignment of their elements only (a step's part of a longer
- *    array will do); every other pointer is 16-byte aligned.
+ *  - topk_idx, topk_w, pos, slots, block_table, seq_lens, draft_lens, mask,
+ *    cu_q, cu_k, k_scale and v_scale need the alignment of their elements only
+ *    (a step's part of a longer array will do); every other pointer is 16-byte
+ *    aligned.
  * ---------------------------------------------------------------------------
  */
 
@@ -599,18 +601,21 @@ typedef struct {
  * context's end and sees the last window - c tokens of the context.
  * q bf16 [B, n, Hq, D] and out bf16 [B, n, Hq, D] by their strides; block_table
  * as in moe_paged_attention; seq_lens, draft_lens int32 [B]; mask int64 [B, n].
- * Rows from draft_lens[b] on, and rows that see nothing, are zeros.  Cache
- * elements that no row may see are not read, and what a row does not see does
- * not reach it, whatever it is (NaN and infinities included).
+ * Rows from draft_lens[b] on, and rows that see nothing, are zeros.  Pages
+ * outside a sequence's length and window are not read; within a page that is
+ * used anything may be, as what a row does not see does not reach it (NaN,
+ * infinities and huge scales included).
  * The cache's length splits over the GPU and the parts are joined in a fixed
  * order, so equal calls give equal bits.  Scores, maxima, sums and outputs are
  * fp32; the softmax weights enter the product with the values as two bf16 parts
  * next to bf16 values (2^-15 of the weight), times the value's scale and rounded
- * to fp16 next to E4M3 values (2^-11; the scales' largest and smallest may lie
- * 2^24 apart without loss).  A page number
- * outside [0, pages), a length outside [0, table_width * page_size] or a
- * draft_lens[b] outside [0, min(n, seq_lens[b])] raises MOE_DEV_BAD_PAGE; the
- * tokens of such a page are left out, and such a length is clamped.
+ * to fp16 next to E4M3 values: 2^-11 of the product down to 2^-23 of the largest
+ * weight times the largest value scale that the row has seen so far, and below
+ * that steps of 2^-33 of it (so a token of tiny weight and a scale many orders
+ * above the others takes bits from them).  A page number outside [0, pages), a
+ * length outside [0, table_width * page_size] or a draft_lens[b] outside [0,
+ * min(n, seq_lens[b])] raises MOE_DEV_BAD_PAGE; the tokens of such a page are
+ * left out, and such a length is clamped.
  */
 moe_status moe_tree_attention_workspace_bytes(moe_draft_dims d, int32_t Hkv,
                                               int32_t D, size_t* bytes);
