@@ -26,7 +26,7 @@
 // more, scores 1900 while pieces are being refilled, softmax 600 to 1200, outputs
 // 1300).
 // 40 ragged sequences up to 6000, 128 heads 65 us (411 TFLOP/s).  32 ragged trees
-// of 16, grouped heads, E4M3 77 us: the conversion of codes and the softmax of 128
+// of 16, grouped heads, E4M3 75 us: the conversion of codes and the softmax of 128
 // rows issue on 37% of cycles.  One sequence of 777 or 900 tokens 11 us.
 // Measured and left out: prefetching later tiles to L2 (2 x 131072: 74.6 us with,
 // 71.3 without), one warp that polls the pieces side by side (73.9 against 68.5),
@@ -321,7 +321,7 @@ struct DraftShared {
   uint32_t tmem_base;
   volatile int abort_flag;
   uint32_t exists[kNotes][2];  // tokens of the tile that are there
-  alignas(8) float scale[E4M3 ? kNotes : 1][2][E4M3 ? kTile : 1];  // of its keys and values
+  alignas(16) float scale[E4M3 ? kNotes : 1][2][E4M3 ? kTile : 1];  // of its keys and values
   float factor[ROWS];  // on the outputs of a row, when its maximum moves
   int vexp[kNotes];    // E4M3: exponents of the tiles' largest value scales
   float q_scale[2][E4M3 ? ROWS : 1];  // E4M3: of the rows' queries, this part's and the next one's
@@ -355,11 +355,17 @@ __device__ __forceinline__ int scale_exp(float v) {
   const uint32_t bits = __float_as_uint(v) & 0x7fffffffu;
   return bits >= 0x7f800000u ? kExpMin : min(max((int)(bits >> 23) - 127, kExpMin), kExpMax);
 }
-// The same of the largest scale of the tokens that a row sees: what it does not
-// see takes no bits from its weights.
-__device__ __noinline__ int seen_exp(const float* scales, uint64_t seen) {
-  int top = kExpMin;
-  for (; seen; seen &= seen - 1) top = max(top, scale_exp(scales[__ffsll((long long)seen) - 1]));
+// The largest of 16 scales, of the tokens that a row sees.
+__device__ __noinline__ float seen_top(const float* scales, uint32_t seen) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(scales + 4 * i);
+    const float f[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if ((seen >> (4 * i + u) & 1) && f[u] < INFINITY) top = fmaxf(top, f[u]);
+  }
   return top;
 }
 
@@ -971,7 +977,21 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             m[x] = mn;
             float vmove = 1.f;
             if (E4M3 && tile_top > vlow) {
-              const int top = mixed ? seen_exp(sh.scale[note][1], sh.seen[ra + 8 * x]) : tile_top;
+              int top = tile_top;
+              if (mixed) {
+                // The scales of what the row sees: what it does not see takes no bits
+                // from its weights.  (A row's four lanes look at 16 tokens each.)
+                const uint64_t seen = sh.seen[ra + 8 * x];
+                float v = 0.f;
+#pragma unroll 1
+                for (int t = ROWS == 64 ? 16 * c : 0; t < (ROWS == 64 ? 16 * c + 16 : kTile); t += 16)
+                  v = fmaxf(v, seen_top(&sh.scale[note][1][E4M3 ? t : 0], (uint32_t)(seen >> t)));
+                if (ROWS == 64) {
+                  v = fmaxf(v, __shfl_xor_sync(kAll, v, 1));
+                  v = fmaxf(v, __shfl_xor_sync(kAll, v, 2));
+                }
+                top = scale_exp(v);
+              }
               if (top > vexp[x]) {
                 vmove = ldexp2f(1.f, vexp[x] - top);
                 vexp[x] = top;
