@@ -265,6 +265,15 @@ def test_one_sequence_whose_heads_do_not_divide_the_columns(torch, n, Hq, Hkv, D
         _close(torch, b.run(ws=ws), *b.reference())
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,lens", [(1024, 8, 64, [200]), (128, 1, 128, [700, 64, 0, 90]), (256, 2, 256, [130])])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_as_many_rows_as_there_may_be(torch, Hq, Hkv, D, lens, kind):
+    """64 new tokens of 128 heads per key/value head: more row tiles than there
+    are columns for every head."""
+    b = Batch(torch, lens, [min(64, x) for x in lens], 64, Hq, Hkv, D, D, 64, kind)
+    _close(torch, b.run(), *b.reference())
+
+
 @pytest.mark.parametrize("n,Hq,Hkv,D,window", [(6, 4, 2, 128, 0), (6, 32, 2, 128, 0), (6, 4, 1, 64, 70), (5, 4, 4, 256, 0)])
 @pytest.mark.parametrize("ps", [16, 24])
 def test_a_huge_scale_stays_with_those_who_see_it(torch, n, Hq, Hkv, D, window, ps):
