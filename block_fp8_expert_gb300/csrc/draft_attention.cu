@@ -1257,7 +1257,9 @@ __global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
       acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        if (m[u] == -INFINITY) continue;  // (nothing of this row: the outputs may hold anything)
+        // A part with nothing of this row: its outputs may hold anything.  (Not told by
+        // the maximum: a row of nothing but NaN scores leaves it at -inf, its sum is NaN.)
+        if (l[u] == 0.f) continue;
         const float f = exp2f(m[u] - Ms);
         L = fmaf(l[u], f, L);
         acc.x = fmaf(v[u].x, f, acc.x);
@@ -1280,7 +1282,7 @@ __global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
         L = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int x = 0; x < shares; ++x) {
-          if (s_m[grp + x] == -INFINITY) continue;
+          if (s_l[grp + x] == 0.f) continue;
           const float f = exp2f(s_m[grp + x] - Ms);
           const float4 v = s_acc[grp + x][d4];
           L = fmaf(s_l[grp + x], f, L);

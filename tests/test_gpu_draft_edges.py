@@ -1,0 +1,68 @@
+"""Attention of drafted tokens and latent attention on the edges: queries and keys
+that are NaN.
+
+Tolerances as in test_gpu_draft_attention.py.
+"""
+import math
+
+import pytest
+
+from gpu_common import require_gpu
+from test_gpu_draft_attention import Batch, _close
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return require_gpu()
+
+
+def _batch(torch, kind, lens, n, Hq, Hkv, D, ps=16, **kw):
+    Dk = D + 64 if kind == "latent" else D
+    return Batch(torch, lens, [min(n, x) for x in lens], n, Hq, Hkv, Dk, D, ps, kind, **kw)
+
+
+# 64 or 128 rows of a CTA, one or two row tiles
+SHAPES = [("bf16", 3, 8, 2, 64), ("bf16", 20, 4, 1, 128), ("bf16", 2, 4, 1, 256), ("e4m3", 3, 8, 2, 64),
+          ("e4m3", 20, 4, 1, 128), ("e4m3", 2, 4, 1, 256), ("latent", 3, 8, 1, 256), ("latent", 1, 20, 1, 512)]
+# segments of one part each; of many parts; of shares that end inside them
+LENS = {"whole": [120, 90, 6], "parts": [9000], "shares": [2000] * 100}
+
+
+# ------------------------------------------------------------------ NaN
+
+@pytest.mark.parametrize("lens", LENS.values(), ids=LENS.keys())
+@pytest.mark.parametrize("kind,n,Hq,Hkv,D", SHAPES)
+def test_a_nan_query_answers_nan(torch, kind, n, Hq, Hkv, D, lens):
+    """However the cache is divided; the other rows do not notice."""
+    b = _batch(torch, kind, lens, n, Hq, Hkv, D)
+    ref, tol = b.reference()
+    hit = torch.zeros(len(lens), n, Hq, dtype=torch.bool, device="cuda")
+    for s, i, h in ((0, 0, 2), (len(lens) - 1, n // 2, Hq - 1)):
+        b.q[s, i, h, 5] = math.nan
+        hit[s, i, h] = i < b.drafts[s]
+    got = b.run()
+    assert torch.isnan(got[hit]).all()
+    _close(torch, got[~hit], ref[~hit], tol[~hit])
+
+
+@pytest.mark.parametrize("lens", LENS.values(), ids=LENS.keys())
+@pytest.mark.parametrize("kind,n,Hq,Hkv,D", SHAPES)
+def test_nan_keys_of_whole_tiles_answer_nan(torch, kind, n, Hq, Hkv, D, lens):
+    """A context with tiles, and so parts, of nothing but NaN scores."""
+    b = _batch(torch, kind, lens, n, Hq, Hkv, D)
+    ref, tol = b.reference()
+    t = torch.arange(640, 1024) if lens[0] > 1100 else torch.arange(0, 64)
+    page, off = b.table[0].long()[t.cuda() // b.ps], t.cuda() % b.ps
+    if kind == "latent":
+        b.data[page, off, D + 3] = math.nan  # of the shared key part: the values stay
+    elif kind == "bf16":
+        b.k[page, :, off] = math.nan
+    else:
+        b.k.view(torch.uint8)[page, :, off] = 0x7F
+    got = b.run()
+    assert torch.isnan(got[0, :b.drafts[0]]).all()
+    _close(torch, got[1:], ref[1:], tol[1:])
+    if kind != "latent" and lens[0] > 1100:  # a window that they lie behind
+        _close(torch, b.run(window=300), *b.reference(window=300))
