@@ -343,17 +343,18 @@ __device__ __forceinline__ uint4 e4m3x8_to_f16(uint32_t lo, uint32_t hi) {
                     e4m3x2_to_f16x2(hi >> 16));
 }
 // Next to E4M3 codes the products are of fp16.  Weights times their value's scale
-// are held as w 2^(kWTop - e), e the exponent of the largest scale so far; as a
-// maximum moves here once it is exceeded by 2^5 (kHalfSlack), they stay below 2^15,
-// and fp16 keeps eleven bits down to 2^-23 of the largest, and steps of 2^-33 of
-// it below.  (Less slack keeps more of them, but maxima of 128 rows then move in
-// half of the tiles: 32 trees of 16: 83.1 us with 2^2.)
-constexpr float kWTop = 9.f, kHalfSlack = 5.f;
-constexpr int kExpMin = -120, kExpMax = 120;
-// The exponent of a scale, for the largest (what is not finite counts as none).
+// are held as w 2^(kWTop - e), e one less than the exponent of the largest scale so
+// far (so that 2^-e is a normal number for every finite scale); as a maximum moves
+// here once it is exceeded by 2^5 (kHalfSlack), they stay below 2^(8 + 5 + 2), and
+// fp16 keeps eleven bits down to 2^-23 of the largest, and steps of 2^-33 of it
+// below.  (Less slack keeps more of them, but maxima of 128 rows then move in half
+// of the tiles: 32 trees of 16: 83.1 us with 2^2.)
+constexpr float kWTop = 8.f, kHalfSlack = 5.f;
+constexpr int kExpMin = -126;
+// e of a scale, for the largest: at most 126 (what is not finite counts as none).
 __device__ __forceinline__ int scale_exp(float v) {
   const uint32_t bits = __float_as_uint(v) & 0x7fffffffu;
-  return bits >= 0x7f800000u ? kExpMin : min(max((int)(bits >> 23) - 127, kExpMin), kExpMax);
+  return bits >= 0x7f800000u ? kExpMin : max((int)(bits >> 23) - 128, kExpMin);
 }
 // The largest of 16 scales, of the tokens that a row sees.
 __device__ __noinline__ float seen_top(const float* scales, uint32_t seen) {

@@ -1,5 +1,5 @@
 """Attention of drafted tokens and latent attention on the edges: queries and keys
-that are NaN.
+that are NaN, E4M3 value scales at the ends of fp32.
 
 Tolerances as in test_gpu_draft_attention.py.
 """
@@ -66,3 +66,27 @@ def test_nan_keys_of_whole_tiles_answer_nan(torch, kind, n, Hq, Hkv, D, lens):
     _close(torch, got[1:], ref[1:], tol[1:])
     if kind != "latent" and lens[0] > 1100:  # a window that they lie behind
         _close(torch, b.run(window=300), *b.reference(window=300))
+
+
+# ------------------------------------------------------------------ E4M3 scales
+
+def _scaled(torch, lens, n, Hq, Hkv, D, ps, e):
+    """A batch whose value scales lie in [2^e, 2^(e + 1)), its values' codes within
+    1/2, with reference and tolerance: that of the formula, and half a step of bf16's
+    subnormals (2^-134) where the outputs are."""
+    b = _batch(torch, "e4m3", lens, n, Hq, Hkv, D, ps)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(e + 1000)
+    f = 1 + 0.99 * torch.rand(b.vs.shape, generator=g, device="cuda", dtype=torch.float64)
+    b.vs.copy_((f * 2.0 ** e).float())
+    b.v.copy_((0.25 * torch.randn(b.v.shape, generator=g, device="cuda")).clamp(-0.5, 0.5).to(torch.float8_e4m3fn))
+    ref, tol = b.reference()
+    return b, ref, (tol - 1e-30).clamp(min=0) + 2.0 ** -133
+
+
+@pytest.mark.parametrize("e", [-140, -126, -121, -60, 60, 119, 120, 121, 122, 125, 126, 127])
+@pytest.mark.parametrize("n,Hq,Hkv,D,ps", [(3, 8, 2, 64, 16), (16, 8, 1, 128, 16), (2, 4, 1, 256, 64), (3, 8, 2, 128, 24)])
+def test_value_scales_of_any_size(torch, n, Hq, Hkv, D, ps, e):
+    """Outputs are finite in bf16, and so are the weights."""
+    b, ref, tol = _scaled(torch, [120, 90, 6], n, Hq, Hkv, D, ps, e)
+    _close(torch, b.run(), ref, tol)
