@@ -327,7 +327,7 @@ struct DraftShared {
   float q_scale[2][E4M3 ? ROWS : 1];  // E4M3: of the rows' queries, this part's and the next one's
   union {
     float top[2][ROWS];  // the largest score of a row, by halves of the tile; after the last tile [1]: half of its sum
-    float inv[ROWS];     // after the last tile: 1 / the row's sum, of a part's row what its weights were held at
+    float inv[ROWS];     // after the last tile: 1 / the row's sum, E4M3: times what its weights were held at
   };
   union {
     unsigned scan[2][WARPS];
@@ -1143,7 +1143,6 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           const bool real = low[x] != kNoRow;
           sh.inv[r] = l[x] == 0.f || !real ? 0.f : E4M3 ? ldexp2f(1.f / l[x], vexp[x]) : 1.f / l[x];
           if (p.slot >= 0) {
-            if (E4M3) sh.inv[r] = pow2f(vexp[x]);
             part_ml[r] = real ? m[x] : -INFINITY;
             part_ml[kRows + r] = real ? l[x] : 0.f;
           }
@@ -1162,6 +1161,8 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           ld_32x32b_x16(quadrant + kOCol + mb * kRows + r0, o);
           tc::wait_ld();
           if (p.slot >= 0) {
+            // (next to E4M3 divided by the part's sum: with large scales the undivided
+            // outputs leave fp32 where the answers do not)
 #pragma unroll
             for (int u = 0; u < 16; ++u)
               if (lives && r0 + u < rows)
@@ -1198,11 +1199,13 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
 // Joins the parts of the segments that several columns hold, in order, and
 // answers zeros for sequences without new tokens: out = sum_i 2^(m_i - M) o_i /
-// sum_i 2^(m_i - M) l_i.  Bound by latency (its parts come from L2, 76 of them for
-// 2 x 131072 tokens): DV / 4 threads have a row's four dimensions each, and enough
-// groups of them share a row's parts for four rounds of loads, in which `kAhead`
-// parts of a thread are on their way at once.  4 to 5 us of a call.
-template <int DV, int THREADS, int kAhead>
+// sum_i 2^(m_i - M) l_i.  DIVIDED: the o_i are divided by their l_i already; what is
+// joined so far is kept divided, so that nothing in between is larger than they are.
+// Bound by latency (its parts come from L2, 76 of them for 2 x 131072 tokens): DV /
+// 4 threads have a row's four dimensions each, and enough groups of them share a
+// row's parts for four rounds of loads, in which `kAhead` parts of a thread are on
+// their way at once.  4 to 5 us of a call.
+template <int DV, int THREADS, int kAhead, bool DIVIDED>
 __global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
   constexpr int kLanes = DV / 4, kGroups = THREADS / kLanes;  // threads per row; rows, or shares of the parts
   __shared__ float4 s_acc[kGroups][kLanes];
@@ -1254,15 +1257,23 @@ __global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) M2 = fmaxf(M2, m[u]);
       const float Ms = M2 == -INFINITY ? 0.f : M2, f0 = M == M2 ? 1.f : exp2f(M - Ms);
-      L *= f0;
-      acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+      const float kept = L * f0;
+      L = kept;
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         // A part with nothing of this row: its outputs may hold anything.  (Not told by
         // the maximum: a row of nothing but NaN scores leaves it at -inf, its sum is NaN.)
         if (l[u] == 0.f) continue;
-        const float f = exp2f(m[u] - Ms);
-        L = fmaf(l[u], f, L);
+        m[u] = exp2f(m[u] - Ms);
+        L = fmaf(l[u], m[u], L);
+      }
+      const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);  // (a sum is below 2^46)
+      const float fa = DIVIDED ? kept * inv : f0;
+      acc = make_float4(acc.x * fa, acc.y * fa, acc.z * fa, acc.w * fa);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (l[u] == 0.f) continue;
+        const float f = DIVIDED ? l[u] * m[u] * inv : m[u];
         acc.x = fmaf(v[u].x, f, acc.x);
         acc.y = fmaf(v[u].y, f, acc.y);
         acc.z = fmaf(v[u].z, f, acc.z);
@@ -1282,11 +1293,18 @@ __global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
         const float Ms = M == -INFINITY ? 0.f : M;
         L = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (DIVIDED)
+          for (int x = 0; x < shares; ++x)
+            if (s_l[grp + x] != 0.f) L = fmaf(s_l[grp + x], exp2f(s_m[grp + x] - Ms), L);
+        const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
         for (int x = 0; x < shares; ++x) {
           if (s_l[grp + x] == 0.f) continue;
-          const float f = exp2f(s_m[grp + x] - Ms);
+          float f = exp2f(s_m[grp + x] - Ms);
           const float4 v = s_acc[grp + x][d4];
-          L = fmaf(s_l[grp + x], f, L);
+          if (DIVIDED)
+            f *= s_l[grp + x] * inv;
+          else
+            L = fmaf(s_l[grp + x], f, L);
           acc.x = fmaf(v.x, f, acc.x);
           acc.y = fmaf(v.y, f, acc.y);
           acc.z = fmaf(v.z, f, acc.z);
@@ -1296,7 +1314,7 @@ __global__ void __launch_bounds__(THREADS) k_draft_join(const DraftArgs a) {
       __syncthreads();
     }
     if (mine == 0 && r < rows) {
-      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const float inv = L == 0.f ? 0.f : DIVIDED ? 1.f : 1.f / L;
       *reinterpret_cast<uint2*>(out) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     }
@@ -1329,9 +1347,9 @@ cudaError_t launch_draft(DraftArgs& a, const CUtensorMap& kmap, const CUtensorMa
   // against 79.9 with the other form; 32 trees of 16, E4M3: 104.5 against 113.8)
   const int segs = a.d.B * a.c.Hkv * a.gtiles;
   if (a.cols >= 8 * a.d.B * a.c.Hkv)
-    return launch_k(k_draft_join<DV, 512, 8>, dim3(segs, std::min(ROWS, cdiv(4 * num_sms(), segs))), dim3(512), 0, s,
-                    true, a);
-  return launch_k(k_draft_join<DV, 256, 4>, dim3(segs, ROWS / (1024 / DV)), dim3(256), 0, s, true, a);
+    return launch_k(k_draft_join<DV, 512, 8, E4M3>, dim3(segs, std::min(ROWS, cdiv(4 * num_sms(), segs))), dim3(512), 0,
+                    s, true, a);
+  return launch_k(k_draft_join<DV, 256, 4, E4M3>, dim3(segs, ROWS / (1024 / DV)), dim3(256), 0, s, true, a);
 }
 
 // A cache of pages that tile boxes divide is copied by maps of [pages, heads,

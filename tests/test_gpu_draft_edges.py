@@ -90,3 +90,13 @@ def test_value_scales_of_any_size(torch, n, Hq, Hkv, D, ps, e):
     """Outputs are finite in bf16, and so are the weights."""
     b, ref, tol = _scaled(torch, [120, 90, 6], n, Hq, Hkv, D, ps, e)
     _close(torch, b.run(), ref, tol)
+
+
+@pytest.mark.parametrize("e", [-140, -126, -110, -90, 90, 105, 115, 121, 127])
+@pytest.mark.parametrize("n,Hq,Hkv,D,ps", [(3, 8, 2, 64, 16), (16, 8, 1, 128, 16), (2, 4, 1, 256, 64), (3, 8, 2, 128, 24)])
+@pytest.mark.parametrize("lens", [[9000], [1500] * 100], ids=["parts", "shares"])
+def test_value_scales_of_any_size_over_parts(torch, lens, n, Hq, Hkv, D, ps, e):
+    """What a part of a long sequence sums up is beyond fp32 where the outputs are
+    not."""
+    b, ref, tol = _scaled(torch, lens, n, Hq, Hkv, D, ps, e)
+    _close(torch, b.run(), ref, tol)
