@@ -200,14 +200,16 @@ __device__ __forceinline__ bool mbar_nap(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Warp-uniform bounded wait.  Once one wait of a CTA has run out, `abort_flag`
+// Warp-uniform bounded wait; whether the phase has come (the same answer in every
+// lane, which a read of `abort_flag` is not: another warp may raise it between two
+// lanes' reads).  Once one wait of a CTA has run out, `abort_flag`
 // is set and the others return after a nap: the roles then run through the rest
 // of their loops, whose results are reported as invalid, and keep their
 // barriers matched.  (Clocks and flag are only read once a nap is over: reading
 // them takes as long as most waits, and a warp that polls takes issue slots and
 // shared-memory cycles from those that work.)
 // (out of line: every wait is in the way of the code that a first call fetches)
-static __device__ __noinline__ void role_wait_on(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
+static __device__ __noinline__ bool role_wait_on(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
                                                  int32_t* status) {
   const WaitBudget b = wait_budget();
   while (true) {
@@ -215,7 +217,7 @@ static __device__ __noinline__ void role_wait_on(volatile int* abort_flag, uint6
     if (__any_sync(kAll, done)) {
       // (the phase is complete: the others see it, too)
       for (int r = 0; !done && r < (1 << 16); ++r) done = mbar_try_wait(bar, parity);
-      if (__all_sync(kAll, done)) return;
+      if (__all_sync(kAll, done)) return true;
       break;
     }
     if (__any_sync(kAll, *abort_flag != 0 || budget_spent(b))) break;
@@ -225,10 +227,11 @@ static __device__ __noinline__ void role_wait_on(volatile int* abort_flag, uint6
     raise_status(status, MOE_DEV_WAIT_TIMEOUT);
   }
   __syncwarp();
+  return false;
 }
-__device__ __forceinline__ void role_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
+__device__ __forceinline__ bool role_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity,
                                           int32_t* status) {
-  if (!__all_sync(kAll, mbar_try_wait(bar, parity))) role_wait_on(abort_flag, bar, parity, status);
+  return __all_sync(kAll, mbar_try_wait(bar, parity)) || role_wait_on(abort_flag, bar, parity, status);
 }
 
 // Three waits at once: a wait for what has long come still takes 180 cycles, which

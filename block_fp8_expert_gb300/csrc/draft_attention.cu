@@ -451,6 +451,10 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       return x;
     };
     int j = 0;
+    // Until a wait has run out; the same in every lane.  (No copy is started after
+    // that: the parities of later waits mean nothing, and what had been started has
+    // long landed.)
+    bool alive = true;
     while (walk.next_tiles(a, p)) {
       // the tile's boxes, and those of the next two
       Box x, x1 = look_up(p.tile), x2 = look_up(p.tile + 1);
@@ -477,15 +481,16 @@ k_draft_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             const int k = 2 * j + y, slot = k % (S::kSlots ? S::kSlots : 1);
             full = &sh.raw_full[slot];
             if (k >= S::kSlots)
-              role_wait(dead, &sh.raw_empty[slot], (uint32_t)((k / (S::kSlots ? S::kSlots : 1) - 1) & 1), a.status);
+              alive = alive && role_wait(dead, &sh.raw_empty[slot],
+                                         (uint32_t)((k / (S::kSlots ? S::kSlots : 1) - 1) & 1), a.status);
           } else if (j >= ST) {  // (as many stages for every piece)
-            role_wait(dead, &sh.empty[st][y], (uint32_t)((j / ST - 1) & 1), a.status);
+            alive = alive && role_wait(dead, &sh.empty[st][y], (uint32_t)((j / ST - 1) & 1), a.status);
           }
           if (y == 0 && lane == 0) {
             sh.exists[note][0] = there_lo;
             sh.exists[note][1] = there_hi;
           }
-          if (*dead) continue;
+          if (!alive) continue;
           constexpr int kFirst = (LATENT ? 3 : S::kKChunks) * kChunk;  // bytes of piece 0
           __syncwarp();
           if (lane == 0)
