@@ -1,5 +1,6 @@
 """Attention of drafted tokens and latent attention on the edges: queries and keys
-that are NaN, E4M3 value scales at the ends of fp32.
+that are NaN, E4M3 value scales at the ends of fp32, the smallest pages and pages
+that are no power of two, negative scales, and every sequence of the divisions.
 
 Tolerances as in test_gpu_draft_attention.py.
 """
@@ -100,3 +101,63 @@ def test_value_scales_of_any_size_over_parts(torch, lens, n, Hq, Hkv, D, ps, e):
     not."""
     b, ref, tol = _scaled(torch, lens, n, Hq, Hkv, D, ps, e)
     _close(torch, b.run(), ref, tol)
+
+
+# ------------------------------------------------------------------ pages
+
+@pytest.mark.parametrize("ps", [8, 192, 320])
+@pytest.mark.parametrize("kind,n,Hq,Hkv,D", SHAPES + [("bf16", 6, 8, 2, 128), ("e4m3", 16, 8, 1, 64), ("latent", 6, 4, 1, 512)])
+def test_pages_of_one_core_row_and_of_several_tiles(torch, kind, n, Hq, Hkv, D, ps):
+    """Pages of 8 tokens, eight boxes to a tile, and of several tiles whose number
+    is no power of two."""
+    b = _batch(torch, kind, [700, 64, 193, 5, 0, 383], n, Hq, Hkv, D, ps)
+    _close(torch, b.run(), *b.reference())
+
+
+@pytest.mark.parametrize("ps", [8, 64, 192])
+@pytest.mark.parametrize("window", [20, 101, 200])
+@pytest.mark.parametrize("kind,n,Hq,Hkv,D", [c for c in SHAPES if c[0] != "latent"])
+def test_windows_that_begin_inside_a_page(torch, kind, n, Hq, Hkv, D, window, ps):
+    """Pages before every row's window have been given away."""
+    b = _batch(torch, kind, [700, 64, 193, 5, 0, 383], n, Hq, Hkv, D, ps)
+    keep = b.table.clone()
+    for s, (length, d) in enumerate(zip(b.lens, b.drafts)):
+        b.table[s, :max(0, length - d + 1 - window) // ps] = -7
+    got = b.run(window=window)
+    b.table.copy_(keep)
+    _close(torch, got, *b.reference(window=window))
+
+
+# ------------------------------------------------------------------ scores
+
+@pytest.mark.parametrize("scale", [-2.0, -0.3, 3.0])
+@pytest.mark.parametrize("kind,n,Hq,Hkv,D", SHAPES)
+def test_scales_of_either_sign(torch, kind, n, Hq, Hkv, D, scale):
+    """Scores that grow along the keys, within the formula's tolerance (of the
+    same scores from queries of the other sign where the scale is negative)."""
+    b = _batch(torch, kind, [900, 300], n, Hq, Hkv, D, spread=0.25)
+    t = torch.arange(900, device="cuda")
+    page, off = b.table[0].long()[t // 16], t % 16
+    if kind == "latent":
+        b.data[page, off] = (b.data[page, off].float() * (0.2 + t / 900.0).view(-1, 1)).to(torch.bfloat16)
+    elif kind == "bf16":
+        b.k[page, :, off] = (b.k[page, :, off].float() * (0.2 + t / 900.0).view(-1, 1, 1)).to(torch.bfloat16)
+    else:
+        b.ks[page, :, off] *= (0.2 + t / 900.0).view(-1, 1)
+    b.op.scale = scale
+    got = b.run()
+    b.scale = abs(scale)
+    b.q = b.q if scale > 0 else -b.q
+    _close(torch, got, *b.reference())
+
+
+# ------------------------------------------------------------------ division
+
+@pytest.mark.parametrize("lens", [[6000] * 3 + [130] * 150, [40] * 400, [3000, 2999, 64, 1, 700], [2] * 1000,
+                                  [100 + 37 * (i * 5 % 23) for i in range(160)], [1000] * 90])
+@pytest.mark.parametrize("kind,n,Hq,Hkv,D", [("bf16", 2, 8, 2, 64), ("e4m3", 2, 8, 2, 64), ("latent", 2, 8, 1, 256),
+                                             ("bf16", 9, 16, 2, 128), ("e4m3", 9, 8, 1, 128)])
+def test_every_sequence_of_a_division(torch, kind, n, Hq, Hkv, D, lens):
+    """Wherever columns begin and end in them."""
+    b = _batch(torch, kind, lens, n, Hq, Hkv, D)
+    _close(torch, b.run(), *b.reference())
