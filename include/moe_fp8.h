@@ -604,7 +604,9 @@ typedef struct {
  * Rows from draft_lens[b] on, and rows that see nothing, are zeros.  Pages
  * outside a sequence's length and window are not read; within a page that is
  * used anything may be, as what a row does not see does not reach it (NaN,
- * infinities and huge scales included).
+ * infinities and huge scales included).  What it sees does: a NaN score makes
+ * the row NaN.  A score of -infinity has no weight, and a row that sees no other
+ * is zeros, too.
  * The cache's length splits over the GPU and the parts are joined in a fixed
  * order, so equal calls give equal bits.  Scores, maxima, sums and outputs are
  * fp32; the softmax weights enter the product with the values as two bf16 parts
@@ -612,7 +614,9 @@ typedef struct {
  * to fp16 next to E4M3 values: 2^-11 of the product down to 2^-23 of the largest
  * weight times the largest value scale that the row has seen so far, and below
  * that steps of 2^-33 of it (so a token of tiny weight and a scale many orders
- * above the others takes bits from them).  A page number outside [0, pages), a
+ * above the others takes bits from them).  Value scales may be any finite
+ * numbers; outputs next to tiny ones are within 2^-126 times the number of
+ * tokens.  A page number outside [0, pages), a
  * length outside [0, table_width * page_size] or a draft_lens[b] outside [0,
  * min(n, seq_lens[b])] raises MOE_DEV_BAD_PAGE; the tokens of such a page are
  * left out, and such a length is clamped.
@@ -708,7 +712,8 @@ typedef struct {
  *                                       + q[i,h,128:] . k_rope[t])) v[t,h]
  * Sequence b has query tokens cu_q[b] .. cu_q[b+1] - 1 and key tokens cu_k[b]
  * .. cu_k[b+1] - 1, of which the last are its query tokens: query token i of lq
- * sees the keys t <= i + lk - lq (a row that sees none answers zeros).
+ * sees the keys t <= i + lk - lq (a row that sees none, or none but scores of
+ * -infinity, answers zeros; one that sees a NaN score is NaN).
  * q bf16 [Tq, H, 192], k_nope [Tk, H, 128], k_rope [Tk, 64], v [Tk, H, 128]
  * and out [Tq, H, 128] by their strides; cu_q, cu_k int32 [B + 1], which do not
  * fall.  Rows of no sequence are left as they were, and keys and values that a

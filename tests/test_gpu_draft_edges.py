@@ -1,6 +1,7 @@
 """Attention of drafted tokens and latent attention on the edges: queries and keys
-that are NaN, E4M3 value scales at the ends of fp32, the smallest pages and pages
-that are no power of two, negative scales, and every sequence of the divisions.
+that are NaN, scores of -infinity, E4M3 value scales at the ends of fp32, the
+smallest pages and pages that are no power of two, negative scales, and every
+sequence of the divisions.
 
 Tolerances as in test_gpu_draft_attention.py.
 """
@@ -9,7 +10,8 @@ import math
 import pytest
 
 from gpu_common import require_gpu
-from test_gpu_draft_attention import Batch, _close
+from test_gpu_draft_attention import Batch, _close, _dec
+from test_gpu_latent import _expanded, _expanded_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -67,6 +69,59 @@ def test_nan_keys_of_whole_tiles_answer_nan(torch, kind, n, Hq, Hkv, D, lens):
     _close(torch, got[1:], ref[1:], tol[1:])
     if kind != "latent" and lens[0] > 1100:  # a window that they lie behind
         _close(torch, b.run(window=300), *b.reference(window=300))
+
+
+def test_a_nan_query_of_a_prompt_answers_nan(torch):
+    q, kv, rope, cu_q, cu_k = _expanded(torch, [300, 90], [0, 700], 3)
+    op = _dec().ExpandedAttention(3)
+    ref, tol = _expanded_ref(torch, q, kv, rope, cu_q, cu_k, op.scale)
+    hit = torch.zeros(390, 3, dtype=torch.bool, device="cuda")
+    for i, h in ((0, 1), (299, 0), (320, 2)):
+        q[i, h, 100] = math.nan
+        hit[i, h] = True
+    got = op.forward(q, kv[..., :128], rope, kv[..., 128:], cu_q, cu_k)
+    assert torch.isnan(got[hit]).all()
+    _close(torch, got[~hit], ref[~hit], tol[~hit])
+
+
+# ------------------------------------------------------------------ scores of -infinity
+
+@pytest.mark.parametrize("lens", LENS.values(), ids=LENS.keys())
+@pytest.mark.parametrize("kind,n,Hq,Hkv,D", [c for c in SHAPES if c[0] != "e4m3"])
+def test_scores_of_minus_infinity_are_not_seen(torch, kind, n, Hq, Hkv, D, lens):
+    """Tokens with such scores have no weight; rows with nothing else answer zeros."""
+    b = _batch(torch, kind, lens, n, Hq, Hkv, D)
+    b.q[..., -2] = 1.0
+    keys = b.data if kind == "latent" else b.k
+    clean = keys.clone()
+
+    def spoil(s, lo, hi):
+        t = torch.arange(lo, hi, device="cuda")
+        page, off = b.table[s].long()[t // b.ps], t % b.ps
+        if kind == "latent":
+            keys[page, off, -2] = -math.inf
+        else:
+            keys[page, :, off, -2] = -math.inf
+    gone = min(70, lens[0] - n) if lens[0] < 1100 else 1000
+    spoil(0, 0, gone)
+    if len(lens) > 1:
+        spoil(1, 0, lens[1])
+    got = b.run()
+    keys.copy_(clean)
+    b.seen = lambda s, i, *a: [t for t in Batch.seen(b, s, i, *a) if s > 1 or (s == 0 and t >= gone)]
+    _close(torch, got, *b.reference())
+
+
+def test_scores_of_minus_infinity_in_a_prompt(torch):
+    q, kv, rope, cu_q, cu_k = _expanded(torch, [500], [0], 2)
+    q[..., 190] = 1.0
+    later = torch.tensor([0, 400], dtype=torch.int32, device="cuda")
+    op = _dec().ExpandedAttention(2)
+    ref, tol = _expanded_ref(torch, q[100:], kv[100:], rope[100:], later, later, op.scale)
+    rope[:100, 62] = -math.inf
+    got = op.forward(q, kv[..., :128], rope, kv[..., 128:], cu_q, cu_k)
+    assert (got[:100] == 0).all()
+    _close(torch, got[100:], ref, tol)
 
 
 # ------------------------------------------------------------------ E4M3 scales
