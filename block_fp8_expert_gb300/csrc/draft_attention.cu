@@ -18,16 +18,21 @@
 // memory.  The maximum that the weights refer to moves once it is exceeded by 2^8
 // (2^5 next to E4M3), which rarely rescales the outputs.
 //
-// What bounds it: bytes where a sequence is long, and otherwise the latency of a
-// tile's chain (loads, scores, softmax, weights, outputs) and of the start, 5 us
-// until the first tile is there.  Latent vectors of 576: 2 x 131072 tokens and 64
-// heads 68 us, 4.46 TB/s, 0.66 of the copy rate; a tile takes 3200 to 3500 cycles,
-// as two stages of 74 KB fit next to the queries and share the chain (load 1900 or
-// more, scores 1900 while pieces are being refilled, softmax 600 to 1200, outputs
-// 1300).
-// 40 ragged sequences up to 6000, 128 heads 65 us (411 TFLOP/s).  32 ragged trees
-// of 16, grouped heads, E4M3 75 us: the conversion of codes and the softmax of 128
-// rows issue on 37% of cycles.  One sequence of 777 or 900 tokens 11 us.
+// What bounds it: bytes in the middle of a long sequence, otherwise the latency of a
+// tile's chain (loads, scores, softmax, weights, outputs) and what stands around the
+// tiles: 5 us until the first one is there, a part's end, its outputs through L2 and
+// the join.  (GPU times of calls in a graph.)
+// Latent vectors of 576, 2 sequences, 64 heads: 131072 tokens 68 us, 262144 114, so
+// that a further token costs its bytes at 6.55 TB/s (0.96 of the copy rate) and 22 us
+// are around them.  40 sequences of 128 heads: 3000 tokens 71 us, 6000 109.5 (866
+// TFLOP/s between them, 32 us around); ragged up to 6000, 56 to 67 us by their lengths.
+// Trees of 16 for 32 sequences, 32 / 4 heads of 128, E4M3: 4096 tokens 109 us, 8192
+// 190, so a tile of 64 tokens and 128 rows takes 1.5 us, of which 27% of the cycles
+// issue and 8% have the tensor pipe at work: latency (28 us are around the tiles); bf16
+// 94 and 165.  One sequence of 777 or 900 tokens 11 us.
+// Pages that boxes do not divide: 2 x 131072 in pages of 24 75 us, of 1 84, of 8 (eight
+// boxes per chunk) 101; the 32 trees, bf16, pages of 16 51 us, of 24 or 1 65; E4M3 65
+// and 102 to 107.
 // Measured and left out: prefetching later tiles to L2 (2 x 131072: 74.6 us with,
 // 71.3 without), one warp that polls the pieces side by side (73.9 against 68.5),
 // two CTAs per SM for E4M3 of 128 dimensions (129 us against 114 on the 32 trees).
@@ -43,9 +48,16 @@ using namespace attn;
 
 constexpr int kTile = 64;      // tokens per tile
 constexpr int kChunk = 8192;   // 64 tokens or rows x 64 dimensions, 128-byte swizzled
-constexpr int kSegCost = 3;    // what a segment costs a CTA beside its tiles, in tiles
+// What a segment costs a CTA beside its tiles, in tiles.  (32 ragged trees of 16: bf16
+// 61 us with 1, 55 with 2, 51 with 3, 52 with 4 or 6; E4M3 89, 74, 69, 62, 61; 40
+// ragged latent sequences 67.6, 67.6, 66.8, 66.8, 66.9; 200 short sequences of 2 heads
+// 26.2, 25.4, 26.4, 25.9, 27.1.)
+constexpr int kSegCost = 3;
 constexpr int kNoRow = 0x7fffffff;
-constexpr int kMinTiles = 2;   // per part, where there are columns for smaller ones
+// Tiles per part, where there are columns for smaller ones.  (One latent sequence of
+// 777 tokens: 13.1 us with 1, 11.8 with 2, 12.7 with 3, 13.9 with 4; 4 of 1000, trees
+// of 3, E4M3: 14.8, 14.0, 14.9, 16.3.)
+constexpr int kMinTiles = 2;
 constexpr int kOCol = 2 * kTile;  // TMEM: two buffers of scores, then the outputs
 constexpr long long kMaxTokens = 0x7fffff80;  // of a sequence: its tiles' ends fit 31 bits
 // Tiles whose tokens' notes (which are there, their scales) are kept: the codes
@@ -65,7 +77,11 @@ template <int DK, int DV, bool LATENT, bool E4M3, bool TMA, int ROWS>
 struct DraftShape {
   static constexpr bool kRaw = E4M3 && TMA;
   static constexpr int kKChunks = DK / 64, kVChunks = LATENT ? 0 : DV / 64;
-  static constexpr int kParts = LATENT || E4M3 ? 1 : 2;  // parts of a softmax weight: bf16, E4M3: fp16
+  // Parts of a softmax weight: bf16, next to E4M3 fp16.  One bf16 part next to latent
+  // vectors, because a second one has no room: queries (72 KB), two stages (144 KB)
+  // and weights (8 KB) of 576 dimensions fill the shared memory, and smaller vectors
+  // round alike.  The sums are of the rounded weights, so equal values come out whole.
+  static constexpr int kParts = LATENT || E4M3 ? 1 : 2;
   static constexpr int kQChunk = ROWS * 128;  // the rows x 64 dimensions, or tokens
   static constexpr int kQ = kKChunks * kQChunk, kP = kParts * kQChunk;
   static constexpr int kCtas = ROWS == 64 && DK <= (kRaw ? 64 : 128) ? 2 : 1;  // per SM

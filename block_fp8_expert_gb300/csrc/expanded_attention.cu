@@ -19,8 +19,11 @@
 // (an S of 128 x 64 x 16 takes 48 cycles for 32 of math: its keys and queries come
 // from shared memory; with 128 keys it would take 64 for 64, but then two buffers
 // of scores per query tile do not fit next to the outputs: 633 us against 520).
-// Short ones are bound by the start and the chain of key tiles: 3 chunks of 9
-// tokens on contexts of 700, 32 heads: 15 us.
+// Short ones are bound by the start and the chain of key tiles, all of which one CTA
+// walks: 3 chunks of 9 tokens on contexts of 700, 32 heads: 14.3 us of the GPU; 200
+// tokens on a context of 8000, 8 or 32 heads: 117.
+// Weights are rounded to bf16 once, as the products take them, and summed as rounded; a
+// second part would add 31% to the MMAs.
 #include <algorithm>
 
 #include "attention_tc.cuh"
@@ -123,8 +126,11 @@ k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   // 32 heads: 497 us; 7 ragged ones, 20 heads: 63.7; head after head 521 and 76.3.
   // All heads at once: 8192, 128 heads 1915 against 1800.)  Where CTAs are so many
   // that their end does not count, or sequences more than a warp's registers hold:
-  // head after head, in the order of the sequences (40 ragged ones up to 900, 128
-  // heads: 850 us against 912 by size).
+  // head after head, in the order of the sequences.  (The limit of 32 CTAs per SM, by
+  // size against head after head: 40 ragged ones up to 900, 18 per SM 184 us, 192; 16
+  // up to 1024, 16 per SM 178.5, 180, 25 per SM 264, 262, 33 per SM 352, 344.5; one of
+  // 8192, 28 per SM 1943, 1910; 40 up to 900, 37 per SM 371, 369, 74 per SM 738, 724;
+  // 100 short ones up to 300, 29 per SM 194, 206, 58 per SM 392, 406.)
   const int group = a.by_size ? min(kHeads, a.d.H) : 1, span = a.blocks * group;
   const int h0 = (int)(blockIdx.x / span) * group, at = blockIdx.x % span;
   const int heads = min(group, a.d.H - h0), h = h0 + at % heads;

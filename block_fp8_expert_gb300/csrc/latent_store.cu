@@ -59,9 +59,11 @@ __device__ __forceinline__ void load8(const float* p, float* f) {
 // A token's steps are dealt to `chunks` warps; a lane's loads go through a ring
 // of its own in shared memory (cp.async), the first ones on their way before the
 // token's position and slot are known.
-// Bound by bytes (8192 tokens with 128 heads: 299 MB read and written in 62 us,
-// 0.71 of the copy rate, every token's 16 KB of queries in 64-element runs of
-// strided heads) and for few tokens by the launch (T 5: 4 us on the GPU).
+// Bound by bytes (8192 tokens with 128 heads: 299 MB read and written in 62 us in
+// the interleaved layout, 0.71 of the copy rate, 56 us in the half layout, 0.79:
+// interleaved, an access of a warp has halves of 32-byte sectors, as a lane's two runs
+// are neighbours; every token's 16 KB of queries are 64-element runs of strided heads)
+// and for few tokens by the launch (T 5: 2.2 us in a graph).
 template <int R>
 __global__ void __launch_bounds__(128, kCtasPerSm) k_latent_store(const StoreArgs a) {
   constexpr unsigned kAll = 0xffffffffu;
